@@ -64,6 +64,10 @@ typedef enum { KDA_BF16 = 0, KDA_F32 = 1 } kda_dtype_t;
 #define KDA_DEVICE_PIPE_TIMEOUT  0x4u  /* an internal pipeline wait gave up         */
 #define KDA_DEVICE_DEBUG_BOUNDS  0x8u  /* debug build only: a computed index fell outside
                                           its buffer (the access was skipped)         */
+#define KDA_DEVICE_BAD_TOKEN     0x10u /* kda_verify_draft: a drafted token outside the
+                                          vocabulary                                   */
+#define KDA_DEVICE_BAD_COUNT     0x20u /* kda_commit_draft: an accepted count outside
+                                          [0, max_steps]                               */
 
 /* Descriptor flags. */
 #define KDA_FLAG_CUDA_CORE_PATH  0x1u  /* prefill: run the fp32 CUDA-core kernel even where
@@ -299,6 +303,150 @@ kda_status_t kda_chunk_prefill_noalloc(const kda_desc_t *desc, const void *q, co
  * less) makes the waits give up on purpose, which is how the failure path is tested.
  */
 kda_status_t kda_set_pipeline_wait_limit(uint64_t nanoseconds);
+
+/* ---------------------------------------------------------------------------------------
+ * Operators of the layers around the recurrence.  The pages have no counterpart of them; they
+ * keep this library's rules: device pointers, packed rows, pools with state indices (-1 is the
+ * sentinel slot num_slots-1), asynchronous calls, a status word at the start of the workspace
+ * (KDA_STATUS_WORKSPACE_BYTES bytes, 256-byte aligned, where no larger size is stated), and
+ * sequences or rows with invalid device data skipped.
+ * ------------------------------------------------------------------------------------- */
+#define KDA_STATUS_WORKSPACE_BYTES 256
+
+/* Problem descriptor of the short causal convolution. */
+typedef struct {
+    int32_t num_seqs;          /* N sequences, rows or requests                         */
+    int64_t total_tokens;      /* T: rows of x and y                                    */
+    int32_t channels;          /* Ch                                                    */
+    int32_t width;             /* W taps, 2..4                                          */
+    kda_dtype_t dtype;         /* of x, weight, bias, y and the states                  */
+    int32_t silu;              /* 0: y as summed; 1: y * sigmoid(y)                     */
+    int64_t x_pitch;           /* elements between consecutive rows of x, >= Ch         */
+    int64_t num_slots;         /* pool: rows                                            */
+    int64_t slot_stride_elems; /* pool: elements between slots; 0 means (W-1)*Ch        */
+} kda_conv_desc_t;
+
+/*
+ * Short causal depthwise convolution of packed sequences:
+ *
+ *     y[t][c] = act( bias[c] + sum_{i < W} weight[c][i] x[t - (W-1) + i][c] )
+ *
+ * where the W-1 inputs before a sequence's first token are its state, oldest first.
+ *
+ *   x       [T, Ch], rows x_pitch elements apart (a slice of a wider projection is fine)
+ *   weight  [Ch, W]     bias [Ch] or NULL     y [T, Ch] packed, must not overlap x
+ *   state, state_indices, final_state  as in kda_chunk_prefill, each state being [W-1, Ch]:
+ *           pool mode updates the slots in place; dense mode reads state (NULL: zeros) and
+ *           writes final_state (NULL: not written; may equal state).  A sequence of length
+ *           zero keeps its state.
+ * Sums are fp32, rounded once to dtype.  Any Ch >= 1 and any alignment of whole elements;
+ * rows that are 16-byte aligned are moved 16 bytes at a time.  Rows of x that belong to no valid
+ * sequence give no output.
+ */
+kda_status_t kda_causal_conv(const kda_conv_desc_t *desc, const void *x, const void *weight,
+                             const void *bias, const int32_t *cu_seqlens, void *state,
+                             const int32_t *state_indices, void *final_state, void *y,
+                             void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The same for one new token a row (cu_seqlens NULL, T == N), or for the drafted tokens
+ * cu_seqlens[n] .. cu_seqlens[n+1]-1 of request n, at most max_steps of them, with the arguments
+ * of kda_decode_draft: the state after step j is written to step_cache + n * cache_pitch_elems +
+ * j * (W-1)*Ch when step_cache is given, and the pool row only if update_pool != 0.
+ * state_indices NULL means row n uses slot n.
+ */
+kda_status_t kda_causal_conv_decode(const kda_conv_desc_t *desc, const void *x, const void *weight,
+                                    const void *bias, const int32_t *cu_seqlens, void *state_pool,
+                                    const int32_t *state_indices, void *step_cache,
+                                    int64_t cache_pitch_elems, int32_t max_steps, int update_pool,
+                                    void *y, void *workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+
+/* Inputs of the selective state space scan; T tokens, H = num_v_heads heads of V = head_v_dim
+ * values, G = num_k_heads groups, state size K = head_k_dim.  Pitches are the elements between
+ * consecutive tokens, so that slices of one projection can be passed; x, b and c need 16-byte
+ * aligned rows (pointers and pitches). */
+typedef struct {
+    const void *x;             /* [T, H, V] qkv_dtype                                   */
+    int64_t x_pitch;
+    const void *dt;            /* [T, H] qkv_dtype, before bias and softplus            */
+    int64_t dt_pitch;
+    const void *b;             /* [T, G, K] qkv_dtype; head h uses group h / (H / G)    */
+    int64_t b_pitch;
+    const void *c;             /* [T, G, K] qkv_dtype                                   */
+    int64_t c_pitch;
+    const float *a_log;        /* [H] fp32: the head's decay rate is exp(a_log)         */
+    const float *dt_bias;      /* [H] fp32 or NULL                                      */
+    const float *d;            /* [H] fp32 or NULL: y += d x                            */
+} kda_ssm_inputs_t;
+
+/*
+ * Selective state space scan over packed sequences.  Per head, with step size
+ * d_t = softplus(dt_t + dt_bias):
+ *
+ *     S_t = exp(-exp(a_log) d_t) S_{t-1} + d_t b_t x_t^T        (S: [K, V], as KDA's state)
+ *     y_t = S_t^T c_t + d x_t
+ *
+ * desc as for kda_chunk_prefill (scale and chunk_size are ignored; flags: KDA_FLAG_CUDA_CORE_PATH
+ * or 0).  y [T, H, V] packed, qkv_dtype, 16-byte aligned.  cu_seqlens, state, state_indices,
+ * final_state: as in kda_chunk_prefill (pool or dense mode, [K][V] layout).  Run to run, results
+ * are bit-identical for the same inputs and workspace size.
+ */
+kda_status_t kda_ssm_scan(const kda_desc_t *desc, const kda_ssm_inputs_t *in,
+                          const int32_t *cu_seqlens, void *state, const int32_t *state_indices,
+                          void *final_state, void *y, void *workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
+/* Bytes of workspace kda_ssm_scan() wants (0 on an invalid descriptor).  The least it accepts is
+ * KDA_STATUS_WORKSPACE_BYTES: with less than this size long sequences are not split over time. */
+size_t kda_ssm_scan_workspace_size(const kda_desc_t *desc);
+
+/* One token a row, or drafted tokens a request: the arguments of kda_causal_conv_decode, with
+ * step states of H*K*V elements in state_dtype. */
+kda_status_t kda_ssm_decode(const kda_desc_t *desc, const kda_ssm_inputs_t *in,
+                            const int32_t *cu_seqlens, void *state_pool,
+                            const int32_t *state_indices, void *step_cache,
+                            int64_t cache_pitch_elems, int32_t max_steps, int update_pool, void *y,
+                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Verification of drafted tokens from given random numbers.  Request n was fed the tokens
+ * cu_seqlens[n] .. cu_seqlens[n+1]-1 (as for kda_decode_draft): its last sampled token, then the
+ * drafted ones.  Row t of the probabilities belongs to the token after t.  Drafted token t+1 is
+ * kept while
+ *                      accept_u[t] * q[t][d] < p[t][d],     d = tokens[t+1].
+ * num_accepted[n] is the number of the request's fed tokens that stand (1 for the first and 1 for
+ * each kept draft; 0 for a request of no tokens), which is the step kda_commit_draft takes.
+ * next_token[n] is drawn at the row r of the last token that stands as the entry with the largest
+ * w / noise, with w = p[r] if every draft was kept, else max(p[r] - q[r], 0), or p[r] where that is
+ * zero throughout: with noise ~ Exp(1) that is a draw in proportion to w.  Entries with w <= 0 or
+ * a NaN are never drawn; of equal entries the lowest is taken; -1 if there is none (or no token).
+ *
+ *   tokens [T] int32    p (target_probs) and q (draft_probs) [T, vocab] fp32, packed; q may be NULL
+ *   (drafts made without drawing: q is 1 at the drafted token)    accept_u [T] fp32 in [0, 1)
+ *   noise [N, vocab] fp32 > 0    num_accepted, next_token [N] int32
+ * Rows of q and elements of accept_u at a request's last token are not read.  A request with a
+ * drafted token outside [0, vocab) or a bad cu_seqlens is skipped (status bit).
+ */
+kda_status_t kda_verify_draft(int32_t num_seqs, int64_t total_tokens, int32_t vocab,
+                              const int32_t *tokens, const float *target_probs,
+                              const float *draft_probs, const float *accept_u, const float *noise,
+                              const int32_t *cu_seqlens, int32_t *num_accepted,
+                              int32_t *next_token, void *workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
+
+/*
+ * Commit of the accepted prefix: for each request n with a = num_accepted[n] > 0, the row_elems
+ * elements at step_cache + n * cache_pitch_elems + (a-1) * row_elems are copied to slot s_n of the
+ * pool (state_indices NULL: s_n = n; -1: the sentinel).  a == 0 leaves the pool as it is; a outside
+ * [0, max_steps] or a bad slot is skipped with a status bit.  For any step cache of this library
+ * (states of KDA or of the scan, inputs of the convolution); cache and pool must not overlap.
+ */
+kda_status_t kda_commit_draft(int32_t num_seqs, kda_dtype_t dtype, int64_t row_elems,
+                              const void *step_cache, int64_t cache_pitch_elems, int32_t max_steps,
+                              const int32_t *num_accepted, void *pool, int64_t num_slots,
+                              int64_t slot_stride_elems, const int32_t *state_indices,
+                              void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Synchronises `stream`, then reads the device status word left in `workspace`
  * by the last prefill or decode call that used it.  Returns KDA_OK or

@@ -23,6 +23,7 @@ KDA_FLAG_QK_L2NORM = 0x4
 KDA_FLAG_STATE_VK = 0x8
 KDA_DEVICE_BAD_SLOT, KDA_DEVICE_BAD_SEQLENS, KDA_DEVICE_PIPE_TIMEOUT = 0x1, 0x2, 0x4
 KDA_DEVICE_DEBUG_BOUNDS = 0x8
+KDA_DEVICE_BAD_TOKEN, KDA_DEVICE_BAD_COUNT = 0x10, 0x20
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration",
            3: "workspace too small", 4: "CUDA error", 5: "invalid device data"}
 
@@ -56,7 +57,8 @@ EXPORTS = ("kda_chunk_prefill_workspace_size", "kda_chunk_prefill_min_workspace_
            "kda_decode_workspace_size", "kda_chunk_prefill",
            "kda_decode", "kda_read_device_status", "kda_chunk_prefill_path", "kda_status_string",
            "kda_chunk_prefill_noalloc", "kda_chunk_prefill_act", "kda_decode_draft",
-           "kda_set_pipeline_wait_limit")
+           "kda_set_pipeline_wait_limit", "kda_causal_conv", "kda_causal_conv_decode", "kda_ssm_scan",
+           "kda_ssm_scan_workspace_size", "kda_ssm_decode", "kda_verify_draft", "kda_commit_draft")
 
 _lib = None
 

@@ -1,0 +1,349 @@
+// kda_conv.cu -- short causal depthwise convolution with a pool of its last inputs.
+//
+//   y_t = act(bias + sum_{i < W} w_i x_{t-(W-1)+i})      per channel, W = 2..4
+//
+// 2 W operations a value against 2 elements moved: the kernels are bound by HBM, so the design
+// is one pass over x and y with 16-byte accesses and enough of them in flight.
+//
+// Prompts: the packed tokens are cut into strips of kStrip; a thread walks one strip for 16 bytes
+// of channels with the last W-1 inputs in registers, so x is read once but for the W-1 rows before
+// a strip (from L2).  Sequences are found per block from cu_seqlens (every block looks through all
+// of it; no order is assumed), which leaves each token's sequence and position in shared memory.
+// The first W-1 tokens of a sequence need its state, which the call also overwrites in pool mode:
+// the thread whose strip holds a sequence's first token also takes those next W-2 tokens, reads
+// the initial state, and then writes the final one, so no other thread reads what it overwrites.
+#include "kda_internal.cuh"
+
+namespace kda {
+namespace {
+
+KDA_DEBUG_FLAG_DEFINE();
+
+constexpr int kStrip = 16;      // tokens a thread walks
+constexpr int kStrips = 8;      // strips a block
+constexpr int kTile = kStrip * kStrips;
+constexpr int kLanes = 32;      // channel vectors a block
+constexpr int kConvThreads = kLanes * kStrips;
+constexpr int kAhead = 8;       // rows loaded before they are used
+
+// Channels [c, c + VEC) of a row.  VEC is 16 bytes of elements where every row is 16-byte
+// aligned, else 1 (an odd channel count or pitch).
+template <typename T, int VEC> struct Row {
+  using Raw = uint4;
+  static __device__ __forceinline__ Raw load(const T* p) { return *reinterpret_cast<const uint4*>(p); }
+  static __device__ __forceinline__ void store(T* p, const Raw& r) { *reinterpret_cast<uint4*>(p) = r; }
+  static __device__ __forceinline__ void unpack(const Raw& r, float* f) { Vec16<T>::unpack(r, f); }
+  static __device__ __forceinline__ Raw pack(const float* f) { return Vec16<T>::pack(f); }
+  static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
+};
+template <typename T> struct Row<T, 1> {
+  using Raw = T;
+  static __device__ __forceinline__ Raw load(const T* p) { return *p; }
+  static __device__ __forceinline__ void store(T* p, const Raw& r) { *p = r; }
+  static __device__ __forceinline__ void unpack(const Raw& r, float* f) { f[0] = to_f32(r); }
+  static __device__ __forceinline__ Raw pack(const float* f) { return from_f32<T>(f[0]); }
+  static __device__ __forceinline__ Raw zero() { return from_f32<T>(0.f); }
+};
+
+// s * sigmoid(s) = s / (1 + e^-s).  The fast exponential and quotient are good to ~2^-21, far
+// below a bf16 result's rounding; fp32 results take the accurate ones.
+template <typename T> __device__ __forceinline__ float silu_f32(float s) {
+  return s / (1.f + expf(-s));
+}
+template <> __device__ __forceinline__ float silu_f32<__nv_bfloat16>(float s) {
+  return __fdividef(s, 1.f + __expf(-s));
+}
+
+// One token: window win[0..W-1], oldest first (win[W-1] is the token itself).
+template <typename T, int VEC, int W>
+__device__ __forceinline__ void apply(const float (&win)[W][VEC], const float (&wt)[W][VEC],
+                                      const float (&bias)[VEC], bool silu, float* out) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    float s = bias[i];
+#pragma unroll
+    for (int j = 0; j < W; ++j) s = fmaf(wt[j][i], win[j][i], s);
+    out[i] = silu ? silu_f32<T>(s) : s;
+  }
+}
+
+template <typename T, int VEC, int W>
+__device__ __forceinline__ void load_taps(const T* w, const T* bias, int c, float (&wt)[W][VEC],
+                                          float (&b)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) wt[j][i] = to_f32(w[(size_t)(c + i) * W + j]);
+    b[i] = bias ? to_f32(bias[c + i]) : 0.f;
+  }
+}
+
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kConvThreads)
+conv_prompt_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict__ w,
+                   const T* __restrict__ bias, const int32_t* __restrict__ cu, const T* state_in,
+                   const int32_t* __restrict__ idx, T* state_out, int64_t slot_stride,
+                   int64_t num_slots, T* __restrict__ y, uint32_t* __restrict__ status, int N,
+                   int64_t total, int ch, bool silu) {
+  using R = Row<T, VEC>;
+  constexpr int H = W - 1;                 // inputs a state holds
+  constexpr int kSpan = kTile + W - 2;     // tokens a block may own (see above)
+  __shared__ int s_seq[kSpan];             // sequence of each token, -1: none
+  __shared__ int64_t s_bos[kSpan];
+
+  const int tid = threadIdx.x;
+  // x's tiles on grid.x (up to 2^31-1 of them), channel blocks on grid.y
+  const int64_t t0 = (int64_t)blockIdx.x * kTile;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    check_all(status, cu, idx, N, total, total, idx ? num_slots : 0);
+
+  for (int i = tid; i < kSpan; i += kConvThreads) s_seq[i] = -1;
+  __syncthreads();
+  for (int base = 0; base < N; base += kConvThreads) {
+    const int n = base + tid;
+    int64_t a = 0, b = 0;
+    bool hit = n < N && seq_bounds(cu, n, total, &a, &b) && a < t0 + kSpan && b > t0;
+    if (hit && idx) hit = resolve_slot(idx, n, num_slots) >= 0;
+    // a warp writes each of its hits together: a long sequence fills the whole tile
+    unsigned m = __ballot_sync(0xffffffffu, hit);
+    while (m) {
+      const int src = __ffs(m) - 1;
+      m &= m - 1;
+      const int64_t sa = __shfl_sync(0xffffffffu, a, src), sb = __shfl_sync(0xffffffffu, b, src);
+      const int sn = __shfl_sync(0xffffffffu, n, src);
+      const int lo = (int)(sa > t0 ? sa - t0 : 0);
+      const int hi = (int)(sb < t0 + kSpan ? sb - t0 : kSpan);
+      for (int i = lo + (tid & 31); i < hi; i += 32) {
+        s_seq[i] = sn;
+        s_bos[i] = sa;
+      }
+    }
+  }
+  __syncthreads();
+
+  const int c = (blockIdx.y * kLanes + tid % kLanes) * VEC;
+  if (c >= ch) return;
+  // Sequences of length zero own no token: in dense mode their state is copied here, shared out
+  // over the tiles.
+  if (!idx && state_out && state_out != state_in) {
+    for (int64_t n = blockIdx.x * (int64_t)kStrips + tid / kLanes; n < N;
+         n += gridDim.x * (int64_t)kStrips) {
+      int64_t a, b;
+      if (!seq_bounds(cu, (int)n, total, &a, &b) || a != b) continue;
+      for (int j = 0; j < H; ++j) {
+        const int64_t at = n * slot_stride + (int64_t)j * ch + c;
+        R::store(state_out + at, state_in ? R::load(state_in + at) : R::zero());
+      }
+    }
+  }
+  const int s0 = (tid / kLanes) * kStrip;  // this strip's first token in the tile
+  float wt[W][VEC], bv[VEC];
+  load_taps<T, VEC, W>(w, bias, c, wt, bv);
+
+  // A strip inside one sequence and past its first W-1 tokens (nearly all of a long prompt): no
+  // state, no owner to find, so the window rotates in registers over unrolled tokens.
+  const int n0 = s_seq[s0];
+  if (n0 >= 0 && s_seq[s0 + kStrip - 1] == n0 && t0 + s0 - s_bos[s0] >= H) {
+    float win[W][VEC];
+#pragma unroll
+    for (int j = 0; j < H; ++j)
+      R::unpack(R::load(x + (t0 + s0 - H + j) * x_pitch + c), win[j]);
+#pragma unroll 1
+    for (int i0 = 0; i0 < kStrip; i0 += kAhead) {
+      const T* xt = x + (t0 + s0 + i0) * x_pitch + c;
+      T* yt = y + (t0 + s0 + i0) * ch + c;
+      typename R::Raw nxt[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) nxt[u] = R::load(xt + u * x_pitch);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        float out[VEC];
+        R::unpack(nxt[u], win[H]);
+        apply<T, VEC, W>(win, wt, bv, silu, out);
+        R::store(yt + (size_t)u * ch, R::pack(out));
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
+        }
+      }
+    }
+    return;
+  }
+
+  typename R::Raw h[H];   // the last W-1 inputs, oldest first
+#pragma unroll
+  for (int j = 0; j < H; ++j) h[j] = R::zero();
+  int have = -1;          // sequence whose inputs h holds
+#pragma unroll 1
+  for (int i0 = 0; i0 < kStrip + W - 2; i0 += kAhead) {
+    typename R::Raw nxt[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = s0 + i0 + u;
+      nxt[u] = R::zero();
+      if (i0 + u < kStrip + W - 2 && s_seq[i] >= 0)
+        nxt[u] = R::load(x + (t0 + i) * x_pitch + c);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = s0 + i0 + u;
+      if (i0 + u >= kStrip + W - 2) break;
+      const int n = s_seq[i];
+      if (n < 0) continue;
+      const int64_t t = t0 + i, bos = s_bos[i], pos = t - bos;
+      // the first W-1 tokens of a sequence belong to the strip of its first token
+      const bool own = pos < H ? bos >= t0 + s0 && bos < t0 + s0 + kStrip : i < s0 + kStrip;
+      if (!own) continue;
+      if (pos == 0) {
+        const int64_t slot = idx ? resolve_slot(idx, n, num_slots) : n;
+        const T* si = state_in ? state_in + slot * slot_stride + c : nullptr;
+#pragma unroll
+        for (int j = 0; j < H; ++j) h[j] = si ? R::load(si + (size_t)j * ch) : R::zero();
+        if (state_out) {
+          const int64_t len = (int64_t)cu[n + 1] - bos;
+          T* so = state_out + slot * slot_stride + c;
+#pragma unroll
+          for (int j = 0; j < H; ++j) {
+            const int64_t p = len - H + j;  // position of the j-th kept input
+            typename R::Raw r = h[0];
+            if (p >= 0) {
+              r = R::load(x + (bos + p) * x_pitch + c);
+            } else {
+#pragma unroll
+              for (int e = 1; e < H; ++e)
+                if (p + H == e) r = h[e];
+            }
+            R::store(so + (size_t)j * ch, r);
+          }
+        }
+        have = n;
+      } else if (have != n) {
+#pragma unroll
+        for (int j = 0; j < H; ++j) h[j] = R::load(x + (t - H + j) * x_pitch + c);
+        have = n;
+      }
+      float win[W][VEC], out[VEC];
+#pragma unroll
+      for (int j = 0; j < H; ++j) R::unpack(h[j], win[j]);
+      R::unpack(nxt[u], win[H]);
+      apply<T, VEC, W>(win, wt, bv, silu, out);
+      if (KDA_CHECK(t >= 0 && t < total && c + VEC <= ch)) R::store(y + t * ch + c, R::pack(out));
+#pragma unroll
+      for (int j = 0; j + 1 < H; ++j) h[j] = h[j + 1];
+      h[H - 1] = nxt[u];
+    }
+  }
+  KDA_DEBUG_FOLD(status);
+}
+
+// One token, or a few drafted ones, a row: a thread holds the W-1 inputs of 16 bytes of channels.
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(128)
+conv_token_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict__ w,
+                  const T* __restrict__ bias, const int32_t* __restrict__ cu, T* pool,
+                  const int32_t* __restrict__ idx, int64_t slot_stride, int64_t num_slots,
+                  T* __restrict__ y, uint32_t* __restrict__ status, int N, int64_t total, int ch,
+                  bool silu, T* __restrict__ cache, int64_t cache_pitch, int max_steps,
+                  bool update_pool) {
+  using R = Row<T, VEC>;
+  constexpr int H = W - 1;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    check_all(status, cu, idx, N, total, max_steps, num_slots);
+  const int n = blockIdx.x;
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
+  if (c >= ch) return;
+  int64_t bos = n, eos = n + 1;
+  if (cu && (!seq_bounds(cu, n, total, &bos, &eos) || eos - bos > max_steps)) return;
+  const int64_t slot = idx ? resolve_slot(idx, n, num_slots) : (n < num_slots ? n : -1);
+  if (slot < 0) return;
+  T* so = pool + slot * slot_stride + c;
+  typename R::Raw h[H];
+#pragma unroll
+  for (int j = 0; j < H; ++j) h[j] = R::load(so + (size_t)j * ch);
+  typename R::Raw cur = bos < eos ? R::load(x + bos * x_pitch + c) : R::zero();
+  float wt[W][VEC], bv[VEC];
+  load_taps<T, VEC, W>(w, bias, c, wt, bv);
+  for (int64_t t = bos; t < eos; ++t) {
+    const typename R::Raw nxt = t + 1 < eos ? R::load(x + (t + 1) * x_pitch + c) : R::zero();
+    float win[W][VEC], out[VEC];
+#pragma unroll
+    for (int j = 0; j < H; ++j) R::unpack(h[j], win[j]);
+    R::unpack(cur, win[H]);
+    apply<T, VEC, W>(win, wt, bv, silu, out);
+    if (KDA_CHECK(t >= 0 && t < total && c + VEC <= ch)) R::store(y + t * ch + c, R::pack(out));
+#pragma unroll
+    for (int j = 0; j + 1 < H; ++j) h[j] = h[j + 1];
+    h[H - 1] = cur;
+    cur = nxt;
+    if (cache) {
+      T* co = cache + n * cache_pitch + (t - bos) * ((int64_t)H * ch) + c;
+#pragma unroll
+      for (int j = 0; j < H; ++j) R::store(co + (size_t)j * ch, h[j]);
+    }
+  }
+  if (update_pool) {
+#pragma unroll
+    for (int j = 0; j < H; ++j) R::store(so + (size_t)j * ch, h[j]);
+  }
+  KDA_DEBUG_FOLD(status);
+}
+
+bool rows16(const void* p, int64_t pitch, int size) {
+  return !p || ((uintptr_t)p % 16 == 0 && (pitch * size) % 16 == 0);
+}
+
+template <typename T, int VEC, int W>
+cudaError_t launch_prompt(const ConvArgs& a, cudaStream_t st) {
+  const int ch = a.d.channels;
+  const int64_t tiles = (a.d.total_tokens + kTile - 1) / kTile;
+  dim3 grid((unsigned)(tiles > 0 ? tiles : 1),  // no tokens: empty sequences may want their state
+            (unsigned)((ch + kLanes * VEC - 1) / (kLanes * VEC)));
+  conv_prompt_kernel<T, VEC, W><<<grid, kConvThreads, 0, st>>>(
+      (const T*)a.x, a.d.x_pitch, (const T*)a.w, (const T*)a.bias, a.cu, (const T*)a.state_in,
+      a.idx, (T*)a.state_out, a.slot_stride, a.d.num_slots, (T*)a.y, a.status, a.d.num_seqs,
+      a.d.total_tokens, ch, a.d.silu != 0);
+  return cudaGetLastError();
+}
+
+template <typename T, int VEC, int W>
+cudaError_t launch_token(const ConvArgs& a, cudaStream_t st) {
+  const int ch = a.d.channels;
+  dim3 grid((unsigned)a.d.num_seqs, (unsigned)((ch + 128 * VEC - 1) / (128 * VEC)));
+  conv_token_kernel<T, VEC, W><<<grid, 128, 0, st>>>(
+      (const T*)a.x, a.d.x_pitch, (const T*)a.w, (const T*)a.bias, a.cu, (T*)a.state_out, a.idx,
+      a.slot_stride, a.d.num_slots, (T*)a.y, a.status, a.d.num_seqs, a.d.total_tokens, ch,
+      a.d.silu != 0, (T*)a.cache, a.cache_pitch, a.max_steps, a.update_pool);
+  return cudaGetLastError();
+}
+
+template <typename T, int VEC>
+cudaError_t by_width(const ConvArgs& a, cudaStream_t st, bool token) {
+  switch (a.d.width) {
+    case 2: return token ? launch_token<T, VEC, 2>(a, st) : launch_prompt<T, VEC, 2>(a, st);
+    case 3: return token ? launch_token<T, VEC, 3>(a, st) : launch_prompt<T, VEC, 3>(a, st);
+    default: return token ? launch_token<T, VEC, 4>(a, st) : launch_prompt<T, VEC, 4>(a, st);
+  }
+}
+
+template <typename T>
+cudaError_t by_type(const ConvArgs& a, cudaStream_t st, bool token) {
+  constexpr int VEC = Vec16<T>::N;
+  const int64_t ch = a.d.channels, e = sizeof(T);
+  const bool wide = rows16(a.x, a.d.x_pitch, e) && rows16(a.y, ch, e) &&
+                    rows16(a.state_in, ch, e) && rows16(a.state_in, a.slot_stride, e) &&
+                    rows16(a.state_out, ch, e) && rows16(a.cache, a.cache_pitch, e) && ch % VEC == 0;
+  return wide ? by_width<T, VEC>(a, st, token) : by_width<T, 1>(a, st, token);
+}
+
+}  // namespace
+
+cudaError_t launch_conv(const ConvArgs& a, cudaStream_t st) {
+  return a.d.dtype == KDA_BF16 ? by_type<__nv_bfloat16>(a, st, false) : by_type<float>(a, st, false);
+}
+
+cudaError_t launch_conv_decode(const ConvArgs& a, cudaStream_t st) {
+  return a.d.dtype == KDA_BF16 ? by_type<__nv_bfloat16>(a, st, true) : by_type<float>(a, st, true);
+}
+
+}  // namespace kda

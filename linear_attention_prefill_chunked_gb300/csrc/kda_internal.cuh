@@ -135,3 +135,118 @@ struct DecodeArgs {
 };
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st);
 }  // namespace kda
+
+// Operators of the layers around the recurrence (kda_conv.cu, kda_ssm.cu, kda_draft.cu).
+namespace kda {
+
+// Their status word is written by one block, which looks every sequence and slot over before
+// anything else of its work, so that a call needs no clear of the word in front of the kernel
+// (one stream operation less a call).  The debug build, where any block may add
+// KDA_DEVICE_DEBUG_BOUNDS, clears it on the host and adds to it instead.
+__device__ __forceinline__ void set_status(uint32_t* status, uint32_t bits) {
+#ifdef KDA_DEBUG
+  if (bits) atomicOr(status, bits);
+#else
+  *status = bits;
+#endif
+}
+
+// The whole block checks cu (null: none; runs longer than max_len are bad) and the slot indices
+// (null: slot n, when num_slots > 0) of n < N and writes the status word.  Ends with a barrier.
+__device__ __forceinline__ void check_all(uint32_t* status, const int32_t* cu, const int32_t* idx,
+                                          int N, int64_t T, int64_t max_len, int64_t num_slots) {
+  uint32_t bits = 0;
+  for (int n = threadIdx.x; n < N; n += blockDim.x) {
+    int64_t a, b;
+    if (cu && (!seq_bounds(cu, n, T, &a, &b) || b - a > max_len)) bits |= KDA_DEVICE_BAD_SEQLENS;
+    if (idx ? resolve_slot(idx, n, num_slots) < 0 : (num_slots > 0 && n >= num_slots))
+      bits |= KDA_DEVICE_BAD_SLOT;
+  }
+  const int s = __syncthreads_or((int)(bits & KDA_DEVICE_BAD_SEQLENS));
+  const int i = __syncthreads_or((int)(bits & KDA_DEVICE_BAD_SLOT));
+  if (threadIdx.x == 0)
+    set_status(status, (s ? KDA_DEVICE_BAD_SEQLENS : 0u) | (i ? KDA_DEVICE_BAD_SLOT : 0u));
+}
+
+// 16 bytes of elements as fp32, and back.
+template <typename T> struct Vec16;
+template <> struct Vec16<float> {
+  static constexpr int N = 4;
+  __device__ static __forceinline__ void unpack(const uint4& u, float* f) {
+    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
+    f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+  }
+  __device__ static __forceinline__ uint4 pack(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  }
+};
+template <> struct Vec16<__nv_bfloat16> {
+  static constexpr int N = 8;
+  __device__ static __forceinline__ void unpack(const uint4& u, float* f) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ static __forceinline__ uint4 pack(const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+struct ConvArgs {
+  kda_conv_desc_t d;
+  const void *x, *w, *bias;
+  const int32_t* cu;       // null: one token a row
+  const void* state_in;    // pool or dense initial states or null
+  const int32_t* idx;      // null: dense, or slot n in the token form
+  void* state_out;         // pool, dense final states or null
+  int64_t slot_stride;
+  void* y;
+  uint32_t* status;
+  void* cache;             // token form: states after each step, or null
+  int64_t cache_pitch;
+  int max_steps;
+  bool update_pool;
+};
+cudaError_t launch_conv(const ConvArgs& a, cudaStream_t st);
+cudaError_t launch_conv_decode(const ConvArgs& a, cudaStream_t st);
+
+struct SsmArgs {
+  kda_desc_t d;
+  kda_ssm_inputs_t in;
+  const int32_t* cu;
+  const void* state_in;
+  const int32_t* idx;
+  void* state_out;
+  int64_t slot_stride;
+  void* y;
+  uint32_t* status;
+  uint8_t* ws;
+  size_t ws_bytes;
+  void* cache;
+  int64_t cache_pitch;
+  int max_steps;
+  bool update_pool;
+};
+cudaError_t launch_ssm_decode(const SsmArgs& a, cudaStream_t st);
+cudaError_t launch_ssm_simt(const SsmArgs& a, cudaStream_t st);
+// Step size and decay of one (token, head): softplus(dt + bias) and the log-decay (<= 0).
+__device__ __forceinline__ float ssm_step(float dt, float bias) { return softplus_f32(dt + bias); }
+
+cudaError_t launch_verify(int N, int64_t T, int vocab, const int32_t* tokens, const float* p,
+                          const float* q, const float* u, const float* noise, const int32_t* cu,
+                          int32_t* kept, int32_t* next, uint32_t* status, cudaStream_t st);
+cudaError_t launch_commit(int N, int elem_bytes, int64_t row, const void* cache, int64_t pitch,
+                          int max_steps, const int32_t* kept, void* pool, int64_t num_slots,
+                          int64_t slot_stride, const int32_t* idx, uint32_t* status,
+                          cudaStream_t st);
+}  // namespace kda
