@@ -19,22 +19,43 @@ namespace {
 
 KDA_DEBUG_FLAG_DEFINE();
 
-constexpr int kStrip = 16;      // tokens a thread walks
-constexpr int kStrips = 8;      // strips a block
-constexpr int kTile = kStrip * kStrips;
+constexpr int kStrips = 8;      // strips a block; a strip is S tokens, walked by one thread
 constexpr int kLanes = 32;      // channel vectors a block
 constexpr int kConvThreads = kLanes * kStrips;
-constexpr int kAhead = 8;       // rows loaded before they are used
+constexpr int kAhead = 4;       // rows in flight while as many are computed
 
-// Channels [c, c + VEC) of a row.  VEC is 16 bytes of elements where every row is 16-byte
-// aligned, else 1 (an odd channel count or pitch).
-template <typename T, int VEC> struct Row {
+// Channels [c, c + VEC) of a row: 4 where every row is aligned to as many elements, else 1 (an odd
+// channel count or pitch).  Eight bf16 channels a thread, in 16-byte accesses, need 124 registers
+// for taps, window and rows in flight, which leaves three warps a scheduler: 309 us for 32768 x
+// 12288 against 288 us with 4 channels and four blocks an SM.
+template <typename T, int VEC> struct Row;
+template <> struct Row<float, 4> {
   using Raw = uint4;
-  static __device__ __forceinline__ Raw load(const T* p) { return *reinterpret_cast<const uint4*>(p); }
-  static __device__ __forceinline__ void store(T* p, const Raw& r) { *reinterpret_cast<uint4*>(p) = r; }
-  static __device__ __forceinline__ void unpack(const Raw& r, float* f) { Vec16<T>::unpack(r, f); }
-  static __device__ __forceinline__ Raw pack(const float* f) { return Vec16<T>::pack(f); }
+  static __device__ __forceinline__ Raw load(const float* p) { return *reinterpret_cast<const uint4*>(p); }
+  static __device__ __forceinline__ void store(float* p, const Raw& r) { *reinterpret_cast<uint4*>(p) = r; }
+  static __device__ __forceinline__ void unpack(const Raw& r, float* f) {
+    f[0] = __uint_as_float(r.x); f[1] = __uint_as_float(r.y);
+    f[2] = __uint_as_float(r.z); f[3] = __uint_as_float(r.w);
+  }
+  static __device__ __forceinline__ Raw pack(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  }
   static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
+};
+template <> struct Row<__nv_bfloat16, 4> {
+  using Raw = uint2;
+  static __device__ __forceinline__ Raw load(const __nv_bfloat16* p) { return *reinterpret_cast<const uint2*>(p); }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const Raw& r) { *reinterpret_cast<uint2*>(p) = r; }
+  static __device__ __forceinline__ void unpack(const Raw& r, float* f) {
+    f[0] = __uint_as_float(r.x << 16); f[1] = __uint_as_float(r.x & 0xffff0000u);
+    f[2] = __uint_as_float(r.y << 16); f[3] = __uint_as_float(r.y & 0xffff0000u);
+  }
+  static __device__ __forceinline__ Raw pack(const float* f) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+  static __device__ __forceinline__ Raw zero() { return make_uint2(0, 0); }
 };
 template <typename T> struct Row<T, 1> {
   using Raw = T;
@@ -67,19 +88,25 @@ __device__ __forceinline__ void apply(const float (&win)[W][VEC], const float (&
   }
 }
 
+// The taps [VEC][W] of VEC channels are W vectors in a row.
 template <typename T, int VEC, int W>
 __device__ __forceinline__ void load_taps(const T* w, const T* bias, int c, float (&wt)[W][VEC],
                                           float (&b)[VEC]) {
+  using R = Row<T, VEC>;
+  float flat[W * VEC];
+#pragma unroll
+  for (int j = 0; j < W; ++j) R::unpack(R::load(w + (size_t)c * W + j * VEC), flat + j * VEC);
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) wt[j][i] = to_f32(w[(size_t)(c + i) * W + j]);
-    b[i] = bias ? to_f32(bias[c + i]) : 0.f;
+    for (int j = 0; j < W; ++j) wt[j][i] = flat[i * W + j];
+    b[i] = 0.f;
   }
+  if (bias) R::unpack(R::load(bias + c), b);
 }
 
-template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kConvThreads)
+template <typename T, int VEC, int W, int kStrip>
+__global__ void __launch_bounds__(kConvThreads, 4)
 conv_prompt_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict__ w,
                    const T* __restrict__ bias, const int32_t* __restrict__ cu, const T* state_in,
                    const int32_t* __restrict__ idx, T* state_out, int64_t slot_stride,
@@ -87,6 +114,7 @@ conv_prompt_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict
                    int64_t total, int ch, bool silu) {
   using R = Row<T, VEC>;
   constexpr int H = W - 1;                 // inputs a state holds
+  constexpr int kTile = kStrip * kStrips;
   constexpr int kSpan = kTile + W - 2;     // tokens a block may own (see above)
   __shared__ int s_seq[kSpan];             // sequence of each token, -1: none
   __shared__ int64_t s_bos[kSpan];
@@ -148,17 +176,24 @@ conv_prompt_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict
 #pragma unroll
     for (int j = 0; j < H; ++j)
       R::unpack(R::load(x + (t0 + s0 - H + j) * x_pitch + c), win[j]);
+    const T* xt = x + (t0 + s0) * x_pitch + c;
+    T* yt = y + (t0 + s0) * ch + c;
+    typename R::Raw nxt[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) nxt[u] = R::load(xt + u * x_pitch);
 #pragma unroll 1
     for (int i0 = 0; i0 < kStrip; i0 += kAhead) {
-      const T* xt = x + (t0 + s0 + i0) * x_pitch + c;
-      T* yt = y + (t0 + s0 + i0) * ch + c;
-      typename R::Raw nxt[kAhead];
+      typename R::Raw cur[kAhead];
+      xt += kAhead * x_pitch;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) nxt[u] = R::load(xt + u * x_pitch);
+      for (int u = 0; u < kAhead; ++u) {
+        cur[u] = nxt[u];
+        if (i0 + kAhead < kStrip) nxt[u] = R::load(xt + u * x_pitch);
+      }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         float out[VEC];
-        R::unpack(nxt[u], win[H]);
+        R::unpack(cur[u], win[H]);
         apply<T, VEC, W>(win, wt, bv, silu, out);
         R::store(yt + (size_t)u * ch, R::pack(out));
 #pragma unroll
@@ -167,6 +202,7 @@ conv_prompt_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict
           for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
         }
       }
+      yt += (size_t)kAhead * ch;
     }
     return;
   }
@@ -289,21 +325,30 @@ conv_token_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
   KDA_DEBUG_FOLD(status);
 }
 
-bool rows16(const void* p, int64_t pitch, int size) {
-  return !p || ((uintptr_t)p % 16 == 0 && (pitch * size) % 16 == 0);
+// Rows that start on a boundary of 4 elements.
+bool rows4(const void* p, int64_t pitch, int size) {
+  return !p || ((uintptr_t)p % (4 * size) == 0 && pitch % 4 == 0);
 }
 
-template <typename T, int VEC, int W>
-cudaError_t launch_prompt(const ConvArgs& a, cudaStream_t st) {
+template <typename T, int VEC, int W, int kStrip>
+cudaError_t launch_strips(const ConvArgs& a, cudaStream_t st) {
   const int ch = a.d.channels;
-  const int64_t tiles = (a.d.total_tokens + kTile - 1) / kTile;
+  const int64_t tiles = (a.d.total_tokens + kStrip * kStrips - 1) / (kStrip * kStrips);
   dim3 grid((unsigned)(tiles > 0 ? tiles : 1),  // no tokens: empty sequences may want their state
             (unsigned)((ch + kLanes * VEC - 1) / (kLanes * VEC)));
-  conv_prompt_kernel<T, VEC, W><<<grid, kConvThreads, 0, st>>>(
+  conv_prompt_kernel<T, VEC, W, kStrip><<<grid, kConvThreads, 0, st>>>(
       (const T*)a.x, a.d.x_pitch, (const T*)a.w, (const T*)a.bias, a.cu, (const T*)a.state_in,
       a.idx, (T*)a.state_out, a.slot_stride, a.d.num_slots, (T*)a.y, a.status, a.d.num_seqs,
       a.d.total_tokens, ch, a.d.silu != 0);
   return cudaGetLastError();
+}
+
+// Long strips read fewer rows twice and set up less often; they are taken once they leave at least
+// two waves of blocks.
+template <typename T, int VEC, int W>
+cudaError_t launch_prompt(const ConvArgs& a, cudaStream_t st) {
+  const int64_t blocks = (a.d.total_tokens / (32 * kStrips)) * (a.d.channels / (kLanes * VEC));
+  return blocks >= 608 ? launch_strips<T, VEC, W, 32>(a, st) : launch_strips<T, VEC, W, 8>(a, st);
 }
 
 template <typename T, int VEC, int W>
@@ -328,11 +373,12 @@ cudaError_t by_width(const ConvArgs& a, cudaStream_t st, bool token) {
 
 template <typename T>
 cudaError_t by_type(const ConvArgs& a, cudaStream_t st, bool token) {
-  constexpr int VEC = Vec16<T>::N;
+  constexpr int VEC = 4;
   const int64_t ch = a.d.channels, e = sizeof(T);
-  const bool wide = rows16(a.x, a.d.x_pitch, e) && rows16(a.y, ch, e) &&
-                    rows16(a.state_in, ch, e) && rows16(a.state_in, a.slot_stride, e) &&
-                    rows16(a.state_out, ch, e) && rows16(a.cache, a.cache_pitch, e) && ch % VEC == 0;
+  const bool wide = rows4(a.x, a.d.x_pitch, e) && rows4(a.y, ch, e) && rows4(a.w, ch, e) &&
+                    rows4(a.bias, ch, e) &&
+                    rows4(a.state_in, ch, e) && rows4(a.state_in, a.slot_stride, e) &&
+                    rows4(a.state_out, ch, e) && rows4(a.cache, a.cache_pitch, e) && ch % VEC == 0;
   return wide ? by_width<T, VEC>(a, st, token) : by_width<T, 1>(a, st, token);
 }
 

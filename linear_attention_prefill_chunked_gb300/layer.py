@@ -64,72 +64,72 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-class _Stream:
-    """The stream of a call: its handle, and allocations that belong to it."""
+# The checks below sit on the host path of every call, a good part of a small call's time: each
+# asks the expected case in one expression and leaves the finding of what is wrong to the slow
+# path behind it.
 
-    def __init__(self, stream):
-        self.given = stream
-        self.handle = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
-
-    def empty(self, shape, dtype, device):
-        if self.given is None:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(self.given):
-            return torch.empty(shape, dtype=dtype, device=device)
-
-    def workspace(self, given, size, least, device):
-        if given is not None and given.numel() * given.element_size() >= least:
-            return given
-        return self.empty(size, torch.uint8, device)
+def _plain(t, name, dtype, shape):
+    """``t`` is a contiguous tensor of ``dtype`` and ``shape``."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, name, dtype, cuda=False)
+        _shape(t, name, shape)
 
 
-def _done(rc, what, owner, workspace):
-    if rc != 0:
-        raise KdaError(rc, what)
-    owner.last_workspace = workspace
+def _rows(t, name, shape, dtype):
+    """``t`` has ``dtype`` and ``shape``, each row (the trailing dimensions) packed and no two rows
+    overlapping; returns the elements between rows."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape:
+        st = t.stride()
+        if shape[0] < 2:
+            pass
+        elif len(st) == 2:
+            if st[1] == 1 and st[0] >= shape[1]:
+                return st[0]
+        elif st[2] == 1 and st[1] == shape[2] and st[0] >= shape[1] * shape[2]:
+            return st[0]
+    return _rows_slow(t, name, shape, dtype)
 
 
-def _rows(t, name, dims, dtype):
-    """``t`` [rows, *dims] of ``dtype`` whose rows are packed; returns the elements between them."""
+def _rows_slow(t, name, shape, dtype):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != len(dims) + 1 or any(d is not None and s != d for s, d in zip(t.shape[1:], dims)):
-        raise ValueError(f"{name} must have shape [*, {', '.join(map(str, dims))}], got {list(t.shape)}")
+    _shape(t, name, shape)
     row = 1
     for i in range(t.dim() - 1, 0, -1):
         if t.shape[i] > 1 and t.stride(i) != row:
             raise ValueError(f"the rows of {name} must be contiguous")
         row *= t.shape[i]
-    if t.shape[0] < 2:
-        return max(row, t.stride(0))
-    if t.stride(0) < row:
+    if t.shape[0] > 1 and t.stride(0) < row:
         raise ValueError(f"the rows of {name} must not overlap")
-    return t.stride(0)
+    return t.stride(0) if t.shape[0] > 1 else row  # the stride of a single row says nothing
 
 
-def _cuda(*named):
-    for name, t in named:
+def _cuda(*tensors):
+    for t in tensors:
         if t is not None and not t.is_cuda:
-            raise ValueError(f"{name} must live on a CUDA device")
+            raise ValueError("every tensor of the call must live on a CUDA device")
 
 
 def _activation(activation):
-    if activation not in (None, "silu"):
+    if activation is None:
+        return 0
+    if activation != "silu":
         raise ValueError(f"activation must be None or 'silu', got {activation!r}")
-    return 1 if activation == "silu" else 0
+    return 1
 
 
-def _out(out, shape, dtype):
-    if out is not None:
-        _need(out, "out", dtype, cuda=False)
-        _shape(out, "out", shape)
-
-
-def _ints(t, name, shape):
-    _need(t, name, torch.int32, cuda=False)
-    _shape(t, name, shape)
+def _num_seqs(cu_seqlens):
+    if not (isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.dtype is torch.int32
+            and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous()):
+        _need(cu_seqlens, "cu_seqlens", torch.int32, cuda=False)
+        _shape(cu_seqlens, "cu_seqlens", (None,))
+    n = cu_seqlens.shape[0] - 1
+    if n < 0:
+        raise ValueError("cu_seqlens needs at least one element")
+    return n
 
 
 def _step_cache(cache, name, N, max_steps, row, dtype):
@@ -138,30 +138,61 @@ def _step_cache(cache, name, N, max_steps, row, dtype):
         raise TypeError(f"{name} must be a tensor of {dtype}")
     if cache.dim() < 2 or cache.shape[0] < N:
         raise ValueError(f"{name} must hold {N} requests, got {list(cache.shape)}")
-    packed = 1
-    for i in range(cache.dim() - 1, 0, -1):
-        if cache.shape[i] > 1 and cache.stride(i) != packed:
-            raise ValueError(f"the requests of {name} must be contiguous")
-        packed *= cache.shape[i]
-    pitch = cache.stride(0) if cache.shape[0] > 1 else max(packed, cache.stride(0))
-    if packed < max_steps * row or pitch < max_steps * row:
+    if cache.is_contiguous():
+        packed = pitch = cache.numel() // cache.shape[0] if cache.shape[0] else 0
+    else:
+        packed = 1
+        for i in range(cache.dim() - 1, 0, -1):
+            if cache.shape[i] > 1 and cache.stride(i) != packed:
+                raise ValueError(f"the requests of {name} must be contiguous")
+            packed *= cache.shape[i]
+        pitch = cache.stride(0) if cache.shape[0] > 1 else packed
+    if N > 0 and (packed < max_steps * row or pitch < packed):
         raise ValueError(f"{name} must hold {max_steps} states of {row} elements a request")
-    return pitch
+    return max(pitch, max_steps * row)
 
 
 def _state_pool(state, name, dims, slot_stride):
     """Pool of [slots, *dims], packed, or a buffer of shape[0] slots slot_stride elements apart."""
-    api._need(state, name, cuda=False)
+    if not (isinstance(state, torch.Tensor) and state.is_contiguous()):
+        _need(state, name, cuda=False)
+    if slot_stride == 0:
+        if state.shape[1:] != dims:
+            _shape(state, name, (None, *dims))
+        if state.shape[0] == 0:
+            raise ValueError(f"{name} has no slots")
+        return
     row = 1
     for d in dims:
         row *= d
-    if slot_stride == 0:
-        _shape(state, name, (None, *dims))
-        if state.shape[0] == 0:
-            raise ValueError(f"{name} has no slots")
-    elif slot_stride < row or state.dim() < 1 or state.shape[0] == 0 or \
+    if slot_stride < row or state.dim() < 1 or state.shape[0] == 0 or \
             state.numel() < (state.shape[0] - 1) * slot_stride + row:
         raise ValueError(f"{name} is too small for its slots of pitch {slot_stride}")
+
+
+def _stream(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _empty(stream, shape, dtype, device):
+    """An uninitialised tensor that belongs to the call's stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(stream, given, size, device):
+    """The given workspace if it holds a status word, else a new one of ``size`` bytes."""
+    if given is not None and given.numel() * given.element_size() >= STATUS_WORKSPACE_BYTES:
+        return given, given.numel() * given.element_size()
+    return _empty(stream, size, torch.uint8, device), size
+
+
+def _done(rc, what, owner, workspace):
+    if rc != 0:
+        raise KdaError(rc, what)
+    owner.last_workspace = workspace
 
 
 # ------------------------------------------------------------------------ short convolution
@@ -173,35 +204,33 @@ def check_conv_args(x, weight, *, bias=None, cu_seqlens=None, state=None, state_
         raise TypeError("x must be a bfloat16 or float32 tensor")
     if x.dim() != 2 or x.shape[1] < 1:
         raise ValueError(f"x must have shape [T, channels], got {list(x.shape)}")
+    dtype = x.dtype
     T, ch = x.shape
-    pitch = _rows(x, "x", (ch,), x.dtype)
-    _need(weight, "weight", x.dtype, cuda=False)
-    _shape(weight, "weight", (ch, None))
-    width = weight.shape[1]
+    pitch = _rows(x, "x", (T, ch), dtype)
+    width = weight.shape[1] if isinstance(weight, torch.Tensor) and weight.dim() == 2 else 0
+    _plain(weight, "weight", dtype, (ch, width))
     if not 2 <= width <= 4:
         raise ValueError(f"weight must have 2 to 4 taps, got {width}")
     if bias is not None:
-        _need(bias, "bias", x.dtype, cuda=False)
-        _shape(bias, "bias", (ch,))
-    N = T
-    if cu_seqlens is not None:
-        _ints(cu_seqlens, "cu_seqlens", (None,))
-        if cu_seqlens.shape[0] < 1:
-            raise ValueError("cu_seqlens needs at least one element")
-        N = cu_seqlens.shape[0] - 1
+        _plain(bias, "bias", dtype, (ch,))
+    N = T if cu_seqlens is None else _num_seqs(cu_seqlens)
     if state_indices is not None:
-        _ints(state_indices, "state_indices", (N,))
+        _plain(state_indices, "state_indices", torch.int32, (N,))
     if token or state_indices is not None:
         if state is None:
             raise ValueError("pool mode needs the pool in `state`")
         _state_pool(state, "state", (width - 1, ch), slot_stride)
-    for name, t in (("state", state), ("final_state", final_state)):
-        if t is None:
-            continue
-        _need(t, name, x.dtype, cuda=False)
-        if not token and state_indices is None:
-            _shape(t, name, (N, width - 1, ch))
-    _out(out, (T, ch), x.dtype)
+        if state.dtype is not dtype:
+            raise TypeError(f"state must be {dtype}, got {state.dtype}")
+        if final_state is not None and final_state is not state:
+            raise ValueError("pool mode updates the pool: final_state must be None or the pool")
+    else:
+        if state is not None:
+            _plain(state, "state", dtype, (N, width - 1, ch))
+        if final_state is not None:
+            _plain(final_state, "final_state", dtype, (N, width - 1, ch))
+    if out is not None:
+        _plain(out, "out", dtype, (T, ch))
     return N, T, ch, width, pitch
 
 
@@ -221,22 +250,22 @@ def causal_conv(x, weight, cu_seqlens, *, bias=None, activation=None, state=None
     N, T, ch, width, pitch = check_conv_args(
         x, weight, bias=bias, cu_seqlens=cu_seqlens, state=state, state_indices=state_indices,
         final_state=final_state, out=out, slot_stride=slot_stride)
-    _cuda(("x", x), ("weight", weight), ("bias", bias), ("cu_seqlens", cu_seqlens), ("state", state),
-          ("state_indices", state_indices), ("final_state", final_state), ("out", out))
+    _cuda(x, weight, bias, cu_seqlens, state, state_indices, final_state, out)
     silu = _activation(activation)
-    lib, st = _load(), _Stream(stream)
+    lib, dev = _load(), x.device
     pool = state_indices is not None
     if pool:
         final_state = state
     elif final_state is None and output_final_state:
-        final_state = st.empty((N, width - 1, ch), x.dtype, x.device)
+        final_state = _empty(stream, (N, width - 1, ch), x.dtype, dev)
     if out is None:
-        out = st.empty((T, ch), x.dtype, x.device)
-    ws = st.workspace(workspace, STATUS_WORKSPACE_BYTES, STATUS_WORKSPACE_BYTES, x.device)
+        out = _empty(stream, (T, ch), x.dtype, dev)
+    ws, nws = _workspace(stream, workspace, STATUS_WORKSPACE_BYTES, dev)
     d = KdaConvDesc(N, T, ch, width, _dt(x.dtype), silu, pitch, state.shape[0] if pool else 0,
                     slot_stride)
     rc = lib.kda_causal_conv(ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(cu_seqlens), _p(state),
-                             _p(state_indices), _p(final_state), _p(out), _p(ws), ws.numel(), st.handle)
+                             _p(state_indices), _p(final_state), _p(out), _p(ws), nws,
+                             _stream(stream, dev))
     _done(rc, "kda_causal_conv", causal_conv, ws)
     return out, final_state
 
@@ -246,20 +275,20 @@ def _conv_token(x, weight, cu_seqlens, state, state_indices, bias, activation, c
     N, T, ch, width, pitch = check_conv_args(x, weight, bias=bias, cu_seqlens=cu_seqlens, state=state,
                                              state_indices=state_indices, out=out,
                                              slot_stride=slot_stride, token=True)
-    _cuda(("x", x), ("weight", weight), ("bias", bias), ("cu_seqlens", cu_seqlens), ("state", state),
-          ("state_indices", state_indices), ("cache", cache), ("out", out))
+    _cuda(x, weight, bias, cu_seqlens, state, state_indices, cache, out)
     silu = _activation(activation)
     cpitch = 0
     if cache is not None:
         cpitch = _step_cache(cache, "cache", N, max_steps, (width - 1) * ch, x.dtype)
-    lib, st = _load(), _Stream(stream)
+    lib, dev = _load(), x.device
     if out is None:
-        out = st.empty((T, ch), x.dtype, x.device)
-    ws = st.workspace(workspace, STATUS_WORKSPACE_BYTES, STATUS_WORKSPACE_BYTES, x.device)
+        out = _empty(stream, (T, ch), x.dtype, dev)
+    ws, nws = _workspace(stream, workspace, STATUS_WORKSPACE_BYTES, dev)
     d = KdaConvDesc(N, T, ch, width, _dt(x.dtype), silu, pitch, state.shape[0], slot_stride)
     rc = lib.kda_causal_conv_decode(ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(cu_seqlens),
                                     _p(state), _p(state_indices), _p(cache), cpitch, max_steps,
-                                    1 if update_state else 0, _p(out), _p(ws), ws.numel(), st.handle)
+                                    1 if update_state else 0, _p(out), _p(ws), nws,
+                                    _stream(stream, dev))
     _done(rc, "kda_causal_conv_decode", owner, ws)
     return out
 
@@ -301,40 +330,35 @@ def check_ssm_args(x, dt, A_log, B, C, *, D=None, dt_bias=None, cu_seqlens=None,
         raise TypeError("x must be a bfloat16 or float32 tensor")
     if x.dim() != 3 or not isinstance(B, torch.Tensor) or B.dim() != 3:
         raise ValueError("x must have shape [T, H, V] and B [T, G, K]")
+    dtype = x.dtype
     T, H, V = x.shape
-    G, K = B.shape[1:]
+    _, G, K = B.shape
     if G == 0 or H == 0 or H % G != 0:
         raise ValueError(f"the head count {H} must be a multiple of the group count {G}")
-    pitches = (_rows(x, "x", (H, V), x.dtype), _rows(dt, "dt", (H,), x.dtype),
-               _rows(B, "B", (G, K), x.dtype), _rows(C, "C", (G, K), x.dtype))
-    for name, t in (("dt", dt), ("B", B), ("C", C)):
-        if t.shape[0] != T:
-            raise ValueError(f"{name} must have {T} rows, got {t.shape[0]}")
-    for name, t in (("A_log", A_log), ("dt_bias", dt_bias), ("D", D)):
-        if t is None and name != "A_log":
-            continue
-        _need(t, name, torch.float32, cuda=False)
-        _shape(t, name, (H,))
-    N = T
-    if cu_seqlens is not None:
-        _ints(cu_seqlens, "cu_seqlens", (None,))
-        if cu_seqlens.shape[0] < 1:
-            raise ValueError("cu_seqlens needs at least one element")
-        N = cu_seqlens.shape[0] - 1
+    pitches = (_rows(x, "x", (T, H, V), dtype), _rows(dt, "dt", (T, H), dtype),
+               _rows(B, "B", (T, G, K), dtype), _rows(C, "C", (T, G, K), dtype))
+    _plain(A_log, "A_log", torch.float32, (H,))
+    if dt_bias is not None:
+        _plain(dt_bias, "dt_bias", torch.float32, (H,))
+    if D is not None:
+        _plain(D, "D", torch.float32, (H,))
+    N = T if cu_seqlens is None else _num_seqs(cu_seqlens)
     if state_indices is not None:
-        _ints(state_indices, "state_indices", (N,))
+        _plain(state_indices, "state_indices", torch.int32, (N,))
     if token or state_indices is not None:
         if state is None:
             raise ValueError("pool mode needs the pool in `state`")
         _state_pool(state, "state", (H, K, V), slot_stride)
+        if final_state is not None and final_state is not state:
+            raise ValueError("pool mode updates the pool: final_state must be None or the pool")
     else:
-        for name, t in (("state", state), ("final_state", final_state)):
-            if t is not None:
-                _need(t, name, cuda=False)
-                _shape(t, name, (N, H, K, V))
-        if state is not None and final_state is not None and state.dtype != final_state.dtype:
-            raise TypeError(f"final_state must be {state.dtype} like state, got {final_state.dtype}")
-    _out(out, (T, H, V), x.dtype)
+        if state is not None:
+            _plain(state, "state", state.dtype, (N, H, K, V))
+        if final_state is not None:
+            want = final_state.dtype if state is None else state.dtype
+            _plain(final_state, "final_state", want, (N, H, K, V))
+    if out is not None:
+        _plain(out, "out", dtype, (T, H, V))
     return N, T, H, G, K, V, pitches
 
 
@@ -367,26 +391,24 @@ def ssm_scan(x, dt, A_log, B, C, cu_seqlens, *, D=None, dt_bias=None, state=None
     N, T, H, G, K, V, pitches = check_ssm_args(
         x, dt, A_log, B, C, D=D, dt_bias=dt_bias, cu_seqlens=cu_seqlens, state=state,
         state_indices=state_indices, final_state=final_state, out=out, slot_stride=slot_stride)
-    _cuda(("x", x), ("dt", dt), ("A_log", A_log), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias),
-          ("cu_seqlens", cu_seqlens), ("state", state), ("state_indices", state_indices),
-          ("final_state", final_state), ("out", out))
-    lib, st = _load(), _Stream(stream)
+    _cuda(x, dt, A_log, B, C, D, dt_bias, cu_seqlens, state, state_indices, final_state, out)
+    lib, dev = _load(), x.device
     pool = state_indices is not None
     sdt = state.dtype if state is not None else (
         final_state.dtype if final_state is not None else torch.float32)
     if pool:
         final_state = state
     elif final_state is None and output_final_state:
-        final_state = st.empty((N, H, K, V), sdt, x.device)
+        final_state = _empty(stream, (N, H, K, V), sdt, dev)
     if out is None:
-        out = st.empty((T, H, V), x.dtype, x.device)
+        out = _empty(stream, (T, H, V), x.dtype, dev)
     d = ssm_desc(N, T, H, G, K, V, x.dtype, sdt, state.shape[0] if pool else 0, slot_stride,
                  KDA_FLAG_CUDA_CORE_PATH if cuda_core_path else 0)
     size = lib.kda_ssm_scan_workspace_size(ctypes.byref(d))
-    ws = st.workspace(workspace, max(size, STATUS_WORKSPACE_BYTES), STATUS_WORKSPACE_BYTES, x.device)
+    ws, nws = _workspace(stream, workspace, max(size, STATUS_WORKSPACE_BYTES), dev)
     ins = _ssm_inputs(x, dt, A_log, B, C, D, dt_bias, pitches)
     rc = lib.kda_ssm_scan(ctypes.byref(d), ctypes.byref(ins), _p(cu_seqlens), _p(state),
-                          _p(state_indices), _p(final_state), _p(out), _p(ws), ws.numel(), st.handle)
+                          _p(state_indices), _p(final_state), _p(out), _p(ws), nws, _stream(stream, dev))
     _done(rc, "kda_ssm_scan", ssm_scan, ws)
     return out, final_state
 
@@ -396,21 +418,19 @@ def _ssm_token(x, dt, A_log, B, C, cu_seqlens, pool, state_indices, D, dt_bias, 
     N, T, H, G, K, V, pitches = check_ssm_args(
         x, dt, A_log, B, C, D=D, dt_bias=dt_bias, cu_seqlens=cu_seqlens, state=pool,
         state_indices=state_indices, out=out, slot_stride=slot_stride, token=True)
-    _cuda(("x", x), ("dt", dt), ("A_log", A_log), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias),
-          ("cu_seqlens", cu_seqlens), ("pool", pool), ("state_indices", state_indices),
-          ("cache", cache), ("out", out))
+    _cuda(x, dt, A_log, B, C, D, dt_bias, cu_seqlens, pool, state_indices, cache, out)
     cpitch = 0
     if cache is not None:
         cpitch = _step_cache(cache, "cache", N, max_steps, H * K * V, pool.dtype)
-    lib, st = _load(), _Stream(stream)
+    lib, dev = _load(), x.device
     if out is None:
-        out = st.empty((T, H, V), x.dtype, x.device)
-    ws = st.workspace(workspace, STATUS_WORKSPACE_BYTES, STATUS_WORKSPACE_BYTES, x.device)
+        out = _empty(stream, (T, H, V), x.dtype, dev)
+    ws, nws = _workspace(stream, workspace, STATUS_WORKSPACE_BYTES, dev)
     d = ssm_desc(N, T, H, G, K, V, x.dtype, pool.dtype, pool.shape[0], slot_stride)
     ins = _ssm_inputs(x, dt, A_log, B, C, D, dt_bias, pitches)
     rc = lib.kda_ssm_decode(ctypes.byref(d), ctypes.byref(ins), _p(cu_seqlens), _p(pool),
                             _p(state_indices), _p(cache), cpitch, max_steps, 1 if update_pool else 0,
-                            _p(out), _p(ws), ws.numel(), st.handle)
+                            _p(out), _p(ws), nws, _stream(stream, dev))
     _done(rc, "kda_ssm_decode", owner, ws)
     return out
 
@@ -446,39 +466,32 @@ def verify_draft(tokens, target_probs, draft_probs, accept_u, noise, cu_seqlens,
     [N+1] int32.  num_accepted counts the tokens of a request that stand, the first among them: the
     step that :func:`commit_draft` keeps.
     """
-    _ints(tokens, "tokens", (None,))
-    T = tokens.shape[0]
-    _need(target_probs, "target_probs", torch.float32, cuda=False)
-    _shape(target_probs, "target_probs", (T, None))
-    vocab = target_probs.shape[1]
+    if not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 2:
+        raise ValueError("target_probs must have shape [T, vocab]")
+    T, vocab = target_probs.shape
     if vocab == 0:
         raise ValueError("target_probs has no entries")
+    _plain(tokens, "tokens", torch.int32, (T,))
+    _plain(target_probs, "target_probs", torch.float32, (T, vocab))
     if draft_probs is not None:
-        _need(draft_probs, "draft_probs", torch.float32, cuda=False)
-        _shape(draft_probs, "draft_probs", (T, vocab))
-    _need(accept_u, "accept_u", torch.float32, cuda=False)
-    _shape(accept_u, "accept_u", (T,))
-    _ints(cu_seqlens, "cu_seqlens", (None,))
-    N = cu_seqlens.shape[0] - 1
-    if N < 0:
-        raise ValueError("cu_seqlens needs at least one element")
-    _need(noise, "noise", torch.float32, cuda=False)
-    _shape(noise, "noise", (N, vocab))
-    for name, t in (("num_accepted", num_accepted), ("next_token", next_token)):
-        if t is not None:
-            _ints(t, name, (N,))
-    _cuda(("tokens", tokens), ("target_probs", target_probs), ("draft_probs", draft_probs),
-          ("accept_u", accept_u), ("noise", noise), ("cu_seqlens", cu_seqlens),
-          ("num_accepted", num_accepted), ("next_token", next_token))
-    lib, st = _load(), _Stream(stream)
+        _plain(draft_probs, "draft_probs", torch.float32, (T, vocab))
+    _plain(accept_u, "accept_u", torch.float32, (T,))
+    N = _num_seqs(cu_seqlens)
+    _plain(noise, "noise", torch.float32, (N, vocab))
+    if num_accepted is not None:
+        _plain(num_accepted, "num_accepted", torch.int32, (N,))
+    if next_token is not None:
+        _plain(next_token, "next_token", torch.int32, (N,))
+    _cuda(tokens, target_probs, draft_probs, accept_u, noise, cu_seqlens, num_accepted, next_token)
+    lib, dev = _load(), tokens.device
     if num_accepted is None:
-        num_accepted = st.empty((N,), torch.int32, tokens.device)
+        num_accepted = _empty(stream, (N,), torch.int32, dev)
     if next_token is None:
-        next_token = st.empty((N,), torch.int32, tokens.device)
-    ws = st.workspace(workspace, STATUS_WORKSPACE_BYTES, STATUS_WORKSPACE_BYTES, tokens.device)
+        next_token = _empty(stream, (N,), torch.int32, dev)
+    ws, nws = _workspace(stream, workspace, STATUS_WORKSPACE_BYTES, dev)
     rc = lib.kda_verify_draft(N, T, vocab, _p(tokens), _p(target_probs), _p(draft_probs), _p(accept_u),
-                              _p(noise), _p(cu_seqlens), _p(num_accepted), _p(next_token), _p(ws),
-                              ws.numel(), st.handle)
+                              _p(noise), _p(cu_seqlens), _p(num_accepted), _p(next_token), _p(ws), nws,
+                              _stream(stream, dev))
     _done(rc, "kda_verify_draft", verify_draft, ws)
     return num_accepted, next_token
 
@@ -487,25 +500,26 @@ def commit_draft(cache, num_accepted, pool, state_indices=None, *, workspace=Non
     """Copies each request's state after its accepted tokens, ``cache[n, num_accepted[n] - 1]``, into
     its slot of ``pool`` (kda_commit_draft); nothing for a count of 0.  cache [N, steps, *row] of any
     step cache (rows packed, requests at any pitch); pool [num_slots, *row].  Returns the pool."""
-    _need(pool, "pool", cuda=False)
-    if pool.dim() < 2 or pool.shape[0] == 0:
-        raise ValueError(f"pool must have shape [num_slots, *row], got {list(pool.shape)}")
-    if not isinstance(cache, torch.Tensor) or cache.dim() != pool.dim() + 1 or \
-            tuple(cache.shape[2:]) != tuple(pool.shape[1:]):
+    if not (isinstance(pool, torch.Tensor) and pool.is_contiguous()):
+        _need(pool, "pool", cuda=False)
+    shape = pool.shape
+    if len(shape) < 2 or shape[0] == 0 or pool.numel() == 0:
+        raise ValueError(f"pool must have shape [num_slots, *row], got {list(shape)}")
+    if not isinstance(cache, torch.Tensor) or cache.dim() != len(shape) + 1 or \
+            cache.shape[2:] != shape[1:] or cache.shape[1] == 0:
         raise ValueError("cache must have shape [N, steps, *row] with the pool's rows")
-    _ints(num_accepted, "num_accepted", (None,))
-    N, steps, row = num_accepted.shape[0], cache.shape[1], pool[0].numel()
-    if row == 0 or steps == 0:
-        raise ValueError("cache has no states")
+    if not isinstance(num_accepted, torch.Tensor) or num_accepted.dim() != 1:
+        raise TypeError("num_accepted must be an int32 tensor of one dimension")
+    N, steps, row = num_accepted.shape[0], cache.shape[1], pool.numel() // shape[0]
+    _plain(num_accepted, "num_accepted", torch.int32, (N,))
     pitch = _step_cache(cache, "cache", N, steps, row, pool.dtype)
     if state_indices is not None:
-        _ints(state_indices, "state_indices", (N,))
-    _cuda(("cache", cache), ("num_accepted", num_accepted), ("pool", pool),
-          ("state_indices", state_indices))
-    lib, st = _load(), _Stream(stream)
-    ws = st.workspace(workspace, STATUS_WORKSPACE_BYTES, STATUS_WORKSPACE_BYTES, pool.device)
+        _plain(state_indices, "state_indices", torch.int32, (N,))
+    _cuda(cache, num_accepted, pool, state_indices)
+    lib, dev = _load(), pool.device
+    ws, nws = _workspace(stream, workspace, STATUS_WORKSPACE_BYTES, dev)
     rc = lib.kda_commit_draft(N, _dt(pool.dtype), row, _p(cache), pitch, steps, _p(num_accepted),
-                              _p(pool), pool.shape[0], 0, _p(state_indices), _p(ws), ws.numel(),
-                              st.handle)
+                              _p(pool), shape[0], 0, _p(state_indices), _p(ws), nws,
+                              _stream(stream, dev))
     _done(rc, "kda_commit_draft", commit_draft, ws)
     return pool
