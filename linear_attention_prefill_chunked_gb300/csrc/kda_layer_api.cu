@@ -172,7 +172,9 @@ kda_status_t kda_ssm_scan(const kda_desc_t* d, const kda_ssm_inputs_t* in,
   a.status = status_of(workspace);
   a.ws = static_cast<uint8_t*>(workspace);
   a.ws_bytes = workspace_bytes;
-  return launched(workspace, stream, [&] { return kda::launch_ssm_simt(a, stream); });
+  return launched(workspace, stream, [&] {
+    return kda::ssm_tc_supported(*d) ? kda::launch_ssm_tc(a, stream) : kda::launch_ssm_simt(a, stream);
+  });
 }
 
 kda_status_t kda_ssm_decode(const kda_desc_t* d, const kda_ssm_inputs_t* in,

@@ -1,0 +1,817 @@
+// kda_ssm_tc.cu -- selective state space scan of packed prompts on the tensor cores (tcgen05 +
+// TMEM + TMA), bf16 inputs.
+//
+// Per head, over chunks of L = 64 tokens (g_t = -exp(a_log) d_t <= 0 the log-decay, d_t the step):
+//
+//   M[t][s] = (c_t . b_s) exp(g_{s+1} + .. + g_t) d_s          s <= t
+//   Y = M X + diag(exp(g_1 + .. + g_t)) C S + D X              S the state before the chunk
+//   S <- exp(g_1 + .. + g_L) S + sum_s exp(g_{s+1} + .. + g_L) d_s b_s x_s^T
+//
+// Every exponent is a sum of log-decays of consecutive tokens taken over just those tokens
+// (prefixes and suffixes of 16-token blocks, and whole blocks between), so none is positive and
+// none is a small difference of large sums; a step of zero (a masked or padded token) is a zero
+// weight.
+//
+// A CTA takes 128 value columns of one sequence: two 64-wide heads of a group, or one 128-wide
+// head. Transposed accumulators (lanes = value columns) put both heads into one M = 128 product
+// with the group's B and C as the shared other operand:
+//
+//   YM [128][head, t] = X^T M^T           A = x tile (smem), B = M tile (smem)      N = 128 or 64
+//   YI [128][t]       = S^T C^T           A = S^T as bf16 (TMEM), B = c tile        N = 64
+//   S^T [128][k]     += X'^T B            A = x' tiles (smem), B = b tile           N = K
+//
+// S^T stays in TMEM in fp32 for the whole sequence. x'_s = exp(..) d_s x_s is fp32; it enters as
+// the sum of three bf16 numbers, which hold all its 24 bits (two with a bf16 pool, 2^-17), so that
+// the state keeps fp32 accuracy -- b is exact in bf16. M and the copy of S that C reads are rounded
+// to bf16 once each, like the output. The scores c . b are 16 x 16 warp-level products: both heads
+// scale the same accumulator registers, with no trip through TMEM.
+//
+// Warps 0-7 (M group): scores, M, x'.  Warps 8-15 (R group): the state's decay and bf16 copy, the
+// output.  Warp 16: issues the tcgen05 products.  Warp 17: claims items and loads tiles (TMA).
+// The M group works a chunk ahead of the R group; what orders them are mbarriers, each wait
+// bounded (a timeout sets KDA_DEVICE_PIPE_TIMEOUT, stops the loads, lets what was issued finish and
+// returns).
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstddef>
+#include <cstring>
+
+#include "kda_internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace kda {
+namespace {
+
+KDA_DEBUG_FLAG_DEFINE();
+using namespace tc;
+
+constexpr int kL = 64;          // tokens a chunk
+constexpr int kStages = 3;      // chunks of c, b and x tiles in flight
+constexpr int kMThreads = 256, kRThreads = 256;
+constexpr int kTcThreads = kMThreads + kRThreads + 64;
+constexpr int kItems = 4;       // claimed items in flight
+
+// ---- shared memory (offsets from a 1024-aligned base) -----------------------------------
+constexpr uint32_t kTileBytes = 16384;               // [2 halves][64 rows][128 B]
+constexpr uint32_t OFF_C = 0, OFF_B = kTileBytes, OFF_X = 2 * kTileBytes;  // within a stage
+constexpr uint32_t kStageBytes = 3 * kTileBytes;
+constexpr uint32_t OFF_XP = kStages * kStageBytes;   // x' as three bf16 parts, each like x
+constexpr uint32_t OFF_M = OFF_XP + 3 * kTileBytes;  // [2 heads][64 t][64 s] (K-major B)
+constexpr uint32_t OFF_Y = OFF_M + kTileBytes;       // [2 halves][64 t][64 v], to be stored
+constexpr uint32_t OFF_CTL = OFF_Y + kTileBytes;
+
+// ---- TMEM columns -------------------------------------------------------------------------
+constexpr uint32_t TM_S = 0;     // S^T fp32 (128)
+constexpr uint32_t TM_SB = 128;  // S^T as bf16 pairs (64)
+constexpr uint32_t TM_YI = 192;  // S^T C^T (64)
+constexpr uint32_t TM_YM = 256;  // X^T M^T, two buffers of 128 by chunk parity
+
+enum TcBar {
+  T_FULL = 0,                    // a stage's tiles have landed
+  T_EMPTY = T_FULL + kStages,    // a stage is free: its products are done and x was read
+  T_M = T_EMPTY + kStages,       // M and the chunk's factors are written, by chunk parity
+  T_XP = T_M + 2,                // x' is written
+  T_S,                           // S is decayed and its bf16 copy written
+  T_MX, T_Y, T_SU,               // the products of M, of C (and M), of x' are done
+  T_ITEM_FULL,
+  T_ITEM_EMPTY = T_ITEM_FULL + kItems,
+  T_DRAIN = T_ITEM_EMPTY + kItems,
+  T_COUNT
+};
+
+struct Item {
+  int32_t n, h0, nchunks, done;
+  int64_t bos, eos;
+  int64_t src, dst;   // element offsets of head h0's state, -1: zero state / not written
+};
+
+struct Ctl {
+  uint64_t bar[T_COUNT];
+  Item ring[kItems];
+  float cl[2][kL];          // [head][t]: log2-decay from the 16-token block's start through t
+  float cls[2][kL];         // cl - log2(d_s)
+  float fcol[2][kL];        // 2^(log2-decay after s to the block's end) d_s
+  float e[2][2][kL];        // [chunk parity][head][t]: decay from the chunk's start through t
+  float bt[2][4];           // [head][block]: log2-decay of a block
+  float dec[2][2];          // [chunk parity][head]: decay of the chunk
+  uint32_t tmem_base;
+  uint32_t abort;
+};
+constexpr uint32_t kTcSmem = OFF_CTL + ((sizeof(Ctl) + 15) & ~15u);
+static_assert(kTcSmem <= 232448, "shared memory budget exceeded");
+
+struct ScanParams {
+  CUtensorMap tm_x, tm_b, tm_c, tm_y;
+  const __nv_bfloat16* dt;
+  int64_t dt_pitch;
+  const float *a_log, *dt_bias, *d;
+  const int32_t *cu, *idx;
+  const void* state_in;
+  void* state_out;
+  __nv_bfloat16* y;
+  uint32_t* status;
+  uint32_t* next_item;
+  uint64_t wait_limit_ns;
+  int32_t N, H, G, V, pairs;   // pairs: items a sequence
+  int64_t T, num_slots, slot_stride;
+};
+
+__device__ __forceinline__ bool tc_aborted(const Ctl* c) {
+  return *reinterpret_cast<const volatile uint32_t*>(&c->abort) != 0u;
+}
+// Bounded wait; after a timeout anywhere in the CTA every wait returns at once (false).
+__device__ __noinline__ bool tc_wait_slow(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                          uint32_t* abort_flag, uint32_t* status) {
+  const bool poll = limit_ns < kSleepHintNs;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (poll ? mbar_test_wait(bar, parity) : mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
+    if (*reinterpret_cast<volatile uint32_t*>(abort_flag) != 0u) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      if (atomicExch(abort_flag, 1u) == 0u) raise_status(status, KDA_DEVICE_PIPE_TIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool tc_wait(const ScanParams& p, Ctl* c, int b, uint32_t parity) {
+  if (mbar_test_wait(&c->bar[b], parity)) return true;
+  return tc_wait_slow(&c->bar[b], parity, p.wait_limit_ns, &c->abort, p.status);
+}
+// One arrival a warp, after what its lanes wrote.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t saddr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr));
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
+      " {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Reads ring entry k (whole group, uniform result) and releases it.
+__device__ __forceinline__ Item tc_item(const ScanParams& p, Ctl* c, uint32_t k, uint32_t bar_id,
+                                        uint32_t nthreads, bool leader) {
+  const int slot = k % kItems;
+  const bool ok = tc_wait(p, c, T_ITEM_FULL + slot, (k / kItems) & 1);
+  Item it = c->ring[slot];
+  const bool stop = named_bar_any(bar_id, nthreads, !ok || it.done != 0 || tc_aborted(c));
+  if (leader && ok) mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
+  it.done = stop ? 1 : 0;
+  return it;
+}
+
+constexpr uint32_t BAR_MG = 1, BAR_RGRP = 2;
+
+// ---- warp 17: items and tiles ------------------------------------------------------------
+template <int K>
+__device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
+  if ((threadIdx.x & 31) != 0) return;
+  const uint32_t total = (uint32_t)p.N * (uint32_t)p.pairs;
+  const int rep = p.H / p.G;                       // heads a group
+  const int per = p.V == 64 ? (rep + 1) / 2 : rep; // items a group
+  uint32_t j = 0;                                  // chunks loaded by this CTA
+  for (uint32_t k = 0;; ++k) {
+    Item it{};
+    for (;;) {
+      const uint32_t w = tc_aborted(c) ? total : atomicAdd(p.next_item, 1u);
+      if (w >= total) {
+        it.done = 1;
+        break;
+      }
+      const int n = (int)(w / (uint32_t)p.pairs), q = (int)(w % (uint32_t)p.pairs);
+      int64_t bos, eos;
+      if (!seq_bounds(p.cu, n, p.T, &bos, &eos)) {
+        raise_status(p.status, KDA_DEVICE_BAD_SEQLENS);
+        continue;
+      }
+      int64_t slot = n;
+      if (p.idx) {
+        slot = resolve_slot(p.idx, n, p.num_slots);
+        if (slot < 0) {
+          raise_status(p.status, KDA_DEVICE_BAD_SLOT);
+          continue;
+        }
+      }
+      const int g = q / per, i = q % per;
+      it.n = n;
+      it.h0 = g * rep + (p.V == 64 ? 2 * i : i);
+      it.bos = bos;
+      it.eos = eos;
+      it.nchunks = (int)((eos - bos + kL - 1) / kL);
+      const int64_t at = slot * p.slot_stride + (int64_t)it.h0 * K * p.V;
+      it.src = p.state_in ? at : -1;
+      it.dst = p.state_out ? at : -1;
+      break;
+    }
+    const int slot = k % kItems;
+    if (k >= (uint32_t)kItems && !tc_wait(p, c, T_ITEM_EMPTY + slot, (k / kItems - 1) & 1)) break;
+    c->ring[slot] = it;
+    mbar_arrive(&c->bar[T_ITEM_FULL + slot]);
+    if (it.done) break;
+    const int g = it.h0 / rep;
+    const bool second = p.V == 128 || (it.h0 % rep) + 1 < rep;
+    const uint32_t bytes = 2u * (K / 64) * 8192u + (second ? 16384u : 8192u);
+    for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
+      const uint32_t st = j % kStages;
+      if (j >= (uint32_t)kStages && !tc_wait(p, c, T_EMPTY + st, (j / kStages - 1) & 1)) break;
+      if (tc_aborted(c)) break;
+      uint8_t* base = sm + st * kStageBytes;
+      uint64_t* bar = &c->bar[T_FULL + st];
+      const int t0 = (int)(it.bos + (int64_t)ch * kL);
+      mbar_expect_tx(bar, bytes);
+#pragma unroll
+      for (int half = 0; half < K / 64; ++half) {
+        tma_load_2d(base + OFF_C + half * 8192, &p.tm_c, bar, g * K + half * 64, t0);
+        tma_load_2d(base + OFF_B + half * 8192, &p.tm_b, bar, g * K + half * 64, t0);
+      }
+      tma_load_2d(base + OFF_X, &p.tm_x, bar, it.h0 * p.V, t0);
+      if (second) tma_load_2d(base + OFF_X + 8192, &p.tm_x, bar, it.h0 * p.V + 64, t0);
+    }
+    if (tc_aborted(c)) break;
+  }
+  // every load that was issued has landed before the CTA may leave
+  for (uint32_t i = j > (uint32_t)kStages ? j - kStages : 0; i < j; ++i)
+    mbar_wait(&c->bar[T_FULL + i % kStages], (i / kStages) & 1);
+}
+
+// ---- warp 16: the products ------------------------------------------------------------------
+template <int K, int PARTS>
+__device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
+  if ((threadIdx.x & 31) != 0) return;
+  const uint32_t sbase = smem_u32(sm);
+  const int mn = p.V == 64 ? 128 : 64;   // columns of YM: (head, t)
+  const uint32_t id_m = idesc_bf16(128, mn, 1, 0), id_c = idesc_bf16(128, kL, 0, 0),
+                 id_s = idesc_bf16(128, K, 1, 1);
+  uint32_t j = 0;
+  for (uint32_t k = 0;; ++k) {
+    const int slot = k % kItems;
+    if (!tc_wait(p, c, T_ITEM_FULL + slot, (k / kItems) & 1)) break;
+    const int nchunks = c->ring[slot].nchunks, done = c->ring[slot].done;
+    mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
+    if (done) break;
+    bool ok = true;
+    for (int ch = 0; ch < nchunks && ok; ++ch, ++j) {
+      const uint32_t st = j % kStages, stage = sbase + st * kStageBytes;
+      ok = tc_wait(p, c, T_FULL + st, (j / kStages) & 1) &&
+           tc_wait(p, c, T_M + (j & 1), (j >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t ym = tbase + TM_YM + (j & 1) * 128;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        mma_bf16(ym, sdesc_sw128(stage + OFF_X + ks * 2048, 8192, 1024),
+                 sdesc_sw128(sbase + OFF_M + ks * 32, 16, 1024), id_m, ks > 0 ? 1u : 0u);
+      mma_commit(&c->bar[T_MX]);
+      ok = tc_wait(p, c, T_S, j & 1);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < K / 16; ++ks)
+        mma_bf16_ta(tbase + TM_YI, tbase + TM_SB + ks * 8,
+                    sdesc_sw128(stage + OFF_C + (ks / 4) * 8192 + (ks % 4) * 32, 16, 1024), id_c,
+                    ks > 0 ? 1u : 0u);
+      mma_commit(&c->bar[T_Y]);
+      ok = tc_wait(p, c, T_XP, j & 1);
+      if (!ok) break;
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_bf16(tbase + TM_S, sdesc_sw128(sbase + OFF_XP + part * kTileBytes + ks * 2048, 8192, 1024),
+                   sdesc_sw128(stage + OFF_B + ks * 2048, 8192, 1024), id_s, 1u);
+      }
+      mma_commit(&c->bar[T_SU]);
+      mma_commit(&c->bar[T_EMPTY + st]);
+    }
+    if (!ok) break;
+  }
+  mma_commit(&c->bar[T_DRAIN]);
+  mbar_wait(&c->bar[T_DRAIN], 0);  // the full limit, aborted or not
+}
+
+// ---- warps 0-7: scores, M and x' --------------------------------------------------------------
+// 16 x 16 tiles of the scores, lower block triangle: warp -> row block, first column block, count.
+// The diagonal tiles cost more (an exponential an element), warps 6 and 7 also scan the steps.
+__device__ __forceinline__ void tile_of(int warp, int& tb, int& sb, int& n) {
+  // tiles (row block, column block): w0 (3,0)(3,1)  w1 (3,2)(3,3)  w2 (2,0)(2,1)  w3 (2,2)
+  //                                  w4 (1,0)       w5 (1,1)       w6 (0,0)       w7 none
+  const uint32_t tbs = 0x00112233u, sbs = 0x00102020u, ns = 0x01111222u;
+  tb = (tbs >> (warp * 4)) & 15;
+  sb = (sbs >> (warp * 4)) & 15;
+  n = (ns >> (warp * 4)) & 15;
+}
+
+// Steps and decays of one head's chunk, by one warp; lane l has tokens 2 l and 2 l + 1.
+__device__ __forceinline__ void scan_steps(Ctl* c, int head, uint32_t par, float d0, float d1,
+                                           float rate2, int lane) {
+  const float g0 = rate2 * d0, g1 = rate2 * d1;  // log2-decays
+  const float pair = g0 + g1;
+  float up = pair, dn = pair;  // inclusive sums over the block's 8 lanes, from either end
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const float a = __shfl_up_sync(0xffffffffu, up, o, 8);
+    const float b = __shfl_down_sync(0xffffffffu, dn, o, 8);
+    if ((lane & 7) >= o) up += a;
+    if ((lane & 7) + o < 8) dn += b;
+  }
+  float before = __shfl_up_sync(0xffffffffu, up, 1, 8);
+  float after = __shfl_down_sync(0xffffffffu, dn, 1, 8);
+  if ((lane & 7) == 0) before = 0.f;
+  if ((lane & 7) == 7) after = 0.f;
+  float bt[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) bt[b] = __shfl_sync(0xffffffffu, up, b * 8 + 7);
+  const int blk = lane >> 3;
+  const float pre = blk == 0 ? 0.f : blk == 1 ? bt[0] : blk == 2 ? bt[0] + bt[1] : bt[0] + bt[1] + bt[2];
+  const float c0 = before + g0, c1 = up;
+  const int t = 2 * lane;
+  *reinterpret_cast<float2*>(&c->cl[head][t]) = make_float2(c0, c1);
+  *reinterpret_cast<float2*>(&c->cls[head][t]) = make_float2(c0 - __log2f(d0), c1 - __log2f(d1));
+  *reinterpret_cast<float2*>(&c->fcol[head][t]) = make_float2(ex2(after + g1) * d0, ex2(after) * d1);
+  *reinterpret_cast<float2*>(&c->e[par][head][t]) = make_float2(ex2(pre + c0), ex2(pre + c1));
+  if (lane < 4) c->bt[head][lane] = bt[lane & 3];
+  if (lane == 0) c->dec[par][head] = ex2((bt[0] + bt[1]) + (bt[2] + bt[3]));
+}
+
+// x' (8 values) as PARTS bf16 numbers each: truncated parts leave exact remainders.
+template <int PARTS>
+__device__ __forceinline__ void split_x(const uint4& raw, float w, uint4 (&out)[PARTS]) {
+  const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t o[PARTS][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = bf_lo(in[i]) * w, b = bf_hi(in[i]) * w;
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) {
+      if (q == PARTS - 1) {
+        o[q][i] = pack_bf16x2(a, b);
+      } else {
+        const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+        o[q][i] = __byte_perm(ua, ub, 0x7632);
+        a -= __uint_as_float(ua & 0xffff0000u);
+        b -= __uint_as_float(ub & 0xffff0000u);
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < PARTS; ++q) out[q] = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
+}
+
+template <int K, int PARTS>
+__device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sbase = smem_u32(sm);
+  const int rep = p.H / p.G;
+  const int heads = p.V == 64 ? 2 : 1;
+  int tb, sb0, ntile;
+  tile_of(warp, tb, sb0, ntile);
+  // the blocks of M above the diagonal are never written again
+  for (uint32_t i = tid; i < kTileBytes / 16; i += kMThreads)
+    *reinterpret_cast<uint4*>(sm + OFF_M + i * 16) = make_uint4(0, 0, 0, 0);
+
+  const bool scans = warp >= 8 - heads;   // warp 7 scans head 0, warp 6 head 1
+  const int sh = 7 - warp;
+  uint32_t j = 0;
+  for (uint32_t k = 0;; ++k) {
+    const Item it = tc_item(p, c, k, BAR_MG, kMThreads, tid == 0);
+    if (it.done) return;
+    const bool second = p.V == 128 || (it.h0 % rep) + 1 < rep;
+    const bool mine = scans && (sh == 0 || second);
+    float rate2 = 0.f, bias = 0.f;
+    if (mine) {
+      rate2 = -expf(p.a_log[it.h0 + sh]) * 1.4426950408889634f;
+      bias = p.dt_bias ? p.dt_bias[it.h0 + sh] : 0.f;
+    }
+    // the steps are read a chunk ahead of their scan
+    const __nv_bfloat16* dtp = p.dt + it.h0 + sh;
+    auto load_dt = [&](int ch, float& a, float& b) {
+      const int64_t t = it.bos + (int64_t)ch * kL + 2 * lane;
+      a = mine && t < it.eos ? to_f32(dtp[t * p.dt_pitch]) : -INFINITY;
+      b = mine && t + 1 < it.eos ? to_f32(dtp[(t + 1) * p.dt_pitch]) : -INFINITY;
+    };
+    float n0 = -INFINITY, n1 = -INFINITY;
+    if (scans && it.nchunks > 0) load_dt(0, n0, n1);
+    for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
+      const uint32_t st = j % kStages, par = j & 1;
+      uint8_t* stage = sm + st * kStageBytes;
+      const uint32_t sstage = sbase + st * kStageBytes;
+      const int64_t left = it.eos - it.bos - (int64_t)ch * kL;
+      const int m = left < kL ? (int)left : kL;
+      tc_wait(p, c, T_FULL + st, (j / kStages) & 1);
+      // the rows after the sequence's last token are another's (or nobody's): they must not reach
+      // a product, where a zero weight would not hide an infinity
+      if (m < kL) {
+        const int rows = kL - m;
+        for (int i = tid; i < rows * 32; i += kMThreads) {
+          const uint32_t tile = (i >> 3) & 3;  // b and x, two halves each
+          *reinterpret_cast<uint4*>(stage + OFF_B + tile * 8192 + sw128_off(m + (i >> 5), i & 7)) =
+              make_uint4(0, 0, 0, 0);
+        }
+      }
+      // scores
+      float acc[2][2][4] = {};
+      if (ntile > 0) {
+#pragma unroll
+        for (int ks = 0; ks < K / 16; ++ks) {
+          uint32_t a[4];
+          const uint32_t kc = ks * 2;  // 16-byte chunk of the k range
+          {
+            const uint32_t q = kc + (lane >> 4);
+            ldsm_x4(a, sstage + OFF_C + (q >> 3) * 8192 + sw128_off(tb * 16 + (lane & 15), q & 7));
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (i < ntile) {
+              uint32_t b[4];
+              const uint32_t q = kc + ((lane >> 3) & 1);
+              ldsm_x4(b, sstage + OFF_B + (q >> 3) * 8192 +
+                             sw128_off((sb0 + i) * 16 + ((lane >> 4) << 3) + (lane & 7), q & 7));
+              mma_16816(acc[i][0], a, b[0], b[1]);
+              mma_16816(acc[i][1], a, b[2], b[3]);
+            }
+          }
+        }
+      }
+      if (scans) {
+        // the factors by chunk parity: their reader two chunks back has left the stage it shared
+        if (j >= 2) tc_wait(p, c, T_EMPTY + (j - 2) % kStages, ((j - 2) / kStages) & 1);
+        const float d0 = n0 == -INFINITY ? 0.f : ssm_step(n0, bias);
+        const float d1 = n1 == -INFINITY ? 0.f : ssm_step(n1, bias);
+        scan_steps(c, sh, par, d0, d1, rate2, lane);
+        if (ch + 1 < it.nchunks) load_dt(ch + 1, n0, n1);
+      }
+      if (named_bar_any(BAR_MG, kMThreads, tc_aborted(c))) return;  // factors and cleared rows
+      // M, once the product that read the last one is done
+      if (j > 0) tc_wait(p, c, T_MX, (j - 1) & 1);
+#pragma unroll
+      for (int hd = 0; hd < 2; ++hd) {
+        if (hd >= heads) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i >= ntile) break;
+          const int sb = sb0 + i, r = tb * 16 + (lane >> 2);
+          const float cl0 = c->cl[hd][r], cl1 = c->cl[hd][r + 8];
+          float f0 = 0.f, f1 = 0.f;
+          if (sb < tb) {
+            float mid = 0.f;
+#pragma unroll
+            for (int b = 1; b < 3; ++b)
+              if (b > sb && b < tb) mid += c->bt[hd][b];
+            f0 = ex2(cl0 + mid);
+            f1 = ex2(cl1 + mid);
+          }
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const int s = sb * 16 + nt * 8 + 2 * (lane & 3);
+            float v[4] = {acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]};
+            if (sb < tb) {
+              const float2 fc = *reinterpret_cast<const float2*>(&c->fcol[hd][s]);
+              v[0] *= f0 * fc.x; v[1] *= f0 * fc.y;
+              v[2] *= f1 * fc.x; v[3] *= f1 * fc.y;
+            } else {
+              const float2 cs = *reinterpret_cast<const float2*>(&c->cls[hd][s]);
+              v[0] = s <= r ? v[0] * ex2(cl0 - cs.x) : 0.f;
+              v[1] = s + 1 <= r ? v[1] * ex2(cl0 - cs.y) : 0.f;
+              v[2] = s <= r + 8 ? v[2] * ex2(cl1 - cs.x) : 0.f;
+              v[3] = s + 1 <= r + 8 ? v[3] * ex2(cl1 - cs.y) : 0.f;
+            }
+            uint8_t* mt = sm + OFF_M + hd * 8192 + (s & 7) * 2;
+            *reinterpret_cast<uint32_t*>(mt + sw128_off(r, s >> 3)) = pack_bf16x2(v[0], v[1]);
+            *reinterpret_cast<uint32_t*>(mt + sw128_off(r + 8, s >> 3)) = pack_bf16x2(v[2], v[3]);
+          }
+        }
+      }
+      fence_async_smem();
+      warp_arrive(&c->bar[T_M + par]);
+      // x', written once the product that read the last one is done
+      uint4 parts[4][PARTS];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = (i & 1) * 32 + (tid >> 3), half = i >> 1;
+        const int hd = heads == 2 ? half : 0, blk = row >> 4;
+        float late = 0.f;
+#pragma unroll
+        for (int b = 1; b < 4; ++b)
+          if (b > blk) late += c->bt[hd][b];
+        const float w = (half == 1 && !second) ? 0.f : c->fcol[hd][row] * ex2(late);
+        const uint4 raw = *reinterpret_cast<const uint4*>(stage + OFF_X + half * 8192 +
+                                                          sw128_off(row, tid & 7));
+        split_x<PARTS>(raw, w, parts[i]);
+      }
+      if (j > 0) tc_wait(p, c, T_SU, (j - 1) & 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t at = (i >> 1) * 8192 + sw128_off((i & 1) * 32 + (tid >> 3), tid & 7);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q)
+          *reinterpret_cast<uint4*>(sm + OFF_XP + q * kTileBytes + at) = parts[i][q];
+      }
+      fence_async_smem();
+      warp_arrive(&c->bar[T_XP]);
+      // the next chunk's scan overwrites cl, cls, fcol and bt
+      named_bar(BAR_MG, kMThreads);
+    }
+  }
+}
+
+// ---- warps 8-15: the state and the output ------------------------------------------------------
+// Two warps a TMEM lane quadrant: each takes half of S^T's k columns and half of the tokens.
+template <typename ST, int K>
+__device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
+  constexpr int KH = K / 2;                      // k columns a thread
+  const int rt = threadIdx.x - kMThreads, warp = rt >> 5, lane = rt & 31;
+  const int quad = (threadIdx.x >> 5) & 3, hf = warp >> 2;
+  const int v = quad * 32 + lane;                // value column of the item (TMEM lane)
+  const uint32_t tq = tbase + ((uint32_t)(quad * 32) << 16);
+  const int hd = p.V == 64 ? v >> 6 : 0;         // head of the item
+  const int vh = p.V == 64 ? v & 63 : v;         // column of that head
+  const int half = v >> 6;
+  const int rep = p.H / p.G;
+  uint32_t j = 0;
+  for (uint32_t k = 0;; ++k) {
+    const Item it = tc_item(p, c, k, BAR_RGRP, kRThreads, rt == 0);
+    if (it.done) break;
+    const bool second = p.V == 128 || (it.h0 % rep) + 1 < rep;
+    const bool real = half == 0 || second;
+    const int h = it.h0 + hd;
+    const float dskip = p.d && real ? p.d[h] : 0.f;
+    const int64_t so = (int64_t)hd * K * p.V + vh + (int64_t)hf * KH * p.V;  // within the item's state
+    const ST* src = it.src >= 0 && real ? static_cast<const ST*>(p.state_in) + it.src + so : nullptr;
+    ST* dst = it.dst >= 0 && real ? static_cast<ST*>(p.state_out) + it.dst + so : nullptr;
+    if (it.nchunks == 0) {  // an empty sequence keeps its state
+      if (dst && (const void*)dst != (const void*)src)
+        for (int i = 0; i < KH; ++i)
+          dst[(int64_t)i * p.V] = src ? src[(int64_t)i * p.V] : from_f32<ST>(0.f);
+      continue;
+    }
+    for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
+      const uint32_t st = j % kStages, par = j & 1;
+      const int64_t t0 = it.bos + (int64_t)ch * kL;
+      const int m = it.eos - t0 < kL ? (int)(it.eos - t0) : kL;
+      // S before the chunk: its bf16 copy for the product with C, and its decay over the chunk
+      if (ch == 0) {
+        float s[KH];
+#pragma unroll
+        for (int i = 0; i < KH; ++i) s[i] = src ? to_f32(src[(int64_t)i * p.V]) : 0.f;
+        tc_wait(p, c, T_M + par, (j >> 1) & 1);
+        const float dec = c->dec[par][hd];
+#pragma unroll
+        for (int i0 = 0; i0 < KH; i0 += 32) {
+          float pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            pk[i] = __uint_as_float(pack_bf16x2(s[i0 + 2 * i], s[i0 + 2 * i + 1]));
+          tmem_st16(tq + TM_SB + (hf * KH + i0) / 2, pk);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i0 + i] *= dec;
+          tmem_st16(tq + TM_S + hf * KH + i0, s + i0);
+          tmem_st16(tq + TM_S + hf * KH + i0 + 16, s + i0 + 16);
+        }
+      } else {
+        tc_wait(p, c, T_M + par, (j >> 1) & 1);
+        const float dec = c->dec[par][hd];
+        tc_wait(p, c, T_SU, (j - 1) & 1);
+        tc_fence_after();
+#pragma unroll
+        for (int i0 = 0; i0 < KH; i0 += 32) {
+          float s[32], pk[16];
+          tmem_ld16(tq + TM_S + hf * KH + i0, s);
+          tmem_ld16(tq + TM_S + hf * KH + i0 + 16, s + 16);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            pk[i] = __uint_as_float(pack_bf16x2(s[2 * i], s[2 * i + 1]));
+          tmem_st16(tq + TM_SB + (hf * KH + i0) / 2, pk);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] *= dec;
+          tmem_st16(tq + TM_S + hf * KH + i0, s);
+          tmem_st16(tq + TM_S + hf * KH + i0 + 16, s + 16);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&c->bar[T_S]);
+      // the output of tokens [32 hf, + 32): the y tile's last store has read it
+      if (rt == 0) bulk_wait_read();
+      if (named_bar_any(BAR_RGRP, kRThreads, tc_aborted(c))) goto leave;
+      {
+        tc_wait(p, c, T_FULL + st, (j / kStages) & 1);  // x was loaded long ago: its visibility
+        tc_wait(p, c, T_Y, j & 1);
+        tc_fence_after();
+        const uint8_t* xt = sm + st * kStageBytes + OFF_X + half * 8192 + (v & 7) * 2;
+        const uint32_t vc = (v & 63) >> 3;
+        uint8_t* yt = sm + OFF_Y + half * 8192 + (v & 63) * 2;
+        const bool full = m == kL;
+        __nv_bfloat16* yg = p.y + (t0 * p.H + h) * p.V + vh;
+        const int64_t yrow = (int64_t)p.H * p.V;
+#pragma unroll
+        for (int i0 = 0; i0 < 32; i0 += 16) {
+          const int tt = hf * 32 + i0;
+          float a[16], b[16];
+          tmem_ld16(tq + TM_YI + tt, a);
+          tmem_ld16(tq + TM_YM + par * 128 + (p.V == 64 ? hd * 64 : 0) + tt, b);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int t = tt + i;
+            const float x = to_f32(*reinterpret_cast<const __nv_bfloat16*>(xt + sw128_off(t, vc)));
+            const float r = fmaf(dskip, x, fmaf(c->e[par][hd][t], a[i], b[i]));
+            if (full) {
+              *reinterpret_cast<__nv_bfloat16*>(yt + t * 128) = __float2bfloat16_rn(r);
+            } else if (t < m && real && KDA_CHECK(t0 + t < p.T)) {
+              yg[t * yrow] = __float2bfloat16_rn(r);
+            }
+          }
+        }
+        tc_fence_before();
+        warp_arrive(&c->bar[T_EMPTY + st]);
+        if (full) {
+          fence_async_smem();
+          named_bar(BAR_RGRP, kRThreads);
+          if (rt == 0 && KDA_CHECK(t0 + kL <= p.T)) {
+            tma_store_2d(&p.tm_y, sm + OFF_Y, it.h0 * p.V, (int)t0);
+            if (second) tma_store_2d(&p.tm_y, sm + OFF_Y + 8192, it.h0 * p.V + 64, (int)t0);
+            bulk_commit();
+          }
+        }
+      }
+    }
+    // the state after the sequence
+    tc_wait(p, c, T_SU, (j - 1) & 1);
+    tc_fence_after();
+    if (named_bar_any(BAR_RGRP, kRThreads, tc_aborted(c))) break;
+    {
+#pragma unroll
+      for (int i0 = 0; i0 < KH; i0 += 32) {
+        float s[32];
+        tmem_ld16(tq + TM_S + hf * KH + i0, s);
+        tmem_ld16(tq + TM_S + hf * KH + i0 + 16, s + 16);
+        tmem_ld_wait();
+        if (dst) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) dst[(int64_t)(i0 + i) * p.V] = from_f32<ST>(s[i]);
+        }
+      }
+      tc_fence_before();
+    }
+  }
+leave:
+  if (rt == 0) bulk_wait_all();
+}
+
+template <typename ST, int K>
+__global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid_constant__ ScanParams p) {
+  constexpr int PARTS = sizeof(ST) == 4 ? 3 : 2;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  Ctl* c = reinterpret_cast<Ctl*>(sm + OFF_CTL);
+  const int warp = threadIdx.x >> 5;
+  if (smem_u32(sm) & 1023u) {  // the swizzled tiles need it; the window starts so without static smem
+    if (threadIdx.x == 0) raise_status(p.status, KDA_DEVICE_PIPE_TIMEOUT);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < T_COUNT; ++b) {
+      uint32_t count = 1;                                   // a loader's or a commit's arrival
+      if (b >= T_EMPTY && b < T_EMPTY + kStages) count = 1 + kRThreads / 32;
+      if (b == T_M || b == T_M + 1 || b == T_XP || b == T_S) count = 8;  // one a warp
+      if (b >= T_ITEM_EMPTY && b < T_ITEM_EMPTY + kItems) count = 3;
+      mbar_init(&c->bar[b], count);
+    }
+    c->abort = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&p.tm_x);
+    prefetch_tensormap(&p.tm_b);
+    prefetch_tensormap(&p.tm_c);
+    prefetch_tensormap(&p.tm_y);
+  }
+  if (warp == 16) tmem_alloc(&c->tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = c->tmem_base;
+  if (warp < 8) run_mgroup<K, PARTS>(p, sm, c);
+  else if (warp < 16) run_rgroup<ST, K>(p, sm, c, tbase);
+  else if (warp == 16) run_issuer<K, PARTS>(p, sm, c, tbase);
+  else run_loader<K>(p, sm, c);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 16) tmem_dealloc(tbase, 512);
+  if (threadIdx.x == 0) KDA_DEBUG_FOLD(p.status);
+}
+
+// ---- host ----------------------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 tc_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// [T, cols] bf16 rows `pitch` elements apart, boxes of 64 tokens x 64 columns.
+bool tc_map(CUtensorMap* m, const void* base, int64_t T, int64_t cols, int64_t pitch, bool swizzle) {
+  auto enc = tc_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)(T > 0 ? T : 1)};
+  cuuint64_t strides[1] = {(cuuint64_t)pitch * 2};
+  cuuint32_t box[2] = {64u, (cuuint32_t)kL};
+  cuuint32_t es[2] = {1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int tc_sms() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+    return v > 0 ? v : 1;
+  }();
+  return n;
+}
+
+template <typename ST, int K>
+cudaError_t launch_k(const ScanParams& p, int grid, cudaStream_t st) {
+  auto kern = ssm_scan_tc_kernel<ST, K>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
+  if (err != cudaSuccess) return err;
+  kern<<<grid, kTcThreads, kTcSmem, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool ssm_tc_supported(const kda_desc_t& d) {
+  return d.qkv_dtype == KDA_BF16 && (d.flags & KDA_FLAG_CUDA_CORE_PATH) == 0u &&
+         d.total_tokens > 0 && d.total_tokens < (int64_t)1 << 31;
+}
+
+cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t st) {
+  const kda_desc_t& d = a.d;
+  const int H = d.num_v_heads, G = d.num_k_heads, K = d.head_k_dim, V = d.head_v_dim;
+  ScanParams p;
+  memset(&p, 0, sizeof(p));
+  const int64_t T = d.total_tokens;
+  if (!tc_map(&p.tm_x, a.in.x, T, (int64_t)H * V, a.in.x_pitch, true) ||
+      !tc_map(&p.tm_b, a.in.b, T, (int64_t)G * K, a.in.b_pitch, true) ||
+      !tc_map(&p.tm_c, a.in.c, T, (int64_t)G * K, a.in.c_pitch, true) ||
+      !tc_map(&p.tm_y, a.y, T, (int64_t)H * V, (int64_t)H * V, false))
+    return cudaErrorInvalidValue;
+  p.dt = static_cast<const __nv_bfloat16*>(a.in.dt);
+  p.dt_pitch = a.in.dt_pitch;
+  p.a_log = a.in.a_log;
+  p.dt_bias = a.in.dt_bias;
+  p.d = a.in.d;
+  p.cu = a.cu;
+  p.idx = a.idx;
+  p.state_in = a.state_in;
+  p.state_out = a.state_out;
+  p.y = static_cast<__nv_bfloat16*>(a.y);
+  WsHeader* hdr = reinterpret_cast<WsHeader*>(a.ws);
+  p.status = &hdr->status;
+  p.next_item = &hdr->next_item;
+  p.wait_limit_ns = pipeline_wait_limit_ns();
+  p.N = d.num_seqs;
+  p.H = H;
+  p.G = G;
+  p.V = V;
+  p.T = T;
+  p.num_slots = d.num_slots;
+  p.slot_stride = a.slot_stride;
+  const int rep = H / G;
+  p.pairs = G * (V == 64 ? (rep + 1) / 2 : rep);
+  // the status word and the item counter start every call at zero
+  cudaError_t err = cudaMemsetAsync(a.ws, 0, sizeof(WsHeader), st);
+  if (err != cudaSuccess) return err;
+  const int grid = (int)std::min<int64_t>(tc_sms(), (int64_t)p.N * p.pairs);
+  if (d.state_dtype == KDA_BF16)
+    return K == 128 ? launch_k<__nv_bfloat16, 128>(p, grid, st) : launch_k<__nv_bfloat16, 64>(p, grid, st);
+  return K == 128 ? launch_k<float, 128>(p, grid, st) : launch_k<float, 64>(p, grid, st);
+}
+
+}  // namespace kda
