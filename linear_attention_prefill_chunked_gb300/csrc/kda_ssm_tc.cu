@@ -7,27 +7,30 @@
 //   Y = M X + diag(exp(g_1 + .. + g_t)) C S + D X              S the state before the chunk
 //   S <- exp(g_1 + .. + g_L) S + sum_s exp(g_{s+1} + .. + g_L) d_s b_s x_s^T
 //
-// Every exponent is a sum of log-decays of consecutive tokens taken over just those tokens
-// (prefixes and suffixes of 16-token blocks, and whole blocks between), so none is positive and
-// none is a small difference of large sums; a step of zero (a masked or padded token) is a zero
-// weight.
+// Every exponent is a sum of log-decays of consecutive tokens, so none is positive. Prefixes and
+// suffixes are taken over halves of 32 tokens and across halves they add up, so that a difference
+// of prefixes (within a half) cancels no more than those 32 tokens' sum; a step of zero (a padded
+// token) is a zero weight.
 //
 // A CTA takes 128 value columns of one sequence: two 64-wide heads of a group, or one 128-wide
 // head. Transposed accumulators (lanes = value columns) put both heads into one M = 128 product
 // with the group's B and C as the shared other operand:
 //
-//   YM [128][head, t] = X^T M^T           A = x tile (smem), B = M tile (smem)      N = 128 or 64
-//   YI [128][t]       = S^T C^T           A = S^T as bf16 (TMEM), B = c tile        N = 64
-//   S^T [128][k]     += X'^T B            A = x' tiles (smem), B = b tile           N = K
+//   G [64 t][s]        = C B^T            A = c tile, B = b tile                  N = 64
+//   YM [128][head, t]  = X^T M^T          A = x tile, B = M tile                  N = 128 or 64
+//   YI [128][t]        = S^T C^T          A = S^T as bf16 (TMEM), B = c tile      N = 64
+//   S^T [128][k]      += X'^T B           A = x' tiles, B = b tile                N = K
 //
 // S^T stays in TMEM in fp32 for the whole sequence. x'_s = exp(..) d_s x_s is fp32; it enters as
 // the sum of three bf16 numbers, which hold all its 24 bits (two with a bf16 pool, 2^-17), so that
 // the state keeps fp32 accuracy -- b is exact in bf16. M and the copy of S that C reads are rounded
-// to bf16 once each, like the output. The scores c . b are 16 x 16 warp-level products: both heads
-// scale the same accumulator registers, with no trip through TMEM.
+// to bf16 once each, like the output. (The scores as 16 x 16 warp-level products, which need no trip
+// through TMEM, took 2100 cycles a chunk against some 500 of the tensor pipe: 516 us a call for
+// 32768 tokens against XXX.)
 //
-// Warps 0-7 (M group): scores, M, x'.  Warps 8-15 (R group): the state's decay and bf16 copy, the
-// output.  Warp 16: issues the tcgen05 products.  Warp 17: claims items and loads tiles (TMA).
+// Warps 0, 1, 4, 5 make M from the scores (their TMEM lanes hold the 64 rows), warps 2, 3, 6, 7 scan
+// the steps and make x'; warps 8-15 (R group): the state's decay and bf16 copy, the output. Warp 16
+// issues the tcgen05 products, warp 17 claims items and loads tiles (TMA).
 // The M group works a chunk ahead of the R group; what orders them are mbarriers, each wait
 // bounded (a timeout sets KDA_DEVICE_PIPE_TIMEOUT, stops the loads, lets what was issued finish and
 // returns).
@@ -65,16 +68,18 @@ constexpr uint32_t OFF_CTL = OFF_Y + kTileBytes;
 constexpr uint32_t TM_S = 0;     // S^T fp32 (128)
 constexpr uint32_t TM_SB = 128;  // S^T as bf16 pairs (64)
 constexpr uint32_t TM_YI = 192;  // S^T C^T (64)
-constexpr uint32_t TM_YM = 256;  // X^T M^T, two buffers of 128 by chunk parity
+constexpr uint32_t TM_YM = 256;  // X^T M^T, two buffers of 128 by chunk parity; before it the scores
 
 enum TcBar {
   T_FULL = 0,                    // a stage's tiles have landed
   T_EMPTY = T_FULL + kStages,    // a stage is free: its products are done and x was read
   T_M = T_EMPTY + kStages,       // M and the chunk's factors are written, by chunk parity
-  T_XP = T_M + 2,                // x' is written
+  T_EPI = T_M + 2,               // the output that used the chunk's factors is formed, by parity
+  T_XP = T_EPI + 2,              // x' is written
   T_S,                           // S is decayed and its bf16 copy written
   T_MX, T_Y, T_SU,               // the products of M, of C (and M), of x' are done
-  T_ITEM_FULL,
+  T_G,                           // the scores are done, by chunk parity
+  T_ITEM_FULL = T_G + 2,
   T_ITEM_EMPTY = T_ITEM_FULL + kItems,
   T_DRAIN = T_ITEM_EMPTY + kItems,
   T_COUNT
@@ -89,11 +94,12 @@ struct Item {
 struct Ctl {
   uint64_t bar[T_COUNT];
   Item ring[kItems];
-  float cl[2][kL];          // [head][t]: log2-decay from the 16-token block's start through t
-  float cls[2][kL];         // cl - log2(d_s)
-  float fcol[2][kL];        // 2^(log2-decay after s to the block's end) d_s
+  // by [head][token], in log2; a half is 32 tokens
+  alignas(16) float cl[2][kL];  // decay from the half's start through t
+  float same[2][kL];        // log2(d_s) - cl: + cl_t is the weight of s for t in its half
+  float later[2][kL];       // log2(d_s) + decay after s to its half's end: + cl_t for t in the next
   float e[2][2][kL];        // [chunk parity][head][t]: decay from the chunk's start through t
-  float bt[2][4];           // [head][block]: log2-decay of a block
+  float bt[2];              // [head]: log2-decay of the second half
   float dec[2][2];          // [chunk parity][head]: decay of the chunk
   uint32_t tmem_base;
   uint32_t abort;
@@ -149,20 +155,52 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Two fp32 operations as one packed instruction, each rounded to nearest.
+__device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
+  unsigned long long ab, xy;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(ab) : "l"(xy));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
+}
+// (a, b) <- (a, b) * (x, y) + (u, v)
+__device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float u, float v) {
+  unsigned long long ab, xy, uv;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(uv) : "f"(u), "f"(v));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(ab) : "l"(xy), "l"(uv));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
+}
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t saddr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(saddr));
+// A shared-memory descriptor as two words: tiles and k-steps differ in the low one alone, so that an
+// unrolled run of products needs one addition an operand.
+struct Desc {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ Desc desc128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  const uint64_t d = sdesc_sw128(saddr, lbo, sbo);
+  return {(uint32_t)d, (uint32_t)(d >> 32)};
 }
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+template <bool kAcc>
+__device__ __forceinline__ void mma_ss(uint32_t d, Desc a, uint32_t a_off, Desc b, uint32_t b_off,
+                                       uint32_t idesc) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
-      " {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %6, 0;\n mov.b64 x, {%1, %2};\n"
+      " mov.b64 y, {%3, %4};\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}\n" ::"r"(d),
+      "r"(a.lo + (a_off >> 4)), "r"(a.hi), "r"(b.lo + (b_off >> 4)), "r"(b.hi), "r"(idesc),
+      "n"(kAcc ? 1 : 0)
+      : "memory");
+}
+template <bool kAcc>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, Desc b, uint32_t b_off, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+      "r"(a_tmem), "r"(b.lo + (b_off >> 4)), "r"(b.hi), "r"(idesc), "n"(kAcc ? 1 : 0)
+      : "memory");
 }
 
 // Reads ring entry k (whole group, uniform result) and releases it.
@@ -259,95 +297,121 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
   const int mn = p.V == 64 ? 128 : 64;   // columns of YM: (head, t)
   const uint32_t id_m = idesc_bf16(128, mn, 1, 0), id_c = idesc_bf16(128, kL, 0, 0),
                  id_s = idesc_bf16(128, K, 1, 1);
-  uint32_t j = 0;
-  for (uint32_t k = 0;; ++k) {
+  // The scores run up to two chunks ahead, within this item and the next: `kg`, `cg`, `jg` are the
+  // item, its chunk and the CTA's chunk they come to next (ng: that item's chunks, -1: not read).
+  uint32_t j = 0, kg = 0, jg = 0;
+  int cg = 0, ng = -1;
+  bool more = true, ok = true;
+  auto scores = [&](uint32_t k, uint32_t upto) {
+    while (ok && more && jg < upto) {
+      if (cg >= ng) {
+        if (kg > k) return;
+        ok = tc_wait(p, c, T_ITEM_FULL + (kg + 1) % kItems, ((kg + 1) / kItems) & 1);
+        if (!ok) return;
+        ++kg;
+        cg = 0;
+        ng = c->ring[kg % kItems].nchunks;
+        more = c->ring[kg % kItems].done == 0;
+        continue;
+      }
+      const uint32_t st = jg % kStages, stage = sbase + st * kStageBytes;
+      ok = tc_wait(p, c, T_FULL + st, (jg / kStages) & 1) &&
+           (jg < 2 || tc_wait(p, c, T_EPI + (jg & 1), ((jg >> 1) - 1) & 1));
+      if (!ok) return;
+      tc_fence_after();
+      // rows 64-127 of A are the tile after c's: lanes that nothing reads
+      const Desc da = desc128(stage + OFF_C, 16, 1024), db = desc128(stage + OFF_B, 16, 1024);
+      const uint32_t tg = tbase + TM_YM + (jg & 1) * 128;
+      mma_ss<false>(tg, da, 0, db, 0, id_c);
+#pragma unroll
+      for (int ks = 1; ks < K / 16; ++ks) {
+        const uint32_t at = (ks / 4) * 8192 + (ks % 4) * 32;
+        mma_ss<true>(tg, da, at, db, at, id_c);
+      }
+      mma_commit(&c->bar[T_G + (jg & 1)]);
+      ++cg;
+      ++jg;
+    }
+  };
+  for (uint32_t k = 0; ok; ++k) {
     const int slot = k % kItems;
-    if (!tc_wait(p, c, T_ITEM_FULL + slot, (k / kItems) & 1)) break;
+    ok = tc_wait(p, c, T_ITEM_FULL + slot, (k / kItems) & 1);
+    if (!ok) break;
     const int nchunks = c->ring[slot].nchunks, done = c->ring[slot].done;
-    mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
     if (done) break;
-    bool ok = true;
+    if (ng < 0 || kg < k) {  // nothing left to run ahead with before this item
+      kg = k;
+      cg = 0;
+      ng = nchunks;
+    }
     for (int ch = 0; ch < nchunks && ok; ++ch, ++j) {
       const uint32_t st = j % kStages, stage = sbase + st * kStageBytes;
-      ok = tc_wait(p, c, T_FULL + st, (j / kStages) & 1) &&
-           tc_wait(p, c, T_M + (j & 1), (j >> 1) & 1);
+      scores(k, j + 1);
+      ok = ok && tc_wait(p, c, T_M + (j & 1), (j >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
       const uint32_t ym = tbase + TM_YM + (j & 1) * 128;
+      const Desc dx = desc128(stage + OFF_X, 8192, 1024), dm = desc128(sbase + OFF_M, 16, 1024);
+      mma_ss<false>(ym, dx, 0, dm, 0, id_m);
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        mma_bf16(ym, sdesc_sw128(stage + OFF_X + ks * 2048, 8192, 1024),
-                 sdesc_sw128(sbase + OFF_M + ks * 32, 16, 1024), id_m, ks > 0 ? 1u : 0u);
+      for (int ks = 1; ks < 4; ++ks) mma_ss<true>(ym, dx, ks * 2048, dm, ks * 32, id_m);
       mma_commit(&c->bar[T_MX]);
       ok = tc_wait(p, c, T_S, j & 1);
       if (!ok) break;
       tc_fence_after();
+      const Desc dc = desc128(stage + OFF_C, 16, 1024);
+      mma_ts<false>(tbase + TM_YI, tbase + TM_SB, dc, 0, id_c);
 #pragma unroll
-      for (int ks = 0; ks < K / 16; ++ks)
-        mma_bf16_ta(tbase + TM_YI, tbase + TM_SB + ks * 8,
-                    sdesc_sw128(stage + OFF_C + (ks / 4) * 8192 + (ks % 4) * 32, 16, 1024), id_c,
-                    ks > 0 ? 1u : 0u);
+      for (int ks = 1; ks < K / 16; ++ks)
+        mma_ts<true>(tbase + TM_YI, tbase + TM_SB + ks * 8, dc, (ks / 4) * 8192 + (ks % 4) * 32, id_c);
       mma_commit(&c->bar[T_Y]);
       ok = tc_wait(p, c, T_XP, j & 1);
       if (!ok) break;
+      const Desc dp = desc128(sbase + OFF_XP, 8192, 1024), db = desc128(stage + OFF_B, 8192, 1024);
 #pragma unroll
-      for (int part = 0; part < PARTS; ++part) {
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_bf16(tbase + TM_S, sdesc_sw128(sbase + OFF_XP + part * kTileBytes + ks * 2048, 8192, 1024),
-                   sdesc_sw128(stage + OFF_B + ks * 2048, 8192, 1024), id_s, 1u);
-      }
+      for (int i = 0; i < PARTS * 4; ++i)  // part i / 4, k-step i % 4
+        mma_ss<true>(tbase + TM_S, dp, (i / 4) * kTileBytes + (i % 4) * 2048, db, (i % 4) * 2048, id_s);
       mma_commit(&c->bar[T_SU]);
       mma_commit(&c->bar[T_EMPTY + st]);
+      scores(k, j + 3);
     }
-    if (!ok) break;
+    mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
   }
   mma_commit(&c->bar[T_DRAIN]);
   mbar_wait(&c->bar[T_DRAIN], 0);  // the full limit, aborted or not
 }
 
 // ---- warps 0-7: scores, M and x' --------------------------------------------------------------
-// 16 x 16 tiles of the scores, lower block triangle: warp -> row block, first column block, count.
-// The diagonal tiles cost more (an exponential an element), warps 6 and 7 also scan the steps.
-__device__ __forceinline__ void tile_of(int warp, int& tb, int& sb, int& n) {
-  // tiles (row block, column block): w0 (3,0)(3,1)  w1 (3,2)(3,3)  w2 (2,0)(2,1)  w3 (2,2)
-  //                                  w4 (1,0)       w5 (1,1)       w6 (0,0)       w7 none
-  const uint32_t tbs = 0x00112233u, sbs = 0x00102020u, ns = 0x01111222u;
-  tb = (tbs >> (warp * 4)) & 15;
-  sb = (sbs >> (warp * 4)) & 15;
-  n = (ns >> (warp * 4)) & 15;
-}
-
 // Steps and decays of one head's chunk, by one warp; lane l has tokens 2 l and 2 l + 1.
 __device__ __forceinline__ void scan_steps(Ctl* c, int head, uint32_t par, float d0, float d1,
                                            float rate2, int lane) {
   const float g0 = rate2 * d0, g1 = rate2 * d1;  // log2-decays
   const float pair = g0 + g1;
-  float up = pair, dn = pair;  // inclusive sums over the block's 8 lanes, from either end
+  float up = pair, dn = pair;  // inclusive sums over the half's 16 lanes, from either end
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    const float a = __shfl_up_sync(0xffffffffu, up, o, 8);
-    const float b = __shfl_down_sync(0xffffffffu, dn, o, 8);
-    if ((lane & 7) >= o) up += a;
-    if ((lane & 7) + o < 8) dn += b;
+  for (int o = 1; o < 16; o <<= 1) {
+    const float a = __shfl_up_sync(0xffffffffu, up, o, 16);
+    const float b = __shfl_down_sync(0xffffffffu, dn, o, 16);
+    if ((lane & 15) >= o) up += a;
+    if ((lane & 15) + o < 16) dn += b;
   }
-  float before = __shfl_up_sync(0xffffffffu, up, 1, 8);
-  float after = __shfl_down_sync(0xffffffffu, dn, 1, 8);
-  if ((lane & 7) == 0) before = 0.f;
-  if ((lane & 7) == 7) after = 0.f;
-  float bt[4];
-#pragma unroll
-  for (int b = 0; b < 4; ++b) bt[b] = __shfl_sync(0xffffffffu, up, b * 8 + 7);
-  const int blk = lane >> 3;
-  const float pre = blk == 0 ? 0.f : blk == 1 ? bt[0] : blk == 2 ? bt[0] + bt[1] : bt[0] + bt[1] + bt[2];
+  float before = __shfl_up_sync(0xffffffffu, up, 1, 16);
+  float after = __shfl_down_sync(0xffffffffu, dn, 1, 16);
+  if ((lane & 15) == 0) before = 0.f;
+  if ((lane & 15) == 15) after = 0.f;
+  const float first = __shfl_sync(0xffffffffu, up, 15), second = __shfl_sync(0xffffffffu, up, 31);
+  const float pre = lane < 16 ? 0.f : first;
   const float c0 = before + g0, c1 = up;
   const int t = 2 * lane;
+  const float l0 = __log2f(d0), l1 = __log2f(d1);  // -inf for a step of zero: a weight of zero
   *reinterpret_cast<float2*>(&c->cl[head][t]) = make_float2(c0, c1);
-  *reinterpret_cast<float2*>(&c->cls[head][t]) = make_float2(c0 - __log2f(d0), c1 - __log2f(d1));
-  *reinterpret_cast<float2*>(&c->fcol[head][t]) = make_float2(ex2(after + g1) * d0, ex2(after) * d1);
+  *reinterpret_cast<float2*>(&c->same[head][t]) = make_float2(l0 - c0, l1 - c1);
+  *reinterpret_cast<float2*>(&c->later[head][t]) = make_float2(l0 + (after + g1), l1 + after);
   *reinterpret_cast<float2*>(&c->e[par][head][t]) = make_float2(ex2(pre + c0), ex2(pre + c1));
-  if (lane < 4) c->bt[head][lane] = bt[lane & 3];
-  if (lane == 0) c->dec[par][head] = ex2((bt[0] + bt[1]) + (bt[2] + bt[3]));
+  if (lane == 0) {
+    c->bt[head] = second;
+    c->dec[par][head] = ex2(first + second);
+  }
 }
 
 // x' (8 values) as PARTS bf16 numbers each: truncated parts leave exact remainders.
@@ -374,20 +438,53 @@ __device__ __forceinline__ void split_x(const uint4& raw, float w, uint4 (&out)[
   for (int q = 0; q < PARTS; ++q) out[q] = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
 }
 
+// 32 columns of one head's M for the 32 rows of this warp: the scores times the weights of the
+// columns. kDiag: the columns' half is the rows' half.
+template <bool kDiag>
+__device__ __forceinline__ void weigh_scores(const Ctl* c, uint8_t* m_row, uint32_t tmem, int hd, int half,
+                                             float cl, int lane) {
+  const float* src = kDiag ? c->same[hd] + half * 32 : c->later[hd] + half * 32;
+#pragma unroll
+  for (int i0 = 0; i0 < 32; i0 += 16) {
+    float g[16], w[16];
+    tmem_ld16(tmem + half * 32 + i0, g);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(src + i0 + i);
+      w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = ex2(cl + w[i]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      g[i] *= w[i];
+      if (kDiag) g[i] = i0 + i <= lane ? g[i] : 0.f;  // a later token's weight may be anything
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i += 8) {
+      const uint32_t chunk = half * 4 + (i0 + i) / 8;
+      *reinterpret_cast<uint4*>(m_row + (((chunk ^ lane) & 7u) << 4)) =
+          make_uint4(pack_bf16x2(g[i], g[i + 1]), pack_bf16x2(g[i + 2], g[i + 3]),
+                     pack_bf16x2(g[i + 4], g[i + 5]), pack_bf16x2(g[i + 6], g[i + 7]));
+    }
+  }
+}
+
 template <int K, int PARTS>
-__device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c) {
+__device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t sbase = smem_u32(sm);
   const int rep = p.H / p.G;
   const int heads = p.V == 64 ? 2 : 1;
-  int tb, sb0, ntile;
-  tile_of(warp, tb, sb0, ntile);
-  // the blocks of M above the diagonal are never written again
+  // the columns of M after the rows' half are never written again
   for (uint32_t i = tid; i < kTileBytes / 16; i += kMThreads)
     *reinterpret_cast<uint4*>(sm + OFF_M + i * 16) = make_uint4(0, 0, 0, 0);
 
-  const bool scans = warp >= 8 - heads;   // warp 7 scans head 0, warp 6 head 1
-  const int sh = 7 - warp;
+  const bool scores = (warp & 2) == 0;    // warps 0, 1, 4, 5
+  const int rh = warp & 1;                // half of the rows (TMEM lanes 32 rh, + 32)
+  const bool scans = warp == 2 || (warp == 3 && heads == 2);
+  const int sh = warp & 1;                // head that warp 2 or 3 scans
+  const int xt = (warp >> 2) * 64 + (warp & 1) * 32 + lane;  // 0..127 over warps 2, 3, 6, 7
   uint32_t j = 0;
   for (uint32_t k = 0;; ++k) {
     const Item it = tc_item(p, c, k, BAR_MG, kMThreads, tid == 0);
@@ -399,134 +496,77 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c) {
       rate2 = -expf(p.a_log[it.h0 + sh]) * 1.4426950408889634f;
       bias = p.dt_bias ? p.dt_bias[it.h0 + sh] : 0.f;
     }
-    // the steps are read a chunk ahead of their scan
-    const __nv_bfloat16* dtp = p.dt + it.h0 + sh;
-    auto load_dt = [&](int ch, float& a, float& b) {
-      const int64_t t = it.bos + (int64_t)ch * kL + 2 * lane;
-      a = mine && t < it.eos ? to_f32(dtp[t * p.dt_pitch]) : -INFINITY;
-      b = mine && t + 1 < it.eos ? to_f32(dtp[(t + 1) * p.dt_pitch]) : -INFINITY;
-    };
+    // the steps are read a chunk ahead of their scan; -inf: no token, a step of zero
     float n0 = -INFINITY, n1 = -INFINITY;
-    if (scans && it.nchunks > 0) load_dt(0, n0, n1);
+    const __nv_bfloat16* dtp = p.dt + it.h0 + sh;
+    if (mine) {
+      const int64_t t = it.bos + 2 * lane;
+      if (t < it.eos) n0 = to_f32(dtp[t * p.dt_pitch]);
+      if (t + 1 < it.eos) n1 = to_f32(dtp[(t + 1) * p.dt_pitch]);
+    }
     for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
       const uint32_t st = j % kStages, par = j & 1;
       uint8_t* stage = sm + st * kStageBytes;
-      const uint32_t sstage = sbase + st * kStageBytes;
-      const int64_t left = it.eos - it.bos - (int64_t)ch * kL;
-      const int m = left < kL ? (int)left : kL;
-      tc_wait(p, c, T_FULL + st, (j / kStages) & 1);
-      // the rows after the sequence's last token are another's (or nobody's): they must not reach
-      // a product, where a zero weight would not hide an infinity
-      if (m < kL) {
-        const int rows = kL - m;
-        for (int i = tid; i < rows * 32; i += kMThreads) {
-          const uint32_t tile = (i >> 3) & 3;  // b and x, two halves each
-          *reinterpret_cast<uint4*>(stage + OFF_B + tile * 8192 + sw128_off(m + (i >> 5), i & 7)) =
-              make_uint4(0, 0, 0, 0);
+      if (!scores) {
+        if (scans) {
+          const float d0 = n0 == -INFINITY ? 0.f : ssm_step(n0, bias);
+          const float d1 = n1 == -INFINITY ? 0.f : ssm_step(n1, bias);
+          if (j >= 2) tc_wait(p, c, T_EPI + par, ((j >> 1) - 1) & 1);  // the factors' last readers
+          scan_steps(c, sh, par, d0, d1, rate2, lane);
+          n0 = n1 = -INFINITY;
+          const int64_t t = it.bos + (int64_t)(ch + 1) * kL + 2 * lane;
+          if (mine && t < it.eos) n0 = to_f32(dtp[t * p.dt_pitch]);
+          if (mine && t + 1 < it.eos) n1 = to_f32(dtp[(t + 1) * p.dt_pitch]);
         }
-      }
-      // scores
-      float acc[2][2][4] = {};
-      if (ntile > 0) {
-#pragma unroll
-        for (int ks = 0; ks < K / 16; ++ks) {
-          uint32_t a[4];
-          const uint32_t kc = ks * 2;  // 16-byte chunk of the k range
-          {
-            const uint32_t q = kc + (lane >> 4);
-            ldsm_x4(a, sstage + OFF_C + (q >> 3) * 8192 + sw128_off(tb * 16 + (lane & 15), q & 7));
+        tc_wait(p, c, T_FULL + st, (j / kStages) & 1);
+        // the rows after the sequence's last token are another's (or nobody's): they must not reach
+        // a product, where a zero weight would not hide an infinity
+        const int64_t left = it.eos - it.bos - (int64_t)ch * kL;
+        if (left < kL) {
+          const int m = (int)left;
+          for (int i = xt; i < (kL - m) * 32; i += 128) {
+            const uint32_t tile = (i >> 3) & 3;  // b and x, two halves each
+            *reinterpret_cast<uint4*>(stage + OFF_B + tile * 8192 + sw128_off(m + (i >> 5), i & 7)) =
+                make_uint4(0, 0, 0, 0);
           }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (i < ntile) {
-              uint32_t b[4];
-              const uint32_t q = kc + ((lane >> 3) & 1);
-              ldsm_x4(b, sstage + OFF_B + (q >> 3) * 8192 +
-                             sw128_off((sb0 + i) * 16 + ((lane >> 4) << 3) + (lane & 7), q & 7));
-              mma_16816(acc[i][0], a, b[0], b[1]);
-              mma_16816(acc[i][1], a, b[2], b[3]);
-            }
-          }
+          fence_async_smem();
         }
-      }
-      if (scans) {
-        // the factors by chunk parity: their reader two chunks back has left the stage it shared
-        if (j >= 2) tc_wait(p, c, T_EMPTY + (j - 2) % kStages, ((j - 2) / kStages) & 1);
-        const float d0 = n0 == -INFINITY ? 0.f : ssm_step(n0, bias);
-        const float d1 = n1 == -INFINITY ? 0.f : ssm_step(n1, bias);
-        scan_steps(c, sh, par, d0, d1, rate2, lane);
-        if (ch + 1 < it.nchunks) load_dt(ch + 1, n0, n1);
+        warp_arrive(&c->bar[T_M + par]);
       }
       if (named_bar_any(BAR_MG, kMThreads, tc_aborted(c))) return;  // factors and cleared rows
-      // M, once the product that read the last one is done
-      if (j > 0) tc_wait(p, c, T_MX, (j - 1) & 1);
+      if (scores) {
+        tc_wait(p, c, T_G + par, (j >> 1) & 1);
+        if (j > 0) tc_wait(p, c, T_MX, (j - 1) & 1);  // the product that read the last M is done
+        tc_fence_after();
+        const uint32_t tg = tbase + TM_YM + par * 128 + ((uint32_t)(rh * 32) << 16);
+        // pieces of 32 x 32: heads on warps 0, 1 and 4, 5; one head's second row half is shared
+        const int hd = heads == 2 ? warp >> 2 : 0;
+        const float cl = c->cl[hd][rh * 32 + lane];
+        uint8_t* m_row = sm + OFF_M + hd * 8192 + rh * 4096 + (lane >> 3) * 1024 + (lane & 7) * 128;
+        if (rh == 1 && (heads == 2 || warp == 1)) weigh_scores<false>(c, m_row, tg, hd, 0, cl, lane);
+        if (heads == 2 || warp == 0 || warp == 5) weigh_scores<true>(c, m_row, tg, hd, rh, cl, lane);
+        tc_fence_before();
+        fence_async_smem();
+        warp_arrive(&c->bar[T_M + par]);
+      } else {
+        // x', written once the product that read the last one is done
+        if (j > 0) tc_wait(p, c, T_SU, (j - 1) & 1);
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i) {
+          const int row = (i & 3) * 16 + (xt >> 3), half = i >> 2;
+          const int hd = heads == 2 ? half : 0;
+          const uint32_t at = half * 8192 + sw128_off(row, xt & 7);
+          const uint4 raw = *reinterpret_cast<const uint4*>(stage + OFF_X + at);
+          uint4 parts[PARTS];
+          split_x<PARTS>(raw, ex2(c->later[hd][row] + (row < 32 ? c->bt[hd] : 0.f)), parts);
 #pragma unroll
-      for (int hd = 0; hd < 2; ++hd) {
-        if (hd >= heads) break;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (i >= ntile) break;
-          const int sb = sb0 + i, r = tb * 16 + (lane >> 2);
-          const float cl0 = c->cl[hd][r], cl1 = c->cl[hd][r + 8];
-          float f0 = 0.f, f1 = 0.f;
-          if (sb < tb) {
-            float mid = 0.f;
-#pragma unroll
-            for (int b = 1; b < 3; ++b)
-              if (b > sb && b < tb) mid += c->bt[hd][b];
-            f0 = ex2(cl0 + mid);
-            f1 = ex2(cl1 + mid);
-          }
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const int s = sb * 16 + nt * 8 + 2 * (lane & 3);
-            float v[4] = {acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]};
-            if (sb < tb) {
-              const float2 fc = *reinterpret_cast<const float2*>(&c->fcol[hd][s]);
-              v[0] *= f0 * fc.x; v[1] *= f0 * fc.y;
-              v[2] *= f1 * fc.x; v[3] *= f1 * fc.y;
-            } else {
-              const float2 cs = *reinterpret_cast<const float2*>(&c->cls[hd][s]);
-              v[0] = s <= r ? v[0] * ex2(cl0 - cs.x) : 0.f;
-              v[1] = s + 1 <= r ? v[1] * ex2(cl0 - cs.y) : 0.f;
-              v[2] = s <= r + 8 ? v[2] * ex2(cl1 - cs.x) : 0.f;
-              v[3] = s + 1 <= r + 8 ? v[3] * ex2(cl1 - cs.y) : 0.f;
-            }
-            uint8_t* mt = sm + OFF_M + hd * 8192 + (s & 7) * 2;
-            *reinterpret_cast<uint32_t*>(mt + sw128_off(r, s >> 3)) = pack_bf16x2(v[0], v[1]);
-            *reinterpret_cast<uint32_t*>(mt + sw128_off(r + 8, s >> 3)) = pack_bf16x2(v[2], v[3]);
-          }
+          for (int q = 0; q < PARTS; ++q)
+            *reinterpret_cast<uint4*>(sm + OFF_XP + q * kTileBytes + at) = parts[q];
         }
+        fence_async_smem();
+        warp_arrive(&c->bar[T_XP]);
       }
-      fence_async_smem();
-      warp_arrive(&c->bar[T_M + par]);
-      // x', written once the product that read the last one is done
-      uint4 parts[4][PARTS];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = (i & 1) * 32 + (tid >> 3), half = i >> 1;
-        const int hd = heads == 2 ? half : 0, blk = row >> 4;
-        float late = 0.f;
-#pragma unroll
-        for (int b = 1; b < 4; ++b)
-          if (b > blk) late += c->bt[hd][b];
-        const float w = (half == 1 && !second) ? 0.f : c->fcol[hd][row] * ex2(late);
-        const uint4 raw = *reinterpret_cast<const uint4*>(stage + OFF_X + half * 8192 +
-                                                          sw128_off(row, tid & 7));
-        split_x<PARTS>(raw, w, parts[i]);
-      }
-      if (j > 0) tc_wait(p, c, T_SU, (j - 1) & 1);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t at = (i >> 1) * 8192 + sw128_off((i & 1) * 32 + (tid >> 3), tid & 7);
-#pragma unroll
-        for (int q = 0; q < PARTS; ++q)
-          *reinterpret_cast<uint4*>(sm + OFF_XP + q * kTileBytes + at) = parts[i][q];
-      }
-      fence_async_smem();
-      warp_arrive(&c->bar[T_XP]);
-      // the next chunk's scan overwrites cl, cls, fcol and bt
-      named_bar(BAR_MG, kMThreads);
+      named_bar(BAR_MG, kMThreads);  // the next chunk's scan overwrites cl, same, later and bt
     }
   }
 }
@@ -566,44 +606,29 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       const int64_t t0 = it.bos + (int64_t)ch * kL;
       const int m = it.eos - t0 < kL ? (int)(it.eos - t0) : kL;
       // S before the chunk: its bf16 copy for the product with C, and its decay over the chunk
-      if (ch == 0) {
-        float s[KH];
+      tc_wait(p, c, T_M + par, (j >> 1) & 1);
+      const float dec = c->dec[par][hd];
+      if (ch > 0) tc_wait(p, c, T_SU, (j - 1) & 1);
+      tc_fence_after();
+#pragma unroll 1
+      for (int i0 = 0; i0 < KH; i0 += 32) {
+        float s[32], pk[16];
+        if (ch == 0) {
+          const ST* at = src + i0 * p.V;
 #pragma unroll
-        for (int i = 0; i < KH; ++i) s[i] = src ? to_f32(src[(int64_t)i * p.V]) : 0.f;
-        tc_wait(p, c, T_M + par, (j >> 1) & 1);
-        const float dec = c->dec[par][hd];
-#pragma unroll
-        for (int i0 = 0; i0 < KH; i0 += 32) {
-          float pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            pk[i] = __uint_as_float(pack_bf16x2(s[i0 + 2 * i], s[i0 + 2 * i + 1]));
-          tmem_st16(tq + TM_SB + (hf * KH + i0) / 2, pk);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) s[i0 + i] *= dec;
-          tmem_st16(tq + TM_S + hf * KH + i0, s + i0);
-          tmem_st16(tq + TM_S + hf * KH + i0 + 16, s + i0 + 16);
-        }
-      } else {
-        tc_wait(p, c, T_M + par, (j >> 1) & 1);
-        const float dec = c->dec[par][hd];
-        tc_wait(p, c, T_SU, (j - 1) & 1);
-        tc_fence_after();
-#pragma unroll
-        for (int i0 = 0; i0 < KH; i0 += 32) {
-          float s[32], pk[16];
+          for (int i = 0; i < 32; ++i) s[i] = src ? to_f32(at[i * p.V]) : 0.f;
+        } else {
           tmem_ld16(tq + TM_S + hf * KH + i0, s);
           tmem_ld16(tq + TM_S + hf * KH + i0 + 16, s + 16);
           tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            pk[i] = __uint_as_float(pack_bf16x2(s[2 * i], s[2 * i + 1]));
-          tmem_st16(tq + TM_SB + (hf * KH + i0) / 2, pk);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] *= dec;
-          tmem_st16(tq + TM_S + hf * KH + i0, s);
-          tmem_st16(tq + TM_S + hf * KH + i0 + 16, s + 16);
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pk[i] = __uint_as_float(pack_bf16x2(s[2 * i], s[2 * i + 1]));
+        tmem_st16(tq + TM_SB + (hf * KH + i0) / 2, pk);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) mul2(s[i], s[i + 1], dec, dec);
+        tmem_st16(tq + TM_S + hf * KH + i0, s);
+        tmem_st16(tq + TM_S + hf * KH + i0 + 16, s + 16);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -619,29 +644,50 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         const uint32_t vc = (v & 63) >> 3;
         uint8_t* yt = sm + OFF_Y + half * 8192 + (v & 63) * 2;
         const bool full = m == kL;
-        __nv_bfloat16* yg = p.y + (t0 * p.H + h) * p.V + vh;
-        const int64_t yrow = (int64_t)p.H * p.V;
-#pragma unroll
+#pragma unroll 1
         for (int i0 = 0; i0 < 32; i0 += 16) {
           const int tt = hf * 32 + i0;
-          float a[16], b[16];
+          float a[16], b[16], x[16], e[16];
           tmem_ld16(tq + TM_YI + tt, a);
           tmem_ld16(tq + TM_YM + par * 128 + (p.V == 64 ? hd * 64 : 0) + tt, b);
-          tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int t = tt + i;
-            const float x = to_f32(*reinterpret_cast<const __nv_bfloat16*>(xt + sw128_off(t, vc)));
-            const float r = fmaf(dskip, x, fmaf(c->e[par][hd][t], a[i], b[i]));
-            if (full) {
-              *reinterpret_cast<__nv_bfloat16*>(yt + t * 128) = __float2bfloat16_rn(r);
-            } else if (t < m && real && KDA_CHECK(t0 + t < p.T)) {
-              yg[t * yrow] = __float2bfloat16_rn(r);
+          for (int i = 0; i < 16; ++i)
+            x[i] = to_f32(*reinterpret_cast<const __nv_bfloat16*>(xt + sw128_off(tt + i, vc)));
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(&c->e[par][hd][tt + i]);
+            e[i] = q.x; e[i + 1] = q.y; e[i + 2] = q.z; e[i + 3] = q.w;
+          }
+          tmem_ld_wait();
+          __nv_bfloat16 r[16];
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            fma2(a[i], a[i + 1], e[i], e[i + 1], b[i], b[i + 1]);
+            fma2(x[i], x[i + 1], dskip, dskip, a[i], a[i + 1]);
+            const __nv_bfloat162 q = __floats2bfloat162_rn(x[i], x[i + 1]);
+            r[i] = q.x;
+            r[i + 1] = q.y;
+          }
+          if (full) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) *reinterpret_cast<__nv_bfloat16*>(yt + (tt + i) * 128) = r[i];
+          } else if (real) {
+            // a partial chunk's tile would cover the next sequence's rows: rows of its own only
+            __nv_bfloat16* yg = p.y + ((t0 + tt) * p.H + h) * p.V + vh;
+            const int row = p.H * p.V;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (tt + i < m && KDA_CHECK(t0 + tt + i < p.T)) *yg = r[i];
+              yg += row;
             }
           }
         }
         tc_fence_before();
-        warp_arrive(&c->bar[T_EMPTY + st]);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&c->bar[T_EMPTY + st]);
+          mbar_arrive(&c->bar[T_EPI + par]);
+        }
         if (full) {
           fence_async_smem();
           named_bar(BAR_RGRP, kRThreads);
@@ -658,7 +704,7 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
     tc_fence_after();
     if (named_bar_any(BAR_RGRP, kRThreads, tc_aborted(c))) break;
     {
-#pragma unroll
+#pragma unroll 1
       for (int i0 = 0; i0 < KH; i0 += 32) {
         float s[32];
         tmem_ld16(tq + TM_S + hf * KH + i0, s);
@@ -666,7 +712,7 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         tmem_ld_wait();
         if (dst) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) dst[(int64_t)(i0 + i) * p.V] = from_f32<ST>(s[i]);
+          for (int i = 0; i < 32; ++i) dst[(i0 + i) * p.V] = from_f32<ST>(s[i]);
         }
       }
       tc_fence_before();
@@ -690,7 +736,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid
     for (int b = 0; b < T_COUNT; ++b) {
       uint32_t count = 1;                                   // a loader's or a commit's arrival
       if (b >= T_EMPTY && b < T_EMPTY + kStages) count = 1 + kRThreads / 32;
-      if (b == T_M || b == T_M + 1 || b == T_XP || b == T_S) count = 8;  // one a warp
+      if (b >= T_M && b <= T_S) count = b == T_XP ? 4 : 8;  // one a warp that writes
       if (b >= T_ITEM_EMPTY && b < T_ITEM_EMPTY + kItems) count = 3;
       mbar_init(&c->bar[b], count);
     }
@@ -706,7 +752,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = c->tmem_base;
-  if (warp < 8) run_mgroup<K, PARTS>(p, sm, c);
+  if (warp < 8) run_mgroup<K, PARTS>(p, sm, c, tbase);
   else if (warp < 16) run_rgroup<ST, K>(p, sm, c, tbase);
   else if (warp == 16) run_issuer<K, PARTS>(p, sm, c, tbase);
   else run_loader<K>(p, sm, c);
