@@ -28,12 +28,12 @@
 // through TMEM, took 2100 cycles a chunk against some 500 of the tensor pipe: 516 us a call for
 // 32768 tokens against XXX.)
 //
-// Warps 0, 1, 4, 5 make M from the scores (their TMEM lanes hold the 64 rows), warps 2, 3, 6, 7 scan
-// the steps and make x'; warps 8-15 (R group): the state's decay and bf16 copy, the output. Warp 16
-// issues the tcgen05 products, warp 17 claims items and loads tiles (TMA).
-// The M group works a chunk ahead of the R group; what orders them are mbarriers, each wait
-// bounded (a timeout sets KDA_DEVICE_PIPE_TIMEOUT, stops the loads, lets what was issued finish and
-// returns).
+// Warps 0-7 (M group): x', and warps 0, 1, 4, 5, whose TMEM lanes hold the 64 rows of the scores, M.
+// Warps 8-15 (R group): the state's decay and bf16 copy, the output. Warp 16 issues the tcgen05
+// products, warp 17 claims items and loads tiles (TMA), warp 18 scans the steps. What orders them are
+// mbarriers, each wait bounded (a timeout sets KDA_DEVICE_PIPE_TIMEOUT, stops the loads, lets what was
+// issued finish and returns). Only T_SU -> R -> T_S -> products of C and x' -> T_SU is a chain from
+// chunk to chunk; scans, scores, M and the arithmetic of x' run ahead of it.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -52,7 +52,8 @@ using namespace tc;
 constexpr int kL = 64;          // tokens a chunk
 constexpr int kStages = 3;      // chunks of c, b and x tiles in flight
 constexpr int kMThreads = 256, kRThreads = 256;
-constexpr int kTcThreads = kMThreads + kRThreads + 64;
+constexpr int kTcThreads = kMThreads + kRThreads + 96;
+constexpr int kFacs = 3;        // chunks of steps and decays in flight
 constexpr int kItems = 4;       // claimed items in flight
 
 // ---- shared memory (offsets from a 1024-aligned base) -----------------------------------
@@ -61,8 +62,7 @@ constexpr uint32_t OFF_C = 0, OFF_B = kTileBytes, OFF_X = 2 * kTileBytes;  // wi
 constexpr uint32_t kStageBytes = 3 * kTileBytes;
 constexpr uint32_t OFF_XP = kStages * kStageBytes;   // x' as three bf16 parts, each like x
 constexpr uint32_t OFF_M = OFF_XP + 3 * kTileBytes;  // [2 heads][64 t][64 s] (K-major B)
-constexpr uint32_t OFF_Y = OFF_M + kTileBytes;       // [2 halves][64 t][64 v], to be stored
-constexpr uint32_t OFF_CTL = OFF_Y + kTileBytes;
+constexpr uint32_t OFF_CTL = OFF_M + kTileBytes;
 
 // ---- TMEM columns -------------------------------------------------------------------------
 constexpr uint32_t TM_S = 0;     // S^T fp32 (128)
@@ -72,13 +72,15 @@ constexpr uint32_t TM_YM = 256;  // X^T M^T, two buffers of 128 by chunk parity;
 
 enum TcBar {
   T_FULL = 0,                    // a stage's tiles have landed
-  T_EMPTY = T_FULL + kStages,    // a stage is free: its products are done and x was read
-  T_M = T_EMPTY + kStages,       // M and the chunk's factors are written, by chunk parity
-  T_EPI = T_M + 2,               // the output that used the chunk's factors is formed, by parity
-  T_XP = T_EPI + 2,              // x' is written
-  T_S,                           // S is decayed and its bf16 copy written
+  T_EMPTY = T_FULL + kStages,    // a stage is free: its products are done, its output has left
+  T_FAC = T_EMPTY + kStages,     // a chunk's factors are written
+  T_FAC_FREE = T_FAC + kFacs,    // ... and read
+  T_M = T_FAC_FREE + kFacs,      // M is written (and a partial chunk's rows cleared), by chunk parity
+  T_EPI = T_M + 2,               // the output has read YM and YI, by parity
+  T_XP = T_EPI + 2,              // x' is written, by parity
+  T_S = T_XP + 2,                // S is decayed and its bf16 copy written
   T_MX, T_Y, T_SU,               // the products of M, of C (and M), of x' are done
-  T_G,                           // the scores are done, by chunk parity
+  T_G,                           // the scores are done, by parity
   T_ITEM_FULL = T_G + 2,
   T_ITEM_EMPTY = T_ITEM_FULL + kItems,
   T_DRAIN = T_ITEM_EMPTY + kItems,
@@ -91,16 +93,20 @@ struct Item {
   int64_t src, dst;   // element offsets of head h0's state, -1: zero state / not written
 };
 
+// Steps and decays of a chunk, by [head of the item][token], logarithms to base 2; a half is 32 tokens.
+struct Factors {
+  alignas(16) float cl[2][kL];  // log-decay from the half's start through t
+  float same[2][kL];   // log d_s - cl: + cl_t is the weight of s for t in its half
+  float later[2][kL];  // log d_s + log-decay after s to its half's end: + cl_t for t in the next
+  float e[2][kL];      // decay from the chunk's start through t
+  float second[2];     // log-decay of the second half
+  float dec[2];        // decay of the chunk
+};
+
 struct Ctl {
   uint64_t bar[T_COUNT];
   Item ring[kItems];
-  // by [head][token], in log2; a half is 32 tokens
-  alignas(16) float cl[2][kL];  // decay from the half's start through t
-  float same[2][kL];        // log2(d_s) - cl: + cl_t is the weight of s for t in its half
-  float later[2][kL];       // log2(d_s) + decay after s to its half's end: + cl_t for t in the next
-  float e[2][2][kL];        // [chunk parity][head][t]: decay from the chunk's start through t
-  float bt[2];              // [head]: log2-decay of the second half
-  float dec[2][2];          // [chunk parity][head]: decay of the chunk
+  Factors fac[kFacs];
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -119,6 +125,7 @@ struct ScanParams {
   uint32_t* status;
   uint32_t* next_item;
   uint64_t wait_limit_ns;
+  int32_t poll;                // waits poll: the limit is below what try_wait may suspend a thread for
   int32_t N, H, G, V, pairs;   // pairs: items a sequence
   int64_t T, num_slots, slot_stride;
 };
@@ -126,23 +133,24 @@ struct ScanParams {
 __device__ __forceinline__ bool tc_aborted(const Ctl* c) {
   return *reinterpret_cast<const volatile uint32_t*>(&c->abort) != 0u;
 }
-// Bounded wait; after a timeout anywhere in the CTA every wait returns at once (false).
-__device__ __noinline__ bool tc_wait_slow(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
-                                          uint32_t* abort_flag, uint32_t* status) {
-  const bool poll = limit_ns < kSleepHintNs;
+// Bounded wait; after a timeout anywhere in the CTA every wait returns at once (false). The hardware
+// suspends the thread in try_wait until the phase completes or some microseconds have passed, so that
+// a waiting warp takes few issue slots; a limit shorter than that polls instead.
+__device__ __noinline__ bool tc_wait_slow(const ScanParams& p, Ctl* c, int b, uint32_t parity) {
+  uint64_t* bar = &c->bar[b];
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
-    if (poll ? mbar_test_wait(bar, parity) : mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
-    if (*reinterpret_cast<volatile uint32_t*>(abort_flag) != 0u) return false;
-    if (globaltimer_ns() - t0 > limit_ns) {
-      if (atomicExch(abort_flag, 1u) == 0u) raise_status(status, KDA_DEVICE_PIPE_TIMEOUT);
+    if (p.poll ? mbar_test_wait(bar, parity) : mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
+    if (tc_aborted(c)) return false;
+    if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+      if (atomicExch(&c->abort, 1u) == 0u) raise_status(p.status, KDA_DEVICE_PIPE_TIMEOUT);
       return false;
     }
   }
 }
 __device__ __forceinline__ bool tc_wait(const ScanParams& p, Ctl* c, int b, uint32_t parity) {
-  if (mbar_test_wait(&c->bar[b], parity)) return true;
-  return tc_wait_slow(&c->bar[b], parity, p.wait_limit_ns, &c->abort, p.status);
+  if (p.poll == 0 && mbar_try_wait_sleep(&c->bar[b], parity, kSleepHintNs)) return true;
+  return tc_wait_slow(p, c, b, parity);
 }
 // One arrival a warp, after what its lanes wrote.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -215,7 +223,19 @@ __device__ __forceinline__ Item tc_item(const ScanParams& p, Ctl* c, uint32_t k,
   return it;
 }
 
-constexpr uint32_t BAR_MG = 1, BAR_RGRP = 2;
+// The same for one warp.
+__device__ __forceinline__ Item tc_item_warp(const ScanParams& p, Ctl* c, uint32_t k) {
+  const int slot = k % kItems;
+  const bool ok = tc_wait(p, c, T_ITEM_FULL + slot, (k / kItems) & 1);
+  Item it = c->ring[slot];
+  const bool stop = __any_sync(0xffffffffu, !ok || it.done != 0 || tc_aborted(c));
+  __syncwarp();
+  if (ok && (threadIdx.x & 31) == 0) mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
+  it.done = stop ? 1 : 0;
+  return it;
+}
+
+constexpr uint32_t BAR_RGRP = 1;
 
 // ---- warp 17: items and tiles ------------------------------------------------------------
 template <int K>
@@ -346,7 +366,7 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
     }
     for (int ch = 0; ch < nchunks && ok; ++ch, ++j) {
       const uint32_t st = j % kStages, stage = sbase + st * kStageBytes;
-      scores(k, j + 1);
+      scores(k, j + 2);
       ok = ok && tc_wait(p, c, T_M + (j & 1), (j >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
@@ -365,7 +385,7 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       for (int ks = 1; ks < K / 16; ++ks)
         mma_ts<true>(tbase + TM_YI, tbase + TM_SB + ks * 8, dc, (ks / 4) * 8192 + (ks % 4) * 32, id_c);
       mma_commit(&c->bar[T_Y]);
-      ok = tc_wait(p, c, T_XP, j & 1);
+      ok = tc_wait(p, c, T_XP + (j & 1), (j >> 1) & 1);
       if (!ok) break;
       const Desc dp = desc128(sbase + OFF_XP, 8192, 1024), db = desc128(stage + OFF_B, 8192, 1024);
 #pragma unroll
@@ -373,7 +393,6 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         mma_ss<true>(tbase + TM_S, dp, (i / 4) * kTileBytes + (i % 4) * 2048, db, (i % 4) * 2048, id_s);
       mma_commit(&c->bar[T_SU]);
       mma_commit(&c->bar[T_EMPTY + st]);
-      scores(k, j + 3);
     }
     mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
   }
@@ -382,9 +401,12 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
 }
 
 // ---- warps 0-7: scores, M and x' --------------------------------------------------------------
+__device__ __noinline__ float step_of(float dt, float bias) {
+  return dt == -INFINITY ? 0.f : ssm_step(dt, bias);
+}
+
 // Steps and decays of one head's chunk, by one warp; lane l has tokens 2 l and 2 l + 1.
-__device__ __forceinline__ void scan_steps(Ctl* c, int head, uint32_t par, float d0, float d1,
-                                           float rate2, int lane) {
+__device__ __forceinline__ void scan_steps(Factors* f, int head, float d0, float d1, float rate2, int lane) {
   const float g0 = rate2 * d0, g1 = rate2 * d1;  // log2-decays
   const float pair = g0 + g1;
   float up = pair, dn = pair;  // inclusive sums over the half's 16 lanes, from either end
@@ -404,13 +426,61 @@ __device__ __forceinline__ void scan_steps(Ctl* c, int head, uint32_t par, float
   const float c0 = before + g0, c1 = up;
   const int t = 2 * lane;
   const float l0 = __log2f(d0), l1 = __log2f(d1);  // -inf for a step of zero: a weight of zero
-  *reinterpret_cast<float2*>(&c->cl[head][t]) = make_float2(c0, c1);
-  *reinterpret_cast<float2*>(&c->same[head][t]) = make_float2(l0 - c0, l1 - c1);
-  *reinterpret_cast<float2*>(&c->later[head][t]) = make_float2(l0 + (after + g1), l1 + after);
-  *reinterpret_cast<float2*>(&c->e[par][head][t]) = make_float2(ex2(pre + c0), ex2(pre + c1));
+  *reinterpret_cast<float2*>(&f->cl[head][t]) = make_float2(c0, c1);
+  *reinterpret_cast<float2*>(&f->same[head][t]) = make_float2(l0 - c0, l1 - c1);
+  *reinterpret_cast<float2*>(&f->later[head][t]) = make_float2(l0 + (after + g1), l1 + after);
+  *reinterpret_cast<float2*>(&f->e[head][t]) = make_float2(ex2(pre + c0), ex2(pre + c1));
   if (lane == 0) {
-    c->bt[head] = second;
-    c->dec[par][head] = ex2(first + second);
+    f->second[head] = second;
+    f->dec[head] = ex2(first + second);
+  }
+}
+
+// ---- warp 18: steps and decays ------------------------------------------------------------------
+__device__ void run_scan(const ScanParams& p, Ctl* c) {
+  const int lane = threadIdx.x & 31, rep = p.H / p.G, heads = p.V == 64 ? 2 : 1;
+  uint32_t j = 0;
+  for (uint32_t k = 0;; ++k) {
+    const Item it = tc_item_warp(p, c, k);
+    if (it.done) return;
+    const bool second = heads == 2 && (it.h0 % rep) + 1 < rep;
+    float rate2[2] = {0.f, 0.f}, bias[2] = {0.f, 0.f};
+#pragma unroll
+    for (int hd = 0; hd < 2; ++hd) {
+      if (hd == 1 && !second) break;
+      rate2[hd] = -expf(p.a_log[it.h0 + hd]) * 1.4426950408889634f;
+      bias[hd] = p.dt_bias ? p.dt_bias[it.h0 + hd] : 0.f;
+    }
+    // the steps of a chunk are read while the one before is scanned; -inf: no token, a step of zero
+    float n[2][2];
+    auto read = [&](int ch) {
+      const int64_t t = it.bos + (int64_t)ch * kL + 2 * lane;
+      const __nv_bfloat16* at = p.dt + t * p.dt_pitch + it.h0;
+#pragma unroll
+      for (int hd = 0; hd < 2; ++hd) {
+        const bool any = hd == 0 || second;
+        n[hd][0] = any && t < it.eos ? to_f32(at[hd]) : -INFINITY;
+        n[hd][1] = any && t + 1 < it.eos ? to_f32(at[p.dt_pitch + hd]) : -INFINITY;
+      }
+    };
+    read(0);
+    for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
+      const uint32_t fi = j % kFacs;
+      if (__any_sync(0xffffffffu, tc_aborted(c))) return;
+      float d[2][2];
+#pragma unroll
+      for (int hd = 0; hd < 2; ++hd) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) d[hd][i] = step_of(n[hd][i], bias[hd]);
+      }
+      read(ch + 1);
+      if (j >= (uint32_t)kFacs) tc_wait(p, c, T_FAC_FREE + fi, (j / kFacs - 1) & 1);
+#pragma unroll 1
+      for (int hd = 0; hd < heads; ++hd)
+        scan_steps(&c->fac[fi], hd, hd ? d[1][0] : d[0][0], hd ? d[1][1] : d[0][1],
+                   hd ? rate2[1] : rate2[0], lane);
+      warp_arrive(&c->bar[T_FAC + fi]);
+    }
   }
 }
 
@@ -441,9 +511,9 @@ __device__ __forceinline__ void split_x(const uint4& raw, float w, uint4 (&out)[
 // 32 columns of one head's M for the 32 rows of this warp: the scores times the weights of the
 // columns. kDiag: the columns' half is the rows' half.
 template <bool kDiag>
-__device__ __forceinline__ void weigh_scores(const Ctl* c, uint8_t* m_row, uint32_t tmem, int hd, int half,
+__device__ __forceinline__ void weigh_scores(const Factors* f, uint8_t* m_row, uint32_t tmem, int hd, int half,
                                              float cl, int lane) {
-  const float* src = kDiag ? c->same[hd] + half * 32 : c->later[hd] + half * 32;
+  const float* src = kDiag ? f->same[hd] + half * 32 : f->later[hd] + half * 32;
 #pragma unroll
   for (int i0 = 0; i0 < 32; i0 += 16) {
     float g[16], w[16];
@@ -473,67 +543,46 @@ __device__ __forceinline__ void weigh_scores(const Ctl* c, uint8_t* m_row, uint3
 
 template <int K, int PARTS>
 __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rep = p.H / p.G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = p.V == 64 ? 2 : 1;
   // the columns of M after the rows' half are never written again
-  for (uint32_t i = tid; i < kTileBytes / 16; i += kMThreads)
+  for (uint32_t i = threadIdx.x; i < kTileBytes / 16; i += kMThreads)
     *reinterpret_cast<uint4*>(sm + OFF_M + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_async_smem();
+  named_bar(BAR_RGRP + 1, kMThreads);
 
   const bool scores = (warp & 2) == 0;    // warps 0, 1, 4, 5
   const int rh = warp & 1;                // half of the rows (TMEM lanes 32 rh, + 32)
-  const bool scans = warp == 2 || (warp == 3 && heads == 2);
-  const int sh = warp & 1;                // head that warp 2 or 3 scans
-  const int xt = (warp >> 2) * 64 + (warp & 1) * 32 + lane;  // 0..127 over warps 2, 3, 6, 7
+  // x' in 32 pieces of 4 rows x 8 cells of 16 bytes, 3 for a warp that makes M and 5 for another; a
+  // warp's pieces are 8 rows and so 1024 bytes apart, on from the first half of the columns to the
+  // second
+  constexpr int kMost = 5;
+  const int nq = scores ? 3 : 5, q0 = (scores ? 0 : 6) + (warp >> 2) * nq;  // in pieces of 8 rows
+  const int r0 = (warp & 1) * 4 + (lane >> 3);                              // row within 8
+  const uint32_t cell0 = q0 * 1024 + r0 * 128 + (((lane ^ r0) & 7u) << 4);
   uint32_t j = 0;
   for (uint32_t k = 0;; ++k) {
-    const Item it = tc_item(p, c, k, BAR_MG, kMThreads, tid == 0);
+    const Item it = tc_item_warp(p, c, k);
     if (it.done) return;
-    const bool second = p.V == 128 || (it.h0 % rep) + 1 < rep;
-    const bool mine = scans && (sh == 0 || second);
-    float rate2 = 0.f, bias = 0.f;
-    if (mine) {
-      rate2 = -expf(p.a_log[it.h0 + sh]) * 1.4426950408889634f;
-      bias = p.dt_bias ? p.dt_bias[it.h0 + sh] : 0.f;
-    }
-    // the steps are read a chunk ahead of their scan; -inf: no token, a step of zero
-    float n0 = -INFINITY, n1 = -INFINITY;
-    const __nv_bfloat16* dtp = p.dt + it.h0 + sh;
-    if (mine) {
-      const int64_t t = it.bos + 2 * lane;
-      if (t < it.eos) n0 = to_f32(dtp[t * p.dt_pitch]);
-      if (t + 1 < it.eos) n1 = to_f32(dtp[(t + 1) * p.dt_pitch]);
-    }
     for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
-      const uint32_t st = j % kStages, par = j & 1;
+      const uint32_t st = j % kStages, par = j & 1, fi = j % kFacs;
       uint8_t* stage = sm + st * kStageBytes;
-      if (!scores) {
-        if (scans) {
-          const float d0 = n0 == -INFINITY ? 0.f : ssm_step(n0, bias);
-          const float d1 = n1 == -INFINITY ? 0.f : ssm_step(n1, bias);
-          if (j >= 2) tc_wait(p, c, T_EPI + par, ((j >> 1) - 1) & 1);  // the factors' last readers
-          scan_steps(c, sh, par, d0, d1, rate2, lane);
-          n0 = n1 = -INFINITY;
-          const int64_t t = it.bos + (int64_t)(ch + 1) * kL + 2 * lane;
-          if (mine && t < it.eos) n0 = to_f32(dtp[t * p.dt_pitch]);
-          if (mine && t + 1 < it.eos) n1 = to_f32(dtp[(t + 1) * p.dt_pitch]);
-        }
-        tc_wait(p, c, T_FULL + st, (j / kStages) & 1);
-        // the rows after the sequence's last token are another's (or nobody's): they must not reach
-        // a product, where a zero weight would not hide an infinity
-        const int64_t left = it.eos - it.bos - (int64_t)ch * kL;
-        if (left < kL) {
-          const int m = (int)left;
-          for (int i = xt; i < (kL - m) * 32; i += 128) {
-            const uint32_t tile = (i >> 3) & 3;  // b and x, two halves each
-            *reinterpret_cast<uint4*>(stage + OFF_B + tile * 8192 + sw128_off(m + (i >> 5), i & 7)) =
-                make_uint4(0, 0, 0, 0);
+      const Factors* f = &c->fac[fi];
+      if (__any_sync(0xffffffffu, tc_aborted(c))) return;
+      tc_wait(p, c, T_FAC + fi, (j / kFacs) & 1);
+      tc_wait(p, c, T_FULL + st, (j / kStages) & 1);
+      // the rows after the sequence's last token are another's (or nobody's): they must not reach a
+      // product, where a zero weight would not hide an infinity
+      const int64_t left = it.eos - it.bos - (int64_t)ch * kL;
+      if (left < kL) {
+#pragma unroll 1
+        for (int i = 0; i < nq; ++i) {
+          if (((q0 + i) & 7) * 8 + r0 >= (int)left) {
+            *reinterpret_cast<uint4*>(stage + OFF_X + cell0 + i * 1024) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(stage + OFF_B + cell0 + i * 1024) = make_uint4(0, 0, 0, 0);
           }
-          fence_async_smem();
         }
-        warp_arrive(&c->bar[T_M + par]);
       }
-      if (named_bar_any(BAR_MG, kMThreads, tc_aborted(c))) return;  // factors and cleared rows
       if (scores) {
         tc_wait(p, c, T_G + par, (j >> 1) & 1);
         if (j > 0) tc_wait(p, c, T_MX, (j - 1) & 1);  // the product that read the last M is done
@@ -541,32 +590,34 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         const uint32_t tg = tbase + TM_YM + par * 128 + ((uint32_t)(rh * 32) << 16);
         // pieces of 32 x 32: heads on warps 0, 1 and 4, 5; one head's second row half is shared
         const int hd = heads == 2 ? warp >> 2 : 0;
-        const float cl = c->cl[hd][rh * 32 + lane];
+        const float cl = f->cl[hd][rh * 32 + lane];
         uint8_t* m_row = sm + OFF_M + hd * 8192 + rh * 4096 + (lane >> 3) * 1024 + (lane & 7) * 128;
-        if (rh == 1 && (heads == 2 || warp == 1)) weigh_scores<false>(c, m_row, tg, hd, 0, cl, lane);
-        if (heads == 2 || warp == 0 || warp == 5) weigh_scores<true>(c, m_row, tg, hd, rh, cl, lane);
+        if (rh == 1 && (heads == 2 || warp == 1)) weigh_scores<false>(f, m_row, tg, hd, 0, cl, lane);
+        if (heads == 2 || warp == 0 || warp == 5) weigh_scores<true>(f, m_row, tg, hd, rh, cl, lane);
         tc_fence_before();
-        fence_async_smem();
-        warp_arrive(&c->bar[T_M + par]);
-      } else {
-        // x', written once the product that read the last one is done
-        if (j > 0) tc_wait(p, c, T_SU, (j - 1) & 1);
-#pragma unroll 2
-        for (int i = 0; i < 8; ++i) {
-          const int row = (i & 3) * 16 + (xt >> 3), half = i >> 2;
-          const int hd = heads == 2 ? half : 0;
-          const uint32_t at = half * 8192 + sw128_off(row, xt & 7);
-          const uint4 raw = *reinterpret_cast<const uint4*>(stage + OFF_X + at);
-          uint4 parts[PARTS];
-          split_x<PARTS>(raw, ex2(c->later[hd][row] + (row < 32 ? c->bt[hd] : 0.f)), parts);
-#pragma unroll
-          for (int q = 0; q < PARTS; ++q)
-            *reinterpret_cast<uint4*>(sm + OFF_XP + q * kTileBytes + at) = parts[q];
-        }
-        fence_async_smem();
-        warp_arrive(&c->bar[T_XP]);
       }
-      named_bar(BAR_MG, kMThreads);  // the next chunk's scan overwrites cl, same, later and bt
+      fence_async_smem();
+      warp_arrive(&c->bar[T_M + par]);
+      // x' into registers, and to shared memory once the product that read the last one is done
+      uint4 parts[kMost][PARTS];
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) {
+        if (i >= nq) break;
+        const int row = ((q0 + i) & 7) * 8 + r0, hd = heads == 2 ? (q0 + i) >> 3 : 0;
+        const float w = ex2(f->later[hd][row] + (row < 32 ? f->second[hd] : 0.f));
+        split_x<PARTS>(*reinterpret_cast<const uint4*>(stage + OFF_X + cell0 + i * 1024), w, parts[i]);
+      }
+      warp_arrive(&c->bar[T_FAC_FREE + fi]);
+      if (j > 0) tc_wait(p, c, T_SU, (j - 1) & 1);
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) {
+        if (i >= nq) break;
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q)
+          *reinterpret_cast<uint4*>(sm + OFF_XP + q * kTileBytes + cell0 + i * 1024) = parts[i][q];
+      }
+      fence_async_smem();
+      warp_arrive(&c->bar[T_XP + par]);
     }
   }
 }
@@ -584,6 +635,9 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
   const int vh = p.V == 64 ? v & 63 : v;         // column of that head
   const int half = v >> 6;
   const int rep = p.H / p.G;
+  uint32_t swz[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) swz[i] = ((((v & 63) >> 3) ^ i) & 7u) << 4;
   uint32_t j = 0;
   for (uint32_t k = 0;; ++k) {
     const Item it = tc_item(p, c, k, BAR_RGRP, kRThreads, rt == 0);
@@ -597,17 +651,18 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
     ST* dst = it.dst >= 0 && real ? static_cast<ST*>(p.state_out) + it.dst + so : nullptr;
     if (it.nchunks == 0) {  // an empty sequence keeps its state
       if (dst && (const void*)dst != (const void*)src)
+#pragma unroll 1
         for (int i = 0; i < KH; ++i)
           dst[(int64_t)i * p.V] = src ? src[(int64_t)i * p.V] : from_f32<ST>(0.f);
       continue;
     }
     for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
-      const uint32_t st = j % kStages, par = j & 1;
+      const uint32_t st = j % kStages, par = j & 1, fi = j % kFacs;
       const int64_t t0 = it.bos + (int64_t)ch * kL;
       const int m = it.eos - t0 < kL ? (int)(it.eos - t0) : kL;
       // S before the chunk: its bf16 copy for the product with C, and its decay over the chunk
-      tc_wait(p, c, T_M + par, (j >> 1) & 1);
-      const float dec = c->dec[par][hd];
+      tc_wait(p, c, T_FAC + fi, (j / kFacs) & 1);
+      const float dec = c->fac[fi].dec[hd];
       if (ch > 0) tc_wait(p, c, T_SU, (j - 1) & 1);
       tc_fence_after();
 #pragma unroll 1
@@ -633,29 +688,33 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&c->bar[T_S]);
-      // the output of tokens [32 hf, + 32): the y tile's last store has read it
-      if (rt == 0) bulk_wait_read();
+      // every warp is done with the chunk before; its stage is free once its output has left it
       if (named_bar_any(BAR_RGRP, kRThreads, tc_aborted(c))) goto leave;
+      if (rt == 0 && j > 0) {
+        bulk_wait_read();
+        mbar_arrive(&c->bar[T_EMPTY + (j - 1) % kStages]);
+      }
+      // the output of tokens [32 hf, + 32), which takes the place of x in its tile
       {
-        tc_wait(p, c, T_FULL + st, (j / kStages) & 1);  // x was loaded long ago: its visibility
+        tc_wait(p, c, T_XP + par, (j >> 1) & 1);  // the M group has seen x land and has read it
         tc_wait(p, c, T_Y, j & 1);
         tc_fence_after();
-        const uint8_t* xt = sm + st * kStageBytes + OFF_X + half * 8192 + (v & 7) * 2;
-        const uint32_t vc = (v & 63) >> 3;
-        uint8_t* yt = sm + OFF_Y + half * 8192 + (v & 63) * 2;
+        // rows of 128 bytes whose 16-byte cells are swizzled by the row's low three bits
+        uint8_t* xt = sm + st * kStageBytes + OFF_X + half * 8192 + hf * 4096 + (v & 7) * 2;
         const bool full = m == kL;
+        const float* ef = c->fac[fi].e[hd];
 #pragma unroll 1
-        for (int i0 = 0; i0 < 32; i0 += 16) {
+        for (int i0 = 0; i0 < 32; i0 += 16, xt += 2048) {
           const int tt = hf * 32 + i0;
           float a[16], b[16], x[16], e[16];
           tmem_ld16(tq + TM_YI + tt, a);
           tmem_ld16(tq + TM_YM + par * 128 + (p.V == 64 ? hd * 64 : 0) + tt, b);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            x[i] = to_f32(*reinterpret_cast<const __nv_bfloat16*>(xt + sw128_off(tt + i, vc)));
+            x[i] = to_f32(*reinterpret_cast<const __nv_bfloat16*>(xt + i * 128 + swz[i & 7]));
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
-            const float4 q = *reinterpret_cast<const float4*>(&c->e[par][hd][tt + i]);
+            const float4 q = *reinterpret_cast<const float4*>(ef + tt + i);
             e[i] = q.x; e[i + 1] = q.y; e[i + 2] = q.z; e[i + 3] = q.w;
           }
           tmem_ld_wait();
@@ -670,7 +729,8 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
           }
           if (full) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) *reinterpret_cast<__nv_bfloat16*>(yt + (tt + i) * 128) = r[i];
+            for (int i = 0; i < 16; ++i)
+              *reinterpret_cast<__nv_bfloat16*>(xt + i * 128 + swz[i & 7]) = r[i];
           } else if (real) {
             // a partial chunk's tile would cover the next sequence's rows: rows of its own only
             __nv_bfloat16* yg = p.y + ((t0 + tt) * p.H + h) * p.V + vh;
@@ -685,15 +745,16 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&c->bar[T_EMPTY + st]);
           mbar_arrive(&c->bar[T_EPI + par]);
+          mbar_arrive(&c->bar[T_FAC_FREE + fi]);
         }
         if (full) {
           fence_async_smem();
           named_bar(BAR_RGRP, kRThreads);
           if (rt == 0 && KDA_CHECK(t0 + kL <= p.T)) {
-            tma_store_2d(&p.tm_y, sm + OFF_Y, it.h0 * p.V, (int)t0);
-            if (second) tma_store_2d(&p.tm_y, sm + OFF_Y + 8192, it.h0 * p.V + 64, (int)t0);
+            const uint8_t* yt = sm + st * kStageBytes + OFF_X;
+            tma_store_2d(&p.tm_y, yt, it.h0 * p.V, (int)t0);
+            if (second) tma_store_2d(&p.tm_y, yt + 8192, it.h0 * p.V + 64, (int)t0);
             bulk_commit();
           }
         }
@@ -734,10 +795,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid
   }
   if (threadIdx.x == 0) {
     for (int b = 0; b < T_COUNT; ++b) {
-      uint32_t count = 1;                                   // a loader's or a commit's arrival
-      if (b >= T_EMPTY && b < T_EMPTY + kStages) count = 1 + kRThreads / 32;
-      if (b >= T_M && b <= T_S) count = b == T_XP ? 4 : 8;  // one a warp that writes
-      if (b >= T_ITEM_EMPTY && b < T_ITEM_EMPTY + kItems) count = 3;
+      uint32_t count = 1;  // a loader's, a scan's or a commit's arrival
+      if (b >= T_EMPTY && b < T_EMPTY + kStages) count = 2;        // a commit's and the R group's
+      if (b >= T_FAC_FREE && b < T_FAC_FREE + kFacs) count = 16;   // one a warp of both groups
+      if (b >= T_M && b <= T_S) count = 8;                         // one a warp of a group
+      if (b >= T_ITEM_EMPTY && b < T_ITEM_EMPTY + kItems) count = 11;  // M warps, R, issuer, scan
       mbar_init(&c->bar[b], count);
     }
     c->abort = 0;
@@ -755,7 +817,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid
   if (warp < 8) run_mgroup<K, PARTS>(p, sm, c, tbase);
   else if (warp < 16) run_rgroup<ST, K>(p, sm, c, tbase);
   else if (warp == 16) run_issuer<K, PARTS>(p, sm, c, tbase);
-  else run_loader<K>(p, sm, c);
+  else if (warp == 17) run_loader<K>(p, sm, c);
+  else run_scan(p, c);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -778,7 +841,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tc_encoder() {
 }
 
 // [T, cols] bf16 rows `pitch` elements apart, boxes of 64 tokens x 64 columns.
-bool tc_map(CUtensorMap* m, const void* base, int64_t T, int64_t cols, int64_t pitch, bool swizzle) {
+bool tc_map(CUtensorMap* m, const void* base, int64_t T, int64_t cols, int64_t pitch) {
   auto enc = tc_encoder();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)(T > 0 ? T : 1)};
@@ -786,8 +849,7 @@ bool tc_map(CUtensorMap* m, const void* base, int64_t T, int64_t cols, int64_t p
   cuuint32_t box[2] = {64u, (cuuint32_t)kL};
   cuuint32_t es[2] = {1u, 1u};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE,
-             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -823,10 +885,10 @@ cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t st) {
   ScanParams p;
   memset(&p, 0, sizeof(p));
   const int64_t T = d.total_tokens;
-  if (!tc_map(&p.tm_x, a.in.x, T, (int64_t)H * V, a.in.x_pitch, true) ||
-      !tc_map(&p.tm_b, a.in.b, T, (int64_t)G * K, a.in.b_pitch, true) ||
-      !tc_map(&p.tm_c, a.in.c, T, (int64_t)G * K, a.in.c_pitch, true) ||
-      !tc_map(&p.tm_y, a.y, T, (int64_t)H * V, (int64_t)H * V, false))
+  if (!tc_map(&p.tm_x, a.in.x, T, (int64_t)H * V, a.in.x_pitch) ||
+      !tc_map(&p.tm_b, a.in.b, T, (int64_t)G * K, a.in.b_pitch) ||
+      !tc_map(&p.tm_c, a.in.c, T, (int64_t)G * K, a.in.c_pitch) ||
+      !tc_map(&p.tm_y, a.y, T, (int64_t)H * V, (int64_t)H * V))
     return cudaErrorInvalidValue;
   p.dt = static_cast<const __nv_bfloat16*>(a.in.dt);
   p.dt_pitch = a.in.dt_pitch;
@@ -842,6 +904,7 @@ cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t st) {
   p.status = &hdr->status;
   p.next_item = &hdr->next_item;
   p.wait_limit_ns = pipeline_wait_limit_ns();
+  p.poll = p.wait_limit_ns < kSleepHintNs ? 1 : 0;
   p.N = d.num_seqs;
   p.H = H;
   p.G = G;
