@@ -16,17 +16,21 @@
 // head. Transposed accumulators (lanes = value columns) put both heads into one M = 128 product
 // with the group's B and C as the shared other operand:
 //
-//   G [64 t][s]        = C B^T            A = c tile, B = b tile                  N = 64
-//   YM [128][head, t]  = X^T M^T          A = x tile, B = M tile                  N = 128 or 64
-//   YI [128][t]        = S^T C^T          A = S^T as bf16 (TMEM), B = c tile      N = 64
-//   S^T [128][k]      += X'^T B           A = x' tiles, B = b tile                N = K
+//   G [64 t][s]    = C B^T      A = c tile, B = b tile                                   N = 64
+//   YM [128][t]    = X^T M^T    A = x tile, B = M tile (two 64-wide heads: one product a head,
+//                               the other head's rows of A being zeros)                  N = 64
+//   YI [128][t]    = S^T C^T    A = S^T as bf16 (TMEM), B = c tile                       N = 64
+//   S^T [128][k]  += X'^T B     A = x' (TMEM), B = b tile                                N = K
 //
 // S^T stays in TMEM in fp32 for the whole sequence. x'_s = exp(..) d_s x_s is fp32; it enters as
-// the sum of three bf16 numbers, which hold all its 24 bits (two with a bf16 pool, 2^-17), so that
+// the sum of three bf16 numbers, which hold all its 24 bits (two with a bf16 pool, 2^-16), so that
 // the state keeps fp32 accuracy -- b is exact in bf16. M and the copy of S that C reads are rounded
 // to bf16 once each, like the output. (The scores as 16 x 16 warp-level products, which need no trip
-// through TMEM, took 2100 cycles a chunk against some 500 of the tensor pipe: 516 us a call for
-// 32768 tokens against XXX.)
+// through TMEM, took 2100 cycles a chunk against some 500 of the tensor pipe.)
+//
+// Shared memory's bandwidth is what the products and the warps compete for (with x' as a tile there,
+// and x and y read and written by TMEM lane, two bytes at a time, 3350 wavefronts a chunk): x' goes
+// from registers to TMEM, and x and y move as 8 x 8 blocks transposed on the way (ldmatrix, stmatrix).
 //
 // Warps 0-7 (M group): x', and warps 0, 1, 4, 5, whose TMEM lanes hold the 64 rows of the scores, M.
 // Warps 8-15 (R group): the state's decay and bf16 copy, the output. Warp 16 issues the tcgen05
@@ -58,17 +62,20 @@ constexpr int kItems = 4;       // claimed items in flight
 
 // ---- shared memory (offsets from a 1024-aligned base) -----------------------------------
 constexpr uint32_t kTileBytes = 16384;               // [2 halves][64 rows][128 B]
+constexpr uint32_t OFF_Z0 = 0;                       // 64 rows of zeros: the half of A before x's
+constexpr uint32_t OFF_ST = 8192;
 constexpr uint32_t OFF_C = 0, OFF_B = kTileBytes, OFF_X = 2 * kTileBytes;  // within a stage
 constexpr uint32_t kStageBytes = 3 * kTileBytes;
-constexpr uint32_t OFF_XP = kStages * kStageBytes;   // x' as three bf16 parts, each like x
-constexpr uint32_t OFF_M = OFF_XP + 3 * kTileBytes;  // [2 heads][64 t][64 s] (K-major B)
+constexpr uint32_t OFF_Z1 = OFF_ST + kStages * kStageBytes;  // and the half after
+constexpr uint32_t OFF_M = OFF_Z1 + 8192;            // [2 heads][64 t][64 s] (K-major B)
 constexpr uint32_t OFF_CTL = OFF_M + kTileBytes;
 
 // ---- TMEM columns -------------------------------------------------------------------------
 constexpr uint32_t TM_S = 0;     // S^T fp32 (128)
 constexpr uint32_t TM_SB = 128;  // S^T as bf16 pairs (64)
 constexpr uint32_t TM_YI = 192;  // S^T C^T (64)
-constexpr uint32_t TM_YM = 256;  // X^T M^T, two buffers of 128 by chunk parity; before it the scores
+constexpr uint32_t TM_YM = 256;  // X^T M^T, two buffers of 64 by chunk parity; before it the scores
+constexpr uint32_t TM_XP = 384;  // x'^T as bf16 pairs of tokens, 32 columns a part
 
 enum TcBar {
   T_FULL = 0,                    // a stage's tiles have landed
@@ -211,6 +218,41 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, Desc b, uint
       : "memory");
 }
 
+// Four 8 x 8 blocks of 16-bit elements, transposed: lanes 8 m .. 8 m + 7 give the 16-byte rows of
+// block m; lane l has elements (2 (l % 4), + 1) of the row l / 4 of each transposed block.
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t saddr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
+__device__ __forceinline__ void stsm_x4_trans(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(saddr), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+// TMEM as the same blocks, 16 lanes at a time: 32 fp32 columns (register 4 c + 2 h + i: lane
+// l / 4 + 8 h, column 8 c + 2 (l % 4) + i), or 16 columns of pairs (2 c + h: lane l / 4 + 8 h, column
+// 4 c + l % 4).
+__device__ __forceinline__ void tmem_ld_16x256_x4(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15},"
+      " [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st_16x128_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 // Reads ring entry k (whole group, uniform result) and releases it.
 __device__ __forceinline__ Item tc_item(const ScanParams& p, Ctl* c, uint32_t k, uint32_t bar_id,
                                         uint32_t nthreads, bool leader) {
@@ -290,7 +332,7 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
       const uint32_t st = j % kStages;
       if (j >= (uint32_t)kStages && !tc_wait(p, c, T_EMPTY + st, (j / kStages - 1) & 1)) break;
       if (tc_aborted(c)) break;
-      uint8_t* base = sm + st * kStageBytes;
+      uint8_t* base = sm + OFF_ST + st * kStageBytes;
       uint64_t* bar = &c->bar[T_FULL + st];
       const int t0 = (int)(it.bos + (int64_t)ch * kL);
       mbar_expect_tx(bar, bytes);
@@ -314,9 +356,9 @@ template <int K, int PARTS>
 __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
   if ((threadIdx.x & 31) != 0) return;
   const uint32_t sbase = smem_u32(sm);
-  const int mn = p.V == 64 ? 128 : 64;   // columns of YM: (head, t)
-  const uint32_t id_m = idesc_bf16(128, mn, 1, 0), id_c = idesc_bf16(128, kL, 0, 0),
-                 id_s = idesc_bf16(128, K, 1, 1);
+  const int rep = p.H / p.G;
+  const uint32_t id_m = idesc_bf16(128, kL, 1, 0), id_c = idesc_bf16(128, kL, 0, 0),
+                 id_s = idesc_bf16(128, K, 0, 1);  // an A in TMEM is K-major
   // The scores run up to two chunks ahead, within this item and the next: `kg`, `cg`, `jg` are the
   // item, its chunk and the CTA's chunk they come to next (ng: that item's chunks, -1: not read).
   uint32_t j = 0, kg = 0, jg = 0;
@@ -334,14 +376,14 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         more = c->ring[kg % kItems].done == 0;
         continue;
       }
-      const uint32_t st = jg % kStages, stage = sbase + st * kStageBytes;
+      const uint32_t st = jg % kStages, stage = sbase + OFF_ST + st * kStageBytes;
       ok = tc_wait(p, c, T_FULL + st, (jg / kStages) & 1) &&
            (jg < 2 || tc_wait(p, c, T_EPI + (jg & 1), ((jg >> 1) - 1) & 1));
       if (!ok) return;
       tc_fence_after();
       // rows 64-127 of A are the tile after c's: lanes that nothing reads
       const Desc da = desc128(stage + OFF_C, 16, 1024), db = desc128(stage + OFF_B, 16, 1024);
-      const uint32_t tg = tbase + TM_YM + (jg & 1) * 128;
+      const uint32_t tg = tbase + TM_YM + (jg & 1) * 64;
       mma_ss<false>(tg, da, 0, db, 0, id_c);
 #pragma unroll
       for (int ks = 1; ks < K / 16; ++ks) {
@@ -359,22 +401,30 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
     if (!ok) break;
     const int nchunks = c->ring[slot].nchunks, done = c->ring[slot].done;
     if (done) break;
+    const bool second = p.V == 64 && (c->ring[slot].h0 % rep) + 1 < rep;
     if (ng < 0 || kg < k) {  // nothing left to run ahead with before this item
       kg = k;
       cg = 0;
       ng = nchunks;
     }
     for (int ch = 0; ch < nchunks && ok; ++ch, ++j) {
-      const uint32_t st = j % kStages, stage = sbase + st * kStageBytes;
+      const uint32_t st = j % kStages, stage = sbase + OFF_ST + st * kStageBytes;
       scores(k, j + 2);
       ok = ok && tc_wait(p, c, T_M + (j & 1), (j >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t ym = tbase + TM_YM + (j & 1) * 128;
-      const Desc dx = desc128(stage + OFF_X, 8192, 1024), dm = desc128(sbase + OFF_M, 16, 1024);
+      const uint32_t ym = tbase + TM_YM + (j & 1) * 64;
+      const Desc dm = desc128(sbase + OFF_M, 16, 1024);
+      // the second half of A: x's, or zeros where it is another head's
+      const Desc dx = desc128(stage + OFF_X, p.V == 128 ? 8192 : sbase + OFF_Z1 - (stage + OFF_X), 1024);
       mma_ss<false>(ym, dx, 0, dm, 0, id_m);
 #pragma unroll
       for (int ks = 1; ks < 4; ++ks) mma_ss<true>(ym, dx, ks * 2048, dm, ks * 32, id_m);
+      if (second) {
+        const Desc dy = desc128(sbase + OFF_Z0, stage + OFF_X + 8192 - (sbase + OFF_Z0), 1024);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_ss<true>(ym, dy, ks * 2048, dm, 8192 + ks * 32, id_m);
+      }
       mma_commit(&c->bar[T_MX]);
       ok = tc_wait(p, c, T_S, j & 1);
       if (!ok) break;
@@ -387,10 +437,11 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       mma_commit(&c->bar[T_Y]);
       ok = tc_wait(p, c, T_XP + (j & 1), (j >> 1) & 1);
       if (!ok) break;
-      const Desc dp = desc128(sbase + OFF_XP, 8192, 1024), db = desc128(stage + OFF_B, 8192, 1024);
+      tc_fence_after();
+      const Desc db = desc128(stage + OFF_B, 8192, 1024);
 #pragma unroll
       for (int i = 0; i < PARTS * 4; ++i)  // part i / 4, k-step i % 4
-        mma_ss<true>(tbase + TM_S, dp, (i / 4) * kTileBytes + (i % 4) * 2048, db, (i % 4) * 2048, id_s);
+        mma_ts<true>(tbase + TM_S, tbase + TM_XP + i * 8, db, (i % 4) * 2048, id_s);
       mma_commit(&c->bar[T_SU]);
       mma_commit(&c->bar[T_EMPTY + st]);
     }
@@ -484,28 +535,21 @@ __device__ void run_scan(const ScanParams& p, Ctl* c) {
   }
 }
 
-// x' (8 values) as PARTS bf16 numbers each: truncated parts leave exact remainders.
+// Two values of x' as PARTS bf16 numbers each: truncated parts leave exact remainders.
 template <int PARTS>
-__device__ __forceinline__ void split_x(const uint4& raw, float w, uint4 (&out)[PARTS]) {
-  const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-  uint32_t o[PARTS][4];
+__device__ __forceinline__ void split_x(uint32_t raw, float2 w, uint32_t (&out)[PARTS]) {
+  float a = bf_lo(raw) * w.x, b = bf_hi(raw) * w.y;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a = bf_lo(in[i]) * w, b = bf_hi(in[i]) * w;
-#pragma unroll
-    for (int q = 0; q < PARTS; ++q) {
-      if (q == PARTS - 1) {
-        o[q][i] = pack_bf16x2(a, b);
-      } else {
-        const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-        o[q][i] = __byte_perm(ua, ub, 0x7632);
-        a -= __uint_as_float(ua & 0xffff0000u);
-        b -= __uint_as_float(ub & 0xffff0000u);
-      }
+  for (int q = 0; q < PARTS; ++q) {
+    if (q == PARTS - 1) {
+      out[q] = pack_bf16x2(a, b);
+    } else {
+      const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+      out[q] = __byte_perm(ua, ub, 0x7632);
+      a -= __uint_as_float(ua & 0xffff0000u);
+      b -= __uint_as_float(ub & 0xffff0000u);
     }
   }
-#pragma unroll
-  for (int q = 0; q < PARTS; ++q) out[q] = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
 }
 
 // 32 columns of one head's M for the 32 rows of this warp: the scores times the weights of the
@@ -545,49 +589,54 @@ template <int K, int PARTS>
 __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = p.V == 64 ? 2 : 1;
-  // the columns of M after the rows' half are never written again
-  for (uint32_t i = threadIdx.x; i < kTileBytes / 16; i += kMThreads)
+  // the columns of M after the rows' half are never written again, the zero rows never at all
+  for (uint32_t i = threadIdx.x; i < kTileBytes / 16; i += kMThreads) {
     *reinterpret_cast<uint4*>(sm + OFF_M + i * 16) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(sm + (i < 512 ? OFF_Z0 + i * 16 : OFF_Z1 + (i - 512) * 16)) = make_uint4(0, 0, 0, 0);
+  }
   fence_async_smem();
   named_bar(BAR_RGRP + 1, kMThreads);
 
   const bool scores = (warp & 2) == 0;    // warps 0, 1, 4, 5
   const int rh = warp & 1;                // half of the rows (TMEM lanes 32 rh, + 32)
-  // x' in 32 pieces of 4 rows x 8 cells of 16 bytes, 3 for a warp that makes M and 5 for another; a
-  // warp's pieces are 8 rows and so 1024 bytes apart, on from the first half of the columns to the
-  // second
-  constexpr int kMost = 5;
-  const int nq = scores ? 3 : 5, q0 = (scores ? 0 : 6) + (warp >> 2) * nq;  // in pieces of 8 rows
-  const int r0 = (warp & 1) * 4 + (lane >> 3);                              // row within 8
-  const uint32_t cell0 = q0 * 1024 + r0 * 128 + (((lane ^ r0) & 7u) << 4);
+  // x' of 32 value columns (TMEM lanes of the warp's quadrant) and 32 tokens: where the lane's row of
+  // the 8 x 8 blocks lies in the x tile, for tokens 0-15 and columns 0-15 of those
+  const int quad = warp & 3, th = warp >> 2;
+  const uint32_t row0 = th * 4096 + ((lane >> 4) << 10) + (lane & 7) * 128;
+  const uint32_t col0 = ((quad & 1) * 4 + ((lane >> 3) & 1)) ^ (lane & 7);  // 16-byte cell
+  const uint32_t xoff = OFF_X + (quad >> 1) * 8192 + row0;
+  const uint32_t txp = tbase + TM_XP + th * 16 + ((uint32_t)(quad * 32) << 16);
+  const int hx = heads == 2 ? quad >> 1 : 0;
   uint32_t j = 0;
   for (uint32_t k = 0;; ++k) {
     const Item it = tc_item_warp(p, c, k);
     if (it.done) return;
     for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
       const uint32_t st = j % kStages, par = j & 1, fi = j % kFacs;
-      uint8_t* stage = sm + st * kStageBytes;
+      uint8_t* stage = sm + OFF_ST + st * kStageBytes;
       const Factors* f = &c->fac[fi];
       if (__any_sync(0xffffffffu, tc_aborted(c))) return;
       tc_wait(p, c, T_FAC + fi, (j / kFacs) & 1);
       tc_wait(p, c, T_FULL + st, (j / kStages) & 1);
       // the rows after the sequence's last token are another's (or nobody's): they must not reach a
-      // product, where a zero weight would not hide an infinity
+      // product, where a zero weight would not hide an infinity. Each warp clears its 32 rows and 4
+      // cells of x and b.
       const int64_t left = it.eos - it.bos - (int64_t)ch * kL;
       if (left < kL) {
 #pragma unroll 1
-        for (int i = 0; i < nq; ++i) {
-          if (((q0 + i) & 7) * 8 + r0 >= (int)left) {
-            *reinterpret_cast<uint4*>(stage + OFF_X + cell0 + i * 1024) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(stage + OFF_B + cell0 + i * 1024) = make_uint4(0, 0, 0, 0);
+        for (int r = (int)left > th * 32 ? (int)left : th * 32; r < th * 32 + 32; ++r) {
+          if (lane < 8) {
+            const uint32_t at = (quad >> 1) * 8192 + sw128_off(r, (quad & 1) * 4 + (lane & 3));
+            *reinterpret_cast<uint4*>(stage + (lane < 4 ? OFF_X : OFF_B) + at) = make_uint4(0, 0, 0, 0);
           }
         }
+        __syncwarp();
       }
       if (scores) {
         tc_wait(p, c, T_G + par, (j >> 1) & 1);
         if (j > 0) tc_wait(p, c, T_MX, (j - 1) & 1);  // the product that read the last M is done
         tc_fence_after();
-        const uint32_t tg = tbase + TM_YM + par * 128 + ((uint32_t)(rh * 32) << 16);
+        const uint32_t tg = tbase + TM_YM + par * 64 + ((uint32_t)(rh * 32) << 16);
         // pieces of 32 x 32: heads on warps 0, 1 and 4, 5; one head's second row half is shared
         const int hd = heads == 2 ? warp >> 2 : 0;
         const float cl = f->cl[hd][rh * 32 + lane];
@@ -598,25 +647,41 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       }
       fence_async_smem();
       warp_arrive(&c->bar[T_M + par]);
-      // x' into registers, and to shared memory once the product that read the last one is done
-      uint4 parts[kMost][PARTS];
+      // x' into registers, and to TMEM once the product that read the last one is done
+      float2 w[4];
 #pragma unroll
-      for (int i = 0; i < kMost; ++i) {
-        if (i >= nq) break;
-        const int row = ((q0 + i) & 7) * 8 + r0, hd = heads == 2 ? (q0 + i) >> 3 : 0;
-        const float w = ex2(f->later[hd][row] + (row < 32 ? f->second[hd] : 0.f));
-        split_x<PARTS>(*reinterpret_cast<const uint4*>(stage + OFF_X + cell0 + i * 1024), w, parts[i]);
+      for (int i = 0; i < 4; ++i) {
+        const float2 q = *reinterpret_cast<const float2*>(&f->later[hx][th * 32 + i * 8 + 2 * (lane & 3)]);
+        const float then = th == 0 ? f->second[hx] : 0.f;
+        w[i] = make_float2(ex2(q.x + then), ex2(q.y + then));
+      }
+      uint32_t parts[PARTS][2][8];
+#pragma unroll
+      for (int lh = 0; lh < 2; ++lh) {
+#pragma unroll
+        for (int t2 = 0; t2 < 2; ++t2) {
+          uint32_t raw[4];
+          ldsm_x4_trans(raw, smem_u32(stage) + xoff + t2 * 2048 + ((col0 ^ (lh * 2)) << 4));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[PARTS];
+            split_x<PARTS>(raw[i], w[t2 * 2 + (i >> 1)], o);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) parts[q][lh][t2 * 4 + i] = o[q];
+          }
+        }
       }
       warp_arrive(&c->bar[T_FAC_FREE + fi]);
       if (j > 0) tc_wait(p, c, T_SU, (j - 1) & 1);
+      tc_fence_after();
 #pragma unroll
-      for (int i = 0; i < kMost; ++i) {
-        if (i >= nq) break;
+      for (int q = 0; q < PARTS; ++q) {
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q)
-          *reinterpret_cast<uint4*>(sm + OFF_XP + q * kTileBytes + cell0 + i * 1024) = parts[i][q];
+        for (int lh = 0; lh < 2; ++lh)
+          tmem_st_16x128_x4(txp + q * 32 + ((uint32_t)(lh * 16) << 16), parts[q][lh]);
       }
-      fence_async_smem();
+      tmem_st_wait();
+      tc_fence_before();
       warp_arrive(&c->bar[T_XP + par]);
     }
   }
@@ -635,9 +700,9 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
   const int vh = p.V == 64 ? v & 63 : v;         // column of that head
   const int half = v >> 6;
   const int rep = p.H / p.G;
-  uint32_t swz[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) swz[i] = ((((v & 63) >> 3) ^ i) & 7u) << 4;
+  // the output's 8 x 8 blocks, as in the M group: 32 value columns, tokens [32 hf, + 32)
+  const uint32_t xoff = OFF_X + half * 8192 + hf * 4096 + ((lane >> 4) << 10) + (lane & 7) * 128;
+  const uint32_t col0 = ((quad & 1) * 4 + ((lane >> 3) & 1)) ^ (lane & 7);
   uint32_t j = 0;
   for (uint32_t k = 0;; ++k) {
     const Item it = tc_item(p, c, k, BAR_RGRP, kRThreads, rt == 0);
@@ -699,48 +764,30 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         tc_wait(p, c, T_XP + par, (j >> 1) & 1);  // the M group has seen x land and has read it
         tc_wait(p, c, T_Y, j & 1);
         tc_fence_after();
-        // rows of 128 bytes whose 16-byte cells are swizzled by the row's low three bits
-        uint8_t* xt = sm + st * kStageBytes + OFF_X + half * 8192 + hf * 4096 + (v & 7) * 2;
-        const bool full = m == kL;
-        const float* ef = c->fac[fi].e[hd];
-#pragma unroll 1
-        for (int i0 = 0; i0 < 32; i0 += 16, xt += 2048) {
-          const int tt = hf * 32 + i0;
-          float a[16], b[16], x[16], e[16];
-          tmem_ld16(tq + TM_YI + tt, a);
-          tmem_ld16(tq + TM_YM + par * 128 + (p.V == 64 ? hd * 64 : 0) + tt, b);
+        uint8_t* stage = sm + OFF_ST + st * kStageBytes;
+        float2 e[4];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            x[i] = to_f32(*reinterpret_cast<const __nv_bfloat16*>(xt + i * 128 + swz[i & 7]));
+        for (int i = 0; i < 4; ++i)
+          e[i] = *reinterpret_cast<const float2*>(&c->fac[fi].e[hd][hf * 32 + i * 8 + 2 * (lane & 3)]);
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 q = *reinterpret_cast<const float4*>(ef + tt + i);
-            e[i] = q.x; e[i + 1] = q.y; e[i + 2] = q.z; e[i + 3] = q.w;
-          }
+        for (int lh = 0; lh < 2; ++lh) {
+          float a[16], b[16];
+          tmem_ld_16x256_x4(tq + ((uint32_t)(lh * 16) << 16) + TM_YI + hf * 32, a);
+          tmem_ld_16x256_x4(tq + ((uint32_t)(lh * 16) << 16) + TM_YM + par * 64 + hf * 32, b);
+          const uint32_t at = smem_u32(stage) + xoff + ((col0 ^ (lh * 2)) << 4);
+          uint32_t x[2][4];
+          ldsm_x4_trans(x[0], at);
+          ldsm_x4_trans(x[1], at + 2048);
           tmem_ld_wait();
-          __nv_bfloat16 r[16];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            fma2(a[i], a[i + 1], e[i], e[i + 1], b[i], b[i + 1]);
-            fma2(x[i], x[i + 1], dskip, dskip, a[i], a[i + 1]);
-            const __nv_bfloat162 q = __floats2bfloat162_rn(x[i], x[i + 1]);
-            r[i] = q.x;
-            r[i + 1] = q.y;
+          for (int i = 0; i < 8; ++i) {  // block i / 2 of 8 tokens, lanes 0-7 or 8-15 of the 16
+            float u = bf_lo(x[i >> 2][i & 3]), w = bf_hi(x[i >> 2][i & 3]);
+            fma2(a[2 * i], a[2 * i + 1], e[i >> 1].x, e[i >> 1].y, b[2 * i], b[2 * i + 1]);
+            fma2(u, w, dskip, dskip, a[2 * i], a[2 * i + 1]);
+            x[i >> 2][i & 3] = pack_bf16x2(u, w);
           }
-          if (full) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              *reinterpret_cast<__nv_bfloat16*>(xt + i * 128 + swz[i & 7]) = r[i];
-          } else if (real) {
-            // a partial chunk's tile would cover the next sequence's rows: rows of its own only
-            __nv_bfloat16* yg = p.y + ((t0 + tt) * p.H + h) * p.V + vh;
-            const int row = p.H * p.V;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (tt + i < m && KDA_CHECK(t0 + tt + i < p.T)) *yg = r[i];
-              yg += row;
-            }
-          }
+          stsm_x4_trans(at, x[0][0], x[0][1], x[0][2], x[0][3]);
+          stsm_x4_trans(at + 2048, x[1][0], x[1][1], x[1][2], x[1][3]);
         }
         tc_fence_before();
         __syncwarp();
@@ -748,14 +795,22 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
           mbar_arrive(&c->bar[T_EPI + par]);
           mbar_arrive(&c->bar[T_FAC_FREE + fi]);
         }
-        if (full) {
-          fence_async_smem();
-          named_bar(BAR_RGRP, kRThreads);
+        fence_async_smem();
+        named_bar(BAR_RGRP, kRThreads);
+        if (m == kL) {
           if (rt == 0 && KDA_CHECK(t0 + kL <= p.T)) {
-            const uint8_t* yt = sm + st * kStageBytes + OFF_X;
-            tma_store_2d(&p.tm_y, yt, it.h0 * p.V, (int)t0);
-            if (second) tma_store_2d(&p.tm_y, yt + 8192, it.h0 * p.V + 64, (int)t0);
+            tma_store_2d(&p.tm_y, stage + OFF_X, it.h0 * p.V, (int)t0);
+            if (second) tma_store_2d(&p.tm_y, stage + OFF_X + 8192, it.h0 * p.V + 64, (int)t0);
             bulk_commit();
+          }
+        } else {
+          // the box of a partial chunk would cover the next sequence's rows: 16 bytes a thread of its own
+#pragma unroll 1
+          for (int i = rt; i < m * 16; i += kRThreads) {
+            const int row = i >> 4, hh = (i >> 3) & 1, cell = i & 7;
+            if ((hh == 0 || second) && KDA_CHECK(t0 + row < p.T))
+              *reinterpret_cast<uint4*>(p.y + ((t0 + row) * p.H + it.h0) * p.V + hh * 64 + cell * 8) =
+                  *reinterpret_cast<const uint4*>(stage + OFF_X + hh * 8192 + sw128_off(row, cell));
           }
         }
       }
