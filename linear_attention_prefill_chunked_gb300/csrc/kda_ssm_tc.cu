@@ -114,8 +114,11 @@ struct Ctl {
   uint64_t bar[T_COUNT];
   Item ring[kItems];
   Factors fac[kFacs];
+  uint64_t wait_limit_ns;
+  uint32_t* status;
   uint32_t tmem_base;
   uint32_t abort;
+  uint32_t poll;            // waits poll: the limit is below what try_wait may suspend a thread for
 };
 constexpr uint32_t kTcSmem = OFF_CTL + ((sizeof(Ctl) + 15) & ~15u);
 static_assert(kTcSmem <= 232448, "shared memory budget exceeded");
@@ -132,7 +135,6 @@ struct ScanParams {
   uint32_t* status;
   uint32_t* next_item;
   uint64_t wait_limit_ns;
-  int32_t poll;                // waits poll: the limit is below what try_wait may suspend a thread for
   int32_t N, H, G, V, pairs;   // pairs: items a sequence
   int64_t T, num_slots, slot_stride;
 };
@@ -140,24 +142,30 @@ struct ScanParams {
 __device__ __forceinline__ bool tc_aborted(const Ctl* c) {
   return *reinterpret_cast<const volatile uint32_t*>(&c->abort) != 0u;
 }
+extern __shared__ __align__(1024) uint8_t ssm_smem[];
+__device__ __forceinline__ Ctl* ctl() { return reinterpret_cast<Ctl*>(ssm_smem + OFF_CTL); }
+
 // Bounded wait; after a timeout anywhere in the CTA every wait returns at once (false). The hardware
 // suspends the thread in try_wait until the phase completes or some microseconds have passed, so that
-// a waiting warp takes few issue slots; a limit shorter than that polls instead.
-__device__ __noinline__ bool tc_wait_slow(const ScanParams& p, Ctl* c, int b, uint32_t parity) {
-  uint64_t* bar = &c->bar[b];
+// a waiting warp takes few issue slots; a limit shorter than that polls instead. Out of line, as is
+// what else the chunk loop runs at several places: the warps of a CTA run five programs at once, and
+// their instruction cache is what they are short of (see the launch).
+__device__ __noinline__ bool tc_wait_slow(uint64_t* bar, uint32_t parity) {
+  Ctl* c = ctl();
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
-    if (p.poll ? mbar_test_wait(bar, parity) : mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
+    if (c->poll ? mbar_test_wait(bar, parity) : mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
     if (tc_aborted(c)) return false;
-    if (globaltimer_ns() - t0 > p.wait_limit_ns) {
-      if (atomicExch(&c->abort, 1u) == 0u) raise_status(p.status, KDA_DEVICE_PIPE_TIMEOUT);
+    if (globaltimer_ns() - t0 > c->wait_limit_ns) {
+      if (atomicExch(&c->abort, 1u) == 0u) raise_status(c->status, KDA_DEVICE_PIPE_TIMEOUT);
       return false;
     }
   }
 }
-__device__ __forceinline__ bool tc_wait(const ScanParams& p, Ctl* c, int b, uint32_t parity) {
-  if (p.poll == 0 && mbar_try_wait_sleep(&c->bar[b], parity, kSleepHintNs)) return true;
-  return tc_wait_slow(p, c, b, parity);
+__device__ __forceinline__ bool tc_wait(int b, uint32_t parity) {
+  uint64_t* bar = &ctl()->bar[b];
+  if (mbar_test_wait(bar, parity)) return true;
+  return tc_wait_slow(bar, parity);
 }
 // One arrival a warp, after what its lanes wrote.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -176,6 +184,13 @@ __device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
   asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
   asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(ab) : "l"(xy));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
+}
+__device__ __forceinline__ void sub2(float& a, float& b, float x, float y) {
+  unsigned long long ab, xy;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
+  asm("sub.rn.f32x2 %0, %0, %1;" : "+l"(ab) : "l"(xy));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
 }
 // (a, b) <- (a, b) * (x, y) + (u, v)
@@ -199,23 +214,29 @@ __device__ __forceinline__ Desc desc128(uint32_t saddr, uint32_t lbo, uint32_t s
   const uint64_t d = sdesc_sw128(saddr, lbo, sbo);
   return {(uint32_t)d, (uint32_t)(d >> 32)};
 }
-template <bool kAcc>
-__device__ __forceinline__ void mma_ss(uint32_t d, Desc a, uint32_t a_off, Desc b, uint32_t b_off,
-                                       uint32_t idesc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %6, 0;\n mov.b64 x, {%1, %2};\n"
-      " mov.b64 y, {%3, %4};\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}\n" ::"r"(d),
-      "r"(a.lo + (a_off >> 4)), "r"(a.hi), "r"(b.lo + (b_off >> 4)), "r"(b.hi), "r"(idesc),
-      "n"(kAcc ? 1 : 0)
-      : "memory");
+// Four k-steps of a product, A and B from shared memory, their descriptors a_step and b_step apart;
+// `acc`: the first step adds to D too.
+__device__ __forceinline__ void issue_ss(uint32_t d, Desc a, uint32_t a_step, Desc b, uint32_t b_step,
+                                      uint32_t idesc, uint32_t acc) {
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks)
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %6, 0;\n mov.b64 x, {%1, %2};\n"
+        " mov.b64 y, {%3, %4};\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}\n" ::"r"(d),
+        "r"(a.lo + ks * (a_step >> 4)), "r"(a.hi), "r"(b.lo + ks * (b_step >> 4)), "r"(b.hi), "r"(idesc),
+        "r"(ks ? 1u : acc)
+        : "memory");
 }
-template <bool kAcc>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, Desc b, uint32_t b_off, uint32_t idesc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
-      "r"(a_tmem), "r"(b.lo + (b_off >> 4)), "r"(b.hi), "r"(idesc), "n"(kAcc ? 1 : 0)
-      : "memory");
+// The same with A in TMEM, 8 columns a k-step.
+__device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a_tmem, Desc b, uint32_t b_step, uint32_t idesc,
+                                      uint32_t acc) {
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks)
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+        "r"(a_tmem + ks * 8), "r"(b.lo + ks * (b_step >> 4)), "r"(b.hi), "r"(idesc), "r"(ks ? 1u : acc)
+        : "memory");
 }
 
 // Four 8 x 8 blocks of 16-bit elements, transposed: lanes 8 m .. 8 m + 7 give the 16-byte rows of
@@ -257,7 +278,7 @@ __device__ __forceinline__ void tmem_st_16x128_x4(uint32_t taddr, const uint32_t
 __device__ __forceinline__ Item tc_item(const ScanParams& p, Ctl* c, uint32_t k, uint32_t bar_id,
                                         uint32_t nthreads, bool leader) {
   const int slot = k % kItems;
-  const bool ok = tc_wait(p, c, T_ITEM_FULL + slot, (k / kItems) & 1);
+  const bool ok = tc_wait(T_ITEM_FULL + slot, (k / kItems) & 1);
   Item it = c->ring[slot];
   const bool stop = named_bar_any(bar_id, nthreads, !ok || it.done != 0 || tc_aborted(c));
   if (leader && ok) mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
@@ -268,7 +289,7 @@ __device__ __forceinline__ Item tc_item(const ScanParams& p, Ctl* c, uint32_t k,
 // The same for one warp.
 __device__ __forceinline__ Item tc_item_warp(const ScanParams& p, Ctl* c, uint32_t k) {
   const int slot = k % kItems;
-  const bool ok = tc_wait(p, c, T_ITEM_FULL + slot, (k / kItems) & 1);
+  const bool ok = tc_wait(T_ITEM_FULL + slot, (k / kItems) & 1);
   Item it = c->ring[slot];
   const bool stop = __any_sync(0xffffffffu, !ok || it.done != 0 || tc_aborted(c));
   __syncwarp();
@@ -321,28 +342,48 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
       break;
     }
     const int slot = k % kItems;
-    if (k >= (uint32_t)kItems && !tc_wait(p, c, T_ITEM_EMPTY + slot, (k / kItems - 1) & 1)) break;
+    if (k >= (uint32_t)kItems && !tc_wait(T_ITEM_EMPTY + slot, (k / kItems - 1) & 1)) break;
     c->ring[slot] = it;
     mbar_arrive(&c->bar[T_ITEM_FULL + slot]);
     if (it.done) break;
     const int g = it.h0 / rep;
     const bool second = p.V == 128 || (it.h0 % rep) + 1 < rep;
     const uint32_t bytes = 2u * (K / 64) * 8192u + (second ? 16384u : 8192u);
-    for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
+    // a stage comes free little more than a chunk before its tiles are wanted, less than a load from
+    // HBM takes: the tiles are brought into L2 kAhead chunks before
+    constexpr int kAhead = 3;
+    auto prefetch = [&](int ch) {
+      const int t0 = (int)(it.bos + (int64_t)ch * kL);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (half < K / 64) {
+          tma_prefetch_2d(&p.tm_c, g * K + half * 64, t0);
+          tma_prefetch_2d(&p.tm_b, g * K + half * 64, t0);
+        }
+        if (half == 0 || second) tma_prefetch_2d(&p.tm_x, it.h0 * p.V + half * 64, t0);
+      }
+    };
+#pragma unroll 1
+    for (int ch = -kAhead; ch < it.nchunks; ++ch) {
+      if (ch + kAhead < it.nchunks) prefetch(ch + kAhead);
+      if (ch < 0) continue;
       const uint32_t st = j % kStages;
-      if (j >= (uint32_t)kStages && !tc_wait(p, c, T_EMPTY + st, (j / kStages - 1) & 1)) break;
+      if (j >= (uint32_t)kStages && !tc_wait(T_EMPTY + st, (j / kStages - 1) & 1)) break;
       if (tc_aborted(c)) break;
       uint8_t* base = sm + OFF_ST + st * kStageBytes;
       uint64_t* bar = &c->bar[T_FULL + st];
       const int t0 = (int)(it.bos + (int64_t)ch * kL);
       mbar_expect_tx(bar, bytes);
 #pragma unroll
-      for (int half = 0; half < K / 64; ++half) {
-        tma_load_2d(base + OFF_C + half * 8192, &p.tm_c, bar, g * K + half * 64, t0);
-        tma_load_2d(base + OFF_B + half * 8192, &p.tm_b, bar, g * K + half * 64, t0);
+      for (int half = 0; half < 2; ++half) {
+        if (half < K / 64) {
+          tma_load_2d(base + OFF_C + half * 8192, &p.tm_c, bar, g * K + half * 64, t0);
+          tma_load_2d(base + OFF_B + half * 8192, &p.tm_b, bar, g * K + half * 64, t0);
+        }
+        if (half == 0 || second)
+          tma_load_2d(base + OFF_X + half * 8192, &p.tm_x, bar, it.h0 * p.V + half * 64, t0);
       }
-      tma_load_2d(base + OFF_X, &p.tm_x, bar, it.h0 * p.V, t0);
-      if (second) tma_load_2d(base + OFF_X + 8192, &p.tm_x, bar, it.h0 * p.V + 64, t0);
+      ++j;
     }
     if (tc_aborted(c)) break;
   }
@@ -368,7 +409,7 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
     while (ok && more && jg < upto) {
       if (cg >= ng) {
         if (kg > k) return;
-        ok = tc_wait(p, c, T_ITEM_FULL + (kg + 1) % kItems, ((kg + 1) / kItems) & 1);
+        ok = tc_wait(T_ITEM_FULL + (kg + 1) % kItems, ((kg + 1) / kItems) & 1);
         if (!ok) return;
         ++kg;
         cg = 0;
@@ -377,19 +418,15 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         continue;
       }
       const uint32_t st = jg % kStages, stage = sbase + OFF_ST + st * kStageBytes;
-      ok = tc_wait(p, c, T_FULL + st, (jg / kStages) & 1) &&
-           (jg < 2 || tc_wait(p, c, T_EPI + (jg & 1), ((jg >> 1) - 1) & 1));
+      ok = tc_wait(T_FULL + st, (jg / kStages) & 1) &&
+           (jg < 2 || tc_wait(T_EPI + (jg & 1), ((jg >> 1) - 1) & 1));
       if (!ok) return;
       tc_fence_after();
       // rows 64-127 of A are the tile after c's: lanes that nothing reads
-      const Desc da = desc128(stage + OFF_C, 16, 1024), db = desc128(stage + OFF_B, 16, 1024);
-      const uint32_t tg = tbase + TM_YM + (jg & 1) * 64;
-      mma_ss<false>(tg, da, 0, db, 0, id_c);
 #pragma unroll
-      for (int ks = 1; ks < K / 16; ++ks) {
-        const uint32_t at = (ks / 4) * 8192 + (ks % 4) * 32;
-        mma_ss<true>(tg, da, at, db, at, id_c);
-      }
+      for (uint32_t kh = 0; kh < K / 64; ++kh)
+        issue_ss(tbase + TM_YM + (jg & 1) * 64, desc128(stage + OFF_C + kh * 8192, 16, 1024), 32,
+                 desc128(stage + OFF_B + kh * 8192, 16, 1024), 32, id_c, kh);
       mma_commit(&c->bar[T_G + (jg & 1)]);
       ++cg;
       ++jg;
@@ -397,7 +434,7 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
   };
   for (uint32_t k = 0; ok; ++k) {
     const int slot = k % kItems;
-    ok = tc_wait(p, c, T_ITEM_FULL + slot, (k / kItems) & 1);
+    ok = tc_wait(T_ITEM_FULL + slot, (k / kItems) & 1);
     if (!ok) break;
     const int nchunks = c->ring[slot].nchunks, done = c->ring[slot].done;
     if (done) break;
@@ -410,38 +447,32 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
     for (int ch = 0; ch < nchunks && ok; ++ch, ++j) {
       const uint32_t st = j % kStages, stage = sbase + OFF_ST + st * kStageBytes;
       scores(k, j + 2);
-      ok = ok && tc_wait(p, c, T_M + (j & 1), (j >> 1) & 1);
+      ok = ok && tc_wait(T_M + (j & 1), (j >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
       const uint32_t ym = tbase + TM_YM + (j & 1) * 64;
-      const Desc dm = desc128(sbase + OFF_M, 16, 1024);
       // the second half of A: x's, or zeros where it is another head's
-      const Desc dx = desc128(stage + OFF_X, p.V == 128 ? 8192 : sbase + OFF_Z1 - (stage + OFF_X), 1024);
-      mma_ss<false>(ym, dx, 0, dm, 0, id_m);
-#pragma unroll
-      for (int ks = 1; ks < 4; ++ks) mma_ss<true>(ym, dx, ks * 2048, dm, ks * 32, id_m);
-      if (second) {
-        const Desc dy = desc128(sbase + OFF_Z0, stage + OFF_X + 8192 - (sbase + OFF_Z0), 1024);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_ss<true>(ym, dy, ks * 2048, dm, 8192 + ks * 32, id_m);
-      }
+      const uint32_t x0 = stage + OFF_X;
+      issue_ss(ym, desc128(x0, p.V == 128 ? 8192 : sbase + OFF_Z1 - x0, 1024), 2048,
+               desc128(sbase + OFF_M, 16, 1024), 32, id_m, 0);
+      if (second)
+        issue_ss(ym, desc128(sbase + OFF_Z0, x0 + 8192 - (sbase + OFF_Z0), 1024), 2048,
+                 desc128(sbase + OFF_M + 8192, 16, 1024), 32, id_m, 1);
       mma_commit(&c->bar[T_MX]);
-      ok = tc_wait(p, c, T_S, j & 1);
+      ok = tc_wait(T_S, j & 1);
       if (!ok) break;
       tc_fence_after();
-      const Desc dc = desc128(stage + OFF_C, 16, 1024);
-      mma_ts<false>(tbase + TM_YI, tbase + TM_SB, dc, 0, id_c);
 #pragma unroll
-      for (int ks = 1; ks < K / 16; ++ks)
-        mma_ts<true>(tbase + TM_YI, tbase + TM_SB + ks * 8, dc, (ks / 4) * 8192 + (ks % 4) * 32, id_c);
+      for (uint32_t kh = 0; kh < K / 64; ++kh)
+        issue_ts(tbase + TM_YI, tbase + TM_SB + kh * 32, desc128(stage + OFF_C + kh * 8192, 16, 1024), 32, id_c,
+                 kh);
       mma_commit(&c->bar[T_Y]);
-      ok = tc_wait(p, c, T_XP + (j & 1), (j >> 1) & 1);
+      ok = tc_wait(T_XP + (j & 1), (j >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      const Desc db = desc128(stage + OFF_B, 8192, 1024);
 #pragma unroll
-      for (int i = 0; i < PARTS * 4; ++i)  // part i / 4, k-step i % 4
-        mma_ts<true>(tbase + TM_S, tbase + TM_XP + i * 8, db, (i % 4) * 2048, id_s);
+      for (uint32_t part = 0; part < PARTS; ++part)
+        issue_ts(tbase + TM_S, tbase + TM_XP + part * 32, desc128(stage + OFF_B, 8192, 1024), 2048, id_s, 1);
       mma_commit(&c->bar[T_SU]);
       mma_commit(&c->bar[T_EMPTY + st]);
     }
@@ -499,7 +530,7 @@ __device__ void run_scan(const ScanParams& p, Ctl* c) {
 #pragma unroll
     for (int hd = 0; hd < 2; ++hd) {
       if (hd == 1 && !second) break;
-      rate2[hd] = -expf(p.a_log[it.h0 + hd]) * 1.4426950408889634f;
+      rate2[hd] = -ex2(p.a_log[it.h0 + hd] * 1.4426950408889634f) * 1.4426950408889634f;
       bias[hd] = p.dt_bias ? p.dt_bias[it.h0 + hd] : 0.f;
     }
     // the steps of a chunk are read while the one before is scanned; -inf: no token, a step of zero
@@ -514,23 +545,27 @@ __device__ void run_scan(const ScanParams& p, Ctl* c) {
         n[hd][1] = any && t + 1 < it.eos ? to_f32(at[p.dt_pitch + hd]) : -INFINITY;
       }
     };
-    read(0);
-    for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
-      const uint32_t fi = j % kFacs;
+#pragma unroll 1
+    for (int ch = -1; ch < it.nchunks; ++ch) {
       if (__any_sync(0xffffffffu, tc_aborted(c))) return;
       float d[2][2];
+      if (ch >= 0) {
 #pragma unroll
-      for (int hd = 0; hd < 2; ++hd) {
+        for (int hd = 0; hd < 2; ++hd) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) d[hd][i] = step_of(n[hd][i], bias[hd]);
+          for (int i = 0; i < 2; ++i) d[hd][i] = step_of(n[hd][i], bias[hd]);
+        }
       }
       read(ch + 1);
-      if (j >= (uint32_t)kFacs) tc_wait(p, c, T_FAC_FREE + fi, (j / kFacs - 1) & 1);
+      if (ch < 0) continue;
+      const uint32_t fi = j % kFacs;
+      if (j >= (uint32_t)kFacs) tc_wait(T_FAC_FREE + fi, (j / kFacs - 1) & 1);
 #pragma unroll 1
       for (int hd = 0; hd < heads; ++hd)
         scan_steps(&c->fac[fi], hd, hd ? d[1][0] : d[0][0], hd ? d[1][1] : d[0][1],
                    hd ? rate2[1] : rate2[0], lane);
       warp_arrive(&c->bar[T_FAC + fi]);
+      ++j;
     }
   }
 }
@@ -538,7 +573,8 @@ __device__ void run_scan(const ScanParams& p, Ctl* c) {
 // Two values of x' as PARTS bf16 numbers each: truncated parts leave exact remainders.
 template <int PARTS>
 __device__ __forceinline__ void split_x(uint32_t raw, float2 w, uint32_t (&out)[PARTS]) {
-  float a = bf_lo(raw) * w.x, b = bf_hi(raw) * w.y;
+  float a = bf_lo(raw), b = bf_hi(raw);
+  mul2(a, b, w.x, w.y);
 #pragma unroll
   for (int q = 0; q < PARTS; ++q) {
     if (q == PARTS - 1) {
@@ -546,19 +582,20 @@ __device__ __forceinline__ void split_x(uint32_t raw, float2 w, uint32_t (&out)[
     } else {
       const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
       out[q] = __byte_perm(ua, ub, 0x7632);
-      a -= __uint_as_float(ua & 0xffff0000u);
-      b -= __uint_as_float(ub & 0xffff0000u);
+      // a - trunc(a), exact
+      sub2(a, b, __uint_as_float(ua & 0xffff0000u), __uint_as_float(ub & 0xffff0000u));
     }
   }
 }
 
 // 32 columns of one head's M for the 32 rows of this warp: the scores times the weights of the
-// columns. kDiag: the columns' half is the rows' half.
-template <bool kDiag>
-__device__ __forceinline__ void weigh_scores(const Factors* f, uint8_t* m_row, uint32_t tmem, int hd, int half,
-                                             float cl, int lane) {
-  const float* src = kDiag ? f->same[hd] + half * 32 : f->later[hd] + half * 32;
-#pragma unroll
+// columns. diag: the columns' half is the rows' half.
+__device__ __noinline__ void weigh_scores(const Factors* f, uint8_t* m_row, uint32_t tmem, int hd, int half,
+                                          bool diag, float cl) {
+  const int lane = threadIdx.x & 31;
+  const float* src = (diag ? f->same[hd] : f->later[hd]) + half * 32;
+  const int last = diag ? lane : 31;  // a later token's weight may be anything
+#pragma unroll 1
   for (int i0 = 0; i0 < 32; i0 += 16) {
     float g[16], w[16];
     tmem_ld16(tmem + half * 32 + i0, g);
@@ -571,10 +608,7 @@ __device__ __forceinline__ void weigh_scores(const Factors* f, uint8_t* m_row, u
     for (int i = 0; i < 16; ++i) w[i] = ex2(cl + w[i]);
     tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      g[i] *= w[i];
-      if (kDiag) g[i] = i0 + i <= lane ? g[i] : 0.f;  // a later token's weight may be anything
-    }
+    for (int i = 0; i < 16; ++i) g[i] = i <= last - i0 ? g[i] * w[i] : 0.f;
 #pragma unroll
     for (int i = 0; i < 16; i += 8) {
       const uint32_t chunk = half * 4 + (i0 + i) / 8;
@@ -616,8 +650,8 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       uint8_t* stage = sm + OFF_ST + st * kStageBytes;
       const Factors* f = &c->fac[fi];
       if (__any_sync(0xffffffffu, tc_aborted(c))) return;
-      tc_wait(p, c, T_FAC + fi, (j / kFacs) & 1);
-      tc_wait(p, c, T_FULL + st, (j / kStages) & 1);
+      tc_wait(T_FAC + fi, (j / kFacs) & 1);
+      tc_wait(T_FULL + st, (j / kStages) & 1);
       // the rows after the sequence's last token are another's (or nobody's): they must not reach a
       // product, where a zero weight would not hide an infinity. Each warp clears its 32 rows and 4
       // cells of x and b.
@@ -633,16 +667,16 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         __syncwarp();
       }
       if (scores) {
-        tc_wait(p, c, T_G + par, (j >> 1) & 1);
-        if (j > 0) tc_wait(p, c, T_MX, (j - 1) & 1);  // the product that read the last M is done
+        tc_wait(T_G + par, (j >> 1) & 1);
+        if (j > 0) tc_wait(T_MX, (j - 1) & 1);  // the product that read the last M is done
         tc_fence_after();
         const uint32_t tg = tbase + TM_YM + par * 64 + ((uint32_t)(rh * 32) << 16);
         // pieces of 32 x 32: heads on warps 0, 1 and 4, 5; one head's second row half is shared
         const int hd = heads == 2 ? warp >> 2 : 0;
         const float cl = f->cl[hd][rh * 32 + lane];
         uint8_t* m_row = sm + OFF_M + hd * 8192 + rh * 4096 + (lane >> 3) * 1024 + (lane & 7) * 128;
-        if (rh == 1 && (heads == 2 || warp == 1)) weigh_scores<false>(f, m_row, tg, hd, 0, cl, lane);
-        if (heads == 2 || warp == 0 || warp == 5) weigh_scores<true>(f, m_row, tg, hd, rh, cl, lane);
+        if (rh == 1 && (heads == 2 || warp == 1)) weigh_scores(f, m_row, tg, hd, 0, false, cl);
+        if (heads == 2 || warp == 0 || warp == 5) weigh_scores(f, m_row, tg, hd, rh, true, cl);
         tc_fence_before();
       }
       fence_async_smem();
@@ -672,7 +706,7 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         }
       }
       warp_arrive(&c->bar[T_FAC_FREE + fi]);
-      if (j > 0) tc_wait(p, c, T_SU, (j - 1) & 1);
+      if (j > 0) tc_wait(T_SU, (j - 1) & 1);
       tc_fence_after();
 #pragma unroll
       for (int q = 0; q < PARTS; ++q) {
@@ -721,27 +755,32 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
           dst[(int64_t)i * p.V] = src ? src[(int64_t)i * p.V] : from_f32<ST>(0.f);
       continue;
     }
+    // the state before the sequence
+#pragma unroll 1
+    for (int i0 = 0; i0 < KH; i0 += 16) {
+      float s[16];
+      const ST* at = src + i0 * p.V;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = src ? to_f32(at[i * p.V]) : 0.f;
+      tmem_st16(tq + TM_S + hf * KH + i0, s);
+    }
+    tmem_st_wait();
+#pragma unroll 1
     for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
       const uint32_t st = j % kStages, par = j & 1, fi = j % kFacs;
       const int64_t t0 = it.bos + (int64_t)ch * kL;
       const int m = it.eos - t0 < kL ? (int)(it.eos - t0) : kL;
       // S before the chunk: its bf16 copy for the product with C, and its decay over the chunk
-      tc_wait(p, c, T_FAC + fi, (j / kFacs) & 1);
+      tc_wait(T_FAC + fi, (j / kFacs) & 1);
       const float dec = c->fac[fi].dec[hd];
-      if (ch > 0) tc_wait(p, c, T_SU, (j - 1) & 1);
+      if (ch > 0) tc_wait(T_SU, (j - 1) & 1);
       tc_fence_after();
 #pragma unroll 1
       for (int i0 = 0; i0 < KH; i0 += 32) {
         float s[32], pk[16];
-        if (ch == 0) {
-          const ST* at = src + i0 * p.V;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = src ? to_f32(at[i * p.V]) : 0.f;
-        } else {
-          tmem_ld16(tq + TM_S + hf * KH + i0, s);
-          tmem_ld16(tq + TM_S + hf * KH + i0 + 16, s + 16);
-          tmem_ld_wait();
-        }
+        tmem_ld16(tq + TM_S + hf * KH + i0, s);
+        tmem_ld16(tq + TM_S + hf * KH + i0 + 16, s + 16);
+        tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 16; ++i) pk[i] = __uint_as_float(pack_bf16x2(s[2 * i], s[2 * i + 1]));
         tmem_st16(tq + TM_SB + (hf * KH + i0) / 2, pk);
@@ -761,15 +800,15 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       }
       // the output of tokens [32 hf, + 32), which takes the place of x in its tile
       {
-        tc_wait(p, c, T_XP + par, (j >> 1) & 1);  // the M group has seen x land and has read it
-        tc_wait(p, c, T_Y, j & 1);
+        tc_wait(T_XP + par, (j >> 1) & 1);  // the M group has seen x land and has read it
+        tc_wait(T_Y, j & 1);
         tc_fence_after();
         uint8_t* stage = sm + OFF_ST + st * kStageBytes;
         float2 e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           e[i] = *reinterpret_cast<const float2*>(&c->fac[fi].e[hd][hf * 32 + i * 8 + 2 * (lane & 3)]);
-#pragma unroll
+#pragma unroll 1
         for (int lh = 0; lh < 2; ++lh) {
           float a[16], b[16];
           tmem_ld_16x256_x4(tq + ((uint32_t)(lh * 16) << 16) + TM_YI + hf * 32, a);
@@ -816,19 +855,19 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       }
     }
     // the state after the sequence
-    tc_wait(p, c, T_SU, (j - 1) & 1);
+    tc_wait(T_SU, (j - 1) & 1);
     tc_fence_after();
     if (named_bar_any(BAR_RGRP, kRThreads, tc_aborted(c))) break;
     {
 #pragma unroll 1
-      for (int i0 = 0; i0 < KH; i0 += 32) {
-        float s[32];
+      for (int i0 = 0; i0 < KH; i0 += 16) {
+        float s[16];
         tmem_ld16(tq + TM_S + hf * KH + i0, s);
-        tmem_ld16(tq + TM_S + hf * KH + i0 + 16, s + 16);
         tmem_ld_wait();
         if (dst) {
+          ST* at = dst + i0 * p.V;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) dst[(i0 + i) * p.V] = from_f32<ST>(s[i]);
+          for (int i = 0; i < 16; ++i) at[i * p.V] = from_f32<ST>(s[i]);
         }
       }
       tc_fence_before();
@@ -841,8 +880,8 @@ leave:
 template <typename ST, int K>
 __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid_constant__ ScanParams p) {
   constexpr int PARTS = sizeof(ST) == 4 ? 3 : 2;
-  extern __shared__ __align__(1024) uint8_t sm[];
-  Ctl* c = reinterpret_cast<Ctl*>(sm + OFF_CTL);
+  uint8_t* sm = ssm_smem;
+  Ctl* c = ctl();
   const int warp = threadIdx.x >> 5;
   if (smem_u32(sm) & 1023u) {  // the swizzled tiles need it; the window starts so without static smem
     if (threadIdx.x == 0) raise_status(p.status, KDA_DEVICE_PIPE_TIMEOUT);
@@ -858,6 +897,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid
       mbar_init(&c->bar[b], count);
     }
     c->abort = 0;
+    c->wait_limit_ns = p.wait_limit_ns;
+    c->status = p.status;
+    c->poll = p.wait_limit_ns < kSleepHintNs ? 1 : 0;
     fence_mbar_init();
     prefetch_tensormap(&p.tm_x);
     prefetch_tensormap(&p.tm_b);
@@ -959,7 +1001,6 @@ cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t st) {
   p.status = &hdr->status;
   p.next_item = &hdr->next_item;
   p.wait_limit_ns = pipeline_wait_limit_ns();
-  p.poll = p.wait_limit_ns < kSleepHintNs ? 1 : 0;
   p.N = d.num_seqs;
   p.H = H;
   p.G = G;
