@@ -33,8 +33,9 @@
 // from registers to TMEM, and x and y move as 8 x 8 blocks transposed on the way (ldmatrix, stmatrix).
 //
 // Warps 0-7 (M group): x', and warps 0, 1, 4, 5, whose TMEM lanes hold the 64 rows of the scores, M.
-// Warps 8-15 (R group): the state's decay and bf16 copy, the output. Warp 16 issues the tcgen05
-// products, warp 17 claims items and loads tiles (TMA), warp 18 scans the steps. What orders them are
+// Warps 8-15 (R group): the state's decay and bf16 copy, the output. Warps 16 and 19 issue the
+// tcgen05 products (a thread issues one in ~100 cycles here, the pipe takes 52 to 71), warp 17 claims
+// items and loads tiles (TMA), warp 18 scans the steps. What orders them are
 // mbarriers, each wait bounded (a timeout sets KDA_DEVICE_PIPE_TIMEOUT, stops the loads, lets what was
 // issued finish and returns). Only T_SU -> R -> T_S -> products of C and x' -> T_SU is a chain from
 // chunk to chunk; scans, scores, M and the arithmetic of x' run ahead of it.
@@ -56,7 +57,7 @@ using namespace tc;
 constexpr int kL = 64;          // tokens a chunk
 constexpr int kStages = 3;      // chunks of c, b and x tiles in flight
 constexpr int kMThreads = 256, kRThreads = 256;
-constexpr int kTcThreads = kMThreads + kRThreads + 96;
+constexpr int kTcThreads = kMThreads + kRThreads + 128;
 constexpr int kFacs = 3;        // chunks of steps and decays in flight
 constexpr int kItems = 4;       // claimed items in flight
 
@@ -86,12 +87,13 @@ enum TcBar {
   T_EPI = T_M + 2,               // the output has read YM and YI, by parity
   T_XP = T_EPI + 2,              // x' is written, by parity
   T_S = T_XP + 2,                // S is decayed and its bf16 copy written
-  T_MX, T_Y, T_SU,               // the products of M, of C (and M), of x' are done
-  T_G,                           // the scores are done, by parity
+  T_Y, T_SU,                     // the products of C and of x' are done
+  T_MX,                          // the products of M are done, by parity
+  T_G = T_MX + 2,                // the scores are done, by parity
   T_ITEM_FULL = T_G + 2,
   T_ITEM_EMPTY = T_ITEM_FULL + kItems,
   T_DRAIN = T_ITEM_EMPTY + kItems,
-  T_COUNT
+  T_COUNT = T_DRAIN + 2
 };
 
 struct Item {
@@ -392,14 +394,13 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
     mbar_wait(&c->bar[T_FULL + i % kStages], (i / kStages) & 1);
 }
 
-// ---- warp 16: the products ------------------------------------------------------------------
-template <int K, int PARTS>
+// ---- warp 16: the products of the output ------------------------------------------------------
+template <int K>
 __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
   if ((threadIdx.x & 31) != 0) return;
   const uint32_t sbase = smem_u32(sm);
   const int rep = p.H / p.G;
-  const uint32_t id_m = idesc_bf16(128, kL, 1, 0), id_c = idesc_bf16(128, kL, 0, 0),
-                 id_s = idesc_bf16(128, K, 0, 1);  // an A in TMEM is K-major
+  const uint32_t id_m = idesc_bf16(128, kL, 1, 0), id_c = idesc_bf16(128, kL, 0, 0);
   // The scores run up to two chunks ahead, within this item and the next: `kg`, `cg`, `jg` are the
   // item, its chunk and the CTA's chunk they come to next (ng: that item's chunks, -1: not read).
   uint32_t j = 0, kg = 0, jg = 0;
@@ -458,7 +459,7 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       if (second)
         issue_ss(ym, desc128(sbase + OFF_Z0, x0 + 8192 - (sbase + OFF_Z0), 1024), 2048,
                  desc128(sbase + OFF_M + 8192, 16, 1024), 32, id_m, 1);
-      mma_commit(&c->bar[T_MX]);
+      mma_commit(&c->bar[T_MX + (j & 1)]);
       ok = tc_wait(T_S, j & 1);
       if (!ok) break;
       tc_fence_after();
@@ -467,14 +468,6 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         issue_ts(tbase + TM_YI, tbase + TM_SB + kh * 32, desc128(stage + OFF_C + kh * 8192, 16, 1024), 32, id_c,
                  kh);
       mma_commit(&c->bar[T_Y]);
-      ok = tc_wait(T_XP + (j & 1), (j >> 1) & 1);
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (uint32_t part = 0; part < PARTS; ++part)
-        issue_ts(tbase + TM_S, tbase + TM_XP + part * 32, desc128(stage + OFF_B, 8192, 1024), 2048, id_s, 1);
-      mma_commit(&c->bar[T_SU]);
-      mma_commit(&c->bar[T_EMPTY + st]);
     }
     mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
   }
@@ -516,6 +509,39 @@ __device__ __forceinline__ void scan_steps(Factors* f, int head, float d0, float
     f->second[head] = second;
     f->dec[head] = ex2(first + second);
   }
+}
+
+// ---- warp 19: the state's product, the one on the chain from chunk to chunk ---------------------
+template <int K, int PARTS>
+__device__ void run_state(uint8_t* sm, Ctl* c, uint32_t tbase) {
+  if ((threadIdx.x & 31) != 0) return;
+  const uint32_t sbase = smem_u32(sm);
+  const uint32_t id_s = idesc_bf16(128, K, 0, 1);  // an A in TMEM is K-major
+  uint32_t j = 0;
+  bool ok = true;
+  for (uint32_t k = 0; ok; ++k) {
+    const int slot = k % kItems;
+    ok = tc_wait(T_ITEM_FULL + slot, (k / kItems) & 1);
+    if (!ok) break;
+    const int nchunks = c->ring[slot].nchunks, done = c->ring[slot].done;
+    mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
+    if (done) break;
+    for (int ch = 0; ch < nchunks; ++ch, ++j) {
+      const uint32_t st = j % kStages, stage = sbase + OFF_ST + st * kStageBytes;
+      // (x' is made of a tile that has landed, and b landed with it)
+      ok = tc_wait(T_XP + (j & 1), (j >> 1) & 1) && tc_wait(T_FULL + st, (j / kStages) & 1) &&
+           tc_wait(T_S, j & 1);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t part = 0; part < PARTS; ++part)
+        issue_ts(tbase + TM_S, tbase + TM_XP + part * 32, desc128(stage + OFF_B, 8192, 1024), 2048, id_s, 1);
+      mma_commit(&c->bar[T_SU]);
+      mma_commit(&c->bar[T_EMPTY + st]);
+    }
+  }
+  mma_commit(&c->bar[T_DRAIN + 1]);
+  mbar_wait(&c->bar[T_DRAIN + 1], 0);  // the full limit, aborted or not
 }
 
 // ---- warp 18: steps and decays ------------------------------------------------------------------
@@ -668,7 +694,7 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       }
       if (scores) {
         tc_wait(T_G + par, (j >> 1) & 1);
-        if (j > 0) tc_wait(T_MX, (j - 1) & 1);  // the product that read the last M is done
+        if (j > 0) tc_wait(T_MX + (par ^ 1), ((j - 1) >> 1) & 1);  // the product that read the last M is done
         tc_fence_after();
         const uint32_t tg = tbase + TM_YM + par * 64 + ((uint32_t)(rh * 32) << 16);
         // pieces of 32 x 32: heads on warps 0, 1 and 4, 5; one head's second row half is shared
@@ -801,6 +827,7 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       // the output of tokens [32 hf, + 32), which takes the place of x in its tile
       {
         tc_wait(T_XP + par, (j >> 1) & 1);  // the M group has seen x land and has read it
+        tc_wait(T_MX + par, (j >> 1) & 1);
         tc_wait(T_Y, j & 1);
         tc_fence_after();
         uint8_t* stage = sm + OFF_ST + st * kStageBytes;
@@ -893,7 +920,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid
       if (b >= T_EMPTY && b < T_EMPTY + kStages) count = 2;        // a commit's and the R group's
       if (b >= T_FAC_FREE && b < T_FAC_FREE + kFacs) count = 16;   // one a warp of both groups
       if (b >= T_M && b <= T_S) count = 8;                         // one a warp of a group
-      if (b >= T_ITEM_EMPTY && b < T_ITEM_EMPTY + kItems) count = 11;  // M warps, R, issuer, scan
+      if (b >= T_ITEM_EMPTY && b < T_ITEM_EMPTY + kItems) count = 12;  // M warps, R, issuers, scan
       mbar_init(&c->bar[b], count);
     }
     c->abort = 0;
@@ -913,9 +940,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid
   const uint32_t tbase = c->tmem_base;
   if (warp < 8) run_mgroup<K, PARTS>(p, sm, c, tbase);
   else if (warp < 16) run_rgroup<ST, K>(p, sm, c, tbase);
-  else if (warp == 16) run_issuer<K, PARTS>(p, sm, c, tbase);
+  else if (warp == 16) run_issuer<K>(p, sm, c, tbase);
   else if (warp == 17) run_loader<K>(p, sm, c);
-  else run_scan(p, c);
+  else if (warp == 18) run_scan(p, c);
+  else run_state<K, PARTS>(sm, c, tbase);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
