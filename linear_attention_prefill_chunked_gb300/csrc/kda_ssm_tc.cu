@@ -34,8 +34,7 @@
 //
 // Warps 0-7 (M group): x', and warps 0, 1, 4, 5, whose TMEM lanes hold the 64 rows of the scores, M.
 // Warps 8-15 (R group): the state's decay and bf16 copy, the output. Warps 16 and 19 issue the
-// tcgen05 products (a thread issues one in ~100 cycles here, the pipe takes 52 to 71), warp 17 claims
-// items and loads tiles (TMA), warp 18 scans the steps. What orders them are
+// tcgen05 products, warp 17 claims items and moves tiles (TMA), warp 18 scans the steps. What orders them are
 // mbarriers, each wait bounded (a timeout sets KDA_DEVICE_PIPE_TIMEOUT, stops the loads, lets what was
 // issued finish and returns). Only T_SU -> R -> T_S -> products of C and x' -> T_SU is a chain from
 // chunk to chunk; scans, scores, M and the arithmetic of x' run ahead of it.
@@ -123,6 +122,7 @@ struct Ctl {
   uint32_t poll;            // waits poll: the limit is below what try_wait may suspend a thread for
 };
 constexpr uint32_t kTcSmem = OFF_CTL + ((sizeof(Ctl) + 15) & ~15u);
+static_assert(kStages == 3, "the loader keeps three outputs");
 static_assert(kTcSmem <= 232448, "shared memory budget exceeded");
 
 struct ScanParams {
@@ -276,19 +276,7 @@ __device__ __forceinline__ void tmem_st_16x128_x4(uint32_t taddr, const uint32_t
       : "memory");
 }
 
-// Reads ring entry k (whole group, uniform result) and releases it.
-__device__ __forceinline__ Item tc_item(const ScanParams& p, Ctl* c, uint32_t k, uint32_t bar_id,
-                                        uint32_t nthreads, bool leader) {
-  const int slot = k % kItems;
-  const bool ok = tc_wait(T_ITEM_FULL + slot, (k / kItems) & 1);
-  Item it = c->ring[slot];
-  const bool stop = named_bar_any(bar_id, nthreads, !ok || it.done != 0 || tc_aborted(c));
-  if (leader && ok) mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
-  it.done = stop ? 1 : 0;
-  return it;
-}
-
-// The same for one warp.
+// Reads ring entry k (whole warp, uniform result) and releases it.
 __device__ __forceinline__ Item tc_item_warp(const ScanParams& p, Ctl* c, uint32_t k) {
   const int slot = k % kItems;
   const bool ok = tc_wait(T_ITEM_FULL + slot, (k / kItems) & 1);
@@ -300,7 +288,6 @@ __device__ __forceinline__ Item tc_item_warp(const ScanParams& p, Ctl* c, uint32
   return it;
 }
 
-constexpr uint32_t BAR_RGRP = 1;
 
 // ---- warp 17: items and tiles ------------------------------------------------------------
 template <int K>
@@ -310,6 +297,23 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
   const int rep = p.H / p.G;                       // heads a group
   const int per = p.V == 64 ? (rep + 1) / 2 : rep; // items a group
   uint32_t j = 0;                                  // chunks loaded by this CTA
+  // what the chunks in the stages leave as: column, first token, halves (0: stored by the R group)
+  struct Out {
+    int col, t0, halves;
+  } out[kStages] = {};
+  // stage st (chunk i of the CTA) is done with: its output leaves, and it is free once that was read
+  auto leave = [&](uint32_t i) -> bool {
+    const uint32_t st = i % kStages;
+    if (!tc_wait(T_EMPTY + st, (i / kStages) & 1)) return false;
+    const Out o = st == 0 ? out[0] : st == 1 ? out[1] : out[2];
+    if (o.halves > 0) {
+      tma_store_2d(&p.tm_y, sm + OFF_ST + st * kStageBytes + OFF_X, o.col, o.t0);
+      if (o.halves > 1) tma_store_2d(&p.tm_y, sm + OFF_ST + st * kStageBytes + OFF_X + 8192, o.col + 64, o.t0);
+      bulk_commit();
+      bulk_wait_read();
+    }
+    return true;
+  };
   for (uint32_t k = 0;; ++k) {
     Item it{};
     for (;;) {
@@ -370,7 +374,7 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
       if (ch + kAhead < it.nchunks) prefetch(ch + kAhead);
       if (ch < 0) continue;
       const uint32_t st = j % kStages;
-      if (j >= (uint32_t)kStages && !tc_wait(T_EMPTY + st, (j / kStages - 1) & 1)) break;
+      if (j >= (uint32_t)kStages && !leave(j - kStages)) break;
       if (tc_aborted(c)) break;
       uint8_t* base = sm + OFF_ST + st * kStageBytes;
       uint64_t* bar = &c->bar[T_FULL + st];
@@ -385,22 +389,77 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
         if (half == 0 || second)
           tma_load_2d(base + OFF_X + half * 8192, &p.tm_x, bar, it.h0 * p.V + half * 64, t0);
       }
+      const Out o{it.h0 * p.V, t0, it.bos + (int64_t)(ch + 1) * kL > it.eos ? 0 : second ? 2 : 1};
+      if (st == 0) out[0] = o;
+      else if (st == 1) out[1] = o;
+      else out[2] = o;
       ++j;
     }
     if (tc_aborted(c)) break;
   }
-  // every load that was issued has landed before the CTA may leave
+  // the last outputs; every load that was issued has landed, and every store has been made, before
+  // the CTA may leave
+  for (uint32_t i = j > (uint32_t)kStages ? j - kStages : 0; i < j; ++i)
+    if (!leave(i)) break;
+  bulk_wait_all();
   for (uint32_t i = j > (uint32_t)kStages ? j - kStages : 0; i < j; ++i)
     mbar_wait(&c->bar[T_FULL + i % kStages], (i / kStages) & 1);
 }
 
+// Two warps issue the products, each for one loop from chunk to chunk: a thread takes ~100 cycles a
+// product here, the pipe 52 to 71, and a product never waits for one of the other loop's.
+
 // ---- warp 16: the products of the output ------------------------------------------------------
 template <int K>
-__device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
+__device__ void run_output(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
   if ((threadIdx.x & 31) != 0) return;
   const uint32_t sbase = smem_u32(sm);
   const int rep = p.H / p.G;
   const uint32_t id_m = idesc_bf16(128, kL, 1, 0), id_c = idesc_bf16(128, kL, 0, 0);
+  uint32_t j = 0;
+  bool ok = true;
+  for (uint32_t k = 0; ok; ++k) {
+    const int slot = k % kItems;
+    ok = tc_wait(T_ITEM_FULL + slot, (k / kItems) & 1);
+    if (!ok) break;
+    const int nchunks = c->ring[slot].nchunks, done = c->ring[slot].done;
+    const bool second = p.V == 64 && (c->ring[slot].h0 % rep) + 1 < rep;
+    mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
+    if (done) break;
+    for (int ch = 0; ch < nchunks; ++ch, ++j) {
+      const uint32_t st = j % kStages, stage = sbase + OFF_ST + st * kStageBytes;
+      ok = tc_wait(T_M + (j & 1), (j >> 1) & 1) && tc_wait(T_FULL + st, (j / kStages) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t ym = tbase + TM_YM + (j & 1) * 64;
+      // the second half of A: x's, or zeros where it is another head's
+      const uint32_t x0 = stage + OFF_X;
+      issue_ss(ym, desc128(x0, p.V == 128 ? 8192 : sbase + OFF_Z1 - x0, 1024), 2048,
+               desc128(sbase + OFF_M, 16, 1024), 32, id_m, 0);
+      if (second)
+        issue_ss(ym, desc128(sbase + OFF_Z0, x0 + 8192 - (sbase + OFF_Z0), 1024), 2048,
+                 desc128(sbase + OFF_M + 8192, 16, 1024), 32, id_m, 1);
+      mma_commit(&c->bar[T_MX + (j & 1)]);
+      ok = tc_wait(T_S, j & 1);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t kh = 0; kh < K / 64; ++kh)
+        issue_ts(tbase + TM_YI, tbase + TM_SB + kh * 32, desc128(stage + OFF_C + kh * 8192, 16, 1024), 32, id_c,
+                 kh);
+      mma_commit(&c->bar[T_Y]);
+    }
+  }
+  mma_commit(&c->bar[T_DRAIN]);
+  mbar_wait(&c->bar[T_DRAIN], 0);  // the full limit, aborted or not
+}
+
+// ---- warp 19: the state's product, and the scores of the chunk after next ------------------------
+template <int K, int PARTS>
+__device__ void run_state(uint8_t* sm, Ctl* c, uint32_t tbase) {
+  if ((threadIdx.x & 31) != 0) return;
+  const uint32_t sbase = smem_u32(sm);
+  const uint32_t id_c = idesc_bf16(128, kL, 0, 0), id_s = idesc_bf16(128, K, 0, 1);  // A in TMEM: K-major
   // The scores run up to two chunks ahead, within this item and the next: `kg`, `cg`, `jg` are the
   // item, its chunk and the CTA's chunk they come to next (ng: that item's chunks, -1: not read).
   uint32_t j = 0, kg = 0, jg = 0;
@@ -439,7 +498,6 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
     if (!ok) break;
     const int nchunks = c->ring[slot].nchunks, done = c->ring[slot].done;
     if (done) break;
-    const bool second = p.V == 64 && (c->ring[slot].h0 % rep) + 1 < rep;
     if (ng < 0 || kg < k) {  // nothing left to run ahead with before this item
       kg = k;
       cg = 0;
@@ -448,34 +506,23 @@ __device__ void run_issuer(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
     for (int ch = 0; ch < nchunks && ok; ++ch, ++j) {
       const uint32_t st = j % kStages, stage = sbase + OFF_ST + st * kStageBytes;
       scores(k, j + 2);
-      ok = ok && tc_wait(T_M + (j & 1), (j >> 1) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t ym = tbase + TM_YM + (j & 1) * 64;
-      // the second half of A: x's, or zeros where it is another head's
-      const uint32_t x0 = stage + OFF_X;
-      issue_ss(ym, desc128(x0, p.V == 128 ? 8192 : sbase + OFF_Z1 - x0, 1024), 2048,
-               desc128(sbase + OFF_M, 16, 1024), 32, id_m, 0);
-      if (second)
-        issue_ss(ym, desc128(sbase + OFF_Z0, x0 + 8192 - (sbase + OFF_Z0), 1024), 2048,
-                 desc128(sbase + OFF_M + 8192, 16, 1024), 32, id_m, 1);
-      mma_commit(&c->bar[T_MX + (j & 1)]);
-      ok = tc_wait(T_S, j & 1);
+      // (x' is made of a tile that has landed, and b landed with it)
+      ok = ok && tc_wait(T_XP + (j & 1), (j >> 1) & 1) && tc_wait(T_S, j & 1);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
-      for (uint32_t kh = 0; kh < K / 64; ++kh)
-        issue_ts(tbase + TM_YI, tbase + TM_SB + kh * 32, desc128(stage + OFF_C + kh * 8192, 16, 1024), 32, id_c,
-                 kh);
-      mma_commit(&c->bar[T_Y]);
+      for (uint32_t part = 0; part < PARTS; ++part)
+        issue_ts(tbase + TM_S, tbase + TM_XP + part * 32, desc128(stage + OFF_B, 8192, 1024), 2048, id_s, 1);
+      mma_commit(&c->bar[T_SU]);
+      mma_commit(&c->bar[T_EMPTY + st]);
     }
     mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
   }
-  mma_commit(&c->bar[T_DRAIN]);
-  mbar_wait(&c->bar[T_DRAIN], 0);  // the full limit, aborted or not
+  mma_commit(&c->bar[T_DRAIN + 1]);
+  mbar_wait(&c->bar[T_DRAIN + 1], 0);
 }
 
-// ---- warps 0-7: scores, M and x' --------------------------------------------------------------
+// ---- warp 18: steps and decays ------------------------------------------------------------------
 __device__ __noinline__ float step_of(float dt, float bias) {
   return dt == -INFINITY ? 0.f : ssm_step(dt, bias);
 }
@@ -511,40 +558,6 @@ __device__ __forceinline__ void scan_steps(Factors* f, int head, float d0, float
   }
 }
 
-// ---- warp 19: the state's product, the one on the chain from chunk to chunk ---------------------
-template <int K, int PARTS>
-__device__ void run_state(uint8_t* sm, Ctl* c, uint32_t tbase) {
-  if ((threadIdx.x & 31) != 0) return;
-  const uint32_t sbase = smem_u32(sm);
-  const uint32_t id_s = idesc_bf16(128, K, 0, 1);  // an A in TMEM is K-major
-  uint32_t j = 0;
-  bool ok = true;
-  for (uint32_t k = 0; ok; ++k) {
-    const int slot = k % kItems;
-    ok = tc_wait(T_ITEM_FULL + slot, (k / kItems) & 1);
-    if (!ok) break;
-    const int nchunks = c->ring[slot].nchunks, done = c->ring[slot].done;
-    mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
-    if (done) break;
-    for (int ch = 0; ch < nchunks; ++ch, ++j) {
-      const uint32_t st = j % kStages, stage = sbase + OFF_ST + st * kStageBytes;
-      // (x' is made of a tile that has landed, and b landed with it)
-      ok = tc_wait(T_XP + (j & 1), (j >> 1) & 1) && tc_wait(T_FULL + st, (j / kStages) & 1) &&
-           tc_wait(T_S, j & 1);
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (uint32_t part = 0; part < PARTS; ++part)
-        issue_ts(tbase + TM_S, tbase + TM_XP + part * 32, desc128(stage + OFF_B, 8192, 1024), 2048, id_s, 1);
-      mma_commit(&c->bar[T_SU]);
-      mma_commit(&c->bar[T_EMPTY + st]);
-    }
-  }
-  mma_commit(&c->bar[T_DRAIN + 1]);
-  mbar_wait(&c->bar[T_DRAIN + 1], 0);  // the full limit, aborted or not
-}
-
-// ---- warp 18: steps and decays ------------------------------------------------------------------
 __device__ void run_scan(const ScanParams& p, Ctl* c) {
   const int lane = threadIdx.x & 31, rep = p.H / p.G, heads = p.V == 64 ? 2 : 1;
   uint32_t j = 0;
@@ -596,6 +609,7 @@ __device__ void run_scan(const ScanParams& p, Ctl* c) {
   }
 }
 
+// ---- warps 0-7: M and x' ------------------------------------------------------------------------
 // Two values of x' as PARTS bf16 numbers each: truncated parts leave exact remainders.
 template <int PARTS>
 __device__ __forceinline__ void split_x(uint32_t raw, float2 w, uint32_t (&out)[PARTS]) {
@@ -655,7 +669,7 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
     *reinterpret_cast<uint4*>(sm + (i < 512 ? OFF_Z0 + i * 16 : OFF_Z1 + (i - 512) * 16)) = make_uint4(0, 0, 0, 0);
   }
   fence_async_smem();
-  named_bar(BAR_RGRP + 1, kMThreads);
+  named_bar(1, kMThreads);
 
   const bool scores = (warp & 2) == 0;    // warps 0, 1, 4, 5
   const int rh = warp & 1;                // half of the rows (TMEM lanes 32 rh, + 32)
@@ -765,8 +779,8 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
   const uint32_t col0 = ((quad & 1) * 4 + ((lane >> 3) & 1)) ^ (lane & 7);
   uint32_t j = 0;
   for (uint32_t k = 0;; ++k) {
-    const Item it = tc_item(p, c, k, BAR_RGRP, kRThreads, rt == 0);
-    if (it.done) break;
+    const Item it = tc_item_warp(p, c, k);
+    if (it.done) return;
     const bool second = p.V == 128 || (it.h0 % rep) + 1 < rep;
     const bool real = half == 0 || second;
     const int h = it.h0 + hd;
@@ -796,6 +810,7 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       const uint32_t st = j % kStages, par = j & 1, fi = j % kFacs;
       const int64_t t0 = it.bos + (int64_t)ch * kL;
       const int m = it.eos - t0 < kL ? (int)(it.eos - t0) : kL;
+      if (__any_sync(0xffffffffu, tc_aborted(c))) return;
       // S before the chunk: its bf16 copy for the product with C, and its decay over the chunk
       tc_wait(T_FAC + fi, (j / kFacs) & 1);
       const float dec = c->fac[fi].dec[hd];
@@ -818,12 +833,6 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&c->bar[T_S]);
-      // every warp is done with the chunk before; its stage is free once its output has left it
-      if (named_bar_any(BAR_RGRP, kRThreads, tc_aborted(c))) goto leave;
-      if (rt == 0 && j > 0) {
-        bulk_wait_read();
-        mbar_arrive(&c->bar[T_EMPTY + (j - 1) % kStages]);
-      }
       // the output of tokens [32 hf, + 32), which takes the place of x in its tile
       {
         tc_wait(T_XP + par, (j >> 1) & 1);  // the M group has seen x land and has read it
@@ -861,30 +870,24 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
           mbar_arrive(&c->bar[T_EPI + par]);
           mbar_arrive(&c->bar[T_FAC_FREE + fi]);
         }
-        fence_async_smem();
-        named_bar(BAR_RGRP, kRThreads);
-        if (m == kL) {
-          if (rt == 0 && KDA_CHECK(t0 + kL <= p.T)) {
-            tma_store_2d(&p.tm_y, stage + OFF_X, it.h0 * p.V, (int)t0);
-            if (second) tma_store_2d(&p.tm_y, stage + OFF_X + 8192, it.h0 * p.V + 64, (int)t0);
-            bulk_commit();
-          }
-        } else {
-          // the box of a partial chunk would cover the next sequence's rows: 16 bytes a thread of its own
+        if (m < kL && real) {
+          // a partial chunk's box would cover the next sequence's rows: the warp's own, 16 bytes a lane
 #pragma unroll 1
-          for (int i = rt; i < m * 16; i += kRThreads) {
-            const int row = i >> 4, hh = (i >> 3) & 1, cell = i & 7;
-            if ((hh == 0 || second) && KDA_CHECK(t0 + row < p.T))
-              *reinterpret_cast<uint4*>(p.y + ((t0 + row) * p.H + it.h0) * p.V + hh * 64 + cell * 8) =
-                  *reinterpret_cast<const uint4*>(stage + OFF_X + hh * 8192 + sw128_off(row, cell));
+          for (int i = lane >> 2; i < 32; i += 8) {
+            const int row = hf * 32 + i, cell = (quad & 1) * 4 + (lane & 3);
+            if (row < m && KDA_CHECK(t0 + row < p.T))
+              *reinterpret_cast<uint4*>(p.y + ((t0 + row) * p.H + it.h0) * p.V + half * 64 + cell * 8) =
+                  *reinterpret_cast<const uint4*>(stage + OFF_X + half * 8192 + sw128_off(row, cell));
           }
         }
+        fence_async_smem();
+        warp_arrive(&c->bar[T_EMPTY + st]);  // a full chunk's tile is stored by the loader
       }
     }
     // the state after the sequence
     tc_wait(T_SU, (j - 1) & 1);
     tc_fence_after();
-    if (named_bar_any(BAR_RGRP, kRThreads, tc_aborted(c))) break;
+    if (__any_sync(0xffffffffu, tc_aborted(c))) return;
     {
 #pragma unroll 1
       for (int i0 = 0; i0 < KH; i0 += 16) {
@@ -900,8 +903,6 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       tc_fence_before();
     }
   }
-leave:
-  if (rt == 0) bulk_wait_all();
 }
 
 template <typename ST, int K>
@@ -917,10 +918,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid
   if (threadIdx.x == 0) {
     for (int b = 0; b < T_COUNT; ++b) {
       uint32_t count = 1;  // a loader's, a scan's or a commit's arrival
-      if (b >= T_EMPTY && b < T_EMPTY + kStages) count = 2;        // a commit's and the R group's
+      if (b >= T_EMPTY && b < T_EMPTY + kStages) count = 9;        // a commit's, one an R warp
       if (b >= T_FAC_FREE && b < T_FAC_FREE + kFacs) count = 16;   // one a warp of both groups
       if (b >= T_M && b <= T_S) count = 8;                         // one a warp of a group
-      if (b >= T_ITEM_EMPTY && b < T_ITEM_EMPTY + kItems) count = 12;  // M warps, R, issuers, scan
+      if (b >= T_ITEM_EMPTY && b < T_ITEM_EMPTY + kItems) count = 19;  // M and R warps, issuers, scan
       mbar_init(&c->bar[b], count);
     }
     c->abort = 0;
@@ -940,7 +941,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid
   const uint32_t tbase = c->tmem_base;
   if (warp < 8) run_mgroup<K, PARTS>(p, sm, c, tbase);
   else if (warp < 16) run_rgroup<ST, K>(p, sm, c, tbase);
-  else if (warp == 16) run_issuer<K>(p, sm, c, tbase);
+  else if (warp == 16) run_output<K>(p, sm, c, tbase);
   else if (warp == 17) run_loader<K>(p, sm, c);
   else if (warp == 18) run_scan(p, c);
   else run_state<K, PARTS>(sm, c, tbase);
