@@ -292,7 +292,7 @@ __device__ __forceinline__ Item tc_item_warp(const ScanParams& p, Ctl* c, uint32
 // ---- warp 17: items and tiles ------------------------------------------------------------
 template <int K>
 __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
-  if ((threadIdx.x & 31) != 0) return;
+  if (!elect_one()) return;
   const uint32_t total = (uint32_t)p.N * (uint32_t)p.pairs;
   const int rep = p.H / p.G;                       // heads a group
   const int per = p.V == 64 ? (rep + 1) / 2 : rep; // items a group
@@ -412,7 +412,7 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
 // ---- warp 16: the products of the output ------------------------------------------------------
 template <int K>
 __device__ void run_output(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
-  if ((threadIdx.x & 31) != 0) return;
+  if (!elect_one()) return;
   const uint32_t sbase = smem_u32(sm);
   const int rep = p.H / p.G;
   const uint32_t id_m = idesc_bf16(128, kL, 1, 0), id_c = idesc_bf16(128, kL, 0, 0);
@@ -457,7 +457,7 @@ __device__ void run_output(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
 // ---- warp 19: the state's product, and the scores of the chunk after next ------------------------
 template <int K, int PARTS>
 __device__ void run_state(uint8_t* sm, Ctl* c, uint32_t tbase) {
-  if ((threadIdx.x & 31) != 0) return;
+  if (!elect_one()) return;
   const uint32_t sbase = smem_u32(sm);
   const uint32_t id_c = idesc_bf16(128, kL, 0, 0), id_s = idesc_bf16(128, K, 0, 1);  // A in TMEM: K-major
   // The scores run up to two chunks ahead, within this item and the next: `kg`, `cg`, `jg` are the

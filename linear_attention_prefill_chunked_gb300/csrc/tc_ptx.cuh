@@ -108,6 +108,15 @@ __device__ __forceinline__ bool named_bar_any(uint32_t id, uint32_t nthreads, bo
   return r != 0;
 }
 
+// True in one lane of a converged warp. What only that lane runs after it compiles to about half the
+// instructions a tcgen05.mma than after a test of the lane's number: the operands' moves to uniform
+// registers need no loop over the lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+
 // ---- programmatic dependent launch ------------------------------------------------
 // The next kernel on the stream (launched with programmatic stream serialisation) may be
 // scheduled from now on; it still waits for this grid in grid_dep_wait before reading
