@@ -16,7 +16,7 @@
 // head. Transposed accumulators (lanes = value columns) put both heads into one M = 128 product
 // with the group's B and C as the shared other operand:
 //
-//   G [64 t][s]    = C B^T      A = c tile, B = b tile                                   N = 64
+//   G [64 t][s]    = C B^T      A = c tile, B = b tile (M = 64: rows 16 q .. on lanes 32 q ..)  N = 64
 //   YM [128][t]    = X^T M^T    A = x tile, B = M tile (two 64-wide heads: one product a head,
 //                               the other head's rows of A being zeros)                  N = 64
 //   YI [128][t]    = S^T C^T    A = S^T as bf16 (TMEM), B = c tile                       N = 64
@@ -32,8 +32,7 @@
 // and x and y read and written by TMEM lane, two bytes at a time, 3350 wavefronts a chunk): x' goes
 // from registers to TMEM, and x and y move as 8 x 8 blocks transposed on the way (ldmatrix, stmatrix).
 //
-// Warps 0-7 (M group): x', and warps 0, 1, 4, 5, whose TMEM lanes hold the 64 rows of the scores, M.
-// Warps 8-15 (R group): the state's decay and bf16 copy, the output. Warps 16 and 19 issue the
+// Warps 0-7 (M group): M from the scores, and x'. Warps 8-15 (R group): the state's decay and bf16 copy, the output. Warps 16 and 19 issue the
 // tcgen05 products, warp 17 claims items and moves tiles (TMA), warp 18 scans the steps. What orders them are
 // mbarriers, each wait bounded (a timeout sets KDA_DEVICE_PIPE_TIMEOUT, stops the loads, lets what was
 // issued finish and returns). Only T_SU -> R -> T_S -> products of C and x' -> T_SU is a chain from
@@ -96,10 +95,26 @@ enum TcBar {
 };
 
 struct Item {
-  int32_t n, h0, nchunks, done;
-  int64_t bos, eos;
-  int64_t src, dst;   // element offsets of head h0's state, -1: zero state / not written
+  int32_t h0, nchunks, done;
+  int32_t part;       // -1: a whole sequence; else the part's slot of the split scratch
+  int32_t first, last;  // of the sequence's parts (1, 1 for a whole one)
+  int64_t bos, eos;   // its tokens
+  int64_t state;      // element offset of head h0's state in the initial and final states
 };
+
+// Work-list entry, for every item of a sequence (or part) alike. Long sequences are cut in time where
+// few items would leave SMs idle (see the planning kernel).
+struct Entry {
+  int32_t n, chunk0, nchunks, part;  // part: as in Item
+  int32_t first, last, pad[2];
+};
+struct Split {  // a cut sequence: its parts' slots
+  int32_t part0, parts;
+};
+struct PlanHdr {  // over the workspace header
+  uint32_t status, next_state, next_full, n_state, n_full, n_splits;
+};
+static_assert(sizeof(PlanHdr) <= sizeof(WsHeader), "the plan's header lies in the workspace header");
 
 // Steps and decays of a chunk, by [head of the item][token], logarithms to base 2; a half is 32 tokens.
 struct Factors {
@@ -136,6 +151,10 @@ struct ScanParams {
   __nv_bfloat16* y;
   uint32_t* status;
   uint32_t* next_item;
+  const Entry* list;           // null: sequences in order
+  const uint32_t* entries;     // of the list
+  float* scratch;              // [part][H][K][V]: the state before each part of a cut sequence
+  float* decay;                // [part][H]: a part's decay
   uint64_t wait_limit_ns;
   int32_t N, H, G, V, pairs;   // pairs: items a sequence
   int64_t T, num_slots, slot_stride;
@@ -147,18 +166,20 @@ __device__ __forceinline__ bool tc_aborted(const Ctl* c) {
 extern __shared__ __align__(1024) uint8_t ssm_smem[];
 __device__ __forceinline__ Ctl* ctl() { return reinterpret_cast<Ctl*>(ssm_smem + OFF_CTL); }
 
-// Bounded wait; after a timeout anywhere in the CTA every wait returns at once (false). The hardware
+// Bounded wait; after a timeout anywhere in the CTA every wait gives up soon (false). The hardware
 // suspends the thread in try_wait until the phase completes or some microseconds have passed, so that
 // a waiting warp takes few issue slots; a limit shorter than that polls instead. Out of line, as is
 // what else the chunk loop runs at several places: the warps of a CTA run five programs at once, and
 // their instruction cache is what they are short of (see the launch).
 __device__ __noinline__ bool tc_wait_slow(uint64_t* bar, uint32_t parity) {
   Ctl* c = ctl();
-  const uint64_t t0 = globaltimer_ns();
+  uint64_t t0 = 0;
   for (;;) {
     if (c->poll ? mbar_test_wait(bar, parity) : mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
     if (tc_aborted(c)) return false;
-    if (globaltimer_ns() - t0 > c->wait_limit_ns) {
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > c->wait_limit_ns) {
       if (atomicExch(&c->abort, 1u) == 0u) raise_status(c->status, KDA_DEVICE_PIPE_TIMEOUT);
       return false;
     }
@@ -169,6 +190,28 @@ __device__ __forceinline__ bool tc_wait(int b, uint32_t parity) {
   if (mbar_test_wait(bar, parity)) return true;
   return tc_wait_slow(bar, parity);
 }
+// Several at once: what is usually complete already costs one test each and one branch. (None of this
+// may need a stack: with 200 KB of shared memory taken, local memory is an L2 trip away.)
+struct At {
+  int b;
+  uint32_t parity;
+};
+__device__ __forceinline__ bool tc_wait2(At x, At y) {
+  uint64_t* bar = ctl()->bar;
+  const bool a = mbar_test_wait(bar + x.b, x.parity), b = mbar_test_wait(bar + y.b, y.parity);
+  if ((int)a & (int)b) return true;
+  return tc_wait_slow(bar + x.b, x.parity) && tc_wait_slow(bar + y.b, y.parity);
+}
+__device__ __forceinline__ bool tc_wait3(At x, At y, At z) {
+  uint64_t* bar = ctl()->bar;
+  const bool a = mbar_test_wait(bar + x.b, x.parity), b = mbar_test_wait(bar + y.b, y.parity);
+  const bool d = mbar_test_wait(bar + z.b, z.parity);
+  if ((int)a & (int)b & (int)d) return true;
+  return tc_wait_slow(bar + x.b, x.parity) && tc_wait_slow(bar + y.b, y.parity) &&
+         tc_wait_slow(bar + z.b, z.parity);
+}
+// The lanes' common result: after a timeout the warp leaves as one.
+__device__ __forceinline__ bool all_lanes(bool ok) { return __all_sync(0xffffffffu, ok) != 0; }
 // One arrival a warp, after what its lanes wrote.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
@@ -249,6 +292,11 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t saddr) 
                : "r"(saddr)
                : "memory");
 }
+__device__ __forceinline__ void stsm_x4(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(saddr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
 __device__ __forceinline__ void stsm_x4_trans(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(saddr), "r"(a),
                "r"(b), "r"(c), "r"(d)
@@ -269,6 +317,14 @@ __device__ __forceinline__ void tmem_ld_16x256_x4(uint32_t taddr, float (&v)[16]
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_ld_16x256_x2(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_st_16x128_x4(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
@@ -281,7 +337,7 @@ __device__ __forceinline__ Item tc_item_warp(const ScanParams& p, Ctl* c, uint32
   const int slot = k % kItems;
   const bool ok = tc_wait(T_ITEM_FULL + slot, (k / kItems) & 1);
   Item it = c->ring[slot];
-  const bool stop = __any_sync(0xffffffffu, !ok || it.done != 0 || tc_aborted(c));
+  const bool stop = !all_lanes(ok && it.done == 0);
   __syncwarp();
   if (ok && (threadIdx.x & 31) == 0) mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
   it.done = stop ? 1 : 0;
@@ -290,10 +346,10 @@ __device__ __forceinline__ Item tc_item_warp(const ScanParams& p, Ctl* c, uint32
 
 
 // ---- warp 17: items and tiles ------------------------------------------------------------
-template <int K>
+template <int K, bool kState>
 __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
   if (!elect_one()) return;
-  const uint32_t total = (uint32_t)p.N * (uint32_t)p.pairs;
+  const uint32_t total = (p.list ? *p.entries : (uint32_t)p.N) * (uint32_t)p.pairs;
   const int rep = p.H / p.G;                       // heads a group
   const int per = p.V == 64 ? (rep + 1) / 2 : rep; // items a group
   uint32_t j = 0;                                  // chunks loaded by this CTA
@@ -322,29 +378,32 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
         it.done = 1;
         break;
       }
-      const int n = (int)(w / (uint32_t)p.pairs), q = (int)(w % (uint32_t)p.pairs);
+      const int e = (int)(w / (uint32_t)p.pairs), q = (int)(w % (uint32_t)p.pairs);
+      Entry en{e, 0, 0, -1, 1, 1, {0, 0}};
+      if (p.list) en = p.list[e];
       int64_t bos, eos;
-      if (!seq_bounds(p.cu, n, p.T, &bos, &eos)) {
+      if (!seq_bounds(p.cu, en.n, p.T, &bos, &eos)) {
         raise_status(p.status, KDA_DEVICE_BAD_SEQLENS);
         continue;
       }
-      int64_t slot = n;
+      int64_t slot = en.n;
       if (p.idx) {
-        slot = resolve_slot(p.idx, n, p.num_slots);
+        slot = resolve_slot(p.idx, en.n, p.num_slots);
         if (slot < 0) {
           raise_status(p.status, KDA_DEVICE_BAD_SLOT);
           continue;
         }
       }
       const int g = q / per, i = q % per;
-      it.n = n;
       it.h0 = g * rep + (p.V == 64 ? 2 * i : i);
-      it.bos = bos;
-      it.eos = eos;
-      it.nchunks = (int)((eos - bos + kL - 1) / kL);
-      const int64_t at = slot * p.slot_stride + (int64_t)it.h0 * K * p.V;
-      it.src = p.state_in ? at : -1;
-      it.dst = p.state_out ? at : -1;
+      it.bos = bos + (int64_t)en.chunk0 * kL;
+      const int64_t end = it.bos + (int64_t)en.nchunks * kL;
+      it.eos = p.list && end < eos ? end : eos;
+      it.nchunks = (int)((it.eos - it.bos + kL - 1) / kL);
+      it.part = en.part;
+      it.first = en.first;
+      it.last = en.last;
+      it.state = slot * p.slot_stride + (int64_t)it.h0 * K * p.V;
       break;
     }
     const int slot = k % kItems;
@@ -354,7 +413,7 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
     if (it.done) break;
     const int g = it.h0 / rep;
     const bool second = p.V == 128 || (it.h0 % rep) + 1 < rep;
-    const uint32_t bytes = 2u * (K / 64) * 8192u + (second ? 16384u : 8192u);
+    const uint32_t bytes = (kState ? 1u : 2u) * (K / 64) * 8192u + (second ? 16384u : 8192u);
     // a stage comes free little more than a chunk before its tiles are wanted, less than a load from
     // HBM takes: the tiles are brought into L2 kAhead chunks before
     constexpr int kAhead = 3;
@@ -363,7 +422,7 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         if (half < K / 64) {
-          tma_prefetch_2d(&p.tm_c, g * K + half * 64, t0);
+          if (!kState) tma_prefetch_2d(&p.tm_c, g * K + half * 64, t0);
           tma_prefetch_2d(&p.tm_b, g * K + half * 64, t0);
         }
         if (half == 0 || second) tma_prefetch_2d(&p.tm_x, it.h0 * p.V + half * 64, t0);
@@ -383,13 +442,13 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         if (half < K / 64) {
-          tma_load_2d(base + OFF_C + half * 8192, &p.tm_c, bar, g * K + half * 64, t0);
+          if (!kState) tma_load_2d(base + OFF_C + half * 8192, &p.tm_c, bar, g * K + half * 64, t0);
           tma_load_2d(base + OFF_B + half * 8192, &p.tm_b, bar, g * K + half * 64, t0);
         }
         if (half == 0 || second)
           tma_load_2d(base + OFF_X + half * 8192, &p.tm_x, bar, it.h0 * p.V + half * 64, t0);
       }
-      const Out o{it.h0 * p.V, t0, it.bos + (int64_t)(ch + 1) * kL > it.eos ? 0 : second ? 2 : 1};
+      const Out o{it.h0 * p.V, t0, kState || it.bos + (int64_t)(ch + 1) * kL > it.eos ? 0 : second ? 2 : 1};
       if (st == 0) out[0] = o;
       else if (st == 1) out[1] = o;
       else out[2] = o;
@@ -428,7 +487,7 @@ __device__ void run_output(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
     if (done) break;
     for (int ch = 0; ch < nchunks; ++ch, ++j) {
       const uint32_t st = j % kStages, stage = sbase + OFF_ST + st * kStageBytes;
-      ok = tc_wait(T_M + (j & 1), (j >> 1) & 1) && tc_wait(T_FULL + st, (j / kStages) & 1);
+      ok = tc_wait2({T_M + (int)(j & 1), (j >> 1) & 1}, {T_FULL + (int)st, (j / kStages) & 1});
       if (!ok) break;
       tc_fence_after();
       const uint32_t ym = tbase + TM_YM + (j & 1) * 64;
@@ -455,11 +514,11 @@ __device__ void run_output(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
 }
 
 // ---- warp 19: the state's product, and the scores of the chunk after next ------------------------
-template <int K, int PARTS>
+template <int K, int PARTS, bool kState>
 __device__ void run_state(uint8_t* sm, Ctl* c, uint32_t tbase) {
   if (!elect_one()) return;
   const uint32_t sbase = smem_u32(sm);
-  const uint32_t id_c = idesc_bf16(128, kL, 0, 0), id_s = idesc_bf16(128, K, 0, 1);  // A in TMEM: K-major
+  const uint32_t id_g = idesc_bf16(64, kL, 0, 0), id_s = idesc_bf16(128, K, 0, 1);  // A in TMEM: K-major
   // The scores run up to two chunks ahead, within this item and the next: `kg`, `cg`, `jg` are the
   // item, its chunk and the CTA's chunk they come to next (ng: that item's chunks, -1: not read).
   uint32_t j = 0, kg = 0, jg = 0;
@@ -478,15 +537,15 @@ __device__ void run_state(uint8_t* sm, Ctl* c, uint32_t tbase) {
         continue;
       }
       const uint32_t st = jg % kStages, stage = sbase + OFF_ST + st * kStageBytes;
-      ok = tc_wait(T_FULL + st, (jg / kStages) & 1) &&
-           (jg < 2 || tc_wait(T_EPI + (jg & 1), ((jg >> 1) - 1) & 1));
+      const At full{T_FULL + (int)st, (jg / kStages) & 1};
+      ok = jg < 2 ? tc_wait(full.b, full.parity)
+                  : tc_wait2(full, {T_EPI + (int)(jg & 1), ((jg >> 1) - 1) & 1});
       if (!ok) return;
       tc_fence_after();
-      // rows 64-127 of A are the tile after c's: lanes that nothing reads
 #pragma unroll
       for (uint32_t kh = 0; kh < K / 64; ++kh)
         issue_ss(tbase + TM_YM + (jg & 1) * 64, desc128(stage + OFF_C + kh * 8192, 16, 1024), 32,
-                 desc128(stage + OFF_B + kh * 8192, 16, 1024), 32, id_c, kh);
+                 desc128(stage + OFF_B + kh * 8192, 16, 1024), 32, id_g, kh);
       mma_commit(&c->bar[T_G + (jg & 1)]);
       ++cg;
       ++jg;
@@ -505,9 +564,10 @@ __device__ void run_state(uint8_t* sm, Ctl* c, uint32_t tbase) {
     }
     for (int ch = 0; ch < nchunks && ok; ++ch, ++j) {
       const uint32_t st = j % kStages, stage = sbase + OFF_ST + st * kStageBytes;
-      scores(k, j + 2);
-      // (x' is made of a tile that has landed, and b landed with it)
-      ok = ok && tc_wait(T_XP + (j & 1), (j >> 1) & 1) && tc_wait(T_S, j & 1);
+      if (!kState) scores(k, j + 2);
+      // (b's tile: seen to land for the scores, where there are any)
+      if (kState) ok = tc_wait(T_FULL + st, (j / kStages) & 1);
+      ok = ok && tc_wait2({T_XP + (int)(j & 1), (j >> 1) & 1}, {T_S, j & 1});
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
@@ -586,7 +646,6 @@ __device__ void run_scan(const ScanParams& p, Ctl* c) {
     };
 #pragma unroll 1
     for (int ch = -1; ch < it.nchunks; ++ch) {
-      if (__any_sync(0xffffffffu, tc_aborted(c))) return;
       float d[2][2];
       if (ch >= 0) {
 #pragma unroll
@@ -598,7 +657,7 @@ __device__ void run_scan(const ScanParams& p, Ctl* c) {
       read(ch + 1);
       if (ch < 0) continue;
       const uint32_t fi = j % kFacs;
-      if (j >= (uint32_t)kFacs) tc_wait(T_FAC_FREE + fi, (j / kFacs - 1) & 1);
+      if (j >= (uint32_t)kFacs && !all_lanes(tc_wait(T_FAC_FREE + fi, (j / kFacs - 1) & 1))) return;
 #pragma unroll 1
       for (int hd = 0; hd < heads; ++hd)
         scan_steps(&c->fac[fi], hd, hd ? d[1][0] : d[0][0], hd ? d[1][1] : d[0][1],
@@ -628,38 +687,35 @@ __device__ __forceinline__ void split_x(uint32_t raw, float2 w, uint32_t (&out)[
   }
 }
 
-// 32 columns of one head's M for the 32 rows of this warp: the scores times the weights of the
-// columns. diag: the columns' half is the rows' half.
-__device__ __noinline__ void weigh_scores(const Factors* f, uint8_t* m_row, uint32_t tmem, int hd, int half,
-                                          bool diag, float cl) {
-  const int lane = threadIdx.x & 31;
-  const float* src = (diag ? f->same[hd] : f->later[hd]) + half * 32;
-  const int last = diag ? lane : 31;  // a later token's weight may be anything
-#pragma unroll 1
-  for (int i0 = 0; i0 < 32; i0 += 16) {
-    float g[16], w[16];
-    tmem_ld16(tmem + half * 32 + i0, g);
+// A 16 x 16 block of M, 8 elements a lane: the scores times their weights, rounded into the M tile at
+// `at` (the lane's row of the four 8 x 8 blocks). `col`: the lane's columns' part of the log-weights;
+// diag: columns after the row are not weighted (their weight may be anything) but zero.
+__device__ __forceinline__ void weigh_block(uint32_t tmem, const float* col, float cl0, float cl1, bool diag,
+                                            uint32_t at, int lane) {
+  float g[8];
+  tmem_ld_16x256_x2(tmem, g);
+  uint32_t o[4];
+  float w[8];
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(src + i0 + i);
-      w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = ex2(cl + w[i]);
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) g[i] = i <= last - i0 ? g[i] * w[i] : 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; i += 8) {
-      const uint32_t chunk = half * 4 + (i0 + i) / 8;
-      *reinterpret_cast<uint4*>(m_row + (((chunk ^ lane) & 7u) << 4)) =
-          make_uint4(pack_bf16x2(g[i], g[i + 1]), pack_bf16x2(g[i + 2], g[i + 3]),
-                     pack_bf16x2(g[i + 4], g[i + 5]), pack_bf16x2(g[i + 6], g[i + 7]));
-    }
+  for (int c = 0; c < 2; ++c) {
+    const float2 q = *reinterpret_cast<const float2*>(col + c * 8);
+    w[4 * c] = ex2(cl0 + q.x);
+    w[4 * c + 1] = ex2(cl0 + q.y);
+    w[4 * c + 2] = ex2(cl1 + q.x);
+    w[4 * c + 3] = ex2(cl1 + q.y);
   }
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {  // column 8 (i / 4) + 2 (lane % 4) + i % 2, row lane / 4 + 8 (i / 2 % 2)
+    const int over = (i >> 2) * 8 + 2 * (lane & 3) + (i & 1) - ((lane >> 2) + ((i >> 1) & 1) * 8);
+    g[i] = diag && over > 0 ? 0.f : g[i] * w[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(g[2 * i], g[2 * i + 1]);
+  stsm_x4(at, o[0], o[1], o[2], o[3]);
 }
 
-template <int K, int PARTS>
+template <int K, int PARTS, bool kState>
 __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = p.V == 64 ? 2 : 1;
@@ -671,11 +727,13 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
   fence_async_smem();
   named_bar(1, kMThreads);
 
-  const bool scores = (warp & 2) == 0;    // warps 0, 1, 4, 5
-  const int rh = warp & 1;                // half of the rows (TMEM lanes 32 rh, + 32)
   // x' of 32 value columns (TMEM lanes of the warp's quadrant) and 32 tokens: where the lane's row of
   // the 8 x 8 blocks lies in the x tile, for tokens 0-15 and columns 0-15 of those
+  // and M's rows [16 quad, + 16): one head a warp, or every other column block of the one head
   const int quad = warp & 3, th = warp >> 2;
+  const int hm = heads == 2 ? th : 0, sb0 = heads == 2 ? 0 : th, sbn = heads == 2 ? 1 : 2;
+  const uint32_t mrow = quad * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+  const uint32_t m0 = smem_u32(sm) + OFF_M + hm * 8192 + mrow * 128;
   const uint32_t row0 = th * 4096 + ((lane >> 4) << 10) + (lane & 7) * 128;
   const uint32_t col0 = ((quad & 1) * 4 + ((lane >> 3) & 1)) ^ (lane & 7);  // 16-byte cell
   const uint32_t xoff = OFF_X + (quad >> 1) * 8192 + row0;
@@ -689,9 +747,13 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       const uint32_t st = j % kStages, par = j & 1, fi = j % kFacs;
       uint8_t* stage = sm + OFF_ST + st * kStageBytes;
       const Factors* f = &c->fac[fi];
-      if (__any_sync(0xffffffffu, tc_aborted(c))) return;
-      tc_wait(T_FAC + fi, (j / kFacs) & 1);
-      tc_wait(T_FULL + st, (j / kStages) & 1);
+      // (the scores: their tiles have landed. j > 0: the product that read the last M is done.)
+      const At g = kState ? At{T_FAC + (int)fi, (j / kFacs) & 1} : At{T_G + (int)par, (j >> 1) & 1};
+      if (!all_lanes(tc_wait3({T_FAC + (int)fi, (j / kFacs) & 1}, g,
+                              j > 0 && !kState ? At{T_MX + (int)(par ^ 1), ((j - 1) >> 1) & 1} : g) &&
+                     tc_wait(T_FULL + st, (j / kStages) & 1)))
+        return;
+      tc_fence_after();
       // the rows after the sequence's last token are another's (or nobody's): they must not reach a
       // product, where a zero weight would not hide an infinity. Each warp clears its 32 rows and 4
       // cells of x and b.
@@ -706,21 +768,17 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         }
         __syncwarp();
       }
-      if (scores) {
-        tc_wait(T_G + par, (j >> 1) & 1);
-        if (j > 0) tc_wait(T_MX + (par ^ 1), ((j - 1) >> 1) & 1);  // the product that read the last M is done
-        tc_fence_after();
-        const uint32_t tg = tbase + TM_YM + par * 64 + ((uint32_t)(rh * 32) << 16);
-        // pieces of 32 x 32: heads on warps 0, 1 and 4, 5; one head's second row half is shared
-        const int hd = heads == 2 ? warp >> 2 : 0;
-        const float cl = f->cl[hd][rh * 32 + lane];
-        uint8_t* m_row = sm + OFF_M + hd * 8192 + rh * 4096 + (lane >> 3) * 1024 + (lane & 7) * 128;
-        if (rh == 1 && (heads == 2 || warp == 1)) weigh_scores(f, m_row, tg, hd, 0, false, cl);
-        if (heads == 2 || warp == 0 || warp == 5) weigh_scores(f, m_row, tg, hd, rh, true, cl);
+      if (!kState) {
+        const float cl0 = f->cl[hm][quad * 16 + (lane >> 2)], cl1 = f->cl[hm][quad * 16 + (lane >> 2) + 8];
+        const uint32_t tg = tbase + TM_YM + par * 64 + ((uint32_t)(quad * 32) << 16);
+#pragma unroll 1
+        for (int sb = sb0; sb <= quad; sb += sbn)
+          weigh_block(tg + sb * 16, (sb >> 1 == quad >> 1 ? f->same[hm] : f->later[hm]) + sb * 16 + 2 * (lane & 3),
+                      cl0, cl1, sb == quad, m0 + (((sb * 2 + (lane >> 4)) ^ (lane & 7)) << 4), lane);
         tc_fence_before();
       }
       fence_async_smem();
-      warp_arrive(&c->bar[T_M + par]);
+      if (!kState) warp_arrive(&c->bar[T_M + par]);
       // x' into registers, and to TMEM once the product that read the last one is done
       float2 w[4];
 #pragma unroll
@@ -729,31 +787,31 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         const float then = th == 0 ? f->second[hx] : 0.f;
         w[i] = make_float2(ex2(q.x + then), ex2(q.y + then));
       }
-      uint32_t parts[PARTS][2][8];
+      uint32_t raw[4][4], parts[PARTS][8];
 #pragma unroll
-      for (int lh = 0; lh < 2; ++lh) {
+      for (int i = 0; i < 4; ++i)  // columns 16 (i / 2), tokens 16 (i % 2)
+        ldsm_x4_trans(raw[i], smem_u32(stage) + xoff + (i & 1) * 2048 + ((col0 ^ (i & 2)) << 4));
+      auto split = [&](int lh) {
 #pragma unroll
-        for (int t2 = 0; t2 < 2; ++t2) {
-          uint32_t raw[4];
-          ldsm_x4_trans(raw, smem_u32(stage) + xoff + t2 * 2048 + ((col0 ^ (lh * 2)) << 4));
+        for (int i = 0; i < 8; ++i) {
+          uint32_t o[PARTS];
+          split_x<PARTS>(raw[lh * 2 + (i >> 2)][i & 3], w[i >> 1], o);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o[PARTS];
-            split_x<PARTS>(raw[i], w[t2 * 2 + (i >> 1)], o);
-#pragma unroll
-            for (int q = 0; q < PARTS; ++q) parts[q][lh][t2 * 4 + i] = o[q];
-          }
+          for (int q = 0; q < PARTS; ++q) parts[q][i] = o[q];
         }
-      }
+      };
+      auto put = [&](int lh) {
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q)
+          tmem_st_16x128_x4(txp + q * 32 + ((uint32_t)(lh * 16) << 16), parts[q]);
+      };
+      split(0);
       warp_arrive(&c->bar[T_FAC_FREE + fi]);
-      if (j > 0) tc_wait(T_SU, (j - 1) & 1);
+      if (j > 0 && !all_lanes(tc_wait(T_SU, (j - 1) & 1))) return;
       tc_fence_after();
-#pragma unroll
-      for (int q = 0; q < PARTS; ++q) {
-#pragma unroll
-        for (int lh = 0; lh < 2; ++lh)
-          tmem_st_16x128_x4(txp + q * 32 + ((uint32_t)(lh * 16) << 16), parts[q][lh]);
-      }
+      put(0);
+      split(1);
+      put(1);
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&c->bar[T_XP + par]);
@@ -763,7 +821,7 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
 
 // ---- warps 8-15: the state and the output ------------------------------------------------------
 // Two warps a TMEM lane quadrant: each takes half of S^T's k columns and half of the tokens.
-template <typename ST, int K>
+template <typename ST, int K, bool kState>
 __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
   constexpr int KH = K / 2;                      // k columns a thread
   const int rt = threadIdx.x - kMThreads, warp = rt >> 5, lane = rt & 31;
@@ -786,8 +844,17 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
     const int h = it.h0 + hd;
     const float dskip = p.d && real ? p.d[h] : 0.f;
     const int64_t so = (int64_t)hd * K * p.V + vh + (int64_t)hf * KH * p.V;  // within the item's state
-    const ST* src = it.src >= 0 && real ? static_cast<const ST*>(p.state_in) + it.src + so : nullptr;
-    ST* dst = it.dst >= 0 && real ? static_cast<ST*>(p.state_out) + it.dst + so : nullptr;
+    // A whole sequence's state comes from and goes to the caller's states. A part's comes from its
+    // slot of the scratch, written by the pass that takes the states only: the initial state into the
+    // first part's slot (in pool mode the last part overwrites the caller's), a part's end (for all but
+    // the first from a zero state) into the next one's, completed by the combining kernel.
+    const int64_t whole = (int64_t)p.H * K * p.V, head = (int64_t)it.h0 * K * p.V + so;
+    const ST* src = p.state_in && real && (it.part < 0 || (kState && it.first))
+                        ? static_cast<const ST*>(p.state_in) + it.state + so : nullptr;
+    const float* fsrc = !kState && real && it.part >= 0 ? p.scratch + it.part * whole + head : nullptr;
+    ST* dst = !kState && p.state_out && real && it.last ? static_cast<ST*>(p.state_out) + it.state + so : nullptr;
+    float* fdst = kState && real ? p.scratch + (it.part + 1) * whole + head : nullptr;
+    float* keep = kState && real && it.first ? p.scratch + it.part * whole + head : nullptr;
     if (it.nchunks == 0) {  // an empty sequence keeps its state
       if (dst && (const void*)dst != (const void*)src)
 #pragma unroll 1
@@ -795,27 +862,30 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
           dst[(int64_t)i * p.V] = src ? src[(int64_t)i * p.V] : from_f32<ST>(0.f);
       continue;
     }
-    // the state before the sequence
+    // the state before the sequence or part
 #pragma unroll 1
     for (int i0 = 0; i0 < KH; i0 += 16) {
       float s[16];
-      const ST* at = src + i0 * p.V;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = src ? to_f32(at[i * p.V]) : 0.f;
+      for (int i = 0; i < 16; ++i) {
+        const int at = (i0 + i) * p.V;
+        s[i] = src ? to_f32(src[at]) : fsrc ? fsrc[at] : 0.f;
+        if (kState && keep) keep[at] = s[i];
+      }
       tmem_st16(tq + TM_S + hf * KH + i0, s);
     }
     tmem_st_wait();
+    float total = 1.f;  // decay of the part
 #pragma unroll 1
     for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
       const uint32_t st = j % kStages, par = j & 1, fi = j % kFacs;
       const int64_t t0 = it.bos + (int64_t)ch * kL;
       const int m = it.eos - t0 < kL ? (int)(it.eos - t0) : kL;
-      if (__any_sync(0xffffffffu, tc_aborted(c))) return;
       // S before the chunk: its bf16 copy for the product with C, and its decay over the chunk
-      tc_wait(T_FAC + fi, (j / kFacs) & 1);
-      const float dec = c->fac[fi].dec[hd];
-      if (ch > 0) tc_wait(T_SU, (j - 1) & 1);
+      const At fac{T_FAC + (int)fi, (j / kFacs) & 1};
+      if (!all_lanes(tc_wait2(fac, ch > 0 ? At{T_SU, (j - 1) & 1} : fac))) return;
       tc_fence_after();
+      const float dec = c->fac[fi].dec[hd];
 #pragma unroll 1
       for (int i0 = 0; i0 < KH; i0 += 32) {
         float s[32], pk[16];
@@ -824,7 +894,7 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 16; ++i) pk[i] = __uint_as_float(pack_bf16x2(s[2 * i], s[2 * i + 1]));
-        tmem_st16(tq + TM_SB + (hf * KH + i0) / 2, pk);
+        if (!kState) tmem_st16(tq + TM_SB + (hf * KH + i0) / 2, pk);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) mul2(s[i], s[i + 1], dec, dec);
         tmem_st16(tq + TM_S + hf * KH + i0, s);
@@ -833,11 +903,18 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&c->bar[T_S]);
-      // the output of tokens [32 hf, + 32), which takes the place of x in its tile
-      {
-        tc_wait(T_XP + par, (j >> 1) & 1);  // the M group has seen x land and has read it
-        tc_wait(T_MX + par, (j >> 1) & 1);
-        tc_wait(T_Y, j & 1);
+      if (kState) {
+        total *= dec;
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&c->bar[T_FAC_FREE + fi]);
+          mbar_arrive(&c->bar[T_EMPTY + st]);
+        }
+      } else {
+        // the output of tokens [32 hf, + 32), which takes the place of x in its tile
+        // (T_XP: the M group has seen x land and has read it)
+        if (!all_lanes(tc_wait3({T_XP + (int)par, (j >> 1) & 1}, {T_MX + (int)par, (j >> 1) & 1}, {T_Y, j & 1})))
+          return;
         tc_fence_after();
         uint8_t* stage = sm + OFF_ST + st * kStageBytes;
         float2 e[4];
@@ -885,32 +962,36 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       }
     }
     // the state after the sequence
-    tc_wait(T_SU, (j - 1) & 1);
+    if (!all_lanes(tc_wait(T_SU, (j - 1) & 1))) return;
     tc_fence_after();
-    if (__any_sync(0xffffffffu, tc_aborted(c))) return;
     {
 #pragma unroll 1
       for (int i0 = 0; i0 < KH; i0 += 16) {
         float s[16];
         tmem_ld16(tq + TM_S + hf * KH + i0, s);
         tmem_ld_wait();
-        if (dst) {
-          ST* at = dst + i0 * p.V;
+        if (kState ? fdst != nullptr : dst != nullptr) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) at[i * p.V] = from_f32<ST>(s[i]);
+          for (int i = 0; i < 16; ++i) {
+            const int at = (i0 + i) * p.V;
+            if (kState) fdst[at] = s[i];
+            else dst[at] = from_f32<ST>(s[i]);
+          }
         }
       }
       tc_fence_before();
     }
+    if (kState && real && vh == 0 && hf == 0) p.decay[it.part * p.H + h] = total;
   }
 }
 
-template <typename ST, int K>
+template <typename ST, int K, bool kState>
 __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid_constant__ ScanParams p) {
   constexpr int PARTS = sizeof(ST) == 4 ? 3 : 2;
   uint8_t* sm = ssm_smem;
   Ctl* c = ctl();
   const int warp = threadIdx.x >> 5;
+  if (kState && *p.entries == 0) return;  // no sequence was cut
   if (smem_u32(sm) & 1023u) {  // the swizzled tiles need it; the window starts so without static smem
     if (threadIdx.x == 0) raise_status(p.status, KDA_DEVICE_PIPE_TIMEOUT);
     return;
@@ -921,7 +1002,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid
       if (b >= T_EMPTY && b < T_EMPTY + kStages) count = 9;        // a commit's, one an R warp
       if (b >= T_FAC_FREE && b < T_FAC_FREE + kFacs) count = 16;   // one a warp of both groups
       if (b >= T_M && b <= T_S) count = 8;                         // one a warp of a group
-      if (b >= T_ITEM_EMPTY && b < T_ITEM_EMPTY + kItems) count = 19;  // M and R warps, issuers, scan
+      if (b >= T_ITEM_EMPTY && b < T_ITEM_EMPTY + kItems) count = kState ? 18 : 19;  // M and R warps, issuers, scan
       mbar_init(&c->bar[b], count);
     }
     c->abort = 0;
@@ -939,18 +1020,146 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = c->tmem_base;
-  if (warp < 8) run_mgroup<K, PARTS>(p, sm, c, tbase);
-  else if (warp < 16) run_rgroup<ST, K>(p, sm, c, tbase);
-  else if (warp == 16) run_output<K>(p, sm, c, tbase);
-  else if (warp == 17) run_loader<K>(p, sm, c);
+  if (warp < 8) run_mgroup<K, PARTS, kState>(p, sm, c, tbase);
+  else if (warp < 16) run_rgroup<ST, K, kState>(p, sm, c, tbase);
+  else if (warp == 16) {
+    if (!kState) run_output<K>(p, sm, c, tbase);
+  } else if (warp == 17) run_loader<K, kState>(p, sm, c);
   else if (warp == 18) run_scan(p, c);
-  else run_state<K, PARTS>(sm, c, tbase);
+  else run_state<K, PARTS, kState>(sm, c, tbase);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 16) tmem_dealloc(tbase, 512);
   if (threadIdx.x == 0) KDA_DEBUG_FOLD(p.status);
+}
+
+// ---- planning: the work lists ---------------------------------------------------------------------
+// One block, in front of the scan on its stream; it writes the whole header, so that nothing has to be
+// cleared before. Entries are sorted by chunk count, most first (a counting sort), as items are claimed
+// in the list's order: an item claimed last is a short one.
+//
+// Cuts. A CTA's share is L = chunks x items a sequence / CTAs. A sequence of more than S = max(1.2 L, 8)
+// chunks would outlast the others: it is cut into parts of at most S chunks. A pass that forms states
+// only (some 60 % of a chunk's time) takes all parts but the last from a zero state, a kernel adds up
+// S_end = decay S_start + S_local along the parts, and then all parts run at once, each from its own
+// start. S and so the parts' number follow from the lengths, the heads and the GPU alone: parts of more
+// than S / 2 chunks, at most 2 / 1.2 CTAs' worth of items, for which the scratch has room.
+constexpr int kPlanThreads = 1024, kKeys = 1024, kMinPart = 8;
+
+__global__ void __launch_bounds__(kPlanThreads)
+ssm_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ idx, int N, int64_t T,
+                int64_t num_slots, int pairs, int grid, int cap, PlanHdr* hdr, Entry* full, Entry* state,
+                Split* splits) {
+  __shared__ uint32_t s_at[2][kKeys];  // entries of a chunk count, then where they go: full, state list
+  __shared__ uint32_t s_scan[2][kPlanThreads / 32];
+  __shared__ unsigned long long s_chunks;
+  __shared__ uint32_t s_parts, s_splits;
+  const int tid = threadIdx.x;
+  check_all(&hdr->status, cu, idx, N, T, T, idx ? num_slots : 0);
+  if (tid == 0) {
+    s_chunks = 0;
+    s_parts = s_splits = 0;
+  }
+  s_at[0][tid] = s_at[1][tid] = 0;
+  __syncthreads();
+  auto chunks_of = [&](int n) -> int64_t {  // -1: not run
+    int64_t a, b;
+    if (!seq_bounds(cu, n, T, &a, &b) || (idx && resolve_slot(idx, n, num_slots) < 0)) return -1;
+    return (b - a + kL - 1) / kL;
+  };
+  unsigned long long mine = 0;
+  for (int n = tid; n < N; n += kPlanThreads) {
+    const int64_t c = chunks_of(n);
+    if (c > 0) mine += (unsigned long long)c;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if ((tid & 31) == 0) atomicAdd(&s_chunks, mine);
+  __syncthreads();
+  // S = ceil(1.2 L) in whole numbers
+  const unsigned long long work = s_chunks * (unsigned)pairs;
+  int64_t S = (int64_t)((work * 6 + 5ull * grid - 1) / (5ull * grid));
+  if (S < kMinPart) S = kMinPart;
+  if (cap == 0) S = INT64_MAX;
+  auto key = [](int64_t len) { return (int)(len < kKeys - 1 ? len : kKeys - 1); };
+  for (int n = tid; n < N; n += kPlanThreads) {
+    const int64_t c = chunks_of(n);
+    if (c < 0) continue;
+    const int64_t m = c > S ? (c + S - 1) / S : 1, len = (c + m - 1) / m;
+    const int64_t whole = m > 1 ? c / len : 1, tail = m > 1 ? c - whole * len : 0;  // full parts, the rest
+    atomicAdd(&s_at[0][key(len)], (uint32_t)whole);
+    if (tail > 0) atomicAdd(&s_at[0][key(tail)], 1u);
+    if (m > 1) atomicAdd(&s_at[1][key(len)], (uint32_t)(tail > 0 ? whole : whole - 1));
+  }
+  __syncthreads();
+  // where each count's entries begin: an exclusive scan from the largest count down
+#pragma unroll 1
+  for (int l = 0; l < 2; ++l) {
+    const int k = kKeys - 1 - tid;
+    const uint32_t v = s_at[l][k];
+    uint32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if ((tid & 31) >= o) x += y;
+    }
+    if ((tid & 31) == 31) s_scan[l][tid >> 5] = x;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < (tid >> 5)) before += s_scan[l][w];
+      all += s_scan[l][w];
+    }
+    s_at[l][k] = before + x - v;
+    if (tid == 0) (l == 0 ? hdr->n_full : hdr->n_state) = all;
+    __syncthreads();
+  }
+  for (int n = tid; n < N; n += kPlanThreads) {
+    const int64_t c = chunks_of(n);
+    if (c < 0) continue;
+    const int64_t m = c > S ? (c + S - 1) / S : 1, len = (c + m - 1) / m;
+    if (m == 1) {
+      full[atomicAdd(&s_at[0][key(len)], 1u)] = Entry{n, 0, (int)c, -1, 1, 1, {0, 0}};
+      continue;
+    }
+    const int parts = (int)((c + len - 1) / len);
+    const int p0 = (int)atomicAdd(&s_parts, (uint32_t)parts);
+    splits[atomicAdd(&s_splits, 1u)] = Split{p0, parts};
+    for (int i = 0; i < parts; ++i) {
+      const int64_t left = c - i * len;
+      const Entry e{n, (int)(i * len), (int)(left < len ? left : len), p0 + i, i == 0, i == parts - 1, {0, 0}};
+      full[atomicAdd(&s_at[0][key(e.nchunks)], 1u)] = e;
+      if (i < parts - 1) state[atomicAdd(&s_at[1][key(len)], 1u)] = e;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    hdr->next_state = hdr->next_full = 0;
+    hdr->n_splits = s_splits;
+  }
+}
+
+// S_end = decay S_start + S_local along the parts of each cut sequence, four elements a thread.
+__global__ void __launch_bounds__(256)
+ssm_combine_kernel(const PlanHdr* __restrict__ hdr, const Split* __restrict__ splits, float* scratch,
+                   const float* __restrict__ decay, int H, int KV) {
+  const int64_t whole = (int64_t)H * KV;
+  const int64_t at = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
+  if (at >= whole) return;
+  const int h = (int)(at / KV);
+  for (uint32_t i = 0; i < hdr->n_splits; ++i) {
+    const Split sp = splits[i];
+    float4 s = *reinterpret_cast<const float4*>(scratch + (sp.part0 + 1) * whole + at);
+    for (int q = 1; q + 1 < sp.parts; ++q) {
+      float* next = scratch + (sp.part0 + q + 1) * whole + at;
+      const float d = decay[(sp.part0 + q) * H + h];
+      const float4 l = *reinterpret_cast<const float4*>(next);
+      s = make_float4(fmaf(d, s.x, l.x), fmaf(d, s.y, l.y), fmaf(d, s.z, l.z), fmaf(d, s.w, l.w));
+      *reinterpret_cast<float4*>(next) = s;
+    }
+  }
 }
 
 // ---- host ----------------------------------------------------------------------------------------
@@ -982,20 +1191,93 @@ bool tc_map(CUtensorMap* m, const void* base, int64_t T, int64_t cols, int64_t p
 int tc_sms() {
   static const int n = [] {
     int dev = 0, v = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-    return v > 0 ? v : 1;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) {
+      (void)cudaGetLastError();
+      v = 152;  // a size asked for where there is no GPU
+    }
+    return v;
   }();
   return n;
 }
 
-template <typename ST, int K>
-cudaError_t launch_k(const ScanParams& p, int grid, cudaStream_t st) {
-  auto kern = ssm_scan_tc_kernel<ST, K>;
+template <typename ST, int K, bool kState>
+cudaError_t launch_scan(const ScanParams& p, int grid, cudaStream_t st) {
+  auto kern = ssm_scan_tc_kernel<ST, K, kState>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
   if (err != cudaSuccess) return err;
   kern<<<grid, kTcThreads, kTcSmem, st>>>(p);
   return cudaGetLastError();
+}
+
+// The workspace behind the header: the lists, and where there is room for cuts the scratch of the parts.
+struct Layout {
+  int cap;  // parts of cut sequences
+  size_t full, state, splits, decay, scratch, lists_end, end;
+};
+Layout layout(const kda_desc_t& d, int pairs) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  Layout l;
+  // at most 2 / 1.2 of the CTAs' number of items, and each cut sequence's rounding
+  l.cap = 2 * tc_sms() / pairs + 2;
+  size_t at = kWsPayload;
+  l.full = at;
+  at += up(sizeof(Entry) * ((size_t)d.num_seqs + l.cap));
+  l.lists_end = at;
+  l.state = at;
+  at += up(sizeof(Entry) * (size_t)l.cap);
+  l.splits = at;
+  at += up(sizeof(Split) * (size_t)l.cap);
+  l.decay = at;
+  at += up(sizeof(float) * (size_t)l.cap * d.num_v_heads);
+  l.scratch = at;
+  at += sizeof(float) * (size_t)l.cap * d.num_v_heads * d.head_k_dim * d.head_v_dim;
+  l.end = at;
+  return l;
+}
+int items_a_sequence(const kda_desc_t& d) {
+  const int rep = d.num_v_heads / d.num_k_heads;
+  return d.num_k_heads * (d.head_v_dim == 64 ? (rep + 1) / 2 : rep);
+}
+
+template <typename ST, int K>
+cudaError_t launch_all(ScanParams& p, const Layout& l, uint8_t* ws, bool lists, bool cuts, cudaStream_t st) {
+  PlanHdr* hdr = reinterpret_cast<PlanHdr*>(ws);
+  const int sms = tc_sms();
+  p.status = &hdr->status;
+  p.next_item = &hdr->next_full;
+  if (!lists) {  // the sequences in their order; the header starts at zero
+    cudaError_t err = cudaMemsetAsync(ws, 0, sizeof(WsHeader), st);
+    if (err != cudaSuccess) return err;
+    return launch_scan<ST, K, false>(p, (int)std::min<int64_t>(sms, (int64_t)p.N * p.pairs), st);
+  }
+  Entry* full = reinterpret_cast<Entry*>(ws + l.full);
+  Entry* state = reinterpret_cast<Entry*>(ws + l.state);
+  Split* splits = reinterpret_cast<Split*>(ws + l.splits);
+  ssm_plan_kernel<<<1, kPlanThreads, 0, st>>>(p.cu, p.idx, p.N, p.T, p.num_slots, p.pairs, sms,
+                                              cuts ? l.cap : 0, hdr, full, state, splits);
+  cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  p.decay = reinterpret_cast<float*>(ws + l.decay);
+  p.scratch = reinterpret_cast<float*>(ws + l.scratch);
+  int64_t items = (int64_t)p.N * p.pairs;
+  if (cuts) {
+    items = sms;
+    p.list = state;
+    p.entries = &hdr->n_state;
+    p.next_item = &hdr->next_state;
+    err = launch_scan<ST, K, true>(p, sms, st);
+    if (err != cudaSuccess) return err;
+    const int64_t whole = (int64_t)p.H * K * p.V;
+    ssm_combine_kernel<<<(unsigned)((whole / 4 + 255) / 256), 256, 0, st>>>(hdr, splits, p.scratch, p.decay,
+                                                                            p.H, K * p.V);
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+  }
+  p.list = full;
+  p.entries = &hdr->n_full;
+  p.next_item = &hdr->next_full;
+  return launch_scan<ST, K, false>(p, (int)std::min<int64_t>(sms, items), st);
 }
 
 }  // namespace
@@ -1004,6 +1286,8 @@ bool ssm_tc_supported(const kda_desc_t& d) {
   return d.qkv_dtype == KDA_BF16 && (d.flags & KDA_FLAG_CUDA_CORE_PATH) == 0u &&
          d.total_tokens > 0 && d.total_tokens < (int64_t)1 << 31;
 }
+
+size_t ssm_tc_workspace(const kda_desc_t& d) { return layout(d, items_a_sequence(d)).end; }
 
 cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t st) {
   const kda_desc_t& d = a.d;
@@ -1026,9 +1310,6 @@ cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t st) {
   p.state_in = a.state_in;
   p.state_out = a.state_out;
   p.y = static_cast<__nv_bfloat16*>(a.y);
-  WsHeader* hdr = reinterpret_cast<WsHeader*>(a.ws);
-  p.status = &hdr->status;
-  p.next_item = &hdr->next_item;
   p.wait_limit_ns = pipeline_wait_limit_ns();
   p.N = d.num_seqs;
   p.H = H;
@@ -1037,15 +1318,16 @@ cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t st) {
   p.T = T;
   p.num_slots = d.num_slots;
   p.slot_stride = a.slot_stride;
-  const int rep = H / G;
-  p.pairs = G * (V == 64 ? (rep + 1) / 2 : rep);
-  // the status word and the item counter start every call at zero
-  cudaError_t err = cudaMemsetAsync(a.ws, 0, sizeof(WsHeader), st);
-  if (err != cudaSuccess) return err;
-  const int grid = (int)std::min<int64_t>(tc_sms(), (int64_t)p.N * p.pairs);
+  p.pairs = items_a_sequence(d);
+  const Layout l = layout(d, p.pairs);
+  const bool lists = a.ws_bytes >= l.lists_end;
+  // a cut takes a sequence of more than kMinPart chunks
+  const bool cuts = a.ws_bytes >= l.end && T > (int64_t)kMinPart * kL;
   if (d.state_dtype == KDA_BF16)
-    return K == 128 ? launch_k<__nv_bfloat16, 128>(p, grid, st) : launch_k<__nv_bfloat16, 64>(p, grid, st);
-  return K == 128 ? launch_k<float, 128>(p, grid, st) : launch_k<float, 64>(p, grid, st);
+    return K == 128 ? launch_all<__nv_bfloat16, 128>(p, l, a.ws, lists, cuts, st)
+                    : launch_all<__nv_bfloat16, 64>(p, l, a.ws, lists, cuts, st);
+  return K == 128 ? launch_all<float, 128>(p, l, a.ws, lists, cuts, st)
+                  : launch_all<float, 64>(p, l, a.ws, lists, cuts, st);
 }
 
 }  // namespace kda
