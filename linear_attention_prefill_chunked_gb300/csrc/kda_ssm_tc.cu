@@ -583,89 +583,115 @@ __device__ void run_state(uint8_t* sm, Ctl* c, uint32_t tbase) {
 }
 
 // ---- warp 18: steps and decays ------------------------------------------------------------------
-__device__ __noinline__ float step_of(float dt, float bias) {
-  return dt == -INFINITY ? 0.f : ssm_step(dt, bias);
+// softplus(x) = max(x, 0) + log(1 + e^-|x|), the logarithm as 2 atanh(u / (2 + u)) with u = e^-|x|:
+// u / (2 + u) <= 1/3, so that seven terms of the series leave a relative error of 2e-8, at small u too.
+// One warp makes the steps of all others' chunks, a thousand dependent cycles with the library's
+// functions; good to ~4e-7 with the fast exponential and quotient.
+__device__ __forceinline__ float softplus_fast(float x) {
+  const float u = ex2(-fabsf(x) * 1.4426950408889634f);
+  const float z = __fdividef(u, 2.f + u), q = z * z;
+  float s = fmaf(q, 1.f / 13.f, 1.f / 11.f);
+  s = fmaf(q, s, 1.f / 9.f);
+  s = fmaf(q, s, 1.f / 7.f);
+  s = fmaf(q, s, 1.f / 5.f);
+  s = fmaf(q, s, 1.f / 3.f);
+  s = fmaf(q, s, 1.f);
+  return fmaxf(x, 0.f) + 2.f * z * s;
 }
 
-// Steps and decays of one head's chunk, by one warp; lane l has tokens 2 l and 2 l + 1.
-__device__ __forceinline__ void scan_steps(Factors* f, int head, float d0, float d1, float rate2, int lane) {
-  const float g0 = rate2 * d0, g1 = rate2 * d1;  // log2-decays
-  const float pair = g0 + g1;
-  float up = pair, dn = pair;  // inclusive sums over the half's 16 lanes, from either end
+// Steps and decays of a chunk, for kHeads heads side by side; lane l has tokens 2 l and 2 l + 1.
+template <int kHeads>
+__device__ __forceinline__ void scan_steps(Factors* f, const float (&d)[2][2], const float (&rate2)[2], int lane) {
+  float g0[kHeads], g1[kHeads], up[kHeads], dn[kHeads];
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) {
+    g0[h] = rate2[h] * d[h][0];  // log2-decays
+    g1[h] = rate2[h] * d[h][1];
+    up[h] = dn[h] = g0[h] + g1[h];  // inclusive sums over the half's 16 lanes, from either end
+  }
 #pragma unroll
   for (int o = 1; o < 16; o <<= 1) {
-    const float a = __shfl_up_sync(0xffffffffu, up, o, 16);
-    const float b = __shfl_down_sync(0xffffffffu, dn, o, 16);
-    if ((lane & 15) >= o) up += a;
-    if ((lane & 15) + o < 16) dn += b;
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+      const float a = __shfl_up_sync(0xffffffffu, up[h], o, 16);
+      const float b = __shfl_down_sync(0xffffffffu, dn[h], o, 16);
+      if ((lane & 15) >= o) up[h] += a;
+      if ((lane & 15) + o < 16) dn[h] += b;
+    }
   }
-  float before = __shfl_up_sync(0xffffffffu, up, 1, 16);
-  float after = __shfl_down_sync(0xffffffffu, dn, 1, 16);
-  if ((lane & 15) == 0) before = 0.f;
-  if ((lane & 15) == 15) after = 0.f;
-  const float first = __shfl_sync(0xffffffffu, up, 15), second = __shfl_sync(0xffffffffu, up, 31);
-  const float pre = lane < 16 ? 0.f : first;
-  const float c0 = before + g0, c1 = up;
-  const int t = 2 * lane;
-  const float l0 = __log2f(d0), l1 = __log2f(d1);  // -inf for a step of zero: a weight of zero
-  *reinterpret_cast<float2*>(&f->cl[head][t]) = make_float2(c0, c1);
-  *reinterpret_cast<float2*>(&f->same[head][t]) = make_float2(l0 - c0, l1 - c1);
-  *reinterpret_cast<float2*>(&f->later[head][t]) = make_float2(l0 + (after + g1), l1 + after);
-  *reinterpret_cast<float2*>(&f->e[head][t]) = make_float2(ex2(pre + c0), ex2(pre + c1));
-  if (lane == 0) {
-    f->second[head] = second;
-    f->dec[head] = ex2(first + second);
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) {
+    float before = __shfl_up_sync(0xffffffffu, up[h], 1, 16);
+    float after = __shfl_down_sync(0xffffffffu, dn[h], 1, 16);
+    if ((lane & 15) == 0) before = 0.f;
+    if ((lane & 15) == 15) after = 0.f;
+    const float first = __shfl_sync(0xffffffffu, up[h], 15), second = __shfl_sync(0xffffffffu, up[h], 31);
+    const float pre = lane < 16 ? 0.f : first;
+    const float c0 = before + g0[h], c1 = up[h];
+    const int t = 2 * lane;
+    const float l0 = __log2f(d[h][0]), l1 = __log2f(d[h][1]);  // -inf for a step of zero: no weight
+    *reinterpret_cast<float2*>(&f->cl[h][t]) = make_float2(c0, c1);
+    *reinterpret_cast<float2*>(&f->same[h][t]) = make_float2(l0 - c0, l1 - c1);
+    *reinterpret_cast<float2*>(&f->later[h][t]) = make_float2(l0 + (after + g1[h]), l1 + after);
+    *reinterpret_cast<float2*>(&f->e[h][t]) = make_float2(ex2(pre + c0), ex2(pre + c1));
+    if (lane == 0) {
+      f->second[h] = second;
+      f->dec[h] = ex2(first + second);
+    }
   }
 }
 
-__device__ void run_scan(const ScanParams& p, Ctl* c) {
-  const int lane = threadIdx.x & 31, rep = p.H / p.G, heads = p.V == 64 ? 2 : 1;
+template <int kHeads>
+__device__ void run_scan_heads(const ScanParams& p, Ctl* c) {
+  const int lane = threadIdx.x & 31, rep = p.H / p.G;
   uint32_t j = 0;
   for (uint32_t k = 0;; ++k) {
     const Item it = tc_item_warp(p, c, k);
     if (it.done) return;
-    const bool second = heads == 2 && (it.h0 % rep) + 1 < rep;
+    const bool second = kHeads == 2 && (it.h0 % rep) + 1 < rep;
     float rate2[2] = {0.f, 0.f}, bias[2] = {0.f, 0.f};
 #pragma unroll
-    for (int hd = 0; hd < 2; ++hd) {
-      if (hd == 1 && !second) break;
-      rate2[hd] = -ex2(p.a_log[it.h0 + hd] * 1.4426950408889634f) * 1.4426950408889634f;
-      bias[hd] = p.dt_bias ? p.dt_bias[it.h0 + hd] : 0.f;
+    for (int h = 0; h < kHeads; ++h) {
+      if (h == 1 && !second) break;
+      rate2[h] = -ex2(p.a_log[it.h0 + h] * 1.4426950408889634f) * 1.4426950408889634f;
+      bias[h] = p.dt_bias ? p.dt_bias[it.h0 + h] : 0.f;
     }
-    // the steps of a chunk are read while the one before is scanned; -inf: no token, a step of zero
-    float n[2][2];
-    auto read = [&](int ch) {
-      const int64_t t = it.bos + (int64_t)ch * kL + 2 * lane;
-      const __nv_bfloat16* at = p.dt + t * p.dt_pitch + it.h0;
+    // the steps of a chunk are read two scans ahead; -inf: no token, a step of zero
+    const __nv_bfloat16* at = p.dt + (it.bos + 2 * lane) * p.dt_pitch + it.h0;
+    int left = (int)(it.eos - it.bos) - 2 * lane;
+    auto read = [&](float (&n)[2][2]) {
 #pragma unroll
-      for (int hd = 0; hd < 2; ++hd) {
-        const bool any = hd == 0 || second;
-        n[hd][0] = any && t < it.eos ? to_f32(at[hd]) : -INFINITY;
-        n[hd][1] = any && t + 1 < it.eos ? to_f32(at[p.dt_pitch + hd]) : -INFINITY;
+      for (int h = 0; h < kHeads; ++h) {
+        n[h][0] = left > 0 && (h == 0 || second) ? to_f32(at[h]) : -INFINITY;
+        n[h][1] = left > 1 && (h == 0 || second) ? to_f32(at[p.dt_pitch + h]) : -INFINITY;
       }
+      at += kL * p.dt_pitch;
+      left -= kL;
     };
+    float cur[2][2], nxt[2][2], d[2][2];
+    read(cur);
+    read(nxt);
 #pragma unroll 1
-    for (int ch = -1; ch < it.nchunks; ++ch) {
-      float d[2][2];
-      if (ch >= 0) {
+    for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
+      const uint32_t fi = j % kFacs;
 #pragma unroll
-        for (int hd = 0; hd < 2; ++hd) {
+      for (int h = 0; h < kHeads; ++h) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) d[hd][i] = step_of(n[hd][i], bias[hd]);
+        for (int i = 0; i < 2; ++i) {
+          d[h][i] = cur[h][i] == -INFINITY ? 0.f : softplus_fast(cur[h][i] + bias[h]);
+          cur[h][i] = nxt[h][i];
         }
       }
-      read(ch + 1);
-      if (ch < 0) continue;
-      const uint32_t fi = j % kFacs;
+      read(nxt);
       if (j >= (uint32_t)kFacs && !all_lanes(tc_wait(T_FAC_FREE + fi, (j / kFacs - 1) & 1))) return;
-#pragma unroll 1
-      for (int hd = 0; hd < heads; ++hd)
-        scan_steps(&c->fac[fi], hd, hd ? d[1][0] : d[0][0], hd ? d[1][1] : d[0][1],
-                   hd ? rate2[1] : rate2[0], lane);
+      scan_steps<kHeads>(&c->fac[fi], d, rate2, lane);
       warp_arrive(&c->bar[T_FAC + fi]);
-      ++j;
     }
   }
+}
+__device__ void run_scan(const ScanParams& p, Ctl* c) {
+  if (p.V == 64) run_scan_heads<2>(p, c);
+  else run_scan_heads<1>(p, c);
 }
 
 // ---- warps 0-7: M and x' ------------------------------------------------------------------------
