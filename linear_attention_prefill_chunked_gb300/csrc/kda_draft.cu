@@ -18,7 +18,7 @@ namespace cg = cooperative_groups;
 // Bound by HBM (a request reads one row of p and noise, and of q after a refusal: 8..12 bytes an
 // entry), or by latency for few requests: a cluster of CTAs shares a request's row, reads it once
 // with 16-byte loads and joins its best entries through distributed shared memory.
-constexpr int kVerThreads = 512;
+constexpr int kVerThreads = 512, kMaxRanks = 8;
 
 struct Best {
   float score;
@@ -71,28 +71,27 @@ __device__ __forceinline__ Best scan_row(const float* __restrict__ p, const floa
   return best;
 }
 
-// Joins the cluster's best entries; every thread of every CTA gets the result.
-__device__ __forceinline__ Best join(Best b, Best* s_warp, Best* s_cta, cg::cluster_group& cl) {
+// Joins the cluster's best entries: each CTA puts its own into every CTA's `all`, so that one barrier
+// of the cluster suffices and what is read after it is the CTA's own.
+__device__ __forceinline__ Best join(Best b, Best* s_warp, Best* all, cg::cluster_group& cl) {
+  auto across = [](Best x) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    Best other{__shfl_xor_sync(0xffffffffu, b.score, o), __shfl_xor_sync(0xffffffffu, b.at, o)};
-    b = better(b, other);
-  }
+    for (int o = 16; o; o >>= 1) {
+      Best other{__shfl_xor_sync(0xffffffffu, x.score, o), __shfl_xor_sync(0xffffffffu, x.at, o)};
+      x = better(x, other);
+    }
+    return x;
+  };
+  b = across(b);
   if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = b;
   __syncthreads();
   if (threadIdx.x < 32) {
-    b = threadIdx.x < kVerThreads / 32 ? s_warp[threadIdx.x] : Best{-1.f, 0x7fffffff};
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      Best other{__shfl_xor_sync(0xffffffffu, b.score, o), __shfl_xor_sync(0xffffffffu, b.at, o)};
-      b = better(b, other);
-    }
-    if (threadIdx.x == 0) *s_cta = b;
+    b = across(threadIdx.x < kVerThreads / 32 ? s_warp[threadIdx.x] : Best{-1.f, 0x7fffffff});
+    if (threadIdx.x < cl.num_blocks()) cl.map_shared_rank(all, threadIdx.x)[cl.block_rank()] = b;
   }
   cl.sync();
-  b = {-1.f, 0x7fffffff};
-  for (unsigned r = 0; r < cl.num_blocks(); ++r) b = better(b, *cl.map_shared_rank(s_cta, r));
-  cl.sync();  // before a CTA overwrites or leaves what others read
+  b = all[0];
+  for (unsigned r = 1; r < cl.num_blocks(); ++r) b = better(b, all[r]);
   return b;
 }
 
@@ -102,11 +101,15 @@ verify_kernel(const int32_t* __restrict__ tokens, const float* __restrict__ p,
               const float* __restrict__ noise, const int32_t* __restrict__ cu,
               int32_t* __restrict__ kept, int32_t* __restrict__ next,
               uint32_t* __restrict__ status, int N, int64_t T, int vocab) {
-  __shared__ Best s_warp[kVerThreads / 32], s_cta;
+  __shared__ Best s_warp[kVerThreads / 32], s_all[2][kMaxRanks];
   __shared__ int s_stop, s_bad;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
   const int n = blockIdx.x / ranks, tid = threadIdx.x;
+
+  // this CTA's part of the noise is wanted whatever is accepted: on its way while that is found out
+  for (int64_t i = ((int64_t)rank * kVerThreads + tid) * 32; i < vocab; i += (int64_t)ranks * kVerThreads * 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + (int64_t)n * vocab + i));
 
   if (blockIdx.x == 0) {  // the status word: bad lengths, drafted tokens outside the vocabulary
     uint32_t bits = 0;
@@ -160,11 +163,11 @@ verify_kernel(const int32_t* __restrict__ tokens, const float* __restrict__ p,
   Best best{-1.f, 0x7fffffff};
   if (stop < len - 1) {
     best = scan_row<true>(pr, q ? q + r * vocab : nullptr, tokens[r + 1], e, vocab, rank, ranks);
-    best = join(best, s_warp, &s_cta, cl);
+    best = join(best, s_warp, s_all[0], cl);
   }
   if (best.score < 0.f) {  // every draft kept, or nothing left of the difference
     best = scan_row<false>(pr, nullptr, 0, e, vocab, rank, ranks);
-    best = join(best, s_warp, &s_cta, cl);
+    best = join(best, s_warp, s_all[1], cl);
   }
   if (rank == 0 && tid == 0) {
     kept[n] = stop + 1;
@@ -237,7 +240,7 @@ cudaError_t launch_verify(int N, int64_t T, int vocab, const int32_t* tokens, co
                           int32_t* kept, int32_t* next, uint32_t* status, cudaStream_t st) {
   // a CTA a request fills the GPU from a few hundred requests on; below that the row is shared
   int ranks = 1;
-  while (ranks < 8 && (int64_t)N * ranks < 304 && (int64_t)ranks * kVerThreads * 8 < vocab) ranks *= 2;
+  while (ranks < kMaxRanks && (int64_t)N * ranks < 304 && (int64_t)ranks * kVerThreads * 8 < vocab) ranks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(N * ranks));
   cfg.blockDim = dim3(kVerThreads);

@@ -207,6 +207,7 @@ cudaError_t launch_ssm_decode(const SsmArgs& a, cudaStream_t st);
 cudaError_t launch_ssm_simt(const SsmArgs& a, cudaStream_t st);
 bool ssm_tc_supported(const kda_desc_t& d);
 size_t ssm_tc_workspace(const kda_desc_t& d);  // the whole workspace, header included
+size_t ssm_simt_workspace(const kda_desc_t& d);
 cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t st);
 // Step size and decay of one (token, head): softplus(dt + bias) and the log-decay (<= 0).
 __device__ __forceinline__ float ssm_step(float dt, float bias) { return softplus_f32(dt + bias); }

@@ -140,7 +140,7 @@ kda_status_t kda_causal_conv_decode(const kda_conv_desc_t* d, const void* x, con
 
 size_t kda_ssm_scan_workspace_size(const kda_desc_t* d) {
   if (!ssm_ok(d) || !ssm_supported(d)) return 0;
-  return kda::ssm_tc_supported(*d) ? kda::ssm_tc_workspace(*d) : KDA_STATUS_WORKSPACE_BYTES;
+  return kda::ssm_tc_supported(*d) ? kda::ssm_tc_workspace(*d) : kda::ssm_simt_workspace(*d);
 }
 
 kda_status_t kda_ssm_scan(const kda_desc_t* d, const kda_ssm_inputs_t* in,

@@ -5,6 +5,7 @@
 //
 // per head, S [K, V] in fp32 registers.
 #include "kda_internal.cuh"
+#include "kda_ssm_plan.cuh"
 
 namespace kda {
 namespace {
@@ -114,93 +115,180 @@ ssm_decode_kernel(kda_ssm_inputs_t in, ST* pool, const int32_t* __restrict__ idx
 }
 
 // ---- prompts, token by token ---------------------------------------------------------------
-// A block takes one sequence, one head and VT columns of its state: a thread holds K/8 rows of one
-// column, eight lanes share a column and add their parts of y by shuffles.  Tokens are staged in
-// shared memory kStage at a time.  fp32 FMAs bound it; time runs along one thread's registers.
-constexpr int kStage = 32, kVT = 32, kScanThreads = 256;
+// A block takes one sequence (or part of one), one head and VT columns of its state: a thread holds 4
+// rows of 4 columns, K/4 lanes all rows of a column. Tokens are staged in shared memory kStage at a
+// time, the next ones on their way in registers. The lanes' parts of y are added for eight tokens and
+// four columns at once, every step of the tree halving the sums a lane still carries.
+// Bound by instructions and their latency, ~45 a token and warp: 115 ns a token where a block has its SM
+// alone (fp32, K = 128); with 16 rows of one column a thread, whose reads of b and c alone take 256 cycles
+// of shared memory, it was 265 ns. Time runs along a block, so long sequences are cut as
+// the tensor-core scan's are: a pass that forms states only (kState), the combine, all parts at once.
+constexpr int kStage = 32, kScanThreads = 256, kEight = 8;
+constexpr int kSimtMinPart = 8;  // chunks
 
-template <typename QT, typename ST, int K>
+struct SimtLists {
+  const Entry* list;        // null: a sequence each
+  const uint32_t* entries;
+  float *scratch, *decay;
+};
+
+template <typename QT, typename ST, int K, bool kState>
 __global__ void __launch_bounds__(kScanThreads)
 ssm_scan_simt_kernel(kda_ssm_inputs_t in, const ST* state_in, const int32_t* __restrict__ idx,
                      ST* state_out, const int32_t* __restrict__ cu, QT* __restrict__ y,
                      uint32_t* __restrict__ status, int N, int64_t T, int H, int G, int V,
-                     int64_t num_slots, int64_t slot_stride) {
-  constexpr int RPT = K / 8;
-  __shared__ __align__(16) float s_b[kStage][K], s_c[kStage][K];
-  __shared__ float s_x[kStage][kVT], s_y[kStage][kVT], s_step[kStage], s_keep[kStage];
+                     int64_t num_slots, int64_t slot_stride, SimtLists lists) {
+  constexpr int KL = K / 4;                 // lanes of a column
+  constexpr int VT = 32 / KL * 4 * 8;       // columns a block: 32 (K = 128) or 64
+  constexpr int NB = kStage * K / 4 / kScanThreads, NX = kStage * VT / 4 / kScanThreads;
+  __shared__ __align__(16) float s_b[kStage][K], s_c[kState ? 1 : kStage][K];
+  __shared__ __align__(16) float s_x[kStage][VT], s_y[kState ? 1 : kStage][VT];
+  __shared__ float2 s_step[kStage];         // step and decay of a token
 
-  const int n = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * kVT, tid = threadIdx.x;
-  if (n == 0 && h == 0 && v0 == 0)
+  const int tid = threadIdx.x, tiles = V / VT;
+  const int e = (int)(blockIdx.x / (unsigned)(H * tiles)), q = (int)(blockIdx.x % (unsigned)(H * tiles));
+  const int h = q / tiles, v0 = q % tiles * VT;
+  Entry en{e, 0, 0, -1, 1, 1, {0, 0}};
+  if (lists.list) {
+    if (e >= (int)*lists.entries) return;
+    en = lists.list[e];
+  } else if (blockIdx.x == 0) {
     check_all(status, cu, idx, N, T, T, idx ? num_slots : 0);
+  }
   int64_t bos, eos;
-  if (!seq_bounds(cu, n, T, &bos, &eos)) return;
-  const int64_t slot = idx ? resolve_slot(idx, n, num_slots) : n;
+  if (!seq_bounds(cu, en.n, T, &bos, &eos)) return;
+  const int64_t slot = idx ? resolve_slot(idx, en.n, num_slots) : en.n;
   if (slot < 0) return;
+  if (lists.list) {
+    bos += (int64_t)en.chunk0 * kSsmChunk;
+    const int64_t end = bos + (int64_t)en.nchunks * kSsmChunk;
+    if (end < eos) eos = end;
+  }
 
-  // lane l of a warp: column l / 8 of the warp's four, rows [(l % 8) * 4, + 4) of each 32 rows
-  const int warp = tid >> 5, lane = tid & 31;
-  const int vc = warp * 4 + lane / 8, r0 = (lane % 8) * 4;
-  const size_t at = slot * slot_stride + (size_t)h * K * V + v0 + vc;
-  float s[RPT];
+  const int warp = tid >> 5, lane = tid & 31, l = lane % KL;
+  const int r0 = l * 4, c0 = (warp * (32 / KL) + lane / KL) * 4;  // the thread's rows and columns
+  const size_t in_state = (size_t)h * K * V + (size_t)r0 * V + v0 + c0, at = slot * slot_stride + in_state;
+  // a part starts from its slot of the scratch, and leaves its end in the next one's (kState)
+  float* part = en.part >= 0 ? lists.scratch + (size_t)en.part * H * K * V + in_state : nullptr;
+  float s[4][4];  // [row][column]
 #pragma unroll
-  for (int j = 0; j < RPT; ++j) {
-    const int k = (j / 4) * 32 + r0 + j % 4;
-    s[j] = state_in ? to_f32(state_in[at + (size_t)k * V]) : 0.f;
+  for (int r = 0; r < 4; ++r) {
+    if (part && !kState) load4(part + (size_t)r * V, s[r]);
+    else if (state_in && en.first) load4(state_in + at + (size_t)r * V, s[r]);
+    else s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.f;
+    if (kState && en.first) store4(part + (size_t)r * V, s[r]);
   }
   const float rate = -expf(in.a_log[h]);
   const float bias = in.dt_bias ? in.dt_bias[h] : 0.f;
   const float dskip = in.d ? in.d[h] : 0.f;
-  const int g = h / (H / G);
+  const QT* pb = static_cast<const QT*>(in.b) + h / (H / G) * K;
+  const QT* pc = static_cast<const QT*>(in.c) + h / (H / G) * K;
+  const QT* px = static_cast<const QT*>(in.x) + h * V + v0;
+  const QT* pd = static_cast<const QT*>(in.dt) + h;
+
+  float nb[NB][4], nc[NB][4], nx[NX][4], nd = 0.f;
+  // tokens past the end: of no step, of a decay of one, zero otherwise
+  auto fetch = [&](int64_t t0) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int j = tid + i * kScanThreads, k = j % (K / 4) * 4;
+      const int64_t t = t0 + j / (K / 4);
+      nb[i][0] = nb[i][1] = nb[i][2] = nb[i][3] = 0.f;
+      nc[i][0] = nc[i][1] = nc[i][2] = nc[i][3] = 0.f;
+      if (t < eos) {
+        load4(pb + t * in.b_pitch + k, nb[i]);
+        if (!kState) load4(pc + t * in.c_pitch + k, nc[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      const int j = tid + i * kScanThreads;
+      const int64_t t = t0 + j / (VT / 4);
+      nx[i][0] = nx[i][1] = nx[i][2] = nx[i][3] = 0.f;
+      if (t < eos) load4(px + t * in.x_pitch + j % (VT / 4) * 4, nx[i]);
+    }
+    if (tid < kStage && t0 + tid < eos) nd = to_f32(pd[(t0 + tid) * in.dt_pitch]);
+  };
+  if (bos < eos) fetch(bos);
+  float total = 1.f;
   for (int64_t t0 = bos; t0 < eos; t0 += kStage) {
     const int m = eos - t0 < kStage ? (int)(eos - t0) : kStage;
     __syncthreads();  // the readers of the stage before are done
-    for (int i = tid; i < m * K; i += kScanThreads) {
-      const int t = i / K, k = i % K;
-      s_b[t][k] = to_f32(static_cast<const QT*>(in.b)[(t0 + t) * in.b_pitch + g * K + k]);
-      s_c[t][k] = to_f32(static_cast<const QT*>(in.c)[(t0 + t) * in.c_pitch + g * K + k]);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int j = tid + i * kScanThreads;
+      store4(&s_b[0][0] + j * 4, nb[i]);
+      if (!kState) store4(&s_c[0][0] + j * 4, nc[i]);
     }
-    for (int i = tid; i < m * kVT; i += kScanThreads)
-      s_x[i / kVT][i % kVT] = to_f32(
-          static_cast<const QT*>(in.x)[(t0 + i / kVT) * in.x_pitch + h * V + v0 + i % kVT]);
-    if (tid < m) {
-      const float step =
-          ssm_step(to_f32(static_cast<const QT*>(in.dt)[(t0 + tid) * in.dt_pitch + h]), bias);
-      s_step[tid] = step;
-      s_keep[tid] = expf(rate * step);
+#pragma unroll
+    for (int i = 0; i < NX; ++i) store4(&s_x[0][0] + (tid + i * kScanThreads) * 4, nx[i]);
+    if (tid < kStage) {
+      const float step = tid < m ? ssm_step(nd, bias) : 0.f;
+      s_step[tid] = make_float2(step, tid < m ? expf(rate * step) : 1.f);
     }
     __syncthreads();
-    for (int t = 0; t < m; ++t) {
-      const float x = s_x[t][vc], dx = s_step[t] * x, keep = s_keep[t];
-      float acc = 0.f;
+    if (t0 + kStage < eos) fetch(t0 + kStage);
+#pragma unroll 1
+    for (int tb = 0; tb < m; tb += kEight) {
+      float acc[kEight * 4];
 #pragma unroll
-      for (int j4 = 0; j4 < RPT / 4; ++j4) {
-        const float4 b = *reinterpret_cast<const float4*>(&s_b[t][j4 * 32 + r0]);
-        const float4 c = *reinterpret_cast<const float4*>(&s_c[t][j4 * 32 + r0]);
-        float* q = s + j4 * 4;
-        q[0] = fmaf(b.x, dx, keep * q[0]); acc = fmaf(c.x, q[0], acc);
-        q[1] = fmaf(b.y, dx, keep * q[1]); acc = fmaf(c.y, q[1], acc);
-        q[2] = fmaf(b.z, dx, keep * q[2]); acc = fmaf(c.z, q[2], acc);
-        q[3] = fmaf(b.w, dx, keep * q[3]); acc = fmaf(c.w, q[3], acc);
+      for (int u = 0; u < kEight; ++u) {
+        const float2 st = s_step[tb + u];
+        float dx[4], b[4], c[4];
+        load4(&s_x[tb + u][c0], dx);
+        load4(&s_b[tb + u][r0], b);
+        if (!kState) load4(&s_c[tb + u][r0], c);
+        mul2(dx[0], dx[1], st.x, st.x);
+        mul2(dx[2], dx[3], st.x, st.x);
+        float* a = acc + u * 4;
+        a[0] = a[1] = a[2] = a[3] = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          mul2(s[r][0], s[r][1], st.y, st.y);
+          mul2(s[r][2], s[r][3], st.y, st.y);
+          acc2(s[r][0], s[r][1], dx[0], dx[1], b[r], b[r]);
+          acc2(s[r][2], s[r][3], dx[2], dx[3], b[r], b[r]);
+          if (!kState) {
+            acc2(a[0], a[1], s[r][0], s[r][1], c[r], c[r]);
+            acc2(a[2], a[3], s[r][2], s[r][3], c[r], c[r]);
+          }
+        }
+        if (kState) total *= st.y;
       }
-      acc += __shfl_xor_sync(0xffffffffu, acc, 1);
-      acc += __shfl_xor_sync(0xffffffffu, acc, 2);
-      acc += __shfl_xor_sync(0xffffffffu, acc, 4);
-      if (lane % 8 == 0) s_y[t][vc] = fmaf(dskip, x, acc);
-    }
-    __syncthreads();
-    for (int i = tid; i < m * kVT; i += kScanThreads) {
-      const int64_t t = t0 + i / kVT;
-      if (KDA_CHECK(t >= 0 && t < T))
-        y[((size_t)t * H + h) * V + v0 + i % kVT] = from_f32<QT>(s_y[i / kVT][i % kVT]);
-    }
-  }
-  if (state_out) {
+      if (!kState) {
+        // sums over a column's lanes: a lane keeps the half of its values that its lane bit names
 #pragma unroll
-    for (int j = 0; j < RPT; ++j) {
-      const int k = (j / 4) * 32 + r0 + j % 4;
-      state_out[at + (size_t)k * V] = from_f32<ST>(s[j]);
+        for (int i = 0; i < (KL == 32 ? 5 : 4); ++i) {
+          const int o = (KL / 2) >> i, n = (kEight * 2) >> i;
+#pragma unroll
+          for (int u = 0; u < n; ++u) {
+            const float mine = l & o ? acc[u + n] : acc[u], other = l & o ? acc[u] : acc[u + n];
+            acc[u] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+          }
+        }
+        // value l n + u: token / 4, column % 4
+#pragma unroll
+        for (int u = 0; u < kEight * 4 / KL; ++u) {
+          const int i = l * (kEight * 4 / KL) + u, t = tb + i / 4, v = c0 + i % 4;
+          s_y[t][v] = fmaf(dskip, s_x[t][v], acc[u]);
+        }
+      }
+    }
+    if (kState) continue;
+    __syncthreads();
+    for (int i = tid; i < m * (VT / 4); i += kScanThreads) {
+      const int64_t t = t0 + i / (VT / 4);
+      float r[4];
+      load4(&s_y[i / (VT / 4)][i % (VT / 4) * 4], r);
+      if (KDA_CHECK(t >= 0 && t < T)) store4(y + ((size_t)t * H + h) * V + v0 + i % (VT / 4) * 4, r);
     }
   }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (kState) store4(part + (size_t)H * K * V + (size_t)r * V, s[r]);
+    else if (state_out && en.last) store4(state_out + at + (size_t)r * V, s[r]);
+  }
+  if (kState && tid == 0 && v0 == 0) lists.decay[en.part * H + h] = total;
   KDA_DEBUG_FOLD(status);
 }
 
@@ -221,14 +309,33 @@ cudaError_t decode_types(const SsmArgs& a, cudaStream_t st) {
   return a.d.head_v_dim == 128 ? decode_kv<QT, ST, 64, 128>(a, st) : decode_kv<QT, ST, 64, 64>(a, st);
 }
 
+// Blocks that run at once: two an SM (256 threads of 128 registers).
+int simt_workers() { return 2 * gpu_sms(); }
+int simt_items(const kda_desc_t& d) { return d.num_v_heads * (d.head_v_dim / (d.head_k_dim == 128 ? 32 : 64)); }
+
+template <typename QT, typename ST, int K, bool kState>
+cudaError_t scan_pass(const SsmArgs& a, int64_t entries, const SimtLists& lists, cudaStream_t st) {
+  const int64_t blocks = entries * simt_items(a.d);  // entries outermost: those not there leave last
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  ssm_scan_simt_kernel<QT, ST, K, kState><<<(unsigned)blocks, kScanThreads, 0, st>>>(
+      a.in, (const ST*)a.state_in, a.idx, (ST*)a.state_out, a.cu, (QT*)a.y, a.status, a.d.num_seqs,
+      a.d.total_tokens, a.d.num_v_heads, a.d.num_k_heads, a.d.head_v_dim, a.d.num_slots, a.slot_stride,
+      lists);
+  return cudaGetLastError();
+}
+
 template <typename QT, typename ST, int K>
 cudaError_t scan_k(const SsmArgs& a, cudaStream_t st) {
-  dim3 grid((unsigned)a.d.num_seqs, (unsigned)a.d.num_v_heads, (unsigned)(a.d.head_v_dim / kVT));
-  ssm_scan_simt_kernel<QT, ST, K><<<grid, kScanThreads, 0, st>>>(
-      a.in, (const ST*)a.state_in, a.idx, (ST*)a.state_out, a.cu, (QT*)a.y, a.status, a.d.num_seqs,
-      a.d.total_tokens, a.d.num_v_heads, a.d.num_k_heads, a.d.head_v_dim, a.d.num_slots,
-      a.slot_stride);
-  return cudaGetLastError();
+  const SsmPlan p = ssm_plan(a, simt_items(a.d), simt_workers(), kSimtMinPart);
+  if (p.cap == 0)
+    return scan_pass<QT, ST, K, false>(a, a.d.num_seqs, SimtLists{nullptr, nullptr, nullptr, nullptr}, st);
+  cudaError_t err = launch_ssm_plan(p, a, st);
+  if (err == cudaSuccess)
+    err = scan_pass<QT, ST, K, true>(a, p.cap, SimtLists{p.state, &p.hdr->n_state, p.scratch, p.decay}, st);
+  if (err == cudaSuccess) err = launch_ssm_combine(p, a, st);
+  if (err != cudaSuccess) return err;
+  return scan_pass<QT, ST, K, false>(a, (int64_t)a.d.num_seqs + p.cap,
+                                     SimtLists{p.full, &p.hdr->n_full, p.scratch, p.decay}, st);
 }
 
 template <typename QT, typename ST>
@@ -242,6 +349,10 @@ cudaError_t launch_ssm_decode(const SsmArgs& a, cudaStream_t st) {
   const bool qb = a.d.qkv_dtype == KDA_BF16, sb = a.d.state_dtype == KDA_BF16;
   if (qb) return sb ? decode_types<__nv_bfloat16, __nv_bfloat16>(a, st) : decode_types<__nv_bfloat16, float>(a, st);
   return sb ? decode_types<float, __nv_bfloat16>(a, st) : decode_types<float, float>(a, st);
+}
+
+size_t ssm_simt_workspace(const kda_desc_t& d) {
+  return ssm_plan_workspace(d, simt_items(d), simt_workers());
 }
 
 cudaError_t launch_ssm_simt(const SsmArgs& a, cudaStream_t st) {

@@ -1,0 +1,217 @@
+// kda_ssm_plan.cu -- the planning kernel of the state space scan, and the kernel that adds up the states
+// along the parts of a cut sequence.
+#include "kda_ssm_plan.cuh"
+
+namespace kda {
+namespace {
+
+// ---- planning: the work lists ---------------------------------------------------------------------
+// One block, in front of the scan on its stream; it writes the whole header, so that nothing has to be
+// cleared before. Entries are sorted by chunk count, most first (a counting sort), as items are claimed
+// in the list's order: an item claimed last is a short one.
+//
+// Cuts. A worker's share is L = chunks x items a sequence / workers. A sequence of many more than
+// S = max(1.2 L, min_part) chunks would outlast the others. Parts of S chunks take their pass over the
+// states and then the whole, ~1.8 S in all, and two more launches: a sequence of more than 2 S + 4 chunks
+// is cut into parts of at most S. A pass that forms states
+// only (some 60 % of a chunk's time) takes all parts but the last from a zero state, a kernel adds up
+// S_end = decay S_start + S_local along the parts, and then all parts run at once, each from its own
+// start. S and so the parts' number follow from the lengths, the heads and the GPU alone: parts of more
+// than S / 2 chunks, at most 2 / 1.2 CTAs' worth of items, for which the scratch has room.
+constexpr int kPlanThreads = 1024, kKeys = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads)
+ssm_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ idx, int N, int64_t T,
+                int64_t num_slots, int items, int workers, int cap, int min_part, PlanHdr* hdr, Entry* full,
+                Entry* state, Split* splits) {
+  __shared__ uint32_t s_at[2][kKeys];  // entries of a chunk count, then where they go: full, state list
+  __shared__ uint32_t s_scan[2][kPlanThreads / 32];
+  __shared__ unsigned long long s_chunks;
+  __shared__ uint32_t s_parts, s_splits;
+  const int tid = threadIdx.x;
+  check_all(&hdr->status, cu, idx, N, T, T, idx ? num_slots : 0);
+  if (tid == 0) {
+    s_chunks = 0;
+    s_parts = s_splits = 0;
+  }
+  s_at[0][tid] = s_at[1][tid] = 0;
+  __syncthreads();
+  auto chunks_of = [&](int n) -> int64_t {  // -1: not run
+    int64_t a, b;
+    if (!seq_bounds(cu, n, T, &a, &b) || (idx && resolve_slot(idx, n, num_slots) < 0)) return -1;
+    return (b - a + kSsmChunk - 1) / kSsmChunk;
+  };
+  unsigned long long mine = 0;
+  for (int n = tid; n < N; n += kPlanThreads) {
+    const int64_t c = chunks_of(n);
+    if (c > 0) mine += (unsigned long long)c;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if ((tid & 31) == 0) atomicAdd(&s_chunks, mine);
+  __syncthreads();
+  // S = ceil(1.2 L) in whole numbers
+  const unsigned long long work = s_chunks * (unsigned)items;
+  int64_t S = (int64_t)((work * 6 + 5ull * workers - 1) / (5ull * workers));
+  if (S < min_part) S = min_part;
+  const int64_t most = cap == 0 ? INT64_MAX : 2 * S + 4;  // chunks of a sequence that stays whole
+  auto key = [](int64_t len) { return (int)(len < kKeys - 1 ? len : kKeys - 1); };
+  for (int n = tid; n < N; n += kPlanThreads) {
+    const int64_t c = chunks_of(n);
+    if (c < 0) continue;
+    const int64_t m = c > most ? (c + S - 1) / S : 1, len = (c + m - 1) / m;
+    const int64_t whole = m > 1 ? c / len : 1, tail = m > 1 ? c - whole * len : 0;  // full parts, the rest
+    atomicAdd(&s_at[0][key(len)], (uint32_t)whole);
+    if (tail > 0) atomicAdd(&s_at[0][key(tail)], 1u);
+    if (m > 1) atomicAdd(&s_at[1][key(len)], (uint32_t)(tail > 0 ? whole : whole - 1));
+  }
+  __syncthreads();
+  // where each count's entries begin: an exclusive scan from the largest count down
+#pragma unroll 1
+  for (int l = 0; l < 2; ++l) {
+    const int k = kKeys - 1 - tid;
+    const uint32_t v = s_at[l][k];
+    uint32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if ((tid & 31) >= o) x += y;
+    }
+    if ((tid & 31) == 31) s_scan[l][tid >> 5] = x;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < (tid >> 5)) before += s_scan[l][w];
+      all += s_scan[l][w];
+    }
+    s_at[l][k] = before + x - v;
+    if (tid == 0) (l == 0 ? hdr->n_full : hdr->n_state) = all;
+    __syncthreads();
+  }
+  for (int n = tid; n < N; n += kPlanThreads) {
+    const int64_t c = chunks_of(n);
+    if (c < 0) continue;
+    const int64_t m = c > most ? (c + S - 1) / S : 1, len = (c + m - 1) / m;
+    if (m == 1) {
+      full[atomicAdd(&s_at[0][key(len)], 1u)] = Entry{n, 0, (int)c, -1, 1, 1, {0, 0}};
+      continue;
+    }
+    const int parts = (int)((c + len - 1) / len);
+    const int p0 = (int)atomicAdd(&s_parts, (uint32_t)parts);
+    splits[atomicAdd(&s_splits, 1u)] = Split{p0, parts};
+    for (int i = 0; i < parts; ++i) {
+      const int64_t left = c - i * len;
+      const Entry e{n, (int)(i * len), (int)(left < len ? left : len), p0 + i, i == 0, i == parts - 1, {0, 0}};
+      full[atomicAdd(&s_at[0][key(e.nchunks)], 1u)] = e;
+      if (i < parts - 1) state[atomicAdd(&s_at[1][key(len)], 1u)] = e;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    hdr->next_state = hdr->next_full = 0;
+    hdr->n_splits = s_splits;
+  }
+}
+
+// S_end = decay S_start + S_local along the parts of each cut sequence, four elements a thread.
+__global__ void __launch_bounds__(256)
+ssm_combine_kernel(const PlanHdr* __restrict__ hdr, const Split* __restrict__ splits, float* scratch,
+                   const float* __restrict__ decay, int H, int KV) {
+  const int64_t whole = (int64_t)H * KV;
+  const int64_t at = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
+  if (at >= whole) return;
+  const int h = (int)(at / KV);
+  for (uint32_t i = 0; i < hdr->n_splits; ++i) {
+    const Split sp = splits[i];
+    float4 s = *reinterpret_cast<const float4*>(scratch + (sp.part0 + 1) * whole + at);
+    for (int q = 1; q + 1 < sp.parts; ++q) {
+      float* next = scratch + (sp.part0 + q + 1) * whole + at;
+      const float d = decay[(sp.part0 + q) * H + h];
+      const float4 l = *reinterpret_cast<const float4*>(next);
+      s = make_float4(fmaf(d, s.x, l.x), fmaf(d, s.y, l.y), fmaf(d, s.z, l.z), fmaf(d, s.w, l.w));
+      *reinterpret_cast<float4*>(next) = s;
+    }
+  }
+}
+
+}  // namespace
+
+int gpu_sms() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) {
+      (void)cudaGetLastError();
+      v = 152;
+    }
+    return v;
+  }();
+  return n;
+}
+
+namespace {
+// Offsets behind the header: the list of sequences, then what cuts need.
+struct Layout {
+  int cap;
+  size_t full, lists_end, state, splits, decay, scratch, end;
+};
+Layout layout(const kda_desc_t& d, int items, int workers) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  Layout l;
+  l.cap = 2 * workers / items + 2;  // 2 / 1.2 workers' worth of items, rounded up
+  size_t at = kWsPayload;
+  l.full = at;
+  at += up(sizeof(Entry) * ((size_t)d.num_seqs + l.cap));
+  l.lists_end = at;
+  l.state = at;
+  at += up(sizeof(Entry) * (size_t)l.cap);
+  l.splits = at;
+  at += up(sizeof(Split) * (size_t)l.cap);
+  l.decay = at;
+  at += up(sizeof(float) * (size_t)l.cap * d.num_v_heads);
+  l.scratch = at;
+  at += sizeof(float) * (size_t)l.cap * d.num_v_heads * d.head_k_dim * d.head_v_dim;
+  l.end = at;
+  return l;
+}
+}  // namespace
+
+size_t ssm_plan_workspace(const kda_desc_t& d, int items, int workers) {
+  return layout(d, items, workers).end;
+}
+
+SsmPlan ssm_plan(const SsmArgs& a, int items, int workers, int min_part) {
+  const Layout l = layout(a.d, items, workers);
+  SsmPlan p;
+  // Where no sequence can be long enough to be cut, none is long enough for its place in the order to
+  // matter: the sequences are taken as they come, in one launch.
+  p.lists = a.ws_bytes >= l.lists_end && a.d.total_tokens > (int64_t)(2 * min_part + 4) * kSsmChunk;
+  p.cap = p.lists && a.ws_bytes >= l.end ? l.cap : 0;
+  p.items = items;
+  p.workers = workers;
+  p.min_part = min_part;
+  p.hdr = reinterpret_cast<PlanHdr*>(a.ws);
+  p.full = reinterpret_cast<Entry*>(a.ws + l.full);
+  p.state = reinterpret_cast<Entry*>(a.ws + l.state);
+  p.splits = reinterpret_cast<Split*>(a.ws + l.splits);
+  p.decay = reinterpret_cast<float*>(a.ws + l.decay);
+  p.scratch = reinterpret_cast<float*>(a.ws + l.scratch);
+  return p;
+}
+
+cudaError_t launch_ssm_plan(const SsmPlan& p, const SsmArgs& a, cudaStream_t st) {
+  ssm_plan_kernel<<<1, kPlanThreads, 0, st>>>(a.cu, a.idx, a.d.num_seqs, a.d.total_tokens, a.d.num_slots,
+                                              p.items, p.workers, p.cap, p.min_part, p.hdr, p.full, p.state,
+                                              p.splits);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_ssm_combine(const SsmPlan& p, const SsmArgs& a, cudaStream_t st) {
+  const int kv = a.d.head_k_dim * a.d.head_v_dim;
+  const int64_t whole = (int64_t)a.d.num_v_heads * kv;
+  ssm_combine_kernel<<<(unsigned)((whole / 4 + 255) / 256), 256, 0, st>>>(p.hdr, p.splits, p.scratch, p.decay,
+                                                                          a.d.num_v_heads, kv);
+  return cudaGetLastError();
+}
+
+}  // namespace kda

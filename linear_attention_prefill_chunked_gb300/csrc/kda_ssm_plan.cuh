@@ -1,0 +1,77 @@
+// kda_ssm_plan.cuh -- work lists of the state space scan, and the cuts of long sequences.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+constexpr int kSsmChunk = 64;  // tokens a chunk
+
+// Two fp32 operations as one packed instruction, each rounded to nearest.
+__device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
+  unsigned long long ab, xy;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(ab) : "l"(xy));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
+}
+__device__ __forceinline__ void sub2(float& a, float& b, float x, float y) {
+  unsigned long long ab, xy;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
+  asm("sub.rn.f32x2 %0, %0, %1;" : "+l"(ab) : "l"(xy));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
+}
+// (a, b) <- (a, b) + (x, y) * (u, v)
+__device__ __forceinline__ void acc2(float& a, float& b, float x, float y, float u, float v) {
+  unsigned long long ab, xy, uv;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(uv) : "f"(u), "f"(v));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(ab) : "l"(xy), "l"(uv));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
+}
+// (a, b) <- (a, b) * (x, y) + (u, v)
+__device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float u, float v) {
+  unsigned long long ab, xy, uv;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(uv) : "f"(u), "f"(v));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(ab) : "l"(xy), "l"(uv));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
+}
+
+// Work-list entry, for every item of a sequence (or part) alike. Long sequences are cut in time where
+// few items would leave SMs idle (see the planning kernel).
+struct Entry {
+  int32_t n, chunk0, nchunks, part;  // part: as in Item
+  int32_t first, last, pad[2];
+};
+struct Split {  // a cut sequence: its parts' slots
+  int32_t part0, parts;
+};
+struct PlanHdr {  // over the workspace header
+  uint32_t status, next_state, next_full, n_state, n_full, n_splits;
+};
+static_assert(sizeof(PlanHdr) <= sizeof(WsHeader), "the plan's header lies in the workspace header");
+
+// Where the lists and the parts' scratch lie in a workspace (see the planning kernel).
+struct SsmPlan {
+  bool lists;          // there is room for the list of sequences
+  int cap;             // most parts of cut sequences, 0: none is cut
+  int items, workers;  // items a sequence, items that run at once
+  int min_part;        // chunks a part has at least, or so
+  PlanHdr* hdr;
+  Entry *full, *state;
+  Split* splits;
+  float *decay, *scratch;
+};
+SsmPlan ssm_plan(const SsmArgs& a, int items, int workers, int min_part);
+// The whole workspace a plan uses, header included.
+size_t ssm_plan_workspace(const kda_desc_t& d, int items, int workers);
+cudaError_t launch_ssm_plan(const SsmPlan& p, const SsmArgs& a, cudaStream_t st);
+cudaError_t launch_ssm_combine(const SsmPlan& p, const SsmArgs& a, cudaStream_t st);
+// SMs of the current device (152, for sizes asked for where there is none).
+int gpu_sms();
+
+}  // namespace kda

@@ -44,6 +44,7 @@
 #include <cstring>
 
 #include "kda_internal.cuh"
+#include "kda_ssm_plan.cuh"
 #include "tc_ptx.cuh"
 
 namespace kda {
@@ -52,12 +53,13 @@ namespace {
 KDA_DEBUG_FLAG_DEFINE();
 using namespace tc;
 
-constexpr int kL = 64;          // tokens a chunk
+constexpr int kL = kSsmChunk;   // tokens a chunk
 constexpr int kStages = 3;      // chunks of c, b and x tiles in flight
 constexpr int kMThreads = 256, kRThreads = 256;
 constexpr int kTcThreads = kMThreads + kRThreads + 128;
 constexpr int kFacs = 3;        // chunks of steps and decays in flight
 constexpr int kItems = 4;       // claimed items in flight
+constexpr int kMinPart = 12;    // chunks a sequence is cut into parts of at least, or so
 
 // ---- shared memory (offsets from a 1024-aligned base) -----------------------------------
 constexpr uint32_t kTileBytes = 16384;               // [2 halves][64 rows][128 B]
@@ -101,20 +103,6 @@ struct Item {
   int64_t bos, eos;   // its tokens
   int64_t state;      // element offset of head h0's state in the initial and final states
 };
-
-// Work-list entry, for every item of a sequence (or part) alike. Long sequences are cut in time where
-// few items would leave SMs idle (see the planning kernel).
-struct Entry {
-  int32_t n, chunk0, nchunks, part;  // part: as in Item
-  int32_t first, last, pad[2];
-};
-struct Split {  // a cut sequence: its parts' slots
-  int32_t part0, parts;
-};
-struct PlanHdr {  // over the workspace header
-  uint32_t status, next_state, next_full, n_state, n_full, n_splits;
-};
-static_assert(sizeof(PlanHdr) <= sizeof(WsHeader), "the plan's header lies in the workspace header");
 
 // Steps and decays of a chunk, by [head of the item][token], logarithms to base 2; a half is 32 tokens.
 struct Factors {
@@ -222,30 +210,6 @@ __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
-}
-// Two fp32 operations as one packed instruction, each rounded to nearest.
-__device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
-  unsigned long long ab, xy;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
-  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(ab) : "l"(xy));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
-}
-__device__ __forceinline__ void sub2(float& a, float& b, float x, float y) {
-  unsigned long long ab, xy;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
-  asm("sub.rn.f32x2 %0, %0, %1;" : "+l"(ab) : "l"(xy));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
-}
-// (a, b) <- (a, b) * (x, y) + (u, v)
-__device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float u, float v) {
-  unsigned long long ab, xy, uv;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(uv) : "f"(u), "f"(v));
-  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(ab) : "l"(xy), "l"(uv));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -1061,133 +1025,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid
   if (threadIdx.x == 0) KDA_DEBUG_FOLD(p.status);
 }
 
-// ---- planning: the work lists ---------------------------------------------------------------------
-// One block, in front of the scan on its stream; it writes the whole header, so that nothing has to be
-// cleared before. Entries are sorted by chunk count, most first (a counting sort), as items are claimed
-// in the list's order: an item claimed last is a short one.
-//
-// Cuts. A CTA's share is L = chunks x items a sequence / CTAs. A sequence of more than S = max(1.2 L, 8)
-// chunks would outlast the others: it is cut into parts of at most S chunks. A pass that forms states
-// only (some 60 % of a chunk's time) takes all parts but the last from a zero state, a kernel adds up
-// S_end = decay S_start + S_local along the parts, and then all parts run at once, each from its own
-// start. S and so the parts' number follow from the lengths, the heads and the GPU alone: parts of more
-// than S / 2 chunks, at most 2 / 1.2 CTAs' worth of items, for which the scratch has room.
-constexpr int kPlanThreads = 1024, kKeys = 1024, kMinPart = 8;
-
-__global__ void __launch_bounds__(kPlanThreads)
-ssm_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ idx, int N, int64_t T,
-                int64_t num_slots, int pairs, int grid, int cap, PlanHdr* hdr, Entry* full, Entry* state,
-                Split* splits) {
-  __shared__ uint32_t s_at[2][kKeys];  // entries of a chunk count, then where they go: full, state list
-  __shared__ uint32_t s_scan[2][kPlanThreads / 32];
-  __shared__ unsigned long long s_chunks;
-  __shared__ uint32_t s_parts, s_splits;
-  const int tid = threadIdx.x;
-  check_all(&hdr->status, cu, idx, N, T, T, idx ? num_slots : 0);
-  if (tid == 0) {
-    s_chunks = 0;
-    s_parts = s_splits = 0;
-  }
-  s_at[0][tid] = s_at[1][tid] = 0;
-  __syncthreads();
-  auto chunks_of = [&](int n) -> int64_t {  // -1: not run
-    int64_t a, b;
-    if (!seq_bounds(cu, n, T, &a, &b) || (idx && resolve_slot(idx, n, num_slots) < 0)) return -1;
-    return (b - a + kL - 1) / kL;
-  };
-  unsigned long long mine = 0;
-  for (int n = tid; n < N; n += kPlanThreads) {
-    const int64_t c = chunks_of(n);
-    if (c > 0) mine += (unsigned long long)c;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if ((tid & 31) == 0) atomicAdd(&s_chunks, mine);
-  __syncthreads();
-  // S = ceil(1.2 L) in whole numbers
-  const unsigned long long work = s_chunks * (unsigned)pairs;
-  int64_t S = (int64_t)((work * 6 + 5ull * grid - 1) / (5ull * grid));
-  if (S < kMinPart) S = kMinPart;
-  if (cap == 0) S = INT64_MAX;
-  auto key = [](int64_t len) { return (int)(len < kKeys - 1 ? len : kKeys - 1); };
-  for (int n = tid; n < N; n += kPlanThreads) {
-    const int64_t c = chunks_of(n);
-    if (c < 0) continue;
-    const int64_t m = c > S ? (c + S - 1) / S : 1, len = (c + m - 1) / m;
-    const int64_t whole = m > 1 ? c / len : 1, tail = m > 1 ? c - whole * len : 0;  // full parts, the rest
-    atomicAdd(&s_at[0][key(len)], (uint32_t)whole);
-    if (tail > 0) atomicAdd(&s_at[0][key(tail)], 1u);
-    if (m > 1) atomicAdd(&s_at[1][key(len)], (uint32_t)(tail > 0 ? whole : whole - 1));
-  }
-  __syncthreads();
-  // where each count's entries begin: an exclusive scan from the largest count down
-#pragma unroll 1
-  for (int l = 0; l < 2; ++l) {
-    const int k = kKeys - 1 - tid;
-    const uint32_t v = s_at[l][k];
-    uint32_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if ((tid & 31) >= o) x += y;
-    }
-    if ((tid & 31) == 31) s_scan[l][tid >> 5] = x;
-    __syncthreads();
-    uint32_t before = 0, all = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-      if (w < (tid >> 5)) before += s_scan[l][w];
-      all += s_scan[l][w];
-    }
-    s_at[l][k] = before + x - v;
-    if (tid == 0) (l == 0 ? hdr->n_full : hdr->n_state) = all;
-    __syncthreads();
-  }
-  for (int n = tid; n < N; n += kPlanThreads) {
-    const int64_t c = chunks_of(n);
-    if (c < 0) continue;
-    const int64_t m = c > S ? (c + S - 1) / S : 1, len = (c + m - 1) / m;
-    if (m == 1) {
-      full[atomicAdd(&s_at[0][key(len)], 1u)] = Entry{n, 0, (int)c, -1, 1, 1, {0, 0}};
-      continue;
-    }
-    const int parts = (int)((c + len - 1) / len);
-    const int p0 = (int)atomicAdd(&s_parts, (uint32_t)parts);
-    splits[atomicAdd(&s_splits, 1u)] = Split{p0, parts};
-    for (int i = 0; i < parts; ++i) {
-      const int64_t left = c - i * len;
-      const Entry e{n, (int)(i * len), (int)(left < len ? left : len), p0 + i, i == 0, i == parts - 1, {0, 0}};
-      full[atomicAdd(&s_at[0][key(e.nchunks)], 1u)] = e;
-      if (i < parts - 1) state[atomicAdd(&s_at[1][key(len)], 1u)] = e;
-    }
-  }
-  __syncthreads();
-  if (tid == 0) {
-    hdr->next_state = hdr->next_full = 0;
-    hdr->n_splits = s_splits;
-  }
-}
-
-// S_end = decay S_start + S_local along the parts of each cut sequence, four elements a thread.
-__global__ void __launch_bounds__(256)
-ssm_combine_kernel(const PlanHdr* __restrict__ hdr, const Split* __restrict__ splits, float* scratch,
-                   const float* __restrict__ decay, int H, int KV) {
-  const int64_t whole = (int64_t)H * KV;
-  const int64_t at = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
-  if (at >= whole) return;
-  const int h = (int)(at / KV);
-  for (uint32_t i = 0; i < hdr->n_splits; ++i) {
-    const Split sp = splits[i];
-    float4 s = *reinterpret_cast<const float4*>(scratch + (sp.part0 + 1) * whole + at);
-    for (int q = 1; q + 1 < sp.parts; ++q) {
-      float* next = scratch + (sp.part0 + q + 1) * whole + at;
-      const float d = decay[(sp.part0 + q) * H + h];
-      const float4 l = *reinterpret_cast<const float4*>(next);
-      s = make_float4(fmaf(d, s.x, l.x), fmaf(d, s.y, l.y), fmaf(d, s.z, l.z), fmaf(d, s.w, l.w));
-      *reinterpret_cast<float4*>(next) = s;
-    }
-  }
-}
-
 // ---- host ----------------------------------------------------------------------------------------
 PFN_cuTensorMapEncodeTiled_v12000 tc_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -1214,19 +1051,6 @@ bool tc_map(CUtensorMap* m, const void* base, int64_t T, int64_t cols, int64_t p
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int tc_sms() {
-  static const int n = [] {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) {
-      (void)cudaGetLastError();
-      v = 152;  // a size asked for where there is no GPU
-    }
-    return v;
-  }();
-  return n;
-}
-
 template <typename ST, int K, bool kState>
 cudaError_t launch_scan(const ScanParams& p, int grid, cudaStream_t st) {
   auto kern = ssm_scan_tc_kernel<ST, K, kState>;
@@ -1236,74 +1060,37 @@ cudaError_t launch_scan(const ScanParams& p, int grid, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// The workspace behind the header: the lists, and where there is room for cuts the scratch of the parts.
-struct Layout {
-  int cap;  // parts of cut sequences
-  size_t full, state, splits, decay, scratch, lists_end, end;
-};
-Layout layout(const kda_desc_t& d, int pairs) {
-  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  Layout l;
-  // at most 2 / 1.2 of the CTAs' number of items, and each cut sequence's rounding
-  l.cap = 2 * tc_sms() / pairs + 2;
-  size_t at = kWsPayload;
-  l.full = at;
-  at += up(sizeof(Entry) * ((size_t)d.num_seqs + l.cap));
-  l.lists_end = at;
-  l.state = at;
-  at += up(sizeof(Entry) * (size_t)l.cap);
-  l.splits = at;
-  at += up(sizeof(Split) * (size_t)l.cap);
-  l.decay = at;
-  at += up(sizeof(float) * (size_t)l.cap * d.num_v_heads);
-  l.scratch = at;
-  at += sizeof(float) * (size_t)l.cap * d.num_v_heads * d.head_k_dim * d.head_v_dim;
-  l.end = at;
-  return l;
-}
 int items_a_sequence(const kda_desc_t& d) {
   const int rep = d.num_v_heads / d.num_k_heads;
   return d.num_k_heads * (d.head_v_dim == 64 ? (rep + 1) / 2 : rep);
 }
 
 template <typename ST, int K>
-cudaError_t launch_all(ScanParams& p, const Layout& l, uint8_t* ws, bool lists, bool cuts, cudaStream_t st) {
-  PlanHdr* hdr = reinterpret_cast<PlanHdr*>(ws);
-  const int sms = tc_sms();
-  p.status = &hdr->status;
-  p.next_item = &hdr->next_full;
-  if (!lists) {  // the sequences in their order; the header starts at zero
-    cudaError_t err = cudaMemsetAsync(ws, 0, sizeof(WsHeader), st);
-    if (err != cudaSuccess) return err;
-    return launch_scan<ST, K, false>(p, (int)std::min<int64_t>(sms, (int64_t)p.N * p.pairs), st);
+cudaError_t launch_all(ScanParams& p, const SsmArgs& a, cudaStream_t st) {
+  const SsmPlan plan = ssm_plan(a, p.pairs, gpu_sms(), kMinPart);
+  p.status = &reinterpret_cast<PlanHdr*>(a.ws)->status;
+  const int grid = (int)std::min<int64_t>(gpu_sms(), (int64_t)p.N * p.pairs);
+  if (!plan.lists) {  // the sequences in their order; the header starts at zero
+    p.next_item = &reinterpret_cast<PlanHdr*>(a.ws)->next_full;
+    cudaError_t err = cudaMemsetAsync(a.ws, 0, sizeof(WsHeader), st);
+    return err == cudaSuccess ? launch_scan<ST, K, false>(p, grid, st) : err;
   }
-  Entry* full = reinterpret_cast<Entry*>(ws + l.full);
-  Entry* state = reinterpret_cast<Entry*>(ws + l.state);
-  Split* splits = reinterpret_cast<Split*>(ws + l.splits);
-  ssm_plan_kernel<<<1, kPlanThreads, 0, st>>>(p.cu, p.idx, p.N, p.T, p.num_slots, p.pairs, sms,
-                                              cuts ? l.cap : 0, hdr, full, state, splits);
-  cudaError_t err = cudaGetLastError();
+  cudaError_t err = launch_ssm_plan(plan, a, st);
   if (err != cudaSuccess) return err;
-  p.decay = reinterpret_cast<float*>(ws + l.decay);
-  p.scratch = reinterpret_cast<float*>(ws + l.scratch);
-  int64_t items = (int64_t)p.N * p.pairs;
-  if (cuts) {
-    items = sms;
-    p.list = state;
-    p.entries = &hdr->n_state;
-    p.next_item = &hdr->next_state;
-    err = launch_scan<ST, K, true>(p, sms, st);
-    if (err != cudaSuccess) return err;
-    const int64_t whole = (int64_t)p.H * K * p.V;
-    ssm_combine_kernel<<<(unsigned)((whole / 4 + 255) / 256), 256, 0, st>>>(hdr, splits, p.scratch, p.decay,
-                                                                            p.H, K * p.V);
-    err = cudaGetLastError();
+  p.decay = plan.decay;
+  p.scratch = plan.scratch;
+  if (plan.cap > 0) {
+    p.list = plan.state;
+    p.entries = &plan.hdr->n_state;
+    p.next_item = &plan.hdr->next_state;
+    err = launch_scan<ST, K, true>(p, gpu_sms(), st);
+    if (err == cudaSuccess) err = launch_ssm_combine(plan, a, st);
     if (err != cudaSuccess) return err;
   }
-  p.list = full;
-  p.entries = &hdr->n_full;
-  p.next_item = &hdr->next_full;
-  return launch_scan<ST, K, false>(p, (int)std::min<int64_t>(sms, items), st);
+  p.list = plan.full;
+  p.entries = &plan.hdr->n_full;
+  p.next_item = &plan.hdr->next_full;
+  return launch_scan<ST, K, false>(p, plan.cap > 0 ? gpu_sms() : grid, st);
 }
 
 }  // namespace
@@ -1313,7 +1100,9 @@ bool ssm_tc_supported(const kda_desc_t& d) {
          d.total_tokens > 0 && d.total_tokens < (int64_t)1 << 31;
 }
 
-size_t ssm_tc_workspace(const kda_desc_t& d) { return layout(d, items_a_sequence(d)).end; }
+size_t ssm_tc_workspace(const kda_desc_t& d) {
+  return ssm_plan_workspace(d, items_a_sequence(d), gpu_sms());
+}
 
 cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t st) {
   const kda_desc_t& d = a.d;
@@ -1345,15 +1134,9 @@ cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t st) {
   p.num_slots = d.num_slots;
   p.slot_stride = a.slot_stride;
   p.pairs = items_a_sequence(d);
-  const Layout l = layout(d, p.pairs);
-  const bool lists = a.ws_bytes >= l.lists_end;
-  // a cut takes a sequence of more than kMinPart chunks
-  const bool cuts = a.ws_bytes >= l.end && T > (int64_t)kMinPart * kL;
   if (d.state_dtype == KDA_BF16)
-    return K == 128 ? launch_all<__nv_bfloat16, 128>(p, l, a.ws, lists, cuts, st)
-                    : launch_all<__nv_bfloat16, 64>(p, l, a.ws, lists, cuts, st);
-  return K == 128 ? launch_all<float, 128>(p, l, a.ws, lists, cuts, st)
-                  : launch_all<float, 64>(p, l, a.ws, lists, cuts, st);
+    return K == 128 ? launch_all<__nv_bfloat16, 128>(p, a, st) : launch_all<__nv_bfloat16, 64>(p, a, st);
+  return K == 128 ? launch_all<float, 128>(p, a, st) : launch_all<float, 64>(p, a, st);
 }
 
 }  // namespace kda
