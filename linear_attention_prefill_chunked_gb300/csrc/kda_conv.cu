@@ -66,26 +66,47 @@ template <typename T> struct Row<T, 1> {
   static __device__ __forceinline__ Raw zero() { return from_f32<T>(0.f); }
 };
 
-// s * sigmoid(s) = s / (1 + e^-s).  The fast exponential and quotient are good to ~2^-21, far
+// s * sigmoid(s) = s / (1 + e^-s).  The fast exponential and reciprocal are good to ~2^-21, far
 // below a bf16 result's rounding; fp32 results take the accurate ones.
-template <typename T> __device__ __forceinline__ float silu_f32(float s) {
-  return s / (1.f + expf(-s));
+template <typename T, int VEC> __device__ __forceinline__ void silu(float* s) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) s[i] = s[i] / (1.f + expf(-s[i]));
 }
-template <> __device__ __forceinline__ float silu_f32<__nv_bfloat16>(float s) {
-  return __fdividef(s, 1.f + __expf(-s));
+template <> __device__ __forceinline__ void silu<__nv_bfloat16, 1>(float* s) {
+  s[0] = __fdividef(s[0], 1.f + __expf(-s[0]));
+}
+template <> __device__ __forceinline__ void silu<__nv_bfloat16, 4>(float* s) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    float a = s[i], b = s[i + 1];
+    mul2(a, b, -1.4426950408889634f, -1.4426950408889634f);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+    a += 1.f;
+    b += 1.f;
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+    mul2(s[i], s[i + 1], a, b);
+  }
 }
 
-// One token: window win[0..W-1], oldest first (win[W-1] is the token itself).
+// One token: window win[0..W-1], oldest first (win[W-1] is the token itself). Channels in pairs: the
+// kernel's instructions would otherwise take as long as its bytes.
 template <typename T, int VEC, int W>
 __device__ __forceinline__ void apply(const float (&win)[W][VEC], const float (&wt)[W][VEC],
-                                      const float (&bias)[VEC], bool silu, float* out) {
+                                      const float (&bias)[VEC], bool act, float* out) {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    float s = bias[i];
+  for (int i = 0; i < VEC; ++i) out[i] = bias[i];
 #pragma unroll
-    for (int j = 0; j < W; ++j) s = fmaf(wt[j][i], win[j][i], s);
-    out[i] = silu ? silu_f32<T>(s) : s;
+  for (int j = 0; j < W; ++j) {
+    if constexpr (VEC == 4) {
+      acc2(out[0], out[1], wt[j][0], wt[j][1], win[j][0], win[j][1]);
+      acc2(out[2], out[3], wt[j][2], wt[j][3], win[j][2], win[j][3]);
+    } else {
+      out[0] = fmaf(wt[j][0], win[j][0], out[0]);
+    }
   }
+  if (act) silu<T, VEC>(out);
 }
 
 // The taps [VEC][W] of VEC channels are W vectors in a row.
@@ -111,7 +132,7 @@ conv_prompt_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict
                    const T* __restrict__ bias, const int32_t* __restrict__ cu, const T* state_in,
                    const int32_t* __restrict__ idx, T* state_out, int64_t slot_stride,
                    int64_t num_slots, T* __restrict__ y, uint32_t* __restrict__ status, int N,
-                   int64_t total, int ch, bool silu) {
+                   int64_t total, int ch, bool act) {
   using R = Row<T, VEC>;
   constexpr int H = W - 1;                 // inputs a state holds
   constexpr int kTile = kStrip * kStrips;
@@ -194,7 +215,7 @@ conv_prompt_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict
       for (int u = 0; u < kAhead; ++u) {
         float out[VEC];
         R::unpack(cur[u], win[H]);
-        apply<T, VEC, W>(win, wt, bv, silu, out);
+        apply<T, VEC, W>(win, wt, bv, act, out);
         R::store(yt + (size_t)u * ch, R::pack(out));
 #pragma unroll
         for (int j = 0; j < H; ++j) {
@@ -263,7 +284,7 @@ conv_prompt_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict
 #pragma unroll
       for (int j = 0; j < H; ++j) R::unpack(h[j], win[j]);
       R::unpack(nxt[u], win[H]);
-      apply<T, VEC, W>(win, wt, bv, silu, out);
+      apply<T, VEC, W>(win, wt, bv, act, out);
       if (KDA_CHECK(t >= 0 && t < total && c + VEC <= ch)) R::store(y + t * ch + c, R::pack(out));
 #pragma unroll
       for (int j = 0; j + 1 < H; ++j) h[j] = h[j + 1];
@@ -280,7 +301,7 @@ conv_token_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
                   const T* __restrict__ bias, const int32_t* __restrict__ cu, T* pool,
                   const int32_t* __restrict__ idx, int64_t slot_stride, int64_t num_slots,
                   T* __restrict__ y, uint32_t* __restrict__ status, int N, int64_t total, int ch,
-                  bool silu, T* __restrict__ cache, int64_t cache_pitch, int max_steps,
+                  bool act, T* __restrict__ cache, int64_t cache_pitch, int max_steps,
                   bool update_pool) {
   using R = Row<T, VEC>;
   constexpr int H = W - 1;
@@ -306,7 +327,7 @@ conv_token_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
 #pragma unroll
     for (int j = 0; j < H; ++j) R::unpack(h[j], win[j]);
     R::unpack(cur, win[H]);
-    apply<T, VEC, W>(win, wt, bv, silu, out);
+    apply<T, VEC, W>(win, wt, bv, act, out);
     if (KDA_CHECK(t >= 0 && t < total && c + VEC <= ch)) R::store(y + t * ch + c, R::pack(out));
 #pragma unroll
     for (int j = 0; j + 1 < H; ++j) h[j] = h[j + 1];

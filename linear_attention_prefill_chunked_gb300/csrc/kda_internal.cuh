@@ -168,6 +168,40 @@ __device__ __forceinline__ void check_all(uint32_t* status, const int32_t* cu, c
     set_status(status, (s ? KDA_DEVICE_BAD_SEQLENS : 0u) | (i ? KDA_DEVICE_BAD_SLOT : 0u));
 }
 
+// Two fp32 operations as one packed instruction, each rounded to nearest.
+__device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
+  unsigned long long ab, xy;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(ab) : "l"(xy));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
+}
+__device__ __forceinline__ void sub2(float& a, float& b, float x, float y) {
+  unsigned long long ab, xy;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
+  asm("sub.rn.f32x2 %0, %0, %1;" : "+l"(ab) : "l"(xy));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
+}
+// (a, b) <- (a, b) + (x, y) * (u, v)
+__device__ __forceinline__ void acc2(float& a, float& b, float x, float y, float u, float v) {
+  unsigned long long ab, xy, uv;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(uv) : "f"(u), "f"(v));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(ab) : "l"(xy), "l"(uv));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
+}
+// (a, b) <- (a, b) * (x, y) + (u, v)
+__device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float u, float v) {
+  unsigned long long ab, xy, uv;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(uv) : "f"(u), "f"(v));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(ab) : "l"(xy), "l"(uv));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
+}
+
 struct ConvArgs {
   kda_conv_desc_t d;
   const void *x, *w, *bias;
