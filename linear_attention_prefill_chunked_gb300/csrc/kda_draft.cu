@@ -2,6 +2,8 @@
 // probabilities, and the commit of the accepted step's state into the pool.
 #include <cooperative_groups.h>
 
+#include <utility>
+
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -18,7 +20,13 @@ namespace cg = cooperative_groups;
 // Bound by HBM (a request reads one row of p and noise, and of q after a refusal: 8..12 bytes an
 // entry), or by latency for few requests: a cluster of CTAs shares a request's row, reads it once
 // with 16-byte loads and joins its best entries through distributed shared memory.
-constexpr int kVerThreads = 512, kMaxRanks = 8;
+//
+// 64 requests of 131072 entries (82 MB) take 16.7 us, 4.9 TB/s; 12.4 us is a copy's rate, and the
+// chain before the row (lengths, tokens, their probabilities) is three trips to memory.  Loads are
+// issued three rows of 16 bytes an operand ahead of their use (one: 21 us; four need 72 registers: 23 us).
+// CTAs of 256 threads let all 512 of those be resident (512 threads: two waves, 20.1 us); requests too
+// few to fill the GPU so take 512 (one of 32003 entries: 5.9 us against 7.4 us).
+constexpr int kMaxRanks = 8, kBatch = 3;
 
 struct Best {
   float score;
@@ -37,7 +45,7 @@ __device__ __forceinline__ void race(Best& best, float w, float e, int at) {
 }
 
 // The best entry of this CTA's share of the row.  kDiff: w = max(p - q, 0).
-template <bool kDiff>
+template <int kThreads, bool kDiff>
 __device__ __forceinline__ Best scan_row(const float* __restrict__ p, const float* __restrict__ q,
                                          int hot, const float* __restrict__ e, int vocab, int rank,
                                          int ranks) {
@@ -47,25 +55,36 @@ __device__ __forceinline__ Best scan_row(const float* __restrict__ p, const floa
     race(best, pv, ev, i);
   };
   const bool wide = vocab % 4 == 0 && (((uintptr_t)p | (uintptr_t)e | (uintptr_t)(kDiff && q ? q : p)) % 16) == 0;
-  const int stride = ranks * kVerThreads;
+  const int stride = ranks * kThreads;
   if (wide) {
     const int nv = vocab / 4;
     const float4* p4 = reinterpret_cast<const float4*>(p);
     const float4* q4 = reinterpret_cast<const float4*>(q);
     const float4* e4 = reinterpret_cast<const float4*>(e);
-#pragma unroll 4
-    for (int i = rank * kVerThreads + threadIdx.x; i < nv; i += stride) {
-      const float4 a = p4[i], c = e4[i];
-      float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (kDiff && q) b = q4[i];
-      one(4 * i, a.x, b.x, c.x);
-      one(4 * i + 1, a.y, b.y, c.y);
-      one(4 * i + 2, a.z, b.z, c.z);
-      one(4 * i + 3, a.w, b.w, c.w);
+    for (int i0 = rank * kThreads + threadIdx.x; i0 < nv; i0 += kBatch * stride) {
+      float4 a[kBatch], b[kBatch], c[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {  // a batch's loads before its first use
+        const int i = i0 + k * stride;
+        a[k] = b[k] = c[k] = make_float4(0.f, 0.f, 0.f, 0.f);  // a weight of zero never wins
+        if (i < nv) {
+          a[k] = p4[i];
+          c[k] = e4[i];
+          if (kDiff && q) b[k] = q4[i];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = 4 * (i0 + k * stride);
+        one(i, a[k].x, b[k].x, c[k].x);
+        one(i + 1, a[k].y, b[k].y, c[k].y);
+        one(i + 2, a[k].z, b[k].z, c[k].z);
+        one(i + 3, a[k].w, b[k].w, c[k].w);
+      }
     }
   } else {
 #pragma unroll 4
-    for (int i = rank * kVerThreads + threadIdx.x; i < vocab; i += stride)
+    for (int i = rank * kThreads + threadIdx.x; i < vocab; i += stride)
       one(i, p[i], kDiff && q ? q[i] : 0.f, e[i]);
   }
   return best;
@@ -73,6 +92,7 @@ __device__ __forceinline__ Best scan_row(const float* __restrict__ p, const floa
 
 // Joins the cluster's best entries: each CTA puts its own into every CTA's `all`, so that one barrier
 // of the cluster suffices and what is read after it is the CTA's own.
+template <int kThreads>
 __device__ __forceinline__ Best join(Best b, Best* s_warp, Best* all, cg::cluster_group& cl) {
   auto across = [](Best x) {
 #pragma unroll
@@ -86,7 +106,7 @@ __device__ __forceinline__ Best join(Best b, Best* s_warp, Best* all, cg::cluste
   if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = b;
   __syncthreads();
   if (threadIdx.x < 32) {
-    b = across(threadIdx.x < kVerThreads / 32 ? s_warp[threadIdx.x] : Best{-1.f, 0x7fffffff});
+    b = across(threadIdx.x < kThreads / 32 ? s_warp[threadIdx.x] : Best{-1.f, 0x7fffffff});
     if (threadIdx.x < cl.num_blocks()) cl.map_shared_rank(all, threadIdx.x)[cl.block_rank()] = b;
   }
   cl.sync();
@@ -95,25 +115,23 @@ __device__ __forceinline__ Best join(Best b, Best* s_warp, Best* all, cg::cluste
   return b;
 }
 
-__global__ void __launch_bounds__(kVerThreads)
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads)
 verify_kernel(const int32_t* __restrict__ tokens, const float* __restrict__ p,
               const float* __restrict__ q, const float* __restrict__ u,
               const float* __restrict__ noise, const int32_t* __restrict__ cu,
               int32_t* __restrict__ kept, int32_t* __restrict__ next,
               uint32_t* __restrict__ status, int N, int64_t T, int vocab) {
-  __shared__ Best s_warp[kVerThreads / 32], s_all[2][kMaxRanks];
+  __shared__ Best s_warp[kThreads / 32], s_all[2][kMaxRanks];
   __shared__ int s_stop, s_bad;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
-  const int n = blockIdx.x / ranks, tid = threadIdx.x;
+  const int n = (int)(blockIdx.x / ranks) - 1, tid = threadIdx.x;
 
-  // this CTA's part of the noise is wanted whatever is accepted: on its way while that is found out
-  for (int64_t i = ((int64_t)rank * kVerThreads + tid) * 32; i < vocab; i += (int64_t)ranks * kVerThreads * 32)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + (int64_t)n * vocab + i));
-
-  if (blockIdx.x == 0) {  // the status word: bad lengths, drafted tokens outside the vocabulary
+  if (n < 0) {  // the first cluster's: the status word, bad lengths and drafted tokens outside the vocabulary
+    if (rank != 0) return;
     uint32_t bits = 0;
-    for (int i = tid; i < N; i += kVerThreads) {
+    for (int i = tid; i < N; i += kThreads) {
       int64_t a, b;
       if (!seq_bounds(cu, i, T, &a, &b)) {
         bits |= KDA_DEVICE_BAD_SEQLENS;
@@ -126,12 +144,24 @@ verify_kernel(const int32_t* __restrict__ tokens, const float* __restrict__ p,
     const int k = __syncthreads_or((int)(bits & KDA_DEVICE_BAD_TOKEN));
     if (tid == 0)
       set_status(status, (s ? KDA_DEVICE_BAD_SEQLENS : 0u) | (k ? KDA_DEVICE_BAD_TOKEN : 0u));
+    return;
   }
 
+  // this CTA's part of the noise is wanted whatever is accepted: on its way while that is found out
+  for (int64_t i = ((int64_t)rank * kThreads + tid) * 32; i < vocab; i += (int64_t)ranks * kThreads * 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + (int64_t)n * vocab + i));
+
+  // every CTA of the cluster has to have started before another writes into its shared memory: said
+  // here and waited for after the accepted tokens are known
+  auto started = cl.barrier_arrive();
   int64_t bos, eos;
-  if (!seq_bounds(cu, n, T, &bos, &eos)) return;  // the whole cluster
+  if (!seq_bounds(cu, n, T, &bos, &eos)) {  // the whole cluster, as at each return below
+    cl.barrier_wait(std::move(started));
+    return;
+  }
   const int len = (int)(eos - bos);
   if (len == 0) {
+    cl.barrier_wait(std::move(started));
     if (rank == 0 && tid == 0) {
       kept[n] = 0;
       next[n] = -1;
@@ -144,7 +174,7 @@ verify_kernel(const int32_t* __restrict__ tokens, const float* __restrict__ p,
     s_bad = 0;
   }
   __syncthreads();
-  for (int j = tid; j < len - 1; j += kVerThreads) {
+  for (int j = tid; j < len - 1; j += kThreads) {
     const int64_t t = bos + j;
     const int d = tokens[t + 1];
     if (d < 0 || d >= vocab) {
@@ -155,6 +185,7 @@ verify_kernel(const int32_t* __restrict__ tokens, const float* __restrict__ p,
     }
   }
   __syncthreads();
+  cl.barrier_wait(std::move(started));
   if (s_bad) return;  // the whole cluster read the same tokens
   const int stop = s_stop;
   const int64_t r = bos + stop;
@@ -162,12 +193,12 @@ verify_kernel(const int32_t* __restrict__ tokens, const float* __restrict__ p,
   const float* e = noise + (int64_t)n * vocab;
   Best best{-1.f, 0x7fffffff};
   if (stop < len - 1) {
-    best = scan_row<true>(pr, q ? q + r * vocab : nullptr, tokens[r + 1], e, vocab, rank, ranks);
-    best = join(best, s_warp, s_all[0], cl);
+    best = scan_row<kThreads, true>(pr, q ? q + r * vocab : nullptr, tokens[r + 1], e, vocab, rank, ranks);
+    best = join<kThreads>(best, s_warp, s_all[0], cl);
   }
   if (best.score < 0.f) {  // every draft kept, or nothing left of the difference
-    best = scan_row<false>(pr, nullptr, 0, e, vocab, rank, ranks);
-    best = join(best, s_warp, s_all[1], cl);
+    best = scan_row<kThreads, false>(pr, nullptr, 0, e, vocab, rank, ranks);
+    best = join<kThreads>(best, s_warp, s_all[1], cl);
   }
   if (rank == 0 && tid == 0) {
     kept[n] = stop + 1;
@@ -240,10 +271,11 @@ cudaError_t launch_verify(int N, int64_t T, int vocab, const int32_t* tokens, co
                           int32_t* kept, int32_t* next, uint32_t* status, cudaStream_t st) {
   // a CTA a request fills the GPU from a few hundred requests on; below that the row is shared
   int ranks = 1;
-  while (ranks < kMaxRanks && (int64_t)N * ranks < 304 && (int64_t)ranks * kVerThreads * 8 < vocab) ranks *= 2;
+  while (ranks < kMaxRanks && (int64_t)N * ranks < 304 && (int64_t)ranks * 4096 < vocab) ranks *= 2;
+  const bool few = (int64_t)N * ranks <= 152;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(N * ranks));
-  cfg.blockDim = dim3(kVerThreads);
+  cfg.gridDim = dim3((unsigned)((N + 1) * ranks));  // (num_seqs is at most 2^27)
+  cfg.blockDim = dim3(few ? 512 : 256);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -251,7 +283,7 @@ cudaError_t launch_verify(int N, int64_t T, int vocab, const int32_t* tokens, co
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_kernel, tokens, p, q, u, noise, cu, kept, next, status, N,
+  return cudaLaunchKernelEx(&cfg, few ? verify_kernel<512> : verify_kernel<256>, tokens, p, q, u, noise, cu, kept, next, status, N,
                             T, vocab);
 }
 
