@@ -220,6 +220,25 @@ struct ConvArgs {
 cudaError_t launch_conv(const ConvArgs& a, cudaStream_t st);
 cudaError_t launch_conv_decode(const ConvArgs& a, cudaStream_t st);
 
+// Four elements as fp32, aligned to four.
+__device__ __forceinline__ void load4(const float* p, float (&r)[4]) {
+  const float4 x = *reinterpret_cast<const float4*>(p);
+  r[0] = x.x; r[1] = x.y; r[2] = x.z; r[3] = x.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&r)[4]) {
+  const uint2 x = *reinterpret_cast<const uint2*>(p);
+  r[0] = __uint_as_float(x.x << 16); r[1] = __uint_as_float(x.x & 0xffff0000u);
+  r[2] = __uint_as_float(x.y << 16); r[3] = __uint_as_float(x.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float (&r)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(r[0], r[1], r[2], r[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&r)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(r[0], r[1]), b = __floats2bfloat162_rn(r[2], r[3]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                            *reinterpret_cast<const uint32_t*>(&b));
+}
+
 struct SsmArgs {
   kda_desc_t d;
   kda_ssm_inputs_t in;

@@ -12,25 +12,6 @@ namespace {
 
 KDA_DEBUG_FLAG_DEFINE();
 
-// Four consecutive state elements as fp32.
-__device__ __forceinline__ void load4(const float* p, float (&r)[4]) {
-  const float4 x = *reinterpret_cast<const float4*>(p);
-  r[0] = x.x; r[1] = x.y; r[2] = x.z; r[3] = x.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&r)[4]) {
-  const uint2 x = *reinterpret_cast<const uint2*>(p);
-  r[0] = __uint_as_float(x.x << 16); r[1] = __uint_as_float(x.x & 0xffff0000u);
-  r[2] = __uint_as_float(x.y << 16); r[3] = __uint_as_float(x.y & 0xffff0000u);
-}
-__device__ __forceinline__ void store4(float* p, const float (&r)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(r[0], r[1], r[2], r[3]);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&r)[4]) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(r[0], r[1]), b = __floats2bfloat162_rn(r[2], r[3]);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                            *reinterpret_cast<const uint32_t*>(&b));
-}
-
 // ---- one token, or a few drafted ones, a row ---------------------------------------------
 // Bound by HBM: each state is streamed in and out once (with drafts: in once, out once a step).
 // Grid (rows, heads): rows and heads on axes of their own, rows on grid.x.  A block of 256 threads
@@ -148,7 +129,7 @@ ssm_scan_simt_kernel(kda_ssm_inputs_t in, const ST* state_in, const int32_t* __r
   const int tid = threadIdx.x, tiles = V / VT;
   const int e = (int)(blockIdx.x / (unsigned)(H * tiles)), q = (int)(blockIdx.x % (unsigned)(H * tiles));
   const int h = q / tiles, v0 = q % tiles * VT;
-  Entry en{e, 0, 0, -1, 1, 1, {0, 0}};
+  Entry en{e, 0, 0, -1, 1, {0, 0, 0}};
   if (lists.list) {
     if (e >= (int)*lists.entries) return;
     en = lists.list[e];
@@ -168,15 +149,14 @@ ssm_scan_simt_kernel(kda_ssm_inputs_t in, const ST* state_in, const int32_t* __r
   const int warp = tid >> 5, lane = tid & 31, l = lane % KL;
   const int r0 = l * 4, c0 = (warp * (32 / KL) + lane / KL) * 4;  // the thread's rows and columns
   const size_t in_state = (size_t)h * K * V + (size_t)r0 * V + v0 + c0, at = slot * slot_stride + in_state;
-  // a part starts from its slot of the scratch, and leaves its end in the next one's (kState)
+  // a part starts from its slot of the scratch; what it adds goes into the next one's (kState)
   float* part = en.part >= 0 ? lists.scratch + (size_t)en.part * H * K * V + in_state : nullptr;
   float s[4][4];  // [row][column]
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     if (part && !kState) load4(part + (size_t)r * V, s[r]);
-    else if (state_in && en.first) load4(state_in + at + (size_t)r * V, s[r]);
+    else if (state_in && !kState) load4(state_in + at + (size_t)r * V, s[r]);
     else s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.f;
-    if (kState && en.first) store4(part + (size_t)r * V, s[r]);
   }
   const float rate = -expf(in.a_log[h]);
   const float bias = in.dt_bias ? in.dt_bias[h] : 0.f;

@@ -2,6 +2,8 @@
 // along the parts of a cut sequence.
 #include "kda_ssm_plan.cuh"
 
+#include <algorithm>
+
 namespace kda {
 namespace {
 
@@ -93,15 +95,15 @@ ssm_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ idx,
     if (c < 0) continue;
     const int64_t m = c > most ? (c + S - 1) / S : 1, len = (c + m - 1) / m;
     if (m == 1) {
-      full[atomicAdd(&s_at[0][key(len)], 1u)] = Entry{n, 0, (int)c, -1, 1, 1, {0, 0}};
+      full[atomicAdd(&s_at[0][key(len)], 1u)] = Entry{n, 0, (int)c, -1, 1, {0, 0, 0}};
       continue;
     }
     const int parts = (int)((c + len - 1) / len);
     const int p0 = (int)atomicAdd(&s_parts, (uint32_t)parts);
-    splits[atomicAdd(&s_splits, 1u)] = Split{p0, parts};
+    splits[atomicAdd(&s_splits, 1u)] = Split{p0, parts, idx ? resolve_slot(idx, n, num_slots) : n};
     for (int i = 0; i < parts; ++i) {
       const int64_t left = c - i * len;
-      const Entry e{n, (int)(i * len), (int)(left < len ? left : len), p0 + i, i == 0, i == parts - 1, {0, 0}};
+      const Entry e{n, (int)(i * len), (int)(left < len ? left : len), p0 + i, i == parts - 1, {0, 0, 0}};
       full[atomicAdd(&s_at[0][key(e.nchunks)], 1u)] = e;
       if (i < parts - 1) state[atomicAdd(&s_at[1][key(len)], 1u)] = e;
     }
@@ -113,24 +115,33 @@ ssm_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ idx,
   }
 }
 
-// S_end = decay S_start + S_local along the parts of each cut sequence, four elements a thread.
+// The state before each part of the cut sequences, four elements a thread: the initial one, then
+// S_end = decay S_start + what the part adds. The next part's are read before they are wanted.
+template <typename ST>
 __global__ void __launch_bounds__(256)
 ssm_combine_kernel(const PlanHdr* __restrict__ hdr, const Split* __restrict__ splits, float* scratch,
-                   const float* __restrict__ decay, int H, int KV) {
+                   const float* __restrict__ decay, const ST* __restrict__ state_in, int64_t slot_stride, int H,
+                   int KV) {
   const int64_t whole = (int64_t)H * KV;
   const int64_t at = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
   if (at >= whole) return;
   const int h = (int)(at / KV);
-  for (uint32_t i = 0; i < hdr->n_splits; ++i) {
+  for (uint32_t i = blockIdx.y; i < hdr->n_splits; i += gridDim.y) {
     const Split sp = splits[i];
-    float4 s = *reinterpret_cast<const float4*>(scratch + (sp.part0 + 1) * whole + at);
-    for (int q = 1; q + 1 < sp.parts; ++q) {
-      float* next = scratch + (sp.part0 + q + 1) * whole + at;
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, l[4], n[4];
+    if (state_in) load4(state_in + sp.slot * slot_stride + at, s);
+    float* part = scratch + sp.part0 * whole + at;
+    load4(part + whole, n);
+    for (int q = 0; q + 1 < sp.parts; ++q, part += whole) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) l[u] = n[u];
+      if (q + 2 < sp.parts) load4(part + 2 * whole, n);
       const float d = decay[(sp.part0 + q) * H + h];
-      const float4 l = *reinterpret_cast<const float4*>(next);
-      s = make_float4(fmaf(d, s.x, l.x), fmaf(d, s.y, l.y), fmaf(d, s.z, l.z), fmaf(d, s.w, l.w));
-      *reinterpret_cast<float4*>(next) = s;
+      store4(part, s);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) s[u] = fmaf(d, s[u], l[u]);
     }
+    store4(part, s);
   }
 }
 
@@ -209,8 +220,14 @@ cudaError_t launch_ssm_plan(const SsmPlan& p, const SsmArgs& a, cudaStream_t st)
 cudaError_t launch_ssm_combine(const SsmPlan& p, const SsmArgs& a, cudaStream_t st) {
   const int kv = a.d.head_k_dim * a.d.head_v_dim;
   const int64_t whole = (int64_t)a.d.num_v_heads * kv;
-  ssm_combine_kernel<<<(unsigned)((whole / 4 + 255) / 256), 256, 0, st>>>(p.hdr, p.splits, p.scratch, p.decay,
-                                                                          a.d.num_v_heads, kv);
+  const dim3 grid((unsigned)((whole / 4 + 255) / 256), (unsigned)std::min(p.cap / 2, 16));
+  if (a.d.state_dtype == KDA_BF16)
+    ssm_combine_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p.hdr, p.splits, p.scratch, p.decay,
+                                                            (const __nv_bfloat16*)a.state_in, a.slot_stride,
+                                                            a.d.num_v_heads, kv);
+  else
+    ssm_combine_kernel<float><<<grid, 256, 0, st>>>(p.hdr, p.splits, p.scratch, p.decay, (const float*)a.state_in,
+                                                    a.slot_stride, a.d.num_v_heads, kv);
   return cudaGetLastError();
 }
 

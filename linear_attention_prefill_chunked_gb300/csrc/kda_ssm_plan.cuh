@@ -10,11 +10,12 @@ constexpr int kSsmChunk = 64;  // tokens a chunk
 // Work-list entry, for every item of a sequence (or part) alike. Long sequences are cut in time where
 // few items would leave SMs idle (see the planning kernel).
 struct Entry {
-  int32_t n, chunk0, nchunks, part;  // part: as in Item
-  int32_t first, last, pad[2];
+  int32_t n, chunk0, nchunks, part;  // part: its slot of the scratch, -1: a whole sequence
+  int32_t last, pad[3];              // of the sequence's parts
 };
-struct Split {  // a cut sequence: its parts' slots
+struct Split {  // a cut sequence: its parts' slots of the scratch, its slot of the states
   int32_t part0, parts;
+  int64_t slot;
 };
 struct PlanHdr {  // over the workspace header
   uint32_t status, next_state, next_full, n_state, n_full, n_splits;

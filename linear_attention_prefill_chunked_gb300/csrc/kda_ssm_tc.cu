@@ -99,7 +99,7 @@ enum TcBar {
 struct Item {
   int32_t h0, nchunks, done;
   int32_t part;       // -1: a whole sequence; else the part's slot of the split scratch
-  int32_t first, last;  // of the sequence's parts (1, 1 for a whole one)
+  int32_t last;       // of the sequence's parts (1 for a whole one)
   int64_t bos, eos;   // its tokens
   int64_t state;      // element offset of head h0's state in the initial and final states
 };
@@ -343,7 +343,7 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
         break;
       }
       const int e = (int)(w / (uint32_t)p.pairs), q = (int)(w % (uint32_t)p.pairs);
-      Entry en{e, 0, 0, -1, 1, 1, {0, 0}};
+      Entry en{e, 0, 0, -1, 1, {0, 0, 0}};
       if (p.list) en = p.list[e];
       int64_t bos, eos;
       if (!seq_bounds(p.cu, en.n, p.T, &bos, &eos)) {
@@ -365,7 +365,6 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
       it.eos = p.list && end < eos ? end : eos;
       it.nchunks = (int)((it.eos - it.bos + kL - 1) / kL);
       it.part = en.part;
-      it.first = en.first;
       it.last = en.last;
       it.state = slot * p.slot_stride + (int64_t)it.h0 * K * p.V;
       break;
@@ -381,8 +380,8 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
     // a stage comes free little more than a chunk before its tiles are wanted, less than a load from
     // HBM takes: the tiles are brought into L2 kAhead chunks before
     constexpr int kAhead = 3;
-    auto prefetch = [&](int ch) {
-      const int t0 = (int)(it.bos + (int64_t)ch * kL);
+    auto prefetch = [&](int i) {
+      const int t0 = (int)(it.bos + (int64_t)(kState ? it.nchunks - 1 - i : i) * kL);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         if (half < K / 64) {
@@ -393,9 +392,10 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
       }
     };
 #pragma unroll 1
-    for (int ch = -kAhead; ch < it.nchunks; ++ch) {
-      if (ch + kAhead < it.nchunks) prefetch(ch + kAhead);
-      if (ch < 0) continue;
+    for (int i = -kAhead; i < it.nchunks; ++i) {
+      if (i + kAhead < it.nchunks) prefetch(i + kAhead);
+      if (i < 0) continue;
+      const int ch = kState ? it.nchunks - 1 - i : i;
       const uint32_t st = j % kStages;
       if (j >= (uint32_t)kStages && !leave(j - kStages)) break;
       if (tc_aborted(c)) break;
@@ -478,7 +478,7 @@ __device__ void run_output(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
 }
 
 // ---- warp 19: the state's product, and the scores of the chunk after next ------------------------
-template <int K, int PARTS, bool kState>
+template <int K, int PARTS>
 __device__ void run_state(uint8_t* sm, Ctl* c, uint32_t tbase) {
   if (!elect_one()) return;
   const uint32_t sbase = smem_u32(sm);
@@ -528,9 +528,7 @@ __device__ void run_state(uint8_t* sm, Ctl* c, uint32_t tbase) {
     }
     for (int ch = 0; ch < nchunks && ok; ++ch, ++j) {
       const uint32_t st = j % kStages, stage = sbase + OFF_ST + st * kStageBytes;
-      if (!kState) scores(k, j + 2);
-      // (b's tile: seen to land for the scores, where there are any)
-      if (kState) ok = tc_wait(T_FULL + st, (j / kStages) & 1);
+      scores(k, j + 2);  // which have seen b's tile land
       ok = ok && tc_wait2({T_XP + (int)(j & 1), (j >> 1) & 1}, {T_S, j & 1});
       if (!ok) break;
       tc_fence_after();
@@ -677,6 +675,30 @@ __device__ __forceinline__ void split_x(uint32_t raw, float2 w, uint32_t (&out)[
   }
 }
 
+// The lane's part of 32 value columns and 32 tokens of the x tile, as 8 x 8 blocks: columns 16 (i / 2),
+// tokens 16 (i % 2).
+__device__ __forceinline__ void load_x(uint32_t (&raw)[4][4], uint32_t tile, uint32_t col0) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ldsm_x4_trans(raw[i], tile + (i & 1) * 2048 + ((col0 ^ (i & 2)) << 4));
+}
+// x' of 16 of those columns, and its way to TMEM.
+template <int PARTS>
+__device__ __forceinline__ void split_half(const uint32_t (&a)[4], const uint32_t (&b)[4], const float2 (&w)[4],
+                                           uint32_t (&parts)[PARTS][8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t o[PARTS];
+    split_x<PARTS>(i < 4 ? a[i & 3] : b[i & 3], w[i >> 1], o);
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) parts[q][i] = o[q];
+  }
+}
+template <int PARTS>
+__device__ __forceinline__ void put_half(uint32_t taddr, const uint32_t (&parts)[PARTS][8]) {
+#pragma unroll
+  for (int q = 0; q < PARTS; ++q) tmem_st_16x128_x4(taddr + q * 32, parts[q]);
+}
+
 // A 16 x 16 block of M, 8 elements a lane: the scores times their weights, rounded into the M tile at
 // `at` (the lane's row of the four 8 x 8 blocks). `col`: the lane's columns' part of the log-weights;
 // diag: columns after the row are not weighted (their weight may be anything) but zero.
@@ -705,7 +727,7 @@ __device__ __forceinline__ void weigh_block(uint32_t tmem, const float* col, flo
   stsm_x4(at, o[0], o[1], o[2], o[3]);
 }
 
-template <int K, int PARTS, bool kState>
+template <int PARTS>
 __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = p.V == 64 ? 2 : 1;
@@ -738,9 +760,9 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       uint8_t* stage = sm + OFF_ST + st * kStageBytes;
       const Factors* f = &c->fac[fi];
       // (the scores: their tiles have landed. j > 0: the product that read the last M is done.)
-      const At g = kState ? At{T_FAC + (int)fi, (j / kFacs) & 1} : At{T_G + (int)par, (j >> 1) & 1};
+      const At g{T_G + (int)par, (j >> 1) & 1};
       if (!all_lanes(tc_wait3({T_FAC + (int)fi, (j / kFacs) & 1}, g,
-                              j > 0 && !kState ? At{T_MX + (int)(par ^ 1), ((j - 1) >> 1) & 1} : g) &&
+                              j > 0 ? At{T_MX + (int)(par ^ 1), ((j - 1) >> 1) & 1} : g) &&
                      tc_wait(T_FULL + st, (j / kStages) & 1)))
         return;
       tc_fence_after();
@@ -758,17 +780,15 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         }
         __syncwarp();
       }
-      if (!kState) {
-        const float cl0 = f->cl[hm][quad * 16 + (lane >> 2)], cl1 = f->cl[hm][quad * 16 + (lane >> 2) + 8];
-        const uint32_t tg = tbase + TM_YM + par * 64 + ((uint32_t)(quad * 32) << 16);
+      const float cl0 = f->cl[hm][quad * 16 + (lane >> 2)], cl1 = f->cl[hm][quad * 16 + (lane >> 2) + 8];
+      const uint32_t tg = tbase + TM_YM + par * 64 + ((uint32_t)(quad * 32) << 16);
 #pragma unroll 1
-        for (int sb = sb0; sb <= quad; sb += sbn)
-          weigh_block(tg + sb * 16, (sb >> 1 == quad >> 1 ? f->same[hm] : f->later[hm]) + sb * 16 + 2 * (lane & 3),
-                      cl0, cl1, sb == quad, m0 + (((sb * 2 + (lane >> 4)) ^ (lane & 7)) << 4), lane);
-        tc_fence_before();
-      }
+      for (int sb = sb0; sb <= quad; sb += sbn)
+        weigh_block(tg + sb * 16, (sb >> 1 == quad >> 1 ? f->same[hm] : f->later[hm]) + sb * 16 + 2 * (lane & 3),
+                    cl0, cl1, sb == quad, m0 + (((sb * 2 + (lane >> 4)) ^ (lane & 7)) << 4), lane);
+      tc_fence_before();
       fence_async_smem();
-      if (!kState) warp_arrive(&c->bar[T_M + par]);
+      warp_arrive(&c->bar[T_M + par]);
       // x' into registers, and to TMEM once the product that read the last one is done
       float2 w[4];
 #pragma unroll
@@ -778,30 +798,14 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         w[i] = make_float2(ex2(q.x + then), ex2(q.y + then));
       }
       uint32_t raw[4][4], parts[PARTS][8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)  // columns 16 (i / 2), tokens 16 (i % 2)
-        ldsm_x4_trans(raw[i], smem_u32(stage) + xoff + (i & 1) * 2048 + ((col0 ^ (i & 2)) << 4));
-      auto split = [&](int lh) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t o[PARTS];
-          split_x<PARTS>(raw[lh * 2 + (i >> 2)][i & 3], w[i >> 1], o);
-#pragma unroll
-          for (int q = 0; q < PARTS; ++q) parts[q][i] = o[q];
-        }
-      };
-      auto put = [&](int lh) {
-#pragma unroll
-        for (int q = 0; q < PARTS; ++q)
-          tmem_st_16x128_x4(txp + q * 32 + ((uint32_t)(lh * 16) << 16), parts[q]);
-      };
-      split(0);
+      load_x(raw, smem_u32(stage) + xoff, col0);
+      split_half<PARTS>(raw[0], raw[1], w, parts);
       warp_arrive(&c->bar[T_FAC_FREE + fi]);
       if (j > 0 && !all_lanes(tc_wait(T_SU, (j - 1) & 1))) return;
       tc_fence_after();
-      put(0);
-      split(1);
-      put(1);
+      put_half<PARTS>(txp, parts);
+      split_half<PARTS>(raw[2], raw[3], w, parts);
+      put_half<PARTS>(txp + (16u << 16), parts);
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&c->bar[T_XP + par]);
@@ -811,7 +815,7 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
 
 // ---- warps 8-15: the state and the output ------------------------------------------------------
 // Two warps a TMEM lane quadrant: each takes half of S^T's k columns and half of the tokens.
-template <typename ST, int K, bool kState>
+template <typename ST, int K>
 __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
   constexpr int KH = K / 2;                      // k columns a thread
   const int rt = threadIdx.x - kMThreads, warp = rt >> 5, lane = rt & 31;
@@ -834,17 +838,11 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
     const int h = it.h0 + hd;
     const float dskip = p.d && real ? p.d[h] : 0.f;
     const int64_t so = (int64_t)hd * K * p.V + vh + (int64_t)hf * KH * p.V;  // within the item's state
-    // A whole sequence's state comes from and goes to the caller's states. A part's comes from its
-    // slot of the scratch, written by the pass that takes the states only: the initial state into the
-    // first part's slot (in pool mode the last part overwrites the caller's), a part's end (for all but
-    // the first from a zero state) into the next one's, completed by the combining kernel.
+    // A part starts from its slot of the scratch, which the combining kernel has completed.
     const int64_t whole = (int64_t)p.H * K * p.V, head = (int64_t)it.h0 * K * p.V + so;
-    const ST* src = p.state_in && real && (it.part < 0 || (kState && it.first))
-                        ? static_cast<const ST*>(p.state_in) + it.state + so : nullptr;
-    const float* fsrc = !kState && real && it.part >= 0 ? p.scratch + it.part * whole + head : nullptr;
-    ST* dst = !kState && p.state_out && real && it.last ? static_cast<ST*>(p.state_out) + it.state + so : nullptr;
-    float* fdst = kState && real ? p.scratch + (it.part + 1) * whole + head : nullptr;
-    float* keep = kState && real && it.first ? p.scratch + it.part * whole + head : nullptr;
+    const ST* src = p.state_in && real && it.part < 0 ? static_cast<const ST*>(p.state_in) + it.state + so : nullptr;
+    const float* fsrc = real && it.part >= 0 ? p.scratch + it.part * whole + head : nullptr;
+    ST* dst = p.state_out && real && it.last ? static_cast<ST*>(p.state_out) + it.state + so : nullptr;
     if (it.nchunks == 0) {  // an empty sequence keeps its state
       if (dst && (const void*)dst != (const void*)src)
 #pragma unroll 1
@@ -860,12 +858,10 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       for (int i = 0; i < 16; ++i) {
         const int at = (i0 + i) * p.V;
         s[i] = src ? to_f32(src[at]) : fsrc ? fsrc[at] : 0.f;
-        if (kState && keep) keep[at] = s[i];
       }
       tmem_st16(tq + TM_S + hf * KH + i0, s);
     }
     tmem_st_wait();
-    float total = 1.f;  // decay of the part
 #pragma unroll 1
     for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
       const uint32_t st = j % kStages, par = j & 1, fi = j % kFacs;
@@ -884,7 +880,7 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 16; ++i) pk[i] = __uint_as_float(pack_bf16x2(s[2 * i], s[2 * i + 1]));
-        if (!kState) tmem_st16(tq + TM_SB + (hf * KH + i0) / 2, pk);
+        tmem_st16(tq + TM_SB + (hf * KH + i0) / 2, pk);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) mul2(s[i], s[i + 1], dec, dec);
         tmem_st16(tq + TM_S + hf * KH + i0, s);
@@ -893,63 +889,54 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&c->bar[T_S]);
-      if (kState) {
-        total *= dec;
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&c->bar[T_FAC_FREE + fi]);
-          mbar_arrive(&c->bar[T_EMPTY + st]);
-        }
-      } else {
-        // the output of tokens [32 hf, + 32), which takes the place of x in its tile
-        // (T_XP: the M group has seen x land and has read it)
-        if (!all_lanes(tc_wait3({T_XP + (int)par, (j >> 1) & 1}, {T_MX + (int)par, (j >> 1) & 1}, {T_Y, j & 1})))
-          return;
-        tc_fence_after();
-        uint8_t* stage = sm + OFF_ST + st * kStageBytes;
-        float2 e[4];
+      // the output of tokens [32 hf, + 32), which takes the place of x in its tile
+      // (T_XP: the M group has seen x land and has read it)
+      if (!all_lanes(tc_wait3({T_XP + (int)par, (j >> 1) & 1}, {T_MX + (int)par, (j >> 1) & 1}, {T_Y, j & 1})))
+        return;
+      tc_fence_after();
+      uint8_t* stage = sm + OFF_ST + st * kStageBytes;
+      float2 e[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          e[i] = *reinterpret_cast<const float2*>(&c->fac[fi].e[hd][hf * 32 + i * 8 + 2 * (lane & 3)]);
+      for (int i = 0; i < 4; ++i)
+        e[i] = *reinterpret_cast<const float2*>(&c->fac[fi].e[hd][hf * 32 + i * 8 + 2 * (lane & 3)]);
 #pragma unroll 1
-        for (int lh = 0; lh < 2; ++lh) {
-          float a[16], b[16];
-          tmem_ld_16x256_x4(tq + ((uint32_t)(lh * 16) << 16) + TM_YI + hf * 32, a);
-          tmem_ld_16x256_x4(tq + ((uint32_t)(lh * 16) << 16) + TM_YM + par * 64 + hf * 32, b);
-          const uint32_t at = smem_u32(stage) + xoff + ((col0 ^ (lh * 2)) << 4);
-          uint32_t x[2][4];
-          ldsm_x4_trans(x[0], at);
-          ldsm_x4_trans(x[1], at + 2048);
-          tmem_ld_wait();
+      for (int lh = 0; lh < 2; ++lh) {
+        float a[16], b[16];
+        tmem_ld_16x256_x4(tq + ((uint32_t)(lh * 16) << 16) + TM_YI + hf * 32, a);
+        tmem_ld_16x256_x4(tq + ((uint32_t)(lh * 16) << 16) + TM_YM + par * 64 + hf * 32, b);
+        const uint32_t at = smem_u32(stage) + xoff + ((col0 ^ (lh * 2)) << 4);
+        uint32_t x[2][4];
+        ldsm_x4_trans(x[0], at);
+        ldsm_x4_trans(x[1], at + 2048);
+        tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {  // block i / 2 of 8 tokens, lanes 0-7 or 8-15 of the 16
-            float u = bf_lo(x[i >> 2][i & 3]), w = bf_hi(x[i >> 2][i & 3]);
-            fma2(a[2 * i], a[2 * i + 1], e[i >> 1].x, e[i >> 1].y, b[2 * i], b[2 * i + 1]);
-            fma2(u, w, dskip, dskip, a[2 * i], a[2 * i + 1]);
-            x[i >> 2][i & 3] = pack_bf16x2(u, w);
-          }
-          stsm_x4_trans(at, x[0][0], x[0][1], x[0][2], x[0][3]);
-          stsm_x4_trans(at + 2048, x[1][0], x[1][1], x[1][2], x[1][3]);
+        for (int i = 0; i < 8; ++i) {  // block i / 2 of 8 tokens, lanes 0-7 or 8-15 of the 16
+          float u = bf_lo(x[i >> 2][i & 3]), w = bf_hi(x[i >> 2][i & 3]);
+          fma2(a[2 * i], a[2 * i + 1], e[i >> 1].x, e[i >> 1].y, b[2 * i], b[2 * i + 1]);
+          fma2(u, w, dskip, dskip, a[2 * i], a[2 * i + 1]);
+          x[i >> 2][i & 3] = pack_bf16x2(u, w);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&c->bar[T_EPI + par]);
-          mbar_arrive(&c->bar[T_FAC_FREE + fi]);
-        }
-        if (m < kL && real) {
-          // a partial chunk's box would cover the next sequence's rows: the warp's own, 16 bytes a lane
-#pragma unroll 1
-          for (int i = lane >> 2; i < 32; i += 8) {
-            const int row = hf * 32 + i, cell = (quad & 1) * 4 + (lane & 3);
-            if (row < m && KDA_CHECK(t0 + row < p.T))
-              *reinterpret_cast<uint4*>(p.y + ((t0 + row) * p.H + it.h0) * p.V + half * 64 + cell * 8) =
-                  *reinterpret_cast<const uint4*>(stage + OFF_X + half * 8192 + sw128_off(row, cell));
-          }
-        }
-        fence_async_smem();
-        warp_arrive(&c->bar[T_EMPTY + st]);  // a full chunk's tile is stored by the loader
+        stsm_x4_trans(at, x[0][0], x[0][1], x[0][2], x[0][3]);
+        stsm_x4_trans(at + 2048, x[1][0], x[1][1], x[1][2], x[1][3]);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&c->bar[T_EPI + par]);
+        mbar_arrive(&c->bar[T_FAC_FREE + fi]);
+      }
+      if (m < kL && real) {
+        // a partial chunk's box would cover the next sequence's rows: the warp's own, 16 bytes a lane
+#pragma unroll 1
+        for (int i = lane >> 2; i < 32; i += 8) {
+          const int row = hf * 32 + i, cell = (quad & 1) * 4 + (lane & 3);
+          if (row < m && KDA_CHECK(t0 + row < p.T))
+            *reinterpret_cast<uint4*>(p.y + ((t0 + row) * p.H + it.h0) * p.V + half * 64 + cell * 8) =
+                *reinterpret_cast<const uint4*>(stage + OFF_X + half * 8192 + sw128_off(row, cell));
+        }
+      }
+      fence_async_smem();
+      warp_arrive(&c->bar[T_EMPTY + st]);  // a full chunk's tile is stored by the loader
     }
     // the state after the sequence
     if (!all_lanes(tc_wait(T_SU, (j - 1) & 1))) return;
@@ -960,39 +947,190 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         float s[16];
         tmem_ld16(tq + TM_S + hf * KH + i0, s);
         tmem_ld_wait();
-        if (kState ? fdst != nullptr : dst != nullptr) {
+        if (dst) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int at = (i0 + i) * p.V;
-            if (kState) fdst[at] = s[i];
-            else dst[at] = from_f32<ST>(s[i]);
-          }
+          for (int i = 0; i < 16; ++i) dst[(i0 + i) * p.V] = from_f32<ST>(s[i]);
         }
       }
       tc_fence_before();
     }
-    if (kState && real && vh == 0 && hf == 0) p.decay[it.part * p.H + h] = total;
   }
 }
 
-template <typename ST, int K, bool kState>
-__global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid_constant__ ScanParams p) {
-  constexpr int PARTS = sizeof(ST) == 4 ? 3 : 2;
-  uint8_t* sm = ssm_smem;
-  Ctl* c = ctl();
-  const int warp = threadIdx.x >> 5;
-  if (kState && *p.entries == 0) return;  // no sequence was cut
-  if (smem_u32(sm) & 1023u) {  // the swizzled tiles need it; the window starts so without static smem
+// ---- the pass that forms states only -------------------------------------------------------------
+// What a part adds to the state, sum_s exp(g_{s+1} + .. + g_end) d_s b_s x_s^T, from its last chunk to
+// its first: the sum of the log-decays after a chunk is then known when the chunk comes, so that x'
+// can take the decay to the part's end and S is not decayed on the way. No chain is left from chunk to
+// chunk but the accumulator, and no exponent is positive. Both groups make x' (a chunk each, in turn),
+// warps 18 and 16 scan a head each, two buffers hold x' and two S^T. (In the order of time, with S
+// decayed every chunk, the pass took as long as the one that makes the outputs.) Chunks are all full: a
+// sequence's last part is not in the list.
+constexpr int S_XFREE = T_MX, S_DONE = T_G, S_FREE = T_EPI;  // x' is read, S complete, S read: by parity
+__device__ __forceinline__ uint32_t states_xp(uint32_t par) { return par ? TM_SB : TM_XP; }
+__device__ __forceinline__ uint32_t states_s(uint32_t par) { return par ? TM_YM : TM_S; }
+
+__device__ void run_suffixes(const ScanParams& p, Ctl* c, int hd) {
+  const int lane = threadIdx.x & 31, rep = p.H / p.G;
+  uint32_t j = 0;
+  for (uint32_t k = 0;; ++k) {
+    const Item it = tc_item_warp(p, c, k);
+    if (it.done) return;
+    const int h = it.h0 + hd;
+    const bool real = hd == 0 || (it.h0 % rep) + 1 < rep;
+    const float rate2 = real ? -ex2(p.a_log[h] * 1.4426950408889634f) * 1.4426950408889634f : 0.f;
+    const float bias = real && p.dt_bias ? p.dt_bias[h] : 0.f;
+    const __nv_bfloat16* at = p.dt + (it.bos + (int64_t)(it.nchunks - 1) * kL + 2 * lane) * p.dt_pitch + h;
+    int left = real ? it.nchunks : 0;
+    auto read = [&](float (&n)[2]) {  // two scans ahead; -inf: no step
+      n[0] = left > 0 ? to_f32(at[0]) : -INFINITY;
+      n[1] = left > 0 ? to_f32(at[p.dt_pitch]) : -INFINITY;
+      at -= kL * p.dt_pitch;
+      --left;
+    };
+    float cur[2], nxt[2], later = 0.f;  // later: log2-decay of the part after the chunk
+    read(cur);
+    read(nxt);
+#pragma unroll 1
+    for (int i = 0; i < it.nchunks; ++i, ++j) {
+      const uint32_t fi = j % kFacs;
+      float d[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        d[u] = cur[u] == -INFINITY ? 0.f : softplus_fast(cur[u] + bias);
+        cur[u] = nxt[u];
+      }
+      read(nxt);
+      const float g0 = rate2 * d[0], g1 = rate2 * d[1];
+      float dn = g0 + g1;  // sum over the half's 16 lanes from here on
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) {
+        const float b = __shfl_down_sync(0xffffffffu, dn, o, 16);
+        if ((lane & 15) + o < 16) dn += b;
+      }
+      float after = __shfl_down_sync(0xffffffffu, dn, 1, 16);
+      if ((lane & 15) == 15) after = 0.f;
+      const float first = __shfl_sync(0xffffffffu, dn, 0), second = __shfl_sync(0xffffffffu, dn, 16);
+      const float then = lane < 16 ? second + later : later;
+      const float2 w = make_float2(ex2(__log2f(d[0]) + ((after + g1) + then)), ex2(__log2f(d[1]) + (after + then)));
+      later += first + second;
+      if (j >= (uint32_t)kFacs && !all_lanes(tc_wait(T_FAC_FREE + fi, (j / kFacs - 1) & 1))) return;
+      *reinterpret_cast<float2*>(&c->fac[fi].e[hd][2 * lane]) = w;
+      warp_arrive(&c->bar[T_FAC + fi]);
+    }
+    if (real && lane == 0) p.decay[it.part * p.H + h] = ex2(later);
+  }
+}
+
+template <int K, int PARTS>
+__device__ void run_sums(uint8_t* sm, Ctl* c, uint32_t tbase) {
+  if (!elect_one()) return;
+  const uint32_t sbase = smem_u32(sm), id_s = idesc_bf16(128, K, 0, 1);
+  uint32_t j = 0;
+  bool ok = true;
+  for (uint32_t k = 0; ok; ++k) {
+    const int slot = k % kItems, sp = k & 1;
+    ok = tc_wait(T_ITEM_FULL + slot, (k / kItems) & 1);
+    if (!ok) break;
+    const int nchunks = c->ring[slot].nchunks, done = c->ring[slot].done;
+    mbar_arrive(&c->bar[T_ITEM_EMPTY + slot]);
+    if (done) break;
+    ok = k < 2 || tc_wait(S_FREE + sp, ((k >> 1) - 1) & 1);
+    for (int i = 0; i < nchunks && ok; ++i, ++j) {
+      const uint32_t st = j % kStages, par = j & 1;
+      ok = tc_wait2({T_FULL + (int)st, (j / kStages) & 1}, {T_XP + (int)par, (j >> 1) & 1});
+      if (!ok) break;
+      tc_fence_after();
+      const Desc b = desc128(sbase + OFF_ST + st * kStageBytes + OFF_B, 8192, 1024);
+#pragma unroll
+      for (uint32_t part = 0; part < PARTS; ++part)
+        issue_ts(tbase + states_s(sp), tbase + states_xp(par) + part * 32, b, 2048, id_s, part > 0 || i > 0);
+      mma_commit(&c->bar[S_XFREE + par]);
+      mma_commit(&c->bar[T_EMPTY + st]);
+    }
+    if (ok) mma_commit(&c->bar[S_DONE + sp]);
+  }
+  mma_commit(&c->bar[T_DRAIN]);
+  mbar_wait(&c->bar[T_DRAIN], 0);  // the full limit, aborted or not
+}
+
+template <int K, int PARTS>
+__device__ void run_weighted(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
+  constexpr int KQ = K / 4;  // k columns of S^T a warp reads
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = warp & 3, th = (warp >> 2) & 1;
+  const uint32_t group = warp >> 3, par = group;
+  // as in the M group
+  const uint32_t xoff = OFF_X + (quad >> 1) * 8192 + th * 4096 + ((lane >> 4) << 10) + (lane & 7) * 128;
+  const uint32_t col0 = ((quad & 1) * 4 + ((lane >> 3) & 1)) ^ (lane & 7);
+  const uint32_t tq = tbase + ((uint32_t)(quad * 32) << 16), txp = tq + states_xp(par) + th * 16;
+  const int v = quad * 32 + lane, hd = p.V == 64 ? v >> 6 : 0, vh = p.V == 64 ? v & 63 : v;
+  const int rep = p.H / p.G;
+  const int64_t whole = (int64_t)p.H * K * p.V;
+  uint32_t j = 0;
+  for (uint32_t k = 0;; ++k) {
+    const Item it = tc_item_warp(p, c, k);
+    if (it.done) return;
+    for (int i = 0; i < it.nchunks; ++i, ++j) {
+      if ((j & 1) != group) continue;
+      const uint32_t st = j % kStages, fi = j % kFacs;
+      if (!all_lanes(tc_wait2({T_FULL + (int)st, (j / kStages) & 1}, {T_FAC + (int)fi, (j / kFacs) & 1}))) return;
+      float2 w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        w[u] = *reinterpret_cast<const float2*>(&c->fac[fi].e[hd][th * 32 + u * 8 + 2 * (lane & 3)]);
+      uint32_t raw[4][4], parts[PARTS][8];
+      load_x(raw, smem_u32(sm) + OFF_ST + st * kStageBytes + xoff, col0);
+      split_half<PARTS>(raw[0], raw[1], w, parts);
+      warp_arrive(&c->bar[T_FAC_FREE + fi]);
+      if (j >= 2 && !all_lanes(tc_wait(S_XFREE + (int)par, ((j >> 1) - 1) & 1))) return;
+      tc_fence_after();
+      put_half<PARTS>(txp, parts);
+      split_half<PARTS>(raw[2], raw[3], w, parts);
+      put_half<PARTS>(txp + (16u << 16), parts);
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&c->bar[T_XP + par]);
+    }
+    // what the part adds, into the slot of the part after it
+    const int sp = k & 1;
+    if (!all_lanes(tc_wait(S_DONE + sp, (k >> 1) & 1))) return;
+    tc_fence_after();
+    const bool real = p.V == 128 || hd == 0 || (it.h0 % rep) + 1 < rep;
+    float* dst = p.scratch + (it.part + 1) * whole + ((int64_t)(it.h0 + hd) * K + (warp >> 2) * KQ) * p.V + vh;
+#pragma unroll 1
+    for (int i0 = 0; i0 < KQ; i0 += 16) {
+      float s[16];
+      tmem_ld16(tq + states_s(sp) + (warp >> 2) * KQ + i0, s);
+      tmem_ld_wait();
+      if (real) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dst[(int64_t)(i0 + i) * p.V] = s[i];
+      }
+    }
+    tc_fence_before();
+    warp_arrive(&c->bar[S_FREE + sp]);
+  }
+}
+
+// ---- kernels ---------------------------------------------------------------------------------------
+// Barriers and TMEM; false: the CTA leaves.
+template <bool kState>
+__device__ __forceinline__ bool tc_begin(const ScanParams& p, Ctl* c) {
+  if (smem_u32(ssm_smem) & 1023u) {  // the swizzled tiles need it; the window starts so without static smem
     if (threadIdx.x == 0) raise_status(p.status, KDA_DEVICE_PIPE_TIMEOUT);
-    return;
+    return false;
   }
   if (threadIdx.x == 0) {
+    const uint32_t scans = kState && p.V == 64 ? 2 : 1;  // warps
     for (int b = 0; b < T_COUNT; ++b) {
       uint32_t count = 1;  // a loader's, a scan's or a commit's arrival
-      if (b >= T_EMPTY && b < T_EMPTY + kStages) count = 9;        // a commit's, one an R warp
-      if (b >= T_FAC_FREE && b < T_FAC_FREE + kFacs) count = 16;   // one a warp of both groups
-      if (b >= T_M && b <= T_S) count = 8;                         // one a warp of a group
-      if (b >= T_ITEM_EMPTY && b < T_ITEM_EMPTY + kItems) count = kState ? 18 : 19;  // M and R warps, issuers, scan
+      if (b >= T_EMPTY && b < T_EMPTY + kStages) count = kState ? 1 : 9;        // a commit's, one an R warp
+      if (b >= T_FAC && b < T_FAC + kFacs) count = scans;
+      if (b >= T_FAC_FREE && b < T_FAC_FREE + kFacs) count = kState ? 8 : 16;   // one a warp of a group, of both
+      if (b >= T_M && b <= T_S) count = 8;                                      // one a warp of a group
+      if (kState && b >= S_FREE && b < S_FREE + 2) count = 16;
+      // both groups' warps, issuers, scans
+      if (b >= T_ITEM_EMPTY && b < T_ITEM_EMPTY + kItems) count = 16 + (kState ? 1 : 2) + scans;
       mbar_init(&c->bar[b], count);
     }
     c->abort = 0;
@@ -1002,27 +1140,59 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid
     fence_mbar_init();
     prefetch_tensormap(&p.tm_x);
     prefetch_tensormap(&p.tm_b);
-    prefetch_tensormap(&p.tm_c);
-    prefetch_tensormap(&p.tm_y);
+    if (!kState) {
+      prefetch_tensormap(&p.tm_c);
+      prefetch_tensormap(&p.tm_y);
+    }
   }
-  if (warp == 16) tmem_alloc(&c->tmem_base, 512);
+  if (threadIdx.x >> 5 == 16) tmem_alloc(&c->tmem_base, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = c->tmem_base;
-  if (warp < 8) run_mgroup<K, PARTS, kState>(p, sm, c, tbase);
-  else if (warp < 16) run_rgroup<ST, K, kState>(p, sm, c, tbase);
-  else if (warp == 16) {
-    if (!kState) run_output<K>(p, sm, c, tbase);
-  } else if (warp == 17) run_loader<K, kState>(p, sm, c);
-  else if (warp == 18) run_scan(p, c);
-  else run_state<K, PARTS, kState>(sm, c, tbase);
+  return true;
+}
+__device__ __forceinline__ void tc_end(const ScanParams& p, uint32_t tbase) {
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) tmem_dealloc(tbase, 512);
+  if (threadIdx.x >> 5 == 16) tmem_dealloc(tbase, 512);
   if (threadIdx.x == 0) KDA_DEBUG_FOLD(p.status);
+}
+
+template <typename ST, int K>
+__global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid_constant__ ScanParams p) {
+  constexpr int PARTS = sizeof(ST) == 4 ? 3 : 2;
+  uint8_t* sm = ssm_smem;
+  Ctl* c = ctl();
+  const int warp = threadIdx.x >> 5;
+  if (!tc_begin<false>(p, c)) return;
+  const uint32_t tbase = c->tmem_base;
+  if (warp < 8) run_mgroup<PARTS>(p, sm, c, tbase);
+  else if (warp < 16) run_rgroup<ST, K>(p, sm, c, tbase);
+  else if (warp == 16) run_output<K>(p, sm, c, tbase);
+  else if (warp == 17) run_loader<K, false>(p, sm, c);
+  else if (warp == 18) run_scan(p, c);
+  else run_state<K, PARTS>(sm, c, tbase);
+  tc_end(p, tbase);
+}
+
+template <int K, int PARTS>
+__global__ void __launch_bounds__(kTcThreads, 1) ssm_states_tc_kernel(const __grid_constant__ ScanParams p) {
+  uint8_t* sm = ssm_smem;
+  Ctl* c = ctl();
+  const int warp = threadIdx.x >> 5;
+  if (*p.entries == 0) return;  // no sequence was cut
+  if (!tc_begin<true>(p, c)) return;
+  const uint32_t tbase = c->tmem_base;
+  if (warp < 16) {
+    run_weighted<K, PARTS>(p, sm, c, tbase);
+  } else if (warp == 16) {
+    if (p.V == 64) run_suffixes(p, c, 1);
+  } else if (warp == 17) run_loader<K, true>(p, sm, c);
+  else if (warp == 18) run_suffixes(p, c, 0);
+  else run_sums<K, PARTS>(sm, c, tbase);
+  tc_end(p, tbase);
 }
 
 // ---- host ----------------------------------------------------------------------------------------
@@ -1051,9 +1221,7 @@ bool tc_map(CUtensorMap* m, const void* base, int64_t T, int64_t cols, int64_t p
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename ST, int K, bool kState>
-cudaError_t launch_scan(const ScanParams& p, int grid, cudaStream_t st) {
-  auto kern = ssm_scan_tc_kernel<ST, K, kState>;
+cudaError_t launch_tc(void (*kern)(ScanParams), const ScanParams& p, int grid, cudaStream_t st) {
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
   if (err != cudaSuccess) return err;
   kern<<<grid, kTcThreads, kTcSmem, st>>>(p);
@@ -1073,7 +1241,7 @@ cudaError_t launch_all(ScanParams& p, const SsmArgs& a, cudaStream_t st) {
   if (!plan.lists) {  // the sequences in their order; the header starts at zero
     p.next_item = &reinterpret_cast<PlanHdr*>(a.ws)->next_full;
     cudaError_t err = cudaMemsetAsync(a.ws, 0, sizeof(WsHeader), st);
-    return err == cudaSuccess ? launch_scan<ST, K, false>(p, grid, st) : err;
+    return err == cudaSuccess ? launch_tc(ssm_scan_tc_kernel<ST, K>, p, grid, st) : err;
   }
   cudaError_t err = launch_ssm_plan(plan, a, st);
   if (err != cudaSuccess) return err;
@@ -1083,14 +1251,14 @@ cudaError_t launch_all(ScanParams& p, const SsmArgs& a, cudaStream_t st) {
     p.list = plan.state;
     p.entries = &plan.hdr->n_state;
     p.next_item = &plan.hdr->next_state;
-    err = launch_scan<ST, K, true>(p, gpu_sms(), st);
+    err = launch_tc(ssm_states_tc_kernel<K, sizeof(ST) == 4 ? 3 : 2>, p, gpu_sms(), st);
     if (err == cudaSuccess) err = launch_ssm_combine(plan, a, st);
     if (err != cudaSuccess) return err;
   }
   p.list = plan.full;
   p.entries = &plan.hdr->n_full;
   p.next_item = &plan.hdr->next_full;
-  return launch_scan<ST, K, false>(p, plan.cap > 0 ? gpu_sms() : grid, st);
+  return launch_tc(ssm_scan_tc_kernel<ST, K>, p, plan.cap > 0 ? gpu_sms() : grid, st);
 }
 
 }  // namespace
