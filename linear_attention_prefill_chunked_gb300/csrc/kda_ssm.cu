@@ -289,15 +289,28 @@ cudaError_t decode_types(const SsmArgs& a, cudaStream_t st) {
   return a.d.head_v_dim == 128 ? decode_kv<QT, ST, 64, 128>(a, st) : decode_kv<QT, ST, 64, 64>(a, st);
 }
 
-// Blocks that run at once: two an SM (256 threads of 128 registers).
-int simt_workers() { return 2 * gpu_sms(); }
 int simt_items(const kda_desc_t& d) { return d.num_v_heads * (d.head_v_dim / (d.head_k_dim == 128 ? 32 : 64)); }
+// Blocks an SM. Two have hardly more throughput than one (106 ns a token against 115), and the order in
+// which a grid's blocks reach the SMs pairs some while other SMs stay empty: 1024 tokens of 64 heads, 128
+// blocks of a longer grid, took 219 us against 120 us. So a block has its SM alone, by the shared memory
+// it asks for (8192 tokens of those heads: 940 us, in pairs 1247), unless there are several rounds of them
+// (32 sequences, 4096 tokens: 396 us in pairs, 488 alone).
+int simt_per_sm(const kda_desc_t& d) { return (int64_t)d.num_seqs * simt_items(d) >= 4ll * gpu_sms() ? 2 : 1; }
+int simt_workers(const kda_desc_t& d) { return simt_per_sm(d) * gpu_sms(); }
+constexpr int kAloneSmem = 120 * 1024;  // more than half of an SM's
+
 
 template <typename QT, typename ST, int K, bool kState>
 cudaError_t scan_pass(const SsmArgs& a, int64_t entries, const SimtLists& lists, cudaStream_t st) {
   const int64_t blocks = entries * simt_items(a.d);  // entries outermost: those not there leave last
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  ssm_scan_simt_kernel<QT, ST, K, kState><<<(unsigned)blocks, kScanThreads, 0, st>>>(
+  auto kern = ssm_scan_simt_kernel<QT, ST, K, kState>;
+  const int smem = simt_per_sm(a.d) == 1 ? kAloneSmem : 0;
+  if (smem) {
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+  }
+  kern<<<(unsigned)blocks, kScanThreads, smem, st>>>(
       a.in, (const ST*)a.state_in, a.idx, (ST*)a.state_out, a.cu, (QT*)a.y, a.status, a.d.num_seqs,
       a.d.total_tokens, a.d.num_v_heads, a.d.num_k_heads, a.d.head_v_dim, a.d.num_slots, a.slot_stride,
       lists);
@@ -306,7 +319,7 @@ cudaError_t scan_pass(const SsmArgs& a, int64_t entries, const SimtLists& lists,
 
 template <typename QT, typename ST, int K>
 cudaError_t scan_k(const SsmArgs& a, cudaStream_t st) {
-  const SsmPlan p = ssm_plan(a, simt_items(a.d), simt_workers(), kSimtMinPart);
+  const SsmPlan p = ssm_plan(a, simt_items(a.d), simt_workers(a.d), kSimtMinPart);
   if (p.cap == 0)
     return scan_pass<QT, ST, K, false>(a, a.d.num_seqs, SimtLists{nullptr, nullptr, nullptr, nullptr}, st);
   cudaError_t err = launch_ssm_plan(p, a, st);
@@ -332,7 +345,7 @@ cudaError_t launch_ssm_decode(const SsmArgs& a, cudaStream_t st) {
 }
 
 size_t ssm_simt_workspace(const kda_desc_t& d) {
-  return ssm_plan_workspace(d, simt_items(d), simt_workers());
+  return ssm_plan_workspace(d, simt_items(d), simt_workers(d));
 }
 
 cudaError_t launch_ssm_simt(const SsmArgs& a, cudaStream_t st) {

@@ -13,12 +13,12 @@ namespace {
 // in the list's order: an item claimed last is a short one.
 //
 // Cuts. A worker's share is L = chunks x items a sequence / workers. A sequence of many more than
-// S = max(1.2 L, min_part) chunks would outlast the others. Parts of S chunks take their pass over the
-// states and then the whole, ~1.8 S in all, and two more launches: a sequence of more than 2 S + 4 chunks
-// is cut into parts of at most S. A pass that forms states
-// only (some 60 % of a chunk's time) takes all parts but the last from a zero state, a kernel adds up
-// S_end = decay S_start + S_local along the parts, and then all parts run at once, each from its own
-// start. S and so the parts' number follow from the lengths, the heads and the GPU alone: parts of more
+// S = max(1.2 L, min_part) chunks would outlast the others: one of more than 1.5 S + 4 is cut into parts
+// of at most S. A pass that forms states only (0.45 of a chunk's time on the tensor cores, 0.6 on CUDA
+// cores) takes all parts but the last, each from a zero state; a kernel adds up S_end = decay S_start +
+// S_local along the parts; then all parts run at once, each from its own start. One sequence of 64 heads
+// takes 125 us for 8192 tokens (of 276 uncut), 50 us for 2048 (74); 1024 tokens stay whole (44, cut 51).
+// S and so the parts' number follow from the lengths, the heads and the GPU alone: parts of more
 // than S / 2 chunks, at most 2 / 1.2 CTAs' worth of items, for which the scratch has room.
 constexpr int kPlanThreads = 1024, kKeys = 1024;
 
@@ -56,7 +56,7 @@ ssm_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ idx,
   const unsigned long long work = s_chunks * (unsigned)items;
   int64_t S = (int64_t)((work * 6 + 5ull * workers - 1) / (5ull * workers));
   if (S < min_part) S = min_part;
-  const int64_t most = cap == 0 ? INT64_MAX : 2 * S + 4;  // chunks of a sequence that stays whole
+  const int64_t most = cap == 0 ? INT64_MAX : S + S / 2 + 4;  // chunks of a sequence that stays whole
   auto key = [](int64_t len) { return (int)(len < kKeys - 1 ? len : kKeys - 1); };
   for (int n = tid; n < N; n += kPlanThreads) {
     const int64_t c = chunks_of(n);
@@ -196,7 +196,7 @@ SsmPlan ssm_plan(const SsmArgs& a, int items, int workers, int min_part) {
   SsmPlan p;
   // Where no sequence can be long enough to be cut, none is long enough for its place in the order to
   // matter: the sequences are taken as they come, in one launch.
-  p.lists = a.ws_bytes >= l.lists_end && a.d.total_tokens > (int64_t)(2 * min_part + 4) * kSsmChunk;
+  p.lists = a.ws_bytes >= l.lists_end && a.d.total_tokens > (int64_t)(min_part + min_part / 2 + 4) * kSsmChunk;
   p.cap = p.lists && a.ws_bytes >= l.end ? l.cap : 0;
   p.items = items;
   p.workers = workers;

@@ -59,7 +59,7 @@ constexpr int kMThreads = 256, kRThreads = 256;
 constexpr int kTcThreads = kMThreads + kRThreads + 128;
 constexpr int kFacs = 3;        // chunks of steps and decays in flight
 constexpr int kItems = 4;       // claimed items in flight
-constexpr int kMinPart = 12;    // chunks a sequence is cut into parts of at least, or so
+constexpr int kMinPart = 8;     // chunks a sequence is cut into parts of at least, or so
 
 // ---- shared memory (offsets from a 1024-aligned base) -----------------------------------
 constexpr uint32_t kTileBytes = 16384;               // [2 halves][64 rows][128 B]
