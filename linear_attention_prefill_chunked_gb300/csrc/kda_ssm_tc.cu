@@ -32,11 +32,17 @@
 // and x and y read and written by TMEM lane, two bytes at a time, 3350 wavefronts a chunk): x' goes
 // from registers to TMEM, and x and y move as 8 x 8 blocks transposed on the way (ldmatrix, stmatrix).
 //
-// Warps 0-7 (M group): M from the scores, and x'. Warps 8-15 (R group): the state's decay and bf16 copy, the output. Warps 16 and 19 issue the
-// tcgen05 products, warp 17 claims items and moves tiles (TMA), warp 18 scans the steps. What orders them are
-// mbarriers, each wait bounded (a timeout sets KDA_DEVICE_PIPE_TIMEOUT, stops the loads, lets what was
-// issued finish and returns). Only T_SU -> R -> T_S -> products of C and x' -> T_SU is a chain from
-// chunk to chunk; scans, scores, M and the arithmetic of x' run ahead of it.
+// Warps 0-7 (M group): M from the scores, and x'. Warps 8-15 (R group): the state's decay and bf16 copy,
+// the output. Warps 16 and 19 issue the tcgen05 products, warp 17 claims items and moves tiles (TMA),
+// warp 18 scans the steps. What orders them are mbarriers, each wait bounded (a timeout sets
+// KDA_DEVICE_PIPE_TIMEOUT, stops the loads, lets what was issued finish and returns). Only T_SU -> R ->
+// T_S -> products of C and x' -> T_SU is a chain from chunk to chunk; scans, scores, M and the arithmetic
+// of x' run ahead of it.
+//
+// 32768 tokens of 32 heads (V = 128) take 235 us, against 109 us for the bytes at a copy's rate: a chunk
+// is 3800 cycles, of which the products take 2100 (their pipe gives one M = 128, N = 64 step of 16 in 52
+// cycles, N = 128 in 71) and the chain of barriers, TMEM reads and writes between them the rest; the
+// schedulers issue on 55 % of the cycles.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -68,8 +74,8 @@ constexpr uint32_t OFF_ST = 8192;
 constexpr uint32_t OFF_C = 0, OFF_B = kTileBytes, OFF_X = 2 * kTileBytes;  // within a stage
 constexpr uint32_t kStageBytes = 3 * kTileBytes;
 constexpr uint32_t OFF_Z1 = OFF_ST + kStages * kStageBytes;  // and the half after
-constexpr uint32_t OFF_M = OFF_Z1 + 8192;            // [2 heads][64 t][64 s] (K-major B)
-constexpr uint32_t OFF_CTL = OFF_M + kTileBytes;
+constexpr uint32_t OFF_M = OFF_Z1 + 8192;            // [2 by chunk parity][2 heads][64 t][64 s] (K-major B)
+constexpr uint32_t OFF_CTL = OFF_M + 2 * kTileBytes;
 
 // ---- TMEM columns -------------------------------------------------------------------------
 constexpr uint32_t TM_S = 0;     // S^T fp32 (128)
@@ -110,7 +116,7 @@ struct Factors {
   float same[2][kL];   // log d_s - cl: + cl_t is the weight of s for t in its half
   float later[2][kL];  // log d_s + log-decay after s to its half's end: + cl_t for t in the next
   float e[2][kL];      // decay from the chunk's start through t
-  float second[2];     // log-decay of the second half
+  float to_end[2][kL];  // weight of s in the state after the chunk
   float dec[2];        // decay of the chunk
 };
 
@@ -154,12 +160,16 @@ __device__ __forceinline__ bool tc_aborted(const Ctl* c) {
 extern __shared__ __align__(1024) uint8_t ssm_smem[];
 __device__ __forceinline__ Ctl* ctl() { return reinterpret_cast<Ctl*>(ssm_smem + OFF_CTL); }
 
-// Bounded wait; after a timeout anywhere in the CTA every wait gives up soon (false). The hardware
-// suspends the thread in try_wait until the phase completes or some microseconds have passed, so that
-// a waiting warp takes few issue slots; a limit shorter than that polls instead. Out of line, as is
+// Bounded wait; after a timeout anywhere in the CTA every wait gives up soon (false). A few tests catch
+// what completes at once (252 -> 239 us for 32768 tokens of 32 heads, with the M blocks of 32 columns);
+// then the hardware suspends the thread in try_wait until the phase completes or some microseconds have
+// passed, so that a waiting warp takes few issue slots; a limit shorter than that polls instead. Out of line, as is
 // what else the chunk loop runs at several places: the warps of a CTA run five programs at once, and
 // their instruction cache is what they are short of (see the launch).
 __device__ __noinline__ bool tc_wait_slow(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i)
+    if (mbar_test_wait(bar, parity)) return true;
   Ctl* c = ctl();
   uint64_t t0 = 0;
   for (;;) {
@@ -454,14 +464,14 @@ __device__ void run_output(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       ok = tc_wait2({T_M + (int)(j & 1), (j >> 1) & 1}, {T_FULL + (int)st, (j / kStages) & 1});
       if (!ok) break;
       tc_fence_after();
-      const uint32_t ym = tbase + TM_YM + (j & 1) * 64;
+      const uint32_t ym = tbase + TM_YM + (j & 1) * 64, m = sbase + OFF_M + (j & 1) * kTileBytes;
       // the second half of A: x's, or zeros where it is another head's
       const uint32_t x0 = stage + OFF_X;
       issue_ss(ym, desc128(x0, p.V == 128 ? 8192 : sbase + OFF_Z1 - x0, 1024), 2048,
-               desc128(sbase + OFF_M, 16, 1024), 32, id_m, 0);
+               desc128(m, 16, 1024), 32, id_m, 0);
       if (second)
         issue_ss(ym, desc128(sbase + OFF_Z0, x0 + 8192 - (sbase + OFF_Z0), 1024), 2048,
-                 desc128(sbase + OFF_M + 8192, 16, 1024), 32, id_m, 1);
+                 desc128(m + 8192, 16, 1024), 32, id_m, 1);
       mma_commit(&c->bar[T_MX + (j & 1)]);
       ok = tc_wait(T_S, j & 1);
       if (!ok) break;
@@ -596,10 +606,10 @@ __device__ __forceinline__ void scan_steps(Factors* f, const float (&d)[2][2], c
     *reinterpret_cast<float2*>(&f->same[h][t]) = make_float2(l0 - c0, l1 - c1);
     *reinterpret_cast<float2*>(&f->later[h][t]) = make_float2(l0 + (after + g1[h]), l1 + after);
     *reinterpret_cast<float2*>(&f->e[h][t]) = make_float2(ex2(pre + c0), ex2(pre + c1));
-    if (lane == 0) {
-      f->second[h] = second;
-      f->dec[h] = ex2(first + second);
-    }
+    const float then = lane < 16 ? second : 0.f;
+    *reinterpret_cast<float2*>(&f->to_end[h][t]) =
+        make_float2(ex2(l0 + (after + g1[h]) + then), ex2(l1 + after + then));
+    if (lane == 0) f->dec[h] = ex2(first + second);
   }
 }
 
@@ -699,32 +709,33 @@ __device__ __forceinline__ void put_half(uint32_t taddr, const uint32_t (&parts)
   for (int q = 0; q < PARTS; ++q) tmem_st_16x128_x4(taddr + q * 32, parts[q]);
 }
 
-// A 16 x 16 block of M, 8 elements a lane: the scores times their weights, rounded into the M tile at
-// `at` (the lane's row of the four 8 x 8 blocks). `col`: the lane's columns' part of the log-weights;
-// diag: columns after the row are not weighted (their weight may be anything) but zero.
-__device__ __forceinline__ void weigh_block(uint32_t tmem, const float* col, float cl0, float cl1, bool diag,
-                                            uint32_t at, int lane) {
-  float g[8];
-  tmem_ld_16x256_x2(tmem, g);
-  uint32_t o[4];
-  float w[8];
+// 16 x 32 elements of M, 16 a lane: the scores times their weights, rounded into the M tile at `at0` and
+// `at1` (the lane's row of the 8 x 8 blocks, of either 16 columns). `col`: the lane's columns' part of the
+// log-weights; `row`: the block's first row, from its first column on: columns after the row are not
+// weighted (their weight may be anything) but zero.
+__device__ __forceinline__ void weigh_block(uint32_t tmem, const float* col, float cl0, float cl1, int row,
+                                            uint32_t at0, uint32_t at1, int lane) {
+  float g[16];
+  tmem_ld_16x256_x4(tmem, g);
+  float w[16];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
+  for (int c = 0; c < 4; ++c) {
     const float2 q = *reinterpret_cast<const float2*>(col + c * 8);
     w[4 * c] = ex2(cl0 + q.x);
     w[4 * c + 1] = ex2(cl0 + q.y);
     w[4 * c + 2] = ex2(cl1 + q.x);
     w[4 * c + 3] = ex2(cl1 + q.y);
   }
+  const int last = row + (lane >> 2) - 2 * (lane & 3);
   tmem_ld_wait();
+  uint32_t o[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {  // column 8 (i / 4) + 2 (lane % 4) + i % 2, row lane / 4 + 8 (i / 2 % 2)
-    const int over = (i >> 2) * 8 + 2 * (lane & 3) + (i & 1) - ((lane >> 2) + ((i >> 1) & 1) * 8);
-    g[i] = diag && over > 0 ? 0.f : g[i] * w[i];
-  }
+  for (int i = 0; i < 16; ++i)  // column 8 (i / 4) + 2 (lane % 4) + i % 2, row lane / 4 + 8 (i / 2 % 2)
+    g[i] = (i >> 2) * 8 + (i & 1) - ((i >> 1) & 1) * 8 > last ? 0.f : g[i] * w[i];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(g[2 * i], g[2 * i + 1]);
-  stsm_x4(at, o[0], o[1], o[2], o[3]);
+  for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(g[2 * i], g[2 * i + 1]);
+  stsm_x4(at0, o[0], o[1], o[2], o[3]);
+  stsm_x4(at1, o[4], o[5], o[6], o[7]);
 }
 
 template <int PARTS>
@@ -734,6 +745,7 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
   // the columns of M after the rows' half are never written again, the zero rows never at all
   for (uint32_t i = threadIdx.x; i < kTileBytes / 16; i += kMThreads) {
     *reinterpret_cast<uint4*>(sm + OFF_M + i * 16) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(sm + OFF_M + kTileBytes + i * 16) = make_uint4(0, 0, 0, 0);
     *reinterpret_cast<uint4*>(sm + (i < 512 ? OFF_Z0 + i * 16 : OFF_Z1 + (i - 512) * 16)) = make_uint4(0, 0, 0, 0);
   }
   fence_async_smem();
@@ -741,9 +753,10 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
 
   // x' of 32 value columns (TMEM lanes of the warp's quadrant) and 32 tokens: where the lane's row of
   // the 8 x 8 blocks lies in the x tile, for tokens 0-15 and columns 0-15 of those
-  // and M's rows [16 quad, + 16): one head a warp, or every other column block of the one head
+  // and M's rows [16 quad, + 16): one head a warp, or one half of the columns of the one head. (Two M
+  // tiles in turn, so that M does not wait for the product of the chunk before: 239 -> 235 us.)
   const int quad = warp & 3, th = warp >> 2;
-  const int hm = heads == 2 ? th : 0, sb0 = heads == 2 ? 0 : th, sbn = heads == 2 ? 1 : 2;
+  const int hm = heads == 2 ? th : 0, half0 = heads == 2 ? 0 : th, halfn = heads == 2 ? 1 : 2;
   const uint32_t mrow = quad * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
   const uint32_t m0 = smem_u32(sm) + OFF_M + hm * 8192 + mrow * 128;
   const uint32_t row0 = th * 4096 + ((lane >> 4) << 10) + (lane & 7) * 128;
@@ -759,10 +772,10 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       const uint32_t st = j % kStages, par = j & 1, fi = j % kFacs;
       uint8_t* stage = sm + OFF_ST + st * kStageBytes;
       const Factors* f = &c->fac[fi];
-      // (the scores: their tiles have landed. j > 0: the product that read the last M is done.)
+      // (the scores: their tiles have landed. j > 1: the product that read the M before last is done.)
       const At g{T_G + (int)par, (j >> 1) & 1};
       if (!all_lanes(tc_wait3({T_FAC + (int)fi, (j / kFacs) & 1}, g,
-                              j > 0 ? At{T_MX + (int)(par ^ 1), ((j - 1) >> 1) & 1} : g) &&
+                              j > 1 ? At{T_MX + (int)par, ((j >> 1) - 1) & 1} : g) &&
                      tc_wait(T_FULL + st, (j / kStages) & 1)))
         return;
       tc_fence_after();
@@ -781,22 +794,20 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         __syncwarp();
       }
       const float cl0 = f->cl[hm][quad * 16 + (lane >> 2)], cl1 = f->cl[hm][quad * 16 + (lane >> 2) + 8];
-      const uint32_t tg = tbase + TM_YM + par * 64 + ((uint32_t)(quad * 32) << 16);
+      const uint32_t mt = m0 + par * kTileBytes, tg = tbase + TM_YM + par * 64 + ((uint32_t)(quad * 32) << 16);
 #pragma unroll 1
-      for (int sb = sb0; sb <= quad; sb += sbn)
-        weigh_block(tg + sb * 16, (sb >> 1 == quad >> 1 ? f->same[hm] : f->later[hm]) + sb * 16 + 2 * (lane & 3),
-                    cl0, cl1, sb == quad, m0 + (((sb * 2 + (lane >> 4)) ^ (lane & 7)) << 4), lane);
+      for (int half = half0; half <= quad >> 1; half += halfn)
+        weigh_block(tg + half * 32, (half == quad >> 1 ? f->same[hm] : f->later[hm]) + half * 32 + 2 * (lane & 3),
+                    cl0, cl1, quad * 16 - half * 32, mt + (((half * 4 + (lane >> 4)) ^ (lane & 7)) << 4),
+                    mt + (((half * 4 + 2 + (lane >> 4)) ^ (lane & 7)) << 4), lane);
       tc_fence_before();
       fence_async_smem();
       warp_arrive(&c->bar[T_M + par]);
       // x' into registers, and to TMEM once the product that read the last one is done
       float2 w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 q = *reinterpret_cast<const float2*>(&f->later[hx][th * 32 + i * 8 + 2 * (lane & 3)]);
-        const float then = th == 0 ? f->second[hx] : 0.f;
-        w[i] = make_float2(ex2(q.x + then), ex2(q.y + then));
-      }
+      for (int i = 0; i < 4; ++i)
+        w[i] = *reinterpret_cast<const float2*>(&f->to_end[hx][th * 32 + i * 8 + 2 * (lane & 3)]);
       uint32_t raw[4][4], parts[PARTS][8];
       load_x(raw, smem_u32(stage) + xoff, col0);
       split_half<PARTS>(raw[0], raw[1], w, parts);
