@@ -127,6 +127,8 @@ ssm_scan_simt_kernel(kda_ssm_inputs_t in, const ST* state_in, const int32_t* __r
   __shared__ float2 s_step[kStage];         // step and decay of a token
 
   const int tid = threadIdx.x, tiles = V / VT;
+  if (kState) grid_release();
+  grid_wait();
   const int e = (int)(blockIdx.x / (unsigned)(H * tiles)), q = (int)(blockIdx.x % (unsigned)(H * tiles));
   const int h = q / tiles, v0 = q % tiles * VT;
   Entry en{e, 0, 0, -1, 1, {0, 0, 0}};
@@ -310,11 +312,10 @@ cudaError_t scan_pass(const SsmArgs& a, int64_t entries, const SimtLists& lists,
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
   }
-  kern<<<(unsigned)blocks, kScanThreads, smem, st>>>(
-      a.in, (const ST*)a.state_in, a.idx, (ST*)a.state_out, a.cu, (QT*)a.y, a.status, a.d.num_seqs,
-      a.d.total_tokens, a.d.num_v_heads, a.d.num_k_heads, a.d.head_v_dim, a.d.num_slots, a.slot_stride,
-      lists);
-  return cudaGetLastError();
+  return launch_pass(kern, dim3((unsigned)blocks), kScanThreads, smem, lists.list != nullptr, st, a.in,
+                     (const ST*)a.state_in, a.idx, (ST*)a.state_out, a.cu, (QT*)a.y, a.status, a.d.num_seqs,
+                     a.d.total_tokens, a.d.num_v_heads, a.d.num_k_heads, a.d.head_v_dim, a.d.num_slots,
+                     a.slot_stride, lists);
 }
 
 template <typename QT, typename ST, int K>

@@ -31,6 +31,7 @@ ssm_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ idx,
   __shared__ unsigned long long s_chunks;
   __shared__ uint32_t s_parts, s_splits;
   const int tid = threadIdx.x;
+  grid_release();
   check_all(&hdr->status, cu, idx, N, T, T, idx ? num_slots : 0);
   if (tid == 0) {
     s_chunks = 0;
@@ -122,6 +123,8 @@ __global__ void __launch_bounds__(256)
 ssm_combine_kernel(const PlanHdr* __restrict__ hdr, const Split* __restrict__ splits, float* scratch,
                    const float* __restrict__ decay, const ST* __restrict__ state_in, int64_t slot_stride, int H,
                    int KV) {
+  grid_release();
+  grid_wait();
   const int64_t whole = (int64_t)H * KV;
   const int64_t at = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
   if (at >= whole) return;
@@ -222,13 +225,10 @@ cudaError_t launch_ssm_combine(const SsmPlan& p, const SsmArgs& a, cudaStream_t 
   const int64_t whole = (int64_t)a.d.num_v_heads * kv;
   const dim3 grid((unsigned)((whole / 4 + 255) / 256), (unsigned)std::min(p.cap / 2, 16));
   if (a.d.state_dtype == KDA_BF16)
-    ssm_combine_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p.hdr, p.splits, p.scratch, p.decay,
-                                                            (const __nv_bfloat16*)a.state_in, a.slot_stride,
-                                                            a.d.num_v_heads, kv);
-  else
-    ssm_combine_kernel<float><<<grid, 256, 0, st>>>(p.hdr, p.splits, p.scratch, p.decay, (const float*)a.state_in,
-                                                    a.slot_stride, a.d.num_v_heads, kv);
-  return cudaGetLastError();
+    return launch_pass(ssm_combine_kernel<__nv_bfloat16>, grid, 256, 0, true, st, p.hdr, p.splits, p.scratch,
+                       p.decay, (const __nv_bfloat16*)a.state_in, a.slot_stride, a.d.num_v_heads, kv);
+  return launch_pass(ssm_combine_kernel<float>, grid, 256, 0, true, st, p.hdr, p.splits, p.scratch, p.decay,
+                     (const float*)a.state_in, a.slot_stride, a.d.num_v_heads, kv);
 }
 
 }  // namespace kda

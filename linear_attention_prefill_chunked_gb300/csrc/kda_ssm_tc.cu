@@ -1127,7 +1127,9 @@ __device__ void run_weighted(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t 
 // Barriers and TMEM; false: the CTA leaves.
 template <bool kState>
 __device__ __forceinline__ bool tc_begin(const ScanParams& p, Ctl* c) {
+  if (kState) grid_release();
   if (smem_u32(ssm_smem) & 1023u) {  // the swizzled tiles need it; the window starts so without static smem
+    grid_wait();
     if (threadIdx.x == 0) raise_status(p.status, KDA_DEVICE_PIPE_TIMEOUT);
     return false;
   }
@@ -1160,6 +1162,7 @@ __device__ __forceinline__ bool tc_begin(const ScanParams& p, Ctl* c) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_wait();
   return true;
 }
 __device__ __forceinline__ void tc_end(const ScanParams& p, uint32_t tbase) {
@@ -1193,10 +1196,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_states_tc_kernel(const __gr
   uint8_t* sm = ssm_smem;
   Ctl* c = ctl();
   const int warp = threadIdx.x >> 5;
-  if (*p.entries == 0) return;  // no sequence was cut
   if (!tc_begin<true>(p, c)) return;
   const uint32_t tbase = c->tmem_base;
-  if (warp < 16) {
+  if (*p.entries == 0) {  // no sequence was cut
+  } else if (warp < 16) {
     run_weighted<K, PARTS>(p, sm, c, tbase);
   } else if (warp == 16) {
     if (p.V == 64) run_suffixes(p, c, 1);
@@ -1235,8 +1238,7 @@ bool tc_map(CUtensorMap* m, const void* base, int64_t T, int64_t cols, int64_t p
 cudaError_t launch_tc(void (*kern)(ScanParams), const ScanParams& p, int grid, cudaStream_t st) {
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
   if (err != cudaSuccess) return err;
-  kern<<<grid, kTcThreads, kTcSmem, st>>>(p);
-  return cudaGetLastError();
+  return launch_pass(kern, dim3((unsigned)grid), kTcThreads, kTcSmem, p.list != nullptr, st, p);
 }
 
 int items_a_sequence(const kda_desc_t& d) {
