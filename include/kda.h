@@ -292,7 +292,7 @@ kda_status_t kda_chunk_prefill_noalloc(const kda_desc_t *desc, const void *q, co
                                        void *o, cudaStream_t stream);
 
 /*
- * Bound of the internal pipeline waits of the tensor-core prefill, for launches made
+ * Bound of the internal pipeline waits of the tensor-core prefill and scan, for launches made
  * after the call (process-wide; 0 restores the default of 2 seconds; more than 2 s is
  * KDA_ERR_INVALID_ARGUMENT).  The pages have no counterpart: it is the watchdog of this
  * library's own kernels.  Every wait between the kernel's producer and consumer warps

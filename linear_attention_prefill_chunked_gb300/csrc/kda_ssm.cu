@@ -17,7 +17,7 @@ KDA_DEBUG_FLAG_DEFINE();
 // Grid (rows, heads): rows and heads on axes of their own, rows on grid.x.  A block of 256 threads
 // holds a head's K x V state in registers, V/4 threads a row of 16-byte accesses, the row groups
 // splitting K; all state loads are issued before anything is computed.  y's sum over K goes through
-// shared memory.
+// shared memory.  1024 rows of 32 heads of 128 x 128 in fp32, 4.3 GB, take 636 us: a copy's rate.
 constexpr int kDecThreads = 256;
 
 template <typename QT, typename ST, int K, int V>
