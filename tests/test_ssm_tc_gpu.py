@@ -8,7 +8,7 @@ import torch
 import linear_attention_prefill_chunked_gb300 as kda
 from linear_attention_prefill_chunked_gb300 import api, layer
 from tests import _layer_ref as ref
-from tests.test_ssm_gpu import _close, _inputs, _scan, _want
+from tests.test_ssm_gpu import S_BOUND, Y_BOUND, _close, _inputs, _scan, _want
 
 pytestmark = pytest.mark.gpu
 BF, F32 = ref.BF, ref.F32
@@ -39,6 +39,33 @@ def test_cut_sequences(lens, H, G, K, V, sdt):
     pool[idx.long()] = d["h0"]
     yp, _ = _scan(d, lens, state=pool, state_indices=idx)
     assert torch.equal(yp, y) and torch.equal(pool[idx.long()], fin)
+
+
+@pytest.mark.parametrize("memory", ["endless", "short", "none", "padded"])
+@pytest.mark.parametrize("H,G,K,V", [(3, 1, 128, 64), (1, 1, 128, 128)])
+def test_cut_memories(memory, H, G, K, V):
+    """Parts whose decay is hardly any, whose decay leaves nothing, and with most steps at zero."""
+    lens = [4500, 1500, 70]
+    d = _inputs(lens, H, G, K, V, BF, seed=H + 90, a_max=1.5)
+    if memory == "endless":
+        d["dt"] -= 7  # 4500 tokens keep some 0.9 of the first
+        d["h0"].zero_()
+    elif memory == "short":
+        d["dt"] += 2
+    elif memory == "none":  # decays below the smallest fp32 number within a few tokens
+        d["dt"] += 40
+    else:  # steps of zero, as of padded tokens: softplus underflows
+        d["dt"][torch.rand(sum(lens), generator=torch.Generator().manual_seed(1)).cuda() < 0.7] = -300
+    want, wfin, _ = _want(d, lens, list(d["h0"]))
+    y, fin = _scan(d, lens, state=d["h0"])
+    assert kda.read_device_status(kda.ssm_scan.last_workspace) == 0
+    assert ref.rel(y, want) <= Y_BOUND[BF]
+    for i, n in enumerate(lens):
+        # every sum of 16 tokens' products, in three parts, is cut off to 24 bits once more
+        adds = 3 * (n + 15) // 16
+        for h in range(H):
+            e = ref.rel(fin[i, h], wfin[i][h])
+            assert e <= 1.5 * S_BOUND[F32] + adds * 2.0 ** -23, (i, h, e)
 
 
 def test_every_workspace_size_gives_the_same_up_to_rounding():
