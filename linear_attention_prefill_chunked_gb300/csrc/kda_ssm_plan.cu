@@ -17,7 +17,7 @@ namespace {
 // of at most S. A pass that forms states only (0.45 of a chunk's time on the tensor cores, 0.6 on CUDA
 // cores) takes all parts but the last, each from a zero state; a kernel adds up S_end = decay S_start +
 // S_local along the parts; then all parts run at once, each from its own start. One sequence of 64 heads
-// takes 125 us for 8192 tokens (of 276 uncut), 50 us for 2048 (74); 1024 tokens stay whole (44, cut 51).
+// takes 115 us for 8192 tokens (of 276 uncut), 50 us for 2048 (74); 1024 tokens stay whole (40, cut 51).
 // S and so the parts' number follow from the lengths, the heads and the GPU alone: parts of more
 // than S / 2 chunks, at most 2 / 1.2 CTAs' worth of items, for which the scratch has room.
 constexpr int kPlanThreads = 1024, kKeys = 1024;

@@ -33,14 +33,14 @@
 // from registers to TMEM, and x and y move as 8 x 8 blocks transposed on the way (ldmatrix, stmatrix).
 //
 // Warps 0-7 (M group): M from the scores, and x'. Warps 8-15 (R group): the state's decay and bf16 copy,
-// the output. Warps 16 and 19 issue the tcgen05 products, warp 17 claims items and moves tiles (TMA),
-// warp 18 scans the steps. What orders them are mbarriers, each wait bounded (a timeout sets
-// KDA_DEVICE_PIPE_TIMEOUT, stops the loads, lets what was issued finish and returns). Only T_SU -> R ->
-// T_S -> products of C and x' -> T_SU is a chain from chunk to chunk; scans, scores, M and the arithmetic
-// of x' run ahead of it.
+// the output. Warps 16 and 19 issue the tcgen05 products, warp 17 scans the steps (its scheduler has the
+// least of M; on the schedulers that have the most, 2 to 4 % slower), warp 18 claims items and moves tiles
+// (TMA). What orders them are mbarriers, each wait bounded (a timeout sets KDA_DEVICE_PIPE_TIMEOUT, stops
+// the loads, lets what was issued finish and returns). Only T_SU -> R -> T_S -> products of C and x' ->
+// T_SU is a chain from chunk to chunk; scans, scores, M and the arithmetic of x' run ahead of it.
 //
-// 32768 tokens of 32 heads (V = 128) take 235 us, against 109 us for the bytes at a copy's rate: a chunk
-// is 3800 cycles, of which the products take 2100 (their pipe gives one M = 128, N = 64 step of 16 in 52
+// 32768 tokens of 32 heads (V = 128) take 232 us, against 109 us for the bytes at a copy's rate: a chunk
+// is ~3800 cycles, of which the products take 2100 (their pipe gives one M = 128, N = 64 step of 16 in 52
 // cycles, N = 128 in 71) and the chain of barriers, TMEM reads and writes between them the rest; the
 // schedulers issue on 55 % of the cycles.
 #include <cudaTypedefs.h>
@@ -319,7 +319,7 @@ __device__ __forceinline__ Item tc_item_warp(const ScanParams& p, Ctl* c, uint32
 }
 
 
-// ---- warp 17: items and tiles ------------------------------------------------------------
+// ---- warp 18: items and tiles ------------------------------------------------------------
 template <int K, bool kState>
 __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
   if (!elect_one()) return;
@@ -442,7 +442,7 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
 // Two warps issue the products, each for one loop from chunk to chunk: a thread takes ~100 cycles a
 // product here, the pipe 52 to 71, and a product never waits for one of the other loop's.
 
-// ---- warp 16: the products of the output ------------------------------------------------------
+// ---- warp 19: the products of the output ------------------------------------------------------
 template <int K>
 __device__ void run_output(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
   if (!elect_one()) return;
@@ -487,7 +487,7 @@ __device__ void run_output(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
   mbar_wait(&c->bar[T_DRAIN], 0);  // the full limit, aborted or not
 }
 
-// ---- warp 19: the state's product, and the scores of the chunk after next ------------------------
+// ---- warp 16: the state's product, and the scores of the chunk after next ------------------------
 template <int K, int PARTS>
 __device__ void run_state(uint8_t* sm, Ctl* c, uint32_t tbase) {
   if (!elect_one()) return;
@@ -554,7 +554,7 @@ __device__ void run_state(uint8_t* sm, Ctl* c, uint32_t tbase) {
   mbar_wait(&c->bar[T_DRAIN + 1], 0);
 }
 
-// ---- warp 18: steps and decays ------------------------------------------------------------------
+// ---- warp 17: steps and decays ------------------------------------------------------------------
 // softplus(x) = max(x, 0) + log(1 + e^-|x|), the logarithm as 2 atanh(u / (2 + u)) with u = e^-|x|:
 // u / (2 + u) <= 1/3, so that seven terms of the series leave a relative error of 2e-8, at small u too.
 // One warp makes the steps of all others' chunks, a thousand dependent cycles with the library's
@@ -973,7 +973,7 @@ __device__ void run_rgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
 // its first: the sum of the log-decays after a chunk is then known when the chunk comes, so that x'
 // can take the decay to the part's end and S is not decayed on the way. No chain is left from chunk to
 // chunk but the accumulator, and no exponent is positive. Both groups make x' (a chunk each, in turn),
-// warps 18 and 16 scan a head each, two buffers hold x' and two S^T. (In the order of time, with S
+// warps 17 and 16 scan a head each, two buffers hold x' and two S^T. (In the order of time, with S
 // decayed every chunk, the pass took as long as the one that makes the outputs.) Chunks are all full: a
 // sequence's last part is not in the list.
 constexpr int S_XFREE = T_MX, S_DONE = T_G, S_FREE = T_EPI;  // x' is read, S complete, S read: by parity
@@ -1184,10 +1184,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_scan_tc_kernel(const __grid
   const uint32_t tbase = c->tmem_base;
   if (warp < 8) run_mgroup<PARTS>(p, sm, c, tbase);
   else if (warp < 16) run_rgroup<ST, K>(p, sm, c, tbase);
-  else if (warp == 16) run_output<K>(p, sm, c, tbase);
-  else if (warp == 17) run_loader<K, false>(p, sm, c);
-  else if (warp == 18) run_scan(p, c);
-  else run_state<K, PARTS>(sm, c, tbase);
+  else if (warp == 16) run_state<K, PARTS>(sm, c, tbase);
+  else if (warp == 17) run_scan(p, c);
+  else if (warp == 18) run_loader<K, false>(p, sm, c);
+  else run_output<K>(p, sm, c, tbase);
   tc_end(p, tbase);
 }
 
@@ -1203,8 +1203,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_states_tc_kernel(const __gr
     run_weighted<K, PARTS>(p, sm, c, tbase);
   } else if (warp == 16) {
     if (p.V == 64) run_suffixes(p, c, 1);
-  } else if (warp == 17) run_loader<K, true>(p, sm, c);
-  else if (warp == 18) run_suffixes(p, c, 0);
+  } else if (warp == 17) run_suffixes(p, c, 0);
+  else if (warp == 18) run_loader<K, true>(p, sm, c);
   else run_sums<K, PARTS>(sm, c, tbase);
   tc_end(p, tbase);
 }
