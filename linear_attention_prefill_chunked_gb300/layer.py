@@ -171,7 +171,9 @@ def _state_pool(state, name, dims, slot_stride):
 
 
 def _stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if stream is None:  # the handle alone: torch.cuda.current_stream() builds an object, 2 us of a call's 20
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream
 
 
 def _empty(stream, shape, dtype, device):
