@@ -28,6 +28,8 @@ constexpr int kConvThreads = kLanes * kStrips;
 // for taps, window and rows in flight, which leaves three warps a scheduler: 309 us for 32768 x 12288
 // (1.6 GB) against 277 us, 5.8 TB/s or 86 % of a copy's rate, with 4 channels, eight rows in flight and
 // three blocks an SM (four blocks: 282 us with four rows in flight, 316 with eight, which then spill).
+// One channel a thread has less in flight, so there five blocks share an SM: 155 us for 16384 x 8193 in
+// bf16 (with three: 189; 8192 channels, four a thread: 99), 227 us in fp32 (with two: 304; 211).
 template <typename T, int VEC> struct Row;
 template <> struct Row<float, 4> {
   using Raw = uint4;
@@ -127,7 +129,7 @@ __device__ __forceinline__ void load_taps(const T* w, const T* bias, int c, floa
 }
 
 template <typename T, int VEC, int W, int kStrip>
-__global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 2 : 3)
+__global__ void __launch_bounds__(kConvThreads, VEC == 1 ? 5 : sizeof(T) == 4 ? 2 : 3)
 conv_prompt_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict__ w,
                    const T* __restrict__ bias, const int32_t* __restrict__ cu, const T* state_in,
                    const int32_t* __restrict__ idx, T* state_out, int64_t slot_stride,
@@ -136,7 +138,7 @@ conv_prompt_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict
   using R = Row<T, VEC>;
   constexpr int H = W - 1;                 // inputs a state holds
   constexpr int kTile = kStrip * kStrips;
-  constexpr int kAhead = sizeof(T) == 4 ? 4 : 8;  // rows in flight while as many are computed
+  constexpr int kAhead = VEC > 1 && sizeof(T) == 4 ? 4 : 8;  // rows in flight while as many are computed
   static_assert(kStrip % kAhead == 0, "a strip is whole groups of rows");
   constexpr int kSpan = kTile + W - 2;     // tokens a block may own (see above)
   __shared__ int s_seq[kSpan];             // sequence of each token, -1: none
