@@ -256,6 +256,10 @@ conv_prompt_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict
       // the first W-1 tokens of a sequence belong to the strip of its first token
       const bool own = pos < H ? bos >= t0 + s0 && bos < t0 + s0 + kStrip : i < s0 + kStrip;
       if (!own) continue;
+      // Lengths that run backwards make sequences overlap, and a token goes to one of them. Where that
+      // took a sequence's first token away, its next W-1 have no state to start from (and perhaps no rows
+      // before them): they are skipped.
+      if (pos != 0 && pos < H && have != n) continue;
       if (pos == 0) {
         const int64_t slot = idx ? resolve_slot(idx, n, num_slots) : n;
         const T* si = state_in ? state_in + slot * slot_stride + c : nullptr;
@@ -281,7 +285,8 @@ conv_prompt_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict
         have = n;
       } else if (have != n) {
 #pragma unroll
-        for (int j = 0; j < H; ++j) h[j] = R::load(x + (t - H + j) * x_pitch + c);
+        for (int j = 0; j < H; ++j)
+          h[j] = KDA_CHECK(t - H + j >= bos) ? R::load(x + (t - H + j) * x_pitch + c) : R::zero();
         have = n;
       }
       float win[W][VEC], out[VEC];
