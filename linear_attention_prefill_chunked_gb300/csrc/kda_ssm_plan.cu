@@ -151,16 +151,12 @@ ssm_combine_kernel(const PlanHdr* __restrict__ hdr, const Split* __restrict__ sp
 }  // namespace
 
 int gpu_sms() {
-  static const int n = [] {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) {
-      (void)cudaGetLastError();
-      v = 152;
-    }
-    return v;
-  }();
-  return n;
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess &&
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0)
+    return n;
+  (void)cudaGetLastError();
+  return 152;
 }
 
 namespace {

@@ -108,9 +108,21 @@ def _rows_slow(t, name, shape, dtype):
 
 
 def _cuda(*tensors):
+    """Every tensor of the call, a given workspace among them, lives on one CUDA device, the current one:
+    the library launches there, and a stream's handle of 0 means that device's default stream."""
+    dev = None
     for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError("every tensor of the call must live on a CUDA device")
+        if t is not None:
+            i = t.get_device()
+            if i < 0:
+                raise ValueError("every tensor of the call must live on a CUDA device")
+            if dev is None:
+                dev = i
+            elif i != dev:
+                raise ValueError(f"the call's tensors must share one device, got cuda:{dev} and cuda:{i}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the call's tensors live on cuda:{dev}, which must be the current device "
+                         "(torch.cuda.device)")
 
 
 def _activation(activation):
@@ -173,6 +185,8 @@ def _state_pool(state, name, dims, slot_stride):
 def _stream(stream, device):
     if stream is None:  # the handle alone: torch.cuda.current_stream() builds an object, 2 us of a call's 20
         return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device_index != device.index:
+        raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the call's tensors to {device}")
     return stream.cuda_stream
 
 
@@ -186,8 +200,11 @@ def _empty(stream, shape, dtype, device):
 
 def _workspace(stream, given, size, device):
     """The given workspace if it holds a status word, else a new one of ``size`` bytes."""
-    if given is not None and given.numel() * given.element_size() >= STATUS_WORKSPACE_BYTES:
-        return given, given.numel() * given.element_size()
+    if given is not None:
+        if not given.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        if given.numel() * given.element_size() >= STATUS_WORKSPACE_BYTES:
+            return given, given.numel() * given.element_size()
     return _empty(stream, size, torch.uint8, device), size
 
 
@@ -252,7 +269,7 @@ def causal_conv(x, weight, cu_seqlens, *, bias=None, activation=None, state=None
     N, T, ch, width, pitch = check_conv_args(
         x, weight, bias=bias, cu_seqlens=cu_seqlens, state=state, state_indices=state_indices,
         final_state=final_state, out=out, slot_stride=slot_stride)
-    _cuda(x, weight, bias, cu_seqlens, state, state_indices, final_state, out)
+    _cuda(x, weight, bias, cu_seqlens, state, state_indices, final_state, out, workspace)
     silu = _activation(activation)
     lib, dev = _load(), x.device
     pool = state_indices is not None
@@ -277,7 +294,7 @@ def _conv_token(x, weight, cu_seqlens, state, state_indices, bias, activation, c
     N, T, ch, width, pitch = check_conv_args(x, weight, bias=bias, cu_seqlens=cu_seqlens, state=state,
                                              state_indices=state_indices, out=out,
                                              slot_stride=slot_stride, token=True)
-    _cuda(x, weight, bias, cu_seqlens, state, state_indices, cache, out)
+    _cuda(x, weight, bias, cu_seqlens, state, state_indices, cache, out, workspace)
     silu = _activation(activation)
     cpitch = 0
     if cache is not None:
@@ -393,7 +410,7 @@ def ssm_scan(x, dt, A_log, B, C, cu_seqlens, *, D=None, dt_bias=None, state=None
     N, T, H, G, K, V, pitches = check_ssm_args(
         x, dt, A_log, B, C, D=D, dt_bias=dt_bias, cu_seqlens=cu_seqlens, state=state,
         state_indices=state_indices, final_state=final_state, out=out, slot_stride=slot_stride)
-    _cuda(x, dt, A_log, B, C, D, dt_bias, cu_seqlens, state, state_indices, final_state, out)
+    _cuda(x, dt, A_log, B, C, D, dt_bias, cu_seqlens, state, state_indices, final_state, out, workspace)
     lib, dev = _load(), x.device
     pool = state_indices is not None
     sdt = state.dtype if state is not None else (
@@ -420,7 +437,7 @@ def _ssm_token(x, dt, A_log, B, C, cu_seqlens, pool, state_indices, D, dt_bias, 
     N, T, H, G, K, V, pitches = check_ssm_args(
         x, dt, A_log, B, C, D=D, dt_bias=dt_bias, cu_seqlens=cu_seqlens, state=pool,
         state_indices=state_indices, out=out, slot_stride=slot_stride, token=True)
-    _cuda(x, dt, A_log, B, C, D, dt_bias, cu_seqlens, pool, state_indices, cache, out)
+    _cuda(x, dt, A_log, B, C, D, dt_bias, cu_seqlens, pool, state_indices, cache, out, workspace)
     cpitch = 0
     if cache is not None:
         cpitch = _step_cache(cache, "cache", N, max_steps, H * K * V, pool.dtype)
@@ -484,7 +501,7 @@ def verify_draft(tokens, target_probs, draft_probs, accept_u, noise, cu_seqlens,
         _plain(num_accepted, "num_accepted", torch.int32, (N,))
     if next_token is not None:
         _plain(next_token, "next_token", torch.int32, (N,))
-    _cuda(tokens, target_probs, draft_probs, accept_u, noise, cu_seqlens, num_accepted, next_token)
+    _cuda(tokens, target_probs, draft_probs, accept_u, noise, cu_seqlens, num_accepted, next_token, workspace)
     lib, dev = _load(), tokens.device
     if num_accepted is None:
         num_accepted = _empty(stream, (N,), torch.int32, dev)
@@ -517,7 +534,7 @@ def commit_draft(cache, num_accepted, pool, state_indices=None, *, workspace=Non
     pitch = _step_cache(cache, "cache", N, steps, row, pool.dtype)
     if state_indices is not None:
         _plain(state_indices, "state_indices", torch.int32, (N,))
-    _cuda(cache, num_accepted, pool, state_indices)
+    _cuda(cache, num_accepted, pool, state_indices, workspace)
     lib, dev = _load(), pool.device
     ws, nws = _workspace(stream, workspace, STATUS_WORKSPACE_BYTES, dev)
     rc = lib.kda_commit_draft(N, _dt(pool.dtype), row, _p(cache), pitch, steps, _p(num_accepted),
