@@ -147,9 +147,11 @@ verify_kernel(const int32_t* __restrict__ tokens, const float* __restrict__ p,
     return;
   }
 
-  // this CTA's part of the noise is wanted whatever is accepted: on its way while that is found out
-  for (int64_t i = ((int64_t)rank * kThreads + tid) * 32; i < vocab; i += (int64_t)ranks * kThreads * 32)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + (int64_t)n * vocab + i));
+  // this CTA's part of the noise is wanted whatever is accepted: on its way while that is found out (without
+  // a token in the batch there may be no noise)
+  if (T > 0)
+    for (int64_t i = ((int64_t)rank * kThreads + tid) * 32; i < vocab; i += (int64_t)ranks * kThreads * 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + (int64_t)n * vocab + i));
 
   // every CTA of the cluster has to have started before another writes into its shared memory: said
   // here and waited for after the accepted tokens are known
