@@ -183,6 +183,13 @@ __device__ __forceinline__ void sub2(float& a, float& b, float x, float y) {
   asm("sub.rn.f32x2 %0, %0, %1;" : "+l"(ab) : "l"(xy));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
 }
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
+  unsigned long long ab, xy;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ab) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(ab) : "l"(xy));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(ab));
+}
 // (a, b) <- (a, b) + (x, y) * (u, v)
 __device__ __forceinline__ void acc2(float& a, float& b, float x, float y, float u, float v) {
   unsigned long long ab, xy, uv;
@@ -262,7 +269,13 @@ bool ssm_tc_supported(const kda_desc_t& d);
 size_t ssm_tc_workspace(const kda_desc_t& d);  // the whole workspace, header included
 size_t ssm_simt_workspace(const kda_desc_t& d);
 cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t st);
-// Step size and decay of one (token, head): softplus(dt + bias) and the log-decay (<= 0).
+// Log-decay a unit of step of a head, -exp(a_log) (times `unit`: its logarithm's base). Kept finite: from
+// a_log = 89 on any step above 1e-36 forgets everything all the same, and a step of zero nothing.
+__device__ __forceinline__ float ssm_rate(float a_log, float unit = 1.f) {
+  const float r = -expf(a_log) * unit;
+  return r < -3.402823466e38f ? -3.402823466e38f : r;  // NaN stays
+}
+// Step size of one (token, head): softplus(dt + bias).
 __device__ __forceinline__ float ssm_step(float dt, float bias) { return softplus_f32(dt + bias); }
 
 cudaError_t launch_verify(int N, int64_t T, int vocab, const int32_t* tokens, const float* p,

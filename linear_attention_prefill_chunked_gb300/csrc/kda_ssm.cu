@@ -46,7 +46,7 @@ ssm_decode_kernel(kda_ssm_inputs_t in, ST* pool, const int32_t* __restrict__ idx
 #pragma unroll
   for (int j = 0; j < RPT; ++j) load4(S + (size_t)(rg + j * RG) * V, s[j]);
 
-  const float rate = -expf(in.a_log[h]);
+  const float rate = ssm_rate(in.a_log[h]);
   const float bias = in.dt_bias ? in.dt_bias[h] : 0.f;
   const float dskip = in.d ? in.d[h] : 0.f;
   const int g = h / (H / G);
@@ -160,7 +160,7 @@ ssm_scan_simt_kernel(kda_ssm_inputs_t in, const ST* state_in, const int32_t* __r
     else if (state_in && !kState) load4(state_in + at + (size_t)r * V, s[r]);
     else s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.f;
   }
-  const float rate = -expf(in.a_log[h]);
+  const float rate = ssm_rate(in.a_log[h]);
   const float bias = in.dt_bias ? in.dt_bias[h] : 0.f;
   const float dskip = in.d ? in.d[h] : 0.f;
   const QT* pb = static_cast<const QT*>(in.b) + h / (H / G) * K;

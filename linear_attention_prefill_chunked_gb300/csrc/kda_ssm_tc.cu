@@ -8,9 +8,11 @@
 //   S <- exp(g_1 + .. + g_L) S + sum_s exp(g_{s+1} + .. + g_L) d_s b_s x_s^T
 //
 // Every exponent is a sum of log-decays of consecutive tokens, so none is positive. Prefixes and
-// suffixes are taken over halves of 32 tokens and across halves they add up, so that a difference
-// of prefixes (within a half) cancels no more than those 32 tokens' sum; a step of zero (a padded
-// token) is a zero weight.
+// suffixes are taken over halves of 32 tokens and across halves they add up; within a half the weight of
+// s for t is exp((cl_t - cl_s) + log d_s) with cl the prefixes, so that a token's own weight is its step
+// however strong the decays are. A log2-decay counts as -256 at least, past which nothing is left of
+// anything in fp32: cl stays within 2^13, and a difference of two is off by some 2^-12 at most. A step of
+// zero (a padded token) is a zero weight.
 //
 // A CTA takes 128 value columns of one sequence: two 64-wide heads of a group, or one 128-wide
 // head. Transposed accumulators (lanes = value columns) put both heads into one M = 128 product
@@ -113,7 +115,7 @@ struct Item {
 // Steps and decays of a chunk, by [head of the item][token], logarithms to base 2; a half is 32 tokens.
 struct Factors {
   alignas(16) float cl[2][kL];  // log-decay from the half's start through t
-  float same[2][kL];   // log d_s - cl: + cl_t is the weight of s for t in its half
+  float step[2][kL];   // log d_s: + cl_t - cl_s is the weight of s for t in its half
   float later[2][kL];  // log d_s + log-decay after s to its half's end: + cl_t for t in the next
   float e[2][kL];      // decay from the chunk's start through t
   float to_end[2][kL];  // weight of s in the state after the chunk
@@ -129,6 +131,7 @@ struct Ctl {
   uint32_t tmem_base;
   uint32_t abort;
   uint32_t poll;            // waits poll: the limit is below what try_wait may suspend a thread for
+  alignas(16) float none[kL / 2];  // zeros: what `later` takes in the place of cl_s
 };
 constexpr uint32_t kTcSmem = OFF_CTL + ((sizeof(Ctl) + 15) & ~15u);
 static_assert(kStages == 3, "the loader keeps three outputs");
@@ -579,6 +582,8 @@ __device__ __forceinline__ void scan_steps(Factors* f, const float (&d)[2][2], c
   for (int h = 0; h < kHeads; ++h) {
     g0[h] = rate2[h] * d[h][0];  // log2-decays
     g1[h] = rate2[h] * d[h][1];
+    g0[h] = g0[h] < -256.f ? -256.f : g0[h];
+    g1[h] = g1[h] < -256.f ? -256.f : g1[h];
     up[h] = dn[h] = g0[h] + g1[h];  // inclusive sums over the half's 16 lanes, from either end
   }
 #pragma unroll
@@ -603,7 +608,7 @@ __device__ __forceinline__ void scan_steps(Factors* f, const float (&d)[2][2], c
     const int t = 2 * lane;
     const float l0 = __log2f(d[h][0]), l1 = __log2f(d[h][1]);  // -inf for a step of zero: no weight
     *reinterpret_cast<float2*>(&f->cl[h][t]) = make_float2(c0, c1);
-    *reinterpret_cast<float2*>(&f->same[h][t]) = make_float2(l0 - c0, l1 - c1);
+    *reinterpret_cast<float2*>(&f->step[h][t]) = make_float2(l0, l1);
     *reinterpret_cast<float2*>(&f->later[h][t]) = make_float2(l0 + (after + g1[h]), l1 + after);
     *reinterpret_cast<float2*>(&f->e[h][t]) = make_float2(ex2(pre + c0), ex2(pre + c1));
     const float then = lane < 16 ? second : 0.f;
@@ -625,7 +630,7 @@ __device__ void run_scan_heads(const ScanParams& p, Ctl* c) {
 #pragma unroll
     for (int h = 0; h < kHeads; ++h) {
       if (h == 1 && !second) break;
-      rate2[h] = -ex2(p.a_log[it.h0 + h] * 1.4426950408889634f) * 1.4426950408889634f;
+      rate2[h] = ssm_rate(p.a_log[it.h0 + h], 1.4426950408889634f);
       bias[h] = p.dt_bias ? p.dt_bias[it.h0 + h] : 0.f;
     }
     // the steps of a chunk are read two scans ahead; -inf: no token, a step of zero
@@ -710,21 +715,26 @@ __device__ __forceinline__ void put_half(uint32_t taddr, const uint32_t (&parts)
 }
 
 // 16 x 32 elements of M, 16 a lane: the scores times their weights, rounded into the M tile at `at0` and
-// `at1` (the lane's row of the 8 x 8 blocks, of either 16 columns). `col`: the lane's columns' part of the
-// log-weights; `row`: the block's first row, from its first column on: columns after the row are not
-// weighted (their weight may be anything) but zero.
-__device__ __forceinline__ void weigh_block(uint32_t tmem, const float* col, float cl0, float cl1, int row,
-                                            uint32_t at0, uint32_t at1, int lane) {
+// `at1` (the lane's row of the 8 x 8 blocks, of either 16 columns). `col` and `cls`: the lane's columns'
+// part of the log-weights and what is taken off for them; `row`: the block's first row, from its first
+// column on: columns after the row are not weighted (their weight may be anything) but zero.
+__device__ __forceinline__ void weigh_block(uint32_t tmem, const float* col, const float* cls, float cl0, float cl1,
+                                            int row, uint32_t at0, uint32_t at1, int lane) {
   float g[16];
   tmem_ld_16x256_x4(tmem, g);
   float w[16];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const float2 q = *reinterpret_cast<const float2*>(col + c * 8);
-    w[4 * c] = ex2(cl0 + q.x);
-    w[4 * c + 1] = ex2(cl0 + q.y);
-    w[4 * c + 2] = ex2(cl1 + q.x);
-    w[4 * c + 3] = ex2(cl1 + q.y);
+    const float2 s = *reinterpret_cast<const float2*>(cls + c * 8);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float u = r ? cl1 : cl0, v = u;
+      sub2(u, v, s.x, s.y);
+      add2(u, v, q.x, q.y);
+      w[4 * c + 2 * r] = ex2(u);
+      w[4 * c + 2 * r + 1] = ex2(v);
+    }
   }
   const int last = row + (lane >> 2) - 2 * (lane & 3);
   tmem_ld_wait();
@@ -748,6 +758,7 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
     *reinterpret_cast<uint4*>(sm + OFF_M + kTileBytes + i * 16) = make_uint4(0, 0, 0, 0);
     *reinterpret_cast<uint4*>(sm + (i < 512 ? OFF_Z0 + i * 16 : OFF_Z1 + (i - 512) * 16)) = make_uint4(0, 0, 0, 0);
   }
+  if (threadIdx.x < kL / 2) c->none[threadIdx.x] = 0.f;
   fence_async_smem();
   named_bar(1, kMThreads);
 
@@ -797,8 +808,9 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
       const uint32_t mt = m0 + par * kTileBytes, tg = tbase + TM_YM + par * 64 + ((uint32_t)(quad * 32) << 16);
 #pragma unroll 1
       for (int half = half0; half <= quad >> 1; half += halfn)
-        weigh_block(tg + half * 32, (half == quad >> 1 ? f->same[hm] : f->later[hm]) + half * 32 + 2 * (lane & 3),
-                    cl0, cl1, quad * 16 - half * 32, mt + (((half * 4 + (lane >> 4)) ^ (lane & 7)) << 4),
+        weigh_block(tg + half * 32, (half == quad >> 1 ? f->step[hm] : f->later[hm]) + half * 32 + 2 * (lane & 3),
+                    (half == quad >> 1 ? f->cl[hm] + half * 32 : c->none) + 2 * (lane & 3), cl0, cl1,
+                    quad * 16 - half * 32, mt + (((half * 4 + (lane >> 4)) ^ (lane & 7)) << 4),
                     mt + (((half * 4 + 2 + (lane >> 4)) ^ (lane & 7)) << 4), lane);
       tc_fence_before();
       fence_async_smem();
@@ -988,7 +1000,7 @@ __device__ void run_suffixes(const ScanParams& p, Ctl* c, int hd) {
     if (it.done) return;
     const int h = it.h0 + hd;
     const bool real = hd == 0 || (it.h0 % rep) + 1 < rep;
-    const float rate2 = real ? -ex2(p.a_log[h] * 1.4426950408889634f) * 1.4426950408889634f : 0.f;
+    const float rate2 = real ? ssm_rate(p.a_log[h], 1.4426950408889634f) : 0.f;
     const float bias = real && p.dt_bias ? p.dt_bias[h] : 0.f;
     const __nv_bfloat16* at = p.dt + (it.bos + (int64_t)(it.nchunks - 1) * kL + 2 * lane) * p.dt_pitch + h;
     int left = real ? it.nchunks : 0;
