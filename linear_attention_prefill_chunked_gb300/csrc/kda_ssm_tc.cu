@@ -132,6 +132,10 @@ struct Ctl {
   uint32_t abort;
   uint32_t poll;            // waits poll: the limit is below what try_wait may suspend a thread for
   alignas(16) float none[kL / 2];  // zeros: what `later` takes in the place of cl_s
+  // x that is no number, by chunk parity: whether 32 value columns (a quadrant) and 32 tokens hold any (set by
+  // hide_x, cleared by spoil_x), and if so each column's first of those tokens (kL: none)
+  alignas(8) uint8_t odd[2][4][2];
+  uint8_t first[2][2][128];
 };
 constexpr uint32_t kTcSmem = OFF_CTL + ((sizeof(Ctl) + 15) & ~15u);
 static_assert(kStages == 3, "the loader keeps three outputs");
@@ -446,6 +450,28 @@ __device__ void run_loader(const ScanParams& p, uint8_t* sm, Ctl* c) {
 // product here, the pipe 52 to 71, and a product never waits for one of the other loop's.
 
 // ---- warp 19: the products of the output ------------------------------------------------------
+// One thread, in chunks with an x that is no number, once the product with M is done: NaN stands in the x
+// tile from a column's first such token on, so that these outputs become NaN by their D x.
+__device__ __noinline__ bool spoil_x(uint32_t j) {
+  const uint32_t par = j & 1;
+  uint8_t* x = ssm_smem + OFF_ST + j % kStages * kStageBytes + OFF_X;
+  Ctl* c = ctl();
+  if (!tc_wait(T_MX + (int)par, (j >> 1) & 1)) return false;
+  tc_fence_after();
+#pragma unroll 1
+  for (int v = 0; v < 128; ++v) {
+    int r = kL;
+    if (c->odd[par][v >> 5][1]) r = c->first[par][1][v];
+    if (c->odd[par][v >> 5][0]) r = min(r, (int)c->first[par][0][v]);
+#pragma unroll 1
+    for (; r < kL; ++r)
+      reinterpret_cast<uint16_t*>(x + (v >> 6) * 8192 + sw128_off(r, (v & 63) >> 3))[v & 7] = 0x7fffu;
+  }
+  *reinterpret_cast<uint64_t*>(c->odd[par]) = 0u;
+  __threadfence_block();  // before the R group can see the products of C done
+  return true;
+}
+
 template <int K>
 __device__ void run_output(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tbase) {
   if (!elect_one()) return;
@@ -476,7 +502,8 @@ __device__ void run_output(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
         issue_ss(ym, desc128(sbase + OFF_Z0, x0 + 8192 - (sbase + OFF_Z0), 1024), 2048,
                  desc128(m + 8192, 16, 1024), 32, id_m, 1);
       mma_commit(&c->bar[T_MX + (j & 1)]);
-      ok = tc_wait(T_S, j & 1);
+      if (*reinterpret_cast<const uint64_t*>(c->odd[j & 1]) != 0u) ok = spoil_x(j);
+      ok = ok && tc_wait(T_S, j & 1);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
@@ -725,6 +752,33 @@ __device__ __forceinline__ void load_x(uint32_t (&raw)[4][4], uint32_t tile, uin
 #pragma unroll
   for (int i = 0; i < 4; ++i) ldsm_x4_trans(raw[i], tile + (i & 1) * 2048 + ((col0 ^ (i & 2)) << 4));
 }
+// Whether any of those is no number: zero times it is not zero.
+__device__ __forceinline__ bool not_finite(const uint32_t (&raw)[4][4]) {
+  uint32_t z[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(z[i & 3]) : "r"(raw[i >> 2][i & 3]), "r"(0u));
+  return ((z[0] | z[1] | z[2] | z[3]) & 0x7fff7fffu) != 0u;
+}
+// Its treatment in chunk j of the CTA, for the warp's 32 columns (lane: column) and 32 rows. A zero weight of
+// M would not hide it from the tokens before it: zeros take its place for the product with M (x' has been
+// read), then spoil_x makes up for it.
+__device__ __noinline__ void hide_x(uint32_t j) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, th = warp >> 2;
+  uint8_t* half = ssm_smem + OFF_ST + j % kStages * kStageBytes + OFF_X + (quad >> 1) * 8192;
+  int first = kL;
+#pragma unroll 1
+  for (int r = th * 32 + 31; r >= th * 32; --r) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(half + sw128_off(r, (quad & 1) * 4 + (lane >> 3))) + (lane & 7);
+    if ((*p & 0x7f80u) == 0x7f80u) {
+      *p = 0;
+      first = r;
+    }
+  }
+  Ctl* c = ctl();
+  c->first[j & 1][th][quad * 32 + lane] = (uint8_t)first;
+  if (lane == 0) c->odd[j & 1][quad][th] = 1;
+}
 // x' of 16 of those columns, and its way to TMEM.
 template <int PARTS>
 __device__ __forceinline__ void split_half(const uint32_t (&a)[4], const uint32_t (&b)[4], const float2 (&w)[4],
@@ -788,6 +842,7 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
     *reinterpret_cast<uint4*>(sm + (i < 512 ? OFF_Z0 + i * 16 : OFF_Z1 + (i - 512) * 16)) = make_uint4(0, 0, 0, 0);
   }
   if (threadIdx.x < kL / 2) c->none[threadIdx.x] = 0.f;
+  if (threadIdx.x < 2) *reinterpret_cast<uint64_t*>(c->odd[threadIdx.x]) = 0u;
   fence_async_smem();
   named_bar(1, kMThreads);
 
@@ -804,10 +859,12 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
   const uint32_t xoff = OFF_X + (quad >> 1) * 8192 + row0;
   const uint32_t txp = tbase + TM_XP + th * 16 + ((uint32_t)(quad * 32) << 16);
   const int hx = heads == 2 ? quad >> 1 : 0;
+  const int rep = p.H / p.G;
   uint32_t j = 0;
   for (uint32_t k = 0;; ++k) {
     const Item it = tc_item_warp(p, c, k);
     if (it.done) return;
+    const bool real = hx == 0 || (it.h0 % rep) + 1 < rep;  // else its half of x's tile is nobody's
     for (int ch = 0; ch < it.nchunks; ++ch, ++j) {
       const uint32_t st = j % kStages, par = j & 1, fi = j % kFacs;
       uint8_t* stage = sm + OFF_ST + st * kStageBytes;
@@ -841,6 +898,9 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
                     (half == quad >> 1 ? f->cl[hm] + half * 32 : c->none) + 2 * (lane & 3), cl0, cl1,
                     quad * 16 - half * 32, mt + (((half * 4 + (lane >> 4)) ^ (lane & 7)) << 4),
                     mt + (((half * 4 + 2 + (lane >> 4)) ^ (lane & 7)) << 4), lane);
+      uint32_t raw[4][4], parts[PARTS][8];
+      load_x(raw, smem_u32(stage) + xoff, col0);
+      if (__any_sync(0xffffffffu, not_finite(raw)) && real) hide_x(j);
       tc_fence_before();
       fence_async_smem();
       warp_arrive(&c->bar[T_M + par]);
@@ -849,8 +909,6 @@ __device__ void run_mgroup(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t tb
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         w[i] = *reinterpret_cast<const float2*>(&f->to_end[hx][th * 32 + i * 8 + 2 * (lane & 3)]);
-      uint32_t raw[4][4], parts[PARTS][8];
-      load_x(raw, smem_u32(stage) + xoff, col0);
       split_half<PARTS>(raw[0], raw[1], w, parts);
       warp_arrive(&c->bar[T_FAC_FREE + fi]);
       if (j > 0 && !all_lanes(tc_wait(T_SU, (j - 1) & 1))) return;
