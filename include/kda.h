@@ -425,9 +425,20 @@ kda_status_t kda_ssm_decode(const kda_desc_t *desc, const kda_ssm_inputs_t *in,
  *   tokens [T] int32    p (target_probs) and q (draft_probs) [T, vocab] fp32, packed; q may be NULL
  *   (drafts made without drawing: q is 1 at the drafted token)    accept_u [T] fp32 in [0, 1)
  *   noise [N, vocab] fp32 > 0    num_accepted, next_token [N] int32
- * Rows of q and elements of accept_u at a request's last token are not read.  A request with a
- * drafted token outside [0, vocab) or a bad cu_seqlens is skipped (status bit).
+ * Rows of q and elements of accept_u at a request's last token are not read.  With total_tokens == 0
+ * all but cu_seqlens and the outputs may be NULL.  A request with a drafted token outside [0, vocab) or a
+ * bad cu_seqlens is skipped (status bit): kda_verify_draft leaves its num_accepted and next_token as they
+ * are.  Where those go on to kda_commit_draft unseen, use kda_verify_draft_marked, which writes 0 (nothing
+ * to commit) and -1 there, each if its flag is given.
  */
+#define KDA_VERIFY_MARK_COUNT 0x1u /* num_accepted of skipped requests: 0 */
+#define KDA_VERIFY_MARK_TOKEN 0x2u /* next_token of skipped requests: -1  */
+kda_status_t kda_verify_draft_marked(int32_t num_seqs, int64_t total_tokens, int32_t vocab,
+                                     const int32_t *tokens, const float *target_probs,
+                                     const float *draft_probs, const float *accept_u,
+                                     const float *noise, const int32_t *cu_seqlens,
+                                     int32_t *num_accepted, int32_t *next_token, uint32_t flags,
+                                     void *workspace, size_t workspace_bytes, cudaStream_t stream);
 kda_status_t kda_verify_draft(int32_t num_seqs, int64_t total_tokens, int32_t vocab,
                               const int32_t *tokens, const float *target_probs,
                               const float *draft_probs, const float *accept_u, const float *noise,

@@ -58,7 +58,8 @@ EXPORTS = ("kda_chunk_prefill_workspace_size", "kda_chunk_prefill_min_workspace_
            "kda_decode", "kda_read_device_status", "kda_chunk_prefill_path", "kda_status_string",
            "kda_chunk_prefill_noalloc", "kda_chunk_prefill_act", "kda_decode_draft",
            "kda_set_pipeline_wait_limit", "kda_causal_conv", "kda_causal_conv_decode", "kda_ssm_scan",
-           "kda_ssm_scan_workspace_size", "kda_ssm_decode", "kda_verify_draft", "kda_commit_draft")
+           "kda_ssm_scan_workspace_size", "kda_ssm_decode", "kda_verify_draft",
+           "kda_verify_draft_marked", "kda_commit_draft")
 
 _lib = None
 

@@ -121,7 +121,7 @@ verify_kernel(const int32_t* __restrict__ tokens, const float* __restrict__ p,
               const float* __restrict__ q, const float* __restrict__ u,
               const float* __restrict__ noise, const int32_t* __restrict__ cu,
               int32_t* __restrict__ kept, int32_t* __restrict__ next,
-              uint32_t* __restrict__ status, int N, int64_t T, int vocab) {
+              uint32_t* __restrict__ status, int N, int64_t T, int vocab, uint32_t flags) {
   __shared__ Best s_warp[kThreads / 32], s_all[2][kMaxRanks];
   __shared__ int s_stop, s_bad;
   cg::cluster_group cl = cg::this_cluster();
@@ -156,9 +156,15 @@ verify_kernel(const int32_t* __restrict__ tokens, const float* __restrict__ p,
   // every CTA of the cluster has to have started before another writes into its shared memory: said
   // here and waited for after the accepted tokens are known
   auto started = cl.barrier_arrive();
+  auto skipped = [&] {
+    if (rank != 0 || tid != 0) return;
+    if (flags & KDA_VERIFY_MARK_COUNT) kept[n] = 0;
+    if (flags & KDA_VERIFY_MARK_TOKEN) next[n] = -1;
+  };
   int64_t bos, eos;
   if (!seq_bounds(cu, n, T, &bos, &eos)) {  // the whole cluster, as at each return below
     cl.barrier_wait(std::move(started));
+    skipped();
     return;
   }
   const int len = (int)(eos - bos);
@@ -188,7 +194,10 @@ verify_kernel(const int32_t* __restrict__ tokens, const float* __restrict__ p,
   }
   __syncthreads();
   cl.barrier_wait(std::move(started));
-  if (s_bad) return;  // the whole cluster read the same tokens
+  if (s_bad) {  // the whole cluster read the same tokens
+    skipped();
+    return;
+  }
   const int stop = s_stop;
   const int64_t r = bos + stop;
   const float* pr = p + r * vocab;
@@ -271,7 +280,7 @@ cudaError_t commit_as(int N, int64_t row, const void* cache, int64_t pitch, int 
 
 cudaError_t launch_verify(int N, int64_t T, int vocab, const int32_t* tokens, const float* p,
                           const float* q, const float* u, const float* noise, const int32_t* cu,
-                          int32_t* kept, int32_t* next, uint32_t* status, cudaStream_t st) {
+                          int32_t* kept, int32_t* next, uint32_t* status, uint32_t flags, cudaStream_t st) {
   // a CTA a request fills the GPU from a few hundred requests on; below that the row is shared
   int ranks = 1;
   while (ranks < kMaxRanks && (int64_t)N * ranks < 304 && (int64_t)ranks * 4096 < vocab) ranks *= 2;
@@ -287,7 +296,7 @@ cudaError_t launch_verify(int N, int64_t T, int vocab, const int32_t* tokens, co
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, few ? verify_kernel<512> : verify_kernel<256>, tokens, p, q, u, noise, cu, kept, next, status, N,
-                            T, vocab);
+                            T, vocab, flags);
 }
 
 cudaError_t launch_commit(int N, int elem_bytes, int64_t row, const void* cache, int64_t pitch,

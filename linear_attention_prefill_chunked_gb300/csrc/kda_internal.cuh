@@ -280,7 +280,7 @@ __device__ __forceinline__ float ssm_step(float dt, float bias) { return softplu
 
 cudaError_t launch_verify(int N, int64_t T, int vocab, const int32_t* tokens, const float* p,
                           const float* q, const float* u, const float* noise, const int32_t* cu,
-                          int32_t* kept, int32_t* next, uint32_t* status, cudaStream_t st);
+                          int32_t* kept, int32_t* next, uint32_t* status, uint32_t flags, cudaStream_t st);
 cudaError_t launch_commit(int N, int elem_bytes, int64_t row, const void* cache, int64_t pitch,
                           int max_steps, const int32_t* kept, void* pool, int64_t num_slots,
                           int64_t slot_stride, const int32_t* idx, uint32_t* status,

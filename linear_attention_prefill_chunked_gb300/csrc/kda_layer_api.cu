@@ -221,7 +221,19 @@ kda_status_t kda_verify_draft(int32_t num_seqs, int64_t total_tokens, int32_t vo
                               const int32_t* cu_seqlens, int32_t* num_accepted,
                               int32_t* next_token, void* workspace, size_t workspace_bytes,
                               cudaStream_t stream) {
-  if (num_seqs < 0 || total_tokens < 0 || vocab <= 0 || !cu_seqlens || !ws_ok(workspace))
+  return kda_verify_draft_marked(num_seqs, total_tokens, vocab, tokens, target_probs, draft_probs, accept_u,
+                                 noise, cu_seqlens, num_accepted, next_token, 0u, workspace, workspace_bytes,
+                                 stream);
+}
+
+kda_status_t kda_verify_draft_marked(int32_t num_seqs, int64_t total_tokens, int32_t vocab,
+                                     const int32_t* tokens, const float* target_probs,
+                                     const float* draft_probs, const float* accept_u, const float* noise,
+                                     const int32_t* cu_seqlens, int32_t* num_accepted,
+                                     int32_t* next_token, uint32_t flags, void* workspace,
+                                     size_t workspace_bytes, cudaStream_t stream) {
+  if (num_seqs < 0 || total_tokens < 0 || vocab <= 0 || !cu_seqlens || !ws_ok(workspace) ||
+      (flags & ~(KDA_VERIFY_MARK_COUNT | KDA_VERIFY_MARK_TOKEN)) != 0)
     return KDA_ERR_INVALID_ARGUMENT;
   if (num_seqs > (1 << 27)) return KDA_ERR_UNSUPPORTED;
   if (num_seqs > 0 && (!num_accepted || !next_token)) return KDA_ERR_INVALID_ARGUMENT;
@@ -237,7 +249,7 @@ kda_status_t kda_verify_draft(int32_t num_seqs, int64_t total_tokens, int32_t vo
   return launched(workspace, stream, [&] {
     return kda::launch_verify(num_seqs, total_tokens, vocab, tokens, target_probs, draft_probs,
                               accept_u, noise, cu_seqlens, num_accepted, next_token,
-                              status_of(workspace), stream);
+                              status_of(workspace), flags, stream);
   });
 }
 

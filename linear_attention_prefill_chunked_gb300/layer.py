@@ -51,6 +51,8 @@ def _load():
                 ("kda_ssm_decode",
                  [desc, ins, *[_P] * 4, _I64, _I32, ctypes.c_int, _P, _P, size, _P], ctypes.c_int),
                 ("kda_verify_draft", [_I32, _I64, _I32, *[_P] * 9, size, _P], ctypes.c_int),
+                ("kda_verify_draft_marked",
+                 [_I32, _I64, _I32, *[_P] * 8, ctypes.c_uint32, _P, size, _P], ctypes.c_int),
                 ("kda_commit_draft",
                  [_I32, ctypes.c_int, _I64, _P, _I64, _I32, _P, _P, _I64, _I64, _P, _P, size, _P],
                  ctypes.c_int)):
@@ -475,7 +477,7 @@ def ssm_decode_draft(x, dt, A_log, B, C, cu_seqlens, pool, state_indices=None, *
 # ------------------------------------------------------------------------ drafted tokens
 
 def verify_draft(tokens, target_probs, draft_probs, accept_u, noise, cu_seqlens, *,
-                 num_accepted=None, next_token=None, workspace=None, stream=None):
+                 num_accepted=None, next_token=None, mark_skipped=None, workspace=None, stream=None):
     """Drafted tokens against the target's probabilities from given random numbers
     (kda_verify_draft).  Returns ``(num_accepted, next_token)``, int32 [N].
 
@@ -483,7 +485,10 @@ def verify_draft(tokens, target_probs, draft_probs, accept_u, noise, cu_seqlens,
     [T, vocab] fp32, row t following token t; draft_probs the same of the draft, or None for drafts
     made without drawing; accept_u [T] fp32 in [0, 1); noise [N, vocab] fp32 ~ Exp(1); cu_seqlens
     [N+1] int32.  num_accepted counts the tokens of a request that stand, the first among them: the
-    step that :func:`commit_draft` keeps.
+    step that :func:`commit_draft` keeps.  A request that is skipped (a drafted token outside the
+    vocabulary, bad lengths: see the status word) gets 0 and -1 in outputs made here; outputs given
+    (``num_accepted``, ``next_token`` [N] int32) keep what they hold for it, unless ``mark_skipped``
+    is True.
     """
     if not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 2:
         raise ValueError("target_probs must have shape [T, vocab]")
@@ -503,14 +508,17 @@ def verify_draft(tokens, target_probs, draft_probs, accept_u, noise, cu_seqlens,
         _plain(next_token, "next_token", torch.int32, (N,))
     _cuda(tokens, target_probs, draft_probs, accept_u, noise, cu_seqlens, num_accepted, next_token, workspace)
     lib, dev = _load(), tokens.device
+    flags = 3 if mark_skipped else 0  # KDA_VERIFY_MARK_COUNT, KDA_VERIFY_MARK_TOKEN
     if num_accepted is None:
         num_accepted = _empty(stream, (N,), torch.int32, dev)
+        flags |= 1
     if next_token is None:
         next_token = _empty(stream, (N,), torch.int32, dev)
+        flags |= 2
     ws, nws = _workspace(stream, workspace, STATUS_WORKSPACE_BYTES, dev)
-    rc = lib.kda_verify_draft(N, T, vocab, _p(tokens), _p(target_probs), _p(draft_probs), _p(accept_u),
-                              _p(noise), _p(cu_seqlens), _p(num_accepted), _p(next_token), _p(ws), nws,
-                              _stream(stream, dev))
+    rc = lib.kda_verify_draft_marked(N, T, vocab, _p(tokens), _p(target_probs), _p(draft_probs),
+                                     _p(accept_u), _p(noise), _p(cu_seqlens), _p(num_accepted),
+                                     _p(next_token), flags, _p(ws), nws, _stream(stream, dev))
     _done(rc, "kda_verify_draft", verify_draft, ws)
     return num_accepted, next_token
 
