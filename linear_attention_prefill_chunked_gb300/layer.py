@@ -523,21 +523,26 @@ def verify_draft(tokens, target_probs, draft_probs, accept_u, noise, cu_seqlens,
     return num_accepted, next_token
 
 
-def commit_draft(cache, num_accepted, pool, state_indices=None, *, workspace=None, stream=None):
+def commit_draft(cache, num_accepted, pool, state_indices=None, *, slot_stride=0, workspace=None,
+                 stream=None):
     """Copies each request's state after its accepted tokens, ``cache[n, num_accepted[n] - 1]``, into
     its slot of ``pool`` (kda_commit_draft); nothing for a count of 0.  cache [N, steps, *row] of any
-    step cache (rows packed, requests at any pitch); pool [num_slots, *row].  Returns the pool."""
+    step cache (rows packed, requests at any pitch); pool [num_slots, *row], or with ``slot_stride`` a
+    buffer of pool.shape[0] slots that many elements apart, as the draft steps take it.  Returns the
+    pool."""
     if not (isinstance(pool, torch.Tensor) and pool.is_contiguous()):
         _need(pool, "pool", cuda=False)
     shape = pool.shape
-    if len(shape) < 2 or shape[0] == 0 or pool.numel() == 0:
+    if len(shape) < 1 or shape[0] == 0 or pool.numel() == 0 or (len(shape) < 2 and slot_stride == 0):
         raise ValueError(f"pool must have shape [num_slots, *row], got {list(shape)}")
-    if not isinstance(cache, torch.Tensor) or cache.dim() != len(shape) + 1 or \
-            cache.shape[2:] != shape[1:] or cache.shape[1] == 0:
+    if not isinstance(cache, torch.Tensor) or cache.dim() < 3 or cache.shape[1] == 0 or \
+            (slot_stride == 0 and cache.shape[2:] != shape[1:]):
         raise ValueError("cache must have shape [N, steps, *row] with the pool's rows")
     if not isinstance(num_accepted, torch.Tensor) or num_accepted.dim() != 1:
         raise TypeError("num_accepted must be an int32 tensor of one dimension")
-    N, steps, row = num_accepted.shape[0], cache.shape[1], pool.numel() // shape[0]
+    N, steps, row = num_accepted.shape[0], cache.shape[1], cache.shape[2:].numel()
+    if slot_stride != 0:
+        _state_pool(pool, "pool", cache.shape[2:], slot_stride)
     _plain(num_accepted, "num_accepted", torch.int32, (N,))
     pitch = _step_cache(cache, "cache", N, steps, row, pool.dtype)
     if state_indices is not None:
@@ -546,7 +551,7 @@ def commit_draft(cache, num_accepted, pool, state_indices=None, *, workspace=Non
     lib, dev = _load(), pool.device
     ws, nws = _workspace(stream, workspace, STATUS_WORKSPACE_BYTES, dev)
     rc = lib.kda_commit_draft(N, _dt(pool.dtype), row, _p(cache), pitch, steps, _p(num_accepted),
-                              _p(pool), shape[0], 0, _p(state_indices), _p(ws), nws,
+                              _p(pool), shape[0], slot_stride, _p(state_indices), _p(ws), nws,
                               _stream(stream, dev))
     _done(rc, "kda_commit_draft", commit_draft, ws)
     return pool
