@@ -322,12 +322,13 @@ def causal_conv_decode(x, weight, state, state_indices=None, *, bias=None, activ
                        slot_stride, out, workspace, stream, causal_conv_decode)
 
 
-def _steps(cu_seqlens, max_steps):
+def _steps(cu_seqlens, max_steps, stream):
     if max_steps is not None:
         return int(max_steps)
-    if cu_seqlens.numel() < 2:
+    if _num_seqs(cu_seqlens) < 1:
         return 1
-    return max(1, int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item()))
+    with torch.cuda.stream(stream):  # after what the call's stream has still to write (None: the current one)
+        return max(1, int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item()))
 
 
 def causal_conv_draft(x, weight, cu_seqlens, state, state_indices=None, *, bias=None,
@@ -338,7 +339,7 @@ def causal_conv_draft(x, weight, cu_seqlens, state, state_indices=None, *, bias=
     after each.  ``max_steps`` (the most tokens of a request) is read from the device if not given.
     Returns y [T, Ch]."""
     return _conv_token(x, weight, cu_seqlens, state, state_indices, bias, activation, cache,
-                       _steps(cu_seqlens, max_steps), update_state, slot_stride, out, workspace,
+                       _steps(cu_seqlens, max_steps, stream), update_state, slot_stride, out, workspace,
                        stream, causal_conv_draft)
 
 
@@ -470,7 +471,7 @@ def ssm_decode_draft(x, dt, A_log, B, C, cu_seqlens, pool, state_indices=None, *
     """Scan steps of drafted tokens, as :func:`decode_draft`; ``cache`` [N, steps, H, K, V] gets the
     state after each.  Returns y [T, H, V]."""
     return _ssm_token(x, dt, A_log, B, C, cu_seqlens, pool, state_indices, D, dt_bias, cache,
-                      _steps(cu_seqlens, max_steps), update_pool, slot_stride, out, workspace, stream,
+                      _steps(cu_seqlens, max_steps, stream), update_pool, slot_stride, out, workspace, stream,
                       ssm_decode_draft)
 
 
