@@ -346,7 +346,7 @@ cudaError_t launch_ssm_decode(const SsmArgs& a, cudaStream_t st) {
 }
 
 size_t ssm_simt_workspace(const kda_desc_t& d) {
-  return ssm_plan_workspace(d, simt_items(d), simt_workers(d));
+  return ssm_plan_workspace(d, simt_items(d), simt_workers(d), kSimtMinPart);
 }
 
 cudaError_t launch_ssm_simt(const SsmArgs& a, cudaStream_t st) {

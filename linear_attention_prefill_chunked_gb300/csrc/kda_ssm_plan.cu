@@ -186,16 +186,20 @@ Layout layout(const kda_desc_t& d, int items, int workers) {
 }
 }  // namespace
 
-size_t ssm_plan_workspace(const kda_desc_t& d, int items, int workers) {
-  return layout(d, items, workers).end;
+// Where no sequence can be long enough to be cut, none is long enough for its place in the order to
+// matter: the sequences are taken as they come, in one launch.
+static bool may_cut(const kda_desc_t& d, int min_part) {
+  return d.total_tokens > (int64_t)(min_part + min_part / 2 + 4) * kSsmChunk;
+}
+
+size_t ssm_plan_workspace(const kda_desc_t& d, int items, int workers, int min_part) {
+  return may_cut(d, min_part) ? layout(d, items, workers).end : kWsPayload;
 }
 
 SsmPlan ssm_plan(const SsmArgs& a, int items, int workers, int min_part) {
   const Layout l = layout(a.d, items, workers);
   SsmPlan p;
-  // Where no sequence can be long enough to be cut, none is long enough for its place in the order to
-  // matter: the sequences are taken as they come, in one launch.
-  p.lists = a.ws_bytes >= l.lists_end && a.d.total_tokens > (int64_t)(min_part + min_part / 2 + 4) * kSsmChunk;
+  p.lists = a.ws_bytes >= l.lists_end && may_cut(a.d, min_part);
   p.cap = p.lists && a.ws_bytes >= l.end ? l.cap : 0;
   p.items = items;
   p.workers = workers;

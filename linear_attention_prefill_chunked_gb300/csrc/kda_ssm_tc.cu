@@ -1389,7 +1389,7 @@ bool ssm_tc_supported(const kda_desc_t& d) {
 }
 
 size_t ssm_tc_workspace(const kda_desc_t& d) {
-  return ssm_plan_workspace(d, items_a_sequence(d), gpu_sms());
+  return ssm_plan_workspace(d, items_a_sequence(d), gpu_sms(), kMinPart);
 }
 
 cudaError_t launch_ssm_tc(const SsmArgs& a, cudaStream_t st) {
