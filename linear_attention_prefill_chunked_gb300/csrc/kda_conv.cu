@@ -379,7 +379,7 @@ cudaError_t launch_strips(const ConvArgs& a, cudaStream_t st) {
 template <typename T, int VEC, int W>
 cudaError_t launch_prompt(const ConvArgs& a, cudaStream_t st) {
   const int64_t blocks = (a.d.total_tokens / (32 * kStrips)) * (a.d.channels / (kLanes * VEC));
-  return blocks >= 608 ? launch_strips<T, VEC, W, 32>(a, st) : launch_strips<T, VEC, W, 8>(a, st);
+  return blocks >= 4 * gpu_sms() ? launch_strips<T, VEC, W, 32>(a, st) : launch_strips<T, VEC, W, 8>(a, st);
 }
 
 template <typename T, int VEC, int W>

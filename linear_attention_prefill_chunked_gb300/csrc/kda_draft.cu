@@ -281,10 +281,11 @@ cudaError_t commit_as(int N, int64_t row, const void* cache, int64_t pitch, int 
 cudaError_t launch_verify(int N, int64_t T, int vocab, const int32_t* tokens, const float* p,
                           const float* q, const float* u, const float* noise, const int32_t* cu,
                           int32_t* kept, int32_t* next, uint32_t* status, uint32_t flags, cudaStream_t st) {
-  // a CTA a request fills the GPU from a few hundred requests on; below that the row is shared
+  // a CTA a request fills the GPU from two an SM on; below that the row is shared
+  const int sms = gpu_sms();
   int ranks = 1;
-  while (ranks < kMaxRanks && (int64_t)N * ranks < 304 && (int64_t)ranks * 4096 < vocab) ranks *= 2;
-  const bool few = (int64_t)N * ranks <= 152;
+  while (ranks < kMaxRanks && (int64_t)N * ranks < 2 * sms && (int64_t)ranks * 4096 < vocab) ranks *= 2;
+  const bool few = (int64_t)N * ranks <= sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((N + 1) * ranks));  // (num_seqs is at most 2^27)
   cfg.blockDim = dim3(few ? 512 : 256);

@@ -139,6 +139,9 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st);
 // Operators of the layers around the recurrence (kda_conv.cu, kda_ssm.cu, kda_draft.cu).
 namespace kda {
 
+// SMs of the current device (152, for sizes asked for where there is none).
+int gpu_sms();
+
 // Their status word is written by one block, which looks every sequence and slot over before
 // anything else of its work, so that a call needs no clear of the word in front of the kernel
 // (one stream operation less a call).  The debug build, where any block may add

@@ -62,7 +62,5 @@ SsmPlan ssm_plan(const SsmArgs& a, int items, int workers, int min_part);
 size_t ssm_plan_workspace(const kda_desc_t& d, int items, int workers, int min_part);
 cudaError_t launch_ssm_plan(const SsmPlan& p, const SsmArgs& a, cudaStream_t st);
 cudaError_t launch_ssm_combine(const SsmPlan& p, const SsmArgs& a, cudaStream_t st);
-// SMs of the current device (152, for sizes asked for where there is none).
-int gpu_sms();
 
 }  // namespace kda
