@@ -127,8 +127,8 @@ ssm_scan_simt_kernel(kda_ssm_inputs_t in, const ST* state_in, const int32_t* __r
   __shared__ float2 s_step[kStage];         // step and decay of a token
 
   const int tid = threadIdx.x, tiles = V / VT;
-  if (kState) grid_release();
-  grid_wait();
+  if (kState) tc::grid_dep_launch_dependents();
+  tc::grid_dep_wait();
   const int e = (int)(blockIdx.x / (unsigned)(H * tiles)), q = (int)(blockIdx.x % (unsigned)(H * tiles));
   const int h = q / tiles, v0 = q % tiles * VT;
   Entry en{e, 0, 0, -1, 1, {0, 0, 0}};

@@ -31,7 +31,7 @@ ssm_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ idx,
   __shared__ unsigned long long s_chunks;
   __shared__ uint32_t s_parts, s_splits;
   const int tid = threadIdx.x;
-  grid_release();
+  tc::grid_dep_launch_dependents();
   check_all(&hdr->status, cu, idx, N, T, T, idx ? num_slots : 0);
   if (tid == 0) {
     s_chunks = 0;
@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(256)
 ssm_combine_kernel(const PlanHdr* __restrict__ hdr, const Split* __restrict__ splits, float* scratch,
                    const float* __restrict__ decay, const ST* __restrict__ state_in, int64_t slot_stride, int H,
                    int KV) {
-  grid_release();
-  grid_wait();
+  tc::grid_dep_launch_dependents();
+  tc::grid_dep_wait();
   const int64_t whole = (int64_t)H * KV;
   const int64_t at = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
   if (at >= whole) return;

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "kda_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace kda {
 
@@ -22,13 +23,11 @@ struct PlanHdr {  // over the workspace header
 };
 static_assert(sizeof(PlanHdr) <= sizeof(WsHeader), "the plan's header lies in the workspace header");
 
-// The passes of a call follow one another on the stream, each small beside the setting up of the next:
-// a pass lets the next one's blocks start as soon as its own have (grid_release), and those wait, before
-// they touch global memory, until the pass is over (grid_wait), and so every pass before it. The plan
-// itself waits for all earlier work, and what follows the call waits for its last pass, as usual. (8192
-// tokens of 64 heads 132 -> 128 us a call, a ragged fp32 batch of 2209 tokens 58 -> 51 us.)
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The passes of a call follow one another on the stream, each small beside the setting up of the next: a
+// pass lets the next one's blocks start as soon as its own have (grid_dep_launch_dependents), and those
+// wait, before they touch global memory, until the pass is over (grid_dep_wait), and so every pass before
+// it. The plan itself waits for all earlier work, and what follows the call waits for its last pass, as
+// usual. (8192 tokens of 64 heads 132 -> 128 us a call, a ragged fp32 batch of 2209 tokens 58 -> 51 us.)
 // after: the kernel follows one of this call's passes on the stream, and waits for it itself.
 template <typename... P, typename... A>
 cudaError_t launch_pass(void (*kern)(P...), dim3 grid, int block, size_t smem, bool after, cudaStream_t st,

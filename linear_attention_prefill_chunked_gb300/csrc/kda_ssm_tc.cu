@@ -298,14 +298,6 @@ __device__ __forceinline__ void tmem_ld_16x256_x4(uint32_t taddr, float (&v)[16]
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_ld_16x256_x2(uint32_t taddr, float (&v)[8]) {
-  uint32_t r[8];
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
 __device__ __forceinline__ void tmem_st_16x128_x4(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
@@ -1232,9 +1224,9 @@ __device__ void run_weighted(const ScanParams& p, uint8_t* sm, Ctl* c, uint32_t 
 // Barriers and TMEM; false: the CTA leaves.
 template <bool kState>
 __device__ __forceinline__ bool tc_begin(const ScanParams& p, Ctl* c) {
-  if (kState) grid_release();
+  if (kState) grid_dep_launch_dependents();
   if (smem_u32(ssm_smem) & 1023u) {  // the swizzled tiles need it; the window starts so without static smem
-    grid_wait();
+    grid_dep_wait();
     if (threadIdx.x == 0) raise_status(p.status, KDA_DEVICE_PIPE_TIMEOUT);
     return false;
   }
@@ -1267,7 +1259,7 @@ __device__ __forceinline__ bool tc_begin(const ScanParams& p, Ctl* c) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  grid_wait();
+  grid_dep_wait();
   return true;
 }
 __device__ __forceinline__ void tc_end(const ScanParams& p, uint32_t tbase) {
