@@ -339,9 +339,11 @@ typedef struct {
  *           pool mode updates the slots in place; dense mode reads state (NULL: zeros) and
  *           writes final_state (NULL: not written; may equal state).  A sequence of length
  *           zero keeps its state.
- * Sums are fp32, rounded once to dtype.  Any Ch >= 1 and any alignment of whole elements;
- * rows that are 16-byte aligned are moved 16 bytes at a time.  Rows of x that belong to no valid
- * sequence give no output.
+ * Sums are fp32, rounded once to dtype.  Any Ch >= 1 and any alignment of whole elements; where
+ * Ch, the pitches and the pointers are multiples of four elements a thread moves four channels at
+ * a time (8 bytes in bf16, 16 in fp32), else one.  Rows of x that belong to no valid sequence give
+ * no output; where lengths run backwards, so that sequences overlap, neither do the first W-1
+ * tokens of a sequence whose first token went to another.
  */
 kda_status_t kda_causal_conv(const kda_conv_desc_t *desc, const void *x, const void *weight,
                              const void *bias, const int32_t *cu_seqlens, void *state,
@@ -391,6 +393,17 @@ typedef struct {
  * or 0).  y [T, H, V] packed, qkv_dtype, 16-byte aligned.  cu_seqlens, state, state_indices,
  * final_state: as in kda_chunk_prefill (pool or dense mode, [K][V] layout).  Run to run, results
  * are bit-identical for the same inputs and workspace size.
+ *
+ * fp32 inputs, and all with KDA_FLAG_CUDA_CORE_PATH, run in fp32 throughout.  bf16 inputs run on the
+ * tensor cores, in chunks of 64 tokens: within a chunk the products c_t . b_s, weighted by step and
+ * decay, and for the rest the state that c reads are rounded to bf16 once each, as is y; steps,
+ * decays and the state are fp32.  What enters the state is exact in 24 bits (16 for a bf16 pool), but
+ * its accumulator cuts every sum of 16 tokens' products off to 24 bits, up to three times: a state
+ * that hardly fades is off by up to 3 (T / 16) 2^-23 of itself after T tokens (1e-4 at 4500), one
+ * that does by as much for T the tokens it remembers.  A token's log-decay counts as -256 ln 2 at
+ * least, past which nothing of fp32 is left, and exp(a_log) as the largest fp32 number at most.
+ * What is no number reaches what it would reach by the recurrence (outputs may be NaN where that has
+ * an infinity); a weighted product c_t . b_s past 3.4e38 counts as such for all heads of its group.
  */
 kda_status_t kda_ssm_scan(const kda_desc_t *desc, const kda_ssm_inputs_t *in,
                           const int32_t *cu_seqlens, void *state, const int32_t *state_indices,

@@ -3,10 +3,11 @@
 //   y_t = act(bias + sum_{i < W} w_i x_{t-(W-1)+i})      per channel, W = 2..4
 //
 // 2 W operations a value against 2 elements moved: the kernels are bound by HBM, so the design
-// is one pass over x and y with 16-byte accesses and enough of them in flight.
+// is one pass over x and y, four channels a thread (one where rows are not aligned to four), with
+// enough rows in flight.
 //
-// Prompts: the packed tokens are cut into strips of kStrip; a thread walks one strip for 16 bytes
-// of channels with the last W-1 inputs in registers, so x is read once but for the W-1 rows before
+// Prompts: the packed tokens are cut into strips of kStrip; a thread walks one strip for its
+// channels with the last W-1 inputs in registers, so x is read once but for the W-1 rows before
 // a strip (from L2).  Sequences are found per block from cu_seqlens (every block looks through all
 // of it; no order is assumed), which leaves each token's sequence and position in shared memory.
 // The first W-1 tokens of a sequence need its state, which the call also overwrites in pool mode:
@@ -29,7 +30,8 @@ constexpr int kConvThreads = kLanes * kStrips;
 // (1.6 GB) against 277 us, 5.8 TB/s or 86 % of a copy's rate, with 4 channels, eight rows in flight and
 // three blocks an SM (four blocks: 282 us with four rows in flight, 316 with eight, which then spill).
 // One channel a thread has less in flight, so there five blocks share an SM: 155 us for 16384 x 8193 in
-// bf16 (with three: 189; 8192 channels, four a thread: 99), 227 us in fp32 (with two: 304; 211).
+// bf16 (with three: 189; 8192 channels, four a thread: 99), 227 us in fp32 (with two: 304; 211), of dense
+// states; with a pool and SiLU 168 and 232 (8192 channels: 106 and 228).
 template <typename T, int VEC> struct Row;
 template <> struct Row<float, 4> {
   using Raw = uint4;
@@ -68,8 +70,9 @@ template <typename T> struct Row<T, 1> {
   static __device__ __forceinline__ Raw zero() { return from_f32<T>(0.f); }
 };
 
-// s * sigmoid(s) = s / (1 + e^-s).  The fast exponential and reciprocal are good to ~2^-21, far
-// below a bf16 result's rounding; fp32 results take the accurate ones.
+// s * sigmoid(s) = s / (1 + e^-s).  The fast exponential and reciprocal are good to ~2^-21 plus what the
+// exponent's rounding to 24 bits does, |s| 2^-24 (2^-18 at s = -80): far below a bf16 result's rounding.
+// fp32 results take the accurate ones.
 template <typename T, int VEC> __device__ __forceinline__ void silu(float* s) {
 #pragma unroll
   for (int i = 0; i < VEC; ++i) s[i] = s[i] / (1.f + expf(-s[i]));
@@ -303,7 +306,7 @@ conv_prompt_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict
   KDA_DEBUG_FOLD(status);
 }
 
-// One token, or a few drafted ones, a row: a thread holds the W-1 inputs of 16 bytes of channels.
+// One token, or a few drafted ones, a row: a thread holds the W-1 inputs of four channels (or one).
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(128)
 conv_token_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict__ w,

@@ -25,10 +25,12 @@
 //   S^T [128][k]  += X'^T B     A = x' (TMEM), B = b tile                                N = K
 //
 // S^T stays in TMEM in fp32 for the whole sequence. x'_s = exp(..) d_s x_s is fp32; it enters as
-// the sum of three bf16 numbers, which hold all its 24 bits (two with a bf16 pool, 2^-16), so that
-// the state keeps fp32 accuracy -- b is exact in bf16. M and the copy of S that C reads are rounded
-// to bf16 once each, like the output. (The scores as 16 x 16 warp-level products, which need no trip
-// through TMEM, took 2100 cycles a chunk against some 500 of the tensor pipe.)
+// the sum of three bf16 numbers, which hold all its 24 bits (two with a bf16 pool, 2^-16); b is exact in
+// bf16. The accumulator cuts each sum of 16 tokens' products, in each part, off to 24 bits: a state that
+// fades within some hundred tokens has fp32 accuracy, one that does not is off by up to 3 (T / 16) 2^-23
+// of itself after T tokens. M and the copy of S that C reads are rounded to bf16 once each, like the
+// output. (The scores as 16 x 16 warp-level products, which need no trip through TMEM, took 2100 cycles a
+// chunk against some 500 of the tensor pipe.)
 //
 // Shared memory's bandwidth is what the products and the warps compete for (with x' as a tile there,
 // and x and y read and written by TMEM lane, two bytes at a time, 3350 wavefronts a chunk): x' goes
@@ -41,10 +43,15 @@
 // the loads, lets what was issued finish and returns). Only T_SU -> R -> T_S -> products of C and x' ->
 // T_SU is a chain from chunk to chunk; scans, scores, M and the arithmetic of x' run ahead of it.
 //
-// 32768 tokens of 32 heads (V = 128) take 232 us, against 109 us for the bytes at a copy's rate: a chunk
-// is ~3800 cycles, of which the products take 2100 (their pipe gives one M = 128, N = 64 step of 16 in 52
-// cycles, N = 128 in 71) and the chain of barriers, TMEM reads and writes between them the rest; the
-// schedulers issue on 55 % of the cycles.
+// 32768 tokens of 32 heads (V = 128) take 236 us, against 109 us for the bytes at a copy's rate: a chunk
+// is ~3900 cycles, of which the products take 2100 (one M = 128, N = 64 step of 16 after the other comes
+// every 52 cycles, N = 128 every 71, of which the pipe works 32 and 64) and the chain of barriers, TMEM
+// reads and writes between them the rest; the schedulers issue on 59 % of the cycles.
+//
+// What is no number. A zero weight does not hide it in a product, so it stays out of those that would take
+// it where the recurrence does not: a step goes to its own head's rows by e and dec alone (scan_steps), an x
+// leaves its tile for the product with M (hide_x) and comes back as NaN for the outputs from its token on
+// (spoil_x). B and C are a group's, and reach its heads alone.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
