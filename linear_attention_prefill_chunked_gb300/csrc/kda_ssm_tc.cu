@@ -590,7 +590,7 @@ __device__ void run_state(uint8_t* sm, Ctl* c, uint32_t tbase) {
 // functions; good to ~4e-7 with the fast exponential and quotient. The exponent -|x| log2 e is rounded to 24
 // bits, which alone would be 4e-6 at |x| = 80: u takes what the rounding left out as a factor.
 __device__ __forceinline__ float softplus_fast(float x) {
-  const float a = fmaxf(-fabsf(x), -150.f);  // u is zero from -104 on
+  const float a = fmaxf(-fabsf(x), -150.f);  // u is zero from -88 on
   const float hi = a * 1.44269502f;
   float u = ex2(hi);
   u = fmaf(u, fmaf(hi, -0.693147182f, a), u);
