@@ -422,6 +422,77 @@ kda_status_t kda_ssm_decode(const kda_desc_t *desc, const kda_ssm_inputs_t *in,
                             int64_t cache_pitch_elems, int32_t max_steps, int update_pool, void *y,
                             void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* Problem descriptor of the gated linear recurrence. */
+typedef struct {
+    int32_t num_seqs;          /* N sequences, rows or requests                         */
+    int64_t total_tokens;      /* T: rows of x, r, i and y                              */
+    int32_t channels;          /* Ch                                                    */
+    kda_dtype_t dtype;         /* of x, r, i, y and the gradients; states are fp32      */
+    int64_t x_pitch;           /* elements between consecutive rows, >= Ch              */
+    int64_t r_pitch;
+    int64_t i_pitch;           /* not used without i                                    */
+    int64_t num_slots;         /* pool: rows                                            */
+    int64_t slot_stride_elems; /* pool: elements between slots; 0 means Ch              */
+} kda_gated_desc_t;
+
+/*
+ * Gated linear recurrence over packed sequences, per channel:
+ *
+ *     a_t = exp(-exp(a_log) sigmoid(r_t))
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t          y_t = h_t
+ *
+ *   x, r, i  [T, Ch], rows at their pitches; i NULL: x_t enters without its gate
+ *   a_log    [Ch] fp32              y [T, Ch] packed, must not overlap an input
+ *   state, state_indices, final_state  as in kda_causal_conv, each state being [Ch] fp32
+ *   carries  NULL, or [ceil(T / KDA_GATED_CARRY_ROWS), Ch] fp32: the state before each row
+ *            whose number is a multiple of KDA_GATED_CARRY_ROWS, for the backward pass
+ *   workspace  kda_gated_scan_workspace_size(desc) bytes
+ *
+ * Everything is fp32 inside, y rounded once; fp32 inputs take CUDA's accurate exponential, bf16 ones the
+ * fast one (relative errors of 2^-20 in the states).  exp(a_log) counts as the largest fp32 number at
+ * most.  Any Ch >= 1 and any alignment of whole elements; where Ch, the pitches and the pointers are
+ * multiples of two elements a thread moves two channels at a time.  Rows of x that belong to no valid
+ * sequence give no output; where lengths run backwards, so that sequences overlap, a row goes to the last
+ * of its sequences and the others' outputs are unspecified.  Results are bit-identical from run to run.
+ */
+#define KDA_GATED_CARRY_ROWS 64
+kda_status_t kda_gated_scan(const kda_gated_desc_t *desc, const void *x, const void *r,
+                            const void *i, const float *a_log, const int32_t *cu_seqlens,
+                            float *state, const int32_t *state_indices, float *final_state,
+                            void *y, float *carries, void *workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+size_t kda_gated_scan_workspace_size(const kda_gated_desc_t *desc); /* 0 on an invalid one */
+
+/*
+ * Its backward pass, from the derivatives of a loss by y and (dfinal, or NULL) by the final states.
+ *
+ *   dy       [T, Ch] dtype, rows dy_pitch elements apart
+ *   x, r, i, a_log, cu_seqlens, state  as the forward call had them (dense mode; state NULL: zeros)
+ *   carries  as the forward call left them
+ *   dx, dr, di  [T, Ch] dtype, packed; di NULL where i is.  Rows of no valid sequence get 0.
+ *   da_log   [Ch] fp32: sums over all rows, in a fixed order
+ *   dstate   NULL or [N, Ch] fp32: by the initial states (0 for an invalid sequence)
+ *   workspace  kda_gated_scan_backward_workspace_size(desc) bytes
+ *
+ * Derivatives are fp32 inside and rounded once.  Where sqrt(1 - a^2) is 0 (a gate that is shut or a rate
+ * of 0), so is what its derivative adds to dr and da_log.
+ */
+kda_status_t kda_gated_scan_backward(const kda_gated_desc_t *desc, const void *dy, int64_t dy_pitch,
+                                     const void *x, const void *r, const void *i,
+                                     const float *a_log, const int32_t *cu_seqlens,
+                                     const float *carries, const float *state, const float *dfinal,
+                                     void *dx, void *dr, void *di, float *da_log, float *dstate,
+                                     void *workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t kda_gated_scan_backward_workspace_size(const kda_gated_desc_t *desc);
+
+/* One token a row, or drafted tokens a request: the arguments of kda_causal_conv_decode, with step
+ * states of Ch elements in fp32. */
+kda_status_t kda_gated_decode(const kda_gated_desc_t *desc, const void *x, const void *r,
+                              const void *i, const float *a_log, const int32_t *cu_seqlens,
+                              float *state_pool, const int32_t *state_indices, float *step_cache,
+                              int64_t cache_pitch_elems, int32_t max_steps, int update_pool, void *y,
+                              void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /*
  * Verification of drafted tokens from given random numbers.  Request n was fed the tokens
  * cu_seqlens[n] .. cu_seqlens[n+1]-1 (as for kda_decode_draft): its last sampled token, then the

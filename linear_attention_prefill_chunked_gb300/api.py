@@ -59,7 +59,9 @@ EXPORTS = ("kda_chunk_prefill_workspace_size", "kda_chunk_prefill_min_workspace_
            "kda_chunk_prefill_noalloc", "kda_chunk_prefill_act", "kda_decode_draft",
            "kda_set_pipeline_wait_limit", "kda_causal_conv", "kda_causal_conv_decode", "kda_ssm_scan",
            "kda_ssm_scan_workspace_size", "kda_ssm_decode", "kda_verify_draft",
-           "kda_verify_draft_marked", "kda_commit_draft")
+           "kda_verify_draft_marked", "kda_commit_draft", "kda_gated_scan",
+           "kda_gated_scan_workspace_size", "kda_gated_scan_backward",
+           "kda_gated_scan_backward_workspace_size", "kda_gated_decode")
 
 _lib = None
 

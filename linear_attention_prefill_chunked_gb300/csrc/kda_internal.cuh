@@ -281,6 +281,37 @@ __device__ __forceinline__ float ssm_rate(float a_log, float unit = 1.f) {
 // Step size of one (token, head): softplus(dt + bias).
 __device__ __forceinline__ float ssm_step(float dt, float bias) { return softplus_f32(dt + bias); }
 
+struct GatedArgs {
+  kda_gated_desc_t d;
+  const void *x, *r, *i;      // i null: no input gate
+  const float* a_log;
+  const int32_t* cu;          // null: one token a row
+  const float* state_in;      // pool, dense initial states or null
+  const int32_t* idx;         // null: dense, or slot n in the token form
+  float* state_out;           // pool, dense final states or null
+  int64_t slot_stride;
+  void* y;
+  float* carries;             // written by the forward pass, read by the backward pass
+  uint8_t* ws;
+  // token form
+  float* cache;
+  int64_t cache_pitch;
+  int max_steps;
+  bool update_pool;
+  // backward pass
+  const void* dy;
+  int64_t dy_pitch;
+  const float* dfinal;
+  void *dx, *dr, *di;
+  float *da_log, *dstate;
+};
+size_t gated_scan_workspace(const kda_gated_desc_t& d);  // the whole workspace, header included
+size_t gated_back_workspace(const kda_gated_desc_t& d);
+bool gated_fits(const kda_gated_desc_t& d);
+cudaError_t launch_gated_scan(const GatedArgs& a, cudaStream_t st);
+cudaError_t launch_gated_back(const GatedArgs& a, cudaStream_t st);
+cudaError_t launch_gated_token(const GatedArgs& a, cudaStream_t st);
+
 cudaError_t launch_verify(int N, int64_t T, int vocab, const int32_t* tokens, const float* p,
                           const float* q, const float* u, const float* noise, const int32_t* cu,
                           int32_t* kept, int32_t* next, uint32_t* status, uint32_t flags, cudaStream_t st);

@@ -64,6 +64,16 @@ bool ssm_inputs_ok(const kda_desc_t* d, const kda_ssm_inputs_t* in) {
          elem_aligned(in->dt, d->qkv_dtype);
 }
 
+bool gated_ok(const kda_gated_desc_t* d) {
+  return d && d->num_seqs >= 0 && d->total_tokens >= 0 && d->total_tokens <= 0x7fffffffll && d->channels > 0 &&
+         (d->dtype == KDA_BF16 || d->dtype == KDA_F32);
+}
+bool gated_inputs_ok(const kda_gated_desc_t* d, const void* x, const void* r, const void* i, const float* a_log) {
+  if (!a_log || !elem_aligned(a_log, KDA_F32) || (d->total_tokens > 0 && (!x || !r))) return false;
+  return elem_aligned(x, d->dtype) && elem_aligned(r, d->dtype) && elem_aligned(i, d->dtype) &&
+         d->x_pitch >= d->channels && d->r_pitch >= d->channels && (!i || d->i_pitch >= d->channels);
+}
+
 }  // namespace
 
 extern "C" {
@@ -213,6 +223,116 @@ kda_status_t kda_ssm_decode(const kda_desc_t* d, const kda_ssm_inputs_t* in,
   a.max_steps = cu_seqlens ? max_steps : 1;
   a.update_pool = update_pool != 0;
   return launched(workspace, stream, [&] { return kda::launch_ssm_decode(a, stream); });
+}
+
+size_t kda_gated_scan_workspace_size(const kda_gated_desc_t* d) {
+  return gated_ok(d) && kda::gated_fits(*d) ? kda::gated_scan_workspace(*d) : 0;
+}
+
+size_t kda_gated_scan_backward_workspace_size(const kda_gated_desc_t* d) {
+  return gated_ok(d) && kda::gated_fits(*d) ? kda::gated_back_workspace(*d) : 0;
+}
+
+kda_status_t kda_gated_scan(const kda_gated_desc_t* d, const void* x, const void* r, const void* i,
+                            const float* a_log, const int32_t* cu_seqlens, float* state,
+                            const int32_t* state_indices, float* final_state, void* y, float* carries,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!gated_ok(d) || !gated_inputs_ok(d, x, r, i, a_log) || !cu_seqlens || !ws_ok(workspace))
+    return KDA_ERR_INVALID_ARGUMENT;
+  if (!kda::gated_fits(*d)) return KDA_ERR_UNSUPPORTED;
+  if (d->total_tokens > 0 && !y) return KDA_ERR_INVALID_ARGUMENT;
+  const bool pool = state_indices != nullptr;
+  const int64_t stride = pool && d->slot_stride_elems != 0 ? d->slot_stride_elems : d->channels;
+  if (pool && (!state || d->num_slots <= 0 || stride < d->channels ||
+               (final_state != nullptr && final_state != state)))
+    return KDA_ERR_INVALID_ARGUMENT;
+  if (!elem_aligned(y, d->dtype) || !elem_aligned(state, KDA_F32) || !elem_aligned(final_state, KDA_F32) ||
+      !elem_aligned(carries, KDA_F32))
+    return KDA_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < kda::gated_scan_workspace(*d)) return KDA_ERR_WORKSPACE_TOO_SMALL;
+  if (d->num_seqs == 0) return clear_status(workspace, stream);
+  kda::GatedArgs a{};
+  a.d = *d;
+  a.x = x; a.r = r; a.i = i; a.a_log = a_log;
+  a.cu = cu_seqlens;
+  a.state_in = state;
+  a.idx = state_indices;
+  a.state_out = pool ? state : final_state;
+  a.slot_stride = stride;
+  a.y = y;
+  a.carries = carries;
+  a.ws = static_cast<uint8_t*>(workspace);
+  return launched(workspace, stream, [&] { return kda::launch_gated_scan(a, stream); });
+}
+
+kda_status_t kda_gated_scan_backward(const kda_gated_desc_t* d, const void* dy, int64_t dy_pitch, const void* x,
+                                     const void* r, const void* i, const float* a_log,
+                                     const int32_t* cu_seqlens, const float* carries, const float* state,
+                                     const float* dfinal, void* dx, void* dr, void* di, float* da_log,
+                                     float* dstate, void* workspace, size_t workspace_bytes,
+                                     cudaStream_t stream) {
+  if (!gated_ok(d) || !gated_inputs_ok(d, x, r, i, a_log) || !cu_seqlens || !ws_ok(workspace) || !da_log ||
+      dy_pitch < d->channels)
+    return KDA_ERR_INVALID_ARGUMENT;
+  if (!kda::gated_fits(*d)) return KDA_ERR_UNSUPPORTED;
+  if (d->total_tokens > 0 && (!dy || !carries || !dx || !dr || !di != !i)) return KDA_ERR_INVALID_ARGUMENT;
+  {
+    const void* rows[] = {dy, dx, dr, di};
+    for (const void* p : rows)
+      if (!elem_aligned(p, d->dtype)) return KDA_ERR_INVALID_ARGUMENT;
+    const void* floats[] = {carries, state, dfinal, da_log, dstate};
+    for (const void* p : floats)
+      if (!elem_aligned(p, KDA_F32)) return KDA_ERR_INVALID_ARGUMENT;
+  }
+  if (workspace_bytes < kda::gated_back_workspace(*d)) return KDA_ERR_WORKSPACE_TOO_SMALL;
+  kda::GatedArgs a{};
+  a.d = *d;
+  a.x = x; a.r = r; a.i = i; a.a_log = a_log;
+  a.cu = cu_seqlens;
+  a.state_in = state;
+  a.slot_stride = d->channels;
+  a.carries = const_cast<float*>(carries);
+  a.dy = dy;
+  a.dy_pitch = dy_pitch;
+  a.dfinal = dfinal;
+  a.dx = dx; a.dr = dr; a.di = di;
+  a.da_log = da_log;
+  a.dstate = dstate;
+  a.ws = static_cast<uint8_t*>(workspace);
+  return launched(workspace, stream, [&] { return kda::launch_gated_back(a, stream); });
+}
+
+kda_status_t kda_gated_decode(const kda_gated_desc_t* d, const void* x, const void* r, const void* i,
+                              const float* a_log, const int32_t* cu_seqlens, float* state_pool,
+                              const int32_t* state_indices, float* step_cache, int64_t cache_pitch_elems,
+                              int32_t max_steps, int update_pool, void* y, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+  if (!gated_ok(d) || !gated_inputs_ok(d, x, r, i, a_log) || !ws_ok(workspace)) return KDA_ERR_INVALID_ARGUMENT;
+  if (d->channels > 65535 * 128) return KDA_ERR_UNSUPPORTED;  // grid.y holds 128 channels a block at least
+  if (d->total_tokens > 0 && !y) return KDA_ERR_INVALID_ARGUMENT;
+  if (!cu_seqlens && d->total_tokens != d->num_seqs) return KDA_ERR_INVALID_ARGUMENT;
+  const int64_t stride = d->slot_stride_elems != 0 ? d->slot_stride_elems : d->channels;
+  if ((d->num_seqs > 0 && !state_pool) || d->num_slots <= 0 || stride < d->channels || max_steps < 1)
+    return KDA_ERR_INVALID_ARGUMENT;
+  if (step_cache && cache_pitch_elems / max_steps < d->channels) return KDA_ERR_INVALID_ARGUMENT;
+  if (!elem_aligned(y, d->dtype) || !elem_aligned(state_pool, KDA_F32) || !elem_aligned(step_cache, KDA_F32))
+    return KDA_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < KDA_STATUS_WORKSPACE_BYTES) return KDA_ERR_WORKSPACE_TOO_SMALL;
+  if (d->num_seqs == 0) return clear_status(workspace, stream);
+  kda::GatedArgs a{};
+  a.d = *d;
+  a.x = x; a.r = r; a.i = i; a.a_log = a_log;
+  a.cu = cu_seqlens;
+  a.state_in = a.state_out = state_pool;
+  a.idx = state_indices;
+  a.slot_stride = stride;
+  a.y = y;
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.cache = step_cache;
+  a.cache_pitch = cache_pitch_elems;
+  a.max_steps = cu_seqlens ? max_steps : 1;
+  a.update_pool = update_pool != 0;
+  return launched(workspace, stream, [&] { return kda::launch_gated_token(a, stream); });
 }
 
 kda_status_t kda_verify_draft(int32_t num_seqs, int64_t total_tokens, int32_t vocab,

@@ -33,6 +33,13 @@ class KdaSsmInputs(ctypes.Structure):
                 ("d", _P)]
 
 
+class KdaGatedDesc(ctypes.Structure):
+    """Mirror of ``kda_gated_desc_t`` in include/kda.h."""
+    _fields_ = [("num_seqs", _I32), ("total_tokens", _I64), ("channels", _I32), ("dtype", ctypes.c_int),
+                ("x_pitch", _I64), ("r_pitch", _I64), ("i_pitch", _I64), ("num_slots", _I64),
+                ("slot_stride_elems", _I64)]
+
+
 _lib = None
 
 
@@ -41,7 +48,7 @@ def _load():
     if _lib is None:
         lib = api.load()
         size, desc, conv = ctypes.c_size_t, ctypes.POINTER(KdaDesc), ctypes.POINTER(KdaConvDesc)
-        ins = ctypes.POINTER(KdaSsmInputs)
+        ins, gated = ctypes.POINTER(KdaSsmInputs), ctypes.POINTER(KdaGatedDesc)
         for name, args, res in (
                 ("kda_causal_conv", [conv, *[_P] * 9, size, _P], ctypes.c_int),
                 ("kda_causal_conv_decode",
@@ -50,6 +57,12 @@ def _load():
                 ("kda_ssm_scan_workspace_size", [desc], size),
                 ("kda_ssm_decode",
                  [desc, ins, *[_P] * 4, _I64, _I32, ctypes.c_int, _P, _P, size, _P], ctypes.c_int),
+                ("kda_gated_scan", [gated, *[_P] * 11, size, _P], ctypes.c_int),
+                ("kda_gated_scan_workspace_size", [gated], size),
+                ("kda_gated_scan_backward", [gated, _P, _I64, *[_P] * 14, size, _P], ctypes.c_int),
+                ("kda_gated_scan_backward_workspace_size", [gated], size),
+                ("kda_gated_decode",
+                 [gated, *[_P] * 8, _I64, _I32, ctypes.c_int, _P, _P, size, _P], ctypes.c_int),
                 ("kda_verify_draft", [_I32, _I64, _I32, *[_P] * 9, size, _P], ctypes.c_int),
                 ("kda_verify_draft_marked",
                  [_I32, _I64, _I32, *[_P] * 8, ctypes.c_uint32, _P, size, _P], ctypes.c_int),
@@ -473,6 +486,154 @@ def ssm_decode_draft(x, dt, A_log, B, C, cu_seqlens, pool, state_indices=None, *
     return _ssm_token(x, dt, A_log, B, C, cu_seqlens, pool, state_indices, D, dt_bias, cache,
                       _steps(cu_seqlens, max_steps, stream), update_pool, slot_stride, out, workspace, stream,
                       ssm_decode_draft)
+
+
+# ------------------------------------------------------------------------ gated linear recurrence
+
+CARRY_ROWS = 64  # KDA_GATED_CARRY_ROWS
+
+
+def check_gated_args(x, r, A_log, *, i=None, cu_seqlens=None, state=None, state_indices=None,
+                     final_state=None, out=None, slot_stride=0, token=False):
+    """Checks of a gated recurrence's call (host only); returns (N, T, channels, pitches of x, r, i)."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("x must be a bfloat16 or float32 tensor")
+    if x.dim() != 2 or x.shape[1] < 1:
+        raise ValueError(f"x must have shape [T, channels], got {list(x.shape)}")
+    dtype = x.dtype
+    T, ch = x.shape
+    pitches = (_rows(x, "x", (T, ch), dtype), _rows(r, "r", (T, ch), dtype),
+               ch if i is None else _rows(i, "i", (T, ch), dtype))
+    _plain(A_log, "A_log", torch.float32, (ch,))
+    N = T if cu_seqlens is None else _num_seqs(cu_seqlens)
+    if state_indices is not None:
+        _plain(state_indices, "state_indices", torch.int32, (N,))
+    if token or state_indices is not None:
+        if state is None:
+            raise ValueError("pool mode needs the pool in `state`")
+        _state_pool(state, "state", (ch,), slot_stride)
+        if state.dtype is not torch.float32:
+            raise TypeError(f"state must be float32, got {state.dtype}")
+        if final_state is not None and final_state is not state:
+            raise ValueError("pool mode updates the pool: final_state must be None or the pool")
+    else:
+        if state is not None:
+            _plain(state, "state", torch.float32, (N, ch))
+        if final_state is not None:
+            _plain(final_state, "final_state", torch.float32, (N, ch))
+    if out is not None:
+        _plain(out, "out", dtype, (T, ch))
+    return N, T, ch, pitches
+
+
+def _gated_desc(N, T, ch, dtype, pitches, num_slots=0, slot_stride=0):
+    return KdaGatedDesc(N, T, ch, _dt(dtype), *pitches, num_slots, slot_stride)
+
+
+def gated_scan(x, r, A_log, cu_seqlens, *, i=None, state=None, state_indices=None, final_state=None,
+               output_final_state=True, output_carries=False, slot_stride=0, out=None, workspace=None,
+               stream=None):
+    """Gated linear recurrence of packed sequences (kda_gated_scan), per channel
+    ``h = a h + sqrt(1 - a^2) sigmoid(i) x`` with ``a = exp(-exp(A_log) sigmoid(r))``.  Returns
+    ``(y, final)``, with ``output_carries`` ``(y, final, carries)``.
+
+    x, r and i [T, Ch] bf16 or fp32 (one dtype), their rows at any pitch; i None: x enters whole; A_log
+    [Ch] fp32; cu_seqlens [N+1] int32.  States are [Ch] fp32; pool and dense mode as in
+    :func:`causal_conv`.  ``carries`` [ceil(T / 64), Ch] fp32 is what :func:`gated_scan_backward` wants of
+    the forward pass.
+    """
+    N, T, ch, pitches = check_gated_args(
+        x, r, A_log, i=i, cu_seqlens=cu_seqlens, state=state, state_indices=state_indices,
+        final_state=final_state, out=out, slot_stride=slot_stride)
+    _cuda(x, r, A_log, cu_seqlens, i, state, state_indices, final_state, out, workspace)
+    lib, dev = _load(), x.device
+    pool = state_indices is not None
+    if pool:
+        final_state = state
+    elif final_state is None and output_final_state:
+        final_state = _empty(stream, (N, ch), torch.float32, dev)
+    if out is None:
+        out = _empty(stream, (T, ch), x.dtype, dev)
+    carries = None
+    if output_carries:
+        carries = _empty(stream, ((T + CARRY_ROWS - 1) // CARRY_ROWS, ch), torch.float32, dev)
+    d = _gated_desc(N, T, ch, x.dtype, pitches, state.shape[0] if pool else 0, slot_stride)
+    size = lib.kda_gated_scan_workspace_size(ctypes.byref(d))
+    ws, nws = _workspace(stream, workspace, max(size, STATUS_WORKSPACE_BYTES), dev)
+    rc = lib.kda_gated_scan(ctypes.byref(d), _p(x), _p(r), _p(i), _p(A_log), _p(cu_seqlens), _p(state),
+                            _p(state_indices), _p(final_state), _p(out), _p(carries), _p(ws), nws,
+                            _stream(stream, dev))
+    _done(rc, "kda_gated_scan", gated_scan, ws)
+    return (out, final_state, carries) if output_carries else (out, final_state)
+
+
+def gated_scan_backward(dy, x, r, A_log, cu_seqlens, carries, *, i=None, state=None, dfinal=None,
+                        workspace=None, stream=None):
+    """The derivatives of a loss by the inputs of a dense :func:`gated_scan` (kda_gated_scan_backward), from
+    those by y (``dy`` [T, Ch], rows at any pitch) and by the final states (``dfinal`` [N, Ch] fp32 or None).
+    Returns ``(dx, dr, di, dA_log, dstate)``: di None without i, dA_log [Ch] fp32, dstate [N, Ch] fp32 or
+    None without ``state``.
+
+    x, r, A_log, cu_seqlens, i and state as the forward call had them, carries as it returned them.
+    """
+    N, T, ch, pitches = check_gated_args(x, r, A_log, i=i, cu_seqlens=cu_seqlens, state=state)
+    dy_pitch = _rows(dy, "dy", (T, ch), x.dtype)
+    _plain(carries, "carries", torch.float32, ((T + CARRY_ROWS - 1) // CARRY_ROWS, ch))
+    if dfinal is not None:
+        _plain(dfinal, "dfinal", torch.float32, (N, ch))
+    _cuda(dy, x, r, A_log, cu_seqlens, carries, i, state, dfinal, workspace)
+    lib, dev = _load(), x.device
+    dx, dr = (_empty(stream, (T, ch), x.dtype, dev) for _ in range(2))
+    di = None if i is None else _empty(stream, (T, ch), x.dtype, dev)
+    da_log = _empty(stream, (ch,), torch.float32, dev)
+    dstate = None if state is None else _empty(stream, (N, ch), torch.float32, dev)
+    d = _gated_desc(N, T, ch, x.dtype, pitches)
+    size = lib.kda_gated_scan_backward_workspace_size(ctypes.byref(d))
+    ws, nws = _workspace(stream, workspace, max(size, STATUS_WORKSPACE_BYTES), dev)
+    rc = lib.kda_gated_scan_backward(ctypes.byref(d), _p(dy), dy_pitch, _p(x), _p(r), _p(i), _p(A_log),
+                                     _p(cu_seqlens), _p(carries), _p(state), _p(dfinal), _p(dx), _p(dr),
+                                     _p(di), _p(da_log), _p(dstate), _p(ws), nws, _stream(stream, dev))
+    _done(rc, "kda_gated_scan_backward", gated_scan_backward, ws)
+    return dx, dr, di, da_log, dstate
+
+
+def _gated_token(x, r, A_log, cu_seqlens, pool, state_indices, i, cache, max_steps, update_pool, slot_stride,
+                 out, workspace, stream, owner):
+    N, T, ch, pitches = check_gated_args(x, r, A_log, i=i, cu_seqlens=cu_seqlens, state=pool,
+                                         state_indices=state_indices, out=out, slot_stride=slot_stride,
+                                         token=True)
+    _cuda(x, r, A_log, i, cu_seqlens, pool, state_indices, cache, out, workspace)
+    cpitch = 0
+    if cache is not None:
+        cpitch = _step_cache(cache, "cache", N, max_steps, ch, torch.float32)
+    lib, dev = _load(), x.device
+    if out is None:
+        out = _empty(stream, (T, ch), x.dtype, dev)
+    ws, nws = _workspace(stream, workspace, STATUS_WORKSPACE_BYTES, dev)
+    d = _gated_desc(N, T, ch, x.dtype, pitches, pool.shape[0], slot_stride)
+    rc = lib.kda_gated_decode(ctypes.byref(d), _p(x), _p(r), _p(i), _p(A_log), _p(cu_seqlens), _p(pool),
+                              _p(state_indices), _p(cache), cpitch, max_steps, 1 if update_pool else 0, _p(out),
+                              _p(ws), nws, _stream(stream, dev))
+    _done(rc, "kda_gated_decode", owner, ws)
+    return out
+
+
+def gated_decode(x, r, A_log, pool, state_indices=None, *, i=None, slot_stride=0, out=None, workspace=None,
+                 stream=None):
+    """One step of the gated recurrence a row (kda_gated_decode), updating ``pool`` [num_slots, Ch] fp32 in
+    place; x, r and i [N, Ch].  Returns y [N, Ch]."""
+    return _gated_token(x, r, A_log, None, pool, state_indices, i, None, 1, True, slot_stride, out, workspace,
+                        stream, gated_decode)
+
+
+def gated_decode_draft(x, r, A_log, cu_seqlens, pool, state_indices=None, *, i=None, cache=None,
+                       max_steps=None, update_pool=False, slot_stride=0, out=None, workspace=None,
+                       stream=None):
+    """Steps of the gated recurrence of drafted tokens, as :func:`decode_draft`; ``cache`` [N, steps, Ch]
+    fp32 gets the state after each.  Returns y [T, Ch]."""
+    return _gated_token(x, r, A_log, cu_seqlens, pool, state_indices, i, cache,
+                        _steps(cu_seqlens, max_steps, stream), update_pool, slot_stride, out, workspace, stream,
+                        gated_decode_draft)
 
 
 # ------------------------------------------------------------------------ drafted tokens
