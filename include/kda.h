@@ -364,6 +364,29 @@ kda_status_t kda_causal_conv_decode(const kda_conv_desc_t *desc, const void *x, 
                                     void *y, void *workspace, size_t workspace_bytes,
                                     cudaStream_t stream);
 
+/*
+ * Backward pass of kda_causal_conv in dense mode, from the derivatives of a loss by y and (dfinal, or
+ * NULL) by the final states.
+ *
+ *   dy       [T, Ch] dtype, rows dy_pitch elements apart
+ *   x, weight, bias, cu_seqlens, state  as the forward call had them (state NULL: zeros); of desc the
+ *            pool's fields are ignored
+ *   dfinal, dstate  [N, W-1, Ch] dtype or NULL; dstate is 0 for an invalid sequence
+ *   dx       [T, Ch] dtype, packed, must not overlap an input; 0 in rows of no valid sequence
+ *   dweight  [Ch, W] fp32    dbias [Ch] fp32 or NULL: sums over all tokens in fp32, in a fixed order
+ *   workspace  kda_causal_conv_backward_workspace_size(desc) bytes
+ *
+ * Where lengths run backwards, so that sequences overlap, a row goes to the last of its sequences, whose
+ * state is read in front of its first row all the same; the others' derivatives are unspecified.
+ */
+kda_status_t kda_causal_conv_backward(const kda_conv_desc_t *desc, const void *dy, int64_t dy_pitch,
+                                      const void *x, const void *weight, const void *bias,
+                                      const int32_t *cu_seqlens, const void *state,
+                                      const void *dfinal, void *dx, float *dweight, float *dbias,
+                                      void *dstate, void *workspace, size_t workspace_bytes,
+                                      cudaStream_t stream);
+size_t kda_causal_conv_backward_workspace_size(const kda_conv_desc_t *desc); /* 0 on an invalid one */
+
 /* Inputs of the selective state space scan; T tokens, H = num_v_heads heads of V = head_v_dim
  * values, G = num_k_heads groups, state size K = head_k_dim.  Pitches are the elements between
  * consecutive tokens, so that slices of one projection can be passed; x, b and c need 16-byte

@@ -358,6 +358,252 @@ conv_token_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
   KDA_DEBUG_FOLD(status);
 }
 
+// ---- backward -------------------------------------------------------------------------------
+// With z the sum before the activation and dz = dy act'(z):
+//   by an input   sum over its taps of w_i dz_{t+(W-1)-i}, and the final state's derivative where it is one
+//                 of the last W-1 inputs
+//   by w_i        sum over the tokens of dz_t x_{t-(W-1)+i}        by the bias: sum of dz
+// Two rows are read and one is written a token, and z is formed again: bound by HBM. A thread walks a strip of
+// S tokens and the W-1 behind it (whose dz its last rows' derivatives need; they are the next strip's to
+// count in the sums), with the last W inputs and dz in registers. The sums by the weights stay in registers over
+// the strip, are added over the block's strips in shared memory, and over the blocks by a second kernel, each
+// in a fixed order.
+constexpr int kBackStrips = 8;
+
+// act'(z): of z sigmoid(z) it is sigmoid(z) (1 + z (1 - sigmoid(z))).
+template <typename T> __device__ __forceinline__ float silu_slope(float z) {
+  const float e = sizeof(T) == 2 ? __expf(-z) : expf(-z);
+  const float s = sizeof(T) == 2 ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e);
+  return s * fmaf(z, 1.f - s, 1.f);
+}
+
+template <typename T, int VEC, int W, int kStrip>
+__global__ void __launch_bounds__(kConvThreads, VEC == 1 ? 4 : 2)
+conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict__ x, int64_t x_pitch,
+                 const T* __restrict__ w, const T* __restrict__ bias, const int32_t* __restrict__ cu,
+                 const T* __restrict__ state, const T* __restrict__ dfinal, T* __restrict__ dx,
+                 T* __restrict__ dstate, float* __restrict__ part, uint32_t* __restrict__ status, int N,
+                 int64_t total, int ch, bool act) {
+  using R = Row<T, VEC>;
+  constexpr int H = W - 1;
+  constexpr int kTile = kStrip * kBackStrips;
+  constexpr int kSpan = kTile + H;
+  __shared__ int s_seq[kSpan];
+  __shared__ int64_t s_bos[kSpan];
+  __shared__ float s_sum[kBackStrips][kLanes * VEC];
+
+  const int tid = threadIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.x * kTile;
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_all(status, cu, nullptr, N, total, total, 0);
+  for (int i = tid; i < kSpan; i += kConvThreads) s_seq[i] = -1;
+  __syncthreads();
+  for (int base = 0; base < N; base += kConvThreads) {
+    const int n = base + tid;
+    int64_t a = 0, b = 0;
+    const bool hit = n < N && seq_bounds(cu, n, total, &a, &b) && a < t0 + kSpan && b > t0;
+    unsigned m = __ballot_sync(0xffffffffu, hit);
+    while (m) {
+      const int src = __ffs(m) - 1;
+      m &= m - 1;
+      const int64_t sa = __shfl_sync(0xffffffffu, a, src), sb = __shfl_sync(0xffffffffu, b, src);
+      const int sn = __shfl_sync(0xffffffffu, n, src);
+      const int lo = (int)(sa > t0 ? sa - t0 : 0);
+      const int hi = (int)(sb < t0 + kSpan ? sb - t0 : kSpan);
+      for (int i = lo + (tid & 31); i < hi; i += 32) atomicMax(&s_seq[i], sn);
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < kSpan; i += kConvThreads) s_bos[i] = s_seq[i] < 0 ? 0 : (int64_t)cu[s_seq[i]];
+  __syncthreads();
+
+  const int c = (blockIdx.y * kLanes + tid % kLanes) * VEC;
+  const bool in = c < ch;
+  // the initial states' derivatives of sequences without tokens, and of invalid ones
+  if (dstate && in) {
+    for (int64_t n = blockIdx.x * (int64_t)kBackStrips + tid / kLanes; n < N;
+         n += gridDim.x * (int64_t)kBackStrips) {
+      int64_t a, b;
+      const bool ok = seq_bounds(cu, (int)n, total, &a, &b);
+      if (ok && a != b) continue;
+      for (int j = 0; j < H; ++j) {
+        const int64_t at = (n * H + j) * ch + c;
+        R::store(dstate + at, ok && dfinal ? R::load(dfinal + at) : R::zero());
+      }
+    }
+  }
+  float wt[W][VEC], bv[VEC], dw[W][VEC], db[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    bv[i] = db[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) wt[j][i] = dw[j][i] = 0.f;
+  }
+  if (in) load_taps<T, VEC, W>(w, bias, c, wt, bv);
+  const int s0 = (tid / kLanes) * kStrip;
+  float win[W][VEC];      // the last W inputs, oldest first
+  float dz[W][VEC];       // dz of the last W tokens, oldest first
+  float ds[H][VEC];       // derivative by the state of the sequence that began in this strip
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) win[j][e] = dz[j][e] = 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < H; ++j) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) ds[j][e] = 0.f;
+  }
+  // Rows of dx are written when the W-1 tokens behind them have been seen.
+#pragma unroll 1
+  for (int i = 0; in && i < kStrip + H; ++i) {
+    const int r = s0 + i;
+    const int64_t t = t0 + r;
+    const int n = r < kSpan ? s_seq[r] : -1;
+    const int64_t bos = n >= 0 ? s_bos[r] : 0, pos = t - bos;
+    float g[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) g[e] = 0.f;
+    if (n >= 0) {
+      if (i == 0 || s_seq[r - 1] != n) {
+        // the inputs before the token: of the sequence, or of its state
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          const int64_t p = pos - H + j;
+          if (p >= 0) R::unpack(R::load(x + (bos + p) * x_pitch + c), win[j + 1]);
+          else if (state) R::unpack(R::load(state + ((int64_t)n * H + H + p) * ch + c), win[j + 1]);
+          else
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) win[j + 1][e] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) ds[j][e] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
+      }
+      R::unpack(R::load(x + t * x_pitch + c), win[H]);
+      R::unpack(R::load(dy + t * dy_pitch + c), g);
+      if (act) {
+        float z[VEC];
+        apply<T, VEC, W>(win, wt, bv, false, z);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) g[e] *= silu_slope<T>(z[e]);
+      }
+      if (i < kStrip) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+          for (int j = 0; j < W; ++j) dw[j][e] = fmaf(g[e], win[j][e], dw[j][e]);
+          db[e] += g[e];
+        }
+      }
+      // a sequence's state is read by its first W-1 tokens, which the strip of the first one sees all
+      if (dstate && pos < H && pos <= i && i - pos < kStrip) {
+        const int64_t len = (int64_t)cu[n + 1] - bos;
+#pragma unroll
+        for (int m = 0; m < H; ++m) {
+#pragma unroll
+          for (int p = 0; p <= m; ++p) {
+            if (p == pos) {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) ds[m][e] = fmaf(g[e], wt[m - p][e], ds[m][e]);
+            }
+          }
+        }
+        if (pos == H - 1 || pos == len - 1) {
+#pragma unroll
+          for (int m = 0; m < H; ++m) {
+            if (dfinal && m >= len) {
+              float f[VEC];
+              R::unpack(R::load(dfinal + ((int64_t)n * H + m - len) * ch + c), f);
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) ds[m][e] += f[e];
+            }
+            R::store(dstate + ((int64_t)n * H + m) * ch + c, R::pack(ds[m]));
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) dz[j][e] = dz[j + 1][e];
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) dz[H][e] = g[e];
+    const int ro = r - H;                   // the row whose derivative is complete
+    if (i < H || t0 + ro >= total) continue;
+    const int no = s_seq[ro];
+    float out[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) out[e] = 0.f;
+    if (no >= 0) {
+#pragma unroll
+      for (int d = 0; d < W; ++d) {
+        if (d == 0 || (ro + d < kSpan && s_seq[ro + d] == no)) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) out[e] = fmaf(dz[d][e], wt[H - d][e], out[e]);
+        }
+      }
+      if (dfinal) {
+        const int64_t back = (int64_t)cu[no + 1] - (t0 + ro);   // 1 for the last token
+        if (back <= H) {
+          float f[VEC];
+          R::unpack(R::load(dfinal + ((int64_t)no * H + H - back) * ch + c), f);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) out[e] += f[e];
+        }
+      }
+    }
+    if (KDA_CHECK(ro >= 0 && c + VEC <= ch)) R::store(dx + (t0 + ro) * ch + c, R::pack(out));
+  }
+  // parts [tile][W + 1][Ch] of the sums
+#pragma unroll
+  for (int j = 0; j <= W; ++j) {
+    float mine[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) mine[e] = j < W ? dw[j < W ? j : 0][e] : db[e];
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s_sum[tid / kLanes][(tid % kLanes) * VEC + e] = mine[e];
+    __syncthreads();
+    for (int k = tid; k < kLanes * VEC; k += kConvThreads) {
+      const int64_t cc = (int64_t)blockIdx.y * kLanes * VEC + k;
+      float sum = 0.f;
+#pragma unroll
+      for (int q = 0; q < kBackStrips; ++q) sum += s_sum[q][k];
+      if (cc < ch) part[((int64_t)blockIdx.x * (W + 1) + j) * ch + cc] = sum;
+    }
+  }
+  KDA_DEBUG_FOLD(status);
+}
+
+// The tiles' parts of the sums, added in a fixed order.
+__global__ void __launch_bounds__(256)
+conv_sum_kernel(const float* __restrict__ part, int64_t tiles, int ch, int W, float* __restrict__ dw,
+                float* __restrict__ db) {
+  __shared__ float s[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = blockIdx.y;
+  const int c = blockIdx.x * 32 + lane;
+  float sum = 0.f;
+  if (c < ch) {
+#pragma unroll 8
+    for (int64_t k = warp; k < tiles; k += 8) sum += part[(k * (W + 1) + j) * ch + c];
+  }
+  s[warp][lane] = sum;
+  __syncthreads();
+  if (warp != 0 || c >= ch) return;
+#pragma unroll
+  for (int q = 1; q < 8; ++q) sum += s[q][lane];
+  if (j < W) dw[(int64_t)c * W + j] = sum;
+  else if (db) db[c] = sum;
+}
+
 // Rows that start on a boundary of 4 elements.
 bool rows4(const void* p, int64_t pitch, int size) {
   return !p || ((uintptr_t)p % (4 * size) == 0 && pitch % 4 == 0);
@@ -416,7 +662,60 @@ cudaError_t by_type(const ConvArgs& a, cudaStream_t st, bool token) {
   return wide ? by_width<T, VEC>(a, st, token) : by_width<T, 1>(a, st, token);
 }
 
+// Strips as in the forward pass.
+int back_strip(const kda_conv_desc_t& d) {
+  const int64_t blocks = (d.total_tokens / (32 * kBackStrips)) * (d.channels / (kLanes * 4));
+  return blocks >= 4 * gpu_sms() ? 32 : 8;
+}
+int64_t back_tiles(const kda_conv_desc_t& d) {
+  const int64_t rows = (int64_t)back_strip(d) * kBackStrips, tiles = (d.total_tokens + rows - 1) / rows;
+  return tiles > 0 ? tiles : 1;   // no tokens: the empty sequences' states
+}
+
+template <typename T, int VEC, int W, int kStrip>
+cudaError_t launch_back(const ConvBackArgs& a, cudaStream_t st) {
+  const int ch = a.d.channels;
+  const int64_t tiles = back_tiles(a.d);
+  dim3 grid((unsigned)tiles, (unsigned)((ch + kLanes * VEC - 1) / (kLanes * VEC)));
+  conv_back_kernel<T, VEC, W, kStrip><<<grid, kConvThreads, 0, st>>>(
+      (const T*)a.dy, a.dy_pitch, (const T*)a.x, a.d.x_pitch, (const T*)a.w, (const T*)a.bias, a.cu,
+      (const T*)a.state, (const T*)a.dfinal, (T*)a.dx, (T*)a.dstate, a.part, a.status, a.d.num_seqs,
+      a.d.total_tokens, ch, a.d.silu != 0);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  conv_sum_kernel<<<dim3((unsigned)((ch + 31) / 32), W + 1), 256, 0, st>>>(a.part, tiles, ch, W, a.dw, a.db);
+  return cudaGetLastError();
+}
+
+template <typename T, int VEC>
+cudaError_t back_by_width(const ConvBackArgs& a, cudaStream_t st) {
+  const bool longer = back_strip(a.d) == 32;
+  switch (a.d.width) {
+    case 2: return longer ? launch_back<T, VEC, 2, 32>(a, st) : launch_back<T, VEC, 2, 8>(a, st);
+    case 3: return longer ? launch_back<T, VEC, 3, 32>(a, st) : launch_back<T, VEC, 3, 8>(a, st);
+    default: return longer ? launch_back<T, VEC, 4, 32>(a, st) : launch_back<T, VEC, 4, 8>(a, st);
+  }
+}
+
+template <typename T>
+cudaError_t back_by_type(const ConvBackArgs& a, cudaStream_t st) {
+  constexpr int VEC = 4;
+  const int64_t ch = a.d.channels, e = sizeof(T);
+  const bool wide = rows4(a.x, a.d.x_pitch, e) && rows4(a.dy, a.dy_pitch, e) && rows4(a.w, ch, e) &&
+                    rows4(a.bias, ch, e) && rows4(a.state, ch, e) && rows4(a.dfinal, ch, e) &&
+                    rows4(a.dx, ch, e) && rows4(a.dstate, ch, e) && ch % VEC == 0;
+  return wide ? back_by_width<T, VEC>(a, st) : back_by_width<T, 1>(a, st);
+}
+
 }  // namespace
+
+size_t conv_back_workspace(const kda_conv_desc_t& d) {
+  return kWsPayload + (size_t)back_tiles(d) * (d.width + 1) * d.channels * 4;
+}
+
+cudaError_t launch_conv_back(const ConvBackArgs& a, cudaStream_t st) {
+  return a.d.dtype == KDA_BF16 ? back_by_type<__nv_bfloat16>(a, st) : back_by_type<float>(a, st);
+}
 
 cudaError_t launch_conv(const ConvArgs& a, cudaStream_t st) {
   return a.d.dtype == KDA_BF16 ? by_type<__nv_bfloat16>(a, st, false) : by_type<float>(a, st, false);

@@ -230,6 +230,21 @@ struct ConvArgs {
 cudaError_t launch_conv(const ConvArgs& a, cudaStream_t st);
 cudaError_t launch_conv_decode(const ConvArgs& a, cudaStream_t st);
 
+struct ConvBackArgs {
+  kda_conv_desc_t d;
+  const void* dy;
+  int64_t dy_pitch;
+  const void *x, *w, *bias;
+  const int32_t* cu;
+  const void *state, *dfinal;  // [N, W-1, Ch] or null
+  void *dx, *dstate;           // dstate may be null
+  float *dw, *db;              // db may be null
+  float* part;                 // the tiles' sums
+  uint32_t* status;
+};
+size_t conv_back_workspace(const kda_conv_desc_t& d);  // the whole workspace, header included
+cudaError_t launch_conv_back(const ConvBackArgs& a, cudaStream_t st);
+
 // Four elements as fp32, aligned to four.
 __device__ __forceinline__ void load4(const float* p, float (&r)[4]) {
   const float4 x = *reinterpret_cast<const float4*>(p);

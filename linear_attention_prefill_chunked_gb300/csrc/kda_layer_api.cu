@@ -148,6 +148,42 @@ kda_status_t kda_causal_conv_decode(const kda_conv_desc_t* d, const void* x, con
   return launched(workspace, stream, [&] { return kda::launch_conv_decode(a, stream); });
 }
 
+size_t kda_causal_conv_backward_workspace_size(const kda_conv_desc_t* d) {
+  return conv_ok(d) && conv_fits(d) ? kda::conv_back_workspace(*d) : 0;
+}
+
+kda_status_t kda_causal_conv_backward(const kda_conv_desc_t* d, const void* dy, int64_t dy_pitch, const void* x,
+                                      const void* weight, const void* bias, const int32_t* cu_seqlens,
+                                      const void* state, const void* dfinal, void* dx, float* dweight,
+                                      float* dbias, void* dstate, void* workspace, size_t workspace_bytes,
+                                      cudaStream_t stream) {
+  if (!conv_ok(d) || !weight || !cu_seqlens || !ws_ok(workspace) || !dweight || dy_pitch < d->channels)
+    return KDA_ERR_INVALID_ARGUMENT;
+  if (!conv_fits(d)) return KDA_ERR_UNSUPPORTED;
+  if (d->total_tokens > 0 && (!x || !dy || !dx)) return KDA_ERR_INVALID_ARGUMENT;
+  {
+    const void* ptrs[] = {dy, x, weight, bias, state, dfinal, dx, dstate};
+    for (const void* p : ptrs)
+      if (!elem_aligned(p, d->dtype)) return KDA_ERR_INVALID_ARGUMENT;
+  }
+  if (!elem_aligned(dweight, KDA_F32) || !elem_aligned(dbias, KDA_F32)) return KDA_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < kda::conv_back_workspace(*d)) return KDA_ERR_WORKSPACE_TOO_SMALL;
+  kda::ConvBackArgs a{};
+  a.d = *d;
+  a.dy = dy;
+  a.dy_pitch = dy_pitch;
+  a.x = x; a.w = weight; a.bias = bias; a.cu = cu_seqlens;
+  a.state = state;
+  a.dfinal = dfinal;
+  a.dx = dx;
+  a.dstate = dstate;
+  a.dw = dweight;
+  a.db = dbias;
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kda::kWsPayload);
+  a.status = status_of(workspace);
+  return launched(workspace, stream, [&] { return kda::launch_conv_back(a, stream); });
+}
+
 size_t kda_ssm_scan_workspace_size(const kda_desc_t* d) {
   if (!ssm_ok(d) || !ssm_supported(d)) return 0;
   return kda::ssm_tc_supported(*d) ? kda::ssm_tc_workspace(*d) : kda::ssm_simt_workspace(*d);

@@ -53,6 +53,8 @@ def _load():
                 ("kda_causal_conv", [conv, *[_P] * 9, size, _P], ctypes.c_int),
                 ("kda_causal_conv_decode",
                  [conv, *[_P] * 7, _I64, _I32, ctypes.c_int, _P, _P, size, _P], ctypes.c_int),
+                ("kda_causal_conv_backward", [conv, _P, _I64, *[_P] * 11, size, _P], ctypes.c_int),
+                ("kda_causal_conv_backward_workspace_size", [conv], size),
                 ("kda_ssm_scan", [desc, ins, *[_P] * 6, size, _P], ctypes.c_int),
                 ("kda_ssm_scan_workspace_size", [desc], size),
                 ("kda_ssm_decode",
@@ -354,6 +356,36 @@ def causal_conv_draft(x, weight, cu_seqlens, state, state_indices=None, *, bias=
     return _conv_token(x, weight, cu_seqlens, state, state_indices, bias, activation, cache,
                        _steps(cu_seqlens, max_steps, stream), update_state, slot_stride, out, workspace,
                        stream, causal_conv_draft)
+
+
+def causal_conv_backward(dy, x, weight, cu_seqlens, *, bias=None, activation=None, state=None, dfinal=None,
+                         workspace=None, stream=None):
+    """The derivatives of a loss by the inputs of a dense :func:`causal_conv` (kda_causal_conv_backward), from
+    those by y (``dy`` [T, Ch], rows at any pitch) and by the final states (``dfinal`` [N, W-1, Ch] or None).
+    Returns ``(dx, dweight, dbias, dstate)``: dx and dstate in x's type, dweight [Ch, W] and dbias [Ch] fp32;
+    dbias None without ``bias``, dstate None without ``state``.
+
+    x, weight, cu_seqlens, bias, activation and state as the forward call had them.
+    """
+    N, T, ch, width, pitch = check_conv_args(x, weight, bias=bias, cu_seqlens=cu_seqlens, state=state)
+    dy_pitch = _rows(dy, "dy", (T, ch), x.dtype)
+    if dfinal is not None:
+        _plain(dfinal, "dfinal", x.dtype, (N, width - 1, ch))
+    _cuda(dy, x, weight, cu_seqlens, bias, state, dfinal, workspace)
+    silu = _activation(activation)
+    lib, dev = _load(), x.device
+    dx = _empty(stream, (T, ch), x.dtype, dev)
+    dweight = _empty(stream, (ch, width), torch.float32, dev)
+    dbias = None if bias is None else _empty(stream, (ch,), torch.float32, dev)
+    dstate = None if state is None else _empty(stream, (N, width - 1, ch), x.dtype, dev)
+    d = KdaConvDesc(N, T, ch, width, _dt(x.dtype), silu, pitch, 0, 0)
+    size = lib.kda_causal_conv_backward_workspace_size(ctypes.byref(d))
+    ws, nws = _workspace(stream, workspace, max(size, STATUS_WORKSPACE_BYTES), dev)
+    rc = lib.kda_causal_conv_backward(ctypes.byref(d), _p(dy), dy_pitch, _p(x), _p(weight), _p(bias),
+                                      _p(cu_seqlens), _p(state), _p(dfinal), _p(dx), _p(dweight), _p(dbias),
+                                      _p(dstate), _p(ws), nws, _stream(stream, dev))
+    _done(rc, "kda_causal_conv_backward", causal_conv_backward, ws)
+    return dx, dweight, dbias, dstate
 
 
 # ------------------------------------------------------------------------ state space scan
