@@ -68,6 +68,8 @@ typedef enum { KDA_BF16 = 0, KDA_F32 = 1 } kda_dtype_t;
                                           vocabulary                                   */
 #define KDA_DEVICE_BAD_COUNT     0x20u /* kda_commit_draft: an accepted count outside
                                           [0, max_steps]                               */
+#define KDA_DEVICE_BAD_PARAM     0x40u /* kda_sample, kda_sample_probs: a temperature below
+                                          0, or a parameter that is no number          */
 
 /* Descriptor flags. */
 #define KDA_FLAG_CUDA_CORE_PATH  0x1u  /* prefill: run the fp32 CUDA-core kernel even where
@@ -515,6 +517,56 @@ kda_status_t kda_gated_decode(const kda_gated_desc_t *desc, const void *x, const
                               float *state_pool, const int32_t *state_indices, float *step_cache,
                               int64_t cache_pitch_elems, int32_t max_steps, int update_pool, void *y,
                               void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Problem descriptor of the draw of tokens. */
+typedef struct {
+    int32_t num_rows;          /* rows of logits: requests, or fed tokens               */
+    int32_t vocab;             /* entries of a row, at most 344064                      */
+    kda_dtype_t dtype;         /* of the logits                                         */
+    int64_t logits_pitch;      /* elements between consecutive rows, >= vocab           */
+    int64_t noise_pitch;       /* the same of noise (kda_sample)                        */
+    float temperature;         /* of all rows, where no array of them is given; the     */
+    int32_t top_k;             /* filters are off at top_k <= 0, top_p >= 1, min_p <= 0 */
+    float top_p;
+    float min_p;
+} kda_sample_desc_t;
+
+/*
+ * A token a row, drawn from logits z and given random numbers.  With the row's entries ordered by
+ * value, of equal values by index, and p_i = exp((z_i - max z) / temperature):
+ *
+ *   top-k   the first top_k entries stand (ties are not kept together)
+ *   top-p   of these an entry stands while the sum of p before it is below top_p of their sum; the
+ *           first always does
+ *   min-p   and only where p_i >= min_p (of the largest p, which is 1; more than 1 counts as 1)
+ *   token   the entry with the largest p_i / noise_i, of equal ones the lowest: with noise ~ Exp(1)
+ *           a draw in proportion to p
+ *
+ *   logits  [num_rows, vocab] dtype      noise [num_rows, vocab] fp32 > 0, read where entries stand
+ *   temperature, top_p, min_p [num_rows] fp32, top_k [num_rows] int32, each or NULL (desc's)
+ *   token   [num_rows] int32
+ *
+ * At temperature 0 (and at top_k 1 or top_p <= 0) the first entry alone stands.  A NaN counts as -inf;
+ * entries of -inf, and those with p below 2^-126, are never drawn; where the largest is +inf its entries
+ * share alike and no other stands.  A row without an entry that could be drawn gets -1, as does a row with
+ * a negative temperature or a parameter that is no number (status bit KDA_DEVICE_BAD_PARAM).  p is
+ * good to 2^-30 and sums of it are exact (in units of 2^-44 of the largest), so results do not
+ * depend on the order of additions.
+ */
+kda_status_t kda_sample(const kda_sample_desc_t *desc, const void *logits, const float *noise,
+                        const float *temperature, const int32_t *top_k, const float *top_p,
+                        const float *min_p, int32_t *token, void *workspace,
+                        size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The probabilities of that draw, as kda_verify_draft wants them of target and draft: probs
+ * [num_rows, vocab] fp32, packed, p_i over its sum for entries that stand, else 0 (throughout, for a row
+ * that gets token -1 above; 1 at the one entry at temperature 0).
+ */
+kda_status_t kda_sample_probs(const kda_sample_desc_t *desc, const void *logits,
+                              const float *temperature, const int32_t *top_k, const float *top_p,
+                              const float *min_p, float *probs, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Verification of drafted tokens from given random numbers.  Request n was fed the tokens

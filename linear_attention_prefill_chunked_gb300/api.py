@@ -62,7 +62,8 @@ EXPORTS = ("kda_chunk_prefill_workspace_size", "kda_chunk_prefill_min_workspace_
            "kda_verify_draft_marked", "kda_commit_draft", "kda_gated_scan",
            "kda_gated_scan_workspace_size", "kda_gated_scan_backward",
            "kda_gated_scan_backward_workspace_size", "kda_gated_decode",
-           "kda_causal_conv_backward", "kda_causal_conv_backward_workspace_size")
+           "kda_causal_conv_backward", "kda_causal_conv_backward_workspace_size", "kda_sample",
+           "kda_sample_probs")
 
 _lib = None
 

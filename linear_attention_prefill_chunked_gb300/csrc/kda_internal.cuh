@@ -327,6 +327,19 @@ cudaError_t launch_gated_scan(const GatedArgs& a, cudaStream_t st);
 cudaError_t launch_gated_back(const GatedArgs& a, cudaStream_t st);
 cudaError_t launch_gated_token(const GatedArgs& a, cudaStream_t st);
 
+struct SampleArgs {
+  kda_sample_desc_t d;
+  const void* logits;
+  const float* noise;                       // tokens only
+  const float *temperature, *top_p, *min_p; // [num_rows], or null: the descriptor's
+  const int32_t* top_k;
+  int32_t* token;                           // one of token and probs is null
+  float* probs;
+  uint32_t* status;
+};
+bool sample_fits(const kda_sample_desc_t& d);
+cudaError_t launch_sample(const SampleArgs& a, cudaStream_t st);
+
 cudaError_t launch_verify(int N, int64_t T, int vocab, const int32_t* tokens, const float* p,
                           const float* q, const float* u, const float* noise, const int32_t* cu,
                           int32_t* kept, int32_t* next, uint32_t* status, uint32_t flags, cudaStream_t st);

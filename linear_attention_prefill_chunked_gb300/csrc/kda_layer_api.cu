@@ -74,6 +74,19 @@ bool gated_inputs_ok(const kda_gated_desc_t* d, const void* x, const void* r, co
          d->x_pitch >= d->channels && d->r_pitch >= d->channels && (!i || d->i_pitch >= d->channels);
 }
 
+bool sample_ok(const kda_sample_desc_t* d, const float* temperature, const int32_t* top_k, const float* top_p,
+               const float* min_p) {
+  if (!d || d->num_rows < 0 || d->vocab <= 0 || d->logits_pitch < d->vocab ||
+      !(d->dtype == KDA_BF16 || d->dtype == KDA_F32))
+    return false;
+  if (!temperature && !(d->temperature >= 0.f)) return false;
+  if ((!top_p && d->top_p != d->top_p) || (!min_p && d->min_p != d->min_p)) return false;
+  const void* ptrs[] = {temperature, top_k, top_p, min_p};
+  for (const void* p : ptrs)
+    if ((uintptr_t)p % 4 != 0) return false;
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -369,6 +382,34 @@ kda_status_t kda_gated_decode(const kda_gated_desc_t* d, const void* x, const vo
   a.max_steps = cu_seqlens ? max_steps : 1;
   a.update_pool = update_pool != 0;
   return launched(workspace, stream, [&] { return kda::launch_gated_token(a, stream); });
+}
+
+kda_status_t kda_sample(const kda_sample_desc_t* d, const void* logits, const float* noise,
+                        const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                        int32_t* token, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!sample_ok(d, temperature, top_k, top_p, min_p) || !ws_ok(workspace)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!kda::sample_fits(*d)) return KDA_ERR_UNSUPPORTED;
+  if (d->num_rows > 0 && (!logits || !noise || !token)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!elem_aligned(logits, d->dtype) || !elem_aligned(noise, KDA_F32) || !elem_aligned(token, KDA_F32) ||
+      d->noise_pitch < d->vocab)
+    return KDA_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < KDA_STATUS_WORKSPACE_BYTES) return KDA_ERR_WORKSPACE_TOO_SMALL;
+  if (d->num_rows == 0) return clear_status(workspace, stream);
+  kda::SampleArgs a{*d, logits, noise, temperature, top_p, min_p, top_k, token, nullptr, status_of(workspace)};
+  return launched(workspace, stream, [&] { return kda::launch_sample(a, stream); });
+}
+
+kda_status_t kda_sample_probs(const kda_sample_desc_t* d, const void* logits, const float* temperature,
+                              const int32_t* top_k, const float* top_p, const float* min_p, float* probs,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!sample_ok(d, temperature, top_k, top_p, min_p) || !ws_ok(workspace)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!kda::sample_fits(*d)) return KDA_ERR_UNSUPPORTED;
+  if (d->num_rows > 0 && (!logits || !probs)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!elem_aligned(logits, d->dtype) || !elem_aligned(probs, KDA_F32)) return KDA_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < KDA_STATUS_WORKSPACE_BYTES) return KDA_ERR_WORKSPACE_TOO_SMALL;
+  if (d->num_rows == 0) return clear_status(workspace, stream);
+  kda::SampleArgs a{*d, logits, nullptr, temperature, top_p, min_p, top_k, nullptr, probs, status_of(workspace)};
+  return launched(workspace, stream, [&] { return kda::launch_sample(a, stream); });
 }
 
 kda_status_t kda_verify_draft(int32_t num_seqs, int64_t total_tokens, int32_t vocab,

@@ -40,6 +40,13 @@ class KdaGatedDesc(ctypes.Structure):
                 ("slot_stride_elems", _I64)]
 
 
+class KdaSampleDesc(ctypes.Structure):
+    """Mirror of ``kda_sample_desc_t`` in include/kda.h."""
+    _fields_ = [("num_rows", _I32), ("vocab", _I32), ("dtype", ctypes.c_int), ("logits_pitch", _I64),
+                ("noise_pitch", _I64), ("temperature", ctypes.c_float), ("top_k", _I32),
+                ("top_p", ctypes.c_float), ("min_p", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -49,6 +56,7 @@ def _load():
         lib = api.load()
         size, desc, conv = ctypes.c_size_t, ctypes.POINTER(KdaDesc), ctypes.POINTER(KdaConvDesc)
         ins, gated = ctypes.POINTER(KdaSsmInputs), ctypes.POINTER(KdaGatedDesc)
+        draw = ctypes.POINTER(KdaSampleDesc)
         for name, args, res in (
                 ("kda_causal_conv", [conv, *[_P] * 9, size, _P], ctypes.c_int),
                 ("kda_causal_conv_decode",
@@ -65,6 +73,8 @@ def _load():
                 ("kda_gated_scan_backward_workspace_size", [gated], size),
                 ("kda_gated_decode",
                  [gated, *[_P] * 8, _I64, _I32, ctypes.c_int, _P, _P, size, _P], ctypes.c_int),
+                ("kda_sample", [draw, *[_P] * 8, size, _P], ctypes.c_int),
+                ("kda_sample_probs", [draw, *[_P] * 7, size, _P], ctypes.c_int),
                 ("kda_verify_draft", [_I32, _I64, _I32, *[_P] * 9, size, _P], ctypes.c_int),
                 ("kda_verify_draft_marked",
                  [_I32, _I64, _I32, *[_P] * 8, ctypes.c_uint32, _P, size, _P], ctypes.c_int),
@@ -666,6 +676,83 @@ def gated_decode_draft(x, r, A_log, cu_seqlens, pool, state_indices=None, *, i=N
     return _gated_token(x, r, A_log, cu_seqlens, pool, state_indices, i, cache,
                         _steps(cu_seqlens, max_steps, stream), update_pool, slot_stride, out, workspace, stream,
                         gated_decode_draft)
+
+
+# ------------------------------------------------------------------------ draw of tokens
+
+def _param(value, name, n, dtype, off):
+    """A parameter of each row ([n] tensor), or of all (a number; None: ``off``): (tensor, number)."""
+    if isinstance(value, torch.Tensor):
+        _plain(value, name, dtype, (n,))
+        return value, off
+    if value is None:
+        return None, off
+    if isinstance(value, bool) or not isinstance(value, (int,) if dtype is torch.int32 else (int, float)):
+        raise TypeError(f"{name} must be a number or a tensor of {dtype}, got {value!r}")
+    if value != value or (dtype is torch.int32 and not -2 ** 31 <= value < 2 ** 31):
+        raise ValueError(f"{name} must be a number within its type, got {value!r}")
+    return None, value
+
+
+def _draw_args(logits, temperature, top_k, top_p, min_p):
+    """Checks of a draw's call (host only); returns (rows, vocab, parameters' tensors, descriptor)."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("logits must be a bfloat16 or float32 tensor")
+    if logits.dim() != 2 or logits.shape[1] < 1:
+        raise ValueError(f"logits must have shape [rows, vocab], got {list(logits.shape)}")
+    n, vocab = logits.shape
+    pitch = _rows(logits, "logits", (n, vocab), logits.dtype)
+    t, t_all = _param(temperature, "temperature", n, torch.float32, 1.0)
+    k, k_all = _param(top_k, "top_k", n, torch.int32, 0)
+    p, p_all = _param(top_p, "top_p", n, torch.float32, 1.0)
+    m, m_all = _param(min_p, "min_p", n, torch.float32, 0.0)
+    if t_all < 0:
+        raise ValueError(f"temperature must not be negative, got {t_all!r}")
+    return n, vocab, (t, k, p, m), KdaSampleDesc(n, vocab, _dt(logits.dtype), pitch, vocab, t_all, k_all, p_all,
+                                                 m_all)
+
+
+def sample(logits, noise, *, temperature=None, top_k=None, top_p=None, min_p=None, out=None, workspace=None,
+           stream=None):
+    """A token a row from logits and given random numbers (kda_sample).  Returns int32 [rows].
+
+    logits [rows, vocab] bf16 or fp32, noise [rows, vocab] fp32 ~ Exp(1), rows of both at any pitch; each
+    parameter a number for all rows, or a tensor of one a row (top_k int32, the others fp32).  The first
+    top_k entries by value (then index), of these the first whose probabilities sum up to top_p, and of
+    these those of at least min_p of the largest one's probability stand; of them the one with the largest
+    probability over noise is drawn.  Temperature 0: the largest.  -1 for a row with nothing to draw from.
+    """
+    n, vocab, params, d = _draw_args(logits, temperature, top_k, top_p, min_p)
+    d.noise_pitch = _rows(noise, "noise", (n, vocab), torch.float32)
+    if out is not None:
+        _plain(out, "out", torch.int32, (n,))
+    _cuda(logits, noise, *params, out, workspace)
+    lib, dev = _load(), logits.device
+    if out is None:
+        out = _empty(stream, (n,), torch.int32, dev)
+    ws, nws = _workspace(stream, workspace, STATUS_WORKSPACE_BYTES, dev)
+    rc = lib.kda_sample(ctypes.byref(d), _p(logits), _p(noise), *map(_p, params), _p(out), _p(ws), nws,
+                        _stream(stream, dev))
+    _done(rc, "kda_sample", sample, ws)
+    return out
+
+
+def sample_probs(logits, *, temperature=None, top_k=None, top_p=None, min_p=None, out=None, workspace=None,
+                 stream=None):
+    """The probabilities that :func:`sample` draws with (kda_sample_probs), [rows, vocab] fp32, 0 for entries
+    that do not stand: what :func:`verify_draft` wants of the target and of the draft."""
+    n, vocab, params, d = _draw_args(logits, temperature, top_k, top_p, min_p)
+    if out is not None:
+        _plain(out, "out", torch.float32, (n, vocab))
+    _cuda(logits, *params, out, workspace)
+    lib, dev = _load(), logits.device
+    if out is None:
+        out = _empty(stream, (n, vocab), torch.float32, dev)
+    ws, nws = _workspace(stream, workspace, STATUS_WORKSPACE_BYTES, dev)
+    rc = lib.kda_sample_probs(ctypes.byref(d), _p(logits), *map(_p, params), _p(out), _p(ws), nws,
+                              _stream(stream, dev))
+    _done(rc, "kda_sample_probs", sample_probs, ws)
+    return out
 
 
 # ------------------------------------------------------------------------ drafted tokens
