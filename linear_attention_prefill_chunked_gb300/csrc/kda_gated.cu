@@ -21,10 +21,14 @@
 //      put together from those of the tiles before it: the state at the start of its group of kGroup
 //      tiles, then the tiles of the group in order;
 //   3. each warp runs through its rows again, from registers, and writes them.
-// Tiles are handed out by a counter, earlier rows first, so a tile waits only for tiles that run already.
-// The state at a group's start comes from the group before it, one wait for kGroup tiles. The order of all
-// sums is fixed, whichever tile comes first: results are bit-identical from run to run. A sequence's first
-// row starts from its own state, and no product carries the state before it (which may be no number).
+// CTAs stay and take tiles by a counter, earlier rows first, so a tile waits only for tiles that are done or
+// in work; the next tile's rows are on their way into shared memory (each thread's own ones, 4 bytes a
+// copy) while this one's steps 2 and 3 run. The state at a group's start comes from the group before it, one
+// wait for kGroup tiles. What tiles tell each other is valid when it is seen: A's place, or a tag beside the
+// state, holds a pattern no result has until its 8 bytes are written at once, so a wait is one trip to the
+// L2 and no fence. The order of all sums is fixed, whichever tile comes first: results are bit-identical
+// from run to run. A sequence's first row starts from its own state, and no product carries the state before
+// it (which may be no number).
 //
 // The backward pass runs over the tiles from the last to the first, e in the place of h. It needs
 // h_{t-1} as well; the forward pass left the state before each kCarryRows rows for it.
@@ -41,13 +45,14 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;
 constexpr int kPlanRows = 1024;   // rows a block of the planning kernel
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kUnset = 0xffffffffu;
 
-// Workspace behind the header: the sequence of each row, each tile's flag, each group's flag, each
-// tile's (A, H) and each group's state, all channels; the backward pass's parts of dA_log.
+// Workspace behind the header: each tile's (A, H) and each group's (state, tag) of all channels, which the
+// planning kernel sets to kUnset; the sequence of each row; the backward pass's parts of dA_log.
 struct Layout {
   int64_t tiles, groups;
   int32_t blocks;               // channel blocks
-  size_t seq, flag, gflag, agg_a, agg_h, group, part, total;
+  size_t agg, group, seq, part, total;
 };
 __host__ __device__ inline Layout layout_of(int64_t T, int32_t ch, int rows, int lane_ch, bool back) {
   Layout l;
@@ -60,12 +65,9 @@ __host__ __device__ inline Layout layout_of(int64_t T, int32_t ch, int rows, int
     at += (bytes + 255) / 256 * 256;
     return was;
   };
-  l.flag = take((size_t)l.tiles * l.blocks * 4);
-  l.gflag = take((size_t)l.groups * l.blocks * 4);
+  l.agg = take((size_t)l.tiles * ch * 8);
+  l.group = take((size_t)l.groups * ch * 8);
   l.seq = take((size_t)T * 4);
-  l.agg_a = take((size_t)l.tiles * ch * 4);
-  l.agg_h = take((size_t)l.tiles * ch * 4);
-  l.group = take((size_t)l.groups * ch * 4);
   l.part = take(back ? (size_t)l.tiles * ch * 4 : 0);
   l.total = at;
   return l;
@@ -128,29 +130,19 @@ template <typename T, int V> __device__ __forceinline__ typename Pack<T, V>::Raw
 template <typename T, int V> __device__ __forceinline__ void store(T* p, const Ch<V>& c) {
   *reinterpret_cast<typename Pack<T, V>::Raw*>(p) = Pack<T, V>::close(c);
 }
-// What other tiles write while this one runs is read past the L1.
-template <int V> __device__ __forceinline__ Ch<V> load_shared_state(const float* p) {
-  if constexpr (V == 2) {
-    const float2 r = __ldcg(reinterpret_cast<const float2*>(p));
-    return {{r.x, r.y}};
-  } else {
-    return {{__ldcg(p)}};
-  }
-}
-
 // ---- gates ----------------------------------------------------------------------------------
-// e^-v, kept below 1e37, and sigmoid(v) = 1 / (1 + e^-v), so that both sigmoid(v) and e^-v sigmoid(v) =
-// 1 - sigmoid(v) keep their leading digits at either end. bf16 inputs take the fast exponential and
+// e^-v and sigmoid(v) = 1 / (1 + e^-v). The backward pass keeps e^-v below 1e37, so that e^-v sigmoid(v) =
+// 1 - sigmoid(v) has its leading digits at either end. bf16 inputs take the fast exponential and
 // reciprocal, good to 2^-21 and |v| 2^-24: far below those inputs' own rounding, and what is fp32 of the
 // results (states, dA_log) keeps 2^-19.
-template <bool kFast, int V> __device__ __forceinline__ Ch<V> exp_neg(const Ch<V>& v) {
+template <bool kFast, bool kClamp, int V> __device__ __forceinline__ Ch<V> exp_neg(const Ch<V>& v) {
   Ch<V> e;
   if constexpr (kFast) e = mul(v, all<V>(-kLog2e));
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     if constexpr (kFast) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.f[i]));
     else e.f[i] = expf(-v.f[i]);
-    e.f[i] = e.f[i] > 1e37f ? 1e37f : e.f[i];  // NaN stays
+    if constexpr (kClamp) e.f[i] = e.f[i] > 1e37f ? 1e37f : e.f[i];  // NaN stays
   }
   return e;
 }
@@ -164,7 +156,7 @@ template <bool kFast, int V> __device__ __forceinline__ Ch<V> one_over(Ch<V> e) 
   return e;
 }
 template <bool kFast, int V> __device__ __forceinline__ Ch<V> sigmoid(const Ch<V>& v) {
-  return one_over<kFast>(exp_neg<kFast>(v));
+  return one_over<kFast>(exp_neg<kFast, false>(v));
 }
 
 // Decay rates of a lane's channels, -exp(A_log), finite.
@@ -175,7 +167,27 @@ template <int V> __device__ __forceinline__ Ch<V> rates(const float* a_log, int 
   return r;
 }
 
-template <bool kFast, int V> __device__ __forceinline__ Ch<V> decay(const Ch<V>& g) {  // e^g
+// a = e^g and 1 - a^2 of a log-decay g <= 0. Above -0.175 by the series of e = e^g - 1 (its next term is 2^-27
+// of it there): a = 1 + e is rounded once, which long memories need (a decay off by 2^-22, as the fast
+// exponential's, is a state off by that times the tokens it remembers), and 1 - a^2 = -e (2 + e) keeps its
+// digits. Below it the difference, which has lost at most two bits. (The backward pass has a already.)
+template <int V> __device__ __forceinline__ Ch<V> series(const Ch<V>& g) {
+  Ch<V> p = fma(g, all<V>(1.f / 720.f), all<V>(1.f / 120.f));
+  p = fma(p, g, all<V>(1.f / 24.f));
+  p = fma(p, g, all<V>(1.f / 6.f));
+  p = fma(p, g, all<V>(0.5f));
+  p = fma(p, g, all<V>(1.f));
+  return mul(p, g);
+}
+constexpr float kSeries = -0.175f;
+template <int V> __device__ __forceinline__ Ch<V> loss(const Ch<V>& g, const Ch<V>& e, const Ch<V>& a) {
+  const Ch<V> near = mul(e, add(neg(e), all<V>(-2.f)));
+  Ch<V> w = fma(neg(a), a, all<V>(1.f));
+#pragma unroll
+  for (int i = 0; i < V; ++i) w.f[i] = g.f[i] > kSeries ? near.f[i] : w.f[i];
+  return w;
+}
+template <bool kFast, int V> __device__ __forceinline__ Ch<V> decay(const Ch<V>& g, Ch<V>& w) {
   Ch<V> a;
   if constexpr (kFast) {
     a = mul(g, all<V>(kLog2e));
@@ -185,24 +197,11 @@ template <bool kFast, int V> __device__ __forceinline__ Ch<V> decay(const Ch<V>&
 #pragma unroll
     for (int i = 0; i < V; ++i) a.f[i] = expf(g.f[i]);
   }
-  return a;
-}
-
-// 1 - a^2 of a = e^g, g <= 0: above -0.175 the series of -expm1(2 g) (its next term is 2^-26 of it there),
-// below it the difference, which has lost at most two bits.
-template <int V> __device__ __forceinline__ Ch<V> loss(const Ch<V>& g, const Ch<V>& a) {
-  const Ch<V> z = add(g, g);
-  Ch<V> p = fma(z, all<V>(1.f / 5040.f), all<V>(1.f / 720.f));
-  p = fma(p, z, all<V>(1.f / 120.f));
-  p = fma(p, z, all<V>(1.f / 24.f));
-  p = fma(p, z, all<V>(1.f / 6.f));
-  p = fma(p, z, all<V>(0.5f));
-  p = fma(p, z, all<V>(1.f));
-  p = mul(p, neg(z));
-  Ch<V> d = fma(neg(a), a, all<V>(1.f));
+  const Ch<V> e = series(g), near = add(e, all<V>(1.f));
+  w = loss(g, e, a);
 #pragma unroll
-  for (int i = 0; i < V; ++i) d.f[i] = z.f[i] > -0.35f ? p.f[i] : d.f[i];
-  return d;
+  for (int i = 0; i < V; ++i) a.f[i] = g.f[i] > kSeries ? near.f[i] : a.f[i];
+  return a;
 }
 
 template <bool kFast> __device__ __forceinline__ float root(float w) {
@@ -221,11 +220,12 @@ template <bool kFast, int V> __device__ __forceinline__ Ch<V> root(Ch<V> w) {
 
 // ---- planning -------------------------------------------------------------------------------
 // The sequence of each row (-1: none that is valid; the last one that holds it where lengths run
-// backwards), flags cleared, rows of the sequences without tokens written: to <- from (zeros if null).
+// backwards), what tiles tell each other unset, rows of the sequences without tokens written: to <- from
+// (zeros if null).
 __global__ void __launch_bounds__(1024)
 gated_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ idx, int N, int64_t T,
-                  int64_t num_slots, WsHeader* hdr, int32_t* __restrict__ seq, uint32_t* __restrict__ flags,
-                  int64_t num_flags, const float* from, float* to, int ch, bool zero_bad) {
+                  int64_t num_slots, WsHeader* hdr, int32_t* __restrict__ seq, uint4* __restrict__ unset,
+                  int64_t num_unset, const float* from, float* to, int ch, bool zero_bad) {
   __shared__ int s_seq[kPlanRows];
   const int tid = threadIdx.x;
   if (blockIdx.x == 0) {
@@ -235,7 +235,8 @@ gated_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ id
       hdr->num_entries = 0;
     }
   }
-  for (int64_t i = blockIdx.x * 1024ll + tid; i < num_flags; i += gridDim.x * 1024ll) flags[i] = 0;
+  for (int64_t i = blockIdx.x * 1024ll + tid; i < num_unset; i += gridDim.x * 1024ll)
+    unset[i] = make_uint4(kUnset, kUnset, kUnset, kUnset);
   for (int64_t t0 = (int64_t)blockIdx.x * kPlanRows; t0 < T; t0 += (int64_t)gridDim.x * kPlanRows) {
     s_seq[tid] = -1;
     __syncthreads();
@@ -269,120 +270,140 @@ gated_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ id
 
 struct Plan {
   const int32_t* seq;
-  uint32_t *flag, *gflag;
-  float *agg_a, *agg_h, *group;
+  float *agg, *group;
   int64_t tiles;
   int32_t blocks;
+  uint32_t items;      // tiles of all channel blocks
 };
 
-// ---- waits between tiles --------------------------------------------------------------------
-__device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
-  uint32_t v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
+// ---- what tiles tell each other ---------------------------------------------------------------
+// Two 32-bit values of each of a lane's channels, 8 bytes a channel, each written and read at once.
+template <int V> struct Pair { float a[V], h[V]; };
+template <int V> __device__ __forceinline__ void tell(float* at, const Pair<V>& p) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    asm volatile("{\n .reg .b64 t;\n mov.b64 t, {%1, %2};\n st.relaxed.gpu.global.b64 [%0], t;\n}\n" ::"l"(at + 2 * i),
+                 "f"(p.a[i]), "f"(p.h[i])
+                 : "memory");
+  }
 }
-__device__ __forceinline__ void store_release(uint32_t* p, uint32_t v) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+template <int V> __device__ __forceinline__ bool hear(const float* at, Pair<V>& p) {
+  bool set = true;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    asm volatile("{\n .reg .b64 t;\n ld.relaxed.gpu.global.b64 t, [%2];\n mov.b64 {%0, %1}, t;\n}\n"
+                 : "=f"(p.a[i]), "=f"(p.h[i])
+                 : "l"(at + 2 * i)
+                 : "memory");
+    set = set && __float_as_uint(p.a[i]) != kUnset;
+  }
+  return set;
 }
-// Waits until *p is set, or until another tile has given up, or for limit_ns; 0 if it gave up.
-__device__ __noinline__ uint32_t wait_flag_slow(const uint32_t* p, WsHeader* hdr, uint64_t limit_ns) {
+// The whole warp waits for its lanes' pairs, or until another tile has given up, or for limit_ns.
+template <int V>
+__device__ __noinline__ void hear_slow(const float* at, Pair<V>& p, bool in, WsHeader* hdr, uint64_t limit_ns) {
   const uint64_t t0 = tc::globaltimer_ns();
   for (;;) {
-    for (int i = 0; i < 64; ++i) {
-      const uint32_t v = load_acquire(p);
-      if (v) return v;
-    }
-    if (load_acquire(&hdr->num_entries)) return 0;
-    if (tc::globaltimer_ns() - t0 > limit_ns) {
+    for (int i = 0; i < 64; ++i)
+      if (__all_sync(0xffffffffu, !in || hear(at, p))) return;
+    if (*(volatile uint32_t*)&hdr->num_entries) return;
+    if (__any_sync(0xffffffffu, tc::globaltimer_ns() - t0 > limit_ns)) {
       raise_status(&hdr->status, KDA_DEVICE_PIPE_TIMEOUT);
-      store_release(&hdr->num_entries, 1);
-      return 0;
+      atomicExch(&hdr->num_entries, 1u);
+      return;
     }
   }
 }
-__device__ __forceinline__ uint32_t wait_flag(const uint32_t* p, WsHeader* hdr, uint64_t limit_ns) {
-  const uint32_t v = load_acquire(p);
-  return v ? v : wait_flag_slow(p, hdr, limit_ns);
-}
 
-// What is shared by the warps of a tile: each warp's (A, H) and whether a sequence begins in it, and
-// those of the tiles before it in its group.
-template <int V> struct Shared {
-  Ch<V> a[kWarps][32], h[kWarps][32];
-  Ch<V> ga[kGroup][32], gh[kGroup][32];
-  uint32_t cut[kWarps], gcut[kGroup];
-  int64_t tile;
-};
-
-template <int V>
-__device__ __forceinline__ void fold(Ch<V>& h, const Ch<V>& A, const Ch<V>& H, bool cut) {
+// h <- A h + H; a run in which a sequence begins has A = -1 and forgets h.
+template <int V> __device__ __forceinline__ void fold(Ch<V>& h, const Ch<V>& A, const Ch<V>& H) {
   const Ch<V> n = fma(A, h, H);
 #pragma unroll
-  for (int i = 0; i < V; ++i) h.f[i] = cut ? H.f[i] : n.f[i];
+  for (int i = 0; i < V; ++i) h.f[i] = A.f[i] < 0.f ? H.f[i] : n.f[i];
+}
+// The run (A, H) followed by (B, G), as one in (A, H).
+template <int V> __device__ __forceinline__ void join(Ch<V>& A, Ch<V>& H, const Ch<V>& B, const Ch<V>& G) {
+  fold(H, B, G);
+  const Ch<V> n = mul(A, B);
+#pragma unroll
+  for (int i = 0; i < V; ++i) A.f[i] = A.f[i] < 0.f || B.f[i] < 0.f ? -1.f : n.f[i];
 }
 
-// The state that reaches tile `pos` (counted in the order of the pass) of channel block cb, of the
-// channels of this lane, for warp `rank` of it (warps counted in that order too).
+// What is shared by the warps of a tile: each warp's (A, H), in the order of the pass, and pairs of tiles
+// before it in its group.
+template <int V> struct Shared {
+  Ch<V> a[kWarps][32], h[kWarps][32];
+  Ch<V> ga[kGroup / 2][32], gh[kGroup / 2][32];
+  Ch<V> start[32];
+  uint32_t next;
+};
+
+// The state that reaches warp `rank` of tile `pos` (both counted in the order of the pass), of this lane's
+// channels.  Each warp looks after two tiles of the group, the last one after one and the group's start.
 template <int V>
-__device__ __forceinline__ Ch<V> enter(Shared<V>& s, const Plan& p, int64_t pos, int cb, int c, int ch,
-                                       int warp, int lane, int rank, WsHeader* hdr, uint64_t limit_ns) {
+__device__ __forceinline__ Ch<V> enter(Shared<V>& s, const Plan& p, int64_t pos, int c, int ch, int warp, int lane,
+                                       int rank, WsHeader* hdr, uint64_t limit_ns) {
+  static_assert(kGroup == 2 * kWarps, "two tiles a warp");
   const int before = (int)(pos % kGroup);
   const int64_t g = pos / kGroup, first = g * kGroup;
   const bool in = c < ch;
-  if (warp == 0) {  // the whole tile's
-    Ch<V> A = s.a[0][lane], H = s.h[0][lane];
-    // warps in the order of the pass: rank 0 is stored first
-    uint32_t cut = s.cut[0];
+  Pair<V> one, two;
+  const int j = 2 * warp;
+  const bool start = warp == kWarps - 1;
+  const bool want1 = j < before, want2 = start ? g > 0 : j + 1 < before;
+  const float* at1 = p.agg + ((first + j) * ch + c) * 2;
+  const float* at2 = start ? p.group + (g * ch + c) * 2 : at1 + 2 * (int64_t)ch;
+  bool got1 = true, got2 = true;
+  if (want1) got1 = !in || hear(at1, one);
+  if (want2) got2 = !in || hear(at2, two);
+  Ch<V> A, H;
+  if (warp == 0 && before < kGroup - 1 && pos + 1 < p.tiles) {  // the whole tile's, for the tiles after it
+    A = s.a[0][lane];
+    H = s.h[0][lane];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-      fold(H, s.a[w][lane], s.h[w][lane], s.cut[w] != 0);
-      A = mul(A, s.a[w][lane]);
-      cut |= s.cut[w];
-    }
-    if (before < kGroup - 1 && pos + 1 < p.tiles) {
-      if (in) {
-        store<float, V>(p.agg_a + pos * ch + c, A);
-        store<float, V>(p.agg_h + pos * ch + c, H);
-      }
-      __syncwarp();
-      if (lane == 0) {
-        __threadfence();
-        store_release(p.flag + pos * p.blocks + cb, cut ? 2u : 1u);
-      }
-    }
-    s.ga[before][lane] = A;
-    s.gh[before][lane] = H;
-    if (lane == 0) s.gcut[before] = cut;
-  }
-  for (int j = warp; j < before; j += kWarps) {
-    uint32_t v = 0;
-    if (lane == 0) v = wait_flag(p.flag + (first + j) * p.blocks + cb, hdr, limit_ns);
-    v = __shfl_sync(0xffffffffu, v, 0);
+    for (int w = 1; w < kWarps; ++w) join(A, H, s.a[w][lane], s.h[w][lane]);
     if (in) {
-      s.ga[j][lane] = load_shared_state<V>(p.agg_a + (first + j) * ch + c);
-      s.gh[j][lane] = load_shared_state<V>(p.agg_h + (first + j) * ch + c);
+      Pair<V> t;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        t.a[i] = A.f[i] != A.f[i] ? __uint_as_float(0x7fc00000u) : A.f[i];
+        t.h[i] = H.f[i];
+      }
+      tell(p.agg + (pos * ch + c) * 2, t);
     }
-    if (lane == 0) s.gcut[j] = v == 2;
   }
-  Ch<V> h = all<V>(0.f);
-  if (g > 0) {
-    if (lane == 0) wait_flag(p.gflag + g * p.blocks + cb, hdr, limit_ns);
-    __syncwarp();
-    if (in) h = load_shared_state<V>(p.group + g * ch + c);
+  if (want1) {
+    if (!__all_sync(0xffffffffu, got1)) hear_slow(at1, one, in, hdr, limit_ns);
+#pragma unroll
+    for (int i = 0; i < V; ++i) A.f[i] = one.a[i], H.f[i] = one.h[i];
+  }
+  if (want2) {
+    if (!__all_sync(0xffffffffu, got2)) hear_slow(at2, two, in, hdr, limit_ns);
+    Ch<V> B, G;
+#pragma unroll
+    for (int i = 0; i < V; ++i) B.f[i] = two.a[i], G.f[i] = two.h[i];
+    if (start) s.start[lane] = G;
+    else join(A, H, B, G);
+  }
+  if (want1) {
+    s.ga[warp][lane] = A;
+    s.gh[warp][lane] = H;
   }
   __syncthreads();
-  for (int j = 0; j < before; ++j) fold(h, s.ga[j][lane], s.gh[j][lane], s.gcut[j] != 0);
-  if (warp == 0 && before == kGroup - 1 && pos + 1 < p.tiles) {
+  Ch<V> h = g > 0 ? s.start[lane] : all<V>(0.f);
+  for (int w = 0; 2 * w < before; ++w) fold(h, s.ga[w][lane], s.gh[w][lane]);
+  if (warp == kWarps - 1 && before == kGroup - 1 && pos + 1 < p.tiles) {  // the next group's start
     Ch<V> n = h;
-    fold(n, s.ga[before][lane], s.gh[before][lane], s.gcut[before] != 0);
-    if (in) store<float, V>(p.group + (g + 1) * ch + c, n);
-    __syncwarp();
-    if (lane == 0) {
-      __threadfence();
-      store_release(p.gflag + (g + 1) * p.blocks + cb, 1u);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) fold(n, s.a[w][lane], s.h[w][lane]);
+    if (in) {
+      Pair<V> t;
+#pragma unroll
+      for (int i = 0; i < V; ++i) t.a[i] = 1.f, t.h[i] = n.f[i];
+      tell(p.group + ((g + 1) * ch + c) * 2, t);
     }
   }
-  for (int w = 0; w < rank; ++w) fold(h, s.a[w][lane], s.h[w][lane], s.cut[w] != 0);
+  for (int w = 0; w < rank; ++w) fold(h, s.a[w][lane], s.h[w][lane]);
   return h;
 }
 
@@ -391,18 +412,40 @@ struct Rows {
   uint32_t valid, first, last;
   int seq;
 };
+struct RowsRaw {
+  int seq, before, after;
+};
 template <int S>
-__device__ __forceinline__ Rows rows_of(const int32_t* seq, int64_t t0, int64_t T, int lane) {
-  Rows r;
+__device__ __forceinline__ RowsRaw rows_load(const int32_t* seq, int64_t t0, int64_t T, int lane) {
   const int64_t t = t0 + lane;
+  RowsRaw r;
   r.seq = lane < S && t < T ? seq[t] : -1;
-  const int before = lane < S && t < T && t > 0 ? seq[t - 1] : -1;
-  const int after = lane < S && t + 1 < T ? seq[t + 1] : -1;
-  r.valid = __ballot_sync(0xffffffffu, r.seq >= 0);
-  r.first = __ballot_sync(0xffffffffu, r.seq >= 0 && before != r.seq);
-  r.last = __ballot_sync(0xffffffffu, r.seq >= 0 && after != r.seq);
+  r.before = lane < S && t < T && t > 0 ? seq[t - 1] : -1;
+  r.after = lane < S && t + 1 < T ? seq[t + 1] : -1;
   return r;
 }
+__device__ __forceinline__ Rows rows_of(const RowsRaw& r) {
+  Rows o;
+  o.seq = r.seq;
+  o.valid = __ballot_sync(0xffffffffu, r.seq >= 0);
+  o.first = __ballot_sync(0xffffffffu, r.seq >= 0 && r.before != r.seq);
+  o.last = __ballot_sync(0xffffffffu, r.seq >= 0 && r.after != r.seq);
+  return o;
+}
+
+// A row's elements on their way into this thread's place of shared memory (zeros where there is none).
+template <typename T, int V>
+__device__ __forceinline__ void fetch(typename Pack<T, V>::Raw* to, const T* from, bool ok) {
+  constexpr int kBytes = sizeof(T) * V;
+  if constexpr (kBytes >= 4) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(tc::smem_u32(to)), "l"(from), "n"(kBytes),
+                 "r"(ok ? kBytes : 0)
+                 : "memory");
+  } else {
+    *to = ok ? load<T, V>(from) : Pack<T, V>::close(all<V>(0.f));
+  }
+}
+__device__ __forceinline__ void fetch_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // ---- forward --------------------------------------------------------------------------------
 template <typename T, int V, bool kGate, int S>
@@ -414,65 +457,88 @@ gated_scan_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
                   int64_t total, int ch, uint64_t limit_ns) {
   constexpr bool kFast = sizeof(T) == 2;
   using P = Pack<T, V>;
+  using Raw = typename P::Raw;
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  Raw* const mine = reinterpret_cast<Raw*>(s_raw) + threadIdx.x;   // [input][row], kThreads apart
   __shared__ Shared<V> s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) s.tile = atomicAdd(&hdr->next_item, 1u);
-  __syncthreads();
-  const int64_t k = s.tile / plan.blocks;
-  const int cb = (int)(s.tile % plan.blocks);
-  const int64_t t0 = (k * kWarps + warp) * S;
-  const int c = (cb * 32 + lane) * V;
-  const bool in = c < ch;
 
-  typename P::Raw xr[S], rr[S], ir[S];
-#pragma unroll
-  for (int j = 0; j < S; ++j) {
-    const bool ok = in && t0 + j < total;
-    xr[j] = ok ? load<T, V>(x + (t0 + j) * x_pitch + c) : P::close(all<V>(0.f));
-    rr[j] = ok ? load<T, V>(r + (t0 + j) * r_pitch + c) : P::close(all<V>(0.f));
-    if (kGate) ir[j] = ok ? load<T, V>(ig + (t0 + j) * i_pitch + c) : P::close(all<V>(0.f));
-  }
-  const Ch<V> rate = rates<V>(a_log, c, ch);
-  const Rows rows = rows_of<S>(plan.seq, t0, total, lane);
-
-  Ch<V> a[S], b[S];
-  Ch<V> A = all<V>(1.f), H = all<V>(0.f);
-#pragma unroll
-  for (int j = 0; j < S; ++j) {
-    const Ch<V> g = mul(rate, sigmoid<kFast>(P::open(rr[j])));
-    a[j] = decay<kFast>(g);
-    b[j] = mul(root<kFast>(loss(g, a[j])), P::open(xr[j]));
-    if (kGate) b[j] = mul(b[j], sigmoid<kFast>(P::open(ir[j])));
-    if ((rows.first >> j) & 1) {  // the sequence's own state instead of what came before
-      const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-      const int64_t slot = idx ? resolve_slot(idx, n, num_slots) : n;
-      Ch<V> h0 = all<V>(0.f);
-      if (state && in && KDA_CHECK(slot >= 0)) h0 = Pack<float, V>::open(load<float, V>(state + slot * stride + c));
-      b[j] = fma(a[j], h0, b[j]);
-      H = b[j];
-    } else {
-      H = fma(a[j], H, b[j]);
-    }
-    A = mul(A, a[j]);
-  }
-  s.a[warp][lane] = A;
-  s.h[warp][lane] = H;
-  if (lane == 0) s.cut[warp] = rows.first != 0;
+  if (tid == 0) s.next = atomicAdd(&hdr->next_item, 1u);
   __syncthreads();
-  Ch<V> h = enter(s, plan, k, cb, c, ch, warp, lane, warp, hdr, limit_ns);
-  if (carries && t0 % KDA_GATED_CARRY_ROWS == 0 && t0 < total && in)
-    store<float, V>(carries + t0 / KDA_GATED_CARRY_ROWS * ch + c, h);
+  uint32_t item = s.next;
+  RowsRaw rows_raw;
+  float rate_raw[V];
+  auto prefetch = [&](uint32_t it) {
+    const int64_t k = it / plan.blocks, t0 = (k * kWarps + warp) * S;
+    const int c = ((int)(it % plan.blocks) * 32 + lane) * V;
+    const bool in = c < ch;
+    const T *xp = x + (in ? t0 * x_pitch + c : 0), *rp = r + (in ? t0 * r_pitch + c : 0);
+    const T* ip = kGate ? ig + (in ? t0 * i_pitch + c : 0) : nullptr;
 #pragma unroll
-  for (int j = 0; j < S; ++j) {
-    if ((rows.first >> j) & 1) h = b[j];
-    else h = fma(a[j], h, b[j]);
-    if (((rows.valid >> j) & 1) && in && KDA_CHECK(t0 + j < total && c + V <= ch))
-      store<T, V>(y + (t0 + j) * ch + c, h);
-    if (((rows.last >> j) & 1) && final_state) {
-      const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-      const int64_t slot = idx ? resolve_slot(idx, n, num_slots) : n;
-      if (in && KDA_CHECK(slot >= 0)) store<float, V>(final_state + slot * stride + c, h);
+    for (int j = 0; j < S; ++j) {
+      const bool ok = in && t0 + j < total;
+      fetch<T, V>(mine + j * kThreads, ok ? xp + j * x_pitch : x, ok);
+      fetch<T, V>(mine + (S + j) * kThreads, ok ? rp + j * r_pitch : r, ok);
+      if (kGate) fetch<T, V>(mine + (2 * S + j) * kThreads, ok ? ip + j * i_pitch : ig, ok);
     }
+    rows_raw = rows_load<S>(plan.seq, t0, total, lane);
+#pragma unroll
+    for (int i = 0; i < V; ++i) rate_raw[i] = c + i < ch ? a_log[c + i] : 0.f;
+  };
+  if (item < plan.items) prefetch(item);
+  while (item < plan.items) {
+    const int64_t k = item / plan.blocks, t0 = (k * kWarps + warp) * S;
+    const int c = ((int)(item % plan.blocks) * 32 + lane) * V;
+    const bool in = c < ch;
+    if (tid == 0) s.next = atomicAdd(&hdr->next_item, 1u);
+    Ch<V> rate;
+#pragma unroll
+    for (int i = 0; i < V; ++i) rate.f[i] = ssm_rate(rate_raw[i]);
+    const Rows rows = rows_of(rows_raw);
+    fetch_done();
+
+    Ch<V> a[S], b[S];
+    Ch<V> A = all<V>(1.f), H = all<V>(0.f);
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      Ch<V> w;
+      a[j] = decay<kFast>(mul(rate, sigmoid<kFast>(P::open(mine[(S + j) * kThreads]))), w);
+      b[j] = mul(root<kFast>(w), P::open(mine[j * kThreads]));
+      if (kGate) b[j] = mul(b[j], sigmoid<kFast>(P::open(mine[(2 * S + j) * kThreads])));
+      if ((rows.first >> j) & 1) {  // the sequence's own state instead of what came before
+        const int n = __shfl_sync(0xffffffffu, rows.seq, j);
+        const int64_t slot = idx ? resolve_slot(idx, n, num_slots) : n;
+        Ch<V> h0 = all<V>(0.f);
+        if (state && in && KDA_CHECK(slot >= 0)) h0 = Pack<float, V>::open(load<float, V>(state + slot * stride + c));
+        b[j] = fma(a[j], h0, b[j]);
+        H = b[j];
+      } else {
+        H = fma(a[j], H, b[j]);
+      }
+      A = mul(A, a[j]);
+    }
+    s.a[warp][lane] = rows.first ? all<V>(-1.f) : A;
+    s.h[warp][lane] = H;
+    __syncthreads();
+    const uint32_t next = s.next;
+    if (next < plan.items) prefetch(next);
+    Ch<V> h = enter(s, plan, k, c, ch, warp, lane, warp, hdr, limit_ns);
+    if (carries && t0 % KDA_GATED_CARRY_ROWS == 0 && t0 < total && in)
+      store<float, V>(carries + t0 / KDA_GATED_CARRY_ROWS * ch + c, h);
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      if ((rows.first >> j) & 1) h = b[j];
+      else h = fma(a[j], h, b[j]);
+      if (((rows.valid >> j) & 1) && in && KDA_CHECK(t0 + j < total && c + V <= ch))
+        store<T, V>(y + (t0 + j) * ch + c, h);
+      if (((rows.last >> j) & 1) && final_state) {
+        const int n = __shfl_sync(0xffffffffu, rows.seq, j);
+        const int64_t slot = idx ? resolve_slot(idx, n, num_slots) : n;
+        if (in && KDA_CHECK(slot >= 0)) store<float, V>(final_state + slot * stride + c, h);
+      }
+    }
+    __syncthreads();   // everyone has read s before the next tile writes it
+    item = next;
   }
   KDA_DEBUG_FOLD(&hdr->status);
 }
@@ -487,134 +553,170 @@ gated_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restric
                   T* __restrict__ dr, T* __restrict__ di, float* __restrict__ dstate, float* __restrict__ part,
                   Plan plan, WsHeader* hdr, int64_t total, int ch, uint64_t limit_ns) {
   constexpr bool kFast = sizeof(T) == 2;
+  constexpr int kInputs = kGate ? 4 : 3;
   static_assert(S * kWarps == KDA_GATED_CARRY_ROWS, "a tile starts where a carry was left");
   using P = Pack<T, V>;
+  using Raw = typename P::Raw;
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  Raw* mine = reinterpret_cast<Raw*>(s_raw) + threadIdx.x;   // [stage][input][row], kThreads apart
+  Raw* other = mine + kInputs * S * kThreads;
   __shared__ Shared<V> s;
-  __shared__ Ch<V> s_fa[kWarps][32], s_fh[kWarps][32];  // the state's own (A, H)
-  __shared__ uint32_t s_first[kWarps];
+  __shared__ Ch<V> s_fa[kWarps][32], s_fh[kWarps][32];       // the state's own (A, H)
+  __shared__ Ch<V> s_sum[kWarps][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) s.tile = atomicAdd(&hdr->next_item, 1u);
-  __syncthreads();
-  const int64_t pos = s.tile / plan.blocks;          // tiles from the last one on
-  const int64_t k = plan.tiles - 1 - pos;
-  const int cb = (int)(s.tile % plan.blocks);
-  const int64_t t0 = (k * kWarps + warp) * S;
-  const int c = (cb * 32 + lane) * V;
-  const bool in = c < ch;
 
-  typename P::Raw xr[S], rr[S], ir[S], gr[S];
-#pragma unroll
-  for (int j = 0; j < S; ++j) {
-    const bool ok = in && t0 + j < total;
-    xr[j] = ok ? load<T, V>(x + (t0 + j) * x_pitch + c) : P::close(all<V>(0.f));
-    rr[j] = ok ? load<T, V>(r + (t0 + j) * r_pitch + c) : P::close(all<V>(0.f));
-    if (kGate) ir[j] = ok ? load<T, V>(ig + (t0 + j) * i_pitch + c) : P::close(all<V>(0.f));
-    gr[j] = ok ? load<T, V>(dy + (t0 + j) * dy_pitch + c) : P::close(all<V>(0.f));
-  }
-  const Ch<V> rate = rates<V>(a_log, c, ch);
-  const Rows rows = rows_of<S>(plan.seq, t0, total, lane);
-  Ch<V> h = in ? Pack<float, V>::open(load<float, V>(carries + k * ch + c)) : all<V>(0.f);
-
-  // the rows' decays and the state's (A, H), then what they do to e, from the last row to the first
-  Ch<V> a[S], er[S], ei[S], hp[S];
-  Ch<V> A = all<V>(1.f), H = all<V>(0.f);
-#pragma unroll
-  for (int j = 0; j < S; ++j) {
-    er[j] = exp_neg<kFast>(P::open(rr[j]));
-    const Ch<V> g = mul(rate, one_over<kFast>(er[j]));
-    a[j] = decay<kFast>(g);
-    Ch<V> b = mul(root<kFast>(loss(g, a[j])), P::open(xr[j]));
-    if (kGate) {
-      ei[j] = exp_neg<kFast>(P::open(ir[j]));
-      b = mul(b, one_over<kFast>(ei[j]));
-    }
-    if ((rows.first >> j) & 1) {
-      const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-      Ch<V> h0 = all<V>(0.f);
-      if (state && in) h0 = Pack<float, V>::open(load<float, V>(state + (int64_t)n * ch + c));
-      hp[j] = h0;
-      H = fma(a[j], h0, b);
-    } else {
-      hp[j] = H;               // within the warp; what reaches it is added below
-      H = fma(a[j], H, b);
-    }
-    A = mul(A, a[j]);
-  }
-  s_fa[warp][lane] = A;
-  s_fh[warp][lane] = H;
-  if (lane == 0) s_first[warp] = rows.first != 0;
-  Ch<V> E = all<V>(0.f);
-#pragma unroll
-  for (int j = S - 1; j >= 0; --j) {
-    Ch<V> l = P::open(gr[j]);
-    if ((rows.last >> j) & 1) {
-      const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-      if (dfinal && in) l = add(l, Pack<float, V>::open(load<float, V>(dfinal + (int64_t)n * ch + c)));
-    } else {
-      l = add(l, E);
-    }
-    E = mul(a[j], l);
-  }
-  const int rank = kWarps - 1 - warp;
-  s.a[rank][lane] = A;
-  s.h[rank][lane] = E;
-  if (lane == 0) s.cut[rank] = rows.last != 0;
+  if (tid == 0) s.next = atomicAdd(&hdr->next_item, 1u);
   __syncthreads();
-  Ch<V> e = enter(s, plan, pos, cb, c, ch, warp, lane, rank, hdr, limit_ns);
-  for (int w = 0; w < warp; ++w) fold(h, s_fa[w][lane], s_fh[w][lane], s_first[w] != 0);
-  {
-    Ch<V> q = h;               // decayed from row to row until a sequence begins
+  uint32_t item = s.next;
+  RowsRaw rows_raw;
+  float rate_raw[V];
+  Ch<V> carry;
+  auto prefetch = [&](uint32_t it, Raw* to) {
+    const int64_t k = plan.tiles - 1 - it / plan.blocks, t0 = (k * kWarps + warp) * S;
+    const int c = ((int)(it % plan.blocks) * 32 + lane) * V;
+    const bool in = c < ch;
+    const T *xp = x + (in ? t0 * x_pitch + c : 0), *rp = r + (in ? t0 * r_pitch + c : 0);
+    const T *gp = dy + (in ? t0 * dy_pitch + c : 0), *ip = kGate ? ig + (in ? t0 * i_pitch + c : 0) : nullptr;
 #pragma unroll
     for (int j = 0; j < S; ++j) {
-      if ((rows.first >> j) & 1) break;
-      hp[j] = add(hp[j], q);
-      q = mul(q, a[j]);
+      const bool ok = in && t0 + j < total;
+      fetch<T, V>(to + j * kThreads, ok ? xp + j * x_pitch : x, ok);
+      fetch<T, V>(to + (S + j) * kThreads, ok ? rp + j * r_pitch : r, ok);
+      fetch<T, V>(to + (2 * S + j) * kThreads, ok ? gp + j * dy_pitch : dy, ok);
+      if (kGate) fetch<T, V>(to + (3 * S + j) * kThreads, ok ? ip + j * i_pitch : ig, ok);
     }
-  }
-  Ch<V> sum = all<V>(0.f);
+    rows_raw = rows_load<S>(plan.seq, t0, total, lane);
+    carry = in ? Pack<float, V>::open(load<float, V>(carries + k * ch + c)) : all<V>(0.f);
 #pragma unroll
-  for (int j = S - 1; j >= 0; --j) {
-    const bool valid = (rows.valid >> j) & 1;
-    Ch<V> l = P::open(gr[j]);
-    if ((rows.last >> j) & 1) {
-      const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-      if (dfinal && in) l = add(l, Pack<float, V>::open(load<float, V>(dfinal + (int64_t)n * ch + c)));
-    } else {
-      l = add(l, e);
-    }
-    e = mul(a[j], l);
-    const Ch<V> sr = one_over<kFast>(er[j]), g = mul(rate, sr);
-    const Ch<V> m = root<kFast>(loss(g, a[j]));
-    Ch<V> q;
+    for (int i = 0; i < V; ++i) rate_raw[i] = c + i < ch ? a_log[c + i] : 0.f;
+  };
+  if (item < plan.items) prefetch(item, mine);
+  while (item < plan.items) {
+    const int64_t pos = item / plan.blocks, k = plan.tiles - 1 - pos;   // tiles from the last one on
+    const int64_t t0 = (k * kWarps + warp) * S;
+    const int c = ((int)(item % plan.blocks) * 32 + lane) * V;
+    const bool in = c < ch;
+    if (tid == 0) s.next = atomicAdd(&hdr->next_item, 1u);
+    Ch<V> rate;
 #pragma unroll
-    for (int i = 0; i < V; ++i) q.f[i] = m.f[i] == 0.f ? 0.f : kFast ? __fdividef(g.f[i], m.f[i]) : g.f[i] / m.f[i];
-    Ch<V> u = P::open(xr[j]), ml = mul(m, l), si;
-    if (kGate) {
-      si = one_over<kFast>(ei[j]);
-      u = mul(u, si);
-    }
-    // p = e (g h_{t-1} - a (g / m) u)
-    const Ch<V> p = mul(e, fma(g, hp[j], neg(mul(mul(a[j], q), u))));
-    if (in && t0 + j < total && KDA_CHECK(c + V <= ch)) {
-      const int64_t at = (t0 + j) * ch + c;
-      const Ch<V> zero = all<V>(0.f);
-      store<T, V>(dx + at, !valid ? zero : kGate ? mul(ml, si) : ml);
-      store<T, V>(dr + at, valid ? mul(p, mul(er[j], sr)) : zero);
-      if (kGate) store<T, V>(di + at, valid ? mul(mul(ml, u), mul(ei[j], si)) : zero);
-    }
-    if (valid) sum = add(sum, p);
-    if (((rows.first >> j) & 1) && dstate) {
-      const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-      if (in) store<float, V>(dstate + (int64_t)n * ch + c, e);
-    }
-  }
-  __syncthreads();
-  s.a[warp][lane] = sum;
-  __syncthreads();
-  if (warp == 0 && in) {
+    for (int i = 0; i < V; ++i) rate.f[i] = ssm_rate(rate_raw[i]);
+    const Rows rows = rows_of(rows_raw);
+    Ch<V> h = carry;
+    fetch_done();
+    // dy, and dfinal where the row is a sequence's last
+    auto slope = [&](int j) {
+      Ch<V> l = P::open(mine[(2 * S + j) * kThreads]);
+      if (((rows.last >> j) & 1) && dfinal) {
+        const int n = __shfl_sync(0xffffffffu, rows.seq, j);
+        if (in) l = add(l, Pack<float, V>::open(load<float, V>(dfinal + (int64_t)n * ch + c)));
+      }
+      return l;
+    };
+
+    // the rows' decays and the state's (A, H), then what they do to e, from the last row to the first
+    Ch<V> a[S], er[S], ei[S], hp[S];
+    Ch<V> A = all<V>(1.f), H = all<V>(0.f);
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) sum = add(sum, s.a[w][lane]);
-    store<float, V>(part + k * ch + c, sum);
+    for (int j = 0; j < S; ++j) {
+      Ch<V> w;
+      er[j] = exp_neg<kFast, true>(P::open(mine[(S + j) * kThreads]));
+      a[j] = decay<kFast>(mul(rate, one_over<kFast>(er[j])), w);
+      Ch<V> b = mul(root<kFast>(w), P::open(mine[j * kThreads]));
+      if (kGate) {
+        ei[j] = exp_neg<kFast, true>(P::open(mine[(3 * S + j) * kThreads]));
+        b = mul(b, one_over<kFast>(ei[j]));
+      }
+      if ((rows.first >> j) & 1) {
+        const int n = __shfl_sync(0xffffffffu, rows.seq, j);
+        Ch<V> h0 = all<V>(0.f);
+        if (state && in) h0 = Pack<float, V>::open(load<float, V>(state + (int64_t)n * ch + c));
+        hp[j] = h0;
+        H = fma(a[j], h0, b);
+      } else {
+        hp[j] = H;               // within the warp; what reaches it is added below
+        H = fma(a[j], H, b);
+      }
+      A = mul(A, a[j]);
+    }
+    s_fa[warp][lane] = rows.first ? all<V>(-1.f) : A;
+    s_fh[warp][lane] = H;
+    Ch<V> E = all<V>(0.f);
+#pragma unroll
+    for (int j = S - 1; j >= 0; --j) {
+      const Ch<V> l = slope(j);
+      E = mul(a[j], (rows.last >> j) & 1 ? l : add(l, E));
+    }
+    const int rank = kWarps - 1 - warp;
+    s.a[rank][lane] = rows.last ? all<V>(-1.f) : A;
+    s.h[rank][lane] = E;
+    __syncthreads();
+    const uint32_t next = s.next;
+    if (next < plan.items) prefetch(next, other);
+    Ch<V> e = enter(s, plan, pos, c, ch, warp, lane, rank, hdr, limit_ns);
+    for (int w = 0; w < warp; ++w) fold(h, s_fa[w][lane], s_fh[w][lane]);
+    {
+      Ch<V> q = h;               // decayed from row to row until a sequence begins
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        if ((rows.first >> j) & 1) break;
+        hp[j] = add(hp[j], q);
+        q = mul(q, a[j]);
+      }
+    }
+    Ch<V> sum = all<V>(0.f);
+#pragma unroll
+    for (int j = S - 1; j >= 0; --j) {
+      const bool valid = (rows.valid >> j) & 1;
+      Ch<V> l = slope(j);
+      if (!((rows.last >> j) & 1)) l = add(l, e);
+      e = mul(a[j], l);
+      const Ch<V> sr = one_over<kFast>(er[j]), g = mul(rate, sr);
+      const Ch<V> w = loss(g, series(g), a[j]);
+      Ch<V> m, q;                // the root and g over it, 0 where it is
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (kFast) {
+          float inv;
+          asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(w.f[i]));
+          inv = w.f[i] < 1e-37f ? 0.f : inv;
+          m.f[i] = w.f[i] * inv;
+          q.f[i] = g.f[i] * inv;
+        } else {
+          m.f[i] = sqrtf(w.f[i]);
+          q.f[i] = m.f[i] == 0.f ? 0.f : g.f[i] / m.f[i];
+        }
+      }
+      Ch<V> u = P::open(mine[j * kThreads]), ml = mul(m, l), si;
+      if (kGate) {
+        si = one_over<kFast>(ei[j]);
+        u = mul(u, si);
+      }
+      // p = e (g h_{t-1} - a (g / m) u)
+      const Ch<V> p = mul(e, fma(g, hp[j], neg(mul(mul(a[j], q), u))));
+      if (in && t0 + j < total && KDA_CHECK(c + V <= ch)) {
+        const int64_t at = (t0 + j) * ch + c;
+        const Ch<V> zero = all<V>(0.f);
+        store<T, V>(dx + at, !valid ? zero : kGate ? mul(ml, si) : ml);
+        store<T, V>(dr + at, valid ? mul(p, mul(er[j], sr)) : zero);
+        if (kGate) store<T, V>(di + at, valid ? mul(mul(ml, u), mul(ei[j], si)) : zero);
+      }
+      if (valid) sum = add(sum, p);
+      if (((rows.first >> j) & 1) && dstate) {
+        const int n = __shfl_sync(0xffffffffu, rows.seq, j);
+        if (in) store<float, V>(dstate + (int64_t)n * ch + c, e);
+      }
+    }
+    s_sum[warp][lane] = sum;
+    __syncthreads();   // everyone has read s, too, before the next tile writes it
+    if (warp == 0 && in) {
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) sum = add(sum, s_sum[w][lane]);
+      store<float, V>(part + k * ch + c, sum);
+    }
+    Raw* t = mine;
+    mine = other;
+    other = t;
+    item = next;
   }
   KDA_DEBUG_FOLD(&hdr->status);
 }
@@ -664,8 +766,9 @@ gated_token_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict
     const typename P::Raw xr = load<T, V>(x + t * x_pitch + c), rr = load<T, V>(r + t * r_pitch + c);
     Ch<V> u = P::open(xr);
     if (kGate) u = mul(u, sigmoid<kFast>(P::open(load<T, V>(ig + t * i_pitch + c))));
-    const Ch<V> g = mul(rate, sigmoid<kFast>(P::open(rr))), a = decay<kFast>(g);
-    h = fma(a, h, mul(root<kFast>(loss(g, a)), u));
+    Ch<V> w;
+    const Ch<V> a = decay<kFast>(mul(rate, sigmoid<kFast>(P::open(rr))), w);
+    h = fma(a, h, mul(root<kFast>(w), u));
     if (KDA_CHECK(t >= 0 && t < total && c + V <= ch)) store<T, V>(y + t * ch + c, h);
     if (cache) store<float, V>(cache + n * cache_pitch + (t - bos) * ch + c, h);
   }
@@ -684,27 +787,36 @@ bool pairs(const void* p, int64_t pitch, int size) {
 Plan plan_of(const Layout& l, uint8_t* ws) {
   Plan p;
   p.seq = reinterpret_cast<int32_t*>(ws + l.seq);
-  p.flag = reinterpret_cast<uint32_t*>(ws + l.flag);
-  p.gflag = reinterpret_cast<uint32_t*>(ws + l.gflag);
-  p.agg_a = reinterpret_cast<float*>(ws + l.agg_a);
-  p.agg_h = reinterpret_cast<float*>(ws + l.agg_h);
+  p.agg = reinterpret_cast<float*>(ws + l.agg);
   p.group = reinterpret_cast<float*>(ws + l.group);
   p.tiles = l.tiles;
   p.blocks = l.blocks;
+  p.items = (uint32_t)(l.tiles * l.blocks);
   return p;
 }
 
 cudaError_t launch_plan(const GatedArgs& a, const Layout& l, const float* from, float* to, bool zero_bad,
                         cudaStream_t st) {
-  const int64_t most = 4ll * gpu_sms();
+  const int64_t most = 2ll * gpu_sms(), unset = (int64_t)((l.seq - l.agg) / 16);
   int64_t blocks = (a.d.total_tokens + kPlanRows - 1) / kPlanRows;
-  if (to) blocks = blocks > (a.d.num_seqs + 31) / 32 ? blocks : (a.d.num_seqs + 31) / 32;
+  auto least = [&](int64_t n) { blocks = blocks > n ? blocks : n; };
+  least((unset + 4095) / 4096);
+  if (to) least((a.d.num_seqs + 31) / 32);
   blocks = blocks < 1 ? 1 : blocks > most ? most : blocks;
   gated_plan_kernel<<<(unsigned)blocks, 1024, 0, st>>>(
       a.cu, a.idx, a.d.num_seqs, a.d.total_tokens, a.d.num_slots, reinterpret_cast<WsHeader*>(a.ws),
-      reinterpret_cast<int32_t*>(a.ws + l.seq), reinterpret_cast<uint32_t*>(a.ws + l.flag),
-      (int64_t)((l.seq - l.flag) / 4), from, to, a.d.channels, zero_bad);
+      reinterpret_cast<int32_t*>(a.ws + l.seq), reinterpret_cast<uint4*>(a.ws + l.agg), unset, from, to,
+      a.d.channels, zero_bad);
   return cudaGetLastError();
+}
+
+// CTAs that stay: two an SM, or one a tile.
+template <typename K>
+cudaError_t stay(K* kernel, const Plan& p, int bytes, unsigned* grid) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const unsigned most = 2u * (unsigned)gpu_sms();
+  *grid = p.items < most ? p.items : most;
+  return e;
 }
 
 template <typename T, int V, bool kGate>
@@ -713,9 +825,14 @@ cudaError_t run_scan(const GatedArgs& a, cudaStream_t st) {
   const bool dense = !a.idx && a.state_out && a.state_out != a.state_in;
   cudaError_t e = launch_plan(a, l, a.state_in, dense ? a.state_out : nullptr, false, st);
   if (e != cudaSuccess || l.tiles == 0) return e;
-  gated_scan_kernel<T, V, kGate, kRows><<<(unsigned)(l.tiles * l.blocks), kThreads, 0, st>>>(
+  const Plan p = plan_of(l, a.ws);
+  auto* kernel = gated_scan_kernel<T, V, kGate, kRows>;
+  const int bytes = (kGate ? 3 : 2) * kRows * kThreads * (int)sizeof(T) * V;
+  unsigned grid;
+  if ((e = stay(kernel, p, bytes, &grid)) != cudaSuccess) return e;
+  kernel<<<grid, kThreads, bytes, st>>>(
       (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i, a.d.i_pitch, a.a_log, a.state_in,
-      a.idx, a.d.num_slots, a.slot_stride, a.state_out, (T*)a.y, a.carries, plan_of(l, a.ws),
+      a.idx, a.d.num_slots, a.slot_stride, a.state_out, (T*)a.y, a.carries, p,
       reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, pipeline_wait_limit_ns());
   return cudaGetLastError();
 }
@@ -727,11 +844,15 @@ cudaError_t run_back(const GatedArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   float* part = reinterpret_cast<float*>(a.ws + l.part);
   if (l.tiles > 0) {
-    gated_back_kernel<T, V, kGate, kBackRows><<<(unsigned)(l.tiles * l.blocks), kThreads, 0, st>>>(
+    const Plan p = plan_of(l, a.ws);
+    auto* kernel = gated_back_kernel<T, V, kGate, kBackRows>;
+    const int bytes = 2 * (kGate ? 4 : 3) * kBackRows * kThreads * (int)sizeof(T) * V;
+    unsigned grid;
+    if ((e = stay(kernel, p, bytes, &grid)) != cudaSuccess) return e;
+    kernel<<<grid, kThreads, bytes, st>>>(
         (const T*)a.dy, a.dy_pitch, (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i,
-        a.d.i_pitch, a.a_log, a.carries, a.state_in, a.dfinal, (T*)a.dx, (T*)a.dr, (T*)a.di, a.dstate, part,
-        plan_of(l, a.ws), reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels,
-        pipeline_wait_limit_ns());
+        a.d.i_pitch, a.a_log, a.carries, a.state_in, a.dfinal, (T*)a.dx, (T*)a.dr, (T*)a.di, a.dstate, part, p,
+        reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, pipeline_wait_limit_ns());
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   gated_sum_kernel<<<(unsigned)((a.d.channels + 31) / 32), 256, 0, st>>>(part, l.tiles, a.d.channels, a.da_log);
@@ -752,25 +873,31 @@ enum class Pass { kScan, kBack, kToken };
 
 template <typename T, int V>
 cudaError_t by_gate(const GatedArgs& a, cudaStream_t st, Pass pass) {
-  switch (pass) {
-    case Pass::kScan: return a.i ? run_scan<T, V, true>(a, st) : run_scan<T, V, false>(a, st);
-    case Pass::kBack: return a.i ? run_back<T, V, true>(a, st) : run_back<T, V, false>(a, st);
-    default: return a.i ? run_token<T, V, true>(a, st) : run_token<T, V, false>(a, st);
-  }
+  if (pass == Pass::kScan) return a.i ? run_scan<T, V, true>(a, st) : run_scan<T, V, false>(a, st);
+  return a.i ? run_back<T, V, true>(a, st) : run_back<T, V, false>(a, st);
+}
+template <typename T, int V>
+cudaError_t token_by_gate(const GatedArgs& a, cudaStream_t st) {
+  return a.i ? run_token<T, V, true>(a, st) : run_token<T, V, false>(a, st);
 }
 
-// Two channels a lane where every row starts on a boundary of two elements, else one.
+// Four bytes of a row a lane: two channels in bf16 where every row starts on a boundary of two elements, else
+// one. (Tokens take two in fp32 as well.)
 template <typename T>
 cudaError_t by_type(const GatedArgs& a, cudaStream_t st, Pass pass) {
   const int e = sizeof(T);
   const int64_t ch = a.d.channels;
-  const bool wide = ch % 2 == 0 && pairs(a.x, a.d.x_pitch, e) && pairs(a.r, a.d.r_pitch, e) &&
-                    pairs(a.i, a.d.i_pitch, e) && pairs(a.dy, a.dy_pitch, e) && pairs(a.y, ch, e) &&
-                    pairs(a.dx, ch, e) && pairs(a.dr, ch, e) && pairs(a.di, ch, e) &&
+  const bool wide = (e == 2 || pass == Pass::kToken) && ch % 2 == 0 && pairs(a.x, a.d.x_pitch, e) &&
+                    pairs(a.r, a.d.r_pitch, e) && pairs(a.i, a.d.i_pitch, e) && pairs(a.dy, a.dy_pitch, e) &&
+                    pairs(a.y, ch, e) && pairs(a.dx, ch, e) && pairs(a.dr, ch, e) && pairs(a.di, ch, e) &&
                     pairs(a.state_in, a.slot_stride, 4) && pairs(a.state_out, a.slot_stride, 4) &&
                     pairs(a.cache, a.cache_pitch, 4) && pairs(a.carries, ch, 4) && pairs(a.dfinal, ch, 4) &&
                     pairs(a.dstate, ch, 4);
-  return wide ? by_gate<T, 2>(a, st, pass) : by_gate<T, 1>(a, st, pass);
+  if (pass == Pass::kToken) return wide ? token_by_gate<T, 2>(a, st) : token_by_gate<T, 1>(a, st);
+  if constexpr (sizeof(T) == 2) {
+    if (wide) return by_gate<T, 2>(a, st, pass);
+  }
+  return by_gate<T, 1>(a, st, pass);
 }
 
 cudaError_t launch(const GatedArgs& a, cudaStream_t st, Pass pass) {
