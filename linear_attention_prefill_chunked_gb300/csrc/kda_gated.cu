@@ -142,7 +142,7 @@ template <bool kFast, bool kClamp, int V> __device__ __forceinline__ Ch<V> exp_n
   for (int i = 0; i < V; ++i) {
     if constexpr (kFast) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.f[i]));
     else e.f[i] = expf(-v.f[i]);
-    if constexpr (kClamp) e.f[i] = e.f[i] > 1e37f ? 1e37f : e.f[i];  // NaN stays
+    if constexpr (kClamp) asm("min.NaN.f32 %0, %0, 0f7cf0bdc2;" : "+f"(e.f[i]));  // 1e37; NaN stays
   }
   return e;
 }
@@ -167,10 +167,11 @@ template <int V> __device__ __forceinline__ Ch<V> rates(const float* a_log, int 
   return r;
 }
 
-// a = e^g and 1 - a^2 of a log-decay g <= 0. Above -0.175 by the series of e = e^g - 1 (its next term is 2^-27
+// a = e^g and a^2 - 1 of a log-decay g <= 0. Above -0.175 by the series of e = e^g - 1 (its next term is 2^-27
 // of it there): a = 1 + e is rounded once, which long memories need (a decay off by 2^-22, as the fast
-// exponential's, is a state off by that times the tokens it remembers), and 1 - a^2 = -e (2 + e) keeps its
+// exponential's, is a state off by that times the tokens it remembers), and a^2 - 1 = e (2 + e) keeps its
 // digits. Below it the difference, which has lost at most two bits. (The backward pass has a already.)
+constexpr float kSeries = -0.175f;
 template <int V> __device__ __forceinline__ Ch<V> series(const Ch<V>& g) {
   Ch<V> p = fma(g, all<V>(1.f / 720.f), all<V>(1.f / 120.f));
   p = fma(p, g, all<V>(1.f / 24.f));
@@ -179,10 +180,9 @@ template <int V> __device__ __forceinline__ Ch<V> series(const Ch<V>& g) {
   p = fma(p, g, all<V>(1.f));
   return mul(p, g);
 }
-constexpr float kSeries = -0.175f;
-template <int V> __device__ __forceinline__ Ch<V> loss(const Ch<V>& g, const Ch<V>& e, const Ch<V>& a) {
-  const Ch<V> near = mul(e, add(neg(e), all<V>(-2.f)));
-  Ch<V> w = fma(neg(a), a, all<V>(1.f));
+template <int V> __device__ __forceinline__ Ch<V> lost(const Ch<V>& g, const Ch<V>& e, const Ch<V>& a) {
+  const Ch<V> near = mul(e, add(e, all<V>(2.f)));
+  Ch<V> w = fma(a, a, all<V>(-1.f));
 #pragma unroll
   for (int i = 0; i < V; ++i) w.f[i] = g.f[i] > kSeries ? near.f[i] : w.f[i];
   return w;
@@ -198,24 +198,39 @@ template <bool kFast, int V> __device__ __forceinline__ Ch<V> decay(const Ch<V>&
     for (int i = 0; i < V; ++i) a.f[i] = expf(g.f[i]);
   }
   const Ch<V> e = series(g), near = add(e, all<V>(1.f));
-  w = loss(g, e, a);
+  w = lost(g, e, a);
 #pragma unroll
   for (int i = 0; i < V; ++i) a.f[i] = g.f[i] > kSeries ? near.f[i] : a.f[i];
   return a;
 }
 
-template <bool kFast> __device__ __forceinline__ float root(float w) {
-  if constexpr (kFast) {
-    asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(w));
-    return w;
-  } else {
-    return sqrtf(w);
-  }
-}
+// sqrt(-w)
 template <bool kFast, int V> __device__ __forceinline__ Ch<V> root(Ch<V> w) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) w.f[i] = root<kFast>(w.f[i]);
+  for (int i = 0; i < V; ++i) {
+    w.f[i] = -w.f[i];
+    if constexpr (kFast) asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(w.f[i]));
+    else w.f[i] = sqrtf(w.f[i]);
+  }
   return w;
+}
+// -g over sqrt(-w) and sqrt(-w); both 0 where that is.
+template <bool kFast, int V>
+__device__ __forceinline__ void over_root(const Ch<V>& g, const Ch<V>& w, Ch<V>& q, Ch<V>& m) {
+  if constexpr (kFast) {
+    Ch<V> k;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(k.f[i]) : "f"(-w.f[i]));
+      k.f[i] = w.f[i] > -1e-37f ? 0.f : -k.f[i];
+    }
+    m = mul(w, k);
+    q = mul(g, k);
+  } else {
+    m = root<false>(w);
+#pragma unroll
+    for (int i = 0; i < V; ++i) q.f[i] = m.f[i] == 0.f ? 0.f : -g.f[i] / m.f[i];
+  }
 }
 
 // ---- planning -------------------------------------------------------------------------------
@@ -433,19 +448,52 @@ __device__ __forceinline__ Rows rows_of(const RowsRaw& r) {
   return o;
 }
 
-// A row's elements on their way into this thread's place of shared memory (zeros where there is none).
-template <typename T, int V>
-__device__ __forceinline__ void fetch(typename Pack<T, V>::Raw* to, const T* from, bool ok) {
+// A warp's S rows of one input on their way into its part of shared memory, [row][lane], zeros where there is
+// nothing: 16 bytes a copy where the rows allow (`wide`), else a lane's own elements.
+template <typename T, int V, int S>
+__device__ __forceinline__ void fetch(typename Pack<T, V>::Raw* to, const T* p, int64_t pitch, int64_t t0, int64_t total,
+                                      int c0, int ch, int lane, bool wide) {
   constexpr int kBytes = sizeof(T) * V;
-  if constexpr (kBytes >= 4) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(tc::smem_u32(to)), "l"(from), "n"(kBytes),
-                 "r"(ok ? kBytes : 0)
-                 : "memory");
-  } else {
-    *to = ok ? load<T, V>(from) : Pack<T, V>::close(all<V>(0.f));
+  if constexpr (kBytes == 4) {
+    if (wide) {
+      constexpr int kElems = 16 / sizeof(T);
+      const int c = c0 + (lane & 7) * kElems;
+      const int64_t t = t0 + (lane >> 3);
+      const uint32_t dst = tc::smem_u32(to) + lane * 16;
+      const T* src = p + t * pitch + c;
+#pragma unroll
+      for (int j = 0; j < S; j += 4) {
+        const bool ok = c < ch && t + j < total;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + j * 128), "l"(ok ? src : p),
+                     "r"(ok ? 16 : 0)
+                     : "memory");
+        src += 4 * pitch;
+      }
+      return;
+    }
+  }
+  const int c = c0 + lane * V;
+  const T* src = p + t0 * pitch + c;
+#pragma unroll
+  for (int j = 0; j < S; ++j) {
+    const bool ok = c < ch && t0 + j < total;
+    if constexpr (kBytes >= 4) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(tc::smem_u32(to + j * 32 + lane)),
+                   "l"(ok ? src : p), "n"(kBytes), "r"(ok ? kBytes : 0)
+                   : "memory");
+    } else {
+      to[j * 32 + lane] = ok ? load<T, V>(src) : Pack<T, V>::close(all<V>(0.f));
+    }
+    src += pitch;
   }
 }
-__device__ __forceinline__ void fetch_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void fetch_done() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+}
+// A body for runs of rows inside one sequence of channels that are all there, and one for the others.
+struct Plain { static constexpr bool value = true; };
+struct Mixed { static constexpr bool value = false; };
 
 // ---- forward --------------------------------------------------------------------------------
 template <typename T, int V, bool kGate, int S>
@@ -454,14 +502,16 @@ gated_scan_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
                   const T* __restrict__ ig, int64_t i_pitch, const float* __restrict__ a_log,
                   const float* state, const int32_t* __restrict__ idx, int64_t num_slots, int64_t stride,
                   float* final_state, T* __restrict__ y, float* __restrict__ carries, Plan plan, WsHeader* hdr,
-                  int64_t total, int ch, uint64_t limit_ns) {
+                  int64_t total, int ch, bool wide, uint64_t limit_ns) {
   constexpr bool kFast = sizeof(T) == 2;
+  constexpr int kInputs = kGate ? 3 : 2;
   using P = Pack<T, V>;
   using Raw = typename P::Raw;
   extern __shared__ __align__(16) uint8_t s_raw[];
-  Raw* const mine = reinterpret_cast<Raw*>(s_raw) + threadIdx.x;   // [input][row], kThreads apart
   __shared__ Shared<V> s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Raw* const own = reinterpret_cast<Raw*>(s_raw) + warp * (kInputs * S * 32);   // [input][row][lane]
+  const Raw* const mine = own + lane;
 
   if (tid == 0) s.next = atomicAdd(&hdr->next_item, 1u);
   __syncthreads();
@@ -470,54 +520,61 @@ gated_scan_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
   float rate_raw[V];
   auto prefetch = [&](uint32_t it) {
     const int64_t k = it / plan.blocks, t0 = (k * kWarps + warp) * S;
-    const int c = ((int)(it % plan.blocks) * 32 + lane) * V;
-    const bool in = c < ch;
-    const T *xp = x + (in ? t0 * x_pitch + c : 0), *rp = r + (in ? t0 * r_pitch + c : 0);
-    const T* ip = kGate ? ig + (in ? t0 * i_pitch + c : 0) : nullptr;
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-      const bool ok = in && t0 + j < total;
-      fetch<T, V>(mine + j * kThreads, ok ? xp + j * x_pitch : x, ok);
-      fetch<T, V>(mine + (S + j) * kThreads, ok ? rp + j * r_pitch : r, ok);
-      if (kGate) fetch<T, V>(mine + (2 * S + j) * kThreads, ok ? ip + j * i_pitch : ig, ok);
-    }
+    const int c0 = (int)(it % plan.blocks) * 32 * V;
+    fetch<T, V, S>(own, x, x_pitch, t0, total, c0, ch, lane, wide);
+    fetch<T, V, S>(own + S * 32, r, r_pitch, t0, total, c0, ch, lane, wide);
+    if (kGate) fetch<T, V, S>(own + 2 * S * 32, ig, i_pitch, t0, total, c0, ch, lane, wide);
     rows_raw = rows_load<S>(plan.seq, t0, total, lane);
+    const int c = c0 + lane * V;
 #pragma unroll
     for (int i = 0; i < V; ++i) rate_raw[i] = c + i < ch ? a_log[c + i] : 0.f;
   };
   if (item < plan.items) prefetch(item);
   while (item < plan.items) {
     const int64_t k = item / plan.blocks, t0 = (k * kWarps + warp) * S;
-    const int c = ((int)(item % plan.blocks) * 32 + lane) * V;
+    const int c0 = (int)(item % plan.blocks) * 32 * V, c = c0 + lane * V;
     const bool in = c < ch;
     if (tid == 0) s.next = atomicAdd(&hdr->next_item, 1u);
     Ch<V> rate;
 #pragma unroll
     for (int i = 0; i < V; ++i) rate.f[i] = ssm_rate(rate_raw[i]);
     const Rows rows = rows_of(rows_raw);
+    const bool plain = rows.valid == (1u << S) - 1 && (rows.first | rows.last) == 0 && c0 + 32 * V <= ch;
     fetch_done();
 
     Ch<V> a[S], b[S];
-    Ch<V> A = all<V>(1.f), H = all<V>(0.f);
 #pragma unroll
     for (int j = 0; j < S; ++j) {
       Ch<V> w;
-      a[j] = decay<kFast>(mul(rate, sigmoid<kFast>(P::open(mine[(S + j) * kThreads]))), w);
-      b[j] = mul(root<kFast>(w), P::open(mine[j * kThreads]));
-      if (kGate) b[j] = mul(b[j], sigmoid<kFast>(P::open(mine[(2 * S + j) * kThreads])));
-      if ((rows.first >> j) & 1) {  // the sequence's own state instead of what came before
-        const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-        const int64_t slot = idx ? resolve_slot(idx, n, num_slots) : n;
-        Ch<V> h0 = all<V>(0.f);
-        if (state && in && KDA_CHECK(slot >= 0)) h0 = Pack<float, V>::open(load<float, V>(state + slot * stride + c));
-        b[j] = fma(a[j], h0, b[j]);
-        H = b[j];
-      } else {
-        H = fma(a[j], H, b[j]);
-      }
-      A = mul(A, a[j]);
+      a[j] = decay<kFast>(mul(rate, sigmoid<kFast>(P::open(mine[(S + j) * 32]))), w);
+      b[j] = mul(root<kFast>(w), P::open(mine[j * 32]));
+      if (kGate) b[j] = mul(b[j], sigmoid<kFast>(P::open(mine[(2 * S + j) * 32])));
     }
-    s.a[warp][lane] = rows.first ? all<V>(-1.f) : A;
+    Ch<V> A = a[0], H = b[0];
+    if (plain) {
+#pragma unroll
+      for (int j = 1; j < S; ++j) {
+        H = fma(a[j], H, b[j]);
+        A = mul(A, a[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        if ((rows.first >> j) & 1) {  // the sequence's own state instead of what came before
+          const int n = __shfl_sync(0xffffffffu, rows.seq, j);
+          const int64_t slot = idx ? resolve_slot(idx, n, num_slots) : n;
+          Ch<V> h0 = all<V>(0.f);
+          if (state && in && KDA_CHECK(slot >= 0)) h0 = Pack<float, V>::open(load<float, V>(state + slot * stride + c));
+          b[j] = fma(a[j], h0, b[j]);
+          H = b[j];
+        } else if (j > 0) {
+          H = fma(a[j], H, b[j]);
+        }
+        if (j > 0) A = mul(A, a[j]);
+      }
+      if (rows.first) A = all<V>(-1.f);
+    }
+    s.a[warp][lane] = A;
     s.h[warp][lane] = H;
     __syncthreads();
     const uint32_t next = s.next;
@@ -525,16 +582,26 @@ gated_scan_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
     Ch<V> h = enter(s, plan, k, c, ch, warp, lane, warp, hdr, limit_ns);
     if (carries && t0 % KDA_GATED_CARRY_ROWS == 0 && t0 < total && in)
       store<float, V>(carries + t0 / KDA_GATED_CARRY_ROWS * ch + c, h);
+    T* yp = y + t0 * ch + c;
+    if (plain) {
 #pragma unroll
-    for (int j = 0; j < S; ++j) {
-      if ((rows.first >> j) & 1) h = b[j];
-      else h = fma(a[j], h, b[j]);
-      if (((rows.valid >> j) & 1) && in && KDA_CHECK(t0 + j < total && c + V <= ch))
-        store<T, V>(y + (t0 + j) * ch + c, h);
-      if (((rows.last >> j) & 1) && final_state) {
-        const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-        const int64_t slot = idx ? resolve_slot(idx, n, num_slots) : n;
-        if (in && KDA_CHECK(slot >= 0)) store<float, V>(final_state + slot * stride + c, h);
+      for (int j = 0; j < S; ++j) {
+        h = fma(a[j], h, b[j]);
+        if (KDA_CHECK(t0 + j < total)) store<T, V>(yp, h);
+        yp += ch;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        if ((rows.first >> j) & 1) h = b[j];
+        else h = fma(a[j], h, b[j]);
+        if (((rows.valid >> j) & 1) && in && KDA_CHECK(t0 + j < total && c + V <= ch)) store<T, V>(yp, h);
+        yp += ch;
+        if (((rows.last >> j) & 1) && final_state) {
+          const int n = __shfl_sync(0xffffffffu, rows.seq, j);
+          const int64_t slot = idx ? resolve_slot(idx, n, num_slots) : n;
+          if (in && KDA_CHECK(slot >= 0)) store<float, V>(final_state + slot * stride + c, h);
+        }
       }
     }
     __syncthreads();   // everyone has read s before the next tile writes it
@@ -551,19 +618,19 @@ gated_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restric
                   const float* __restrict__ a_log, const float* __restrict__ carries,
                   const float* __restrict__ state, const float* __restrict__ dfinal, T* __restrict__ dx,
                   T* __restrict__ dr, T* __restrict__ di, float* __restrict__ dstate, float* __restrict__ part,
-                  Plan plan, WsHeader* hdr, int64_t total, int ch, uint64_t limit_ns) {
+                  Plan plan, WsHeader* hdr, int64_t total, int ch, bool wide, uint64_t limit_ns) {
   constexpr bool kFast = sizeof(T) == 2;
   constexpr int kInputs = kGate ? 4 : 3;
   static_assert(S * kWarps == KDA_GATED_CARRY_ROWS, "a tile starts where a carry was left");
   using P = Pack<T, V>;
   using Raw = typename P::Raw;
   extern __shared__ __align__(16) uint8_t s_raw[];
-  Raw* mine = reinterpret_cast<Raw*>(s_raw) + threadIdx.x;   // [stage][input][row], kThreads apart
-  Raw* other = mine + kInputs * S * kThreads;
   __shared__ Shared<V> s;
   __shared__ Ch<V> s_fa[kWarps][32], s_fh[kWarps][32];       // the state's own (A, H)
   __shared__ Ch<V> s_sum[kWarps][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Raw* own = reinterpret_cast<Raw*>(s_raw) + warp * (kInputs * S * 32);   // [stage][warp][input][row][lane]
+  Raw* other = own + kWarps * kInputs * S * 32;
 
   if (tid == 0) s.next = atomicAdd(&hdr->next_item, 1u);
   __syncthreads();
@@ -573,39 +640,35 @@ gated_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restric
   Ch<V> carry;
   auto prefetch = [&](uint32_t it, Raw* to) {
     const int64_t k = plan.tiles - 1 - it / plan.blocks, t0 = (k * kWarps + warp) * S;
-    const int c = ((int)(it % plan.blocks) * 32 + lane) * V;
-    const bool in = c < ch;
-    const T *xp = x + (in ? t0 * x_pitch + c : 0), *rp = r + (in ? t0 * r_pitch + c : 0);
-    const T *gp = dy + (in ? t0 * dy_pitch + c : 0), *ip = kGate ? ig + (in ? t0 * i_pitch + c : 0) : nullptr;
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-      const bool ok = in && t0 + j < total;
-      fetch<T, V>(to + j * kThreads, ok ? xp + j * x_pitch : x, ok);
-      fetch<T, V>(to + (S + j) * kThreads, ok ? rp + j * r_pitch : r, ok);
-      fetch<T, V>(to + (2 * S + j) * kThreads, ok ? gp + j * dy_pitch : dy, ok);
-      if (kGate) fetch<T, V>(to + (3 * S + j) * kThreads, ok ? ip + j * i_pitch : ig, ok);
-    }
+    const int c0 = (int)(it % plan.blocks) * 32 * V;
+    fetch<T, V, S>(to, x, x_pitch, t0, total, c0, ch, lane, wide);
+    fetch<T, V, S>(to + S * 32, r, r_pitch, t0, total, c0, ch, lane, wide);
+    fetch<T, V, S>(to + 2 * S * 32, dy, dy_pitch, t0, total, c0, ch, lane, wide);
+    if (kGate) fetch<T, V, S>(to + 3 * S * 32, ig, i_pitch, t0, total, c0, ch, lane, wide);
     rows_raw = rows_load<S>(plan.seq, t0, total, lane);
-    carry = in ? Pack<float, V>::open(load<float, V>(carries + k * ch + c)) : all<V>(0.f);
+    const int c = c0 + lane * V;
+    carry = c < ch ? Pack<float, V>::open(load<float, V>(carries + k * ch + c)) : all<V>(0.f);
 #pragma unroll
     for (int i = 0; i < V; ++i) rate_raw[i] = c + i < ch ? a_log[c + i] : 0.f;
   };
-  if (item < plan.items) prefetch(item, mine);
+  if (item < plan.items) prefetch(item, own);
   while (item < plan.items) {
     const int64_t pos = item / plan.blocks, k = plan.tiles - 1 - pos;   // tiles from the last one on
     const int64_t t0 = (k * kWarps + warp) * S;
-    const int c = ((int)(item % plan.blocks) * 32 + lane) * V;
+    const int c0 = (int)(item % plan.blocks) * 32 * V, c = c0 + lane * V;
     const bool in = c < ch;
+    const Raw* const mine = own + lane;
     if (tid == 0) s.next = atomicAdd(&hdr->next_item, 1u);
     Ch<V> rate;
 #pragma unroll
     for (int i = 0; i < V; ++i) rate.f[i] = ssm_rate(rate_raw[i]);
     const Rows rows = rows_of(rows_raw);
+    const bool plain = rows.valid == (1u << S) - 1 && (rows.first | rows.last) == 0 && c0 + 32 * V <= ch;
     Ch<V> h = carry;
     fetch_done();
     // dy, and dfinal where the row is a sequence's last
     auto slope = [&](int j) {
-      Ch<V> l = P::open(mine[(2 * S + j) * kThreads]);
+      Ch<V> l = P::open(mine[(2 * S + j) * 32]);
       if (((rows.last >> j) & 1) && dfinal) {
         const int n = __shfl_sync(0xffffffffu, rows.seq, j);
         if (in) l = add(l, Pack<float, V>::open(load<float, V>(dfinal + (int64_t)n * ch + c)));
@@ -613,39 +676,53 @@ gated_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restric
       return l;
     };
 
-    // the rows' decays and the state's (A, H), then what they do to e, from the last row to the first
+    // the rows' decays and what they add to the state
     Ch<V> a[S], er[S], ei[S], hp[S];
-    Ch<V> A = all<V>(1.f), H = all<V>(0.f);
 #pragma unroll
     for (int j = 0; j < S; ++j) {
       Ch<V> w;
-      er[j] = exp_neg<kFast, true>(P::open(mine[(S + j) * kThreads]));
+      er[j] = exp_neg<kFast, true>(P::open(mine[(S + j) * 32]));
       a[j] = decay<kFast>(mul(rate, one_over<kFast>(er[j])), w);
-      Ch<V> b = mul(root<kFast>(w), P::open(mine[j * kThreads]));
+      hp[j] = mul(root<kFast>(w), P::open(mine[j * 32]));
       if (kGate) {
-        ei[j] = exp_neg<kFast, true>(P::open(mine[(3 * S + j) * kThreads]));
-        b = mul(b, one_over<kFast>(ei[j]));
+        ei[j] = exp_neg<kFast, true>(P::open(mine[(3 * S + j) * 32]));
+        hp[j] = mul(hp[j], one_over<kFast>(ei[j]));
       }
-      if ((rows.first >> j) & 1) {
-        const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-        Ch<V> h0 = all<V>(0.f);
-        if (state && in) h0 = Pack<float, V>::open(load<float, V>(state + (int64_t)n * ch + c));
-        hp[j] = h0;
-        H = fma(a[j], h0, b);
-      } else {
-        hp[j] = H;               // within the warp; what reaches it is added below
+    }
+    // the state's (A, H), and what the rows do to e, from the last one to the first; hp becomes the state
+    // before each row, without what reaches the warp
+    Ch<V> A = a[0], H = all<V>(0.f), E = all<V>(0.f);
+    if (plain) {
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        const Ch<V> b = hp[j];
+        hp[j] = H;
+        H = j > 0 ? fma(a[j], H, b) : b;
+        if (j > 0) A = mul(A, a[j]);
+      }
+#pragma unroll
+      for (int j = S - 1; j >= 0; --j) E = mul(a[j], add(P::open(mine[(2 * S + j) * 32]), E));
+    } else {
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        const Ch<V> b = hp[j];
+        if ((rows.first >> j) & 1) {
+          const int n = __shfl_sync(0xffffffffu, rows.seq, j);
+          H = all<V>(0.f);
+          if (state && in) H = Pack<float, V>::open(load<float, V>(state + (int64_t)n * ch + c));
+        }
+        hp[j] = H;
         H = fma(a[j], H, b);
+        if (j > 0) A = mul(A, a[j]);
       }
-      A = mul(A, a[j]);
+#pragma unroll
+      for (int j = S - 1; j >= 0; --j) {
+        const Ch<V> l = slope(j);
+        E = mul(a[j], (rows.last >> j) & 1 ? l : add(l, E));
+      }
     }
     s_fa[warp][lane] = rows.first ? all<V>(-1.f) : A;
     s_fh[warp][lane] = H;
-    Ch<V> E = all<V>(0.f);
-#pragma unroll
-    for (int j = S - 1; j >= 0; --j) {
-      const Ch<V> l = slope(j);
-      E = mul(a[j], (rows.last >> j) & 1 ? l : add(l, E));
-    }
     const int rank = kWarps - 1 - warp;
     s.a[rank][lane] = rows.last ? all<V>(-1.f) : A;
     s.h[rank][lane] = E;
@@ -654,58 +731,54 @@ gated_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restric
     if (next < plan.items) prefetch(next, other);
     Ch<V> e = enter(s, plan, pos, c, ch, warp, lane, rank, hdr, limit_ns);
     for (int w = 0; w < warp; ++w) fold(h, s_fa[w][lane], s_fh[w][lane]);
-    {
-      Ch<V> q = h;               // decayed from row to row until a sequence begins
 #pragma unroll
-      for (int j = 0; j < S; ++j) {
-        if ((rows.first >> j) & 1) break;
-        hp[j] = add(hp[j], q);
-        q = mul(q, a[j]);
-      }
+    for (int j = 0; j < S; ++j) {  // decayed from row to row until a sequence begins
+      if (!plain && ((rows.first >> j) & 1)) break;
+      hp[j] = add(hp[j], h);
+      h = mul(h, a[j]);
     }
     Ch<V> sum = all<V>(0.f);
+    auto rest = [&](auto kind) {
+      constexpr bool kPlain = decltype(kind)::value;
+      const int64_t at0 = t0 * ch + c;
 #pragma unroll
-    for (int j = S - 1; j >= 0; --j) {
-      const bool valid = (rows.valid >> j) & 1;
-      Ch<V> l = slope(j);
-      if (!((rows.last >> j) & 1)) l = add(l, e);
-      e = mul(a[j], l);
-      const Ch<V> sr = one_over<kFast>(er[j]), g = mul(rate, sr);
-      const Ch<V> w = loss(g, series(g), a[j]);
-      Ch<V> m, q;                // the root and g over it, 0 where it is
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if constexpr (kFast) {
-          float inv;
-          asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(w.f[i]));
-          inv = w.f[i] < 1e-37f ? 0.f : inv;
-          m.f[i] = w.f[i] * inv;
-          q.f[i] = g.f[i] * inv;
+      for (int j = S - 1; j >= 0; --j) {
+        Ch<V> l = kPlain ? P::open(mine[(2 * S + j) * 32]) : slope(j);
+        if (kPlain || !((rows.last >> j) & 1)) l = add(l, e);
+        e = mul(a[j], l);
+        const Ch<V> sr = one_over<kFast>(er[j]), g = mul(rate, sr);
+        Ch<V> m, q, u = P::open(mine[j * 32]), si;
+        over_root<kFast>(g, lost(g, series(g), a[j]), q, m);
+        const Ch<V> ml = mul(m, l);
+        if (kGate) {
+          si = one_over<kFast>(ei[j]);
+          u = mul(u, si);
+        }
+        // p = e (g h_{t-1} - a (g / m) u)
+        const Ch<V> p = mul(e, fma(mul(a[j], q), u, mul(g, hp[j])));
+        Ch<V> ox = kGate ? mul(ml, si) : ml, orr = mul(p, mul(er[j], sr)), oi;
+        if (kGate) oi = mul(mul(ml, u), mul(ei[j], si));
+        const int64_t at = at0 + (int64_t)j * ch;
+        if (kPlain) {
+          sum = add(sum, p);
+        } else if ((rows.valid >> j) & 1) {
+          sum = add(sum, p);
+          if (((rows.first >> j) & 1) && dstate) {
+            const int n = __shfl_sync(0xffffffffu, rows.seq, j);
+            if (in) store<float, V>(dstate + (int64_t)n * ch + c, e);
+          }
         } else {
-          m.f[i] = sqrtf(w.f[i]);
-          q.f[i] = m.f[i] == 0.f ? 0.f : g.f[i] / m.f[i];
+          ox = orr = oi = all<V>(0.f);
+        }
+        if ((kPlain || (in && t0 + j < total)) && KDA_CHECK(t0 + j < total && c + V <= ch)) {
+          store<T, V>(dx + at, ox);
+          store<T, V>(dr + at, orr);
+          if (kGate) store<T, V>(di + at, oi);
         }
       }
-      Ch<V> u = P::open(mine[j * kThreads]), ml = mul(m, l), si;
-      if (kGate) {
-        si = one_over<kFast>(ei[j]);
-        u = mul(u, si);
-      }
-      // p = e (g h_{t-1} - a (g / m) u)
-      const Ch<V> p = mul(e, fma(g, hp[j], neg(mul(mul(a[j], q), u))));
-      if (in && t0 + j < total && KDA_CHECK(c + V <= ch)) {
-        const int64_t at = (t0 + j) * ch + c;
-        const Ch<V> zero = all<V>(0.f);
-        store<T, V>(dx + at, !valid ? zero : kGate ? mul(ml, si) : ml);
-        store<T, V>(dr + at, valid ? mul(p, mul(er[j], sr)) : zero);
-        if (kGate) store<T, V>(di + at, valid ? mul(mul(ml, u), mul(ei[j], si)) : zero);
-      }
-      if (valid) sum = add(sum, p);
-      if (((rows.first >> j) & 1) && dstate) {
-        const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-        if (in) store<float, V>(dstate + (int64_t)n * ch + c, e);
-      }
-    }
+    };
+    if (plain) rest(Plain{});
+    else rest(Mixed{});
     s_sum[warp][lane] = sum;
     __syncthreads();   // everyone has read s, too, before the next tile writes it
     if (warp == 0 && in) {
@@ -713,8 +786,8 @@ gated_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restric
       for (int w = 1; w < kWarps; ++w) sum = add(sum, s_sum[w][lane]);
       store<float, V>(part + k * ch + c, sum);
     }
-    Raw* t = mine;
-    mine = other;
+    Raw* t = own;
+    own = other;
     other = t;
     item = next;
   }
@@ -810,6 +883,13 @@ cudaError_t launch_plan(const GatedArgs& a, const Layout& l, const float* from, 
   return cudaGetLastError();
 }
 
+// Whether rows can be fetched 16 bytes at a time.
+template <typename T> bool wide16(const GatedArgs& a, bool back) {
+  auto rows = [](const void* p, int64_t pitch) { return (uintptr_t)p % 16 == 0 && pitch * (int)sizeof(T) % 16 == 0; };
+  return a.d.channels * (int)sizeof(T) % 16 == 0 && rows(a.x, a.d.x_pitch) && rows(a.r, a.d.r_pitch) &&
+         (!a.i || rows(a.i, a.d.i_pitch)) && (!back || rows(a.dy, a.dy_pitch));
+}
+
 // CTAs that stay: two an SM, or one a tile.
 template <typename K>
 cudaError_t stay(K* kernel, const Plan& p, int bytes, unsigned* grid) {
@@ -833,7 +913,7 @@ cudaError_t run_scan(const GatedArgs& a, cudaStream_t st) {
   kernel<<<grid, kThreads, bytes, st>>>(
       (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i, a.d.i_pitch, a.a_log, a.state_in,
       a.idx, a.d.num_slots, a.slot_stride, a.state_out, (T*)a.y, a.carries, p,
-      reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, pipeline_wait_limit_ns());
+      reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, wide16<T>(a, false), pipeline_wait_limit_ns());
   return cudaGetLastError();
 }
 
@@ -852,7 +932,8 @@ cudaError_t run_back(const GatedArgs& a, cudaStream_t st) {
     kernel<<<grid, kThreads, bytes, st>>>(
         (const T*)a.dy, a.dy_pitch, (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i,
         a.d.i_pitch, a.a_log, a.carries, a.state_in, a.dfinal, (T*)a.dx, (T*)a.dr, (T*)a.di, a.dstate, part, p,
-        reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, pipeline_wait_limit_ns());
+        reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, wide16<T>(a, true),
+        pipeline_wait_limit_ns());
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   gated_sum_kernel<<<(unsigned)((a.d.channels + 31) / 32), 256, 0, st>>>(part, l.tiles, a.d.channels, a.da_log);
