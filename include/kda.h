@@ -480,7 +480,7 @@ typedef struct {
  * sequence give no output; where lengths run backwards, so that sequences overlap, a row goes to the last
  * of its sequences and the others' outputs are unspecified.  Results are bit-identical from run to run.
  */
-#define KDA_GATED_CARRY_ROWS 64
+#define KDA_GATED_CARRY_ROWS 48
 kda_status_t kda_gated_scan(const kda_gated_desc_t *desc, const void *x, const void *r,
                             const void *i, const float *a_log, const int32_t *cu_seqlens,
                             float *state, const int32_t *state_indices, float *final_state,

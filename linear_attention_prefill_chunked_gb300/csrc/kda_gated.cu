@@ -32,6 +32,8 @@
 //
 // The backward pass runs over the tiles from the last to the first, e in the place of h. It needs
 // h_{t-1} as well; the forward pass left the state before each kCarryRows rows for it.
+#include <type_traits>
+
 #include "kda_internal.cuh"
 #include "tc_ptx.cuh"
 
@@ -42,6 +44,7 @@ KDA_DEBUG_FLAG_DEFINE();
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+constexpr int kScanCtas = 2, kBackCtas = 2;   // CTAs an SM
 constexpr int kGroup = 16;
 constexpr int kPlanRows = 1024;   // rows a block of the planning kernel
 constexpr float kLog2e = 1.4426950408889634f;
@@ -314,21 +317,21 @@ template <int V> __device__ __forceinline__ bool hear(const float* at, Pair<V>& 
   }
   return set;
 }
-// The whole warp waits for its lanes' pairs, or until another tile has given up, or for limit_ns.
-template <int V>
-__device__ __noinline__ void hear_slow(const float* at, Pair<V>& p, bool in, WsHeader* hdr, uint64_t limit_ns) {
-  const uint64_t t0 = tc::globaltimer_ns();
-  for (;;) {
-    for (int i = 0; i < 64; ++i)
-      if (__all_sync(0xffffffffu, !in || hear(at, p))) return;
-    if (*(volatile uint32_t*)&hdr->num_entries) return;
-    if (__any_sync(0xffffffffu, tc::globaltimer_ns() - t0 > limit_ns)) {
-      raise_status(&hdr->status, KDA_DEVICE_PIPE_TIMEOUT);
-      atomicExch(&hdr->num_entries, 1u);
-      return;
-    }
+// Whether a warp that waits for other tiles should go on: until one of them has given up, or for limit_ns.
+struct Patience {
+  uint64_t t0 = 0;
+  int tries = 0;
+  __device__ __forceinline__ bool more(WsHeader* hdr, uint64_t limit_ns) {
+    if (++tries % 64) return true;
+    if (*(volatile uint32_t*)&hdr->num_entries) return false;
+    const uint64_t now = __shfl_sync(0xffffffffu, tc::globaltimer_ns(), 0);
+    if (t0 == 0) t0 = now;
+    if (now - t0 <= limit_ns) return true;
+    raise_status(&hdr->status, KDA_DEVICE_PIPE_TIMEOUT);
+    atomicExch(&hdr->num_entries, 1u);
+    return false;
   }
-}
+};
 
 // h <- A h + H; a run in which a sequence begins has A = -1 and forgets h.
 template <int V> __device__ __forceinline__ void fold(Ch<V>& h, const Ch<V>& A, const Ch<V>& H) {
@@ -344,82 +347,118 @@ template <int V> __device__ __forceinline__ void join(Ch<V>& A, Ch<V>& H, const 
   for (int i = 0; i < V; ++i) A.f[i] = A.f[i] < 0.f || B.f[i] < 0.f ? -1.f : n.f[i];
 }
 
-// What is shared by the warps of a tile: each warp's (A, H), in the order of the pass, and pairs of tiles
-// before it in its group.
-template <int V> struct Shared {
-  Ch<V> a[kWarps][32], h[kWarps][32];
-  Ch<V> ga[kGroup / 2][32], gh[kGroup / 2][32];
-  Ch<V> start[32];
-  uint32_t next;
+// What the warps of a CTA share. Tiles of a CTA are counted by `n`.
+struct Info {
+  int64_t t0;        // the tile's first row; -1: no tile
+  int64_t pos;       // its number in the order of the pass
+  int c0;            // its first channel
+  int plain;         // its rows, and one on either side, are of one sequence, its channels all there
 };
+template <int V> struct Shared {
+  Ch<V> a[2][kWarps][32], h[2][kWarps][32];   // each warp's run of tile n & 1, in the order of the pass
+  Ch<V> carry[2][kWarps][32];                 // the state that reaches it
+  Info info[4];                               // of tile n & 3
+  uint64_t full;                              // the next tile's rows are there
+};
+enum : uint32_t { kRan = 1, kCarried = 3 };   // named barriers, two each, by n & 1
+constexpr uint32_t kAll = kThreads + 64;   // with the warp that fetches and the one that carries
+__device__ __forceinline__ void bar_arrive(uint32_t id) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kAll) : "memory");
+}
+__device__ __forceinline__ void bar_sync(uint32_t id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kAll) : "memory");
+}
 
-// The state that reaches warp `rank` of tile `pos` (both counted in the order of the pass), of this lane's
-// channels.  Each warp looks after two tiles of the group, the last one after one and the group's start.
-template <int V>
-__device__ __forceinline__ Ch<V> enter(Shared<V>& s, const Plan& p, int64_t pos, int c, int ch, int warp, int lane,
-                                       int rank, WsHeader* hdr, uint64_t limit_ns) {
-  static_assert(kGroup == 2 * kWarps, "two tiles a warp");
-  const int before = (int)(pos % kGroup);
-  const int64_t g = pos / kGroup, first = g * kGroup;
-  const bool in = c < ch;
-  Pair<V> one, two;
-  const int j = 2 * warp;
-  const bool start = warp == kWarps - 1;
-  const bool want1 = j < before, want2 = start ? g > 0 : j + 1 < before;
-  const float* at1 = p.agg + ((first + j) * ch + c) * 2;
-  const float* at2 = start ? p.group + (g * ch + c) * 2 : at1 + 2 * (int64_t)ch;
-  bool got1 = true, got2 = true;
-  if (want1) got1 = !in || hear(at1, one);
-  if (want2) got2 = !in || hear(at2, two);
-  Ch<V> A, H;
-  if (warp == 0 && before < kGroup - 1 && pos + 1 < p.tiles) {  // the whole tile's, for the tiles after it
-    A = s.a[0][lane];
-    H = s.h[0][lane];
+// The next tile by the counter, into info[n & 3] (one warp).
+template <int V, int S, bool kBack>
+__device__ __forceinline__ void take(Shared<V>& s, int n, const Plan& p, WsHeader* hdr, int64_t total, int ch, int lane) {
+  constexpr int kRowsTile = kWarps * S;
+  uint32_t item = 0;
+  if (lane == 0) item = atomicAdd(&hdr->next_item, 1u);
+  item = __shfl_sync(0xffffffffu, item, 0);
+  Info o;
+  o.t0 = -1;
+  o.pos = item / p.blocks;
+  o.c0 = (int)(item % p.blocks) * 32 * V;
+  o.plain = 0;
+  if (item < p.items) {
+    o.t0 = (kBack ? p.tiles - 1 - o.pos : o.pos) * kRowsTile;
+    const int own = p.seq[o.t0];
+    bool same = own >= 0 && o.c0 + 32 * V <= ch && o.t0 > 0 && o.t0 + kRowsTile < total;
+    if (same) {
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) join(A, H, s.a[w][lane], s.h[w][lane]);
+      for (int j = 0; j < kRowsTile + 2; j += 32)
+        if (j + lane < kRowsTile + 2) same = same && p.seq[o.t0 - 1 + j + lane] == own;
+    }
+    o.plain = __all_sync(0xffffffffu, same);
+  }
+  if (lane == 0) s.info[n & 3] = o;
+  __syncwarp();
+}
+
+// Step 2 of a tile (one warp): its run for the tiles after it, and the state that reaches each of its warps.
+template <int V>
+__device__ __forceinline__ void carry_over(Shared<V>& s, int n, const Plan& p, int ch, int lane, WsHeader* hdr,
+                                           uint64_t limit_ns) {
+  const int64_t pos = s.info[n & 3].pos, g = pos / kGroup;
+  const int c = s.info[n & 3].c0 + lane * V, before = (int)(pos % kGroup);
+  const bool in = c < ch, more = pos + 1 < p.tiles;
+  const Ch<V>(*ra)[32] = s.a[n & 1], (*rh)[32] = s.h[n & 1];
+  if (before < kGroup - 1 && more) {
+    Ch<V> A = ra[0][lane], H = rh[0][lane];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) join(A, H, ra[w][lane], rh[w][lane]);
     if (in) {
-      Pair<V> t;
+      Pair<V> o;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        t.a[i] = A.f[i] != A.f[i] ? __uint_as_float(0x7fc00000u) : A.f[i];
-        t.h[i] = H.f[i];
+        o.a[i] = A.f[i] != A.f[i] ? __uint_as_float(0x7fc00000u) : A.f[i];
+        o.h[i] = H.f[i];
       }
-      tell(p.agg + (pos * ch + c) * 2, t);
+      tell(p.agg + (pos * ch + c) * 2, o);
     }
   }
-  if (want1) {
-    if (!__all_sync(0xffffffffu, got1)) hear_slow(at1, one, in, hdr, limit_ns);
+  Ch<V> h = all<V>(0.f);
+  const float *at = p.agg + (g * kGroup * ch + c) * 2, *at_start = p.group + (g * ch + c) * 2;
+  constexpr int kHalf = kGroup / 2;
+#pragma unroll 1
+  for (int j0 = 0; j0 < kGroup; j0 += kHalf) {
+    const bool start = j0 == 0 && g > 0;
+    if (!start && j0 >= before) break;
+    Pair<V> t[kHalf], u;
+    Patience wait;
+    for (;;) {               // all of them at once, until all are there
+      bool ok = true;
+      if (start && in) ok = hear(at_start, u);
 #pragma unroll
-    for (int i = 0; i < V; ++i) A.f[i] = one.a[i], H.f[i] = one.h[i];
-  }
-  if (want2) {
-    if (!__all_sync(0xffffffffu, got2)) hear_slow(at2, two, in, hdr, limit_ns);
-    Ch<V> B, G;
+      for (int j = 0; j < kHalf; ++j)
+        if (j0 + j < before && in) ok &= hear(at + (int64_t)(j0 + j) * ch * 2, t[j]);
+      if (__all_sync(0xffffffffu, ok) || !wait.more(hdr, limit_ns)) break;
+    }
+    if (start) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) B.f[i] = two.a[i], G.f[i] = two.h[i];
-    if (start) s.start[lane] = G;
-    else join(A, H, B, G);
-  }
-  if (want1) {
-    s.ga[warp][lane] = A;
-    s.gh[warp][lane] = H;
-  }
-  __syncthreads();
-  Ch<V> h = g > 0 ? s.start[lane] : all<V>(0.f);
-  for (int w = 0; 2 * w < before; ++w) fold(h, s.ga[w][lane], s.gh[w][lane]);
-  if (warp == kWarps - 1 && before == kGroup - 1 && pos + 1 < p.tiles) {  // the next group's start
-    Ch<V> n = h;
+      for (int i = 0; i < V; ++i) h.f[i] = u.h[i];
+    }
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) fold(n, s.a[w][lane], s.h[w][lane]);
-    if (in) {
-      Pair<V> t;
+    for (int j = 0; j < kHalf; ++j) {
+      if (j0 + j >= before) continue;
+      Ch<V> A, H;
 #pragma unroll
-      for (int i = 0; i < V; ++i) t.a[i] = 1.f, t.h[i] = n.f[i];
-      tell(p.group + ((g + 1) * ch + c) * 2, t);
+      for (int i = 0; i < V; ++i) A.f[i] = t[j].a[i], H.f[i] = t[j].h[i];
+      fold(h, A, H);
     }
   }
-  for (int w = 0; w < rank; ++w) fold(h, s.a[w][lane], s.h[w][lane]);
-  return h;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    s.carry[n & 1][w][lane] = h;
+    fold(h, ra[w][lane], rh[w][lane]);
+  }
+  if (before == kGroup - 1 && more && in) {  // the next group's start
+    Pair<V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.a[i] = 1.f, o.h[i] = h.f[i];
+    tell(p.group + ((g + 1) * ch + c) * 2, o);
+  }
 }
 
 // Bits of a warp's S rows: valid ones, first and last ones of a sequence; lane j holds row j's sequence.
@@ -427,52 +466,47 @@ struct Rows {
   uint32_t valid, first, last;
   int seq;
 };
-struct RowsRaw {
-  int seq, before, after;
-};
 template <int S>
-__device__ __forceinline__ RowsRaw rows_load(const int32_t* seq, int64_t t0, int64_t T, int lane) {
+__device__ __forceinline__ Rows rows_of(const int32_t* seq, int64_t t0, int64_t T, int lane) {
   const int64_t t = t0 + lane;
-  RowsRaw r;
+  Rows r;
   r.seq = lane < S && t < T ? seq[t] : -1;
-  r.before = lane < S && t < T && t > 0 ? seq[t - 1] : -1;
-  r.after = lane < S && t + 1 < T ? seq[t + 1] : -1;
+  const int before = lane < S && t < T && t > 0 ? seq[t - 1] : -1;
+  const int after = lane < S && t + 1 < T ? seq[t + 1] : -1;
+  r.valid = __ballot_sync(0xffffffffu, r.seq >= 0);
+  r.first = __ballot_sync(0xffffffffu, r.seq >= 0 && before != r.seq);
+  r.last = __ballot_sync(0xffffffffu, r.seq >= 0 && after != r.seq);
   return r;
 }
-__device__ __forceinline__ Rows rows_of(const RowsRaw& r) {
-  Rows o;
-  o.seq = r.seq;
-  o.valid = __ballot_sync(0xffffffffu, r.seq >= 0);
-  o.first = __ballot_sync(0xffffffffu, r.seq >= 0 && r.before != r.seq);
-  o.last = __ballot_sync(0xffffffffu, r.seq >= 0 && r.after != r.seq);
-  return o;
-}
 
-// A warp's S rows of one input on their way into its part of shared memory, [row][lane], zeros where there is
-// nothing: 16 bytes a copy where the rows allow (`wide`), else a lane's own elements.
-template <typename T, int V, int S>
-__device__ __forceinline__ void fetch(typename Pack<T, V>::Raw* to, const T* p, int64_t pitch, int64_t t0, int64_t total,
-                                      int c0, int ch, int lane, bool wide) {
-  constexpr int kBytes = sizeof(T) * V;
-  if constexpr (kBytes == 4) {
-    if (wide) {
-      constexpr int kElems = 16 / sizeof(T);
-      const int c = c0 + (lane & 7) * kElems;
-      const int64_t t = t0 + (lane >> 3);
-      const uint32_t dst = tc::smem_u32(to) + lane * 16;
-      const T* src = p + t * pitch + c;
-#pragma unroll
-      for (int j = 0; j < S; j += 4) {
-        const bool ok = c < ch && t + j < total;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + j * 128), "l"(ok ? src : p),
-                     "r"(ok ? 16 : 0)
-                     : "memory");
-        src += 4 * pitch;
-      }
-      return;
-    }
+// Rows of one input on their way into shared memory, [row][lane], zeros where there is nothing.  Where rows
+// allow, the whole tile's by one warp, 16 bytes a copy; else a warp's own S rows, a lane its own elements.
+template <typename T, int V, int R>
+__device__ __forceinline__ void fetch_tile(void* to, const T* p, int64_t pitch, int64_t t0, int64_t total, int c0, int ch,
+                                           int lane) {
+  constexpr int kRow = 32 * V * (int)sizeof(T), kChunks = kRow / 16, kAtOnce = 32 / kChunks;
+  static_assert(R % kAtOnce == 0, "whole copies");
+  const int c = c0 + lane % kChunks * (16 / (int)sizeof(T));
+  const int left = c < ch ? (int)(total - t0 < R ? total - t0 : R) - lane / kChunks : 0;   // rows from this lane's first
+  uint32_t dst = tc::smem_u32(to) + lane * 16;
+  const T* src = p + (t0 + lane / kChunks) * pitch + c;
+  const int64_t step = kAtOnce * pitch;
+#pragma unroll 8
+  for (int j = 0; j < R; j += kAtOnce) {
+    const bool ok = j < left;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(ok ? src : p), "r"(ok ? 16 : 0)
+                 : "memory");
+    dst += 512;
+    src += step;
   }
-  const int c = c0 + lane * V;
+}
+__device__ __forceinline__ void fetched(uint64_t* full) {   // arrives when this lane's copies are done
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(full)) : "memory");
+}
+template <typename T, int V, int S>
+__device__ __forceinline__ void fetch_own(typename Pack<T, V>::Raw* to, const T* p, int64_t pitch, int64_t t0,
+                                          int64_t total, int c, int ch, int lane) {
+  constexpr int kBytes = sizeof(T) * V;
   const T* src = p + t0 * pitch + c;
 #pragma unroll
   for (int j = 0; j < S; ++j) {
@@ -487,132 +521,198 @@ __device__ __forceinline__ void fetch(typename Pack<T, V>::Raw* to, const T* p, 
     src += pitch;
   }
 }
-__device__ __forceinline__ void fetch_done() {
+__device__ __forceinline__ void fetch_own_done() {
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
 }
-// A body for runs of rows inside one sequence of channels that are all there, and one for the others.
-struct Plain { static constexpr bool value = true; };
-struct Mixed { static constexpr bool value = false; };
-
 // ---- forward --------------------------------------------------------------------------------
 template <typename T, int V, bool kGate, int S>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kAll, kScanCtas)
 gated_scan_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict__ r, int64_t r_pitch,
                   const T* __restrict__ ig, int64_t i_pitch, const float* __restrict__ a_log,
                   const float* state, const int32_t* __restrict__ idx, int64_t num_slots, int64_t stride,
                   float* final_state, T* __restrict__ y, float* __restrict__ carries, Plan plan, WsHeader* hdr,
                   int64_t total, int ch, bool wide, uint64_t limit_ns) {
   constexpr bool kFast = sizeof(T) == 2;
-  constexpr int kInputs = kGate ? 3 : 2;
+  constexpr int kInputs = kGate ? 3 : 2, kRowsTile = kWarps * S;
   using P = Pack<T, V>;
   using Raw = typename P::Raw;
-  extern __shared__ __align__(16) uint8_t s_raw[];
+  using Kept = typename std::conditional<V == 2, float4, float2>::type;
+  extern __shared__ __align__(128) uint8_t s_raw[];   // [input][row][lane], then a and m u of the tile before
   __shared__ Shared<V> s;
+  Raw* const raw = reinterpret_cast<Raw*>(s_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Raw* const own = reinterpret_cast<Raw*>(s_raw) + warp * (kInputs * S * 32);   // [input][row][lane]
-  const Raw* const mine = own + lane;
 
-  if (tid == 0) s.next = atomicAdd(&hdr->next_item, 1u);
+  if (tid == 0) {
+    tc::mbar_init(&s.full, 32);
+    tc::fence_mbar_init();
+  }
+  if (warp == kWarps) {
+    take<V, S, false>(s, 0, plan, hdr, total, ch, lane);
+    take<V, S, false>(s, 1, plan, hdr, total, ch, lane);
+  }
   __syncthreads();
-  uint32_t item = s.next;
-  RowsRaw rows_raw;
-  float rate_raw[V];
-  auto prefetch = [&](uint32_t it) {
-    const int64_t k = it / plan.blocks, t0 = (k * kWarps + warp) * S;
-    const int c0 = (int)(it % plan.blocks) * 32 * V;
-    fetch<T, V, S>(own, x, x_pitch, t0, total, c0, ch, lane, wide);
-    fetch<T, V, S>(own + S * 32, r, r_pitch, t0, total, c0, ch, lane, wide);
-    if (kGate) fetch<T, V, S>(own + 2 * S * 32, ig, i_pitch, t0, total, c0, ch, lane, wide);
-    rows_raw = rows_load<S>(plan.seq, t0, total, lane);
-    const int c = c0 + lane * V;
-#pragma unroll
-    for (int i = 0; i < V; ++i) rate_raw[i] = c + i < ch ? a_log[c + i] : 0.f;
+
+  if (warp == kWarps) {   // this warp takes tiles and fetches their rows
+    auto fetch = [&](int n) {
+      const Info& o = s.info[n & 3];
+      if (!wide || o.t0 < 0) return;
+      fetch_tile<T, V, kRowsTile>(raw, x, x_pitch, o.t0, total, o.c0, ch, lane);
+      fetch_tile<T, V, kRowsTile>(raw + kRowsTile * 32, r, r_pitch, o.t0, total, o.c0, ch, lane);
+      if (kGate) fetch_tile<T, V, kRowsTile>(raw + 2 * kRowsTile * 32, ig, i_pitch, o.t0, total, o.c0, ch, lane);
+      fetched(&s.full);
+    };
+    fetch(0);
+    for (int n = 0; s.info[n & 3].t0 >= 0; ++n) {
+      bar_sync(kRan + (n & 1));
+      fetch(n + 1);
+      take<V, S, false>(s, n + 2, plan, hdr, total, ch, lane);
+      bar_arrive(kCarried + (n & 1));
+    }
+    return;
+  }
+  if (warp > kWarps) {    // and this one carries the state
+    for (int n = 0; s.info[n & 3].t0 >= 0; ++n) {
+      bar_sync(kRan + (n & 1));
+      carry_over(s, n, plan, ch, lane, hdr, limit_ns);
+      bar_arrive(kCarried + (n & 1));
+    }
+    return;
+  }
+
+  const Raw* const mine = raw + warp * S * 32 + lane;
+  Kept* const kept = reinterpret_cast<Kept*>(s_raw + kInputs * kRowsTile * 32 * sizeof(Raw)) + warp * S * 32 + lane;
+  auto fetch = [&](int n) {   // where the other warp does not
+    const Info& o = s.info[n & 3];
+    if (wide || o.t0 < 0) return;
+    const int64_t t0 = o.t0 + warp * S;
+    const int c = o.c0 + lane * V;
+    Raw* const to = raw + warp * S * 32;
+    fetch_own<T, V, S>(to, x, x_pitch, t0, total, c, ch, lane);
+    fetch_own<T, V, S>(to + kRowsTile * 32, r, r_pitch, t0, total, c, ch, lane);
+    if (kGate) fetch_own<T, V, S>(to + 2 * kRowsTile * 32, ig, i_pitch, t0, total, c, ch, lane);
   };
-  if (item < plan.items) prefetch(item);
-  while (item < plan.items) {
-    const int64_t k = item / plan.blocks, t0 = (k * kWarps + warp) * S;
-    const int c0 = (int)(item % plan.blocks) * 32 * V, c = c0 + lane * V;
+  auto unkeep = [&](int j, Ch<V>& a, Ch<V>& b) {
+    const Kept q = kept[j * 32];
+    if constexpr (V == 2) a = {{q.x, q.y}}, b = {{q.z, q.w}};
+    else a = {{q.x}}, b = {{q.y}};
+  };
+  // step 3 of tile n
+  auto finish = [&](int n) {
+    const Info& o = s.info[n & 3];
+    const int64_t t0 = o.t0 + warp * S;
+    const int c = o.c0 + lane * V;
     const bool in = c < ch;
-    if (tid == 0) s.next = atomicAdd(&hdr->next_item, 1u);
+    Ch<V> h = s.carry[n & 1][warp][lane];
+    T* yp = y + t0 * ch + c;
+    const bool marked = carries && t0 % KDA_GATED_CARRY_ROWS == 0;
+    static_assert(KDA_GATED_CARRY_ROWS % S == 0, "carries are left where a warp starts");
+    if (marked && in && t0 < total) store<float, V>(carries + t0 / KDA_GATED_CARRY_ROWS * ch + c, h);
+    if (o.plain) {
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        Ch<V> a, b;
+        unkeep(j, a, b);
+        h = fma(a, h, b);
+        if (KDA_CHECK(t0 + j < total)) store<T, V>(yp, h);
+        yp += ch;
+      }
+    } else {
+      const Rows rows = rows_of<S>(plan.seq, t0, total, lane);
+#pragma unroll 1
+      for (int j = 0; j < S; ++j) {
+        Ch<V> a, b;
+        unkeep(j, a, b);
+        if ((rows.first >> j) & 1) h = b;
+        else h = fma(a, h, b);
+        if (((rows.valid >> j) & 1) && in && KDA_CHECK(t0 + j < total && c + V <= ch)) store<T, V>(yp, h);
+        yp += ch;
+        if (((rows.last >> j) & 1) && final_state) {
+          const int q = __shfl_sync(0xffffffffu, rows.seq, j);
+          const int64_t slot = idx ? resolve_slot(idx, q, num_slots) : q;
+          if (in && KDA_CHECK(slot >= 0)) store<float, V>(final_state + slot * stride + c, h);
+        }
+      }
+    }
+  };
+
+  fetch(0);
+  int n = 0;
+  for (; s.info[n & 3].t0 >= 0; ++n) {
+    const Info& o = s.info[n & 3];
+    const int c = o.c0 + lane * V;
     Ch<V> rate;
 #pragma unroll
-    for (int i = 0; i < V; ++i) rate.f[i] = ssm_rate(rate_raw[i]);
-    const Rows rows = rows_of(rows_raw);
-    const bool plain = rows.valid == (1u << S) - 1 && (rows.first | rows.last) == 0 && c0 + 32 * V <= ch;
-    fetch_done();
+    for (int i = 0; i < V; ++i) rate.f[i] = c + i < ch ? ssm_rate(a_log[c + i]) : 0.f;
+    if (!wide) fetch_own_done();
+    else if (!tc::mbar_wait(&s.full, n & 1)) raise_status(&hdr->status, KDA_DEVICE_PIPE_TIMEOUT);
 
     Ch<V> a[S], b[S];
 #pragma unroll
     for (int j = 0; j < S; ++j) {
       Ch<V> w;
-      a[j] = decay<kFast>(mul(rate, sigmoid<kFast>(P::open(mine[(S + j) * 32]))), w);
+      a[j] = decay<kFast>(mul(rate, sigmoid<kFast>(P::open(mine[(kRowsTile + j) * 32]))), w);
       b[j] = mul(root<kFast>(w), P::open(mine[j * 32]));
-      if (kGate) b[j] = mul(b[j], sigmoid<kFast>(P::open(mine[(2 * S + j) * 32])));
+      if (kGate) b[j] = mul(b[j], sigmoid<kFast>(P::open(mine[(2 * kRowsTile + j) * 32])));
     }
     Ch<V> A = a[0], H = b[0];
-    if (plain) {
+    if (o.plain) {
 #pragma unroll
       for (int j = 1; j < S; ++j) {
         H = fma(a[j], H, b[j]);
         A = mul(A, a[j]);
       }
     } else {
+      const Rows rows = rows_of<S>(plan.seq, o.t0 + warp * S, total, lane);
+      if (rows.first) A = all<V>(-1.f);
 #pragma unroll
       for (int j = 0; j < S; ++j) {
         if ((rows.first >> j) & 1) {  // the sequence's own state instead of what came before
-          const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-          const int64_t slot = idx ? resolve_slot(idx, n, num_slots) : n;
+          const int q = __shfl_sync(0xffffffffu, rows.seq, j);
+          const int64_t slot = idx ? resolve_slot(idx, q, num_slots) : q;
           Ch<V> h0 = all<V>(0.f);
-          if (state && in && KDA_CHECK(slot >= 0)) h0 = Pack<float, V>::open(load<float, V>(state + slot * stride + c));
+          if (state && c < ch && KDA_CHECK(slot >= 0))
+            h0 = Pack<float, V>::open(load<float, V>(state + slot * stride + c));
           b[j] = fma(a[j], h0, b[j]);
           H = b[j];
         } else if (j > 0) {
           H = fma(a[j], H, b[j]);
         }
-        if (j > 0) A = mul(A, a[j]);
+        if (j > 0 && !rows.first) A = mul(A, a[j]);
       }
-      if (rows.first) A = all<V>(-1.f);
     }
-    s.a[warp][lane] = A;
-    s.h[warp][lane] = H;
-    __syncthreads();
-    const uint32_t next = s.next;
-    if (next < plan.items) prefetch(next);
-    Ch<V> h = enter(s, plan, k, c, ch, warp, lane, warp, hdr, limit_ns);
-    if (carries && t0 % KDA_GATED_CARRY_ROWS == 0 && t0 < total && in)
-      store<float, V>(carries + t0 / KDA_GATED_CARRY_ROWS * ch + c, h);
-    T* yp = y + t0 * ch + c;
-    if (plain) {
-#pragma unroll
-      for (int j = 0; j < S; ++j) {
-        h = fma(a[j], h, b[j]);
-        if (KDA_CHECK(t0 + j < total)) store<T, V>(yp, h);
-        yp += ch;
-      }
+    s.a[n & 1][warp][lane] = A;
+    s.h[n & 1][warp][lane] = H;
+    bar_arrive(kRan + (n & 1));
+    if (n > 0) {
+      bar_sync(kCarried + ((n - 1) & 1));
+      fetch(n + 1);
+      finish(n - 1);
     } else {
-#pragma unroll
-      for (int j = 0; j < S; ++j) {
-        if ((rows.first >> j) & 1) h = b[j];
-        else h = fma(a[j], h, b[j]);
-        if (((rows.valid >> j) & 1) && in && KDA_CHECK(t0 + j < total && c + V <= ch)) store<T, V>(yp, h);
-        yp += ch;
-        if (((rows.last >> j) & 1) && final_state) {
-          const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-          const int64_t slot = idx ? resolve_slot(idx, n, num_slots) : n;
-          if (in && KDA_CHECK(slot >= 0)) store<float, V>(final_state + slot * stride + c, h);
-        }
-      }
+      fetch(1);
     }
-    __syncthreads();   // everyone has read s before the next tile writes it
-    item = next;
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      if constexpr (V == 2) kept[j * 32] = make_float4(a[j].f[0], a[j].f[1], b[j].f[0], b[j].f[1]);
+      else kept[j * 32] = make_float2(a[j].f[0], b[j].f[0]);
+    }
+  }
+  if (n > 0) {
+    bar_sync(kCarried + ((n - 1) & 1));
+    finish(n - 1);
   }
   KDA_DEBUG_FOLD(&hdr->status);
 }
 
 // ---- backward -------------------------------------------------------------------------------
+template <int V> struct BackShared : Shared<V> {
+  Ch<V> fa[2][kWarps][32], fh[2][kWarps][32];   // the state's own runs, from the first row on
+  Ch<V> state[2][kWarps][32];                   // the state that reaches each warp
+  Ch<V> sum[2][kWarps][32];                     // each warp's part of dA_log
+};
+
 template <typename T, int V, bool kGate, int S>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kAll, kBackCtas)
 gated_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict__ x, int64_t x_pitch,
                   const T* __restrict__ r, int64_t r_pitch, const T* __restrict__ ig, int64_t i_pitch,
                   const float* __restrict__ a_log, const float* __restrict__ carries,
@@ -620,177 +720,278 @@ gated_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restric
                   T* __restrict__ dr, T* __restrict__ di, float* __restrict__ dstate, float* __restrict__ part,
                   Plan plan, WsHeader* hdr, int64_t total, int ch, bool wide, uint64_t limit_ns) {
   constexpr bool kFast = sizeof(T) == 2;
-  constexpr int kInputs = kGate ? 4 : 3;
-  static_assert(S * kWarps == KDA_GATED_CARRY_ROWS, "a tile starts where a carry was left");
+  constexpr int kInputs = kGate ? 4 : 3, kRowsTile = kWarps * S;
+  static_assert(kRowsTile == KDA_GATED_CARRY_ROWS, "a tile starts where a carry was left");
   using P = Pack<T, V>;
   using Raw = typename P::Raw;
-  extern __shared__ __align__(16) uint8_t s_raw[];
-  __shared__ Shared<V> s;
-  __shared__ Ch<V> s_fa[kWarps][32], s_fh[kWarps][32];       // the state's own (A, H)
-  __shared__ Ch<V> s_sum[kWarps][32];
+  struct alignas(4 * sizeof(Raw)) Row4 { Raw x, r, g, i; };
+  using Kept = typename std::conditional<V == 2, float4, float2>::type;
+  extern __shared__ __align__(128) uint8_t s_raw[];   // [input][row][lane], then what is kept of the tile before
+  __shared__ BackShared<V> s;
+  Raw* const raw = reinterpret_cast<Raw*>(s_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Raw* own = reinterpret_cast<Raw*>(s_raw) + warp * (kInputs * S * 32);   // [stage][warp][input][row][lane]
-  Raw* other = own + kWarps * kInputs * S * 32;
 
-  if (tid == 0) s.next = atomicAdd(&hdr->next_item, 1u);
+  if (tid == 0) {
+    tc::mbar_init(&s.full, 32);
+    tc::fence_mbar_init();
+  }
+  if (warp == kWarps) {
+    take<V, S, true>(s, 0, plan, hdr, total, ch, lane);
+    take<V, S, true>(s, 1, plan, hdr, total, ch, lane);
+  }
   __syncthreads();
-  uint32_t item = s.next;
-  RowsRaw rows_raw;
-  float rate_raw[V];
-  Ch<V> carry;
-  auto prefetch = [&](uint32_t it, Raw* to) {
-    const int64_t k = plan.tiles - 1 - it / plan.blocks, t0 = (k * kWarps + warp) * S;
-    const int c0 = (int)(it % plan.blocks) * 32 * V;
-    fetch<T, V, S>(to, x, x_pitch, t0, total, c0, ch, lane, wide);
-    fetch<T, V, S>(to + S * 32, r, r_pitch, t0, total, c0, ch, lane, wide);
-    fetch<T, V, S>(to + 2 * S * 32, dy, dy_pitch, t0, total, c0, ch, lane, wide);
-    if (kGate) fetch<T, V, S>(to + 3 * S * 32, ig, i_pitch, t0, total, c0, ch, lane, wide);
-    rows_raw = rows_load<S>(plan.seq, t0, total, lane);
-    const int c = c0 + lane * V;
-    carry = c < ch ? Pack<float, V>::open(load<float, V>(carries + k * ch + c)) : all<V>(0.f);
+
+  if (warp == kWarps) {   // this warp takes tiles and fetches their rows
+    auto fetch = [&](int n) {
+      const Info& o = s.info[n & 3];
+      if (!wide || o.t0 < 0) return;
+      fetch_tile<T, V, kRowsTile>(raw, x, x_pitch, o.t0, total, o.c0, ch, lane);
+      fetch_tile<T, V, kRowsTile>(raw + kRowsTile * 32, r, r_pitch, o.t0, total, o.c0, ch, lane);
+      fetch_tile<T, V, kRowsTile>(raw + 2 * kRowsTile * 32, dy, dy_pitch, o.t0, total, o.c0, ch, lane);
+      if (kGate) fetch_tile<T, V, kRowsTile>(raw + 3 * kRowsTile * 32, ig, i_pitch, o.t0, total, o.c0, ch, lane);
+      fetched(&s.full);
+    };
+    auto add_up = [&](int n) {   // dA_log's part of tile n, which all warps are done with
+      if (n < 0) return;
+      const int c = s.info[n & 3].c0 + lane * V;
+      Ch<V> sum = s.sum[n & 1][0][lane];
 #pragma unroll
-    for (int i = 0; i < V; ++i) rate_raw[i] = c + i < ch ? a_log[c + i] : 0.f;
+      for (int w = 1; w < kWarps; ++w) sum = add(sum, s.sum[n & 1][w][lane]);
+      if (c < ch) store<float, V>(part + s.info[n & 3].t0 / kRowsTile * ch + c, sum);
+    };
+    fetch(0);
+    int n = 0;
+    for (; s.info[n & 3].t0 >= 0; ++n) {
+      bar_sync(kRan + (n & 1));
+      fetch(n + 1);
+      add_up(n - 2);
+      take<V, S, true>(s, n + 2, plan, hdr, total, ch, lane);
+      bar_arrive(kCarried + (n & 1));
+    }
+    bar_sync(kRan + (n & 1));
+    add_up(n - 2);
+    add_up(n - 1);
+    return;
+  }
+  if (warp > kWarps) {    // and this one carries state and e
+    int n = 0;
+    for (; s.info[n & 3].t0 >= 0; ++n) {
+      const int c = s.info[n & 3].c0 + lane * V;
+      Ch<V> h = all<V>(0.f);
+      if (c < ch) h = Pack<float, V>::open(load<float, V>(carries + s.info[n & 3].t0 / kRowsTile * ch + c));
+      bar_sync(kRan + (n & 1));
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        s.state[n & 1][w][lane] = h;
+        fold(h, s.fa[n & 1][w][lane], s.fh[n & 1][w][lane]);
+      }
+      carry_over<V>(s, n, plan, ch, lane, hdr, limit_ns);
+      bar_arrive(kCarried + (n & 1));
+    }
+    bar_arrive(kRan + (n & 1));
+    return;
+  }
+
+  const Raw* const mine = raw + warp * S * 32 + lane;
+  Kept* const kept = reinterpret_cast<Kept*>(s_raw + kInputs * kRowsTile * 32 * sizeof(Raw)) + warp * S * 32 + lane;
+  Row4* const kept_rows = reinterpret_cast<Row4*>(s_raw + kRowsTile * 32 * (kInputs * sizeof(Raw) + sizeof(Kept))) +
+                          warp * S * 32 + lane;
+  const int rank = kWarps - 1 - warp;
+  auto fetch = [&](int n) {   // where the other warp does not
+    const Info& o = s.info[n & 3];
+    if (wide || o.t0 < 0) return;
+    const int64_t t0 = o.t0 + warp * S;
+    const int c = o.c0 + lane * V;
+    Raw* const to = raw + warp * S * 32;
+    fetch_own<T, V, S>(to, x, x_pitch, t0, total, c, ch, lane);
+    fetch_own<T, V, S>(to + kRowsTile * 32, r, r_pitch, t0, total, c, ch, lane);
+    fetch_own<T, V, S>(to + 2 * kRowsTile * 32, dy, dy_pitch, t0, total, c, ch, lane);
+    if (kGate) fetch_own<T, V, S>(to + 3 * kRowsTile * 32, ig, i_pitch, t0, total, c, ch, lane);
   };
-  if (item < plan.items) prefetch(item, own);
-  while (item < plan.items) {
-    const int64_t pos = item / plan.blocks, k = plan.tiles - 1 - pos;   // tiles from the last one on
-    const int64_t t0 = (k * kWarps + warp) * S;
-    const int c0 = (int)(item % plan.blocks) * 32 * V, c = c0 + lane * V;
+  // dfinal of a sequence whose last row is row j
+  auto at_end = [&](const Rows& rows, int j, int c) {
+    Ch<V> l = all<V>(0.f);
+    const int q = __shfl_sync(0xffffffffu, rows.seq, j);
+    if (dfinal && c < ch) l = Pack<float, V>::open(load<float, V>(dfinal + (int64_t)q * ch + c));
+    return l;
+  };
+  // step 3 of tile n, from its last row to its first
+  auto finish = [&](int n) {
+    const Info& o = s.info[n & 3];
+    const int64_t t0 = o.t0 + warp * S, at0 = t0 * ch + o.c0 + lane * V;
+    const int c = o.c0 + lane * V;
     const bool in = c < ch;
-    const Raw* const mine = own + lane;
-    if (tid == 0) s.next = atomicAdd(&hdr->next_item, 1u);
     Ch<V> rate;
 #pragma unroll
-    for (int i = 0; i < V; ++i) rate.f[i] = ssm_rate(rate_raw[i]);
-    const Rows rows = rows_of(rows_raw);
-    const bool plain = rows.valid == (1u << S) - 1 && (rows.first | rows.last) == 0 && c0 + 32 * V <= ch;
-    Ch<V> h = carry;
-    fetch_done();
-    // dy, and dfinal where the row is a sequence's last
-    auto slope = [&](int j) {
-      Ch<V> l = P::open(mine[(2 * S + j) * 32]);
-      if (((rows.last >> j) & 1) && dfinal) {
-        const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-        if (in) l = add(l, Pack<float, V>::open(load<float, V>(dfinal + (int64_t)n * ch + c)));
-      }
-      return l;
-    };
-
-    // the rows' decays and what they add to the state
-    Ch<V> a[S], er[S], ei[S], hp[S];
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-      Ch<V> w;
-      er[j] = exp_neg<kFast, true>(P::open(mine[(S + j) * 32]));
-      a[j] = decay<kFast>(mul(rate, one_over<kFast>(er[j])), w);
-      hp[j] = mul(root<kFast>(w), P::open(mine[j * 32]));
+    for (int i = 0; i < V; ++i) rate.f[i] = c + i < ch ? ssm_rate(a_log[c + i]) : 0.f;
+    Ch<V> e = s.carry[n & 1][rank][lane], sum = all<V>(0.f);
+    const Ch<V> h0 = s.state[n & 1][warp][lane];
+    auto one = [&](int j, const Ch<V>& reach, Ch<V> l, Ch<V>& ox, Ch<V>& orr, Ch<V>& oi) {
+      const Kept q = kept[j * 32];
+      const Row4 row = kept_rows[j * 32];
+      Ch<V> a, hp;
+      if constexpr (V == 2) a = {{q.x, q.y}}, hp = {{q.z, q.w}};
+      else a = {{q.x}}, hp = {{q.y}};
+      hp = add(hp, reach);
+      l = add(l, P::open(row.g));
+      e = mul(a, l);
+      const Ch<V> er = exp_neg<kFast, true>(P::open(row.r)), sr = one_over<kFast>(er), g = mul(rate, sr);
+      Ch<V> m, k, u = P::open(row.x);
+      over_root<kFast>(g, lost(g, series(g), a), k, m);
+      const Ch<V> ml = mul(m, l);
+      ox = ml;
       if (kGate) {
-        ei[j] = exp_neg<kFast, true>(P::open(mine[(3 * S + j) * 32]));
-        hp[j] = mul(hp[j], one_over<kFast>(ei[j]));
+        const Ch<V> ei = exp_neg<kFast, true>(P::open(row.i)), si = one_over<kFast>(ei);
+        u = mul(u, si);
+        ox = mul(ml, si);
+        oi = mul(mul(ml, u), mul(ei, si));
       }
-    }
-    // the state's (A, H), and what the rows do to e, from the last one to the first; hp becomes the state
-    // before each row, without what reaches the warp
-    Ch<V> A = a[0], H = all<V>(0.f), E = all<V>(0.f);
-    if (plain) {
+      // p = e (g h_{t-1} - a (g / m) u)
+      const Ch<V> p = mul(e, fma(mul(a, k), u, mul(g, hp)));
+      orr = mul(p, mul(er, sr));
+      return p;
+    };
+    if (o.plain) {
+      // what reaches row j of the warp's state: h0 decayed by the rows before it
+      Ch<V> reach[S];
+      reach[0] = h0;
 #pragma unroll
-      for (int j = 0; j < S; ++j) {
-        const Ch<V> b = hp[j];
-        hp[j] = H;
-        H = j > 0 ? fma(a[j], H, b) : b;
-        if (j > 0) A = mul(A, a[j]);
+      for (int j = 1; j < S; ++j) {
+        const Kept q = kept[(j - 1) * 32];
+        Ch<V> a;
+        if constexpr (V == 2) a = {{q.x, q.y}};
+        else a = {{q.x}};
+        reach[j] = mul(reach[j - 1], a);
       }
 #pragma unroll
-      for (int j = S - 1; j >= 0; --j) E = mul(a[j], add(P::open(mine[(2 * S + j) * 32]), E));
+      for (int j = S - 1; j >= 0; --j) {
+        Ch<V> ox, orr, oi;
+        sum = add(sum, one(j, reach[j], e, ox, orr, oi));
+        if (KDA_CHECK(t0 + j < total && c + V <= ch)) {
+          store<T, V>(dx + at0 + (int64_t)j * ch, ox);
+          store<T, V>(dr + at0 + (int64_t)j * ch, orr);
+          if (kGate) store<T, V>(di + at0 + (int64_t)j * ch, oi);
+        }
+      }
     } else {
-#pragma unroll
-      for (int j = 0; j < S; ++j) {
-        const Ch<V> b = hp[j];
-        if ((rows.first >> j) & 1) {
-          const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-          H = all<V>(0.f);
-          if (state && in) H = Pack<float, V>::open(load<float, V>(state + (int64_t)n * ch + c));
-        }
-        hp[j] = H;
-        H = fma(a[j], H, b);
-        if (j > 0) A = mul(A, a[j]);
-      }
-#pragma unroll
+      const Rows rows = rows_of<S>(plan.seq, t0, total, lane);
+      const int until = rows.first ? __ffs(rows.first) - 1 : S;   // rows that h0 reaches
+#pragma unroll 1
       for (int j = S - 1; j >= 0; --j) {
-        const Ch<V> l = slope(j);
-        E = mul(a[j], (rows.last >> j) & 1 ? l : add(l, E));
-      }
-    }
-    s_fa[warp][lane] = rows.first ? all<V>(-1.f) : A;
-    s_fh[warp][lane] = H;
-    const int rank = kWarps - 1 - warp;
-    s.a[rank][lane] = rows.last ? all<V>(-1.f) : A;
-    s.h[rank][lane] = E;
-    __syncthreads();
-    const uint32_t next = s.next;
-    if (next < plan.items) prefetch(next, other);
-    Ch<V> e = enter(s, plan, pos, c, ch, warp, lane, rank, hdr, limit_ns);
-    for (int w = 0; w < warp; ++w) fold(h, s_fa[w][lane], s_fh[w][lane]);
-#pragma unroll
-    for (int j = 0; j < S; ++j) {  // decayed from row to row until a sequence begins
-      if (!plain && ((rows.first >> j) & 1)) break;
-      hp[j] = add(hp[j], h);
-      h = mul(h, a[j]);
-    }
-    Ch<V> sum = all<V>(0.f);
-    auto rest = [&](auto kind) {
-      constexpr bool kPlain = decltype(kind)::value;
-      const int64_t at0 = t0 * ch + c;
-#pragma unroll
-      for (int j = S - 1; j >= 0; --j) {
-        Ch<V> l = kPlain ? P::open(mine[(2 * S + j) * 32]) : slope(j);
-        if (kPlain || !((rows.last >> j) & 1)) l = add(l, e);
-        e = mul(a[j], l);
-        const Ch<V> sr = one_over<kFast>(er[j]), g = mul(rate, sr);
-        Ch<V> m, q, u = P::open(mine[j * 32]), si;
-        over_root<kFast>(g, lost(g, series(g), a[j]), q, m);
-        const Ch<V> ml = mul(m, l);
-        if (kGate) {
-          si = one_over<kFast>(ei[j]);
-          u = mul(u, si);
+        Ch<V> reach = all<V>(0.f), ox, orr, oi;
+        if (j < until) {
+          reach = h0;
+          for (int i = 0; i < j; ++i) {
+            const Kept q = kept[i * 32];
+            Ch<V> a;
+            if constexpr (V == 2) a = {{q.x, q.y}};
+            else a = {{q.x}};
+            reach = mul(reach, a);
+          }
         }
-        // p = e (g h_{t-1} - a (g / m) u)
-        const Ch<V> p = mul(e, fma(mul(a[j], q), u, mul(g, hp[j])));
-        Ch<V> ox = kGate ? mul(ml, si) : ml, orr = mul(p, mul(er[j], sr)), oi;
-        if (kGate) oi = mul(mul(ml, u), mul(ei[j], si));
+        const Ch<V> p = one(j, reach, (rows.last >> j) & 1 ? at_end(rows, j, c) : e, ox, orr, oi);
         const int64_t at = at0 + (int64_t)j * ch;
-        if (kPlain) {
-          sum = add(sum, p);
-        } else if ((rows.valid >> j) & 1) {
+        if ((rows.valid >> j) & 1) {
           sum = add(sum, p);
           if (((rows.first >> j) & 1) && dstate) {
-            const int n = __shfl_sync(0xffffffffu, rows.seq, j);
-            if (in) store<float, V>(dstate + (int64_t)n * ch + c, e);
+            const int q = __shfl_sync(0xffffffffu, rows.seq, j);
+            if (in) store<float, V>(dstate + (int64_t)q * ch + c, e);
           }
         } else {
           ox = orr = oi = all<V>(0.f);
         }
-        if ((kPlain || (in && t0 + j < total)) && KDA_CHECK(t0 + j < total && c + V <= ch)) {
+        if (in && t0 + j < total && KDA_CHECK(c + V <= ch)) {
           store<T, V>(dx + at, ox);
           store<T, V>(dr + at, orr);
           if (kGate) store<T, V>(di + at, oi);
         }
       }
-    };
-    if (plain) rest(Plain{});
-    else rest(Mixed{});
-    s_sum[warp][lane] = sum;
-    __syncthreads();   // everyone has read s, too, before the next tile writes it
-    if (warp == 0 && in) {
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) sum = add(sum, s_sum[w][lane]);
-      store<float, V>(part + k * ch + c, sum);
     }
-    Raw* t = own;
-    own = other;
-    other = t;
-    item = next;
+    s.sum[n & 1][warp][lane] = sum;
+  };
+
+  fetch(0);
+  int n = 0;
+  for (; s.info[n & 3].t0 >= 0; ++n) {
+    const Info& o = s.info[n & 3];
+    const int c = o.c0 + lane * V;
+    Ch<V> rate;
+#pragma unroll
+    for (int i = 0; i < V; ++i) rate.f[i] = c + i < ch ? ssm_rate(a_log[c + i]) : 0.f;
+    if (!wide) fetch_own_done();
+    else if (!tc::mbar_wait(&s.full, n & 1)) raise_status(&hdr->status, KDA_DEVICE_PIPE_TIMEOUT);
+
+    // the rows' decays and what they add to the state; hp becomes the state before each row, without what
+    // reaches the warp
+    Row4 row[S];
+    Ch<V> a[S], hp[S];
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      row[j].x = mine[j * 32];
+      row[j].r = mine[(kRowsTile + j) * 32];
+      row[j].g = mine[(2 * kRowsTile + j) * 32];
+      if (kGate) row[j].i = mine[(3 * kRowsTile + j) * 32];
+      Ch<V> w;
+      a[j] = decay<kFast>(mul(rate, one_over<kFast>(exp_neg<kFast, true>(P::open(row[j].r)))), w);
+      hp[j] = mul(root<kFast>(w), P::open(row[j].x));
+      if (kGate) hp[j] = mul(hp[j], sigmoid<kFast>(P::open(row[j].i)));
+    }
+    Ch<V> A = a[0], H = all<V>(0.f), E = all<V>(0.f);
+#pragma unroll
+    for (int j = 1; j < S; ++j) A = mul(A, a[j]);
+    Ch<V> EA = A;
+    if (o.plain) {
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        const Ch<V> b = hp[j];
+        hp[j] = H;
+        H = j > 0 ? fma(a[j], H, b) : b;
+      }
+#pragma unroll
+      for (int j = S - 1; j >= 0; --j) E = mul(a[j], add(P::open(row[j].g), E));
+    } else {
+      const Rows rows = rows_of<S>(plan.seq, o.t0 + warp * S, total, lane);
+      if (rows.first) A = all<V>(-1.f);
+      if (rows.last) EA = all<V>(-1.f);
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        const Ch<V> b = hp[j];
+        if ((rows.first >> j) & 1) {
+          const int q = __shfl_sync(0xffffffffu, rows.seq, j);
+          H = all<V>(0.f);
+          if (state && c < ch) H = Pack<float, V>::open(load<float, V>(state + (int64_t)q * ch + c));
+        }
+        hp[j] = H;
+        H = fma(a[j], H, b);
+      }
+#pragma unroll
+      for (int j = S - 1; j >= 0; --j)
+        E = mul(a[j], add(P::open(row[j].g), (rows.last >> j) & 1 ? at_end(rows, j, c) : E));
+    }
+    s.fa[n & 1][warp][lane] = A;
+    s.fh[n & 1][warp][lane] = H;
+    s.a[n & 1][rank][lane] = EA;
+    s.h[n & 1][rank][lane] = E;
+    bar_arrive(kRan + (n & 1));
+    if (n > 0) {
+      bar_sync(kCarried + ((n - 1) & 1));
+      fetch(n + 1);
+      finish(n - 1);
+    } else {
+      fetch(1);
+    }
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      if constexpr (V == 2) kept[j * 32] = make_float4(a[j].f[0], a[j].f[1], hp[j].f[0], hp[j].f[1]);
+      else kept[j * 32] = make_float2(a[j].f[0], hp[j].f[0]);
+      kept_rows[j * 32] = row[j];
+    }
   }
+  if (n > 0) {
+    bar_sync(kCarried + ((n - 1) & 1));
+    finish(n - 1);
+  }
+  bar_arrive(kRan + (n & 1));
   KDA_DEBUG_FOLD(&hdr->status);
 }
 
@@ -850,8 +1051,8 @@ gated_token_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict
 }
 
 // ---- launches -------------------------------------------------------------------------------
-constexpr int kRows = 16;      // rows a warp, forward
-constexpr int kBackRows = 8;   // and backward
+constexpr int kRows = 12;      // rows a warp, forward
+constexpr int kBackRows = 6;   // and backward
 
 bool pairs(const void* p, int64_t pitch, int size) {
   return !p || ((uintptr_t)p % (2 * size) == 0 && pitch % 2 == 0);
@@ -890,11 +1091,11 @@ template <typename T> bool wide16(const GatedArgs& a, bool back) {
          (!a.i || rows(a.i, a.d.i_pitch)) && (!back || rows(a.dy, a.dy_pitch));
 }
 
-// CTAs that stay: two an SM, or one a tile.
+// CTAs that stay: as many as fit, or one a tile.
 template <typename K>
-cudaError_t stay(K* kernel, const Plan& p, int bytes, unsigned* grid) {
+cudaError_t stay(K* kernel, const Plan& p, int ctas, int bytes, unsigned* grid) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  const unsigned most = 2u * (unsigned)gpu_sms();
+  const unsigned most = (unsigned)(ctas * gpu_sms());
   *grid = p.items < most ? p.items : most;
   return e;
 }
@@ -907,10 +1108,10 @@ cudaError_t run_scan(const GatedArgs& a, cudaStream_t st) {
   if (e != cudaSuccess || l.tiles == 0) return e;
   const Plan p = plan_of(l, a.ws);
   auto* kernel = gated_scan_kernel<T, V, kGate, kRows>;
-  const int bytes = (kGate ? 3 : 2) * kRows * kThreads * (int)sizeof(T) * V;
+  const int bytes = kRows * kThreads * V * ((kGate ? 3 : 2) * (int)sizeof(T) + 8);
   unsigned grid;
-  if ((e = stay(kernel, p, bytes, &grid)) != cudaSuccess) return e;
-  kernel<<<grid, kThreads, bytes, st>>>(
+  if ((e = stay(kernel, p, kScanCtas, bytes, &grid)) != cudaSuccess) return e;
+  kernel<<<grid, kAll, bytes, st>>>(
       (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i, a.d.i_pitch, a.a_log, a.state_in,
       a.idx, a.d.num_slots, a.slot_stride, a.state_out, (T*)a.y, a.carries, p,
       reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, wide16<T>(a, false), pipeline_wait_limit_ns());
@@ -926,10 +1127,10 @@ cudaError_t run_back(const GatedArgs& a, cudaStream_t st) {
   if (l.tiles > 0) {
     const Plan p = plan_of(l, a.ws);
     auto* kernel = gated_back_kernel<T, V, kGate, kBackRows>;
-    const int bytes = 2 * (kGate ? 4 : 3) * kBackRows * kThreads * (int)sizeof(T) * V;
+    const int bytes = kBackRows * kThreads * V * (((kGate ? 4 : 3) + 4) * (int)sizeof(T) + 8);
     unsigned grid;
-    if ((e = stay(kernel, p, bytes, &grid)) != cudaSuccess) return e;
-    kernel<<<grid, kThreads, bytes, st>>>(
+    if ((e = stay(kernel, p, kBackCtas, bytes, &grid)) != cudaSuccess) return e;
+    kernel<<<grid, kAll, bytes, st>>>(
         (const T*)a.dy, a.dy_pitch, (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i,
         a.d.i_pitch, a.a_log, a.carries, a.state_in, a.dfinal, (T*)a.dx, (T*)a.dr, (T*)a.di, a.dstate, part, p,
         reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, wide16<T>(a, true),

@@ -532,7 +532,7 @@ def ssm_decode_draft(x, dt, A_log, B, C, cu_seqlens, pool, state_indices=None, *
 
 # ------------------------------------------------------------------------ gated linear recurrence
 
-CARRY_ROWS = 64  # KDA_GATED_CARRY_ROWS
+CARRY_ROWS = 48  # KDA_GATED_CARRY_ROWS
 
 
 def check_gated_args(x, r, A_log, *, i=None, cu_seqlens=None, state=None, state_indices=None,
@@ -581,7 +581,7 @@ def gated_scan(x, r, A_log, cu_seqlens, *, i=None, state=None, state_indices=Non
 
     x, r and i [T, Ch] bf16 or fp32 (one dtype), their rows at any pitch; i None: x enters whole; A_log
     [Ch] fp32; cu_seqlens [N+1] int32.  States are [Ch] fp32; pool and dense mode as in
-    :func:`causal_conv`.  ``carries`` [ceil(T / 64), Ch] fp32 is what :func:`gated_scan_backward` wants of
+    :func:`causal_conv`.  ``carries`` [ceil(T / 48), Ch] fp32 is what :func:`gated_scan_backward` wants of
     the forward pass.
     """
     N, T, ch, pitches = check_gated_args(
