@@ -32,6 +32,8 @@
 //
 // The backward pass runs over the tiles from the last to the first, e in the place of h. It needs
 // h_{t-1} as well; the forward pass left the state before each kCarryRows rows for it.
+#include <cudaTypedefs.h>
+
 #include <type_traits>
 
 #include "kda_internal.cuh"
@@ -49,6 +51,7 @@ constexpr int kGroup = 16;
 constexpr int kPlanRows = 1024;   // rows a block of the planning kernel
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kUnset = 0xffffffffu;
+constexpr int kInfos = 8;         // tiles of a CTA from the ones taken ahead back to the one whose sums are added up
 
 // Workspace behind the header: each tile's (A, H) and each group's (state, tag) of all channels, which the
 // planning kernel sets to kUnset; the sequence of each row; the backward pass's parts of dA_log.
@@ -357,7 +360,7 @@ struct Info {
 template <int V> struct Shared {
   Ch<V> a[2][kWarps][32], h[2][kWarps][32];   // each warp's run of tile n & 1, in the order of the pass
   Ch<V> carry[2][kWarps][32];                 // the state that reaches it
-  Info info[4];                               // of tile n & 3
+  Info info[kInfos];                          // of tile n % kInfos
   uint64_t full;                              // the next tile's rows are there
 };
 enum : uint32_t { kRan = 1, kCarried = 3 };   // named barriers, two each, by n & 1
@@ -369,39 +372,57 @@ __device__ __forceinline__ void bar_sync(uint32_t id) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kAll) : "memory");
 }
 
-// The next tile by the counter, into info[n & 3] (one warp).
-template <int V, int S, bool kBack>
-__device__ __forceinline__ void take(Shared<V>& s, int n, const Plan& p, WsHeader* hdr, int64_t total, int ch, int lane) {
-  constexpr int kRowsTile = kWarps * S;
-  uint32_t item = 0;
-  if (lane == 0) item = atomicAdd(&hdr->next_item, 1u);
-  item = __shfl_sync(0xffffffffu, item, 0);
-  Info o;
-  o.t0 = -1;
-  o.pos = item / p.blocks;
-  o.c0 = (int)(item % p.blocks) * 32 * V;
-  o.plain = 0;
-  if (item < p.items) {
-    o.t0 = (kBack ? p.tiles - 1 - o.pos : o.pos) * kRowsTile;
-    const int own = p.seq[o.t0];
-    bool same = own >= 0 && o.c0 + 32 * V <= ch && o.t0 > 0 && o.t0 + kRowsTile < total;
-    if (same) {
-#pragma unroll
-      for (int j = 0; j < kRowsTile + 2; j += 32)
-        if (j + lane < kRowsTile + 2) same = same && p.seq[o.t0 - 1 + j + lane] == own;
-    }
-    o.plain = __all_sync(0xffffffffu, same);
+// The warp that takes tiles: the counter and the rows' sequences are asked for ahead of where they are needed.
+template <int V, int S, bool kBack> struct Taker {
+  static constexpr int kRowsTile = kWarps * S, kLoads = (kRowsTile + 2 + 31) / 32;
+  uint32_t item, next;
+  int seq[kLoads];
+  __device__ __forceinline__ int64_t first_row(const Plan& p) const {
+    const int64_t pos = item / p.blocks;
+    return (kBack ? p.tiles - 1 - pos : pos) * kRowsTile;
   }
-  if (lane == 0) s.info[n & 3] = o;
-  __syncwarp();
-}
+  __device__ __forceinline__ void start(WsHeader* hdr, int lane) {
+    next = lane == 0 ? atomicAdd(&hdr->next_item, 1u) : 0u;
+  }
+  // the next tile, and the sequences of its rows and of one on either side, on their way
+  __device__ __forceinline__ void ask(const Plan& p, WsHeader* hdr, int64_t total, int lane) {
+    item = __shfl_sync(0xffffffffu, next, 0);
+    next = lane == 0 ? atomicAdd(&hdr->next_item, 1u) : 0u;
+    if (item >= p.items) return;
+    const int64_t t0 = first_row(p) - 1 + lane;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int64_t t = t0 + j * 32;
+      seq[j] = -1;
+      if (j * 32 + lane >= kRowsTile + 2) seq[j] = -2;    // none of the rows asked for
+      else if (t >= 0 && t < total) seq[j] = p.seq[t];
+    }
+  }
+  __device__ __forceinline__ void tell_all(Info& to, const Plan& p, int64_t total, int ch, int lane) const {
+    Info o;
+    o.t0 = -1;
+    o.pos = item / p.blocks;
+    o.c0 = (int)(item % p.blocks) * 32 * V;
+    o.plain = 0;
+    if (item < p.items) {
+      o.t0 = first_row(p);
+      const int own = __shfl_sync(0xffffffffu, seq[0], 0);
+      bool same = own >= 0 && o.c0 + 32 * V <= ch;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) same = same && (seq[j] == own || seq[j] == -2);
+      o.plain = __all_sync(0xffffffffu, same);
+    }
+    if (lane == 0) to = o;
+    __syncwarp();
+  }
+};
 
 // Step 2 of a tile (one warp): its run for the tiles after it, and the state that reaches each of its warps.
 template <int V>
 __device__ __forceinline__ void carry_over(Shared<V>& s, int n, const Plan& p, int ch, int lane, WsHeader* hdr,
                                            uint64_t limit_ns) {
-  const int64_t pos = s.info[n & 3].pos, g = pos / kGroup;
-  const int c = s.info[n & 3].c0 + lane * V, before = (int)(pos % kGroup);
+  const int64_t pos = s.info[n % kInfos].pos, g = pos / kGroup;
+  const int c = s.info[n % kInfos].c0 + lane * V, before = (int)(pos % kGroup);
   const bool in = c < ch, more = pos + 1 < p.tiles;
   const Ch<V>(*ra)[32] = s.a[n & 1], (*rh)[32] = s.h[n & 1];
   if (before < kGroup - 1 && more) {
@@ -420,33 +441,30 @@ __device__ __forceinline__ void carry_over(Shared<V>& s, int n, const Plan& p, i
   }
   Ch<V> h = all<V>(0.f);
   const float *at = p.agg + (g * kGroup * ch + c) * 2, *at_start = p.group + (g * ch + c) * 2;
-  constexpr int kHalf = kGroup / 2;
-#pragma unroll 1
-  for (int j0 = 0; j0 < kGroup; j0 += kHalf) {
-    const bool start = j0 == 0 && g > 0;
-    if (!start && j0 >= before) break;
-    Pair<V> t[kHalf], u;
-    Patience wait;
-    for (;;) {               // all of them at once, until all are there
-      bool ok = true;
-      if (start && in) ok = hear(at_start, u);
+  // all of them at once, then those that were not there, until all are
+  Pair<V> t[kGroup - 1], u;
+  uint32_t need = (1u << before) - 1 | (g > 0 ? 1u << (kGroup - 1) : 0u);
+  Patience wait;
+  while (need) {
+    uint32_t not_yet = 0;
 #pragma unroll
-      for (int j = 0; j < kHalf; ++j)
-        if (j0 + j < before && in) ok &= hear(at + (int64_t)(j0 + j) * ch * 2, t[j]);
-      if (__all_sync(0xffffffffu, ok) || !wait.more(hdr, limit_ns)) break;
-    }
-    if (start) {
+    for (int j = 0; j < kGroup - 1; ++j)
+      if (((need >> j) & 1) && in && !hear(at + (int64_t)j * ch * 2, t[j])) not_yet |= 1u << j;
+    if ((need >> (kGroup - 1)) && in && !hear(at_start, u)) not_yet |= 1u << (kGroup - 1);
+    need = __reduce_or_sync(0xffffffffu, not_yet);
+    if (need && !wait.more(hdr, limit_ns)) break;
+  }
+  if (g > 0) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) h.f[i] = u.h[i];
-    }
+    for (int i = 0; i < V; ++i) h.f[i] = u.h[i];
+  }
 #pragma unroll
-    for (int j = 0; j < kHalf; ++j) {
-      if (j0 + j >= before) continue;
-      Ch<V> A, H;
+  for (int j = 0; j < kGroup - 1; ++j) {
+    if (j >= before) continue;
+    Ch<V> A, H;
 #pragma unroll
-      for (int i = 0; i < V; ++i) A.f[i] = t[j].a[i], H.f[i] = t[j].h[i];
-      fold(h, A, H);
-    }
+    for (int i = 0; i < V; ++i) A.f[i] = t[j].a[i], H.f[i] = t[j].h[i];
+    fold(h, A, H);
   }
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
@@ -479,30 +497,10 @@ __device__ __forceinline__ Rows rows_of(const int32_t* seq, int64_t t0, int64_t 
   return r;
 }
 
-// Rows of one input on their way into shared memory, [row][lane], zeros where there is nothing.  Where rows
-// allow, the whole tile's by one warp, 16 bytes a copy; else a warp's own S rows, a lane its own elements.
-template <typename T, int V, int R>
-__device__ __forceinline__ void fetch_tile(void* to, const T* p, int64_t pitch, int64_t t0, int64_t total, int c0, int ch,
-                                           int lane) {
-  constexpr int kRow = 32 * V * (int)sizeof(T), kChunks = kRow / 16, kAtOnce = 32 / kChunks;
-  static_assert(R % kAtOnce == 0, "whole copies");
-  const int c = c0 + lane % kChunks * (16 / (int)sizeof(T));
-  const int left = c < ch ? (int)(total - t0 < R ? total - t0 : R) - lane / kChunks : 0;   // rows from this lane's first
-  uint32_t dst = tc::smem_u32(to) + lane * 16;
-  const T* src = p + (t0 + lane / kChunks) * pitch + c;
-  const int64_t step = kAtOnce * pitch;
-#pragma unroll 8
-  for (int j = 0; j < R; j += kAtOnce) {
-    const bool ok = j < left;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(ok ? src : p), "r"(ok ? 16 : 0)
-                 : "memory");
-    dst += 512;
-    src += step;
-  }
-}
-__device__ __forceinline__ void fetched(uint64_t* full) {   // arrives when this lane's copies are done
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(full)) : "memory");
-}
+// Rows of the inputs on their way into shared memory, [row][lane], zeros where there is nothing: where rows
+// allow, a tile of each by TMA; else a warp's own S rows, a lane its own elements. (Rows as bulk copies of their
+// own, 288 of 128 bytes a tile, took 10 us a tile.)
+struct Maps { CUtensorMap m[4]; };
 template <typename T, int V, int S>
 __device__ __forceinline__ void fetch_own(typename Pack<T, V>::Raw* to, const T* p, int64_t pitch, int64_t t0,
                                           int64_t total, int c, int ch, int lane) {
@@ -528,7 +526,7 @@ __device__ __forceinline__ void fetch_own_done() {
 // ---- forward --------------------------------------------------------------------------------
 template <typename T, int V, bool kGate, int S>
 __global__ void __launch_bounds__(kAll, kScanCtas)
-gated_scan_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict__ r, int64_t r_pitch,
+gated_scan_kernel(const __grid_constant__ Maps maps, const T* __restrict__ x, int64_t x_pitch, const T* __restrict__ r, int64_t r_pitch,
                   const T* __restrict__ ig, int64_t i_pitch, const float* __restrict__ a_log,
                   const float* state, const int32_t* __restrict__ idx, int64_t num_slots, int64_t stride,
                   float* final_state, T* __restrict__ y, float* __restrict__ carries, Plan plan, WsHeader* hdr,
@@ -538,41 +536,46 @@ gated_scan_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
   using P = Pack<T, V>;
   using Raw = typename P::Raw;
   using Kept = typename std::conditional<V == 2, float4, float2>::type;
-  extern __shared__ __align__(128) uint8_t s_raw[];   // [input][row][lane], then a and m u of the tile before
+  extern __shared__ __align__(1024) uint8_t s_raw[];   // [input][row][lane], then a and m u of the tile before
   __shared__ Shared<V> s;
   Raw* const raw = reinterpret_cast<Raw*>(s_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
-    tc::mbar_init(&s.full, 32);
+    tc::mbar_init(&s.full, 1);
     tc::fence_mbar_init();
   }
+  Taker<V, S, false> taker;
   if (warp == kWarps) {
-    take<V, S, false>(s, 0, plan, hdr, total, ch, lane);
-    take<V, S, false>(s, 1, plan, hdr, total, ch, lane);
+    taker.start(hdr, lane);
+    for (int n = 0; n < 2; ++n) {
+      taker.ask(plan, hdr, total, lane);
+      taker.tell_all(s.info[n], plan, total, ch, lane);
+    }
+    taker.ask(plan, hdr, total, lane);
   }
   __syncthreads();
 
   if (warp == kWarps) {   // this warp takes tiles and fetches their rows
     auto fetch = [&](int n) {
-      const Info& o = s.info[n & 3];
-      if (!wide || o.t0 < 0) return;
-      fetch_tile<T, V, kRowsTile>(raw, x, x_pitch, o.t0, total, o.c0, ch, lane);
-      fetch_tile<T, V, kRowsTile>(raw + kRowsTile * 32, r, r_pitch, o.t0, total, o.c0, ch, lane);
-      if (kGate) fetch_tile<T, V, kRowsTile>(raw + 2 * kRowsTile * 32, ig, i_pitch, o.t0, total, o.c0, ch, lane);
-      fetched(&s.full);
+      const Info& o = s.info[n % kInfos];
+      if (!wide || o.t0 < 0 || lane != 0) return;
+      tc::mbar_expect_tx(&s.full, kInputs * kRowsTile * 32 * (uint32_t)sizeof(Raw));
+#pragma unroll
+      for (int q = 0; q < kInputs; ++q) tc::tma_load_2d(raw + q * kRowsTile * 32, &maps.m[q], &s.full, o.c0, (int)o.t0);
     };
     fetch(0);
-    for (int n = 0; s.info[n & 3].t0 >= 0; ++n) {
+    for (int n = 0; s.info[n % kInfos].t0 >= 0; ++n) {
+      taker.tell_all(s.info[(n + 2) % kInfos], plan, total, ch, lane);
+      taker.ask(plan, hdr, total, lane);
       bar_sync(kRan + (n & 1));
       fetch(n + 1);
-      take<V, S, false>(s, n + 2, plan, hdr, total, ch, lane);
       bar_arrive(kCarried + (n & 1));
     }
     return;
   }
   if (warp > kWarps) {    // and this one carries the state
-    for (int n = 0; s.info[n & 3].t0 >= 0; ++n) {
+    for (int n = 0; s.info[n % kInfos].t0 >= 0; ++n) {
       bar_sync(kRan + (n & 1));
       carry_over(s, n, plan, ch, lane, hdr, limit_ns);
       bar_arrive(kCarried + (n & 1));
@@ -583,7 +586,7 @@ gated_scan_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
   const Raw* const mine = raw + warp * S * 32 + lane;
   Kept* const kept = reinterpret_cast<Kept*>(s_raw + kInputs * kRowsTile * 32 * sizeof(Raw)) + warp * S * 32 + lane;
   auto fetch = [&](int n) {   // where the other warp does not
-    const Info& o = s.info[n & 3];
+    const Info& o = s.info[n % kInfos];
     if (wide || o.t0 < 0) return;
     const int64_t t0 = o.t0 + warp * S;
     const int c = o.c0 + lane * V;
@@ -599,7 +602,7 @@ gated_scan_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
   };
   // step 3 of tile n
   auto finish = [&](int n) {
-    const Info& o = s.info[n & 3];
+    const Info& o = s.info[n % kInfos];
     const int64_t t0 = o.t0 + warp * S;
     const int c = o.c0 + lane * V;
     const bool in = c < ch;
@@ -638,8 +641,8 @@ gated_scan_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
 
   fetch(0);
   int n = 0;
-  for (; s.info[n & 3].t0 >= 0; ++n) {
-    const Info& o = s.info[n & 3];
+  for (; s.info[n % kInfos].t0 >= 0; ++n) {
+    const Info& o = s.info[n % kInfos];
     const int c = o.c0 + lane * V;
     Ch<V> rate;
 #pragma unroll
@@ -713,7 +716,7 @@ template <int V> struct BackShared : Shared<V> {
 
 template <typename T, int V, bool kGate, int S>
 __global__ void __launch_bounds__(kAll, kBackCtas)
-gated_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict__ x, int64_t x_pitch,
+gated_back_kernel(const __grid_constant__ Maps maps, const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict__ x, int64_t x_pitch,
                   const T* __restrict__ r, int64_t r_pitch, const T* __restrict__ ig, int64_t i_pitch,
                   const float* __restrict__ a_log, const float* __restrict__ carries,
                   const float* __restrict__ state, const float* __restrict__ dfinal, T* __restrict__ dx,
@@ -726,46 +729,50 @@ gated_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restric
   using Raw = typename P::Raw;
   struct alignas(4 * sizeof(Raw)) Row4 { Raw x, r, g, i; };
   using Kept = typename std::conditional<V == 2, float4, float2>::type;
-  extern __shared__ __align__(128) uint8_t s_raw[];   // [input][row][lane], then what is kept of the tile before
+  extern __shared__ __align__(1024) uint8_t s_raw[];   // [input][row][lane], then what is kept of the tile before
   __shared__ BackShared<V> s;
   Raw* const raw = reinterpret_cast<Raw*>(s_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
-    tc::mbar_init(&s.full, 32);
+    tc::mbar_init(&s.full, 1);
     tc::fence_mbar_init();
   }
+  Taker<V, S, true> taker;
   if (warp == kWarps) {
-    take<V, S, true>(s, 0, plan, hdr, total, ch, lane);
-    take<V, S, true>(s, 1, plan, hdr, total, ch, lane);
+    taker.start(hdr, lane);
+    for (int n = 0; n < 2; ++n) {
+      taker.ask(plan, hdr, total, lane);
+      taker.tell_all(s.info[n], plan, total, ch, lane);
+    }
+    taker.ask(plan, hdr, total, lane);
   }
   __syncthreads();
 
   if (warp == kWarps) {   // this warp takes tiles and fetches their rows
     auto fetch = [&](int n) {
-      const Info& o = s.info[n & 3];
-      if (!wide || o.t0 < 0) return;
-      fetch_tile<T, V, kRowsTile>(raw, x, x_pitch, o.t0, total, o.c0, ch, lane);
-      fetch_tile<T, V, kRowsTile>(raw + kRowsTile * 32, r, r_pitch, o.t0, total, o.c0, ch, lane);
-      fetch_tile<T, V, kRowsTile>(raw + 2 * kRowsTile * 32, dy, dy_pitch, o.t0, total, o.c0, ch, lane);
-      if (kGate) fetch_tile<T, V, kRowsTile>(raw + 3 * kRowsTile * 32, ig, i_pitch, o.t0, total, o.c0, ch, lane);
-      fetched(&s.full);
+      const Info& o = s.info[n % kInfos];
+      if (!wide || o.t0 < 0 || lane != 0) return;
+      tc::mbar_expect_tx(&s.full, kInputs * kRowsTile * 32 * (uint32_t)sizeof(Raw));
+#pragma unroll
+      for (int q = 0; q < kInputs; ++q) tc::tma_load_2d(raw + q * kRowsTile * 32, &maps.m[q], &s.full, o.c0, (int)o.t0);
     };
     auto add_up = [&](int n) {   // dA_log's part of tile n, which all warps are done with
       if (n < 0) return;
-      const int c = s.info[n & 3].c0 + lane * V;
+      const int c = s.info[n % kInfos].c0 + lane * V;
       Ch<V> sum = s.sum[n & 1][0][lane];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) sum = add(sum, s.sum[n & 1][w][lane]);
-      if (c < ch) store<float, V>(part + s.info[n & 3].t0 / kRowsTile * ch + c, sum);
+      if (c < ch) store<float, V>(part + s.info[n % kInfos].t0 / kRowsTile * ch + c, sum);
     };
     fetch(0);
     int n = 0;
-    for (; s.info[n & 3].t0 >= 0; ++n) {
+    for (; s.info[n % kInfos].t0 >= 0; ++n) {
+      taker.tell_all(s.info[(n + 2) % kInfos], plan, total, ch, lane);
+      taker.ask(plan, hdr, total, lane);
       bar_sync(kRan + (n & 1));
       fetch(n + 1);
       add_up(n - 2);
-      take<V, S, true>(s, n + 2, plan, hdr, total, ch, lane);
       bar_arrive(kCarried + (n & 1));
     }
     bar_sync(kRan + (n & 1));
@@ -775,10 +782,10 @@ gated_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restric
   }
   if (warp > kWarps) {    // and this one carries state and e
     int n = 0;
-    for (; s.info[n & 3].t0 >= 0; ++n) {
-      const int c = s.info[n & 3].c0 + lane * V;
+    for (; s.info[n % kInfos].t0 >= 0; ++n) {
+      const int c = s.info[n % kInfos].c0 + lane * V;
       Ch<V> h = all<V>(0.f);
-      if (c < ch) h = Pack<float, V>::open(load<float, V>(carries + s.info[n & 3].t0 / kRowsTile * ch + c));
+      if (c < ch) h = Pack<float, V>::open(load<float, V>(carries + s.info[n % kInfos].t0 / kRowsTile * ch + c));
       bar_sync(kRan + (n & 1));
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
@@ -798,7 +805,7 @@ gated_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restric
                           warp * S * 32 + lane;
   const int rank = kWarps - 1 - warp;
   auto fetch = [&](int n) {   // where the other warp does not
-    const Info& o = s.info[n & 3];
+    const Info& o = s.info[n % kInfos];
     if (wide || o.t0 < 0) return;
     const int64_t t0 = o.t0 + warp * S;
     const int c = o.c0 + lane * V;
@@ -817,7 +824,7 @@ gated_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restric
   };
   // step 3 of tile n, from its last row to its first
   auto finish = [&](int n) {
-    const Info& o = s.info[n & 3];
+    const Info& o = s.info[n % kInfos];
     const int64_t t0 = o.t0 + warp * S, at0 = t0 * ch + o.c0 + lane * V;
     const int c = o.c0 + lane * V;
     const bool in = c < ch;
@@ -912,8 +919,8 @@ gated_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restric
 
   fetch(0);
   int n = 0;
-  for (; s.info[n & 3].t0 >= 0; ++n) {
-    const Info& o = s.info[n & 3];
+  for (; s.info[n % kInfos].t0 >= 0; ++n) {
+    const Info& o = s.info[n % kInfos];
     const int c = o.c0 + lane * V;
     Ch<V> rate;
 #pragma unroll
@@ -1084,11 +1091,37 @@ cudaError_t launch_plan(const GatedArgs& a, const Layout& l, const float* from, 
   return cudaGetLastError();
 }
 
-// Whether rows can be fetched 16 bytes at a time.
-template <typename T> bool wide16(const GatedArgs& a, bool back) {
-  auto rows = [](const void* p, int64_t pitch) { return (uintptr_t)p % 16 == 0 && pitch * (int)sizeof(T) % 16 == 0; };
-  return a.d.channels * (int)sizeof(T) % 16 == 0 && rows(a.x, a.d.x_pitch) && rows(a.r, a.d.r_pitch) &&
-         (!a.i || rows(a.i, a.d.i_pitch)) && (!back || rows(a.dy, a.dy_pitch));
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// Maps of [T, ch] rows, boxes of `cols` channels x `rows`.  False where the rows allow none (TMA wants them
+// on 16-byte boundaries): the kernel then fetches them by elements.
+template <typename T>
+bool maps_of(Maps* m, const void* const* base, const int64_t* pitch, int count, int64_t total, int ch, int cols, int rows) {
+  auto enc = encoder();
+  if (!enc) return false;
+  for (int q = 0; q < count; ++q) {
+    if ((uintptr_t)base[q] % 16 != 0 || pitch[q] * (int64_t)sizeof(T) % 16 != 0) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)ch, (cuuint64_t)total};
+    cuuint64_t strides[1] = {(cuuint64_t)pitch[q] * sizeof(T)};
+    cuuint32_t box[2] = {(cuuint32_t)cols, (cuuint32_t)rows};
+    cuuint32_t es[2] = {1u, 1u};
+    if (enc(&m->m[q], sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+            const_cast<void*>(base[q]), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  }
+  return true;
 }
 
 // CTAs that stay: as many as fit, or one a tile.
@@ -1111,10 +1144,14 @@ cudaError_t run_scan(const GatedArgs& a, cudaStream_t st) {
   const int bytes = kRows * kThreads * V * ((kGate ? 3 : 2) * (int)sizeof(T) + 8);
   unsigned grid;
   if ((e = stay(kernel, p, kScanCtas, bytes, &grid)) != cudaSuccess) return e;
+  Maps maps;
+  const void* base[] = {a.x, a.r, a.i};
+  const int64_t pitch[] = {a.d.x_pitch, a.d.r_pitch, a.d.i_pitch};
+  const bool wide = maps_of<T>(&maps, base, pitch, kGate ? 3 : 2, a.d.total_tokens, a.d.channels, 32 * V, kRows * kWarps);
   kernel<<<grid, kAll, bytes, st>>>(
-      (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i, a.d.i_pitch, a.a_log, a.state_in,
+      maps, (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i, a.d.i_pitch, a.a_log, a.state_in,
       a.idx, a.d.num_slots, a.slot_stride, a.state_out, (T*)a.y, a.carries, p,
-      reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, wide16<T>(a, false), pipeline_wait_limit_ns());
+      reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, wide, pipeline_wait_limit_ns());
   return cudaGetLastError();
 }
 
@@ -1130,10 +1167,15 @@ cudaError_t run_back(const GatedArgs& a, cudaStream_t st) {
     const int bytes = kBackRows * kThreads * V * (((kGate ? 4 : 3) + 4) * (int)sizeof(T) + 8);
     unsigned grid;
     if ((e = stay(kernel, p, kBackCtas, bytes, &grid)) != cudaSuccess) return e;
+    Maps maps;
+    const void* base[] = {a.x, a.r, a.dy, a.i};
+    const int64_t pitch[] = {a.d.x_pitch, a.d.r_pitch, a.dy_pitch, a.d.i_pitch};
+    const bool wide = maps_of<T>(&maps, base, pitch, kGate ? 4 : 3, a.d.total_tokens, a.d.channels, 32 * V,
+                                 kBackRows * kWarps);
     kernel<<<grid, kAll, bytes, st>>>(
-        (const T*)a.dy, a.dy_pitch, (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i,
+        maps, (const T*)a.dy, a.dy_pitch, (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i,
         a.d.i_pitch, a.a_log, a.carries, a.state_in, a.dfinal, (T*)a.dx, (T*)a.dr, (T*)a.di, a.dstate, part, p,
-        reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, wide16<T>(a, true),
+        reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, wide,
         pipeline_wait_limit_ns());
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
