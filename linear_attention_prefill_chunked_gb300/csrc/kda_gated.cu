@@ -363,13 +363,16 @@ template <int V> struct Shared {
   Info info[kInfos];                          // of tile n % kInfos
   uint64_t full;                              // the next tile's rows are there
 };
-enum : uint32_t { kRan = 1, kCarried = 3 };   // named barriers, two each, by n & 1
+// Named barriers, two each, by n & 1: the warps' runs of a tile are there (for the warp that fetches), the
+// tile's run is published (for the one that carries), the state that reaches the warps is there (for them).
+enum : uint32_t { kRan = 1, kPublished = 3, kCarried = 5 };
 constexpr uint32_t kAll = kThreads + 64;   // with the warp that fetches and the one that carries
-__device__ __forceinline__ void bar_arrive(uint32_t id) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kAll) : "memory");
+constexpr uint32_t kMeet = kThreads + 32;    // the warps that run and one of the others
+__device__ __forceinline__ void bar_arrive(uint32_t id, uint32_t threads = kMeet) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-__device__ __forceinline__ void bar_sync(uint32_t id) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kAll) : "memory");
+__device__ __forceinline__ void bar_sync(uint32_t id, uint32_t threads = kMeet) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // The warp that takes tiles: the counter and the rows' sequences are asked for ahead of where they are needed.
@@ -417,67 +420,87 @@ template <int V, int S, bool kBack> struct Taker {
   }
 };
 
-// Step 2 of a tile (one warp): its run for the tiles after it, and the state that reaches each of its warps.
+// Step 2 of a tile: its run for the tiles after it (one warp),
 template <int V>
-__device__ __forceinline__ void carry_over(Shared<V>& s, int n, const Plan& p, int ch, int lane, WsHeader* hdr,
-                                           uint64_t limit_ns) {
-  const int64_t pos = s.info[n % kInfos].pos, g = pos / kGroup;
-  const int c = s.info[n % kInfos].c0 + lane * V, before = (int)(pos % kGroup);
-  const bool in = c < ch, more = pos + 1 < p.tiles;
+__device__ __forceinline__ void publish(const Shared<V>& s, int n, const Plan& p, int ch, int lane) {
+  const int64_t pos = s.info[n % kInfos].pos;
+  const int c = s.info[n % kInfos].c0 + lane * V;
+  if (pos % kGroup == kGroup - 1 || pos + 1 >= p.tiles) return;
   const Ch<V>(*ra)[32] = s.a[n & 1], (*rh)[32] = s.h[n & 1];
-  if (before < kGroup - 1 && more) {
-    Ch<V> A = ra[0][lane], H = rh[0][lane];
+  Ch<V> A = ra[0][lane], H = rh[0][lane];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) join(A, H, ra[w][lane], rh[w][lane]);
-    if (in) {
-      Pair<V> o;
+  for (int w = 1; w < kWarps; ++w) join(A, H, ra[w][lane], rh[w][lane]);
+  if (c >= ch) return;
+  Pair<V> o;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        o.a[i] = A.f[i] != A.f[i] ? __uint_as_float(0x7fc00000u) : A.f[i];
-        o.h[i] = H.f[i];
-      }
-      tell(p.agg + (pos * ch + c) * 2, o);
-    }
+  for (int i = 0; i < V; ++i) {
+    o.a[i] = A.f[i] != A.f[i] ? __uint_as_float(0x7fc00000u) : A.f[i];
+    o.h[i] = H.f[i];
   }
-  Ch<V> h = all<V>(0.f);
-  const float *at = p.agg + (g * kGroup * ch + c) * 2, *at_start = p.group + (g * ch + c) * 2;
-  // all of them at once, then those that were not there, until all are
-  Pair<V> t[kGroup - 1], u;
-  uint32_t need = (1u << before) - 1 | (g > 0 ? 1u << (kGroup - 1) : 0u);
-  Patience wait;
-  while (need) {
+  tell(p.agg + (pos * ch + c) * 2, o);
+}
+// and the state that reaches each of its warps (another). What is there already of the tiles before it is asked
+// for while its warps still run.
+template <int V> struct Carrier {
+  int64_t pos, g;
+  int c, before;
+  bool in;
+  const float *at, *at_start;
+  int64_t step;
+  uint32_t need;                    // tiles of the group, and its start, that were not there yet
+  Pair<V> t[kGroup - 1], start;
+
+  __device__ __forceinline__ void ask() {   // all at once
     uint32_t not_yet = 0;
 #pragma unroll
     for (int j = 0; j < kGroup - 1; ++j)
-      if (((need >> j) & 1) && in && !hear(at + (int64_t)j * ch * 2, t[j])) not_yet |= 1u << j;
-    if ((need >> (kGroup - 1)) && in && !hear(at_start, u)) not_yet |= 1u << (kGroup - 1);
+      if (((need >> j) & 1) && in && !hear(at + j * step, t[j])) not_yet |= 1u << j;
+    if ((need >> (kGroup - 1)) && in && !hear(at_start, start)) not_yet |= 1u << (kGroup - 1);
     need = __reduce_or_sync(0xffffffffu, not_yet);
-    if (need && !wait.more(hdr, limit_ns)) break;
   }
-  if (g > 0) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) h.f[i] = u.h[i];
+  __device__ __forceinline__ void begin(const Info& o, const Plan& p, int ch, int lane) {
+    pos = o.pos;
+    g = pos / kGroup;
+    c = o.c0 + lane * V;
+    before = (int)(pos % kGroup);
+    in = c < ch;
+    at = p.agg + (g * kGroup * ch + c) * 2;
+    at_start = p.group + (g * ch + c) * 2;
+    step = (int64_t)ch * 2;
+    need = (1u << before) - 1 | (g > 0 ? 1u << (kGroup - 1) : 0u);
+    ask();
   }
+  __device__ __forceinline__ void end(Shared<V>& s, int n, const Plan& p, int ch, int lane, WsHeader* hdr,
+                                      uint64_t limit_ns) {
+    const Ch<V>(*ra)[32] = s.a[n & 1], (*rh)[32] = s.h[n & 1];
+    Patience wait;
+    while (need && wait.more(hdr, limit_ns)) ask();
+    Ch<V> h = all<V>(0.f);
+    if (g > 0) {
 #pragma unroll
-  for (int j = 0; j < kGroup - 1; ++j) {
-    if (j >= before) continue;
-    Ch<V> A, H;
+      for (int i = 0; i < V; ++i) h.f[i] = start.h[i];
+    }
 #pragma unroll
-    for (int i = 0; i < V; ++i) A.f[i] = t[j].a[i], H.f[i] = t[j].h[i];
-    fold(h, A, H);
+    for (int j = 0; j < kGroup - 1; ++j) {
+      if (j >= before) continue;
+      Ch<V> A, H;
+#pragma unroll
+      for (int i = 0; i < V; ++i) A.f[i] = t[j].a[i], H.f[i] = t[j].h[i];
+      fold(h, A, H);
+    }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      s.carry[n & 1][w][lane] = h;
+      fold(h, ra[w][lane], rh[w][lane]);
+    }
+    if (before == kGroup - 1 && pos + 1 < p.tiles && in) {  // the next group's start
+      Pair<V> o;
+#pragma unroll
+      for (int i = 0; i < V; ++i) o.a[i] = 1.f, o.h[i] = h.f[i];
+      tell(p.group + ((g + 1) * ch + c) * 2, o);
+    }
   }
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    s.carry[n & 1][w][lane] = h;
-    fold(h, ra[w][lane], rh[w][lane]);
-  }
-  if (before == kGroup - 1 && more && in) {  // the next group's start
-    Pair<V> o;
-#pragma unroll
-    for (int i = 0; i < V; ++i) o.a[i] = 1.f, o.h[i] = h.f[i];
-    tell(p.group + ((g + 1) * ch + c) * 2, o);
-  }
-}
+};
 
 // Bits of a warp's S rows: valid ones, first and last ones of a sequence; lane j holds row j's sequence.
 struct Rows {
@@ -570,14 +593,17 @@ gated_scan_kernel(const __grid_constant__ Maps maps, const T* __restrict__ x, in
       taker.ask(plan, hdr, total, lane);
       bar_sync(kRan + (n & 1));
       fetch(n + 1);
-      bar_arrive(kCarried + (n & 1));
+      publish(s, n, plan, ch, lane);
+      bar_arrive(kPublished + (n & 1), 64);
     }
     return;
   }
   if (warp > kWarps) {    // and this one carries the state
+    Carrier<V> carrier;
     for (int n = 0; s.info[n % kInfos].t0 >= 0; ++n) {
-      bar_sync(kRan + (n & 1));
-      carry_over(s, n, plan, ch, lane, hdr, limit_ns);
+      carrier.begin(s.info[n % kInfos], plan, ch, lane);
+      bar_sync(kPublished + (n & 1), 64);
+      carrier.end(s, n, plan, ch, lane, hdr, limit_ns);
       bar_arrive(kCarried + (n & 1));
     }
     return;
@@ -772,8 +798,9 @@ gated_back_kernel(const __grid_constant__ Maps maps, const T* __restrict__ dy, i
       taker.ask(plan, hdr, total, lane);
       bar_sync(kRan + (n & 1));
       fetch(n + 1);
+      publish<V>(s, n, plan, ch, lane);
       add_up(n - 2);
-      bar_arrive(kCarried + (n & 1));
+      bar_arrive(kPublished + (n & 1), 64);
     }
     bar_sync(kRan + (n & 1));
     add_up(n - 2);
@@ -781,21 +808,22 @@ gated_back_kernel(const __grid_constant__ Maps maps, const T* __restrict__ dy, i
     return;
   }
   if (warp > kWarps) {    // and this one carries state and e
+    Carrier<V> carrier;
     int n = 0;
     for (; s.info[n % kInfos].t0 >= 0; ++n) {
       const int c = s.info[n % kInfos].c0 + lane * V;
       Ch<V> h = all<V>(0.f);
       if (c < ch) h = Pack<float, V>::open(load<float, V>(carries + s.info[n % kInfos].t0 / kRowsTile * ch + c));
-      bar_sync(kRan + (n & 1));
+      carrier.begin(s.info[n % kInfos], plan, ch, lane);
+      bar_sync(kPublished + (n & 1), 64);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         s.state[n & 1][w][lane] = h;
         fold(h, s.fa[n & 1][w][lane], s.fh[n & 1][w][lane]);
       }
-      carry_over<V>(s, n, plan, ch, lane, hdr, limit_ns);
+      carrier.end(s, n, plan, ch, lane, hdr, limit_ns);
       bar_arrive(kCarried + (n & 1));
     }
-    bar_arrive(kRan + (n & 1));
     return;
   }
 
