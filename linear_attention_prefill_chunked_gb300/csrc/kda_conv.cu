@@ -370,11 +370,49 @@ conv_token_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
 // in a fixed order.
 constexpr int kBackStrips = 8;
 
-// act'(z): of z sigmoid(z) it is sigmoid(z) (1 + z (1 - sigmoid(z))).
-template <typename T> __device__ __forceinline__ float silu_slope(float z) {
-  const float e = sizeof(T) == 2 ? __expf(-z) : expf(-z);
-  const float s = sizeof(T) == 2 ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e);
-  return s * fmaf(z, 1.f - s, 1.f);
+// g *= act'(z): of z sigmoid(z) it is s + s (z - z s), s = sigmoid(z).
+template <typename T, int VEC> __device__ __forceinline__ void silu_slope(const float (&z)[VEC], float (&g)[VEC]) {
+  float s[VEC], q[VEC];
+  if constexpr (sizeof(T) == 2 && VEC == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      s[i] = z[i];
+      s[i + 1] = z[i + 1];
+      mul2(s[i], s[i + 1], -1.4426950408889634f, -1.4426950408889634f);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(s[i]));
+    add2(s[0], s[1], 1.f, 1.f);
+    add2(s[2], s[3], 1.f, 1.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s[i]));
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      float m = z[i], n = z[i + 1];
+      mul2(m, n, s[i], s[i + 1]);
+      q[i] = z[i];
+      q[i + 1] = z[i + 1];
+      sub2(q[i], q[i + 1], m, n);
+      fma2(q[i], q[i + 1], s[i], s[i + 1], s[i], s[i + 1]);
+      mul2(g[i], g[i + 1], q[i], q[i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const float e = sizeof(T) == 2 ? __expf(-z[i]) : expf(-z[i]);
+      s[i] = sizeof(T) == 2 ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e);
+      g[i] *= fmaf(z[i] - z[i] * s[i], s[i], s[i]);
+    }
+  }
+}
+// a += x * y
+template <int VEC> __device__ __forceinline__ void acc(float (&a)[VEC], const float (&x)[VEC], const float (&y)[VEC]) {
+  if constexpr (VEC == 4) {
+    acc2(a[0], a[1], x[0], x[1], y[0], y[1]);
+    acc2(a[2], a[3], x[2], x[3], y[2], y[3]);
+  } else {
+    a[0] = fmaf(x[0], y[0], a[0]);
+  }
 }
 
 template <typename T, int VEC, int W, int kStrip>
@@ -453,9 +491,94 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
 #pragma unroll
     for (int e = 0; e < VEC; ++e) ds[j][e] = 0.f;
   }
+  // A strip inside one sequence, with the W-1 tokens before and behind it (nearly all of a long sequence): no
+  // state, no end, so the windows rotate in registers over unrolled tokens.
+  const int n0 = s_seq[s0];
+  const bool inside = in && n0 >= 0 && s_seq[s0 + kStrip + H - 1] == n0 && t0 + s0 - s_bos[s0] >= H;
+  if (inside) {
+    constexpr int kAhead = 4;
+    const T *xp = x + (t0 + s0) * x_pitch + c, *gp = dy + (t0 + s0) * dy_pitch + c;
+    T* op = dx + (t0 + s0) * ch + c;
+#pragma unroll
+    for (int j = 0; j < H; ++j) R::unpack(R::load(xp + (j - H) * x_pitch), win[j + 1]);
+    typename R::Raw nx[kAhead], ng[kAhead];
+    auto ahead = [&](int rows) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (u < rows) {
+          nx[u] = R::load(xp);
+          ng[u] = R::load(gp);
+          xp += x_pitch;
+          gp += dy_pitch;
+        }
+      }
+    };
+    auto token = [&](const typename R::Raw& xr, const typename R::Raw& gr, bool sums, bool out) {
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          win[j][e] = win[j + 1][e];
+          dz[j][e] = dz[j + 1][e];
+        }
+      }
+      R::unpack(xr, win[H]);
+      R::unpack(gr, dz[H]);
+      if (act) {
+        float z[VEC];
+        apply<T, VEC, W>(win, wt, bv, false, z);
+        silu_slope<T, VEC>(z, dz[H]);
+      }
+      if (sums) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc<VEC>(dw[j], dz[H], win[j]);
+        if constexpr (VEC == 4) {
+          add2(db[0], db[1], dz[H][0], dz[H][1]);
+          add2(db[2], db[3], dz[H][2], dz[H][3]);
+        } else {
+          db[0] += dz[H][0];
+        }
+      }
+      if (out) {
+        float o[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = 0.f;
+#pragma unroll
+        for (int d = 0; d < W; ++d) acc<VEC>(o, dz[d], wt[H - d]);
+        R::store(op, R::pack(o));
+        op += ch;
+      }
+    };
+    typename R::Raw cx[kAhead], cg[kAhead];
+    auto take = [&] {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        cx[u] = nx[u];
+        cg[u] = ng[u];
+      }
+    };
+    ahead(kAhead);
+    take();
+    ahead(kAhead);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) token(cx[u], cg[u], true, u >= H);
+#pragma unroll 1
+    for (int i0 = kAhead; i0 < kStrip - kAhead; i0 += kAhead) {
+      take();
+      ahead(kAhead);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) token(cx[u], cg[u], true, true);
+    }
+    take();
+    ahead(H);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) token(cx[u], cg[u], true, true);
+#pragma unroll
+    for (int u = 0; u < H; ++u) token(nx[u], ng[u], false, true);
+  }
   // Rows of dx are written when the W-1 tokens behind them have been seen.
 #pragma unroll 1
-  for (int i = 0; in && i < kStrip + H; ++i) {
+  for (int i = 0; in && !inside && i < kStrip + H; ++i) {
     const int r = s0 + i;
     const int64_t t = t0 + r;
     const int n = r < kSpan ? s_seq[r] : -1;
@@ -491,8 +614,7 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
       if (act) {
         float z[VEC];
         apply<T, VEC, W>(win, wt, bv, false, z);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) g[e] *= silu_slope<T>(z[e]);
+        silu_slope<T, VEC>(z, g);
       }
       if (i < kStrip) {
 #pragma unroll
@@ -663,9 +785,10 @@ cudaError_t by_type(const ConvArgs& a, cudaStream_t st, bool token) {
 }
 
 // Strips as in the forward pass.
+constexpr int kBackStrip = 32;
 int back_strip(const kda_conv_desc_t& d) {
-  const int64_t blocks = (d.total_tokens / (32 * kBackStrips)) * (d.channels / (kLanes * 4));
-  return blocks >= 4 * gpu_sms() ? 32 : 8;
+  const int64_t blocks = (d.total_tokens / (kBackStrip * kBackStrips)) * (d.channels / (kLanes * 4));
+  return blocks >= 4 * gpu_sms() ? kBackStrip : 8;
 }
 int64_t back_tiles(const kda_conv_desc_t& d) {
   const int64_t rows = (int64_t)back_strip(d) * kBackStrips, tiles = (d.total_tokens + rows - 1) / rows;
@@ -689,11 +812,11 @@ cudaError_t launch_back(const ConvBackArgs& a, cudaStream_t st) {
 
 template <typename T, int VEC>
 cudaError_t back_by_width(const ConvBackArgs& a, cudaStream_t st) {
-  const bool longer = back_strip(a.d) == 32;
+  const bool longer = back_strip(a.d) == kBackStrip;
   switch (a.d.width) {
-    case 2: return longer ? launch_back<T, VEC, 2, 32>(a, st) : launch_back<T, VEC, 2, 8>(a, st);
-    case 3: return longer ? launch_back<T, VEC, 3, 32>(a, st) : launch_back<T, VEC, 3, 8>(a, st);
-    default: return longer ? launch_back<T, VEC, 4, 32>(a, st) : launch_back<T, VEC, 4, 8>(a, st);
+    case 2: return longer ? launch_back<T, VEC, 2, kBackStrip>(a, st) : launch_back<T, VEC, 2, 8>(a, st);
+    case 3: return longer ? launch_back<T, VEC, 3, kBackStrip>(a, st) : launch_back<T, VEC, 3, 8>(a, st);
+    default: return longer ? launch_back<T, VEC, 4, kBackStrip>(a, st) : launch_back<T, VEC, 4, 8>(a, st);
   }
 }
 
