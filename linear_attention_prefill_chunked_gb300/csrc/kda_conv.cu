@@ -14,6 +14,7 @@
 // the thread whose strip holds a sequence's first token also takes those next W-2 tokens, reads
 // the initial state, and then writes the final one, so no other thread reads what it overwrites.
 #include "kda_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace kda {
 namespace {
@@ -363,12 +364,16 @@ conv_token_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
 //   by an input   sum over its taps of w_i dz_{t+(W-1)-i}, and the final state's derivative where it is one
 //                 of the last W-1 inputs
 //   by w_i        sum over the tokens of dz_t x_{t-(W-1)+i}        by the bias: sum of dz
-// Two rows are read and one is written a token, and z is formed again: bound by HBM. A thread walks a strip of
-// S tokens and the W-1 behind it (whose dz its last rows' derivatives need; they are the next strip's to
-// count in the sums), with the last W inputs and dz in registers. The sums by the weights stay in registers over
-// the strip, are added over the block's strips in shared memory, and over the blocks by a second kernel, each
-// in a fixed order.
-constexpr int kBackStrips = 8;
+// Two rows are read and one is written a token, and z is formed again: bound by HBM. A warp walks a long run of
+// the packed rows for its channels, four a lane, and the W-1 rows behind it (whose dz its last rows' derivatives
+// need; they are the next run's to count in the sums), with the last W inputs and dz in registers and the rows
+// ahead of it on their way into shared memory, each lane's own. The sums by the weights stay in
+// registers over the run, are added over a CTA's warps at its end, and over the CTAs by a second kernel, each
+// in a fixed order. Four rows at a time: where they, and W-1 on either side, are of one sequence, nothing is looked up;
+// else row by row. Which sequence a row belongs to is written down beforehand by a small kernel.
+constexpr int kBackWarps = 8;
+constexpr int kBackThreads = kBackWarps * 32;
+constexpr int kQuad = 4;
 
 // g *= act'(z): of z sigmoid(z) it is s + s (z - z s), s = sigmoid(z).
 template <typename T, int VEC> __device__ __forceinline__ void silu_slope(const float (&z)[VEC], float (&g)[VEC]) {
@@ -415,188 +420,111 @@ template <int VEC> __device__ __forceinline__ void acc(float (&a)[VEC], const fl
   }
 }
 
-template <typename T, int VEC, int W, int kStrip>
-__global__ void __launch_bounds__(kConvThreads, VEC == 1 ? 4 : 2)
-conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict__ x, int64_t x_pitch,
-                 const T* __restrict__ w, const T* __restrict__ bias, const int32_t* __restrict__ cu,
-                 const T* __restrict__ state, const T* __restrict__ dfinal, T* __restrict__ dx,
-                 T* __restrict__ dstate, float* __restrict__ part, uint32_t* __restrict__ status, int N,
-                 int64_t total, int ch, bool act) {
-  using R = Row<T, VEC>;
-  constexpr int H = W - 1;
-  constexpr int kTile = kStrip * kBackStrips;
-  constexpr int kSpan = kTile + H;
-  __shared__ int s_seq[kSpan];
-  __shared__ int64_t s_bos[kSpan];
-  __shared__ float s_sum[kBackStrips][kLanes * VEC];
-
-  const int tid = threadIdx.x;
-  const int64_t t0 = (int64_t)blockIdx.x * kTile;
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_all(status, cu, nullptr, N, total, total, 0);
-  for (int i = tid; i < kSpan; i += kConvThreads) s_seq[i] = -1;
-  __syncthreads();
-  for (int base = 0; base < N; base += kConvThreads) {
-    const int n = base + tid;
-    int64_t a = 0, b = 0;
-    const bool hit = n < N && seq_bounds(cu, n, total, &a, &b) && a < t0 + kSpan && b > t0;
-    unsigned m = __ballot_sync(0xffffffffu, hit);
-    while (m) {
-      const int src = __ffs(m) - 1;
-      m &= m - 1;
-      const int64_t sa = __shfl_sync(0xffffffffu, a, src), sb = __shfl_sync(0xffffffffu, b, src);
-      const int sn = __shfl_sync(0xffffffffu, n, src);
-      const int lo = (int)(sa > t0 ? sa - t0 : 0);
-      const int hi = (int)(sb < t0 + kSpan ? sb - t0 : kSpan);
-      for (int i = lo + (tid & 31); i < hi; i += 32) atomicMax(&s_seq[i], sn);
-    }
-  }
-  __syncthreads();
-  for (int i = tid; i < kSpan; i += kConvThreads) s_bos[i] = s_seq[i] < 0 ? 0 : (int64_t)cu[s_seq[i]];
-  __syncthreads();
-
-  const int c = (blockIdx.y * kLanes + tid % kLanes) * VEC;
-  const bool in = c < ch;
-  // the initial states' derivatives of sequences without tokens, and of invalid ones
-  if (dstate && in) {
-    for (int64_t n = blockIdx.x * (int64_t)kBackStrips + tid / kLanes; n < N;
-         n += gridDim.x * (int64_t)kBackStrips) {
-      int64_t a, b;
-      const bool ok = seq_bounds(cu, (int)n, total, &a, &b);
-      if (ok && a != b) continue;
-      for (int j = 0; j < H; ++j) {
-        const int64_t at = (n * H + j) * ch + c;
-        R::store(dstate + at, ok && dfinal ? R::load(dfinal + at) : R::zero());
+// Four rows of x and dy at p on their way to `to`, [row][x, dy][lane].
+template <typename T, int VEC>
+__device__ __forceinline__ void fetch_quad(typename Row<T, VEC>::Raw* to, const T* x, int64_t x_pitch, const T* dy,
+                                           int64_t dy_pitch, int64_t rows) {
+  using Raw = typename Row<T, VEC>::Raw;
+#pragma unroll
+  for (int u = 0; u < kQuad; ++u) {
+    const bool ok = u < rows;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const T* from = q ? dy + u * dy_pitch : x + u * x_pitch;
+      Raw* dst = to + (u * 2 + q) * 32;
+      if constexpr (sizeof(Raw) >= 4) {
+        if (ok)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_u32(dst)), "l"(from),
+                       "n"((int)sizeof(Raw))
+                       : "memory");
+      } else if (ok) {
+        *dst = Row<T, VEC>::load(from);
       }
     }
   }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Fours of rows in shared memory, one of them in work.
+template <typename T, int VEC> constexpr int back_depth() { return sizeof(typename Row<T, VEC>::Raw) == 16 ? 3 : 5; }
+
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kBackThreads, 2)
+conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict__ x, int64_t x_pitch,
+                 const T* __restrict__ w, const T* __restrict__ bias, const int32_t* __restrict__ cu,
+                 const int32_t* __restrict__ seq, const T* __restrict__ state, const T* __restrict__ dfinal,
+                 T* __restrict__ dx, T* __restrict__ dstate, float* __restrict__ part, uint32_t* __restrict__ status,
+                 int64_t total, int64_t run, int ch, bool act) {
+  using R = Row<T, VEC>;
+  using Raw = typename R::Raw;
+  constexpr int H = W - 1;
+  constexpr int kDepth = back_depth<T, VEC>();
+  extern __shared__ __align__(16) uint8_t s_ring[];   // [warp][four of rows][row][x, dy][lane]
+  __shared__ float s_sum[kBackWarps][32 * VEC];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c = (blockIdx.x * 32 + lane) * VEC;
+  const bool in = c < ch;
+  const int64_t t_lo = ((int64_t)blockIdx.y * kBackWarps + warp) * run;
+  const int64_t t_hi = t_lo + run < total ? t_lo + run : total;        // the rows of this run
+  const int64_t t_end = t_hi + H < total ? t_hi + H : total;           // and those behind it
   float wt[W][VEC], bv[VEC], dw[W][VEC], db[VEC];
+  float win[W][VEC];      // the last W inputs, oldest first
+  float dz[W][VEC];       // dz of the last W tokens, oldest first
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
     bv[i] = db[i] = 0.f;
 #pragma unroll
-    for (int j = 0; j < W; ++j) wt[j][i] = dw[j][i] = 0.f;
+    for (int j = 0; j < W; ++j) wt[j][i] = dw[j][i] = win[j][i] = dz[j][i] = 0.f;
   }
   if (in) load_taps<T, VEC, W>(w, bias, c, wt, bv);
-  const int s0 = (tid / kLanes) * kStrip;
-  float win[W][VEC];      // the last W inputs, oldest first
-  float dz[W][VEC];       // dz of the last W tokens, oldest first
-  float ds[H][VEC];       // derivative by the state of the sequence that began in this strip
+
+  auto shift = [&] {
 #pragma unroll
-  for (int j = 0; j < W; ++j) {
+    for (int j = 0; j < H; ++j) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) win[j][e] = dz[j][e] = 0.f;
-  }
-#pragma unroll
-  for (int j = 0; j < H; ++j) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) ds[j][e] = 0.f;
-  }
-  // A strip inside one sequence, with the W-1 tokens before and behind it (nearly all of a long sequence): no
-  // state, no end, so the windows rotate in registers over unrolled tokens.
-  const int n0 = s_seq[s0];
-  const bool inside = in && n0 >= 0 && s_seq[s0 + kStrip + H - 1] == n0 && t0 + s0 - s_bos[s0] >= H;
-  if (inside) {
-    constexpr int kAhead = 4;
-    const T *xp = x + (t0 + s0) * x_pitch + c, *gp = dy + (t0 + s0) * dy_pitch + c;
-    T* op = dx + (t0 + s0) * ch + c;
-#pragma unroll
-    for (int j = 0; j < H; ++j) R::unpack(R::load(xp + (j - H) * x_pitch), win[j + 1]);
-    typename R::Raw nx[kAhead], ng[kAhead];
-    auto ahead = [&](int rows) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (u < rows) {
-          nx[u] = R::load(xp);
-          ng[u] = R::load(gp);
-          xp += x_pitch;
-          gp += dy_pitch;
-        }
+      for (int e = 0; e < VEC; ++e) {
+        win[j][e] = win[j + 1][e];
+        dz[j][e] = dz[j + 1][e];
       }
-    };
-    auto token = [&](const typename R::Raw& xr, const typename R::Raw& gr, bool sums, bool out) {
-#pragma unroll
-      for (int j = 0; j < H; ++j) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          win[j][e] = win[j + 1][e];
-          dz[j][e] = dz[j + 1][e];
-        }
-      }
-      R::unpack(xr, win[H]);
-      R::unpack(gr, dz[H]);
-      if (act) {
-        float z[VEC];
-        apply<T, VEC, W>(win, wt, bv, false, z);
-        silu_slope<T, VEC>(z, dz[H]);
-      }
-      if (sums) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) acc<VEC>(dw[j], dz[H], win[j]);
-        if constexpr (VEC == 4) {
-          add2(db[0], db[1], dz[H][0], dz[H][1]);
-          add2(db[2], db[3], dz[H][2], dz[H][3]);
-        } else {
-          db[0] += dz[H][0];
-        }
-      }
-      if (out) {
-        float o[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] = 0.f;
-#pragma unroll
-        for (int d = 0; d < W; ++d) acc<VEC>(o, dz[d], wt[H - d]);
-        R::store(op, R::pack(o));
-        op += ch;
-      }
-    };
-    typename R::Raw cx[kAhead], cg[kAhead];
-    auto take = [&] {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        cx[u] = nx[u];
-        cg[u] = ng[u];
-      }
-    };
-    ahead(kAhead);
-    take();
-    ahead(kAhead);
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) token(cx[u], cg[u], true, u >= H);
-#pragma unroll 1
-    for (int i0 = kAhead; i0 < kStrip - kAhead; i0 += kAhead) {
-      take();
-      ahead(kAhead);
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) token(cx[u], cg[u], true, true);
     }
-    take();
-    ahead(H);
+  };
+  auto slope = [&] {   // dz of the newest token, from dy in its place
+    if (!act) return;
+    float z[VEC];
+    apply<T, VEC, W>(win, wt, bv, false, z);
+    silu_slope<T, VEC>(z, dz[H]);
+  };
+  auto count = [&] {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) token(cx[u], cg[u], true, true);
+    for (int j = 0; j < W; ++j) acc<VEC>(dw[j], dz[H], win[j]);
+    if constexpr (VEC == 4) {
+      add2(db[0], db[1], dz[H][0], dz[H][1]);
+      add2(db[2], db[3], dz[H][2], dz[H][3]);
+    } else {
+      db[0] += dz[H][0];
+    }
+  };
+  // One row by itself, t < t_end: `n` its sequence; the derivative of row t - H is complete then.
+  int last = -1;          // sequence of the row before, as far as this run has seen it
+  float ds[H][VEC];       // derivative by the state of the sequence that began in this run
+  auto row = [&](int64_t t) {
+    const int n = seq[t];
+    shift();
 #pragma unroll
-    for (int u = 0; u < H; ++u) token(nx[u], ng[u], false, true);
-  }
-  // Rows of dx are written when the W-1 tokens behind them have been seen.
-#pragma unroll 1
-  for (int i = 0; in && !inside && i < kStrip + H; ++i) {
-    const int r = s0 + i;
-    const int64_t t = t0 + r;
-    const int n = r < kSpan ? s_seq[r] : -1;
-    const int64_t bos = n >= 0 ? s_bos[r] : 0, pos = t - bos;
-    float g[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) g[e] = 0.f;
+    for (int e = 0; e < VEC; ++e) dz[H][e] = 0.f;
     if (n >= 0) {
-      if (i == 0 || s_seq[r - 1] != n) {
+      const int64_t bos = cu[n], pos = t - bos;
+      if (last != n) {
         // the inputs before the token: of the sequence, or of its state
 #pragma unroll
         for (int j = 0; j < H; ++j) {
           const int64_t p = pos - H + j;
-          if (p >= 0) R::unpack(R::load(x + (bos + p) * x_pitch + c), win[j + 1]);
-          else if (state) R::unpack(R::load(state + ((int64_t)n * H + H + p) * ch + c), win[j + 1]);
+          if (p >= 0) R::unpack(R::load(x + (bos + p) * x_pitch + c), win[j]);
+          else if (state) R::unpack(R::load(state + ((int64_t)n * H + H + p) * ch + c), win[j]);
           else
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) win[j + 1][e] = 0.f;
+            for (int e = 0; e < VEC; ++e) win[j][e] = 0.f;
         }
 #pragma unroll
         for (int j = 0; j < H; ++j) {
@@ -604,28 +532,12 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
           for (int e = 0; e < VEC; ++e) ds[j][e] = 0.f;
         }
       }
-#pragma unroll
-      for (int j = 0; j < H; ++j) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
-      }
       R::unpack(R::load(x + t * x_pitch + c), win[H]);
-      R::unpack(R::load(dy + t * dy_pitch + c), g);
-      if (act) {
-        float z[VEC];
-        apply<T, VEC, W>(win, wt, bv, false, z);
-        silu_slope<T, VEC>(z, g);
-      }
-      if (i < kStrip) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-          for (int j = 0; j < W; ++j) dw[j][e] = fmaf(g[e], win[j][e], dw[j][e]);
-          db[e] += g[e];
-        }
-      }
-      // a sequence's state is read by its first W-1 tokens, which the strip of the first one sees all
-      if (dstate && pos < H && pos <= i && i - pos < kStrip) {
+      R::unpack(R::load(dy + t * dy_pitch + c), dz[H]);
+      slope();
+      if (t < t_hi) count();
+      // a sequence's state is read by its first W-1 tokens, which the run of the first one sees all
+      if (dstate && pos < H && t - pos >= t_lo && t - pos < t_hi) {
         const int64_t len = (int64_t)cu[n + 1] - bos;
 #pragma unroll
         for (int m = 0; m < H; ++m) {
@@ -633,7 +545,7 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
           for (int p = 0; p <= m; ++p) {
             if (p == pos) {
 #pragma unroll
-              for (int e = 0; e < VEC; ++e) ds[m][e] = fmaf(g[e], wt[m - p][e], ds[m][e]);
+              for (int e = 0; e < VEC; ++e) ds[m][e] = fmaf(dz[H][e], wt[m - p][e], ds[m][e]);
             }
           }
         }
@@ -651,58 +563,138 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
         }
       }
     }
-#pragma unroll
-    for (int j = 0; j < H; ++j) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) dz[j][e] = dz[j + 1][e];
-    }
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) dz[H][e] = g[e];
-    const int ro = r - H;                   // the row whose derivative is complete
-    if (i < H || t0 + ro >= total) continue;
-    const int no = s_seq[ro];
+    last = n;
+  };
+  // dx of row o, whose W-1 tokens behind it are in dz
+  auto derive = [&](int64_t o) {
+    const int n = seq[o];
     float out[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) out[e] = 0.f;
-    if (no >= 0) {
+    if (n >= 0) {
 #pragma unroll
-      for (int d = 0; d < W; ++d) {
-        if (d == 0 || (ro + d < kSpan && s_seq[ro + d] == no)) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) out[e] = fmaf(dz[d][e], wt[H - d][e], out[e]);
-        }
-      }
+      for (int d = 0; d < W; ++d)
+        if (d == 0 || (o + d < total && seq[o + d] == n)) acc<VEC>(out, dz[d], wt[H - d]);
       if (dfinal) {
-        const int64_t back = (int64_t)cu[no + 1] - (t0 + ro);   // 1 for the last token
+        const int64_t back = (int64_t)cu[n + 1] - o;   // 1 for the last token
         if (back <= H) {
           float f[VEC];
-          R::unpack(R::load(dfinal + ((int64_t)no * H + H - back) * ch + c), f);
+          R::unpack(R::load(dfinal + ((int64_t)n * H + H - back) * ch + c), f);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) out[e] += f[e];
         }
       }
     }
-    if (KDA_CHECK(ro >= 0 && c + VEC <= ch)) R::store(dx + (t0 + ro) * ch + c, R::pack(out));
+    if (KDA_CHECK(o >= 0 && o < total && c + VEC <= ch)) R::store(dx + o * ch + c, R::pack(out));
+  };
+
+  if (t_lo < t_hi) {
+    Raw* const ring = reinterpret_cast<Raw*>(s_ring) + warp * (kDepth * kQuad * 2 * 32) + lane;
+    const T *xp = x + t_lo * x_pitch + c, *gp = dy + t_lo * dy_pitch + c;
+    int64_t asked = t_lo;
+    int to = 0, from = 0;
+    auto ahead = [&] {
+      fetch_quad<T, VEC>(ring + to * (kQuad * 2 * 32), xp, x_pitch, gp, dy_pitch, in ? t_end - asked : 0);
+      asked += kQuad;
+      xp += kQuad * x_pitch;
+      gp += kQuad * dy_pitch;
+      to = to + 1 == kDepth ? 0 : to + 1;
+    };
+#pragma unroll 1
+    for (int q = 0; q + 1 < kDepth; ++q) ahead();
+    // bits of the rows t .. t + 31 - kQuad + ...: row t - H + i + 1 continues the sequence of the row before it
+    uint64_t follows = 0;
+    T* op = dx + (t_lo - H) * ch + c;
+#pragma unroll 1
+    for (int64_t t = t_lo; t < t_end; t += kQuad) {
+      if ((t - t_lo) % 16 == 0) {
+        auto same = [&](int64_t u) { return u > 0 && u < total && seq[u] >= 0 && seq[u] == seq[u - 1]; };
+        const int64_t u = t - H + 1 + lane;
+        follows = __ballot_sync(0xffffffffu, same(u));
+      }
+      ahead();
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+      const uint32_t bits = (uint32_t)(follows >> ((t - t_lo) % 16));
+      constexpr uint32_t kPlain = (1u << (kQuad - 1 + 2 * H)) - 1;
+      const Raw* raw = ring + from * (kQuad * 2 * 32);
+      from = from + 1 == kDepth ? 0 : from + 1;
+      if ((bits & kPlain) == kPlain && t >= t_lo + H && t + kQuad <= t_hi) {
+        if (in) {
+#pragma unroll
+          for (int u = 0; u < kQuad; ++u) {
+            shift();
+            R::unpack(raw[(u * 2) * 32], win[H]);
+            R::unpack(raw[(u * 2 + 1) * 32], dz[H]);
+            slope();
+            count();
+            float o[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) o[e] = 0.f;
+#pragma unroll
+            for (int d = 0; d < W; ++d) acc<VEC>(o, dz[d], wt[H - d]);
+            R::store(op + (int64_t)u * ch, R::pack(o));
+          }
+        }
+        last = -2;   // of the rows' sequence; whoever goes on row by row reads the inputs again
+      } else if (in) {
+#pragma unroll 1
+        for (int u = 0; u < kQuad; ++u) {
+          if (t + u < t_end) row(t + u);
+          else shift();
+          const int64_t o = t + u - H;
+          if (o >= t_lo && o < t_hi) derive(o);
+        }
+      }
+      op += kQuad * ch;
+    }
+    if (in) {   // rows at the end of all, with none behind them
+      for (int64_t t = (t_end - t_lo + kQuad - 1) / kQuad * kQuad + t_lo; t - H < t_hi; ++t) {
+        shift();
+        derive(t - H);
+      }
+    }
   }
-  // parts [tile][W + 1][Ch] of the sums
+  // parts [run of CTAs][W + 1][Ch] of the sums
 #pragma unroll
   for (int j = 0; j <= W; ++j) {
-    float mine[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) mine[e] = j < W ? dw[j < W ? j : 0][e] : db[e];
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) s_sum[tid / kLanes][(tid % kLanes) * VEC + e] = mine[e];
+    for (int e = 0; e < VEC; ++e) s_sum[warp][lane * VEC + e] = j < W ? dw[j < W ? j : 0][e] : db[e];
     __syncthreads();
-    for (int k = tid; k < kLanes * VEC; k += kConvThreads) {
-      const int64_t cc = (int64_t)blockIdx.y * kLanes * VEC + k;
+    for (int k = tid; k < 32 * VEC; k += kBackThreads) {
+      const int64_t cc = (int64_t)blockIdx.x * 32 * VEC + k;
       float sum = 0.f;
 #pragma unroll
-      for (int q = 0; q < kBackStrips; ++q) sum += s_sum[q][k];
-      if (cc < ch) part[((int64_t)blockIdx.x * (W + 1) + j) * ch + cc] = sum;
+      for (int q = 0; q < kBackWarps; ++q) sum += s_sum[q][k];
+      if (cc < ch) part[((int64_t)blockIdx.y * (W + 1) + j) * ch + cc] = sum;
     }
   }
   KDA_DEBUG_FOLD(status);
+}
+
+// The sequence of each row (-1: none that is valid; the last one that holds it where lengths run
+// backwards), the status word, and the derivatives by the states of sequences without tokens (dfinal) and of
+// invalid ones (0).
+template <typename T>
+__global__ void __launch_bounds__(1024)
+conv_back_plan_kernel(const int32_t* __restrict__ cu, int N, int64_t total, uint32_t* __restrict__ status,
+                      int32_t* __restrict__ seq, const T* __restrict__ dfinal, T* __restrict__ dstate, int64_t row) {
+  __shared__ int s_seq[1024];
+  const int tid = threadIdx.x;
+  if (blockIdx.x == 0) check_all(status, cu, nullptr, N, total, total, 0);
+  for (int64_t t0 = (int64_t)blockIdx.x * 1024; t0 < total; t0 += (int64_t)gridDim.x * 1024) {
+    sequences_of<1024>(s_seq, cu, nullptr, 0, N, total, t0);
+    if (t0 + tid < total) seq[t0 + tid] = s_seq[tid];
+    __syncthreads();
+  }
+  if (!dstate) return;
+  for (int64_t n = blockIdx.x * 32ll + (tid >> 5); n < N; n += gridDim.x * 32ll) {
+    int64_t a, b;
+    const bool ok = seq_bounds(cu, (int)n, total, &a, &b);
+    if (ok && a != b) continue;
+    for (int64_t i = tid & 31; i < row; i += 32)
+      dstate[n * row + i] = ok && dfinal ? dfinal[n * row + i] : from_f32<T>(0.f);
+  }
 }
 
 // The tiles' parts of the sums, added in a fixed order.
@@ -784,39 +776,58 @@ cudaError_t by_type(const ConvArgs& a, cudaStream_t st, bool token) {
   return wide ? by_width<T, VEC>(a, st, token) : by_width<T, 1>(a, st, token);
 }
 
-// Strips as in the forward pass.
-constexpr int kBackStrip = 32;
-int back_strip(const kda_conv_desc_t& d) {
-  const int64_t blocks = (d.total_tokens / (kBackStrip * kBackStrips)) * (d.channels / (kLanes * 4));
-  return blocks >= 4 * gpu_sms() ? kBackStrip : 8;
+// CTAs a channel block: as many as fill the GPU twice over, of runs of 32 rows at least a warp.
+struct BackShape {
+  int64_t run, ctas;
+};
+BackShape back_shape(const kda_conv_desc_t& d, int vec) {
+  const int64_t blocks = (d.channels + 32 * vec - 1) / (32 * vec), T = d.total_tokens;
+  int64_t ctas = 2ll * gpu_sms() / blocks;
+  const int64_t most = (T + 32 * kBackWarps - 1) / (32 * kBackWarps);
+  ctas = ctas < most ? ctas : most;
+  ctas = ctas > 0 ? ctas : 1;
+  int64_t run = (T + ctas * kBackWarps - 1) / (ctas * kBackWarps);
+  run = (run + 15) / 16 * 16;
+  return {run > 0 ? run : 16, ctas};
 }
-int64_t back_tiles(const kda_conv_desc_t& d) {
-  const int64_t rows = (int64_t)back_strip(d) * kBackStrips, tiles = (d.total_tokens + rows - 1) / rows;
-  return tiles > 0 ? tiles : 1;   // no tokens: the empty sequences' states
+size_t back_part(const kda_conv_desc_t& d) {   // behind the header: the rows' sequences, then the sums
+  return kWsPayload + ((size_t)d.total_tokens * 4 + 255) / 256 * 256;
 }
 
-template <typename T, int VEC, int W, int kStrip>
+template <typename T, int VEC, int W>
 cudaError_t launch_back(const ConvBackArgs& a, cudaStream_t st) {
   const int ch = a.d.channels;
-  const int64_t tiles = back_tiles(a.d);
-  dim3 grid((unsigned)tiles, (unsigned)((ch + kLanes * VEC - 1) / (kLanes * VEC)));
-  conv_back_kernel<T, VEC, W, kStrip><<<grid, kConvThreads, 0, st>>>(
-      (const T*)a.dy, a.dy_pitch, (const T*)a.x, a.d.x_pitch, (const T*)a.w, (const T*)a.bias, a.cu,
-      (const T*)a.state, (const T*)a.dfinal, (T*)a.dx, (T*)a.dstate, a.part, a.status, a.d.num_seqs,
-      a.d.total_tokens, ch, a.d.silu != 0);
-  const cudaError_t e = cudaGetLastError();
+  const BackShape s = back_shape(a.d, VEC);
+  int32_t* seq = reinterpret_cast<int32_t*>(a.ws + kWsPayload);
+  float* part = reinterpret_cast<float*>(a.ws + back_part(a.d));
+  uint32_t* status = &reinterpret_cast<WsHeader*>(a.ws)->status;
+  int64_t plan = (a.d.total_tokens + 1023) / 1024, most = 2ll * gpu_sms();
+  const int64_t rows = a.dstate ? ((int64_t)a.d.num_seqs + 31) / 32 : 1;
+  plan = plan > rows ? plan : rows;
+  plan = plan < 1 ? 1 : plan > most ? most : plan;
+  conv_back_plan_kernel<T><<<(unsigned)plan, 1024, 0, st>>>(a.cu, a.d.num_seqs, a.d.total_tokens, status, seq,
+                                                          (const T*)a.dfinal, (T*)a.dstate, (int64_t)(W - 1) * ch);
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  conv_sum_kernel<<<dim3((unsigned)((ch + 31) / 32), W + 1), 256, 0, st>>>(a.part, tiles, ch, W, a.dw, a.db);
+  dim3 grid((unsigned)((ch + 32 * VEC - 1) / (32 * VEC)), (unsigned)s.ctas);
+  const int bytes = kBackThreads * back_depth<T, VEC>() * kQuad * 2 * (int)sizeof(typename Row<T, VEC>::Raw);
+  auto* kernel = conv_back_kernel<T, VEC, W>;
+  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+  kernel<<<grid, kBackThreads, bytes, st>>>(
+      (const T*)a.dy, a.dy_pitch, (const T*)a.x, a.d.x_pitch, (const T*)a.w, (const T*)a.bias, a.cu, seq,
+      (const T*)a.state, (const T*)a.dfinal, (T*)a.dx, (T*)a.dstate, part, status, a.d.total_tokens, s.run, ch,
+      a.d.silu != 0);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  conv_sum_kernel<<<dim3((unsigned)((ch + 31) / 32), W + 1), 256, 0, st>>>(part, s.ctas, ch, W, a.dw, a.db);
   return cudaGetLastError();
 }
 
 template <typename T, int VEC>
 cudaError_t back_by_width(const ConvBackArgs& a, cudaStream_t st) {
-  const bool longer = back_strip(a.d) == kBackStrip;
   switch (a.d.width) {
-    case 2: return longer ? launch_back<T, VEC, 2, kBackStrip>(a, st) : launch_back<T, VEC, 2, 8>(a, st);
-    case 3: return longer ? launch_back<T, VEC, 3, kBackStrip>(a, st) : launch_back<T, VEC, 3, 8>(a, st);
-    default: return longer ? launch_back<T, VEC, 4, kBackStrip>(a, st) : launch_back<T, VEC, 4, 8>(a, st);
+    case 2: return launch_back<T, VEC, 2>(a, st);
+    case 3: return launch_back<T, VEC, 3>(a, st);
+    default: return launch_back<T, VEC, 4>(a, st);
   }
 }
 
@@ -833,7 +844,8 @@ cudaError_t back_by_type(const ConvBackArgs& a, cudaStream_t st) {
 }  // namespace
 
 size_t conv_back_workspace(const kda_conv_desc_t& d) {
-  return kWsPayload + (size_t)back_tiles(d) * (d.width + 1) * d.channels * 4;
+  const int64_t four = back_shape(d, 4).ctas, one = back_shape(d, 1).ctas;   // either form may be taken
+  return back_part(d) + (size_t)(four > one ? four : one) * (d.width + 1) * d.channels * 4;
 }
 
 cudaError_t launch_conv_back(const ConvBackArgs& a, cudaStream_t st) {

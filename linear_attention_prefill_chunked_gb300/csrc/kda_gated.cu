@@ -259,24 +259,7 @@ gated_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ id
   for (int64_t i = blockIdx.x * 1024ll + tid; i < num_unset; i += gridDim.x * 1024ll)
     unset[i] = make_uint4(kUnset, kUnset, kUnset, kUnset);
   for (int64_t t0 = (int64_t)blockIdx.x * kPlanRows; t0 < T; t0 += (int64_t)gridDim.x * kPlanRows) {
-    s_seq[tid] = -1;
-    __syncthreads();
-    for (int base = 0; base < N; base += 1024) {
-      const int n = base + tid;
-      int64_t a = 0, b = 0;
-      bool hit = n < N && seq_bounds(cu, n, T, &a, &b) && a < t0 + kPlanRows && b > t0 && a < b;
-      if (hit && idx) hit = resolve_slot(idx, n, num_slots) >= 0;
-      unsigned m = __ballot_sync(0xffffffffu, hit);
-      while (m) {
-        const int src = __ffs(m) - 1;
-        m &= m - 1;
-        const int64_t sa = __shfl_sync(0xffffffffu, a, src), sb = __shfl_sync(0xffffffffu, b, src);
-        const int sn = __shfl_sync(0xffffffffu, n, src);
-        const int lo = (int)(sa > t0 ? sa - t0 : 0), hi = (int)(sb < t0 + kPlanRows ? sb - t0 : kPlanRows);
-        for (int i = lo + (tid & 31); i < hi; i += 32) atomicMax(&s_seq[i], sn);
-      }
-    }
-    __syncthreads();
+    sequences_of<kPlanRows>(s_seq, cu, idx, num_slots, N, T, t0);
     if (t0 + tid < T) seq[t0 + tid] = s_seq[tid];
     __syncthreads();
   }

@@ -171,6 +171,32 @@ __device__ __forceinline__ void check_all(uint32_t* status, const int32_t* cu, c
     set_status(status, (s ? KDA_DEVICE_BAD_SEQLENS : 0u) | (i ? KDA_DEVICE_BAD_SLOT : 0u));
 }
 
+// The whole block (of R threads) writes the sequence of rows t0 .. t0 + R - 1 to s_seq: -1 where none that is
+// valid holds a row, the last one where lengths run backwards.  Ends with a barrier.
+template <int R>
+__device__ __forceinline__ void sequences_of(int* s_seq, const int32_t* cu, const int32_t* idx, int64_t num_slots,
+                                             int N, int64_t T, int64_t t0) {
+  const int tid = threadIdx.x;
+  s_seq[tid] = -1;
+  __syncthreads();
+  for (int base = 0; base < N; base += R) {
+    const int n = base + tid;
+    int64_t a = 0, b = 0;
+    bool hit = n < N && seq_bounds(cu, n, T, &a, &b) && a < t0 + R && b > t0 && a < b;
+    if (hit && idx) hit = resolve_slot(idx, n, num_slots) >= 0;
+    unsigned m = __ballot_sync(0xffffffffu, hit);
+    while (m) {  // a warp writes each of its hits together: a long sequence fills all rows
+      const int src = __ffs(m) - 1;
+      m &= m - 1;
+      const int64_t sa = __shfl_sync(0xffffffffu, a, src), sb = __shfl_sync(0xffffffffu, b, src);
+      const int sn = __shfl_sync(0xffffffffu, n, src);
+      const int lo = (int)(sa > t0 ? sa - t0 : 0), hi = (int)(sb < t0 + R ? sb - t0 : R);
+      for (int i = lo + (tid & 31); i < hi; i += 32) atomicMax(&s_seq[i], sn);
+    }
+  }
+  __syncthreads();
+}
+
 // Two fp32 operations as one packed instruction, each rounded to nearest.
 __device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
   unsigned long long ab, xy;
@@ -239,8 +265,7 @@ struct ConvBackArgs {
   const void *state, *dfinal;  // [N, W-1, Ch] or null
   void *dx, *dstate;           // dstate may be null
   float *dw, *db;              // db may be null
-  float* part;                 // the tiles' sums
-  uint32_t* status;
+  uint8_t* ws;
 };
 size_t conv_back_workspace(const kda_conv_desc_t& d);  // the whole workspace, header included
 cudaError_t launch_conv_back(const ConvBackArgs& a, cudaStream_t st);

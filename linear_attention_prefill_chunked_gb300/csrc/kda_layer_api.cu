@@ -192,8 +192,7 @@ kda_status_t kda_causal_conv_backward(const kda_conv_desc_t* d, const void* dy, 
   a.dstate = dstate;
   a.dw = dweight;
   a.db = dbias;
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kda::kWsPayload);
-  a.status = status_of(workspace);
+  a.ws = static_cast<uint8_t*>(workspace);
   return launched(workspace, stream, [&] { return kda::launch_conv_back(a, stream); });
 }
 

@@ -45,4 +45,5 @@ def test_c_boundary_refuses():
     assert _call(lib, ch=big, pitch=big, dy_pitch=big) == 2
     size = lambda **k: lib.kda_causal_conv_backward_workspace_size(ctypes.byref(layer.KdaConvDesc(
         N, k.get("T", T), CH, k.get("W", W), 0, 1, CH, 0, 0)))
-    assert size() >= 256 + 4 * (W + 1) * CH and size(T=0) >= size(W=3) and size(W=5) == 0
+    least = 256 + 4 * (W + 1) * CH
+    assert size() >= least + 4 * T and size(T=0) >= least and size(W=5) == 0
