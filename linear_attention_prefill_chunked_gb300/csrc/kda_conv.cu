@@ -410,6 +410,35 @@ template <typename T, int VEC> __device__ __forceinline__ void silu_slope(const 
     }
   }
 }
+// d = x * y + c
+__device__ __forceinline__ void fma3(float& d, float& e, float x, float y, float u, float v, float c, float f) {
+  unsigned long long de, xy, uv, cf;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(uv) : "f"(u), "f"(v));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(cf) : "f"(c), "f"(f));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(de) : "l"(xy), "l"(uv), "l"(cf));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d), "=f"(e) : "l"(de));
+}
+template <int VEC>
+__device__ __forceinline__ void fma(float (&d)[VEC], const float (&x)[VEC], const float (&y)[VEC], const float (&c)[VEC]) {
+  if constexpr (VEC == 4) {
+    fma3(d[0], d[1], x[0], x[1], y[0], y[1], c[0], c[1]);
+    fma3(d[2], d[3], x[2], x[3], y[2], y[3], c[2], c[3]);
+  } else {
+    d[0] = fmaf(x[0], y[0], c[0]);
+  }
+}
+// d = x * y
+template <int VEC> __device__ __forceinline__ void mul(float (&d)[VEC], const float (&x)[VEC], const float (&y)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) d[i] = x[i];
+  if constexpr (VEC == 4) {
+    mul2(d[0], d[1], y[0], y[1]);
+    mul2(d[2], d[3], y[2], y[3]);
+  } else {
+    d[0] *= y[0];
+  }
+}
 // a += x * y
 template <int VEC> __device__ __forceinline__ void acc(float (&a)[VEC], const float (&x)[VEC], const float (&y)[VEC]) {
   if constexpr (VEC == 4) {
@@ -422,25 +451,30 @@ template <int VEC> __device__ __forceinline__ void acc(float (&a)[VEC], const fl
 
 // Four rows of x and dy at p on their way to `to`, [row][x, dy][lane].
 template <typename T, int VEC>
-__device__ __forceinline__ void fetch_quad(typename Row<T, VEC>::Raw* to, const T* x, int64_t x_pitch, const T* dy,
-                                           int64_t dy_pitch, int64_t rows) {
+__device__ __forceinline__ void fetch_quad(typename Row<T, VEC>::Raw* to, const T*& x, int64_t x_pitch, const T*& dy,
+                                           int64_t dy_pitch, int rows) {
   using Raw = typename Row<T, VEC>::Raw;
-#pragma unroll
-  for (int u = 0; u < kQuad; ++u) {
-    const bool ok = u < rows;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const T* from = q ? dy + u * dy_pitch : x + u * x_pitch;
-      Raw* dst = to + (u * 2 + q) * 32;
-      if constexpr (sizeof(Raw) >= 4) {
-        if (ok)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_u32(dst)), "l"(from),
-                       "n"((int)sizeof(Raw))
-                       : "memory");
-      } else if (ok) {
-        *dst = Row<T, VEC>::load(from);
-      }
+  auto one = [&](int u) {
+    if constexpr (sizeof(Raw) >= 4) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_u32(to + (u * 2) * 32)), "l"(x),
+                   "n"((int)sizeof(Raw))
+                   : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_u32(to + (u * 2 + 1) * 32)), "l"(dy),
+                   "n"((int)sizeof(Raw))
+                   : "memory");
+    } else {
+      to[(u * 2) * 32] = Row<T, VEC>::load(x);
+      to[(u * 2 + 1) * 32] = Row<T, VEC>::load(dy);
     }
+    x += x_pitch;
+    dy += dy_pitch;
+  };
+  if (rows >= kQuad) {
+#pragma unroll
+    for (int u = 0; u < kQuad; ++u) one(u);
+  } else {
+#pragma unroll 1
+    for (int u = 0; u < rows; ++u) one(u);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -492,12 +526,15 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
   auto slope = [&] {   // dz of the newest token, from dy in its place
     if (!act) return;
     float z[VEC];
-    apply<T, VEC, W>(win, wt, bv, false, z);
+    fma<VEC>(z, win[0], wt[0], bv);
+#pragma unroll
+    for (int j = 1; j < W; ++j) acc<VEC>(z, win[j], wt[j]);
     silu_slope<T, VEC>(z, dz[H]);
   };
   auto count = [&] {
 #pragma unroll
     for (int j = 0; j < W; ++j) acc<VEC>(dw[j], dz[H], win[j]);
+    if (!bias) return;
     if constexpr (VEC == 4) {
       add2(db[0], db[1], dz[H][0], dz[H][1]);
       add2(db[2], db[3], dz[H][2], dz[H][3]);
@@ -591,30 +628,37 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
   if (t_lo < t_hi) {
     Raw* const ring = reinterpret_cast<Raw*>(s_ring) + warp * (kDepth * kQuad * 2 * 32) + lane;
     const T *xp = x + t_lo * x_pitch + c, *gp = dy + t_lo * dy_pitch + c;
-    int64_t asked = t_lo;
+    int to_ask = in ? (int)(t_end - t_lo) : 0;   // rows that are not on their way yet
     int to = 0, from = 0;
     auto ahead = [&] {
-      fetch_quad<T, VEC>(ring + to * (kQuad * 2 * 32), xp, x_pitch, gp, dy_pitch, in ? t_end - asked : 0);
-      asked += kQuad;
-      xp += kQuad * x_pitch;
-      gp += kQuad * dy_pitch;
+      fetch_quad<T, VEC>(ring + to * (kQuad * 2 * 32), xp, x_pitch, gp, dy_pitch, to_ask);
+      to_ask -= kQuad;
       to = to + 1 == kDepth ? 0 : to + 1;
     };
 #pragma unroll 1
     for (int q = 0; q + 1 < kDepth; ++q) ahead();
-    // bits of the rows t .. t + 31 - kQuad + ...: row t - H + i + 1 continues the sequence of the row before it
-    uint64_t follows = 0;
+    // bit i: row t - H + 1 + i is of the same sequence as the row before it, of 16 rows t at a time; the next
+    // 16 rows' are looked up ahead
+    uint32_t follows = 0;
+    int mine, prior;
+    auto look = [&](int64_t t) {
+      const int64_t u = t - H + 1 + lane;
+      const bool ok = u > 0 && u < total;
+      mine = ok ? seq[u] : -1;
+      prior = ok ? seq[u - 1] : -1;
+    };
+    look(t_lo);
     T* op = dx + (t_lo - H) * ch + c;
 #pragma unroll 1
     for (int64_t t = t_lo; t < t_end; t += kQuad) {
-      if ((t - t_lo) % 16 == 0) {
-        auto same = [&](int64_t u) { return u > 0 && u < total && seq[u] >= 0 && seq[u] == seq[u - 1]; };
-        const int64_t u = t - H + 1 + lane;
-        follows = __ballot_sync(0xffffffffu, same(u));
+      const int at = (int)(t - t_lo) % 16;
+      if (at == 0) {
+        follows = __ballot_sync(0xffffffffu, mine >= 0 && mine == prior);
+        look(t + 16);
       }
       ahead();
       asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
-      const uint32_t bits = (uint32_t)(follows >> ((t - t_lo) % 16));
+      const uint32_t bits = follows >> at;
       constexpr uint32_t kPlain = (1u << (kQuad - 1 + 2 * H)) - 1;
       const Raw* raw = ring + from * (kQuad * 2 * 32);
       from = from + 1 == kDepth ? 0 : from + 1;
@@ -628,10 +672,9 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
             slope();
             count();
             float o[VEC];
+            mul<VEC>(o, dz[0], wt[H]);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] = 0.f;
-#pragma unroll
-            for (int d = 0; d < W; ++d) acc<VEC>(o, dz[d], wt[H - d]);
+            for (int d = 1; d < W; ++d) acc<VEC>(o, dz[d], wt[H - d]);
             R::store(op + (int64_t)u * ch, R::pack(o));
           }
         }
