@@ -521,7 +521,7 @@ kda_status_t kda_gated_decode(const kda_gated_desc_t *desc, const void *x, const
 /* Problem descriptor of the draw of tokens. */
 typedef struct {
     int32_t num_rows;          /* rows of logits: requests, or fed tokens               */
-    int32_t vocab;             /* entries of a row, at most 344064                      */
+    int32_t vocab;             /* entries of a row, at most 360448                      */
     kda_dtype_t dtype;         /* of the logits                                         */
     int64_t logits_pitch;      /* elements between consecutive rows, >= vocab           */
     int64_t noise_pitch;       /* the same of noise (kda_sample)                        */

@@ -8,18 +8,18 @@
 //
 // All filters keep a prefix of one order, so all that is sought is its last entry, by count or by mass. A row
 // is read once, into the shared memory of a cluster of CTAs (a slice each); no row is sorted. A histogram over
-// the distance from the maximum (2048 bins of counts and masses) gives the bin the last entry lies in; the few
+// the distance from the maximum (1024 bins of counts and masses) gives the bin the last entry lies in; the few
 // entries of that bin are ranked against each other. Where a bin holds too many (equal values, as bf16 logits
 // have them), further digits of the distance, then of the value, then of the index split it.
 //
 // An entry next to top-p's border stands or falls with the last digits of a sum over the row, so masses
 // are whole numbers, p in units of 2^-44, whose sums do not depend on their order: results are bit-identical
-// from run to run, whichever CTA adds first. p itself is 2^-n 2^(-j/64) 2^-r from a table and four terms of the
+// from run to run, whichever CTA adds first. p itself is 2^-n 2^(-j/64) 2^-r from a table and three terms of the
 // exponential series, the distance carried as two floats: good to 2^-31, where a float's sum of a
 // vocabulary would be off by more than the smallest entries that stand.
 //
 // Bound by HBM in principle (the row, and noise or probabilities), by the arithmetic of p and the cluster's
-// exchanges (two to four a row) in practice.
+// exchanges (three to six a row) in practice.
 #include <cooperative_groups.h>
 
 #include "kda_internal.cuh"
@@ -33,12 +33,12 @@ KDA_DEBUG_FLAG_DEFINE();
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 1024;
 constexpr int kPer = kBins / kThreads;     // bins a thread looks after
 constexpr int kList = 1024;                // entries that are ranked against each other
 constexpr int kMaxRanks = 8;
-constexpr int kSliceMax = 43008;           // floats of a row a CTA can hold beside the rest
-constexpr int kPasses = 7;                 // digits: two of the distance, three of the value, two of the index
+constexpr int kMostQuads = 22;             // fours of entries a thread looks after at most
+constexpr int kPasses = 8;                 // digits: two of the distance, four of the value, two of the index
 constexpr int kOneBits = 44;
 constexpr unsigned long long kOne = 1ull << kOneBits;
 constexpr float kMaskedOut = -__builtin_huge_valf();
@@ -82,59 +82,62 @@ struct alignas(16) Shared {
   Item list[kList];      // this CTA's entries of the bin
   Item all[kList];       // the cluster's
   u64 pow[64];
-  Best warp_best[kWarps], best[kMaxRanks];
+  float powf[64];
+  Best warp_best[kWarps], best[2][kMaxRanks];
   float warp_low[kWarps], low[kMaxRanks];
   u64 warp_cnt[kWarps], warp_mass[kWarps], sum[kMaxRanks];
-  u64 cnt_before, mass_before, cnt_in, mass_in;   // of the bin that was found
+  u64 cnt_before, mass_before, total;   // what lies before the bin that was found; all mass
   int bin, n;
-  uint32_t nk;
+  uint32_t nk;                          // the last entry that stands,
   int idx;
-  u64 mass_incl;
+  u64 mass_incl;                        // and the mass up to and with it
 };
 
-static_assert(sizeof(Shared) % 16 == 0 && sizeof(Shared) + kSliceMax * 4 <= 232448, "227 KB a CTA");
+static_assert(sizeof(Shared) + kMostQuads * kThreads * 16 <= 232448, "227 KB a CTA");
 
 // A row's parameters and what follows from them.
 struct Row {
   float top, ch, cl, fx;   // the maximum; log2(e) / T as two floats; bins by distance
-  bool inf;                // the maximum is infinite: its entries alone count
 };
 
 __device__ __forceinline__ uint32_t down_key(float z) {
   const uint32_t b = __float_as_uint(z);
-  return ~((b >> 31) ? ~b : b | 0x80000000u);
+  return (b >> 31) ? b : ~(b | 0x80000000u);
 }
-// The distance from the maximum in octaves of p; infinite for masked entries.
-__device__ __forceinline__ float octaves(const Row& r, float z) {
-  const float d = r.top - z;
-  return z == kMaskedOut ? __builtin_huge_valf() : r.inf ? (z == r.top ? 0.f : __builtin_huge_valf()) : d * r.ch;
+__device__ __forceinline__ int distance(const Row& r, float z) {  // 20 bits, never falling as z falls
+  const float y = (r.top - z) * r.ch * r.fx;
+  return y < 1048575.f ? (int)y : 1048575;
 }
-__device__ __forceinline__ int distance(const Row& r, float z) {  // 22 bits, never falling as z falls
-  const float y = octaves(r, z) * r.fx;
-  return y < 4194303.f ? (int)y : 4194303;
+// p = 2^-n 2^(-j/64) (1 + e)
+struct Power {
+  int n, j;
+  float e;
+};
+__device__ __forceinline__ bool power(const Row& r, float z, Power& o) {
+  const float d = r.top - z, yh = d * r.ch;
+  if (!(yh < 126.f)) return false;       // masked entries too
+  const float b = d - r.top, dl = (r.top - (d - b)) - (z + b);
+  const float yl = fmaf(d, r.ch, -yh) + fmaf(d, r.cl, dl * r.ch);
+  const float m = fmaf(yh, 64.f, 12582912.f);   // 1.5 * 2^23: rounds to whole numbers
+  const int k = __float_as_int(m) - 0x4b400000;
+  const float t = (fmaf(m - 12582912.f, -1.f / 64.f, yh) + yl) * -0.69314718055994531f;
+  o.n = k >> 6;
+  o.j = k & 63;
+  o.e = t * fmaf(t, fmaf(t, 1.f / 6.f, 0.5f), 1.f);
+  return true;
 }
-// p, and p in units of 2^-44.
-__device__ __forceinline__ float weight(const Row& r, float z, const u64* pow, u64& w) {
-  const float yh = octaves(r, z);
-  if (!(yh < 126.f)) {
-    w = 0;
-    return 0.f;
-  }
-  float yl = 0.f;
-  if (!r.inf) {
-    const float d = r.top - z, b = d - r.top, dl = (r.top - (d - b)) - (z + b);
-    yl = fmaf(d, r.ch, -yh) + fmaf(d, r.cl, dl * r.ch);
-  }
-  const float n = floorf(yh), f = yh - n;
-  const int j = (int)(f * 64.f);
-  const float t = (f - (float)j * (1.f / 64.f) + yl) * -0.69314718055994531f;
-  const float e = t * fmaf(t, fmaf(t, fmaf(t, 1.f / 24.f, 1.f / 6.f), 0.5f), 1.f);
-  const u64 whole = pow[j];
-  const float h = (float)(uint32_t)(whole >> 20) * 5.9604644775390625e-8f;  // of 2^24
-  const int ni = (int)n;
-  const long long fine = (long long)__float2int_rn(h * e * 137438953472.f) << 7;  // of 2^37
-  w = ni < 64 ? (whole + (u64)fine) >> ni : 0;
-  return fmaf(h, e, h) * __uint_as_float((uint32_t)(127 - ni) << 23);
+// p in units of 2^-44
+__device__ __forceinline__ u64 mass(const Row& r, float z, const Shared& s) {
+  Power p;
+  if (!power(r, z, p) || p.n >= 45) return 0;
+  const int fine = __float2int_rn(s.powf[p.j] * p.e * 137438953472.f);  // of 2^37
+  return (s.pow[p.j] + ((u64)(long long)fine << 7)) >> p.n;
+}
+__device__ __forceinline__ float weight(const Row& r, float z, const Shared& s) {
+  Power p;
+  if (!power(r, z, p)) return 0.f;
+  const float h = s.powf[p.j];
+  return fmaf(h, p.e, h) * __uint_as_float((uint32_t)(127 - p.n) << 23);
 }
 
 // Sum over the threads before this one, of two numbers.
@@ -156,30 +159,37 @@ __device__ __forceinline__ void before_me(u64 c, u64 m, Shared& s, u64& bc, u64&
   __syncthreads();
   bc = ic - c;
   bm = im - m;
-  for (int w = 0; w < warp; ++w) {
-    bc += s.warp_cnt[w];
-    bm += s.warp_mass[w];
+  u64 tm = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const u64 wc = s.warp_cnt[w], wm = s.warp_mass[w];
+    if (w < warp) {
+      bc += wc;
+      bm += wm;
+    }
+    tm += wm;
   }
+  if (threadIdx.x == 0) s.total = tm;
   __syncthreads();
 }
 
 // The cluster's histogram: this thread's bins and what lies in the bins before them.
 struct Bins {
   uint32_t c[kPer];
-  u64 m[kPer], before_c, before_m, total_m;
+  u64 m[kPer], before_c, before_m;
 };
 
-// One row a cluster. kProbs: probabilities, else a token.
+// One row a cluster, `quads` fours of entries a thread. kProbs: probabilities, else a token.
 template <typename T, bool kProbs>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restrict__ noise, int64_t noise_pitch,
               const float* __restrict__ temperature, const int32_t* __restrict__ top_k,
               const float* __restrict__ top_p, const float* __restrict__ min_p, float temperature_all,
               int top_k_all, float top_p_all, float min_p_all, int32_t* __restrict__ token,
-              float* __restrict__ probs, uint32_t* __restrict__ status, int rows, int vocab, int slice) {
+              float* __restrict__ probs, uint32_t* __restrict__ status, int rows, int vocab, int slice, int quads, bool wide) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   Shared& s = *reinterpret_cast<Shared*>(s_raw);
-  float* s_z = reinterpret_cast<float*>(s_raw + sizeof(Shared));   // this CTA's slice of the row
+  float4* const mine4 = reinterpret_cast<float4*>(s_raw + sizeof(Shared)) + threadIdx.x;   // fours, kThreads apart
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks(), tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5;
@@ -198,17 +208,38 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     if (tid == 0) set_status(status, bad ? KDA_DEVICE_BAD_PARAM : 0u);
     return;
   }
-  const int v0 = rank * slice, v1 = vocab - v0 < slice ? (vocab > v0 ? vocab : v0) : v0 + slice;
-  const int mine = v1 - v0;
-  auto nothing = [&] {  // no entry stands
+  // entry e of four q is at 4 (q kThreads + tid) + e of the slice
+  const int v0 = rank * slice, left = vocab - v0, mine = left < slice ? (left > 0 ? left : 0) : slice;
+  auto place = [&](int q) { return 4 * (q * kThreads + tid); };
+  auto get = [&](int q, float (&z)[4]) {
+    const float4 v = mine4[q * kThreads];
+    z[0] = v.x; z[1] = v.y; z[2] = v.z; z[3] = v.w;
+  };
+  float* const out = kProbs ? probs + (int64_t)row * vocab + v0 : nullptr;
+  auto put = [&](int q, const float (&o)[4]) {
+    const int i = place(q);
+    if (wide && i + 4 <= mine) {
+      *reinterpret_cast<float4*>(out + i) = make_float4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < mine) out[i + e] = o[e];
+    }
+  };
+  auto only = [&](int idx) {  // one entry stands, or none (idx < 0)
     if (kProbs) {
-      for (int i = tid; i < mine; i += kThreads) probs[(int64_t)row * vocab + v0 + i] = 0.f;
+      for (int q = 0; q < quads; ++q) {
+        float o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = v0 + place(q) + e == idx ? 1.f : 0.f;
+        put(q, o);
+      }
     } else if (rank == 0 && tid == 0) {
-      token[row] = -1;
+      token[row] = idx;
     }
   };
   if (bad_params(row)) {  // the whole cluster, as at each return below
-    nothing();
+    only(-1);
     return;
   }
   const float temp = temperature ? temperature[row] : temperature_all;
@@ -218,16 +249,31 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
 
   // every CTA of the cluster has to have started before another writes into its shared memory
   auto started = cl.barrier_arrive();
-  if (tid < 64) s.pow[tid] = c_pow[tid];
+  if (tid < 64) {
+    s.pow[tid] = c_pow[tid];
+    s.powf[tid] = (float)(uint32_t)(c_pow[tid] >> 20) * 5.9604644775390625e-8f;  // 2^-24
+  }
   Best top{kMaskedOut, 0x7fffffff};
   float low = __builtin_huge_valf();
-  const T* z = logits + (int64_t)row * pitch + v0;
-  for (int i = tid; i < mine; i += kThreads) {
-    float x = to_f32(z[i]) + 0.f;         // -0 counts as 0
-    if (x != x) x = kMaskedOut;           // and what is no number as masked
-    s_z[i] = x;
-    top = better(top, Best{x, v0 + i});
-    if (x > kMaskedOut) low = fminf(low, x);
+  const T* from = logits + (int64_t)row * pitch + v0;
+#pragma unroll 4
+  for (int q = 0; q < quads; ++q) {
+    const int i = place(q);
+    float z[4];
+    if (wide && i + 4 <= mine) {
+      load4(from + i, z);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[e] = i + e < mine ? to_f32(from[i + e]) : kMaskedOut;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      z[e] += 0.f;                              // -0 counts as 0
+      z[e] = z[e] != z[e] ? kMaskedOut : z[e];  // and what is no number as masked
+      if (z[e] > top.v) top = Best{z[e], v0 + i + e};
+      if (z[e] > kMaskedOut) low = fminf(low, z[e]);
+    }
+    mine4[q * kThreads] = make_float4(z[0], z[1], z[2], z[3]);
   }
   auto across = [&](Best b) {
 #pragma unroll
@@ -236,17 +282,17 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     return b;
   };
   // joins the cluster's best entries (every CTA has them all then)
-  auto join = [&](Best b) {
+  auto join = [&](Best b, int turn) {
     b = across(b);
     if (lane == 0) s.warp_best[warp] = b;
     __syncthreads();
     if (warp == 0) {
       b = across(lane < kWarps ? s.warp_best[lane] : Best{kMaskedOut, 0x7fffffff});
-      if (lane < ranks) cl.map_shared_rank(s.best, lane)[rank] = b;
+      if (lane < ranks) cl.map_shared_rank(s.best[turn], lane)[rank] = b;
     }
     cl.sync();
-    b = s.best[0];
-    for (int q = 1; q < ranks; ++q) b = better(b, s.best[q]);
+    b = s.best[turn][0];
+    for (int q = 1; q < ranks; ++q) b = better(b, s.best[turn][q]);
     return b;
   };
 #pragma unroll
@@ -260,70 +306,70 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     for (int o = 16; o; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
     if (lane < ranks) cl.map_shared_rank(s.low, lane)[rank] = low;
   }
-  top = join(top);
-  for (int q = 0; q < ranks; ++q) low = fminf(q ? low : s.low[0], s.low[q]);
+  top = join(top, 0);
+  low = s.low[0];
+  for (int q = 1; q < ranks; ++q) low = fminf(low, s.low[q]);
   if (top.v == kMaskedOut) {
-    nothing();
+    only(-1);
     return;
   }
   if (temp == 0.f || k == 1 || tp <= 0.f) {  // the first entry alone
-    if (kProbs) {
-      for (int i = tid; i < mine; i += kThreads) probs[(int64_t)row * vocab + v0 + i] = v0 + i == top.idx ? 1.f : 0.f;
-    } else if (rank == 0 && tid == 0) {
-      token[row] = top.idx;
-    }
+    only(top.idx);
     return;
+  }
+  if (top.v == __builtin_huge_valf()) {      // its entries share alike, no other stands
+    for (int q = 0; q < quads; ++q) {
+      float z[4];
+      get(q, z);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[e] = z[e] == top.v ? 0.f : kMaskedOut;
+      mine4[q * kThreads] = make_float4(z[0], z[1], z[2], z[3]);
+    }
+    top.v = low = 0.f;
   }
   Row r;
   r.top = top.v;
-  r.inf = top.v == __builtin_huge_valf();
   const double c = fmin(1.4426950408889634074 / (double)temp, 1e38);
   r.ch = (float)c;
   r.cl = (float)(c - (double)r.ch);
-  r.fx = 1.f;
   {  // bins over the row's range, of 64 octaves at most
-    const float range = fminf(octaves(r, low), 64.f);
-    r.fx = 4194304.f / fmaxf(range, 1e-30f);
+    const float range = fminf((top.v - low) * r.ch, 64.f);
+    r.fx = 1048576.f / fmaxf(range, 1e-30f);
   }
   const bool by_count = k > 0 && k < vocab, by_mass = tp < 1.f;
   const u64 least = mp > 0.f ? (u64)ceil((double)mp * (double)kOne) : 0;
 
-  // the entries whose digits before `depth` are p[]
+  // Digits 1 and on, for bins with many entries: p[] are those of the entry that is sought.
   int p[kPasses];
-  auto digit = [&](int d, int i, float x) -> int {
+  auto digit = [&](int d, int idx, float x) -> int {
     const uint32_t nk = down_key(x);
     switch (d) {
-      case 0: return distance(r, x) >> 11;
-      case 1: return distance(r, x) & 2047;
-      case 2: return (int)(nk >> 21);
-      case 3: return (int)((nk >> 10) & 2047);
-      case 4: return (int)(nk & 1023);
-      case 5: return (v0 + i) >> 9;
-      default: return (v0 + i) & 511;
+      case 0: return distance(r, x) >> 10;
+      case 1: return distance(r, x) & 1023;
+      case 6: return idx >> 10;
+      case 7: return idx & 1023;
+      default: return (int)(nk >> (8 * (5 - d))) & 255;
     }
   };
-  auto member = [&](int depth, int i, float x) {
-    for (int d = 0; d < depth; ++d)
-      if (digit(d, i, x) != p[d]) return false;
+  auto member = [&](int depth, int idx, float x) {
+    for (int d = 1; d < depth; ++d)
+      if (digit(d, idx, x) != p[d]) return false;
     return true;
   };
-  auto histogram = [&](int depth, Bins& b) {
+  auto add_to = [&](int at, u64 w, bool counts) {
+    if (!KDA_CHECK(at >= 0 && at < kBins)) return;
+    if (counts) atomicAdd(&s.cnt[at], 1u);
+    if (w) {
+      const uint32_t lo = (uint32_t)w, was = atomicAdd(&s.lo[at], lo);
+      const uint32_t hi = (uint32_t)(w >> 32) + (was + lo < was ? 1u : 0u);
+      if (hi) atomicAdd(&s.hi[at], hi);
+    }
+  };
+  auto clear = [&] {
     for (int i = tid; i < kBins; i += kThreads) s.cnt[i] = s.lo[i] = s.hi[i] = 0;
     __syncthreads();
-    for (int i = tid; i < mine; i += kThreads) {
-      const float x = s_z[i];
-      if (!member(depth, i, x)) continue;
-      const int at = digit(depth, i, x);
-      u64 w;
-      weight(r, x, s.pow, w);
-      if (!KDA_CHECK(at >= 0 && at < kBins)) continue;
-      atomicAdd(&s.cnt[at], 1u);
-      if (w) {
-        const uint32_t lo = (uint32_t)w, was = atomicAdd(&s.lo[at], lo);
-        const uint32_t hi = (uint32_t)(w >> 32) + (was + lo < was ? 1u : 0u);
-        if (hi) atomicAdd(&s.hi[at], hi);
-      }
-    }
+  };
+  auto gather = [&](Bins& b) {   // of all CTAs
     cl.sync();
     u64 c = 0, m = 0;
 #pragma unroll
@@ -339,23 +385,17 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
 #pragma unroll
     for (int j = 0; j < kPer; ++j) c += b.c[j], m += b.m[j];
     before_me(c, m, s, b.before_c, b.before_m);
-    if (tid == kThreads - 1) s.mass_incl = b.before_m + m;
-    __syncthreads();
-    b.total_m = s.mass_incl;
-    __syncthreads();
   };
   // the bin where the count (or mass) of the order reaches `target`
-  auto find = [&](const Bins& b, bool mass, u64 target) {
+  auto find = [&](const Bins& b, bool by, u64 target) {
     u64 bc = b.before_c, bm = b.before_m;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const u64 was = mass ? bm : bc, v = mass ? b.m[j] : b.c[j];
+      const u64 was = by ? bm : bc, v = by ? b.m[j] : b.c[j];
       if (was < target && target <= was + v) {
         s.bin = tid * kPer + j;
         s.cnt_before = bc;
         s.mass_before = bm;
-        s.cnt_in = b.c[j];
-        s.mass_in = b.m[j];
       }
       bc += b.c[j];
       bm += b.m[j];
@@ -363,57 +403,81 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     __syncthreads();
   };
   // The last entry that stands, in s.nk and s.idx, and the mass up to and with it, in s.mass_incl.
-  auto last = [&](const Bins& first, bool mass, u64 target) {
-    find(first, mass, target);
+  auto last = [&](const Bins& first, bool by, u64 target) {
+    find(first, by, target);
     int depth = 1;
     p[0] = s.bin;
-    u64 cb = s.cnt_before, mb = s.mass_before, in = s.cnt_in;
-    while (in > kList && depth < kPasses) {
-      cl.sync();   // everyone has read the histogram before
+    u64 cb = s.cnt_before, mb = s.mass_before;
+    int n;
+    for (;;) {
+      if (tid == 0) s.n = 0;
+      __syncthreads();
+#pragma unroll 2
+      for (int q = 0; q < quads; ++q) {
+        float z[4];
+        get(q, z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = place(q) + e;
+          if (distance(r, z[e]) >> 10 != p[0] || i >= mine || !member(depth, v0 + i, z[e])) continue;
+          const int at = atomicAdd(&s.n, 1);
+          if (at < kList) s.list[at] = Item{down_key(z[e]), v0 + i, mass(r, z[e], s)};
+        }
+      }
+      cl.sync();
+      n = 0;
+      for (int q = 0; q < ranks; ++q) n += cl.map_shared_rank(&s, q)->n;
+      if (n <= kList) break;
+      // too many: their next digit
+      cl.sync();
+      clear();
+      for (int q = 0; q < quads; ++q) {
+        float z[4];
+        get(q, z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = place(q) + e;
+          if (distance(r, z[e]) >> 10 != p[0] || i >= mine || !member(depth, v0 + i, z[e])) continue;
+          add_to(digit(depth, v0 + i, z[e]), mass(r, z[e], s), true);
+        }
+      }
       Bins b;
-      histogram(depth, b);
-      find(b, mass, target - (mass ? mb : cb));
+      gather(b);
+      find(b, by, target - (by ? mb : cb));
       p[depth++] = s.bin;
       cb += s.cnt_before;
       mb += s.mass_before;
-      in = s.cnt_in;
+      cl.sync();   // everyone has read the histogram
     }
-    cl.sync();     // everyone has read the histogram, and the lists of a search before
-    if (tid == 0) s.n = 0;
-    __syncthreads();
-    for (int i = tid; i < mine; i += kThreads) {
-      const float x = s_z[i];
-      if (!member(depth, i, x)) continue;
-      Item it;
-      it.nk = down_key(x);
-      it.idx = v0 + i;
-      weight(r, x, s.pow, it.w);
-      const int at = atomicAdd(&s.n, 1);
-      if (KDA_CHECK(at < kList)) s.list[at] = it;
-    }
-    cl.sync();
-    int n = 0;
+    int at = 0;
     for (int q = 0; q < ranks; ++q) {
       const Shared* o = cl.map_shared_rank(&s, q);
       const int m = o->n;
       for (int i = tid; i < m; i += kThreads)
-        if (KDA_CHECK(n + i < kList)) s.all[n + i] = o->list[i];
-      n += m;
+        if (KDA_CHECK(at + i < kList)) s.all[at + i] = o->list[i];
+      at += m;
     }
     __syncthreads();
-    const u64 want = target - (mass ? mb : cb);
-    for (int i = tid; i < n; i += kThreads) {
-      const Item it = s.all[i];
+    const u64 want = target - (by ? mb : cb);
+    // several lanes an entry where there are few
+    const int share = n <= kThreads / 8 ? 8 : n <= kThreads / 4 ? 4 : n <= kThreads / 2 ? 2 : 1;
+    for (int i0 = 0; i0 < n; i0 += kThreads / share) {
+      const int i = i0 + tid / share;
+      const Item it = s.all[i < n ? i : 0];
       u64 c = 0, m = 0;
-      for (int j = 0; j < n; ++j) {
+      for (int j = tid % share; j < n; j += share) {
         const Item o = s.all[j];
         if (o.nk < it.nk || (o.nk == it.nk && o.idx < it.idx)) {
           ++c;
           m += o.w;
         }
       }
-      const u64 was = mass ? m : c, v = mass ? it.w : 1;
-      if (was < want && want <= was + v) {
+      for (int o = 1; o < share; o *= 2) {
+        c += __shfl_xor_sync(0xffffffffu, c, o);
+        m += __shfl_xor_sync(0xffffffffu, m, o);
+      }
+      const u64 was = by ? m : c, v = by ? it.w : 1;
+      if (i < n && was < want && want <= was + v) {
         s.nk = it.nk;
         s.idx = it.idx;
         s.mass_incl = mb + m + it.w;
@@ -422,41 +486,55 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     __syncthreads();
   };
 
-  bool cut = false;
+  uint32_t nk = 0xffffffffu;
+  int at = 0x7fffffff;
   u64 sum = 0;
   if (by_count || by_mass) {
+    clear();
+    const bool masses = by_mass || kProbs;
+#pragma unroll 2
+    for (int q = 0; q < quads; ++q) {
+      float z[4];
+      get(q, z);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (place(q) + e < mine) add_to(distance(r, z[e]) >> 10, masses ? mass(r, z[e], s) : 0, by_count);
+    }
     Bins b;
-    histogram(0, b);
-    sum = b.total_m;
+    gather(b);
+    sum = s.total;
     if (by_count) {
       last(b, false, (u64)k);
       sum = s.mass_incl;
-      cut = true;
     }
     if (by_mass) {
       const double x = ceil((double)tp * (double)sum);
       u64 target = x < 1. ? 1 : (u64)x;
       if (target > sum) target = sum;
-      __syncthreads();
+      if (by_count) cl.sync();   // everyone has read the lists
       last(b, true, target);
       sum = s.mass_incl;
-      cut = true;
     }
+    nk = s.nk;
+    at = s.idx;
   }
-  const uint32_t nk = cut ? s.nk : 0xffffffffu;
-  const int at = cut ? s.idx : 0x7fffffff;
-  auto stands = [&](int i, float x, u64 w) {
+  auto stands = [&](int i, float x) {
     const uint32_t key = down_key(x);
-    return w >= least && (key < nk || (key == nk && v0 + i <= at));
+    return i < mine && (key < nk || (key == nk && v0 + i <= at));
   };
   if (kProbs) {
     if (least || !(by_count || by_mass)) {  // what min-p leaves is not known yet
       u64 part = 0;
-      for (int i = tid; i < mine; i += kThreads) {
-        u64 w;
-        const float x = s_z[i];
-        weight(r, x, s.pow, w);
-        if (stands(i, x, w)) part += w;
+#pragma unroll 2
+      for (int q = 0; q < quads; ++q) {
+        float z[4];
+        get(q, z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (!stands(place(q) + e, z[e])) continue;
+          const u64 w = mass(r, z[e], s);
+          if (w >= least) part += w;
+        }
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
@@ -475,21 +553,49 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       cl.sync();  // no CTA leaves while another reads its lists
     }
     const float inv = (float)((double)kOne / (double)sum);
-    for (int i = tid; i < mine; i += kThreads) {
-      u64 w;
-      const float x = s_z[i], pr = weight(r, x, s.pow, w);
-      probs[(int64_t)row * vocab + v0 + i] = stands(i, x, w) ? pr * inv : 0.f;
+#pragma unroll 2
+    for (int q = 0; q < quads; ++q) {
+      float z[4], o[4];
+      get(q, z);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[e] = 0.f;
+        if (stands(place(q) + e, z[e]) && (least == 0 || mass(r, z[e], s) >= least)) o[e] = weight(r, z[e], s) * inv;
+      }
+      put(q, o);
     }
   } else {
+    const float* from = noise + (int64_t)row * noise_pitch + v0;
     Best best{-1.f, 0x7fffffff};
-    for (int i = tid; i < mine; i += kThreads) {
-      u64 w;
-      const float x = s_z[i], pr = weight(r, x, s.pow, w);
-      if (pr > 0.f && stands(i, x, w))
-        best = better(best, Best{pr / noise[(int64_t)row * noise_pitch + v0 + i], v0 + i});
+    constexpr int kBatch = 4;   // fours whose noise is on its way at once
+#pragma unroll 1
+    for (int q0 = 0; q0 < quads; q0 += kBatch) {
+      float u[kBatch][4];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        float z[4];
+        if (q0 + q < quads) get(q0 + q, z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = place(q0 + q) + e;
+          u[q][e] = __builtin_nanf("");          // a score that is no number never wins
+          if (q0 + q < quads && stands(i, z[e])) u[q][e] = from[i];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        float z[4];
+        if (q0 + q < quads) get(q0 + q, z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (u[q][e] != u[q][e]) continue;
+          const float pr = weight(r, z[e], s);
+          if (pr > 0.f && (least == 0 || mass(r, z[e], s) >= least))
+            best = better(best, Best{pr / u[q][e], v0 + place(q0 + q) + e});
+        }
+      }
     }
-    cl.sync();     // everyone has read s.best, and the lists
-    best = join(best);
+    best = join(best, 1);
     if (rank == 0 && tid == 0) token[row] = best.v < 0.f ? -1 : best.idx;
   }
   KDA_DEBUG_FOLD(status);
@@ -497,22 +603,25 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
 
 template <typename T, bool kProbs>
 cudaError_t launch(const SampleArgs& a, cudaStream_t st) {
-  const int sms = gpu_sms(), vocab = a.d.vocab, rows = a.d.num_rows;
-  // a slice has to fit; below two CTAs an SM the row is shared by more
+  const int vocab = a.d.vocab, rows = a.d.num_rows, sms = gpu_sms(), e = sizeof(T);
+  constexpr int kFour = 4 * kThreads;   // entries of a four a thread
+  // CTAs a row: as many as leave 32 entries a thread, so that two CTAs fit an SM; few rows are shared by more, as
+  // long as there is a four of entries for every thread
   int ranks = 1;
-  while (ranks < kMaxRanks && ((vocab + ranks - 1) / ranks > 16384 ||
-                               ((int64_t)rows * ranks < 2 * sms && vocab / ranks > 4096)))
+  while (ranks < kMaxRanks && (vocab > ranks * 8 * kFour ||
+                               ((int64_t)rows * ranks < 2 * sms && vocab > ranks * kFour)))
     ranks *= 2;
-  const int slice = ((vocab + ranks - 1) / ranks + 7) / 8 * 8;
+  const int slice = ((vocab + ranks - 1) / ranks + 3) / 4 * 4, quads = (slice + kFour - 1) / kFour;
+  const bool wide = (uintptr_t)a.logits % (4 * e) == 0 && a.d.logits_pitch % 4 == 0 &&
+                    (!kProbs || ((uintptr_t)a.probs % 16 == 0 && vocab % 4 == 0));
   auto* kernel = sample_kernel<T, kProbs>;
-  const int bytes = (int)sizeof(Shared) + slice * 4;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(Shared) + kSliceMax * 4);
-  if (e != cudaSuccess) return e;
+  const int most = (int)sizeof(Shared) + kMostQuads * kThreads * 16;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((rows + 1) * ranks));  // (num_rows is at most 2^27)
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
+  cfg.dynamicSmemBytes = sizeof(Shared) + (size_t)quads * kThreads * 16;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -522,13 +631,13 @@ cudaError_t launch(const SampleArgs& a, cudaStream_t st) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, (const T*)a.logits, a.d.logits_pitch, a.noise, a.d.noise_pitch,
                             a.temperature, a.top_k, a.top_p, a.min_p, a.d.temperature, a.d.top_k, a.d.top_p,
-                            a.d.min_p, a.token, a.probs, a.status, rows, vocab, slice);
+                            a.d.min_p, a.token, a.probs, a.status, rows, vocab, slice, quads, wide);
 }
 
 }  // namespace
 
 bool sample_fits(const kda_sample_desc_t& d) {
-  return d.vocab <= kMaxRanks * kSliceMax && d.num_rows <= (1 << 27);
+  return d.vocab <= kMaxRanks * kMostQuads * 4 * kThreads && d.num_rows <= (1 << 27);
 }
 
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t st) {

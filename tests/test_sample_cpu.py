@@ -65,7 +65,7 @@ def test_c_boundary_refuses():
                      dict(out=FAKE + 2), dict(t=FAKE + 2), dict(k=FAKE + 1), dict(p=FAKE + 2), dict(m=FAKE + 2)):
             assert call(**over) == 1, over
         assert call(nws=128) == 3
-        assert call(_desc(vocab=344065, logits_pitch=344065, noise_pitch=344065)) == 2
+        assert call(_desc(vocab=360449, logits_pitch=360449, noise_pitch=360449)) == 2
         assert call(_desc(num_rows=(1 << 27) + 1)) == 2
     assert sample(noise=None) == 1 and sample(_desc(noise_pitch=V - 1)) == 1 and sample(noise=FAKE + 2) == 1
 
