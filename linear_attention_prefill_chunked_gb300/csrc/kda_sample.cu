@@ -15,7 +15,7 @@
 // An entry next to top-p's border stands or falls with the last digits of a sum over the row, so masses
 // are whole numbers, p in units of 2^-44, whose sums do not depend on their order: results are bit-identical
 // from run to run, whichever CTA adds first. p itself is 2^-n 2^(-j/64) 2^-r from a table and three terms of the
-// exponential series, the distance carried as two floats: good to 2^-31, where a float's sum of a
+// exponential series, the distance carried as two floats: good to 2^-30, where a float's sum of a
 // vocabulary would be off by more than the smallest entries that stand.
 //
 // Bound by HBM in principle (the row, and noise or probabilities), by the arithmetic of p and the cluster's
@@ -38,7 +38,7 @@ constexpr int kPer = kBins / kThreads;     // bins a thread looks after
 constexpr int kList = 1024;                // entries that are ranked against each other
 constexpr int kMaxRanks = 8;
 constexpr int kMostQuads = 22;             // fours of entries a thread looks after at most
-constexpr int kPasses = 8;                 // digits: two of the distance, four of the value, two of the index
+constexpr int kPasses = 7;                 // digits: the distance, four of the value, two of the index
 constexpr int kOneBits = 44;
 constexpr unsigned long long kOne = 1ull << kOneBits;
 constexpr float kMaskedOut = -__builtin_huge_valf();
@@ -78,21 +78,28 @@ __device__ __forceinline__ Best better(Best a, Best b) {  // of equal values the
 }
 
 struct alignas(16) Shared {
-  uint32_t cnt[kBins], lo[kBins], hi[kBins];
+  union {
+    struct {
+      uint32_t cnt[kBins], part[3][kBins];   // of masses, 16 bits and 16 and the rest: sums of a CTA fit 32 bits
+    };
+    Item all[kList];     // the cluster's entries of the bin
+  };
   Item list[kList];      // this CTA's entries of the bin
-  Item all[kList];       // the cluster's
   u64 pow[64];
   float powf[64];
   Best warp_best[kWarps], best[2][kMaxRanks];
   float warp_low[kWarps], low[kMaxRanks];
   u64 warp_cnt[kWarps], warp_mass[kWarps], sum[kMaxRanks];
   u64 cnt_before, mass_before, total;   // what lies before the bin that was found; all mass
-  int bin, n;
+  int bin, n, counts[kMaxRanks];
   uint32_t nk;                          // the last entry that stands,
   int idx;
   u64 mass_incl;                        // and the mass up to and with it
+  float ch, cl, inv;                    // what is worked out in 64 bits, by one thread
+  u64 least, target;
 };
 
+static_assert(kMostQuads * 4 * kThreads < 65536, "sums of 16 bits");
 static_assert(sizeof(Shared) + kMostQuads * kThreads * 16 <= 232448, "227 KB a CTA");
 
 // A row's parameters and what follows from them.
@@ -104,9 +111,12 @@ __device__ __forceinline__ uint32_t down_key(float z) {
   const uint32_t b = __float_as_uint(z);
   return (b >> 31) ? b : ~(b | 0x80000000u);
 }
-__device__ __forceinline__ int distance(const Row& r, float z) {  // 20 bits, never falling as z falls
-  const float y = (r.top - z) * r.ch * r.fx;
-  return y < 1048575.f ? (int)y : 1048575;
+// The bin of an entry by its distance from the maximum, never falling as z falls (1.5 * 2^23 rounds to whole
+// numbers).
+constexpr float kRound = 12582912.f;
+constexpr int kRoundBits = 0x4b400000;
+__device__ __forceinline__ int distance(const Row& r, float z) {
+  return __float_as_int(fminf((r.top - z) * r.ch * r.fx, (float)(kBins - 1)) + kRound) - kRoundBits;
 }
 // p = 2^-n 2^(-j/64) (1 + e)
 struct Power {
@@ -118,9 +128,9 @@ __device__ __forceinline__ bool power(const Row& r, float z, Power& o) {
   if (!(yh < 126.f)) return false;       // masked entries too
   const float b = d - r.top, dl = (r.top - (d - b)) - (z + b);
   const float yl = fmaf(d, r.ch, -yh) + fmaf(d, r.cl, dl * r.ch);
-  const float m = fmaf(yh, 64.f, 12582912.f);   // 1.5 * 2^23: rounds to whole numbers
-  const int k = __float_as_int(m) - 0x4b400000;
-  const float t = (fmaf(m - 12582912.f, -1.f / 64.f, yh) + yl) * -0.69314718055994531f;
+  const float m = fmaf(yh, 64.f, kRound);
+  const int k = __float_as_int(m) - kRoundBits;
+  const float t = (fmaf(m - kRound, -1.f / 64.f, yh) + yl) * -0.69314718055994531f;
   o.n = k >> 6;
   o.j = k & 63;
   o.e = t * fmaf(t, fmaf(t, 1.f / 6.f, 0.5f), 1.f);
@@ -130,8 +140,8 @@ __device__ __forceinline__ bool power(const Row& r, float z, Power& o) {
 __device__ __forceinline__ u64 mass(const Row& r, float z, const Shared& s) {
   Power p;
   if (!power(r, z, p) || p.n >= 45) return 0;
-  const int fine = __float2int_rn(s.powf[p.j] * p.e * 137438953472.f);  // of 2^37
-  return (s.pow[p.j] + ((u64)(long long)fine << 7)) >> p.n;
+  const int fine = __float_as_int(fmaf(s.powf[p.j] * p.e, 536870912.f, kRound)) - kRoundBits;  // of 2^29, |e| < 0.0055
+  return (s.pow[p.j] + ((u64)(long long)fine << 15)) >> p.n;
 }
 __device__ __forceinline__ float weight(const Row& r, float z, const Shared& s) {
   Power p;
@@ -245,7 +255,13 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   const float temp = temperature ? temperature[row] : temperature_all;
   const int k = top_k ? top_k[row] : top_k_all;
   const float tp = top_p ? top_p[row] : top_p_all;
-  const float mp = fminf(min_p ? min_p[row] : min_p_all, 1.f);
+  if (tid == 0) {
+    const double c = fmin(1.4426950408889634074 / (double)temp, 1e38);   // (at temperature 0 not used)
+    s.ch = (float)c;
+    s.cl = (float)(c - (double)s.ch);
+    const float mp = fminf(min_p ? min_p[row] : min_p_all, 1.f);
+    s.least = mp > 0.f ? (u64)ceil((double)mp * (double)kOne) : 0;
+  }
 
   // every CTA of the cluster has to have started before another writes into its shared memory
   auto started = cl.barrier_arrive();
@@ -329,27 +345,17 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   }
   Row r;
   r.top = top.v;
-  const double c = fmin(1.4426950408889634074 / (double)temp, 1e38);
-  r.ch = (float)c;
-  r.cl = (float)(c - (double)r.ch);
-  {  // bins over the row's range, of 64 octaves at most
-    const float range = fminf((top.v - low) * r.ch, 64.f);
-    r.fx = 1048576.f / fmaxf(range, 1e-30f);
-  }
+  r.ch = s.ch;
+  r.cl = s.cl;
+  r.fx = (kBins - 1) / fmaxf(fminf((top.v - low) * r.ch, 64.f), 1e-30f);  // over the row's range, 64 octaves at most
   const bool by_count = k > 0 && k < vocab, by_mass = tp < 1.f;
-  const u64 least = mp > 0.f ? (u64)ceil((double)mp * (double)kOne) : 0;
+  const u64 least = s.least;
 
   // Digits 1 and on, for bins with many entries: p[] are those of the entry that is sought.
   int p[kPasses];
   auto digit = [&](int d, int idx, float x) -> int {
     const uint32_t nk = down_key(x);
-    switch (d) {
-      case 0: return distance(r, x) >> 10;
-      case 1: return distance(r, x) & 1023;
-      case 6: return idx >> 10;
-      case 7: return idx & 1023;
-      default: return (int)(nk >> (8 * (5 - d))) & 255;
-    }
+    return d < 5 ? (int)(nk >> (8 * (4 - d))) & 255 : d == 5 ? idx >> 10 : idx & 1023;
   };
   auto member = [&](int depth, int idx, float x) {
     for (int d = 1; d < depth; ++d)
@@ -359,14 +365,13 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   auto add_to = [&](int at, u64 w, bool counts) {
     if (!KDA_CHECK(at >= 0 && at < kBins)) return;
     if (counts) atomicAdd(&s.cnt[at], 1u);
-    if (w) {
-      const uint32_t lo = (uint32_t)w, was = atomicAdd(&s.lo[at], lo);
-      const uint32_t hi = (uint32_t)(w >> 32) + (was + lo < was ? 1u : 0u);
-      if (hi) atomicAdd(&s.hi[at], hi);
-    }
+    const uint32_t lo = (uint32_t)w, hi = (uint32_t)(w >> 32);
+    if (lo & 0xffff) atomicAdd(&s.part[0][at], lo & 0xffff);
+    if (lo >> 16) atomicAdd(&s.part[1][at], lo >> 16);
+    if (hi) atomicAdd(&s.part[2][at], hi);
   };
   auto clear = [&] {
-    for (int i = tid; i < kBins; i += kThreads) s.cnt[i] = s.lo[i] = s.hi[i] = 0;
+    for (int i = tid; i < kBins; i += kThreads) s.cnt[i] = s.part[0][i] = s.part[1][i] = s.part[2][i] = 0;
     __syncthreads();
   };
   auto gather = [&](Bins& b) {   // of all CTAs
@@ -374,12 +379,24 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     u64 c = 0, m = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) b.c[j] = 0, b.m[j] = 0;
-    for (int q = 0; q < ranks; ++q) {
-      const Shared* o = cl.map_shared_rank(&s, q);
+    static_assert(kPer == 2, "a thread's bins are one 8-byte access");
+#pragma unroll 1
+    for (int q0 = 0; q0 < ranks; q0 += 4) {
+      uint2 v[4][4];   // all on their way at once
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        b.c[j] += o->cnt[tid * kPer + j];
-        b.m[j] += (u64)o->hi[tid * kPer + j] << 32 | o->lo[tid * kPer + j];
+      for (int q = 0; q < 4; ++q) {
+        const Shared* o = cl.map_shared_rank(&s, q0 + q < ranks ? q0 + q : rank);
+        v[q][0] = reinterpret_cast<const uint2*>(o->cnt)[tid];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) v[q][1 + i] = reinterpret_cast<const uint2*>(o->part[i])[tid];
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q0 + q >= ranks) continue;
+        b.c[0] += v[q][0].x;
+        b.c[1] += v[q][0].y;
+        b.m[0] += v[q][1].x + ((u64)v[q][2].x << 16) + ((u64)v[q][3].x << 32);
+        b.m[1] += v[q][1].y + ((u64)v[q][2].y << 16) + ((u64)v[q][3].y << 32);
       }
     }
 #pragma unroll
@@ -419,14 +436,16 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = place(q) + e;
-          if (distance(r, z[e]) >> 10 != p[0] || i >= mine || !member(depth, v0 + i, z[e])) continue;
+          if (distance(r, z[e]) != p[0] || i >= mine || !member(depth, v0 + i, z[e])) continue;
           const int at = atomicAdd(&s.n, 1);
           if (at < kList) s.list[at] = Item{down_key(z[e]), v0 + i, mass(r, z[e], s)};
         }
       }
+      __syncthreads();
+      if (tid < ranks) cl.map_shared_rank(&s, tid)->counts[rank] = s.n;
       cl.sync();
       n = 0;
-      for (int q = 0; q < ranks; ++q) n += cl.map_shared_rank(&s, q)->n;
+      for (int q = 0; q < ranks; ++q) n += s.counts[q];
       if (n <= kList) break;
       // too many: their next digit
       cl.sync();
@@ -437,7 +456,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = place(q) + e;
-          if (distance(r, z[e]) >> 10 != p[0] || i >= mine || !member(depth, v0 + i, z[e])) continue;
+          if (distance(r, z[e]) != p[0] || i >= mine || !member(depth, v0 + i, z[e])) continue;
           add_to(digit(depth, v0 + i, z[e]), mass(r, z[e], s), true);
         }
       }
@@ -449,13 +468,10 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       mb += s.mass_before;
       cl.sync();   // everyone has read the histogram
     }
-    int at = 0;
-    for (int q = 0; q < ranks; ++q) {
-      const Shared* o = cl.map_shared_rank(&s, q);
-      const int m = o->n;
-      for (int i = tid; i < m; i += kThreads)
-        if (KDA_CHECK(at + i < kList)) s.all[at + i] = o->list[i];
-      at += m;
+    for (int i = tid; i < n; i += kThreads) {
+      int q = 0, j = i;
+      while (j >= s.counts[q]) j -= s.counts[q++];
+      if (KDA_CHECK(i < kList && q < ranks)) s.all[i] = cl.map_shared_rank(&s, q)->list[j];
     }
     __syncthreads();
     const u64 want = target - (by ? mb : cb);
@@ -489,41 +505,47 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   uint32_t nk = 0xffffffffu;
   int at = 0x7fffffff;
   u64 sum = 0;
-  if (by_count || by_mass) {
+  auto stands = [&](int i, float x) {
+    const uint32_t key = down_key(x);
+    return i < mine && (key < nk || (key == nk && v0 + i <= at));
+  };
+  // what stands into a histogram, by number or by mass
+  auto histogram = [&](Bins& b, bool by) {
     clear();
-    const bool masses = by_mass || kProbs;
 #pragma unroll 2
     for (int q = 0; q < quads; ++q) {
       float z[4];
       get(q, z);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (place(q) + e < mine) add_to(distance(r, z[e]) >> 10, masses ? mass(r, z[e], s) : 0, by_count);
+        if (stands(place(q) + e, z[e])) add_to(distance(r, z[e]), by ? mass(r, z[e], s) : 0, !by);
     }
-    Bins b;
     gather(b);
-    sum = s.total;
-    if (by_count) {
-      last(b, false, (u64)k);
-      sum = s.mass_incl;
+  };
+  if (by_count) {
+    Bins b;
+    histogram(b, false);
+    last(b, false, (u64)k);
+    nk = s.nk;
+    at = s.idx;
+    if (by_mass) cl.sync();     // everyone has read the lists, and what lies in their place
+  }
+  if (by_mass) {
+    Bins b;
+    histogram(b, true);
+    if (tid == 0) {
+      const double x = ceil((double)tp * (double)s.total);
+      const u64 target = x < 1. ? 1 : (u64)x;
+      s.target = target < s.total ? target : s.total;
     }
-    if (by_mass) {
-      const double x = ceil((double)tp * (double)sum);
-      u64 target = x < 1. ? 1 : (u64)x;
-      if (target > sum) target = sum;
-      if (by_count) cl.sync();   // everyone has read the lists
-      last(b, true, target);
-      sum = s.mass_incl;
-    }
+    __syncthreads();
+    last(b, true, s.target);
+    sum = s.mass_incl;
     nk = s.nk;
     at = s.idx;
   }
-  auto stands = [&](int i, float x) {
-    const uint32_t key = down_key(x);
-    return i < mine && (key < nk || (key == nk && v0 + i <= at));
-  };
   if (kProbs) {
-    if (least || !(by_count || by_mass)) {  // what min-p leaves is not known yet
+    if (least || !by_mass) {  // the mass of what stands is not known yet
       u64 part = 0;
 #pragma unroll 2
       for (int q = 0; q < quads; ++q) {
@@ -552,7 +574,9 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     } else {
       cl.sync();  // no CTA leaves while another reads its lists
     }
-    const float inv = (float)((double)kOne / (double)sum);
+    if (tid == 0) s.inv = (float)((double)kOne / (double)sum);
+    __syncthreads();
+    const float inv = s.inv;
 #pragma unroll 2
     for (int q = 0; q < quads; ++q) {
       float z[4], o[4];
