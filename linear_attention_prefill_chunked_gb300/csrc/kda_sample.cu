@@ -34,7 +34,7 @@ KDA_DEBUG_FLAG_DEFINE();
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
-constexpr int kPer = kBins / kThreads;     // bins a thread looks after
+constexpr int kFine = 32, kCoarse = kBins / kFine;   // bins are looked through in two steps
 constexpr int kList = 1024;                // entries that are ranked against each other
 constexpr int kMaxRanks = 8;
 constexpr int kMostQuads = 22;             // fours of entries a thread looks after at most
@@ -89,9 +89,9 @@ struct alignas(16) Shared {
   float powf[64];
   Best warp_best[kWarps], best[2][kMaxRanks];
   float warp_low[kWarps], low[kMaxRanks];
-  u64 warp_cnt[kWarps], warp_mass[kWarps], sum[kMaxRanks];
-  u64 cnt_before, mass_before, total;   // what lies before the bin that was found; all mass
-  int bin, n, counts[kMaxRanks];
+  u64 coarse[kMaxRanks][kCoarse], fine[kMaxRanks][kFine];   // each CTA's sums, of its bins by 32 and of 32 of its bins
+  u64 warp_mass[kWarps], sum[kMaxRanks];
+  int n, counts[kMaxRanks];             // entries of the bin, here and in each CTA
   uint32_t nk;                          // the last entry that stands,
   int idx;
   u64 mass_incl;                        // and the mass up to and with it
@@ -149,45 +149,6 @@ __device__ __forceinline__ float weight(const Row& r, float z, const Shared& s) 
   const float h = s.powf[p.j];
   return fmaf(h, p.e, h) * __uint_as_float((uint32_t)(127 - p.n) << 23);
 }
-
-// Sum over the threads before this one, of two numbers.
-__device__ __forceinline__ void before_me(u64 c, u64 m, Shared& s, u64& bc, u64& bm) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  u64 ic = c, im = m;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const u64 a = __shfl_up_sync(0xffffffffu, ic, o), b = __shfl_up_sync(0xffffffffu, im, o);
-    if (lane >= o) {
-      ic += a;
-      im += b;
-    }
-  }
-  if (lane == 31) {
-    s.warp_cnt[warp] = ic;
-    s.warp_mass[warp] = im;
-  }
-  __syncthreads();
-  bc = ic - c;
-  bm = im - m;
-  u64 tm = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const u64 wc = s.warp_cnt[w], wm = s.warp_mass[w];
-    if (w < warp) {
-      bc += wc;
-      bm += wm;
-    }
-    tm += wm;
-  }
-  if (threadIdx.x == 0) s.total = tm;
-  __syncthreads();
-}
-
-// The cluster's histogram: this thread's bins and what lies in the bins before them.
-struct Bins {
-  uint32_t c[kPer];
-  u64 m[kPer], before_c, before_m;
-};
 
 // One row a cluster, `quads` fours of entries a thread. kProbs: probabilities, else a token.
 template <typename T, bool kProbs>
@@ -351,6 +312,13 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   const bool by_count = k > 0 && k < vocab, by_mass = tp < 1.f;
   const u64 least = s.least;
 
+  uint32_t nk = 0xffffffffu;
+  int at = 0x7fffffff;
+  u64 sum = 0;
+  auto stands = [&](int i, float x) {
+    const uint32_t key = down_key(x);
+    return i < mine && (key < nk || (key == nk && v0 + i <= at));
+  };
   // Digits 1 and on, for bins with many entries: p[] are those of the entry that is sought.
   int p[kPasses];
   auto digit = [&](int d, int idx, float x) -> int {
@@ -374,58 +342,60 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     for (int i = tid; i < kBins; i += kThreads) s.cnt[i] = s.part[0][i] = s.part[1][i] = s.part[2][i] = 0;
     __syncthreads();
   };
-  auto gather = [&](Bins& b) {   // of all CTAs
-    cl.sync();
-    u64 c = 0, m = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) b.c[j] = 0, b.m[j] = 0;
-    static_assert(kPer == 2, "a thread's bins are one 8-byte access");
-#pragma unroll 1
-    for (int q0 = 0; q0 < ranks; q0 += 4) {
-      uint2 v[4][4];   // all on their way at once
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const Shared* o = cl.map_shared_rank(&s, q0 + q < ranks ? q0 + q : rank);
-        v[q][0] = reinterpret_cast<const uint2*>(o->cnt)[tid];
-#pragma unroll
-        for (int i = 0; i < 3; ++i) v[q][1 + i] = reinterpret_cast<const uint2*>(o->part[i])[tid];
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (q0 + q >= ranks) continue;
-        b.c[0] += v[q][0].x;
-        b.c[1] += v[q][0].y;
-        b.m[0] += v[q][1].x + ((u64)v[q][2].x << 16) + ((u64)v[q][3].x << 32);
-        b.m[1] += v[q][1].y + ((u64)v[q][2].y << 16) + ((u64)v[q][3].y << 32);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) c += b.c[j], m += b.m[j];
-    before_me(c, m, s, b.before_c, b.before_m);
+  auto sum_of = [&](int bin, bool by) -> u64 {
+    return by ? s.part[0][bin] + ((u64)s.part[1][bin] << 16) + ((u64)s.part[2][bin] << 32) : s.cnt[bin];
   };
-  // the bin where the count (or mass) of the order reaches `target`
-  auto find = [&](const Bins& b, bool by, u64 target) {
-    u64 bc = b.before_c, bm = b.before_m;
+  // the lane whose entry of sums takes what lies before it up to `target`, and what lies before that
+  auto find = [&](u64 v, u64 target, u64& before, u64& total) {
+    u64 up_to = v;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const u64 was = by ? bm : bc, v = by ? b.m[j] : b.c[j];
-      if (was < target && target <= was + v) {
-        s.bin = tid * kPer + j;
-        s.cnt_before = bc;
-        s.mass_before = bm;
-      }
-      bc += b.c[j];
-      bm += b.m[j];
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 x = __shfl_up_sync(0xffffffffu, up_to, o);
+      if (lane >= o) up_to += x;
     }
+    total = __shfl_sync(0xffffffffu, up_to, 31);
+    const unsigned hit = __ballot_sync(0xffffffffu, up_to >= target);
+    const int at = hit ? __ffs(hit) - 1 : 31;
+    before = __shfl_sync(0xffffffffu, up_to - v, at);
+    return at;
+  };
+  // The bin of the cluster's histogram (filled, in each CTA) where the count or the mass reaches `target`, and what
+  // lies in the bins before it. A target of 0 stands for top-p of all mass, and is set.
+  auto search = [&](bool by, u64& target, u64& before) {
     __syncthreads();
+    for (int g = warp; g < kCoarse; g += kWarps) {
+      u64 v = sum_of(g * kFine + lane, by);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane < ranks) cl.map_shared_rank(&s, lane)->coarse[rank][g] = v;
+    }
+    cl.sync();
+    u64 v = 0, total, rest;
+    for (int q = 0; q < ranks; ++q) v += s.coarse[q][lane];
+    if (target == 0) {
+      find(v, 0, before, total);
+      if (tid == 0) {
+        const double x = ceil((double)tp * (double)total);
+        const u64 t = x < 1. ? 1 : (u64)x;
+        s.target = t < total ? t : total;
+      }
+      __syncthreads();
+      target = s.target;
+    }
+    const int g = find(v, target, before, total);
+    if (warp < ranks) cl.map_shared_rank(&s, warp)->fine[rank][lane] = sum_of(g * kFine + lane, by);
+    cl.sync();
+    v = 0;
+    for (int q = 0; q < ranks; ++q) v += s.fine[q][lane];
+    const int bin = g * kFine + find(v, target - before, rest, total);
+    before += rest;
+    return bin;
   };
-  // The last entry that stands, in s.nk and s.idx, and the mass up to and with it, in s.mass_incl.
-  auto last = [&](const Bins& first, bool by, u64 target) {
-    find(first, by, target);
-    int depth = 1;
-    p[0] = s.bin;
-    u64 cb = s.cnt_before, mb = s.mass_before;
-    int n;
+  // The last entry that stands, in s.nk and s.idx, and the mass up to and with it, in s.mass_incl (by mass).
+  auto last = [&](bool by, u64 target) {
+    u64 before;                   // what lies before the entries whose digits are p[0] .. p[depth - 1]
+    p[0] = search(by, target, before);
+    int depth = 1, n;
     for (;;) {
       if (tid == 0) s.n = 0;
       __syncthreads();
@@ -436,9 +406,9 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = place(q) + e;
-          if (distance(r, z[e]) != p[0] || i >= mine || !member(depth, v0 + i, z[e])) continue;
+          if (distance(r, z[e]) != p[0] || !stands(i, z[e]) || !member(depth, v0 + i, z[e])) continue;
           const int at = atomicAdd(&s.n, 1);
-          if (at < kList) s.list[at] = Item{down_key(z[e]), v0 + i, mass(r, z[e], s)};
+          if (at < kList) s.list[at] = Item{down_key(z[e]), v0 + i, by ? mass(r, z[e], s) : 1};
         }
       }
       __syncthreads();
@@ -448,7 +418,6 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       for (int q = 0; q < ranks; ++q) n += s.counts[q];
       if (n <= kList) break;
       // too many: their next digit
-      cl.sync();
       clear();
       for (int q = 0; q < quads; ++q) {
         float z[4];
@@ -456,17 +425,13 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = place(q) + e;
-          if (distance(r, z[e]) != p[0] || i >= mine || !member(depth, v0 + i, z[e])) continue;
-          add_to(digit(depth, v0 + i, z[e]), mass(r, z[e], s), true);
+          if (distance(r, z[e]) != p[0] || !stands(i, z[e]) || !member(depth, v0 + i, z[e])) continue;
+          add_to(digit(depth, v0 + i, z[e]), by ? mass(r, z[e], s) : 0, !by);
         }
       }
-      Bins b;
-      gather(b);
-      find(b, by, target - (by ? mb : cb));
-      p[depth++] = s.bin;
-      cb += s.cnt_before;
-      mb += s.mass_before;
-      cl.sync();   // everyone has read the histogram
+      u64 rest = target - before, low_part;
+      p[depth++] = search(by, rest, low_part);
+      before += low_part;
     }
     for (int i = tid; i < n; i += kThreads) {
       int q = 0, j = i;
@@ -474,43 +439,29 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       if (KDA_CHECK(i < kList && q < ranks)) s.all[i] = cl.map_shared_rank(&s, q)->list[j];
     }
     __syncthreads();
-    const u64 want = target - (by ? mb : cb);
+    const u64 want = target - before;
     // several lanes an entry where there are few
     const int share = n <= kThreads / 8 ? 8 : n <= kThreads / 4 ? 4 : n <= kThreads / 2 ? 2 : 1;
     for (int i0 = 0; i0 < n; i0 += kThreads / share) {
       const int i = i0 + tid / share;
       const Item it = s.all[i < n ? i : 0];
-      u64 c = 0, m = 0;
+      u64 was = 0;
       for (int j = tid % share; j < n; j += share) {
         const Item o = s.all[j];
-        if (o.nk < it.nk || (o.nk == it.nk && o.idx < it.idx)) {
-          ++c;
-          m += o.w;
-        }
+        if (o.nk < it.nk || (o.nk == it.nk && o.idx < it.idx)) was += o.w;
       }
-      for (int o = 1; o < share; o *= 2) {
-        c += __shfl_xor_sync(0xffffffffu, c, o);
-        m += __shfl_xor_sync(0xffffffffu, m, o);
-      }
-      const u64 was = by ? m : c, v = by ? it.w : 1;
-      if (i < n && was < want && want <= was + v) {
+      for (int o = 1; o < share; o *= 2) was += __shfl_xor_sync(0xffffffffu, was, o);
+      if (i < n && was < want && want <= was + it.w) {
         s.nk = it.nk;
         s.idx = it.idx;
-        s.mass_incl = mb + m + it.w;
+        s.mass_incl = before + was + it.w;
       }
     }
     __syncthreads();
   };
 
-  uint32_t nk = 0xffffffffu;
-  int at = 0x7fffffff;
-  u64 sum = 0;
-  auto stands = [&](int i, float x) {
-    const uint32_t key = down_key(x);
-    return i < mine && (key < nk || (key == nk && v0 + i <= at));
-  };
   // what stands into a histogram, by number or by mass
-  auto histogram = [&](Bins& b, bool by) {
+  auto histogram = [&](bool by) {
     clear();
 #pragma unroll 2
     for (int q = 0; q < quads; ++q) {
@@ -520,26 +471,17 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       for (int e = 0; e < 4; ++e)
         if (stands(place(q) + e, z[e])) add_to(distance(r, z[e]), by ? mass(r, z[e], s) : 0, !by);
     }
-    gather(b);
   };
   if (by_count) {
-    Bins b;
-    histogram(b, false);
-    last(b, false, (u64)k);
+    histogram(false);
+    last(false, (u64)k);
     nk = s.nk;
     at = s.idx;
-    if (by_mass) cl.sync();     // everyone has read the lists, and what lies in their place
+    __syncthreads();
   }
   if (by_mass) {
-    Bins b;
-    histogram(b, true);
-    if (tid == 0) {
-      const double x = ceil((double)tp * (double)s.total);
-      const u64 target = x < 1. ? 1 : (u64)x;
-      s.target = target < s.total ? target : s.total;
-    }
-    __syncthreads();
-    last(b, true, s.target);
+    histogram(true);
+    last(true, 0);
     sum = s.mass_incl;
     nk = s.nk;
     at = s.idx;
