@@ -92,7 +92,7 @@ struct alignas(16) Shared {
   u64 coarse[kMaxRanks][kCoarse], fine[kMaxRanks][kFine];   // each CTA's sums, of its bins by 32 and of 32 of its bins
   u64 warp_mass[kWarps], sum[kMaxRanks];
   int n, counts[kMaxRanks];             // entries of the bin, here and in each CTA
-  uint32_t nk;                          // the last entry that stands,
+  uint32_t nk;                          // the entry that was sought,
   int idx;
   u64 mass_incl;                        // and the mass up to and with it
   float ch, cl, inv;                    // what is worked out in 64 bits, by one thread
@@ -118,36 +118,33 @@ constexpr int kRoundBits = 0x4b400000;
 __device__ __forceinline__ int distance(const Row& r, float z) {
   return __float_as_int(fminf((r.top - z) * r.ch * r.fx, (float)(kBins - 1)) + kRound) - kRoundBits;
 }
-// p = 2^-n 2^(-j/64) (1 + e)
-struct Power {
-  int n, j;
-  float e;
-};
-__device__ __forceinline__ bool power(const Row& r, float z, Power& o) {
-  const float d = r.top - z, yh = d * r.ch;
-  if (!(yh < 126.f)) return false;       // masked entries too
-  const float b = d - r.top, dl = (r.top - (d - b)) - (z + b);
-  const float yl = fmaf(d, r.ch, -yh) + fmaf(d, r.cl, dl * r.ch);
-  const float m = fmaf(yh, 64.f, kRound);
-  const int k = __float_as_int(m) - kRoundBits;
-  const float t = (fmaf(m - kRound, -1.f / 64.f, yh) + yl) * -0.69314718055994531f;
-  o.n = k >> 6;
-  o.j = k & 63;
-  o.e = t * fmaf(t, fmaf(t, 1.f / 6.f, 0.5f), 1.f);
-  return true;
+// The distance from the maximum in octaves of p, as two floats.
+__device__ __forceinline__ void octaves(const Row& r, float z, float& yh, float& yl) {
+  const float d = r.top - z, b = d - r.top, dl = (r.top - (d - b)) - (z + b);
+  yh = d * r.ch;
+  yl = fmaf(d, r.ch, -yh) + fmaf(d, r.cl, dl * r.ch);
 }
-// p in units of 2^-44
+// p = 2^-n 2^(-j/64) (1 + e) in units of 2^-44; 0 for masked entries.
 __device__ __forceinline__ u64 mass(const Row& r, float z, const Shared& s) {
-  Power p;
-  if (!power(r, z, p) || p.n >= 45) return 0;
-  const int fine = __float_as_int(fmaf(s.powf[p.j] * p.e, 536870912.f, kRound)) - kRoundBits;  // of 2^29, |e| < 0.0055
-  return (s.pow[p.j] + ((u64)(long long)fine << 15)) >> p.n;
+  float yh, yl;
+  octaves(r, z, yh, yl);
+  const float m = fmaf(yh, 64.f, kRound);
+  const int k = __float_as_int(m) - kRoundBits, n = k >> 6, j = k & 63;
+  const float t = (fmaf(m - kRound, -1.f / 64.f, yh) + yl) * -0.69314718055994531f;
+  const float e = t * fmaf(t, fmaf(t, 1.f / 6.f, 0.5f), 1.f);          // |e| < 0.0055
+  const int fine = __float_as_int(fmaf(s.powf[j] * e, 536870912.f, kRound)) - kRoundBits;  // of 2^29
+  return yh < 45.f ? (s.pow[j] + ((u64)(long long)fine << 15)) >> n : 0;
 }
-__device__ __forceinline__ float weight(const Row& r, float z, const Shared& s) {
-  Power p;
-  if (!power(r, z, p)) return 0.f;
-  const float h = s.powf[p.j];
-  return fmaf(h, p.e, h) * __uint_as_float((uint32_t)(127 - p.n) << 23);
+// p to 2^-22
+__device__ __forceinline__ float weight(const Row& r, float z) {
+  float yh, yl;
+  octaves(r, z, yh, yl);
+  float p;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(-yh));
+  return yh < 126.f ? fmaf(p, yl * -0.69314718055994531f, p) : 0.f;
+}
+__device__ __forceinline__ float value_of(uint32_t nk) {   // of a descending key
+  return __uint_as_float((nk >> 31) ? nk : ~nk & 0x7fffffffu);
 }
 
 // One row a cluster, `quads` fours of entries a thread. kProbs: probabilities, else a token.
@@ -312,13 +309,11 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   const bool by_count = k > 0 && k < vocab, by_mass = tp < 1.f;
   const u64 least = s.least;
 
-  uint32_t nk = 0xffffffffu;
-  int at = 0x7fffffff;
+  // What stands so far: entries above `border`, and those that equal it up to index `at`. Masked ones never do.
+  float border = kMaskedOut;
+  int at = -1;
   u64 sum = 0;
-  auto stands = [&](int i, float x) {
-    const uint32_t key = down_key(x);
-    return i < mine && (key < nk || (key == nk && v0 + i <= at));
-  };
+  auto stands = [&](int i, float x) { return x > border || (x == border && v0 + i <= at); };
   // Digits 1 and on, for bins with many entries: p[] are those of the entry that is sought.
   int p[kPasses];
   auto digit = [&](int d, int idx, float x) -> int {
@@ -360,7 +355,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     return at;
   };
   // The bin of the cluster's histogram (filled, in each CTA) where the count or the mass reaches `target`, and what
-  // lies in the bins before it. A target of 0 stands for top-p of all mass, and is set.
+  // lies in the bins before it; -1 if it does not. A target of 0 stands for top-p of all mass, and is set.
   auto search = [&](bool by, u64& target, u64& before) {
     __syncthreads();
     for (int g = warp; g < kCoarse; g += kWarps) {
@@ -383,6 +378,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       target = s.target;
     }
     const int g = find(v, target, before, total);
+    if (total < target) return -1;
     if (warp < ranks) cl.map_shared_rank(&s, warp)->fine[rank][lane] = sum_of(g * kFine + lane, by);
     cl.sync();
     v = 0;
@@ -391,10 +387,12 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     before += rest;
     return bin;
   };
-  // The last entry that stands, in s.nk and s.idx, and the mass up to and with it, in s.mass_incl (by mass).
-  auto last = [&](bool by, u64 target) {
+  // Cuts what stands off behind the entry with which its number, or its mass, reaches `target`; the mass up to
+  // and with that is in s.mass_incl then (by mass).
+  auto cut = [&](bool by, u64 target) {
     u64 before;                   // what lies before the entries whose digits are p[0] .. p[depth - 1]
     p[0] = search(by, target, before);
+    if (p[0] < 0) return;
     int depth = 1, n;
     for (;;) {
       if (tid == 0) s.n = 0;
@@ -458,6 +456,9 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       }
     }
     __syncthreads();
+    border = value_of(s.nk);
+    at = s.idx;
+    sum = s.mass_incl;
   };
 
   // what stands into a histogram, by number or by mass
@@ -474,17 +475,12 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   };
   if (by_count) {
     histogram(false);
-    last(false, (u64)k);
-    nk = s.nk;
-    at = s.idx;
+    cut(false, (u64)k);
     __syncthreads();
   }
   if (by_mass) {
     histogram(true);
-    last(true, 0);
-    sum = s.mass_incl;
-    nk = s.nk;
-    at = s.idx;
+    cut(true, 0);
   }
   if (kProbs) {
     if (least || !by_mass) {  // the mass of what stands is not known yet
@@ -526,7 +522,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         o[e] = 0.f;
-        if (stands(place(q) + e, z[e]) && (least == 0 || mass(r, z[e], s) >= least)) o[e] = weight(r, z[e], s) * inv;
+        if (stands(place(q) + e, z[e]) && (least == 0 || mass(r, z[e], s) >= least)) o[e] = weight(r, z[e]) * inv;
       }
       put(q, o);
     }
@@ -555,7 +551,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (u[q][e] != u[q][e]) continue;
-          const float pr = weight(r, z[e], s);
+          const float pr = weight(r, z[e]);
           if (pr > 0.f && (least == 0 || mass(r, z[e], s) >= least))
             best = better(best, Best{pr / u[q][e], v0 + place(q0 + q) + e});
         }
