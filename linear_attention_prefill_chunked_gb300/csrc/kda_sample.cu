@@ -23,6 +23,7 @@
 #include <cooperative_groups.h>
 
 #include "kda_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -117,6 +118,10 @@ constexpr float kRound = 12582912.f;
 constexpr int kRoundBits = 0x4b400000;
 __device__ __forceinline__ int distance(const Row& r, float z) {
   return __float_as_int(fminf((r.top - z) * r.ch * r.fx, (float)(kBins - 1)) + kRound) - kRoundBits;
+}
+// Adds v to a word of shared memory, unless it is 0 (without a branch).
+__device__ __forceinline__ void add_shared(uint32_t at, uint32_t v) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p red.shared.add.u32 [%0], %1;\n}\n" ::"r"(at), "r"(v) : "memory");
 }
 // The distance from the maximum in octaves of p, as two floats.
 __device__ __forceinline__ void octaves(const Row& r, float z, float& yh, float& yl) {
@@ -230,7 +235,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   Best top{kMaskedOut, 0x7fffffff};
   float low = __builtin_huge_valf();
   const T* from = logits + (int64_t)row * pitch + v0;
-#pragma unroll 4
+#pragma unroll 8
   for (int q = 0; q < quads; ++q) {
     const int i = place(q);
     float z[4];
@@ -313,7 +318,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   float border = kMaskedOut;
   int at = -1;
   u64 sum = 0;
-  auto stands = [&](int i, float x) { return x > border || (x == border && v0 + i <= at); };
+  auto stands = [&](int i, float x) { return (x > border) | ((x == border) & (v0 + i <= at)); };
   // Digits 1 and on, for bins with many entries: p[] are those of the entry that is sought.
   int p[kPasses];
   auto digit = [&](int d, int idx, float x) -> int {
@@ -325,13 +330,14 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       if (digit(d, idx, x) != p[d]) return false;
     return true;
   };
-  auto add_to = [&](int at, u64 w, bool counts) {
-    if (!KDA_CHECK(at >= 0 && at < kBins)) return;
-    if (counts) atomicAdd(&s.cnt[at], 1u);
-    const uint32_t lo = (uint32_t)w, hi = (uint32_t)(w >> 32);
-    if (lo & 0xffff) atomicAdd(&s.part[0][at], lo & 0xffff);
-    if (lo >> 16) atomicAdd(&s.part[1][at], lo >> 16);
-    if (hi) atomicAdd(&s.part[2][at], hi);
+  const uint32_t hist = tc::smem_u32(s.cnt);
+  auto add_to = [&](int bin, u64 w, uint32_t count) {
+    if (!KDA_CHECK(bin >= 0 && bin < kBins)) return;
+    const uint32_t to = hist + bin * 4, lo = (uint32_t)w;
+    add_shared(to, count);
+    add_shared(to + kBins * 4, lo & 0xffff);
+    add_shared(to + 2 * kBins * 4, lo >> 16);
+    add_shared(to + 3 * kBins * 4, (uint32_t)(w >> 32));
   };
   auto clear = [&] {
     for (int i = tid; i < kBins; i += kThreads) s.cnt[i] = s.part[0][i] = s.part[1][i] = s.part[2][i] = 0;
@@ -401,7 +407,10 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       for (int q = 0; q < quads; ++q) {
         float z[4];
         get(q, z);
-#pragma unroll
+        if (distance(r, z[0]) != p[0] && distance(r, z[1]) != p[0] && distance(r, z[2]) != p[0] &&
+            distance(r, z[3]) != p[0])
+          continue;
+#pragma unroll 1
         for (int e = 0; e < 4; ++e) {
           const int i = place(q) + e;
           if (distance(r, z[e]) != p[0] || !stands(i, z[e]) || !member(depth, v0 + i, z[e])) continue;
@@ -424,7 +433,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
         for (int e = 0; e < 4; ++e) {
           const int i = place(q) + e;
           if (distance(r, z[e]) != p[0] || !stands(i, z[e]) || !member(depth, v0 + i, z[e])) continue;
-          add_to(digit(depth, v0 + i, z[e]), by ? mass(r, z[e], s) : 0, !by);
+          add_to(digit(depth, v0 + i, z[e]), by ? mass(r, z[e], s) : 0, by ? 0 : 1);
         }
       }
       u64 rest = target - before, low_part;
@@ -437,25 +446,30 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       if (KDA_CHECK(i < kList && q < ranks)) s.all[i] = cl.map_shared_rank(&s, q)->list[j];
     }
     __syncthreads();
+    // each CTA ranks its share of them, several lanes an entry where that is little
     const u64 want = target - before;
-    // several lanes an entry where there are few
-    const int share = n <= kThreads / 8 ? 8 : n <= kThreads / 4 ? 4 : n <= kThreads / 2 ? 2 : 1;
-    for (int i0 = 0; i0 < n; i0 += kThreads / share) {
+    const int each = (n + ranks - 1) / ranks, first = rank * each, end = first + each < n ? first + each : n;
+    const int share = each <= kThreads / 16 ? 16 : each <= kThreads / 8 ? 8 : each <= kThreads / 4 ? 4 : 1;
+    for (int i0 = first; i0 < end; i0 += kThreads / share) {
       const int i = i0 + tid / share;
-      const Item it = s.all[i < n ? i : 0];
+      const Item it = s.all[i < end ? i : first];
       u64 was = 0;
+#pragma unroll 4
       for (int j = tid % share; j < n; j += share) {
         const Item o = s.all[j];
         if (o.nk < it.nk || (o.nk == it.nk && o.idx < it.idx)) was += o.w;
       }
       for (int o = 1; o < share; o *= 2) was += __shfl_xor_sync(0xffffffffu, was, o);
-      if (i < n && was < want && want <= was + it.w) {
-        s.nk = it.nk;
-        s.idx = it.idx;
-        s.mass_incl = before + was + it.w;
+      if (i < end && tid % share == 0 && was < want && want <= was + it.w) {
+        for (int q = 0; q < ranks; ++q) {
+          Shared* o = cl.map_shared_rank(&s, q);
+          o->nk = it.nk;
+          o->idx = it.idx;
+          o->mass_incl = before + was + it.w;
+        }
       }
     }
-    __syncthreads();
+    cl.sync();
     border = value_of(s.nk);
     at = s.idx;
     sum = s.mass_incl;
@@ -464,13 +478,25 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   // what stands into a histogram, by number or by mass
   auto histogram = [&](bool by) {
     clear();
+    if (by) {
 #pragma unroll 2
-    for (int q = 0; q < quads; ++q) {
-      float z[4];
-      get(q, z);
+      for (int q = 0; q < quads; ++q) {
+        float z[4];
+        get(q, z);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (stands(place(q) + e, z[e])) add_to(distance(r, z[e]), by ? mass(r, z[e], s) : 0, !by);
+        for (int e = 0; e < 4; ++e) {
+          const u64 w = mass(r, z[e], s);
+          add_to(distance(r, z[e]), stands(place(q) + e, z[e]) ? w : 0, 0);
+        }
+      }
+    } else {
+#pragma unroll 2
+      for (int q = 0; q < quads; ++q) {
+        float z[4];
+        get(q, z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) add_to(distance(r, z[e]), 0, stands(place(q) + e, z[e]));
+      }
     }
   };
   if (by_count) {
