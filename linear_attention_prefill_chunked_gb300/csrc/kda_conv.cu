@@ -542,11 +542,10 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
       db[0] += dz[H][0];
     }
   };
-  // One row by itself, t < t_end: `n` its sequence; the derivative of row t - H is complete then.
+  // One row by itself, t < t_end, of sequence n; the derivative of row t - H is complete then.
   int last = -1;          // sequence of the row before, as far as this run has seen it
   float ds[H][VEC];       // derivative by the state of the sequence that began in this run
-  auto row = [&](int64_t t) {
-    const int n = seq[t];
+  auto row = [&](int64_t t, int n, const Raw& xr, const Raw& gr) {
     shift();
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dz[H][e] = 0.f;
@@ -569,8 +568,8 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
           for (int e = 0; e < VEC; ++e) ds[j][e] = 0.f;
         }
       }
-      R::unpack(R::load(x + t * x_pitch + c), win[H]);
-      R::unpack(R::load(dy + t * dy_pitch + c), dz[H]);
+      R::unpack(xr, win[H]);
+      R::unpack(gr, dz[H]);
       slope();
       if (t < t_hi) count();
       // a sequence's state is read by its first W-1 tokens, which the run of the first one sees all
@@ -682,7 +681,7 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
       } else if (in) {
 #pragma unroll 1
         for (int u = 0; u < kQuad; ++u) {
-          if (t + u < t_end) row(t + u);
+          if (t + u < t_end) row(t + u, seq[t + u], raw[(u * 2) * 32], raw[(u * 2 + 1) * 32]);
           else shift();
           const int64_t o = t + u - H;
           if (o >= t_lo && o < t_hi) derive(o);
@@ -730,14 +729,7 @@ conv_back_plan_kernel(const int32_t* __restrict__ cu, int N, int64_t total, uint
     if (t0 + tid < total) seq[t0 + tid] = s_seq[tid];
     __syncthreads();
   }
-  if (!dstate) return;
-  for (int64_t n = blockIdx.x * 32ll + (tid >> 5); n < N; n += gridDim.x * 32ll) {
-    int64_t a, b;
-    const bool ok = seq_bounds(cu, (int)n, total, &a, &b);
-    if (ok && a != b) continue;
-    for (int64_t i = tid & 31; i < row; i += 32)
-      dstate[n * row + i] = ok && dfinal ? dfinal[n * row + i] : from_f32<T>(0.f);
-  }
+  if (dstate) rows_without_tokens(cu, N, total, dfinal, dstate, row, true);
 }
 
 // The tiles' parts of the sums, added in a fixed order.
@@ -845,7 +837,7 @@ cudaError_t launch_back(const ConvBackArgs& a, cudaStream_t st) {
   float* part = reinterpret_cast<float*>(a.ws + back_part(a.d));
   uint32_t* status = &reinterpret_cast<WsHeader*>(a.ws)->status;
   int64_t plan = (a.d.total_tokens + 1023) / 1024, most = 2ll * gpu_sms();
-  const int64_t rows = a.dstate ? ((int64_t)a.d.num_seqs + 31) / 32 : 1;
+  const int64_t rows = a.dstate ? row_blocks(a.d.num_seqs, (int64_t)(W - 1) * ch) : 1;
   plan = plan > rows ? plan : rows;
   plan = plan < 1 ? 1 : plan > most ? most : plan;
   conv_back_plan_kernel<T><<<(unsigned)plan, 1024, 0, st>>>(a.cu, a.d.num_seqs, a.d.total_tokens, status, seq,

@@ -263,13 +263,7 @@ gated_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ id
     if (t0 + tid < T) seq[t0 + tid] = s_seq[tid];
     __syncthreads();
   }
-  if (!to) return;
-  for (int64_t n = blockIdx.x * 32ll + (tid >> 5); n < N; n += gridDim.x * 32ll) {
-    int64_t a, b;
-    const bool ok = seq_bounds(cu, (int)n, T, &a, &b);
-    if (ok ? a != b : !zero_bad) continue;
-    for (int c = tid & 31; c < ch; c += 32) to[n * ch + c] = ok && from ? from[n * ch + c] : 0.f;
-  }
+  if (to) rows_without_tokens(cu, N, T, from, to, ch, zero_bad);
 }
 
 struct Plan {
@@ -1014,21 +1008,22 @@ gated_back_kernel(const __grid_constant__ Maps maps, const T* __restrict__ dy, i
 }
 
 // dA_log: the tiles' parts of a channel, added up in a fixed order.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
 gated_sum_kernel(const float* __restrict__ part, int64_t tiles, int ch, float* __restrict__ da) {
-  __shared__ float s[8][32];
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float sum = 0.f;
-  if (c < ch)
-    for (int64_t k = warp; k < tiles; k += 8) sum += part[k * ch + c];
+  if (c < ch) {
+#pragma unroll 8
+    for (int64_t k = warp; k < tiles; k += 32) sum += part[k * ch + c];
+  }
   s[warp][lane] = sum;
   __syncthreads();
-  if (warp == 0 && c < ch) {
+  sum = s[lane][warp];          // the warps' sums of channel `warp` of the block
 #pragma unroll
-    for (int w = 1; w < 8; ++w) sum += s[w][lane];
-    da[c] = sum;
-  }
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0 && blockIdx.x * 32 + warp < ch) da[blockIdx.x * 32 + warp] = sum;
 }
 
 // ---- tokens ---------------------------------------------------------------------------------
@@ -1093,7 +1088,7 @@ cudaError_t launch_plan(const GatedArgs& a, const Layout& l, const float* from, 
   int64_t blocks = (a.d.total_tokens + kPlanRows - 1) / kPlanRows;
   auto least = [&](int64_t n) { blocks = blocks > n ? blocks : n; };
   least((unset + 4095) / 4096);
-  if (to) least((a.d.num_seqs + 31) / 32);
+  if (to) least(row_blocks(a.d.num_seqs, a.d.channels));
   blocks = blocks < 1 ? 1 : blocks > most ? most : blocks;
   gated_plan_kernel<<<(unsigned)blocks, 1024, 0, st>>>(
       a.cu, a.idx, a.d.num_seqs, a.d.total_tokens, a.d.num_slots, reinterpret_cast<WsHeader*>(a.ws),
@@ -1190,7 +1185,7 @@ cudaError_t run_back(const GatedArgs& a, cudaStream_t st) {
         pipeline_wait_limit_ns());
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  gated_sum_kernel<<<(unsigned)((a.d.channels + 31) / 32), 256, 0, st>>>(part, l.tiles, a.d.channels, a.da_log);
+  gated_sum_kernel<<<(unsigned)((a.d.channels + 31) / 32), 1024, 0, st>>>(part, l.tiles, a.d.channels, a.da_log);
   return cudaGetLastError();
 }
 

@@ -197,6 +197,40 @@ __device__ __forceinline__ void sequences_of(int* s_seq, const int32_t* cu, cons
   __syncthreads();
 }
 
+// Rows of `row` elements of the sequences without tokens: to <- from (zeros if null); with `zero_bad` those of
+// invalid sequences become 0.  A warp of the grid's (32 a block) takes 256 elements of 32 sequences at a time.
+constexpr int kRowChunk = 256;
+template <typename T>
+__device__ __forceinline__ void rows_without_tokens(const int32_t* cu, int N, int64_t total, const T* from, T* to,
+                                                    int64_t row, bool zero_bad) {
+  const int lane = threadIdx.x & 31;
+  const int64_t chunks = (row + kRowChunk - 1) / kRowChunk, pairs = ((int64_t)N + 31) / 32 * chunks;
+  for (int64_t w = blockIdx.x * 32ll + (threadIdx.x >> 5); w < pairs; w += gridDim.x * 32ll) {
+    const int n = (int)(w / chunks * 32) + lane;
+    int64_t a = 0, b = 1;
+    const bool ok = n < N && seq_bounds(cu, n, total, &a, &b);
+    const unsigned empty = __ballot_sync(0xffffffffu, ok && a == b);
+    unsigned todo = empty | __ballot_sync(0xffffffffu, n < N && !ok && zero_bad);
+    while (todo) {
+      const int i = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const bool copy = ((empty >> i) & 1) && from;
+      const int64_t at = (w / chunks * 32 + i) * row, c0 = w % chunks * kRowChunk + lane;
+      T v[kRowChunk / 32];
+#pragma unroll
+      for (int j = 0; j < kRowChunk / 32; ++j)
+        v[j] = copy && c0 + j * 32 < row ? from[at + c0 + j * 32] : from_f32<T>(0.f);
+#pragma unroll
+      for (int j = 0; j < kRowChunk / 32; ++j)
+        if (c0 + j * 32 < row) to[at + c0 + j * 32] = v[j];
+    }
+  }
+}
+// Blocks of 32 warps for it.
+inline int64_t row_blocks(int64_t N, int64_t row) {
+  return ((N + 31) / 32 * ((row + kRowChunk - 1) / kRowChunk) + 31) / 32;
+}
+
 // Two fp32 operations as one packed instruction, each rounded to nearest.
 __device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
   unsigned long long ab, xy;
