@@ -9,6 +9,7 @@ is which call follows which and what each keeps:
   prompt   causal_conv -> ssm_scan          causal_conv -> chunk_prefill       (pools updated in place)
   round    causal_conv_draft -> ssm_decode_draft, causal_conv_draft -> decode_draft   (pools untouched,
            the state after every drafted token in a step cache)
+           sample_probs -> the target's probabilities under temperature and filters
            verify_draft -> how many of the fed tokens stand, and the next one
            commit_draft, once a pool -> the state after the last token that stands
 """
@@ -103,9 +104,10 @@ def cu_of(lens):
     return cu.cuda()
 
 
-def serve(prompts, rounds=6, drafts=3, seed=1):
+def serve(prompts, rounds=6, drafts=3, seed=1, temperature=1.0, top_k=None, top_p=None, min_p=None):
     """Prompts (lists of tokens) and what follows them: returns the model, the slots and the texts,
     whose last token has not been fed yet."""
+    filters = dict(temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p)
     n = len(prompts)
     m = Model(slots=n + 2)
     g = torch.Generator(device="cuda").manual_seed(seed)
@@ -115,7 +117,7 @@ def serve(prompts, rounds=6, drafts=3, seed=1):
     flat = torch.tensor([t for p in prompts for t in p], dtype=torch.int32, device="cuda")
     cu = cu_of([len(p) for p in prompts])
     last = m.logits(flat, cu, idx)[cu[1:].long() - 1]
-    fed = torch.argmax(torch.softmax(last, 1) / exp(n, VOCAB), 1).to(torch.int32)
+    fed = kda.sample(last, exp(n, VOCAB), **filters)
     texts = [list(p) + [int(t)] for p, t in zip(prompts, fed)]
 
     caches, steps = m.caches(n, drafts + 1), drafts + 1
@@ -124,14 +126,14 @@ def serve(prompts, rounds=6, drafts=3, seed=1):
         # the draft: tokens from the bigram table, one after another
         tokens, proposed = [fed], []
         for _ in range(drafts):
-            q = torch.softmax(m.bigram[tokens[-1].long()].float(), 1)
-            proposed.append(q)
-            tokens.append(torch.argmax(q / exp(n, VOCAB), 1).to(torch.int32))
+            logits = m.bigram[tokens[-1].long()]
+            proposed.append(kda.sample_probs(logits, **filters))
+            tokens.append(kda.sample(logits, exp(n, VOCAB), **filters))
         proposed.append(torch.zeros(n, VOCAB, device="cuda"))  # the last row is not read
         tokens = torch.stack(tokens, 1).flatten()
         q = torch.stack(proposed, 1).flatten(0, 1)
         # the target on all of them at once, then what stands of them
-        p = torch.softmax(m.logits(tokens, cu, idx, caches), 1)
+        p = kda.sample_probs(m.logits(tokens, cu, idx, caches), **filters)
         u = torch.rand(n * steps, generator=g, device="cuda")
         kept, fed = kda.verify_draft(tokens, p, q, u, exp(n, VOCAB), cu)
         for name, pool in m.pools.items():

@@ -47,7 +47,7 @@ KDA_DEBUG_FLAG_DEFINE();
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kScanCtas = 2, kBackCtas = 2;   // CTAs an SM
-constexpr int kGroup = 16;
+constexpr int kGroup = 8;
 constexpr int kPlanRows = 1024;   // rows a block of the planning kernel
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kUnset = 0xffffffffu;

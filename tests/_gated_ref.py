@@ -72,7 +72,7 @@ def backward(k, dy, dfinal, lens):
         + a * size * g.abs() * k["err_before"] + 4 * unit * p_size * (1 + g.abs())
     ml, ml_size = k["m"] * lam, k["m"] * size
     ml_err = k["m"] * err + unit * ml_size
-    add = (8 + 16 + T / 48 / 8 + 16) * 2.0 ** -24   # roundings on the way of one term of the sum
+    add = (8 + 16 + T / 48 / 32 + 32) * 2.0 ** -24   # roundings on the way of one term of the sum
     z = lambda rows: torch.stack(rows) if rows else torch.zeros(0, ch, dtype=torch.float64)
     return dict(dx=ml * k["gi"], dr=p * k["c"], di=ml * k["u"] * k["hi"], dA_log=p.sum(0), dstate=z(dstate)), \
         dict(dx=(ml_err + unit * ml_size) * k["gi"], dr=(p_err + unit * p_size) * k["c"],
