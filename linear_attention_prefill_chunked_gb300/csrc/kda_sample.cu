@@ -14,8 +14,8 @@
 //
 // An entry next to top-p's border stands or falls with the last digits of a sum over the row, so masses
 // are whole numbers, p in units of 2^-44, whose sums do not depend on their order: results are bit-identical
-// from run to run, whichever CTA adds first. p itself is 2^-n 2^(-j/64) 2^-r from a table and three terms of the
-// exponential series, the distance carried as two floats: good to 2^-30, where a float's sum of a
+// from run to run, whichever CTA adds first. p itself is 2^-n 2^(-j/32) 2^-r from a table, an entry a lane, and four
+// terms of the exponential series, the distance carried as two floats: good to 2^-30, where a float's sum of a
 // vocabulary would be off by more than the smallest entries that stand.
 //
 // Bound by HBM in principle (the row, and noise or probabilities), by the arithmetic of p and the cluster's
@@ -45,24 +45,16 @@ constexpr unsigned long long kOne = 1ull << kOneBits;
 constexpr float kMaskedOut = -__builtin_huge_valf();
 using u64 = unsigned long long;
 
-// 2^(-j/64) in units of 2^-44
-__constant__ u64 c_pow[64] = {
-    17592186044416ull, 17402683248456ull, 17215221774115ull, 17029779632301ull,
-    16846335070792ull, 16664866571680ull, 16485352848846ull, 16307772845465ull,
-    16132105731538ull, 15958330901445ull, 15786427971528ull, 15616376777705ull,
-    15448157373097ull, 15281750025697ull, 15117135216047ull, 14954293634955ull,
-    14793206181226ull, 14633853959423ull, 14476218277651ull, 14320280645363ull,
-    14166022771192ull, 14013426560807ull, 13862474114787ull, 13713147726524ull,
-    13565429880144ull, 13419303248457ull, 13274750690919ull, 13131755251623ull,
-    12990300157313ull, 12850368815412ull, 12711944812080ull, 12575011910285ull,
-    12439554047902ull, 12305555335825ull, 12173000056107ull, 12041872660113ull,
-    11912157766698ull, 11783840160404ull, 11656904789672ull, 11531336765078ull,
-    11407121357589ull, 11284243996830ull, 11162690269381ull, 11042445917079ull,
-    10923496835354ull, 10805829071568ull, 10689428823381ull, 10574282437131ull,
-    10460376406236ull, 10347697369602ull, 10236232110063ull, 10125967552830ull,
-    10016890763953ull, 9908988948806ull, 9802249450589ull, 9696659748838ull,
-    9592207457961ull, 9488880325783ull, 9386666232110ull, 9285553187305ull,
-    9185529330885ull, 9086582930126ull, 8988702378691ull, 8891876195264ull
+// 2^(-j/32) in units of 2^-44
+__constant__ u64 c_pow[32] = {
+    17592186044416ull, 17215221774115ull, 16846335070792ull, 16485352848846ull,
+    16132105731538ull, 15786427971528ull, 15448157373097ull, 15117135216047ull,
+    14793206181226ull, 14476218277651ull, 14166022771192ull, 13862474114787ull,
+    13565429880144ull, 13274750690919ull, 12990300157313ull, 12711944812080ull,
+    12439554047902ull, 12173000056107ull, 11912157766698ull, 11656904789672ull,
+    11407121357589ull, 11162690269381ull, 10923496835354ull, 10689428823381ull,
+    10460376406236ull, 10236232110063ull, 10016890763953ull, 9802249450589ull,
+    9592207457961ull, 9386666232110ull, 9185529330885ull, 8988702378691ull
 };
 
 struct Item {
@@ -86,8 +78,6 @@ struct alignas(16) Shared {
     Item all[kList];     // the cluster's entries of the bin
   };
   Item list[kList];      // this CTA's entries of the bin
-  u64 pow[64];
-  float powf[64];
   Best warp_best[kWarps], best[2][kMaxRanks];
   float warp_low[kWarps], low[kMaxRanks];
   u64 coarse[kMaxRanks][kCoarse], fine[kMaxRanks][kFine];   // each CTA's sums, of its bins by 32 and of 32 of its bins
@@ -129,16 +119,33 @@ __device__ __forceinline__ void octaves(const Row& r, float z, float& yh, float&
   yh = d * r.ch;
   yl = fmaf(d, r.ch, -yh) + fmaf(d, r.cl, dl * r.ch);
 }
-// p = 2^-n 2^(-j/64) (1 + e) in units of 2^-44; 0 for masked entries.
-__device__ __forceinline__ u64 mass(const Row& r, float z, const Shared& s) {
+// p = 2^-n 2^(-j/32) (1 + e) in units of 2^-44; 0 for masked entries.  Of a whole warp, whose lanes hold the table
+// between them (reads of shared memory at 32 places take several times as long), or of some of its lanes.
+struct Table {
+  uint32_t lo, hi;
+  float f;
+  __device__ __forceinline__ explicit Table(int lane)
+      : lo((uint32_t)c_pow[lane]), hi((uint32_t)(c_pow[lane] >> 32)),
+        f((float)(uint32_t)(c_pow[lane] >> 20) * 5.9604644775390625e-8f) {}  // 2^-24
+};
+template <bool kWarp> __device__ __forceinline__ u64 mass(const Row& r, float z, const Table& table) {
   float yh, yl;
   octaves(r, z, yh, yl);
-  const float m = fmaf(yh, 64.f, kRound);
-  const int k = __float_as_int(m) - kRoundBits, n = k >> 6, j = k & 63;
-  const float t = (fmaf(m - kRound, -1.f / 64.f, yh) + yl) * -0.69314718055994531f;
-  const float e = t * fmaf(t, fmaf(t, 1.f / 6.f, 0.5f), 1.f);          // |e| < 0.0055
-  const int fine = __float_as_int(fmaf(s.powf[j] * e, 536870912.f, kRound)) - kRoundBits;  // of 2^29
-  return yh < 45.f ? (s.pow[j] + ((u64)(long long)fine << 15)) >> n : 0;
+  const float m = fmaf(yh, 32.f, kRound);
+  const int k = __float_as_int(m) - kRoundBits, n = k >> 5, j = k & 31;
+  const float t = (fmaf(m - kRound, -1.f / 32.f, yh) + yl) * -0.69314718055994531f;
+  const float e = t * fmaf(t, fmaf(t, fmaf(t, 1.f / 24.f, 1.f / 6.f), 0.5f), 1.f);   // |e| < 0.011
+  u64 whole;
+  float f;
+  if constexpr (kWarp) {
+    whole = (u64)__shfl_sync(0xffffffffu, table.hi, j) << 32 | __shfl_sync(0xffffffffu, table.lo, j);
+    f = __shfl_sync(0xffffffffu, table.f, j);
+  } else {
+    whole = c_pow[j];
+    f = (float)(uint32_t)(whole >> 20) * 5.9604644775390625e-8f;
+  }
+  const int fine = __float2int_rn(f * e * 68719476736.f);    // of 2^36
+  return yh < 45.f ? (whole + ((u64)(long long)fine << 8)) >> n : 0;
 }
 // p to 2^-22
 __device__ __forceinline__ float weight(const Row& r, float z) {
@@ -228,10 +235,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
 
   // every CTA of the cluster has to have started before another writes into its shared memory
   auto started = cl.barrier_arrive();
-  if (tid < 64) {
-    s.pow[tid] = c_pow[tid];
-    s.powf[tid] = (float)(uint32_t)(c_pow[tid] >> 20) * 5.9604644775390625e-8f;  // 2^-24
-  }
+  const Table table(lane);
   Best top{kMaskedOut, 0x7fffffff};
   float low = __builtin_huge_valf();
   const T* from = logits + (int64_t)row * pitch + v0;
@@ -415,7 +419,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
           const int i = place(q) + e;
           if (distance(r, z[e]) != p[0] || !stands(i, z[e]) || !member(depth, v0 + i, z[e])) continue;
           const int at = atomicAdd(&s.n, 1);
-          if (at < kList) s.list[at] = Item{down_key(z[e]), v0 + i, by ? mass(r, z[e], s) : 1};
+          if (at < kList) s.list[at] = Item{down_key(z[e]), v0 + i, by ? mass<false>(r, z[e], table) : 1};
         }
       }
       __syncthreads();
@@ -433,7 +437,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
         for (int e = 0; e < 4; ++e) {
           const int i = place(q) + e;
           if (distance(r, z[e]) != p[0] || !stands(i, z[e]) || !member(depth, v0 + i, z[e])) continue;
-          add_to(digit(depth, v0 + i, z[e]), by ? mass(r, z[e], s) : 0, by ? 0 : 1);
+          add_to(digit(depth, v0 + i, z[e]), by ? mass<false>(r, z[e], table) : 0, by ? 0 : 1);
         }
       }
       u64 rest = target - before, low_part;
@@ -485,7 +489,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
         get(q, z);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const u64 w = mass(r, z[e], s);
+          const u64 w = mass<true>(r, z[e], table);
           add_to(distance(r, z[e]), stands(place(q) + e, z[e]) ? w : 0, 0);
         }
       }
@@ -517,9 +521,8 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
         get(q, z);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (!stands(place(q) + e, z[e])) continue;
-          const u64 w = mass(r, z[e], s);
-          if (w >= least) part += w;
+          const u64 w = mass<true>(r, z[e], table);
+          if (stands(place(q) + e, z[e]) && w >= least) part += w;
         }
       }
 #pragma unroll
@@ -548,7 +551,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         o[e] = 0.f;
-        if (stands(place(q) + e, z[e]) && (least == 0 || mass(r, z[e], s) >= least)) o[e] = weight(r, z[e]) * inv;
+        if (stands(place(q) + e, z[e]) && (least == 0 || mass<false>(r, z[e], table) >= least)) o[e] = weight(r, z[e]) * inv;
       }
       put(q, o);
     }
@@ -578,7 +581,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
         for (int e = 0; e < 4; ++e) {
           if (u[q][e] != u[q][e]) continue;
           const float pr = weight(r, z[e]);
-          if (pr > 0.f && (least == 0 || mass(r, z[e], s) >= least))
+          if (pr > 0.f && (least == 0 || mass<false>(r, z[e], table) >= least))
             best = better(best, Best{pr / u[q][e], v0 + place(q0 + q) + e});
         }
       }

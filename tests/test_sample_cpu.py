@@ -87,9 +87,9 @@ def test_descriptor_layout_matches_header(tmp_path):
 
 
 def test_table_of_powers():
-    """Entry j is the whole number nearest to 2^(44 - j/64): (2 e - 1)^64 < 2^(64 * 45 - j) < (2 e + 1)^64."""
+    """Entry j is the whole number nearest to 2^(44 - j/32): (2 e - 1)^32 < 2^(32 * 45 - j) < (2 e + 1)^32."""
     src = open(os.path.join(ROOT, "linear_attention_prefill_chunked_gb300", "csrc", "kda_sample.cu")).read()
-    table = [int(v) for v in re.findall(r"(\d+)ull", src[src.index("c_pow[64]"):src.index("struct Item")])]
-    assert len(table) == 64 and table[0] == 1 << 44
+    table = [int(v) for v in re.findall(r"(\d+)ull", src[src.index("c_pow[32]"):src.index("struct Item")])]
+    assert len(table) == 32 and table[0] == 1 << 44
     for j, e in enumerate(table[1:], 1):
-        assert Fraction(2 * e - 1) ** 64 < Fraction(2) ** (64 * 45 - j) < Fraction(2 * e + 1) ** 64, j
+        assert Fraction(2 * e - 1) ** 32 < Fraction(2) ** (32 * 45 - j) < Fraction(2 * e + 1) ** 32, j
