@@ -512,6 +512,7 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
     for (int j = 0; j < W; ++j) wt[j][i] = dw[j][i] = win[j][i] = dz[j][i] = 0.f;
   }
   if (in) load_taps<T, VEC, W>(w, bias, c, wt, bv);
+  tc::grid_dep_wait();
 
   auto shift = [&] {
 #pragma unroll
@@ -723,6 +724,7 @@ conv_back_plan_kernel(const int32_t* __restrict__ cu, int N, int64_t total, uint
                       int32_t* __restrict__ seq, const T* __restrict__ dfinal, T* __restrict__ dstate, int64_t row) {
   __shared__ int s_seq[1024];
   const int tid = threadIdx.x;
+  tc::grid_dep_launch_dependents();
   if (blockIdx.x == 0) check_all(status, cu, nullptr, N, total, total, 0);
   for (int64_t t0 = (int64_t)blockIdx.x * 1024; t0 < total; t0 += (int64_t)gridDim.x * 1024) {
     sequences_of<1024>(s_seq, cu, nullptr, 0, N, total, t0);
@@ -737,6 +739,7 @@ __global__ void __launch_bounds__(256)
 conv_sum_kernel(const float* __restrict__ part, int64_t tiles, int ch, int W, float* __restrict__ dw,
                 float* __restrict__ db) {
   __shared__ float s[8][32];
+  tc::grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = blockIdx.y;
   const int c = blockIdx.x * 32 + lane;
   float sum = 0.f;
@@ -848,13 +851,13 @@ cudaError_t launch_back(const ConvBackArgs& a, cudaStream_t st) {
   const int bytes = kBackThreads * back_depth<T, VEC>() * kQuad * 2 * (int)sizeof(typename Row<T, VEC>::Raw);
   auto* kernel = conv_back_kernel<T, VEC, W>;
   if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
-  kernel<<<grid, kBackThreads, bytes, st>>>(
-      (const T*)a.dy, a.dy_pitch, (const T*)a.x, a.d.x_pitch, (const T*)a.w, (const T*)a.bias, a.cu, seq,
+  e = launch_behind(
+      kernel, grid, dim3(kBackThreads), bytes, st, (const T*)a.dy, a.dy_pitch, (const T*)a.x, a.d.x_pitch, (const T*)a.w, (const T*)a.bias, a.cu, seq,
       (const T*)a.state, (const T*)a.dfinal, (T*)a.dx, (T*)a.dstate, part, status, a.d.total_tokens, s.run, ch,
       a.d.silu != 0);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  conv_sum_kernel<<<dim3((unsigned)((ch + 31) / 32), W + 1), 256, 0, st>>>(part, s.ctas, ch, W, a.dw, a.db);
-  return cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_behind(conv_sum_kernel, dim3((unsigned)((ch + 31) / 32), W + 1), dim3(256), 0, st, part, s.ctas, ch, W,
+                       a.dw, a.db);
 }
 
 template <typename T, int VEC>

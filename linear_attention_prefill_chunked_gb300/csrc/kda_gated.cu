@@ -249,6 +249,7 @@ gated_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ id
                   int64_t num_unset, const float* from, float* to, int ch, bool zero_bad) {
   __shared__ int s_seq[kPlanRows];
   const int tid = threadIdx.x;
+  tc::grid_dep_launch_dependents();
   if (blockIdx.x == 0) {
     check_all(&hdr->status, cu, idx, N, T, T, idx ? num_slots : 0);
     if (tid == 0) {
@@ -545,6 +546,7 @@ gated_scan_kernel(const __grid_constant__ Maps maps, const T* __restrict__ x, in
     tc::mbar_init(&s.full, 1);
     tc::fence_mbar_init();
   }
+  tc::grid_dep_wait();
   Taker<V, S, false> taker;
   if (warp == kWarps) {
     taker.start(hdr, lane);
@@ -741,6 +743,7 @@ gated_back_kernel(const __grid_constant__ Maps maps, const T* __restrict__ dy, i
     tc::mbar_init(&s.full, 1);
     tc::fence_mbar_init();
   }
+  tc::grid_dep_wait();
   Taker<V, S, true> taker;
   if (warp == kWarps) {
     taker.start(hdr, lane);
@@ -1011,6 +1014,7 @@ gated_back_kernel(const __grid_constant__ Maps maps, const T* __restrict__ dy, i
 __global__ void __launch_bounds__(1024)
 gated_sum_kernel(const float* __restrict__ part, int64_t tiles, int ch, float* __restrict__ da) {
   __shared__ float s[32][33];
+  tc::grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float sum = 0.f;
@@ -1154,11 +1158,10 @@ cudaError_t run_scan(const GatedArgs& a, cudaStream_t st) {
   const void* base[] = {a.x, a.r, a.i};
   const int64_t pitch[] = {a.d.x_pitch, a.d.r_pitch, a.d.i_pitch};
   const bool wide = maps_of<T>(&maps, base, pitch, kGate ? 3 : 2, a.d.total_tokens, a.d.channels, 32 * V, kRows * kWarps);
-  kernel<<<grid, kAll, bytes, st>>>(
-      maps, (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i, a.d.i_pitch, a.a_log, a.state_in,
+  return launch_behind(
+      kernel, dim3(grid), dim3(kAll), bytes, st, maps, (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i, a.d.i_pitch, a.a_log, a.state_in,
       a.idx, a.d.num_slots, a.slot_stride, a.state_out, (T*)a.y, a.carries, p,
       reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, wide, pipeline_wait_limit_ns());
-  return cudaGetLastError();
 }
 
 template <typename T, int V, bool kGate>
@@ -1178,15 +1181,15 @@ cudaError_t run_back(const GatedArgs& a, cudaStream_t st) {
     const int64_t pitch[] = {a.d.x_pitch, a.d.r_pitch, a.dy_pitch, a.d.i_pitch};
     const bool wide = maps_of<T>(&maps, base, pitch, kGate ? 4 : 3, a.d.total_tokens, a.d.channels, 32 * V,
                                  kBackRows * kWarps);
-    kernel<<<grid, kAll, bytes, st>>>(
-        maps, (const T*)a.dy, a.dy_pitch, (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i,
+    e = launch_behind(
+        kernel, dim3(grid), dim3(kAll), bytes, st, maps, (const T*)a.dy, a.dy_pitch, (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i,
         a.d.i_pitch, a.a_log, a.carries, a.state_in, a.dfinal, (T*)a.dx, (T*)a.dr, (T*)a.di, a.dstate, part, p,
         reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, wide,
         pipeline_wait_limit_ns());
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
   }
-  gated_sum_kernel<<<(unsigned)((a.d.channels + 31) / 32), 1024, 0, st>>>(part, l.tiles, a.d.channels, a.da_log);
-  return cudaGetLastError();
+  return launch_behind(gated_sum_kernel, dim3((unsigned)((a.d.channels + 31) / 32)), dim3(1024), 0, st, part, l.tiles,
+                       a.d.channels, a.da_log);
 }
 
 template <typename T, int V, bool kGate>

@@ -139,6 +139,23 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st);
 // Operators of the layers around the recurrence (kda_conv.cu, kda_ssm.cu, kda_draft.cu).
 namespace kda {
 
+// Launches a kernel that may set itself up while the one before it on the stream still runs; it waits for that
+// (grid_dep_wait) before it reads or writes anything that kernel touches.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t bytes, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // SMs of the current device (152, for sizes asked for where there is none).
 int gpu_sms();
 
