@@ -545,7 +545,8 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
   };
   // One row by itself, t < t_end, of sequence n; the derivative of row t - H is complete then.
   int last = -1;          // sequence of the row before, as far as this run has seen it
-  float ds[H][VEC];       // derivative by the state of the sequence that began in this run
+  // derivative by the state of the sequence that began in this run
+  float (*ds)[VEC] = reinterpret_cast<float(*)[VEC]>(s_ring + kBackThreads * kDepth * kQuad * 2 * sizeof(Raw)) + tid * H;
   auto row = [&](int64_t t, int n, const Raw& xr, const Raw& gr) {
     shift();
 #pragma unroll
@@ -848,7 +849,8 @@ cudaError_t launch_back(const ConvBackArgs& a, cudaStream_t st) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   dim3 grid((unsigned)((ch + 32 * VEC - 1) / (32 * VEC)), (unsigned)s.ctas);
-  const int bytes = kBackThreads * back_depth<T, VEC>() * kQuad * 2 * (int)sizeof(typename Row<T, VEC>::Raw);
+  const int bytes = kBackThreads * (back_depth<T, VEC>() * kQuad * 2 * (int)sizeof(typename Row<T, VEC>::Raw) +
+                                    (W - 1) * VEC * 4);
   auto* kernel = conv_back_kernel<T, VEC, W>;
   if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
   e = launch_behind(
