@@ -480,7 +480,7 @@ __device__ __forceinline__ void fetch_quad(typename Row<T, VEC>::Raw* to, const 
 }
 
 // Fours of rows in shared memory, one of them in work.
-template <typename T, int VEC> constexpr int back_depth() { return sizeof(typename Row<T, VEC>::Raw) == 16 ? 3 : 5; }
+template <typename T, int VEC> constexpr int back_depth() { return sizeof(typename Row<T, VEC>::Raw) == 16 ? 2 : 3; }
 
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kBackThreads, 2)

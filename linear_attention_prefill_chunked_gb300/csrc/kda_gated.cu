@@ -137,18 +137,18 @@ template <typename T, int V> __device__ __forceinline__ void store(T* p, const C
   *reinterpret_cast<typename Pack<T, V>::Raw*>(p) = Pack<T, V>::close(c);
 }
 // ---- gates ----------------------------------------------------------------------------------
-// e^-v and sigmoid(v) = 1 / (1 + e^-v). The backward pass keeps e^-v below 1e37, so that e^-v sigmoid(v) =
-// 1 - sigmoid(v) has its leading digits at either end. bf16 inputs take the fast exponential and
-// reciprocal, good to 2^-21 and |v| 2^-24: far below those inputs' own rounding, and what is fp32 of the
-// results (states, dA_log) keeps 2^-19.
-template <bool kFast, bool kClamp, int V> __device__ __forceinline__ Ch<V> exp_neg(const Ch<V>& v) {
+// e^-v and sigmoid(v) = 1 / (1 + e^-v). Where e^-v is kept below 1e37, e^-v sigmoid(v) = 1 - sigmoid(v) has its
+// leading digits at either end (and the Newton step has no infinity to meet). bf16 inputs take the fast exponential and reciprocal, good to 2^-21 and
+// |v| 2^-24: far below those inputs' own rounding, and what is fp32 of the results (states, dA_log) keeps
+// 2^-19. fp32 inputs take CUDA's exponential and a Newton step behind the reciprocal.
+template <bool kFast, bool kBounded, int V> __device__ __forceinline__ Ch<V> exp_neg(const Ch<V>& v) {
   Ch<V> e;
   if constexpr (kFast) e = mul(v, all<V>(-kLog2e));
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     if constexpr (kFast) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.f[i]));
     else e.f[i] = expf(-v.f[i]);
-    if constexpr (kClamp) asm("min.NaN.f32 %0, %0, 0f7cf0bdc2;" : "+f"(e.f[i]));  // 1e37; NaN stays
+    if constexpr (kBounded) asm("min.NaN.f32 %0, %0, 0f7cf0bdc2;" : "+f"(e.f[i]));  // 1e37; NaN stays
   }
   return e;
 }
@@ -156,13 +156,14 @@ template <bool kFast, int V> __device__ __forceinline__ Ch<V> one_over(Ch<V> e) 
   e = add(e, all<V>(1.f));
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    if constexpr (kFast) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.f[i]));
-    else e.f[i] = 1.f / e.f[i];
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e.f[i]));
+    e.f[i] = kFast ? r : fmaf(r, fmaf(-e.f[i], r, 1.f), r);
   }
   return e;
 }
 template <bool kFast, int V> __device__ __forceinline__ Ch<V> sigmoid(const Ch<V>& v) {
-  return one_over<kFast>(exp_neg<kFast, false>(v));
+  return one_over<kFast>(exp_neg<kFast, !kFast>(v));
 }
 
 // Decay rates of a lane's channels, -exp(A_log), finite.
@@ -210,33 +211,25 @@ template <bool kFast, int V> __device__ __forceinline__ Ch<V> decay(const Ch<V>&
   return a;
 }
 
-// sqrt(-w)
-template <bool kFast, int V> __device__ __forceinline__ Ch<V> root(Ch<V> w) {
+// sqrt(-w), to 2^-23
+template <int V> __device__ __forceinline__ Ch<V> root(Ch<V> w) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     w.f[i] = -w.f[i];
-    if constexpr (kFast) asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(w.f[i]));
-    else w.f[i] = sqrtf(w.f[i]);
+    asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(w.f[i]));
   }
   return w;
 }
-// -g over sqrt(-w) and sqrt(-w); both 0 where that is.
-template <bool kFast, int V>
-__device__ __forceinline__ void over_root(const Ch<V>& g, const Ch<V>& w, Ch<V>& q, Ch<V>& m) {
-  if constexpr (kFast) {
-    Ch<V> k;
+// -g over sqrt(-w) and sqrt(-w), to 2^-22; both 0 where that is.
+template <int V> __device__ __forceinline__ void over_root(const Ch<V>& g, const Ch<V>& w, Ch<V>& q, Ch<V>& m) {
+  Ch<V> k;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(k.f[i]) : "f"(-w.f[i]));
-      k.f[i] = w.f[i] > -1e-37f ? 0.f : -k.f[i];
-    }
-    m = mul(w, k);
-    q = mul(g, k);
-  } else {
-    m = root<false>(w);
-#pragma unroll
-    for (int i = 0; i < V; ++i) q.f[i] = m.f[i] == 0.f ? 0.f : -g.f[i] / m.f[i];
+  for (int i = 0; i < V; ++i) {
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(k.f[i]) : "f"(-w.f[i]));
+    k.f[i] = w.f[i] > -1e-37f ? 0.f : -k.f[i];
   }
+  m = mul(w, k);
+  q = mul(g, k);
 }
 
 // ---- planning -------------------------------------------------------------------------------
@@ -660,7 +653,7 @@ gated_scan_kernel(const __grid_constant__ Maps maps, const T* __restrict__ x, in
     for (int j = 0; j < S; ++j) {
       Ch<V> w;
       a[j] = decay<kFast>(mul(rate, sigmoid<kFast>(P::open(mine[(kRowsTile + j) * 32]))), w);
-      b[j] = mul(root<kFast>(w), P::open(mine[j * 32]));
+      b[j] = mul(root(w), P::open(mine[j * 32]));
       if (kGate) b[j] = mul(b[j], sigmoid<kFast>(P::open(mine[(2 * kRowsTile + j) * 32])));
     }
     Ch<V> A = a[0], H = b[0];
@@ -852,7 +845,7 @@ gated_back_kernel(const __grid_constant__ Maps maps, const T* __restrict__ dy, i
       e = mul(a, l);
       const Ch<V> er = exp_neg<kFast, true>(P::open(row.r)), sr = one_over<kFast>(er), g = mul(rate, sr);
       Ch<V> m, k, u = P::open(row.x);
-      over_root<kFast>(g, lost(g, series(g), a), k, m);
+      over_root(g, lost(g, series(g), a), k, m);
       const Ch<V> ml = mul(m, l);
       ox = ml;
       if (kGate) {
@@ -948,7 +941,7 @@ gated_back_kernel(const __grid_constant__ Maps maps, const T* __restrict__ dy, i
       if (kGate) row[j].i = mine[(3 * kRowsTile + j) * 32];
       Ch<V> w;
       a[j] = decay<kFast>(mul(rate, one_over<kFast>(exp_neg<kFast, true>(P::open(row[j].r)))), w);
-      hp[j] = mul(root<kFast>(w), P::open(row[j].x));
+      hp[j] = mul(root(w), P::open(row[j].x));
       if (kGate) hp[j] = mul(hp[j], sigmoid<kFast>(P::open(row[j].i)));
     }
     Ch<V> A = a[0], H = all<V>(0.f), E = all<V>(0.f);
@@ -1059,7 +1052,7 @@ gated_token_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict
     if (kGate) u = mul(u, sigmoid<kFast>(P::open(load<T, V>(ig + t * i_pitch + c))));
     Ch<V> w;
     const Ch<V> a = decay<kFast>(mul(rate, sigmoid<kFast>(P::open(rr))), w);
-    h = fma(a, h, mul(root<kFast>(w), u));
+    h = fma(a, h, mul(root(w), u));
     if (KDA_CHECK(t >= 0 && t < total && c + V <= ch)) store<T, V>(y + t * ch + c, h);
     if (cache) store<float, V>(cache + n * cache_pitch + (t - bos) * ch + c, h);
   }
