@@ -37,6 +37,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kFine = 32, kCoarse = kBins / kFine;   // bins are looked through in two steps
 constexpr int kList = 1024;                // entries that are ranked against each other
+constexpr int kFew = 512;                  // entries up to the k-th that are ranked by number and mass at once
 constexpr int kMaxRanks = 8;
 constexpr int kMostQuads = 22;             // fours of entries a thread looks after at most
 constexpr int kPasses = 7;                 // digits: the distance, four of the value, two of the index
@@ -85,7 +86,7 @@ struct alignas(16) Shared {
   int n, counts[kMaxRanks];             // entries of the bin, here and in each CTA
   uint32_t nk;                          // the entry that was sought,
   int idx;
-  u64 mass_incl;                        // and the mass up to and with it
+  u64 mass_incl, kth_mass;              // and the mass up to and with it; the same of the k-th
   float ch, cl, inv;                    // what is worked out in 64 bits, by one thread
   u64 least, target;
 };
@@ -365,7 +366,9 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     return at;
   };
   // The bin of the cluster's histogram (filled, in each CTA) where the count or the mass reaches `target`, and what
-  // lies in the bins before it; -1 if it does not. A target of 0 stands for top-p of all mass, and is set.
+  // lies in it and in the bins before it; -1 if it does not. A target of 0 stands for top-p of all mass, and is
+  // set.
+  u64 inside;
   auto search = [&](bool by, u64& target, u64& before) {
     __syncthreads();
     for (int g = warp; g < kCoarse; g += kWarps) {
@@ -393,40 +396,55 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     cl.sync();
     v = 0;
     for (int q = 0; q < ranks; ++q) v += s.fine[q][lane];
-    const int bin = g * kFine + find(v, target - before, rest, total);
+    const int b = find(v, target - before, rest, total);
+    inside = __shfl_sync(0xffffffffu, v, b);
     before += rest;
-    return bin;
+    return g * kFine + b;
   };
-  // Cuts what stands off behind the entry with which its number, or its mass, reaches `target`; the mass up to
-  // and with that is in s.mass_incl then (by mass).
-  auto cut = [&](bool by, u64 target) {
-    u64 before;                   // what lies before the entries whose digits are p[0] .. p[depth - 1]
-    p[0] = search(by, target, before);
-    if (p[0] < 0) return;
-    int depth = 1, n;
-    for (;;) {
-      if (tid == 0) s.n = 0;
-      __syncthreads();
+  // The cluster's entries that are `wanted`, in bins up to `bin` (from `bin` on, if only that is), into every CTA's
+  // s.all with their masses (or ones); their number, which may be too large for that.
+  auto collect = [&](int bin, bool only_that, bool masses, auto wanted) {
+    if (tid == 0) s.n = 0;
+    __syncthreads();
 #pragma unroll 2
-      for (int q = 0; q < quads; ++q) {
-        float z[4];
-        get(q, z);
-        if (distance(r, z[0]) != p[0] && distance(r, z[1]) != p[0] && distance(r, z[2]) != p[0] &&
-            distance(r, z[3]) != p[0])
-          continue;
-#pragma unroll 1
-        for (int e = 0; e < 4; ++e) {
-          const int i = place(q) + e;
-          if (distance(r, z[e]) != p[0] || !stands(i, z[e]) || !member(depth, v0 + i, z[e])) continue;
-          const int at = atomicAdd(&s.n, 1);
-          if (at < kList) s.list[at] = Item{down_key(z[e]), v0 + i, by ? mass<false>(r, z[e], table) : 1};
-        }
+    for (int q = 0; q < quads; ++q) {
+      float z[4];
+      get(q, z);
+      int hits = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d = distance(r, z[e]);
+        hits |= (int)(only_that ? d == bin : d <= bin) << e;
       }
-      __syncthreads();
-      if (tid < ranks) cl.map_shared_rank(&s, tid)->counts[rank] = s.n;
-      cl.sync();
-      n = 0;
-      for (int q = 0; q < ranks; ++q) n += s.counts[q];
+      while (hits) {
+        const int e = __ffs(hits) - 1, i = place(q) + e;
+        hits &= hits - 1;
+        const float x = e == 0 ? z[0] : e == 1 ? z[1] : e == 2 ? z[2] : z[3];
+        if (!stands(i, x) || !wanted(i, x)) continue;
+        const int at = atomicAdd(&s.n, 1);
+        if (at < kList) s.list[at] = Item{down_key(x), v0 + i, masses ? mass<false>(r, x, table) : 1};
+      }
+    }
+    __syncthreads();
+    if (tid < ranks) cl.map_shared_rank(&s, tid)->counts[rank] = s.n;
+    cl.sync();
+    int n = 0;
+    for (int q = 0; q < ranks; ++q) n += s.counts[q];
+    if (n > kList) return n;
+    for (int i = tid; i < n; i += kThreads) {
+      int q = 0, j = i;
+      while (j >= s.counts[q]) j -= s.counts[q++];
+      if (KDA_CHECK(i < kList && q < ranks)) s.all[i] = cl.map_shared_rank(&s, q)->list[j];
+    }
+    __syncthreads();
+    return n;
+  };
+  // Cuts what stands off behind the entry with which its number, or its mass, reaches `target`, in bin p[0] with
+  // `before` in the bins before it; the mass up to and with that entry is in `sum` then (by mass).
+  auto cut = [&](bool by, u64 target, u64 before) {
+    int depth = 1, n;   // before: what lies before the entries whose digits are p[0] .. p[depth - 1]
+    for (;;) {
+      n = collect(p[0], true, by, [&](int i, float x) { return member(depth, v0 + i, x); });
       if (n <= kList) break;
       // too many: their next digit
       clear();
@@ -444,12 +462,6 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       p[depth++] = search(by, rest, low_part);
       before += low_part;
     }
-    for (int i = tid; i < n; i += kThreads) {
-      int q = 0, j = i;
-      while (j >= s.counts[q]) j -= s.counts[q++];
-      if (KDA_CHECK(i < kList && q < ranks)) s.all[i] = cl.map_shared_rank(&s, q)->list[j];
-    }
-    __syncthreads();
     // each CTA ranks its share of them, several lanes an entry where that is little
     const u64 want = target - before;
     const int each = (n + ranks - 1) / ranks, first = rank * each, end = first + each < n ? first + each : n;
@@ -503,17 +515,87 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       }
     }
   };
+  const float* const draw = kProbs ? nullptr : noise + (int64_t)row * noise_pitch;
+  bool known = false;    // the mass of what stands, in `sum`
+  u64 target, before;
+  bool mass_cut = by_mass;
   if (by_count) {
     histogram(false);
-    cut(false, (u64)k);
-    __syncthreads();
+    target = (u64)k;
+    p[0] = search(false, target, before);
+    if (p[0] >= 0 && before + inside <= kFew) {
+      // Few entries up to that bin: they are ranked by number and mass at once, each CTA its share, an entry or less a
+      // thread, and all that follows is asked of them alone.
+      const int n = collect(p[0], false, true, [](int, float) { return true; });
+      const int each = (n + ranks - 1) / ranks, first = rank * each, end = first + each < n ? first + each : n;
+      static_assert(kFew <= kThreads && kFew <= kList, "a lane an entry at least");
+      const int share = each <= kThreads / 16 ? 16 : each <= kThreads / 8 ? 8 : each <= kThreads / 4 ? 4
+                        : each <= kThreads / 2 ? 2 : 1;
+      const int i = first + tid / share;
+      const bool lead = i < end && tid % share == 0;
+      const Item it = s.all[i < end ? i : 0];
+      int ahead = 0;
+      u64 was = 0;
+#pragma unroll 4
+      for (int j = tid % share; j < n; j += share) {
+        const Item o = s.all[j];
+        if (o.nk < it.nk || (o.nk == it.nk && o.idx < it.idx)) {
+          ++ahead;
+          was += o.w;
+        }
+      }
+      for (int o = 1; o < share; o *= 2) {
+        ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+        was += __shfl_xor_sync(0xffffffffu, was, o);
+      }
+      if (lead && ahead == k - 1)
+        for (int q = 0; q < ranks; ++q) cl.map_shared_rank(&s, q)->kth_mass = was + it.w;
+      cl.sync();
+      if (tid == 0) {
+        const double x = ceil((double)tp * (double)s.kth_mass);
+        const u64 t = x < 1. ? 1 : (u64)x;
+        s.target = by_mass && t < s.kth_mass ? t : s.kth_mass;
+      }
+      __syncthreads();
+      const bool stays = lead && ahead < k && was < s.target;
+      if (!kProbs) {
+        Best best{-1.f, 0x7fffffff};
+        if (stays && it.w >= least) {
+          const float pr = weight(r, value_of(it.nk)), u = draw[it.idx];
+          if (pr > 0.f && u == u) best = Best{pr / u, it.idx};
+        }
+        best = join(best, 1);
+        if (rank == 0 && tid == 0) token[row] = best.v < 0.f ? -1 : best.idx;
+        return;
+      }
+      if (stays && (ahead == k - 1 || was + it.w >= s.target)) {   // the last that does
+        for (int q = 0; q < ranks; ++q) {
+          Shared* o = cl.map_shared_rank(&s, q);
+          o->nk = it.nk;
+          o->idx = it.idx;
+          o->mass_incl = was + it.w;
+        }
+      }
+      cl.sync();
+      border = value_of(s.nk);
+      at = s.idx;
+      sum = s.mass_incl;
+      known = true;
+      mass_cut = false;
+    } else if (p[0] >= 0) {
+      cut(false, target, before);
+      __syncthreads();
+    }
   }
-  if (by_mass) {
+  if (mass_cut) {
     histogram(true);
-    cut(true, 0);
+    target = 0;
+    p[0] = search(true, target, before);
+    cut(true, target, before);
+    known = true;
   }
   if (kProbs) {
-    if (least || !by_mass) {  // the mass of what stands is not known yet
+    if (least || !known) {
       u64 part = 0;
 #pragma unroll 2
       for (int q = 0; q < quads; ++q) {
@@ -556,7 +638,6 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       put(q, o);
     }
   } else {
-    const float* from = noise + (int64_t)row * noise_pitch + v0;
     Best best{-1.f, 0x7fffffff};
     constexpr int kBatch = 4;   // fours whose noise is on its way at once
 #pragma unroll 1
@@ -570,7 +651,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
         for (int e = 0; e < 4; ++e) {
           const int i = place(q0 + q) + e;
           u[q][e] = __builtin_nanf("");          // a score that is no number never wins
-          if (q0 + q < quads && stands(i, z[e])) u[q][e] = from[i];
+          if (q0 + q < quads && stands(i, z[e])) u[q][e] = draw[v0 + i];
         }
       }
 #pragma unroll
