@@ -164,3 +164,18 @@ def test_verification_takes_the_probabilities():
     kept, token = kda.verify_draft(tokens, probs, probs, torch.rand(n * (drafts + 1), device="cuda") * 0.999,
                                    noise[last].contiguous(), cu)
     assert (kept == drafts + 1).all() and torch.equal(token, drawn[:, drafts].contiguous())
+
+
+@pytest.mark.parametrize("vocab", [700, 5000, 60000])
+def test_counts_around_the_number_that_is_ranked_at_once(vocab):
+    """top-k from below to above the few hundred entries that are ranked by number and mass at once, over values
+    of their own and over equal ones, alone and with the other filters."""
+    g = torch.Generator().manual_seed(vocab)
+    k = [2, 255, 300, 480, 505, 511, 512, 513, 530, 650, 699, 700]
+    n = len(k)
+    noise = _noise(n, vocab, g)
+    z = torch.randn(n, vocab, generator=g) * 2
+    for logits in (z, torch.round(z * 8) / 8, torch.where(z > 1.0, z, torch.full_like(z, -INF))):
+        _check(logits, noise, k=k)
+        _check(logits, noise, k=k, top_p=[0.3 + 0.06 * i for i in range(n)])
+        _check(logits, noise, k=k, top_p=[0.9] * n, min_p=[0.002 * i for i in range(n)], t=[1.5 - 0.1 * i for i in range(n)])
