@@ -449,11 +449,22 @@ template <int VEC> __device__ __forceinline__ void acc(float (&a)[VEC], const fl
   }
 }
 
-// Four rows of x and dy at p on their way to `to`, [row][x, dy][lane].
+// Four rows of x and dy on their way to `to`, [row][x, dy][lane]. Elements of two bytes, which no asynchronous copy
+// takes, go through registers: those that were asked for last time are put down, the next ones are asked for (8192
+// rows of 12287 channels: 313 us, 559 with each put down at once and one round of CTAs).
+template <typename Raw> struct Ahead {};
+template <> struct Ahead<__nv_bfloat16> { __nv_bfloat16 x[kQuad], dy[kQuad]; };
 template <typename T, int VEC>
-__device__ __forceinline__ void fetch_quad(typename Row<T, VEC>::Raw* to, const T*& x, int64_t x_pitch, const T*& dy,
-                                           int64_t dy_pitch, int rows) {
+__device__ __forceinline__ void fetch_quad(typename Row<T, VEC>::Raw* to, Ahead<typename Row<T, VEC>::Raw>& ahead,
+                                           const T*& x, int64_t x_pitch, const T*& dy, int64_t dy_pitch, int rows) {
   using Raw = typename Row<T, VEC>::Raw;
+  if constexpr (sizeof(Raw) == 2) {
+#pragma unroll
+    for (int u = 0; u < kQuad; ++u) {
+      to[(u * 2) * 32] = ahead.x[u];
+      to[(u * 2 + 1) * 32] = ahead.dy[u];
+    }
+  }
   auto one = [&](int u) {
     if constexpr (sizeof(Raw) >= 4) {
       asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_u32(to + (u * 2) * 32)), "l"(x),
@@ -463,8 +474,8 @@ __device__ __forceinline__ void fetch_quad(typename Row<T, VEC>::Raw* to, const 
                    "n"((int)sizeof(Raw))
                    : "memory");
     } else {
-      to[(u * 2) * 32] = Row<T, VEC>::load(x);
-      to[(u * 2 + 1) * 32] = Row<T, VEC>::load(dy);
+      ahead.x[u] = Row<T, VEC>::load(x);
+      ahead.dy[u] = Row<T, VEC>::load(dy);
     }
     x += x_pitch;
     dy += dy_pitch;
@@ -472,11 +483,15 @@ __device__ __forceinline__ void fetch_quad(typename Row<T, VEC>::Raw* to, const 
   if (rows >= kQuad) {
 #pragma unroll
     for (int u = 0; u < kQuad; ++u) one(u);
+  } else if constexpr (sizeof(Raw) == 2) {
+#pragma unroll
+    for (int u = 0; u < kQuad; ++u)
+      if (u < rows) one(u);
   } else {
 #pragma unroll 1
     for (int u = 0; u < rows; ++u) one(u);
   }
-  asm volatile("cp.async.commit_group;" ::: "memory");
+  if constexpr (sizeof(Raw) >= 4) asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 // Fours of rows in shared memory, one of them in work.
@@ -630,9 +645,10 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
     Raw* const ring = reinterpret_cast<Raw*>(s_ring) + warp * (kDepth * kQuad * 2 * 32) + lane;
     const T *xp = x + t_lo * x_pitch + c, *gp = dy + t_lo * dy_pitch + c;
     int to_ask = in ? (int)(t_end - t_lo) : 0;   // rows that are not on their way yet
-    int to = 0, from = 0;
+    int to = sizeof(Raw) == 2 ? kDepth - 1 : 0, from = 0;   // (what is put down first was not asked for)
+    Ahead<Raw> asked = {};
     auto ahead = [&] {
-      fetch_quad<T, VEC>(ring + to * (kQuad * 2 * 32), xp, x_pitch, gp, dy_pitch, to_ask);
+      fetch_quad<T, VEC>(ring + to * (kQuad * 2 * 32), asked, xp, x_pitch, gp, dy_pitch, to_ask);
       to_ask -= kQuad;
       to = to + 1 == kDepth ? 0 : to + 1;
     };
@@ -815,13 +831,23 @@ cudaError_t by_type(const ConvArgs& a, cudaStream_t st, bool token) {
   return wide ? by_width<T, VEC>(a, st, token) : by_width<T, 1>(a, st, token);
 }
 
-// CTAs a channel block: as many as fill the GPU twice over, of runs of 32 rows at least a warp.
+// CTAs a channel block, of runs of 32 rows at least a warp: as many as fit the GPU at two an SM, or, where
+// that leaves a fifth of it without work, as many as fill it two to four times over (8192 rows in bf16: 10240
+// channels by one round, 240 CTAs of 304 places, 135 us, by two 131; but 8192 channels, 256 places of 304, 105 by
+// one, 113 by two; one CTA an SM: 224 against 135 us for 12288 channels).
 struct BackShape {
   int64_t run, ctas;
 };
 BackShape back_shape(const kda_conv_desc_t& d, int vec) {
-  const int64_t blocks = (d.channels + 32 * vec - 1) / (32 * vec), T = d.total_tokens;
-  int64_t ctas = 2ll * gpu_sms() / blocks;
+  const int64_t blocks = (d.channels + 32 * vec - 1) / (32 * vec), T = d.total_tokens, room = 2ll * gpu_sms();
+  int64_t ctas = 1, best = 0;   // of 1024 places, those with work
+  for (int rounds = 1; rounds <= 4 && best < 820; ++rounds) {
+    const int64_t n = rounds * room / blocks, used = n * blocks * 1024 / (rounds * room);
+    if (used > best) {
+      ctas = n;
+      best = used;
+    }
+  }
   const int64_t most = (T + 32 * kBackWarps - 1) / (32 * kBackWarps);
   ctas = ctas < most ? ctas : most;
   ctas = ctas > 0 ? ctas : 1;
