@@ -37,7 +37,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kFine = 32, kCoarse = kBins / kFine;   // bins are looked through in two steps
 constexpr int kList = 1024;                // entries that are ranked against each other
-constexpr int kFew = 512;                  // entries up to the k-th that are ranked by number and mass at once
+constexpr int kFew = 512;                  // entries up to the k-th that are ranked by number and mass at once,
+constexpr int kPairs = 64;                 // pairs of them a thread
 constexpr int kMaxRanks = 8;
 constexpr int kMostQuads = 22;             // fours of entries a thread looks after at most
 constexpr int kPasses = 7;                 // digits: the distance, four of the value, two of the index
@@ -523,9 +524,11 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     histogram(false);
     target = (u64)k;
     p[0] = search(false, target, before);
-    if (p[0] >= 0 && before + inside <= kFew) {
+    const u64 up_to = before + inside;
+    if (p[0] >= 0 && up_to <= kFew && up_to * up_to <= (u64)kPairs * kThreads * ranks) {
       // Few entries up to that bin: they are ranked by number and mass at once, each CTA its share, an entry or less a
-      // thread, and all that follows is asked of them alone.
+      // thread, and all that follows is asked of them alone. (64 x 131072: 53 us, all by histograms of masses 70. One
+      // CTA a row, 320 x 1000, ranking 400 entries: 51 us, by masses 25.)
       const int n = collect(p[0], false, true, [](int, float) { return true; });
       const int each = (n + ranks - 1) / ranks, first = rank * each, end = first + each < n ? first + each : n;
       static_assert(kFew <= kThreads && kFew <= kList, "a lane an entry at least");
@@ -677,11 +680,13 @@ template <typename T, bool kProbs>
 cudaError_t launch(const SampleArgs& a, cudaStream_t st) {
   const int vocab = a.d.vocab, rows = a.d.num_rows, sms = gpu_sms(), e = sizeof(T);
   constexpr int kFour = 4 * kThreads;   // entries of a four a thread
-  // CTAs a row: as many as leave 32 entries a thread, so that two CTAs fit an SM; few rows are shared by more, as
-  // long as there is a four of entries for every thread
+  // CTAs a row: as many as leave 32 entries a thread, so that two CTAs fit an SM (320 x 131072 probabilities: 267
+  // us, with 64 entries a thread 318); few rows are shared by more, as long as all CTAs fit the GPU at once
+  // (64 x 20001, 4 CTAs a row: 29 us, 8: 39) and there is a four of entries for every thread (1 x 32003: 16 us, 2
+  // CTAs: 23; 40 x 4000, 2 CTAs: 20 us, 4: 23).
   int ranks = 1;
   while (ranks < kMaxRanks && (vocab > ranks * 8 * kFour ||
-                               ((int64_t)rows * ranks < 2 * sms && vocab > ranks * kFour)))
+                               ((int64_t)rows * ranks <= sms && vocab > ranks * kFour)))
     ranks *= 2;
   const int slice = ((vocab + ranks - 1) / ranks + 3) / 4 * 4, quads = (slice + kFour - 1) / kFour;
   const bool wide = (uintptr_t)a.logits % (4 * e) == 0 && a.d.logits_pitch % 4 == 0 &&

@@ -179,3 +179,17 @@ def test_counts_around_the_number_that_is_ranked_at_once(vocab):
         _check(logits, noise, k=k)
         _check(logits, noise, k=k, top_p=[0.3 + 0.06 * i for i in range(n)])
         _check(logits, noise, k=k, top_p=[0.9] * n, min_p=[0.002 * i for i in range(n)], t=[1.5 - 0.1 * i for i in range(n)])
+
+
+@pytest.mark.parametrize("vocab", [1999, 4001, 8190])
+def test_counts_around_what_fewer_ctas_rank_at_once(vocab):
+    """One, two and four CTAs a row rank fewer entries at once, as each has more pairs to look at: top-k around 181, 256
+    and 362, the square roots of 64 x 512 pairs of each."""
+    g = torch.Generator().manual_seed(vocab)
+    k = [170, 180, 181, 182, 200, 254, 256, 257, 350, 361, 363, 400]
+    n = len(k)
+    noise = _noise(n, vocab, g)
+    z = torch.randn(n, vocab, generator=g) * 2
+    for logits in (z, torch.round(z * 4) / 4):
+        _check(logits, noise, k=k)
+        _check(logits, noise, k=k, top_p=[0.4 + 0.05 * i for i in range(n)], min_p=[0.0, 0.01] * (n // 2))
