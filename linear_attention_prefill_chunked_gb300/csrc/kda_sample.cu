@@ -18,8 +18,10 @@
 // terms of the exponential series, the distance carried as two floats: good to 2^-30, where a float's sum of a
 // vocabulary would be off by more than the smallest entries that stand.
 //
-// Bound by HBM in principle (the row, and noise or probabilities), by the arithmetic of p and the cluster's
-// exchanges (three to six a row) in practice.
+// Bound by HBM in principle (the row, and noise or probabilities), by the arithmetic of p, the histogram's shared
+// atomics and the cluster's exchanges (three to six a row) in practice: 64 x 131072 fp32, all filters,
+// 53 us (0.63 TB/s); 1 x 32003 bf16 16 us; probabilities under top-p, 320 x 131072 fp32, 267 us (1.25 TB/s; without the
+// histogram's atomics 232; masses as one 64-bit atomic instead of three of 32 bits 333 against 296 at that step).
 #include <cooperative_groups.h>
 
 #include "kda_internal.cuh"
