@@ -4,8 +4,10 @@ taps, invalid device data, graphs.
 
 Bounds.  z is a sum of W + 1 products, off by (W + 2) 2^-24 of its terms' magnitudes; the activation's slope
 changes by at most half of that, and is itself off by at most 2^-18 (a fast exponential's 2^-20 at |z| <= 16,
-times 1 + |z|); a derivative by an input is a sum of W + 1 terms of dz; a sum over tokens adds 32 of them in
-a row in a strip, eight strips, every eighth tile in a row and eight of those."""
+times 1 + |z|); a derivative by an input is a sum of W + 1 terms of dz. A sum over tokens adds a run of them in
+a row, eight runs, and those sums of the CTAs of a channel block. A run is 48 rows at most (32, rounded up to 16s)
+where T / 256 + 1 CTAs are enough; else T / 8 / CTAs + 16, with 9 CTAs at least for up to 4096 channels (32 blocks of 32
+lanes by four, 304 places; of one channel a lane 1024) and one for any number."""
 import pytest
 import torch
 
@@ -25,7 +27,7 @@ def _inputs(lens, ch, W, dtype, seed=0, pitch=0, bias=True):
                 dfinal=z(N, W - 1, ch).to(dtype).cuda())
 
 
-def _ref(d, silu, lens, h0=True, dfinal=True):
+def _ref(d, silu, lens, h0=True, dfinal=True, ctas=9):
     """dx, dweight, dbias, dstate in 64 bits and a bound of each."""
     w = d["w"].double().cpu()
     ch, W = w.shape
@@ -34,7 +36,7 @@ def _ref(d, silu, lens, h0=True, dfinal=True):
                        dbias=torch.zeros(ch, dtype=torch.float64),
                        dstate=torch.zeros(N, W - 1, ch, dtype=torch.float64)) for _ in range(2)]
     unit, at = 2.0 ** -24, 0
-    adds = 32 + 8 + T / 64 / 8 + 8 + 2
+    adds = max(48, T / 8 / ctas + 16) + 8 + T / 256 + 1 + 2
     for n, m in enumerate(lens):
         first = d["h0"][n].double().cpu() if h0 else torch.zeros(W - 1, ch, dtype=torch.float64)
         ext = torch.cat([first, d["x"][at:at + m].double().cpu()])
@@ -107,6 +109,28 @@ def test_long_strips(dtype):
     lens = [1000, 31, 1, 5000, 2, 0, 2500, 3, 0, 1700]
     d = _inputs(lens, 3200, 4, dtype, seed=2)
     _check(_back(d, lens, True), *_ref(d, True, lens), dtype)
+
+
+@pytest.mark.parametrize("dtype,ch,pitch", [(BF, 20001, 0), (BF, 45000, 1), (F32, 20003, 0), (BF, 48000, 0), (F32, 41000, 4)])
+def test_more_channels_than_ctas_fit(dtype, ch, pitch):
+    """Rounds of CTAs, in every form of access."""
+    lens = [70, 0, 1, 200, 3, 40]
+    d = _inputs(lens, ch, 4, dtype, seed=3, pitch=pitch)
+    _check(_back(d, lens, True), *_ref(d, True, lens, ctas=1), dtype)
+
+
+def test_rows_of_no_sequence_spread_nothing():
+    """NaN in rows before, between (an invalid sequence) and behind the sequences."""
+    lens = [50, 30]
+    for dtype, ch in ((BF, 64), (BF, 37), (F32, 64)):
+        d = _inputs(lens, ch, 4, dtype, seed=4)
+        wide = torch.full((2, 100, ch), float("nan"), dtype=dtype, device="cuda")
+        wide[0, 7:87], wide[1, 7:87] = d["x"], d["dy"]
+        cu = torch.tensor([7, 57, 87], dtype=torch.int32, device="cuda")
+        got = kda.causal_conv_backward(wide[1], wide[0], d["w"], cu, bias=d["b"], activation="silu", state=d["h0"],
+                                       dfinal=d["dfinal"])
+        assert (got[0][:7] == 0).all() and (got[0][87:] == 0).all()
+        _check((got[0][7:87], *got[1:]), *_ref(d, True, lens), dtype)
 
 
 def test_without_states_and_bias():

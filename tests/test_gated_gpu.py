@@ -356,3 +356,37 @@ def test_no_rows_and_no_sequences():
         assert y.shape == (T, 16) and torch.equal(f, h0)
         dx, dr, di, da, dh = kda.gated_scan_backward(x, x, x, al, cu, c, i=x, state=h0, dfinal=h0)
         assert torch.equal(dh, h0) and (da == 0).all() and (dx == 0).all() and dx.shape == (T, 16)
+
+
+@pytest.mark.parametrize("dtype,ch", [(BF, 64), (BF, 37), (F32, 64)])
+def test_rows_of_no_sequence_spread_nothing(dtype, ch):
+    """NaN in the rows before and behind the sequences, in both passes: the sequences' results are those of a
+    call without these rows, and the other rows' gradients are 0."""
+    lens, a, b = [150, 0, 90], 61, 301
+    d = _inputs(lens, ch, dtype, seed=9)
+    pad = {k: torch.full((400, ch), float("nan"), dtype=dtype, device="cuda") for k in ("x", "r", "i", "dy")}
+    for k, t in pad.items():
+        t[a:b] = d[k]
+    cu = torch.tensor([a, a + 150, a + 150, b], dtype=torch.int32, device="cuda")
+    y, final, carries = kda.gated_scan(pad["x"], pad["r"], d["A_log"], cu, i=pad["i"], state=d["h0"],
+                                       output_carries=True)
+    got = kda.gated_scan_backward(pad["dy"], pad["x"], pad["r"], d["A_log"], cu, carries, i=pad["i"], state=d["h0"],
+                                  dfinal=d["dfinal"])
+    k = _ref(d, lens)
+    want, err = ref.backward(k, d["dy"], d["dfinal"], lens)
+    ref.check(y[a:b], k["y"], k["err"], dtype, "y")
+    for name, t in zip(("dx", "dr", "di", "dA_log", "dstate"), got):
+        if name in ("dx", "dr", "di"):
+            assert (t[:a] == 0).all() and (t[b:] == 0).all()
+            t = t[a:b]
+        ref.check(t, want[name], err[name], dtype if name in ("dx", "dr", "di") else F32, name)
+    assert torch.isfinite(final).all()
+
+
+def test_gradients_where_no_sequence_is():
+    """Rows, but no sequences: what the forward pass leaves before each 48 rows is not written then, and not used."""
+    x = torch.full((100, 32), float("nan"), device="cuda")
+    carries, al = torch.full((3, 32), float("nan"), device="cuda"), torch.zeros(32, device="cuda")
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dx, dr, di, da, dh = kda.gated_scan_backward(x, x, x, al, cu, carries, i=x)
+    assert all((t == 0).all() for t in (dx, dr, di, da)) and dh is None
