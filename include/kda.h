@@ -550,7 +550,7 @@ typedef struct {
  * entries of -inf, and those with p below 2^-126, are never drawn; where the largest is +inf its entries
  * share alike and no other stands.  A row without an entry that could be drawn gets -1, as does a row with
  * a negative temperature or a parameter that is no number (status bit KDA_DEVICE_BAD_PARAM).  p is
- * good to 2^-30 and sums of it are exact (in units of 2^-44 of the largest), so results do not
+ * good to 2^-28 and sums of it are exact (in units of 2^-44 of the largest), so results do not
  * depend on the order of additions.
  */
 kda_status_t kda_sample(const kda_sample_desc_t *desc, const void *logits, const float *noise,

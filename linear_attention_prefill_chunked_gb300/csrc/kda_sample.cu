@@ -15,14 +15,16 @@
 // An entry next to top-p's border stands or falls with the last digits of a sum over the row, so masses
 // are whole numbers, p in units of 2^-44, whose sums do not depend on their order: results are bit-identical
 // from run to run, whichever CTA adds first. p itself is 2^-n 2^(-j/32) 2^-r from a table, an entry a lane, and four
-// terms of the exponential series, the distance carried as two floats: good to 2^-30, where a float's sum of a
-// vocabulary would be off by more than the smallest entries that stand.
+// terms of the exponential series, the distance carried as two floats: good to 2^-28 (2^-31 on average), where a
+// float's sum of a vocabulary would be off by more than the smallest entries that stand.
 //
 // Bound by HBM in principle (the row, and noise or probabilities), by the arithmetic of p, the histogram's shared
 // atomics and the cluster's exchanges (three to six a row) in practice: 64 x 131072 fp32, all filters,
-// 53 us (0.63 TB/s); 1 x 32003 bf16 16 us; probabilities under top-p, 320 x 131072 fp32, 267 us (1.25 TB/s; without the
-// histogram's atomics 232; masses as one 64-bit atomic instead of three of 32 bits 333 against 296 at that step).
+// 53 us (0.63 TB/s); 1 x 32003 bf16 16 us; probabilities under top-p, 320 x 131072 fp32, 262 us (1.28 TB/s; without the
+// histogram's atomics 35 less; masses as one 64-bit atomic instead of three of 32 bits 333 against 296 at that step).
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "kda_internal.cuh"
 #include "tc_ptx.cuh"
@@ -113,9 +115,11 @@ constexpr int kRoundBits = 0x4b400000;
 __device__ __forceinline__ int distance(const Row& r, float z) {
   return __float_as_int(fminf((r.top - z) * r.ch * r.fx, (float)(kBins - 1)) + kRound) - kRoundBits;
 }
-// Adds v to a word of shared memory, unless it is 0 (without a branch).
-__device__ __forceinline__ void add_shared(uint32_t at, uint32_t v) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p red.shared.add.u32 [%0], %1;\n}\n" ::"r"(at), "r"(v) : "memory");
+// Adds v to a word of shared memory kOff bytes behind `at`, unless it is 0 (without a branch).
+template <int kOff> __device__ __forceinline__ void add_shared(uint32_t at, uint32_t v) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p red.shared.add.u32 [%0 + %2], %1;\n}\n" ::"r"(at), "r"(v),
+               "n"(kOff)
+               : "memory");
 }
 // The distance from the maximum in octaves of p, as two floats.
 __device__ __forceinline__ void octaves(const Row& r, float z, float& yh, float& yl) {
@@ -149,7 +153,8 @@ template <bool kWarp> __device__ __forceinline__ u64 mass(const Row& r, float z,
     f = (float)(uint32_t)(whole >> 20) * 5.9604644775390625e-8f;
   }
   const int fine = __float2int_rn(f * e * 68719476736.f);    // of 2^36
-  return yh < 45.f ? (whole + ((u64)(long long)fine << 8)) >> n : 0;
+  asm("mad.wide.s32 %0, %1, 256, %0;" : "+l"(whole) : "r"(fine));
+  return yh < 45.f ? whole >> n : 0;
 }
 // p to 2^-22
 __device__ __forceinline__ float weight(const Row& r, float z) {
@@ -339,13 +344,15 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     return true;
   };
   const uint32_t hist = tc::smem_u32(s.cnt);
-  auto add_to = [&](int bin, u64 w, uint32_t count) {
+  auto add_count = [&](int bin, bool one) {
+    if (KDA_CHECK(bin >= 0 && bin < kBins)) add_shared<0>(hist + bin * 4, one);
+  };
+  auto add_mass = [&](int bin, u64 w) {
     if (!KDA_CHECK(bin >= 0 && bin < kBins)) return;
     const uint32_t to = hist + bin * 4, lo = (uint32_t)w;
-    add_shared(to, count);
-    add_shared(to + kBins * 4, lo & 0xffff);
-    add_shared(to + 2 * kBins * 4, lo >> 16);
-    add_shared(to + 3 * kBins * 4, (uint32_t)(w >> 32));
+    add_shared<kBins * 4>(to, lo & 0xffff);
+    add_shared<2 * kBins * 4>(to, lo >> 16);
+    add_shared<3 * kBins * 4>(to, (uint32_t)(w >> 32));
   };
   auto clear = [&] {
     for (int i = tid; i < kBins; i += kThreads) s.cnt[i] = s.part[0][i] = s.part[1][i] = s.part[2][i] = 0;
@@ -458,7 +465,8 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
         for (int e = 0; e < 4; ++e) {
           const int i = place(q) + e;
           if (distance(r, z[e]) != p[0] || !stands(i, z[e]) || !member(depth, v0 + i, z[e])) continue;
-          add_to(digit(depth, v0 + i, z[e]), by ? mass<false>(r, z[e], table) : 0, by ? 0 : 1);
+          if (by) add_mass(digit(depth, v0 + i, z[e]), mass<false>(r, z[e], table));
+          else add_count(digit(depth, v0 + i, z[e]), true);
         }
       }
       u64 rest = target - before, low_part;
@@ -494,27 +502,32 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     sum = s.mass_incl;
   };
 
-  // what stands into a histogram, by number or by mass
+  // what stands into a histogram, by number or by mass (with nothing cut off yet, masked entries have none: 260 us
+  // for 320 x 131072 probabilities, 265 where each entry is asked)
+  auto masses = [&](auto cut_off) {
+#pragma unroll 2
+    for (int q = 0; q < quads; ++q) {
+      float z[4];
+      get(q, z);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const u64 w = mass<true>(r, z[e], table);
+        add_mass(distance(r, z[e]), !cut_off || stands(place(q) + e, z[e]) ? w : 0);
+      }
+    }
+  };
   auto histogram = [&](bool by) {
     clear();
     if (by) {
-#pragma unroll 2
-      for (int q = 0; q < quads; ++q) {
-        float z[4];
-        get(q, z);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const u64 w = mass<true>(r, z[e], table);
-          add_to(distance(r, z[e]), stands(place(q) + e, z[e]) ? w : 0, 0);
-        }
-      }
+      if (border == kMaskedOut) masses(std::false_type());
+      else masses(std::true_type());
     } else {
 #pragma unroll 2
       for (int q = 0; q < quads; ++q) {
         float z[4];
         get(q, z);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) add_to(distance(r, z[e]), 0, stands(place(q) + e, z[e]));
+        for (int e = 0; e < 4; ++e) add_count(distance(r, z[e]), stands(place(q) + e, z[e]));
       }
     }
   };

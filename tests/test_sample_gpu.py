@@ -2,7 +2,7 @@
 largest, every filter alone and together, equal values, masks, extreme parameters, rows with nothing left,
 pitched and misaligned rows, graphs.
 
-Tokens and which entries stand have to be equal: sums are exact to 2^-30 of an entry, and the inputs are
+Tokens and which entries stand have to be equal: sums are exact to 2^-28 of an entry, and the inputs are
 fixed ones whose borders lie further apart.  Probabilities are one fp32 quotient of p (relative error 2^-22:
 its series, its table entry, a product) and a sum, rounded three times: 2^-21."""
 import pytest
