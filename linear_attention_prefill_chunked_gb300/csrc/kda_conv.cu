@@ -372,7 +372,7 @@ conv_token_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
 // in a fixed order. Four rows at a time: where they, and W-1 on either side, are of one sequence, nothing is looked up;
 // else row by row. Which sequence a row belongs to is written down beforehand by a small kernel.
 // 32768 x 12288 bf16, 4 taps, SiLU: 460 us, 5.3 TB/s, 78 % of the copy rate; its two special functions and some 30
-// other instructions an element take about as long as its bytes. 2741 x 1003 fp32 in 37 sequences: 29 us, three
+// other instructions an element take about as long as its bytes. 2741 x 1003 fp32 in 37 sequences: 25 us, three
 // launches and runs of 32 rows whose sequences are looked up one by one.
 constexpr int kBackWarps = 8;
 constexpr int kBackThreads = kBackWarps * 32;
@@ -871,8 +871,7 @@ cudaError_t launch_back(const ConvBackArgs& a, cudaStream_t st) {
   float* part = reinterpret_cast<float*>(a.ws + back_part(a.d));
   uint32_t* status = &reinterpret_cast<WsHeader*>(a.ws)->status;
   int64_t plan = (a.d.total_tokens + 1023) / 1024, most = 2ll * gpu_sms();
-  const int64_t rows = a.dstate ? row_blocks(a.d.num_seqs, (int64_t)(W - 1) * ch) : 1;
-  plan = plan > rows ? plan : rows;
+  if (a.dstate) plan += row_blocks(a.d.num_seqs, (int64_t)(W - 1) * ch, most);
   plan = plan < 1 ? 1 : plan > most ? most : plan;
   conv_back_plan_kernel<T><<<(unsigned)plan, 1024, 0, st>>>(a.cu, a.d.num_seqs, a.d.total_tokens, status, seq,
                                                           (const T*)a.dfinal, (T*)a.dstate, (int64_t)(W - 1) * ch);

@@ -44,6 +44,7 @@
 // sequence: 263 us.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kda_internal.cuh"
@@ -1096,9 +1097,8 @@ cudaError_t launch_plan(const GatedArgs& a, const Layout& l, const float* from, 
                         cudaStream_t st) {
   const int64_t most = 2ll * gpu_sms(), unset = (int64_t)((l.seq - l.agg) / 16);
   int64_t blocks = (a.d.total_tokens + kPlanRows - 1) / kPlanRows;
-  auto least = [&](int64_t n) { blocks = blocks > n ? blocks : n; };
-  least((unset + 4095) / 4096);
-  if (to) least(row_blocks(a.d.num_seqs, a.d.channels));
+  blocks = std::max(blocks, (unset + 4095) / 4096);
+  if (to) blocks += row_blocks(a.d.num_seqs, a.d.channels, most);
   blocks = blocks < 1 ? 1 : blocks > most ? most : blocks;
   gated_plan_kernel<<<(unsigned)blocks, 1024, 0, st>>>(
       a.cu, a.idx, a.d.num_seqs, a.d.total_tokens, a.d.num_slots, reinterpret_cast<WsHeader*>(a.ws),

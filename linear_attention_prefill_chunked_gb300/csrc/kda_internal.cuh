@@ -215,24 +215,30 @@ __device__ __forceinline__ void sequences_of(int* s_seq, const int32_t* cu, cons
 }
 
 // Rows of `row` elements of the sequences without tokens: to <- from (zeros if null); with `zero_bad` those of
-// invalid sequences become 0.  A warp of the grid's (32 a block) takes 256 elements of 32 sequences at a time.
-constexpr int kRowChunk = 256;
+// invalid sequences become 0.  A warp of the grid's (32 a block, the last block's first: others have their rows'
+// sequences to see to) takes 256 elements of 32 sequences at a time, of every eighth of them where the grid has
+// warps enough (2741 x 1003 fp32 in 37 sequences, 7 of them empty: the convolution's backward pass 25 us, 29 where
+// a warp takes all 32 and the first blocks come first).
+constexpr int kRowChunk = 256, kRowParts = 8;
 template <typename T>
 __device__ __forceinline__ void rows_without_tokens(const int32_t* cu, int N, int64_t total, const T* from, T* to,
                                                     int64_t row, bool zero_bad) {
   const int lane = threadIdx.x & 31;
   const int64_t chunks = (row + kRowChunk - 1) / kRowChunk, pairs = ((int64_t)N + 31) / 32 * chunks;
-  for (int64_t w = blockIdx.x * 32ll + (threadIdx.x >> 5); w < pairs; w += gridDim.x * 32ll) {
-    const int n = (int)(w / chunks * 32) + lane;
+  const int parts = pairs * kRowParts <= gridDim.x * 32ll ? kRowParts : 1;
+  for (int64_t w = (gridDim.x - 1 - blockIdx.x) * 32ll + (threadIdx.x >> 5); w < pairs * parts; w += gridDim.x * 32ll) {
+    const int64_t group = w / parts / chunks * 32;
+    const unsigned mine = parts == 1 ? 0xffffffffu : 0x01010101u << (w % parts);
+    const int n = (int)group + lane;
     int64_t a = 0, b = 1;
     const bool ok = n < N && seq_bounds(cu, n, total, &a, &b);
     const unsigned empty = __ballot_sync(0xffffffffu, ok && a == b);
-    unsigned todo = empty | __ballot_sync(0xffffffffu, n < N && !ok && zero_bad);
+    unsigned todo = (empty | __ballot_sync(0xffffffffu, n < N && !ok && zero_bad)) & mine;
     while (todo) {
       const int i = __ffs(todo) - 1;
       todo &= todo - 1;
       const bool copy = ((empty >> i) & 1) && from;
-      const int64_t at = (w / chunks * 32 + i) * row, c0 = w % chunks * kRowChunk + lane;
+      const int64_t at = (group + i) * row, c0 = w / parts % chunks * kRowChunk + lane;
       T v[kRowChunk / 32];
 #pragma unroll
       for (int j = 0; j < kRowChunk / 32; ++j)
@@ -243,9 +249,10 @@ __device__ __forceinline__ void rows_without_tokens(const int32_t* cu, int N, in
     }
   }
 }
-// Blocks of 32 warps for it.
-inline int64_t row_blocks(int64_t N, int64_t row) {
-  return ((N + 31) / 32 * ((row + kRowChunk - 1) / kRowChunk) + 31) / 32;
+// Blocks of 32 warps for it, beside the others of a grid of `most`.
+inline int64_t row_blocks(int64_t N, int64_t row, int64_t most) {
+  const int64_t pairs = (N + 31) / 32 * ((row + kRowChunk - 1) / kRowChunk), parts = (pairs * kRowParts + 31) / 32;
+  return parts <= most ? parts : (pairs + 31) / 32;
 }
 
 // Two fp32 operations as one packed instruction, each rounded to nearest.
