@@ -883,7 +883,8 @@ cudaError_t launch_back(const ConvBackArgs& a, cudaStream_t st) {
   auto* kernel = conv_back_kernel<T, VEC, W>;
   if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
   e = launch_behind(
-      kernel, grid, dim3(kBackThreads), bytes, st, (const T*)a.dy, a.dy_pitch, (const T*)a.x, a.d.x_pitch, (const T*)a.w, (const T*)a.bias, a.cu, seq,
+      kernel, grid, dim3(kBackThreads), bytes, st, (const T*)a.dy, a.dy_pitch,
+      (const T*)a.x, a.d.x_pitch, (const T*)a.w, (const T*)a.bias, a.cu, seq,
       (const T*)a.state, (const T*)a.dfinal, (T*)a.dx, (T*)a.dstate, part, status, a.d.total_tokens, s.run, ch,
       a.d.silu != 0);
   if (e != cudaSuccess) return e;

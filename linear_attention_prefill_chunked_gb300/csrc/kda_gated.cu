@@ -149,9 +149,10 @@ template <typename T, int V> __device__ __forceinline__ void store(T* p, const C
 }
 // ---- gates ----------------------------------------------------------------------------------
 // e^-v and sigmoid(v) = 1 / (1 + e^-v). Where e^-v is kept below 1e37, e^-v sigmoid(v) = 1 - sigmoid(v) has its
-// leading digits at either end (and the Newton step has no infinity to meet). bf16 inputs take the fast exponential and reciprocal, good to 2^-21 and
-// |v| 2^-24: far below those inputs' own rounding, and what is fp32 of the results (states, dA_log) keeps
-// 2^-19. fp32 inputs take CUDA's exponential and a Newton step behind the reciprocal.
+// leading digits at either end (and the Newton step has no infinity to meet). bf16 inputs take the fast exponential
+// and reciprocal, good to 2^-21 and |v| 2^-24: far below those inputs' own rounding, and what is fp32 of the results
+// (states, dA_log) keeps 2^-18 of a step's terms for |v| up to 8. fp32 inputs take CUDA's exponential and a Newton step
+// behind the reciprocal.
 template <bool kFast, bool kBounded, int V> __device__ __forceinline__ Ch<V> exp_neg(const Ch<V>& v) {
   Ch<V> e;
   if constexpr (kFast) e = mul(v, all<V>(-kLog2e));
@@ -531,7 +532,8 @@ __device__ __forceinline__ void fetch_own_done() {
 // ---- forward --------------------------------------------------------------------------------
 template <typename T, int V, bool kGate, int S>
 __global__ void __launch_bounds__(kAll, kScanCtas)
-gated_scan_kernel(const __grid_constant__ Maps maps, const T* __restrict__ x, int64_t x_pitch, const T* __restrict__ r, int64_t r_pitch,
+gated_scan_kernel(const __grid_constant__ Maps maps, const T* __restrict__ x, int64_t x_pitch,
+                  const T* __restrict__ r, int64_t r_pitch,
                   const T* __restrict__ ig, int64_t i_pitch, const float* __restrict__ a_log,
                   const float* state, const int32_t* __restrict__ idx, int64_t num_slots, int64_t stride,
                   float* final_state, T* __restrict__ y, float* __restrict__ carries, Plan plan, WsHeader* hdr,
@@ -725,7 +727,8 @@ template <int V> struct BackShared : Shared<V> {
 
 template <typename T, int V, bool kGate, int S>
 __global__ void __launch_bounds__(kAll, kBackCtas)
-gated_back_kernel(const __grid_constant__ Maps maps, const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict__ x, int64_t x_pitch,
+gated_back_kernel(const __grid_constant__ Maps maps, const T* __restrict__ dy, int64_t dy_pitch,
+                  const T* __restrict__ x, int64_t x_pitch,
                   const T* __restrict__ r, int64_t r_pitch, const T* __restrict__ ig, int64_t i_pitch,
                   const float* __restrict__ a_log, const float* __restrict__ carries,
                   const float* __restrict__ state, const float* __restrict__ dfinal, T* __restrict__ dx,
@@ -1165,7 +1168,8 @@ cudaError_t run_scan(const GatedArgs& a, cudaStream_t st) {
   const int64_t pitch[] = {a.d.x_pitch, a.d.r_pitch, a.d.i_pitch};
   const bool wide = maps_of<T>(&maps, base, pitch, kGate ? 3 : 2, a.d.total_tokens, a.d.channels, 32 * V, kRows * kWarps);
   return launch_behind(
-      kernel, dim3(grid), dim3(kAll), bytes, st, maps, (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i, a.d.i_pitch, a.a_log, a.state_in,
+      kernel, dim3(grid), dim3(kAll), bytes, st, maps, (const T*)a.x, a.d.x_pitch,
+      (const T*)a.r, a.d.r_pitch, (const T*)a.i, a.d.i_pitch, a.a_log, a.state_in,
       a.idx, a.d.num_slots, a.slot_stride, a.state_out, (T*)a.y, a.carries, p,
       reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, wide, pipeline_wait_limit_ns());
 }
@@ -1188,7 +1192,8 @@ cudaError_t run_back(const GatedArgs& a, cudaStream_t st) {
     const bool wide = maps_of<T>(&maps, base, pitch, kGate ? 4 : 3, a.d.total_tokens, a.d.channels, 32 * V,
                                  kBackRows * kWarps);
     e = launch_behind(
-        kernel, dim3(grid), dim3(kAll), bytes, st, maps, (const T*)a.dy, a.dy_pitch, (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i,
+        kernel, dim3(grid), dim3(kAll), bytes, st, maps, (const T*)a.dy, a.dy_pitch,
+        (const T*)a.x, a.d.x_pitch, (const T*)a.r, a.d.r_pitch, (const T*)a.i,
         a.d.i_pitch, a.a_log, a.carries, a.state_in, a.dfinal, (T*)a.dx, (T*)a.dr, (T*)a.di, a.dstate, part, p,
         reinterpret_cast<WsHeader*>(a.ws), a.d.total_tokens, a.d.channels, wide,
         pipeline_wait_limit_ns());
