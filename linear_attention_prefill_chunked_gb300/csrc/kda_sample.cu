@@ -377,7 +377,8 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   };
   // The bin of the cluster's histogram (filled, in each CTA) where the count or the mass reaches `target`, and what
   // lies in it and in the bins before it; -1 if it does not. A target of 0 stands for top-p of all mass, and is
-  // set.
+  // set. Of its two cluster barriers the second stands between the reads of `coarse` and what the other CTAs write
+  // there in the next search, whose first stands behind the reads of `fine`: every way out passes both.
   u64 inside;
   auto search = [&](bool by, u64& target, u64& before) {
     __syncthreads();
@@ -401,7 +402,10 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       target = s.target;
     }
     const int g = find(v, target, before, total);
-    if (total < target) return -1;
+    if (total < target) {
+      cl.sync();
+      return -1;
+    }
     if (warp < ranks) cl.map_shared_rank(&s, warp)->fine[rank][lane] = sum_of(g * kFine + lane, by);
     cl.sync();
     v = 0;
