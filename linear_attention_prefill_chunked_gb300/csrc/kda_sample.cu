@@ -576,10 +576,11 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       if (tid == 0) {
         const double x = ceil((double)tp * (double)s.kth_mass);
         const u64 t = x < 1. ? 1 : (u64)x;
-        s.target = by_mass && t < s.kth_mass ? t : s.kth_mass;
+        s.target = t < s.kth_mass ? t : s.kth_mass;
       }
       __syncthreads();
-      const bool stays = lead && ahead < k && was < s.target;
+      // (without top-p by number alone: entries below 2^-44 of the largest add no mass, and stand all the same)
+      const bool stays = lead && ahead < k && (!by_mass || was < s.target);
       if (!kProbs) {
         Best best{-1.f, 0x7fffffff};
         if (stays && it.w >= least) {
@@ -590,7 +591,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
         if (rank == 0 && tid == 0) token[row] = best.v < 0.f ? -1 : best.idx;
         return;
       }
-      if (stays && (ahead == k - 1 || was + it.w >= s.target)) {   // the last that does
+      if (stays && (by_mass ? was + it.w >= s.target : ahead == k - 1)) {   // the last that does
         for (int q = 0; q < ranks; ++q) {
           Shared* o = cl.map_shared_rank(&s, q);
           o->nk = it.nk;
