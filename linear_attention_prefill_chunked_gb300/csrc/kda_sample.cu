@@ -92,8 +92,8 @@ struct alignas(16) Shared {
   uint32_t nk;                          // the entry that was sought,
   int idx;
   u64 mass_incl, kth_mass;              // and the mass up to and with it; the same of the k-th
-  float ch, cl, inv;                    // what is worked out in 64 bits, by one thread
-  u64 least, target;
+  float ch, cl, far, far_low, inv;      // what is worked out in 64 bits, by one thread
+  u64 target;
 };
 
 static_assert(kMostQuads * 4 * kThreads < 65536, "sums of 16 bits");
@@ -233,13 +233,15 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   }
   const float temp = temperature ? temperature[row] : temperature_all;
   const int k = top_k ? top_k[row] : top_k_all;
-  const float tp = top_p ? top_p[row] : top_p_all;
+  const float tp = top_p ? top_p[row] : top_p_all, mp = min_p ? min_p[row] : min_p_all;
+  const bool by_ratio = mp > 0.f;
   if (tid == 0) {
     const double c = fmin(1.4426950408889634074 / (double)temp, 1e38);   // (at temperature 0 not used)
     s.ch = (float)c;
     s.cl = (float)(c - (double)s.ch);
-    const float mp = fminf(min_p ? min_p[row] : min_p_all, 1.f);
-    s.least = mp > 0.f ? (u64)ceil((double)mp * (double)kOne) : 0;
+    const double far = by_ratio ? -log2((double)fminf(mp, 1.f)) : 0.;
+    s.far = (float)far;
+    s.far_low = (float)(far - (double)s.far);
   }
 
   // every CTA of the cluster has to have started before another writes into its shared memory
@@ -325,7 +327,14 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   r.cl = s.cl;
   r.fx = (kBins - 1) / fmaxf(fminf((top.v - low) * r.ch, 64.f), 1e-30f);  // over the row's range, 64 octaves at most
   const bool by_count = k > 0 && k < vocab, by_mass = tp < 1.f;
-  const u64 least = s.least;
+  // Min-p asks p >= min_p of the distances in octaves, as two floats, for the smallest p as well as for the largest
+  // (whole units of 2^-44 have few digits of those); what is as near to the border as their roundings, 2^-38, stands.
+  const float far = s.far, far_low = s.far_low;
+  auto near = [&](float x) {
+    float yh, yl;
+    octaves(r, x, yh, yl);
+    return (yh - far) + (yl - far_low) <= 3.637978807091713e-12f;   // 2^-38
+  };
 
   // What stands so far: entries above `border`, and those that equal it up to index `at`. Masked ones never do.
   float border = kMaskedOut;
@@ -583,7 +592,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       const bool stays = lead && ahead < k && (!by_mass || was < s.target);
       if (!kProbs) {
         Best best{-1.f, 0x7fffffff};
-        if (stays && it.w >= least) {
+        if (stays && (!by_ratio || near(value_of(it.nk)))) {
           const float pr = weight(r, value_of(it.nk)), u = draw[it.idx];
           if (pr > 0.f && u == u) best = Best{pr / u, it.idx};
         }
@@ -618,7 +627,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
     known = true;
   }
   if (kProbs) {
-    if (least || !known) {
+    if (by_ratio || !known) {
       u64 part = 0;
 #pragma unroll 2
       for (int q = 0; q < quads; ++q) {
@@ -627,7 +636,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const u64 w = mass<true>(r, z[e], table);
-          if (stands(place(q) + e, z[e]) && w >= least) part += w;
+          if (stands(place(q) + e, z[e]) && (!by_ratio || near(z[e]))) part += w;
         }
       }
 #pragma unroll
@@ -656,7 +665,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         o[e] = 0.f;
-        if (stands(place(q) + e, z[e]) && (least == 0 || mass<false>(r, z[e], table) >= least)) o[e] = weight(r, z[e]) * inv;
+        if (stands(place(q) + e, z[e]) && (!by_ratio || near(z[e]))) o[e] = weight(r, z[e]) * inv;
       }
       put(q, o);
     }
@@ -685,7 +694,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
         for (int e = 0; e < 4; ++e) {
           if (u[q][e] != u[q][e]) continue;
           const float pr = weight(r, z[e]);
-          if (pr > 0.f && (least == 0 || mass<false>(r, z[e], table) >= least))
+          if (pr > 0.f && (!by_ratio || near(z[e])))
             best = better(best, Best{pr / u[q][e], v0 + place(q0 + q) + e});
         }
       }

@@ -1,6 +1,6 @@
-"""Entries far below the largest: whatever top-k keeps stands down to 2^-126 of it, through every path of the
+"""Entries far below the largest: whatever top-k or min-p keeps stands down to 2^-126 of it, through every path of the
 search, although a mass (in units of 2^-44) has no digit left of it.  Against the definition in 64 bits, as in
-``test_sample_gpu``."""
+``test_sample_gpu``; no entry lies within 2^-38 of a border of min-p."""
 import pytest
 import torch
 
@@ -25,6 +25,7 @@ def test_few_entries():
     z = torch.tensor([[0.0, -40.0, -50.0, -200.0]]).repeat(6, 1)
     noise = torch.tensor([[1e25, 1.0, 1e-3, 1.0]]).repeat(6, 1)
     _check(z, noise, k=[2, 3, 4, 1, 0, 7])
+    _check(z, noise, k=[2, 3, 3, 2, 0, 3], min_p=[1e-20, 1e-20, 1e-17, 1e-17, 1e-20, 1e-30])
 
 
 @pytest.mark.parametrize("vocab", [700, 5000, 32003, 140000])
@@ -34,6 +35,7 @@ def test_top_k_at_low_temperatures(vocab, dtype, step):
     for t in (0.05, 0.1, 0.2):
         z, noise = _rows(len(k), vocab, [t] * len(k), dtype, vocab + step, step)
         _check(z, noise, t=[t] * len(k), k=k)
+        _check(z, noise, t=[t] * len(k), k=k, min_p=[1e-20, 1e-10, 0.0, 1e-14, 1e-13, 1e-30, 1e-25, 1e-5])
 
 
 def _near_one(top_p, k, t, z, noise):
@@ -62,3 +64,13 @@ def test_top_p_near_one(vocab, dtype, step):
     for t in (0.05, 0.1, 0.2):
         z, noise = _rows(len(k), vocab, [t] * len(k), dtype, vocab + step, step)
         _near_one([0.5, 0.9, 0.99, 0.999, 0.9999, 0.99999, 0.999999, 0.9999999], k, t, z, noise)
+
+
+@pytest.mark.parametrize("vocab", [3000, 32003])
+def test_small_min_p(vocab):
+    """Borders below a mass's unit of 2^-44, and above it where it has few digits."""
+    m = [1e-20, 1e-13, 2.0 ** -44, 2.0 ** -43, 1e-12, 1e-11, 1e-9, 1e-6, 1e-30, 1e-37, 1e-45, 0.0]
+    t = [0.1, 0.3, 0.2, 0.25, 0.3, 0.3, 0.35, 0.4, 0.07, 0.06, 0.05, 0.05]
+    z, noise = _rows(len(m), vocab, t, F32, vocab)
+    for extra in (dict(), dict(k=[vocab - 1] * len(m)), dict(k=[100] * len(m)), dict(top_p=[0.999] * len(m))):
+        _check(z, noise, t=t, min_p=m, **extra)
