@@ -375,7 +375,8 @@ kda_status_t kda_causal_conv_decode(const kda_conv_desc_t *desc, const void *x, 
  *            pool's fields are ignored
  *   dfinal, dstate  [N, W-1, Ch] dtype or NULL; dstate is 0 for an invalid sequence
  *   dx       [T, Ch] dtype, packed, must not overlap an input; 0 in rows of no valid sequence
- *   dweight  [Ch, W] fp32    dbias [Ch] fp32 or NULL: sums over all tokens in fp32, in a fixed order
+ *   dweight  [Ch, W] fp32    dbias [Ch] fp32 or NULL (it may be asked for without a bias, which counts as
+ *            zeros): sums over all tokens in fp32, in a fixed order
  *   workspace  kda_causal_conv_backward_workspace_size(desc) bytes
  *
  * Where lengths run backwards, so that sequences overlap, a row goes to the last of its sequences, whose

@@ -507,7 +507,7 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
                  const T* __restrict__ w, const T* __restrict__ bias, const int32_t* __restrict__ cu,
                  const int32_t* __restrict__ seq, const T* __restrict__ state, const T* __restrict__ dfinal,
                  T* __restrict__ dx, T* __restrict__ dstate, float* __restrict__ part, uint32_t* __restrict__ status,
-                 int64_t total, int64_t run, int ch, bool act) {
+                 int64_t total, int64_t run, int ch, bool act, bool want_db) {
   using R = Row<T, VEC>;
   using Raw = typename R::Raw;
   constexpr int H = W - 1;
@@ -554,7 +554,7 @@ conv_back_kernel(const T* __restrict__ dy, int64_t dy_pitch, const T* __restrict
   auto count = [&] {
 #pragma unroll
     for (int j = 0; j < W; ++j) acc<VEC>(dw[j], dz[H], win[j]);
-    if (!bias) return;
+    if (!want_db) return;   // (without a bias it is the derivative by one of zeros)
     if constexpr (VEC == 4) {
       add2(db[0], db[1], dz[H][0], dz[H][1]);
       add2(db[2], db[3], dz[H][2], dz[H][3]);
@@ -886,7 +886,7 @@ cudaError_t launch_back(const ConvBackArgs& a, cudaStream_t st) {
       kernel, grid, dim3(kBackThreads), bytes, st, (const T*)a.dy, a.dy_pitch,
       (const T*)a.x, a.d.x_pitch, (const T*)a.w, (const T*)a.bias, a.cu, seq,
       (const T*)a.state, (const T*)a.dfinal, (T*)a.dx, (T*)a.dstate, part, status, a.d.total_tokens, s.run, ch,
-      a.d.silu != 0);
+      a.d.silu != 0, a.db != nullptr);
   if (e != cudaSuccess) return e;
   return launch_behind(conv_sum_kernel, dim3((unsigned)((ch + 31) / 32), W + 1), dim3(256), 0, st, part, s.ctas, ch, W,
                        a.dw, a.db);
