@@ -294,8 +294,9 @@ kda_status_t kda_chunk_prefill_noalloc(const kda_desc_t *desc, const void *q, co
                                        void *o, cudaStream_t stream);
 
 /*
- * Bound of the internal pipeline waits of the tensor-core prefill and scan, for launches made
- * after the call (process-wide; 0 restores the default of 2 seconds; more than 2 s is
+ * Bound of the internal pipeline waits of the tensor-core prefill and scan, and of the gated
+ * recurrence's tiles for the tiles before them, for launches made after the call
+ * (process-wide; 0 restores the default of 2 seconds; more than 2 s is
  * KDA_ERR_INVALID_ARGUMENT).  The pages have no counterpart: it is the watchdog of this
  * library's own kernels.  Every wait between the kernel's producer and consumer warps
  * gives up after this long; the kernel then sets KDA_DEVICE_PIPE_TIMEOUT, stops taking

@@ -303,12 +303,14 @@ template <int V> __device__ __forceinline__ bool hear(const float* at, Pair<V>& 
   }
   return set;
 }
-// Whether a warp that waits for other tiles should go on: until one of them has given up, or for limit_ns.
+// Whether a warp that waits for other tiles should go on: until one of them has given up, or for limit_ns. It asks
+// at each 64th try, which is nothing beside seconds; where the limit is shorter than 64 trips take, at each.
+constexpr uint64_t kTriesNs = 100000;
 struct Patience {
   uint64_t t0 = 0;
   int tries = 0;
   __device__ __forceinline__ bool more(WsHeader* hdr, uint64_t limit_ns) {
-    if (++tries % 64) return true;
+    if (++tries % 64 && limit_ns >= kTriesNs) return true;
     if (*(volatile uint32_t*)&hdr->num_entries) return false;
     const uint64_t now = __shfl_sync(0xffffffffu, tc::globaltimer_ns(), 0);
     if (t0 == 0) t0 = now;
