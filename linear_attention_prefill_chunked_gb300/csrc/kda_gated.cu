@@ -232,16 +232,14 @@ template <int V> __device__ __forceinline__ Ch<V> root(Ch<V> w) {
   }
   return w;
 }
-// -g over sqrt(-w) and sqrt(-w), to 2^-22; both 0 where that is.
-template <int V> __device__ __forceinline__ void over_root(const Ch<V>& g, const Ch<V>& w, Ch<V>& q, Ch<V>& m) {
-  Ch<V> k;
+// -1 over sqrt(-w) and sqrt(-w), to 2^-22; both 0 where that is.
+template <int V> __device__ __forceinline__ void over_root(const Ch<V>& w, Ch<V>& k, Ch<V>& m) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(k.f[i]) : "f"(-w.f[i]));
     k.f[i] = w.f[i] > -1e-37f ? 0.f : -k.f[i];
   }
   m = mul(w, k);
-  q = mul(g, k);
 }
 
 // ---- planning -------------------------------------------------------------------------------
@@ -861,7 +859,7 @@ gated_back_kernel(const __grid_constant__ Maps maps, const T* __restrict__ dy, i
       e = mul(a, l);
       const Ch<V> er = exp_neg<kFast, true>(P::open(row.r)), sr = one_over<kFast>(er), g = mul(rate, sr);
       Ch<V> m, k, u = P::open(row.x);
-      over_root(g, lost(g, series(g), a), k, m);
+      over_root(lost(g, series(g), a), k, m);
       const Ch<V> ml = mul(m, l);
       ox = ml;
       if (kGate) {
@@ -870,8 +868,8 @@ gated_back_kernel(const __grid_constant__ Maps maps, const T* __restrict__ dy, i
         ox = mul(ml, si);
         oi = mul(mul(ml, u), mul(ei, si));
       }
-      // p = e (g h_{t-1} - a (g / m) u)
-      const Ch<V> p = mul(e, fma(mul(a, k), u, mul(g, hp)));
+      // p = e g h_{t-1} - e a (g / m) u, by e g: where g is large e is small or 0, but g h_{t-1} may pass fp32's range
+      const Ch<V> eg = mul(e, g), p = fma(mul(mul(eg, k), a), u, mul(eg, hp));
       orr = mul(p, mul(er, sr));
       return p;
     };
