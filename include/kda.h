@@ -477,7 +477,7 @@ typedef struct {
  *
  * Everything is fp32 inside, y rounded once; fp32 inputs take CUDA's accurate exponential, bf16 ones the
  * fast one (up to 2^-18 of what a step adds, for gates of 8 at most).  exp(a_log) counts as the largest
- * fp32 number at most.  Any Ch >= 1 and any alignment of whole elements; where Ch, the pitches and the pointers are
+ * fp32 number at most, a sigmoid below 2^-126 as 0.  Any Ch >= 1 and any alignment of whole elements; where Ch, the pitches and the pointers are
  * multiples of two elements a thread moves two channels at a time.  Rows of x that belong to no valid
  * sequence give no output; where lengths run backwards, so that sequences overlap, a row goes to the last
  * of its sequences and the others' outputs are unspecified.  Results are bit-identical from run to run.

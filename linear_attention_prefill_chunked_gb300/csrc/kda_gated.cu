@@ -148,8 +148,9 @@ template <typename T, int V> __device__ __forceinline__ void store(T* p, const C
   *reinterpret_cast<typename Pack<T, V>::Raw*>(p) = Pack<T, V>::close(c);
 }
 // ---- gates ----------------------------------------------------------------------------------
-// e^-v and sigmoid(v) = 1 / (1 + e^-v). Where e^-v is kept below 1e37, e^-v sigmoid(v) = 1 - sigmoid(v) has its
-// leading digits at either end (and the Newton step has no infinity to meet). bf16 inputs take the fast exponential
+// e^-v and sigmoid(v) = 1 / (1 + e^-v). Where e^-v is kept at 3e38 at most, e^-v sigmoid(v) = 1 - sigmoid(v) has its
+// leading digits at either end, unless sigmoid(v) is below 2^-126 and counts as 0: such a gate has no derivative (and
+// the Newton step has no infinity to meet). bf16 inputs take the fast exponential
 // and reciprocal, good to 2^-21 and |v| 2^-24: far below those inputs' own rounding, and what is fp32 of the results
 // (states, dA_log) keeps 2^-18 of a step's terms for |v| up to 8. fp32 inputs take CUDA's exponential and a Newton step
 // behind the reciprocal.
@@ -160,7 +161,7 @@ template <bool kFast, bool kBounded, int V> __device__ __forceinline__ Ch<V> exp
   for (int i = 0; i < V; ++i) {
     if constexpr (kFast) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.f[i]));
     else e.f[i] = expf(-v.f[i]);
-    if constexpr (kBounded) asm("min.NaN.f32 %0, %0, 0f7cf0bdc2;" : "+f"(e.f[i]));  // 1e37; NaN stays
+    if constexpr (kBounded) asm("min.NaN.f32 %0, %0, 0f7f61b1e6;" : "+f"(e.f[i]));  // 3e38; NaN stays
   }
   return e;
 }
