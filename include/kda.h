@@ -475,12 +475,16 @@ typedef struct {
  *            whose number is a multiple of KDA_GATED_CARRY_ROWS, for the backward pass
  *   workspace  kda_gated_scan_workspace_size(desc) bytes
  *
+ * Every row of a sequence counts alike, its first one too: models in which x enters a document's first
+ * row without sqrt(1 - a^2) have that row of x divided by it beforehand.
+ *
  * Everything is fp32 inside, y rounded once; fp32 inputs take CUDA's accurate exponential, bf16 ones the
  * fast one (up to 2^-18 of what a step adds, for gates of 8 at most).  exp(a_log) counts as the largest
- * fp32 number at most, a sigmoid below 2^-126 as 0.  Any Ch >= 1 and any alignment of whole elements; where Ch, the pitches and the pointers are
- * multiples of two elements a thread moves two channels at a time.  Rows of x that belong to no valid
- * sequence give no output; where lengths run backwards, so that sequences overlap, a row goes to the last
- * of its sequences and the others' outputs are unspecified.  Results are bit-identical from run to run.
+ * fp32 number at most, a sigmoid below 2^-126 as 0.  Any Ch >= 1 and any alignment of whole elements;
+ * where Ch, the pitches and the pointers are multiples of two elements a thread moves two channels at a
+ * time.  Rows of x that belong to no valid sequence give no output; where lengths run backwards, so that
+ * sequences overlap, a row goes to the last of its sequences and the others' outputs are unspecified.
+ * Results are bit-identical from run to run.
  */
 #define KDA_GATED_CARRY_ROWS 48
 kda_status_t kda_gated_scan(const kda_gated_desc_t *desc, const void *x, const void *r,
@@ -551,9 +555,11 @@ typedef struct {
  * At temperature 0 (and at top_k 1 or top_p <= 0) the first entry alone stands.  A NaN counts as -inf;
  * entries of -inf, and those with p below 2^-126, are never drawn; where the largest is +inf its entries
  * share alike and no other stands.  A row without an entry that could be drawn gets -1, as does a row with
- * a negative temperature or a parameter that is no number (status bit KDA_DEVICE_BAD_PARAM).  p is
- * good to 2^-28 and sums of it are exact (in units of 2^-44 of the largest), so results do not
- * depend on the order of additions.
+ * a negative temperature or a parameter that is no number (status bit KDA_DEVICE_BAD_PARAM).
+ *
+ * Accuracy: the sums that top-p's border is found by are of p to 2^-28, in whole units of 2^-44 of the largest,
+ * which add up to the same in any order; min-p's border is found to 2^-38 of p; p / noise and the
+ * probabilities below take p to 2^-22.  Results are bit-identical from run to run.
  */
 kda_status_t kda_sample(const kda_sample_desc_t *desc, const void *logits, const float *noise,
                         const float *temperature, const int32_t *top_k, const float *top_p,
@@ -562,7 +568,7 @@ kda_status_t kda_sample(const kda_sample_desc_t *desc, const void *logits, const
 
 /*
  * The probabilities of that draw, as kda_verify_draft wants them of target and draft: probs
- * [num_rows, vocab] fp32, packed, p_i over its sum for entries that stand, else 0 (throughout, for a row
+ * [num_rows, vocab] fp32, packed, p_i over its sum (to 2^-21) for entries that stand, else 0 (throughout, for a row
  * that gets token -1 above; 1 at the one entry at temperature 0).
  */
 kda_status_t kda_sample_probs(const kda_sample_desc_t *desc, const void *logits,
