@@ -557,9 +557,9 @@ typedef struct {
  * share alike and no other stands.  A row without an entry that could be drawn gets -1, as does a row with
  * a negative temperature or a parameter that is no number (status bit KDA_DEVICE_BAD_PARAM).
  *
- * Accuracy: the sums that top-p's border is found by are of p to 2^-28, in whole units of 2^-44 of the largest,
- * which add up to the same in any order; min-p's border is found to 2^-38 of p; p / noise and the
- * probabilities below take p to 2^-22.  Results are bit-identical from run to run.
+ * Accuracy: the borders of top-p and min-p are found by p to 2^-28 (top-p's by sums in whole units of 2^-44 of
+ * the largest, which add up to the same in any order); p / noise and the probabilities below take p to 2^-22.
+ * Results are bit-identical from run to run.
  */
 kda_status_t kda_sample(const kda_sample_desc_t *desc, const void *logits, const float *noise,
                         const float *temperature, const int32_t *top_k, const float *top_p,

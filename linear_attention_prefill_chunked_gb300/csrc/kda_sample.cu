@@ -92,7 +92,7 @@ struct alignas(16) Shared {
   uint32_t nk;                          // the entry that was sought,
   int idx;
   u64 mass_incl, kth_mass;              // and the mass up to and with it; the same of the k-th
-  float ch, cl, far, far_low, inv;      // what is worked out in 64 bits, by one thread
+  float ch, cl, mp, inv;                    // what is worked out in 64 bits, by one thread
   u64 target;
 };
 
@@ -127,8 +127,10 @@ __device__ __forceinline__ void octaves(const Row& r, float z, float& yh, float&
   yh = d * r.ch;
   yl = fmaf(d, r.ch, -yh) + fmaf(d, r.cl, dl * r.ch);
 }
-// p = 2^-n 2^(-j/32) (1 + e) in units of 2^-44; 0 for masked entries.  Of a whole warp, whose lanes hold the table
-// between them (reads of shared memory at 32 places take several times as long), or of some of its lanes.
+// p = 2^-n 2^(-j/32) (1 + e).  `whole` is p 2^n in units of 2^-44, good to 2^-28 however small p is: min-p is
+// compared with it.  units() is p in units of 2^-44 (0 for masked entries), whose sums are exact.  Of a whole warp,
+// whose lanes hold the table between them (reads of shared memory at 32 places take several times as long), or of
+// some of its lanes.
 struct Table {
   uint32_t lo, hi;
   float f;
@@ -136,7 +138,16 @@ struct Table {
       : lo((uint32_t)c_pow[lane]), hi((uint32_t)(c_pow[lane] >> 32)),
         f((float)(uint32_t)(c_pow[lane] >> 20) * 5.9604644775390625e-8f) {}  // 2^-24
 };
-template <bool kWarp> __device__ __forceinline__ u64 mass(const Row& r, float z, const Table& table) {
+struct Mass {
+  u64 whole;
+  float yh;
+  int n;
+  __device__ __forceinline__ u64 units() const { return yh < 45.f ? whole >> n : 0; }
+  __device__ __forceinline__ bool reaches(float p) const {   // p <= 1
+    return yh < 127.f && whole >= (u64)(fminf(p * __int_as_float((n + 127) << 23), 2.f) * (float)kOne);
+  }
+};
+template <bool kWarp> __device__ __forceinline__ Mass mass_of(const Row& r, float z, const Table& table) {
   float yh, yl;
   octaves(r, z, yh, yl);
   const float m = fmaf(yh, 32.f, kRound);
@@ -154,7 +165,10 @@ template <bool kWarp> __device__ __forceinline__ u64 mass(const Row& r, float z,
   }
   const int fine = __float2int_rn(f * e * 68719476736.f);    // of 2^36
   asm("mad.wide.s32 %0, %1, 256, %0;" : "+l"(whole) : "r"(fine));
-  return yh < 45.f ? whole >> n : 0;
+  return {whole, yh, n};
+}
+template <bool kWarp> __device__ __forceinline__ u64 mass(const Row& r, float z, const Table& table) {
+  return mass_of<kWarp>(r, z, table).units();
 }
 // p to 2^-22
 __device__ __forceinline__ float weight(const Row& r, float z) {
@@ -233,15 +247,12 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   }
   const float temp = temperature ? temperature[row] : temperature_all;
   const int k = top_k ? top_k[row] : top_k_all;
-  const float tp = top_p ? top_p[row] : top_p_all, mp = min_p ? min_p[row] : min_p_all;
-  const bool by_ratio = mp > 0.f;
+  const float tp = top_p ? top_p[row] : top_p_all;
   if (tid == 0) {
     const double c = fmin(1.4426950408889634074 / (double)temp, 1e38);   // (at temperature 0 not used)
     s.ch = (float)c;
     s.cl = (float)(c - (double)s.ch);
-    const double far = by_ratio ? -log2((double)fminf(mp, 1.f)) : 0.;
-    s.far = (float)far;
-    s.far_low = (float)(far - (double)s.far);
+    s.mp = fminf(min_p ? min_p[row] : min_p_all, 1.f);
   }
 
   // every CTA of the cluster has to have started before another writes into its shared memory
@@ -327,14 +338,8 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
   r.cl = s.cl;
   r.fx = (kBins - 1) / fmaxf(fminf((top.v - low) * r.ch, 64.f), 1e-30f);  // over the row's range, 64 octaves at most
   const bool by_count = k > 0 && k < vocab, by_mass = tp < 1.f;
-  // Min-p asks p >= min_p of the distances in octaves, as two floats, for the smallest p as well as for the largest
-  // (whole units of 2^-44 have few digits of those); what is as near to the border as their roundings, 2^-38, stands.
-  const float far = s.far, far_low = s.far_low;
-  auto near = [&](float x) {
-    float yh, yl;
-    octaves(r, x, yh, yl);
-    return (yh - far) + (yl - far_low) <= 3.637978807091713e-12f;   // 2^-38
-  };
+  const float mp = s.mp;
+  const bool by_ratio = mp > 0.f;
 
   // What stands so far: entries above `border`, and those that equal it up to index `at`. Masked ones never do.
   float border = kMaskedOut;
@@ -592,9 +597,10 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
       const bool stays = lead && ahead < k && (!by_mass || was < s.target);
       if (!kProbs) {
         Best best{-1.f, 0x7fffffff};
-        if (stays && (!by_ratio || near(value_of(it.nk)))) {
+        if (stays) {
           const float pr = weight(r, value_of(it.nk)), u = draw[it.idx];
-          if (pr > 0.f && u == u) best = Best{pr / u, it.idx};
+          if (pr > 0.f && u == u && (!by_ratio || mass_of<false>(r, value_of(it.nk), table).reaches(mp)))
+            best = Best{pr / u, it.idx};
         }
         best = join(best, 1);
         if (rank == 0 && tid == 0) token[row] = best.v < 0.f ? -1 : best.idx;
@@ -635,8 +641,8 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
         get(q, z);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const u64 w = mass<true>(r, z[e], table);
-          if (stands(place(q) + e, z[e]) && (!by_ratio || near(z[e]))) part += w;
+          const Mass w = mass_of<true>(r, z[e], table);
+          if (stands(place(q) + e, z[e]) && (!by_ratio || w.reaches(mp))) part += w.units();
         }
       }
 #pragma unroll
@@ -665,7 +671,8 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         o[e] = 0.f;
-        if (stands(place(q) + e, z[e]) && (!by_ratio || near(z[e]))) o[e] = weight(r, z[e]) * inv;
+        if (stands(place(q) + e, z[e]) && (!by_ratio || mass_of<false>(r, z[e], table).reaches(mp)))
+          o[e] = weight(r, z[e]) * inv;
       }
       put(q, o);
     }
@@ -694,7 +701,7 @@ sample_kernel(const T* __restrict__ logits, int64_t pitch, const float* __restri
         for (int e = 0; e < 4; ++e) {
           if (u[q][e] != u[q][e]) continue;
           const float pr = weight(r, z[e]);
-          if (pr > 0.f && (!by_ratio || near(z[e])))
+          if (pr > 0.f && (!by_ratio || mass_of<false>(r, z[e], table).reaches(mp)))
             best = better(best, Best{pr / u[q][e], v0 + place(q0 + q) + e});
         }
       }

@@ -1,6 +1,6 @@
 """Entries far below the largest: whatever top-k or min-p keeps stands down to 2^-126 of it, through every path of the
 search, although a mass (in units of 2^-44) has no digit left of it.  Against the definition in 64 bits, as in
-``test_sample_gpu``; no entry lies within 2^-38 of a border of min-p."""
+``test_sample_gpu``; no entry lies within 2^-28 of a border of min-p."""
 import pytest
 import torch
 
@@ -39,13 +39,14 @@ def test_top_k_at_low_temperatures(vocab, dtype, step):
 
 
 def _near_one(top_p, k, t, z, noise):
-    """Top-p whose border lies in the last millionth of the sum.  A mass is good to 2^-28 of itself and one unit of 2^-44,
-    so what lies before an entry and top_p of the sum are each off by 2^-28 of the sum and 699 units at most: below
+    """Top-p whose border lies in the last millionth of the sum.  A mass is good to 2^-28 of itself and one unit of
+    2^-44, so what lies before an entry and top_p of the sum are each off by 2^-28 of the sum and 699 units at most: below
     2^-27 + 2^-33 together.  What stands lies between what does at top_p less and more that; probabilities and
     tokens are those of what stands."""
     n, slack = z.shape[0], 2.0 ** -27 + 2.0 ** -33
     f32 = lambda v: float(torch.tensor(v, dtype=F32))
-    f = dict(temperature=f32(t), top_p=torch.tensor(top_p, device="cuda"), top_k=torch.tensor(k, dtype=torch.int32, device="cuda"))
+    f = dict(temperature=f32(t), top_p=torch.tensor(top_p, device="cuda"),
+             top_k=torch.tensor(k, dtype=torch.int32, device="cuda"))
     probs, token = kda.sample_probs(z.cuda(), **f).double().cpu(), kda.sample(z.cuda(), noise.cuda(), **f).tolist()
     for i in range(n):
         few, many = (ref.weights(z[i], t=f32(t), k=k[i], top_p=f32(top_p[i]) + d) for d in (-slack, slack))
