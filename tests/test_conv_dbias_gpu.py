@@ -21,8 +21,9 @@ def _call(d, lens, silu, bias, dbias):
     ws = torch.empty(size, dtype=torch.uint8, device="cuda")
     p = layer._p
     assert lib.kda_causal_conv_backward(
-        ctypes.byref(desc), p(d["dy"]), d["dy"].stride(0), p(d["x"]), p(d["w"]), p(bias), p(cu), p(d["h0"]), p(d["dfinal"]),
-        p(dx), p(dw), p(dbias), p(dstate), p(ws), size, torch.cuda.current_stream().cuda_stream) == 0
+        ctypes.byref(desc), p(d["dy"]), d["dy"].stride(0), p(d["x"]), p(d["w"]), p(bias), p(cu), p(d["h0"]),
+        p(d["dfinal"]), p(dx), p(dw), p(dbias), p(dstate), p(ws), size,
+        torch.cuda.current_stream().cuda_stream) == 0
     torch.cuda.synchronize()
     return dx, dw, dstate
 

@@ -15,7 +15,8 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("dtype,gate,pitch", [(BF, True, 0), (BF, False, 1), (F32, True, 0)])
 @pytest.mark.parametrize("lens", [[1], [200], [90, 0, 40, 1, 7]])
 def test_largest_rates(dtype, gate, pitch, lens):
-    al = torch.tensor([-3.0, 0.0, 2.0, 3.0, 4.0, 5.0, 10.0, 40.0, 80.0, 87.0, 88.0, 88.5, 89.0, 100.0, float("inf"), 88.7])
+    al = torch.tensor([-3.0, 0.0, 2.0, 3.0, 4.0, 5.0, 10.0, 40.0, 80.0, 87.0, 88.0, 88.5, 89.0, 100.0, float("inf"),
+                       88.7])
     d = _inputs(lens, al.numel(), dtype, seed=5, gate=gate, pitch=pitch)
     d = dict(d, A_log=al.cuda(), x=d["x"] * 64, h0=d["h0"] * 64)
     y, final, carries = _scan(d, lens, output_carries=True)
