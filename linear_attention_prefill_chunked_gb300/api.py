@@ -278,8 +278,8 @@ def prefill_path(desc: KdaDesc) -> int:
 
 
 def set_pipeline_wait_limit(nanoseconds: int = 0) -> None:
-    """Bound of the tensor-core prefill's internal waits for later launches (0: the default
-    2 s).  A timeout sets KDA_DEVICE_PIPE_TIMEOUT in the device status; the call returns."""
+    """Bound of the internal waits of the tensor-core prefill and scan and of the gated recurrence
+    for later launches (0: the default 2 s).  A timeout sets KDA_DEVICE_PIPE_TIMEOUT in the device status; the call returns."""
     rc = load().kda_set_pipeline_wait_limit(int(nanoseconds))
     if rc != 0:
         raise KdaError(rc, "kda_set_pipeline_wait_limit")

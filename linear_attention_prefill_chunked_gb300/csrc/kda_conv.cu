@@ -371,7 +371,7 @@ conv_token_kernel(const T* __restrict__ x, int64_t x_pitch, const T* __restrict_
 // registers over the run, are added over a CTA's warps at its end, and over the CTAs by a second kernel, each
 // in a fixed order. Four rows at a time: where they, and W-1 on either side, are of one sequence, nothing is looked up;
 // else row by row. Which sequence a row belongs to is written down beforehand by a small kernel.
-// 32768 x 12288 bf16, 4 taps, SiLU: 460 us, 5.3 TB/s, 78 % of the copy rate; its two special functions and some 30
+// 32768 x 12288 bf16, 4 taps, SiLU: 457 us, 5.3 TB/s, 78 % of the copy rate; its two special functions and some 30
 // other instructions an element take about as long as its bytes. 2741 x 1003 fp32 in 37 sequences: 25 us, three
 // launches and runs of 32 rows whose sequences are looked up one by one.
 constexpr int kBackWarps = 8;
@@ -454,7 +454,7 @@ template <int VEC> __device__ __forceinline__ void acc(float (&a)[VEC], const fl
 
 // Four rows of x and dy on their way to `to`, [row][x, dy][lane]. Elements of two bytes, which no asynchronous copy
 // takes, go through registers: those that were asked for last time are put down, the next ones are asked for (8192
-// rows of 12287 channels: 313 us, 559 with each put down at once and one round of CTAs).
+// rows of 12287 channels: 304 us, 559 with each put down at once and one round of CTAs).
 template <typename Raw> struct Ahead {};
 template <> struct Ahead<__nv_bfloat16> { __nv_bfloat16 x[kQuad], dy[kQuad]; };
 template <typename T, int VEC>

@@ -12,10 +12,10 @@
 // (g / m goes to 0 with g, so p needs no case for closed gates; 1 - a^2 is -expm1(2 g), whose digits
 // a subtraction would lose.)
 //
-// Both passes are bound by HBM if their arithmetic (five or six special functions an element) hides behind
-// it, so each reads its inputs once. The packed rows, whatever sequences they belong to, are cut into
-// tiles of kWarps * S rows by 32 * V channels; a warp takes S rows of a tile, a lane V channels. What a
-// run of rows does to the state is h -> A h + H, so
+// Both passes are bound by HBM if their arithmetic (six special functions an element with an input gate, eleven
+// backward, whose last step forms the gates again) hides behind it, so each reads its inputs once. The packed rows,
+// whatever sequences they belong to, are cut into tiles of kWarps * S rows by 32 * V channels; a warp takes S rows of a
+// tile, a lane V channels. What a run of rows does to the state is h -> A h + H, so
 //   1. each warp forms a and m u of its rows, which it keeps in shared memory, and their (A, H);
 //   2. the tile's (A, H) goes to global memory for the tiles after it, and the state before the tile is
 //      put together from those of the tiles before it: the state at the start of its group of kGroup
@@ -40,8 +40,9 @@
 // copy rate; 177 with a state that waits for nobody and gates of two multiplications, 245 with the gates as they
 // are, so the special functions bound it, then the state's trips. Groups of 4 tiles 267 but slower where channels
 // are few, 16: 279. Four warps a CTA 353 us, eight rows a warp 416, two states put together in turns 324. Backward,
-// 16384 x 4096 bf16: 303 us, 3.1 TB/s, bound by its instructions (2.3 a cycle and SM). Both in fp32, 65536 x 320, one
-// sequence: 263 us.
+// 16384 x 4096 bf16: 305 us, 3.1 TB/s; its special functions alone take 160 at 16 a cycle and SM, and with 57 % of
+// the issue slots and 36 % of HBM in use what is left is latency, of 20 warps an SM. Both in fp32, 65536 x 320, one
+// sequence: 265 us.
 #include <cudaTypedefs.h>
 
 #include <algorithm>

@@ -20,7 +20,7 @@
 //
 // Bound by HBM in principle (the row, and noise or probabilities), by the arithmetic of p, the histogram's shared
 // atomics and the cluster's exchanges (three to six a row) in practice: 64 x 131072 fp32, all filters,
-// 53 us (0.63 TB/s); 1 x 32003 bf16 16 us; probabilities under top-p, 320 x 131072 fp32, 262 us (1.28 TB/s; without the
+// 53 us (0.63 TB/s); 1 x 32003 bf16 17 us; probabilities under top-p, 320 x 131072 fp32, 260 us (1.29 TB/s; without the
 // histogram's atomics 35 less; masses as one 64-bit atomic instead of three of 32 bits 333 against 296 at that step).
 #include <cooperative_groups.h>
 

@@ -4,6 +4,10 @@ state space scan, and the verification and commit of drafted tokens.
 As in :mod:`api`, this module only checks tensors, allocates outputs and workspaces and passes raw
 pointers and the stream; the work is in the library's CUDA kernels.  Every call is asynchronous
 and leaves its workspace in ``<function>.last_workspace`` for :func:`read_device_status`.
+
+Results carry no history of PyTorch's autograd, whether or not the inputs require gradients: a training
+program makes a forward and a backward call one node (``examples/recurrent_training.py`` has both nodes of
+its block).
 """
 from __future__ import annotations
 
@@ -582,7 +586,8 @@ def gated_scan(x, r, A_log, cu_seqlens, *, i=None, state=None, state_indices=Non
     x, r and i [T, Ch] bf16 or fp32 (one dtype), their rows at any pitch; i None: x enters whole; A_log
     [Ch] fp32; cu_seqlens [N+1] int32.  States are [Ch] fp32; pool and dense mode as in
     :func:`causal_conv`.  ``carries`` [ceil(T / 48), Ch] fp32 is what :func:`gated_scan_backward` wants of
-    the forward pass.
+    the forward pass.  A sequence's first row counts like any other: where a model lets x enter it whole, it is
+    divided by sqrt(1 - a^2) beforehand.
     """
     N, T, ch, pitches = check_gated_args(
         x, r, A_log, i=i, cu_seqlens=cu_seqlens, state=state, state_indices=state_indices,
